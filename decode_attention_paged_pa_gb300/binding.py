@@ -9,6 +9,7 @@ if that is impossible the call fails.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -45,6 +46,11 @@ EXPORTED_SYMBOLS = (
     "pa_decode_v2_mq",
     "pa_decode_v2_fp8",
     "pa_decode_v2_mq_fp8",
+    "pa_decode_v2_kv4",
+    "pa_decode_v2_mq_kv4",
+    "pa_kv4_append",
+    "pa_kv4_gather",
+    "pa_kv4_block_bytes",
     "pa_decode_v2_workspace_bytes",
     "pa_decode_v2_workspace_layout",
     "pa_decode_v2_host_io",
@@ -91,6 +97,16 @@ def _declare(lib):
     # pa_decode_v2_fp8's arguments with q_len after num_seqs
     lib.pa_decode_v2_mq_fp8.argtypes = [vp, vp] + base[1:7] + [cf, cf, ci, ci] + base[8:]
     lib.pa_decode_v2_mq_fp8.restype = ci
+    # out, lse, query, kv_cache, tables, lens, then pa_decode_v2's from scale on (q_len after num_seqs)
+    lib.pa_decode_v2_kv4.argtypes = [vp] * 6 + base[6:]
+    lib.pa_decode_v2_kv4.restype = ci
+    lib.pa_decode_v2_mq_kv4.argtypes = [vp] * 6 + base[6:8] + [ci] + base[8:]
+    lib.pa_decode_v2_mq_kv4.restype = ci
+    for fn in (lib.pa_kv4_append, lib.pa_kv4_gather):
+        fn.argtypes = [vp] * 6 + [ci] * 5 + [cll, cll, ci, vp, ci, ci, vp, cs]
+        fn.restype = ci
+    lib.pa_kv4_block_bytes.argtypes = [ci, ci]
+    lib.pa_kv4_block_bytes.restype = cs
     lib.pa_decode_v2_host_io.argtypes = base
     lib.pa_decode_v2_host_io.restype = ci
     lib.pa_decode_v2_host_io_workspace_bytes.argtypes = [ci] * 7
@@ -374,6 +390,169 @@ def pa_decode_v2_mq_fp8(out, query, key_cache, value_cache, block_tables, seq_le
     if st != PA_OK:
         raise PaError(st, "pa_decode_v2_mq_fp8")
     return workspace
+
+
+def kv4_block_bytes(head_size: int, block_size: int) -> int:
+    """Bytes of one block of one kv head in a 4-bit cache (0: unsupported sizes)."""
+    return int(lib().pa_kv4_block_bytes(int(head_size), int(block_size)))
+
+
+def _kv4_shape(kv_cache, D):
+    """(num_blocks, KH, block_size) of a 4-bit cache for head size D."""
+    _check_tensor("kv_cache", kv_cache, torch.uint8, 3)
+    NB, KH, rec = kv_cache.shape
+    if rec % (D + 8) != 0 or rec == 0:
+        raise ValueError("kv_cache must be [num_blocks, KH, block_size * (head_size + 8)]")
+    return NB, KH, rec // (D + 8)
+
+
+def _decode_kv4(name, out, query, kv_cache, block_tables, seq_lens, scale, partition_size, workspace, stream, lse):
+    rows = query.shape[:-1]  # [S, H] or [S, q_len, H]
+    dt = query.dtype
+    if dt not in _DTYPE_CODE:
+        raise TypeError("query must be float16 or bfloat16")
+    _check_tensor("out", out, dt, query.dim())
+    _check_tensor("block_tables", block_tables, torch.int32, 2)
+    _check_tensor("seq_lens", seq_lens, torch.int32, 1)
+    S, H, D = query.shape[0], query.shape[-2], query.shape[-1]
+    QL = query.shape[1] if query.dim() == 4 else 1
+    NB, KH, BS = _kv4_shape(kv_cache, D)
+    if out.shape != query.shape:
+        raise ValueError("out must have query's shape")
+    if block_tables.shape[0] != S or seq_lens.shape[0] != S:
+        raise ValueError("block_tables / seq_lens must have num_seqs rows")
+    if lse is not None:
+        _check_tensor("lse", lse, torch.float32, query.dim() - 1)
+        if lse.shape != rows:
+            raise ValueError("lse must be query's shape without the head size")
+    MB = block_tables.shape[1]
+    if workspace is None:  # (a caller's workspace is checked by the library: PA_ERR_WORKSPACE)
+        workspace = torch.empty(max(workspace_bytes(S * QL, H, KH, D, MB, BS, partition_size), 256),
+                                dtype=torch.uint8, device=query.device)
+    _check_tensor("workspace", workspace, torch.uint8)
+    _same_device(query, out=out, kv_cache=kv_cache, block_tables=block_tables, seq_lens=seq_lens,
+                 workspace=workspace, lse=lse)
+    with _current(query):
+        st = lib().pa_decode_v2_mq_kv4(
+            _ptr(out), _ptr(lse), _ptr(query), _ptr(kv_cache), _ptr(block_tables), _ptr(seq_lens), float(scale),
+            S, QL, H, KH, D, BS, int(partition_size), _DTYPE_CODE[dt], _stream_handle(stream, query), MB, NB,
+            _ptr(workspace), workspace.numel())
+    if st != PA_OK:
+        raise PaError(st, name)
+    return workspace
+
+
+def pa_decode_v2_kv4(out, query, kv_cache, block_tables, seq_lens, scale: float, partition_size: int = 512,
+                     workspace: torch.Tensor | None = None, stream=None, lse: torch.Tensor | None = None):
+    """Decode over a cache held in 4 bits (see include/pa_decode.h): query/out
+    [S, H, D] fp16 or bf16; kv_cache uint8 [NB, KH, BS * (D + 8)] as
+    :func:`pa_kv4_append` writes it.  ``lse`` (float32 [S, H]) is optional.
+    Returns the workspace used."""
+    _check_tensor("query", query, ndim=3)
+    return _decode_kv4("pa_decode_v2_kv4", out, query, kv_cache, block_tables, seq_lens, scale, partition_size,
+                       workspace, stream, lse)
+
+
+def pa_decode_v2_mq_kv4(out, query, kv_cache, block_tables, seq_lens, scale: float, partition_size: int = 512,
+                        workspace: torch.Tensor | None = None, stream=None, lse: torch.Tensor | None = None):
+    """Multi-query decode over a cache held in 4 bits: query/out
+    [S, q_len, H, D], rows causal as for :func:`pa_decode_v2_mq`, the cache of
+    :func:`pa_decode_v2_kv4`.  ``lse`` (float32 [S, q_len, H]) is optional.
+    Returns the workspace used."""
+    _check_tensor("query", query, ndim=4)
+    return _decode_kv4("pa_decode_v2_mq_kv4", out, query, kv_cache, block_tables, seq_lens, scale, partition_size,
+                       workspace, stream, lse)
+
+
+_no_switch = contextlib.nullcontext()
+
+
+def _current(like: torch.Tensor):
+    """A context in which ``like``'s device is the current one (nothing to do,
+    and nothing paid for a switch, where it is already)."""
+    return _no_switch if like.get_device() == torch.cuda.current_device() else torch.cuda.device(like.device)
+
+
+def _same_device(like, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != like.device:
+            raise ValueError(f"{name} must be on {like.device}, got {t.device}")
+
+
+def _token_rows(name, t, kv_cache):
+    """(rows, KH, D, row stride) of [N, KH, D] or [S, q_len, KH, D] rows: the
+    heads of a token are contiguous, tokens a constant stride apart."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype not in _DTYPE_CODE:
+        raise TypeError(f"{name} must be float16 or bfloat16")
+    if t.dim() == 4:
+        if t.shape[1] != 1 and t.shape[0] != 1 and t.stride(0) != t.shape[1] * t.stride(1):
+            raise ValueError(f"{name}: tokens must be a constant stride apart")
+        N, stride = t.shape[0] * t.shape[1], t.stride(1) if t.shape[1] != 1 else t.stride(0)
+    elif t.dim() == 3:
+        N, stride = t.shape[0], t.stride(0)
+    else:
+        raise ValueError(f"{name} must have 3 or 4 dims, got shape {tuple(t.shape)}")
+    KH, D = t.shape[-2], t.shape[-1]
+    if (D != 1 and t.stride(-1) != 1) or (KH != 1 and t.stride(-2) != D):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return N, KH, D, (stride if N > 1 else KH * D)
+
+
+def _kv4_tokens(name, fn, first, kv_cache, key, value, block_tables, seq_lens, cu_tokens, workspace, stream):
+    N, KH, D, ks = _token_rows("key", key, kv_cache)
+    Nv, KHv, Dv, vs = _token_rows("value", value, kv_cache)
+    if (N, KH, D) != (Nv, KHv, Dv) or key.dtype != value.dtype:
+        raise ValueError("key and value must have the same shape and dtype")
+    NB, KHc, BS = _kv4_shape(kv_cache, D)
+    if KHc != KH:
+        raise ValueError("key / value and kv_cache must have the same kv heads")
+    _check_tensor("block_tables", block_tables, torch.int32, 2)
+    _check_tensor("seq_lens", seq_lens, torch.int32, 1)
+    S, MB = block_tables.shape
+    if seq_lens.shape[0] != S:
+        raise ValueError("block_tables / seq_lens must have num_seqs rows")
+    if cu_tokens is not None:
+        _check_tensor("cu_tokens", cu_tokens, torch.int32, 1)
+        if cu_tokens.shape[0] != S + 1:
+            raise ValueError("cu_tokens must have num_seqs + 1 entries")
+    if workspace is None:
+        workspace = torch.empty(256, dtype=torch.uint8, device=kv_cache.device)
+    _check_tensor("workspace", workspace, torch.uint8)
+    _same_device(kv_cache, key=key, value=value, block_tables=block_tables, seq_lens=seq_lens, cu_tokens=cu_tokens,
+                 workspace=workspace)
+    args = [_ptr(kv_cache), _ptr(key), _ptr(value)]
+    if not first:
+        args = args[1:] + args[:1]
+    with _current(kv_cache):
+        st = fn(*args, _ptr(block_tables), _ptr(seq_lens), _ptr(cu_tokens), S, N, KH, D, BS, ks, vs,
+                _DTYPE_CODE[key.dtype], _stream_handle(stream, kv_cache), MB, NB, _ptr(workspace), workspace.numel())
+    if st != PA_OK:
+        raise PaError(st, name)
+    return workspace
+
+
+def pa_kv4_append(kv_cache, key, value, block_tables, seq_lens, cu_tokens: torch.Tensor | None = None,
+                  workspace: torch.Tensor | None = None, stream=None):
+    """Quantise new tokens into a 4-bit cache (see include/pa_decode.h): key /
+    value [N, KH, D] (or [S, q_len, KH, D]) fp16 or bf16, slices of wider token
+    rows allowed; ``seq_lens`` counts the new tokens, which are each sequence's
+    last; ``cu_tokens`` int32 [S + 1] gives ragged rows, without it every
+    sequence has N / S.  ``workspace`` (uint8, >= 256 bytes) holds the status.
+    Returns the workspace used."""
+    return _kv4_tokens("pa_kv4_append", lib().pa_kv4_append, True, kv_cache, key, value, block_tables, seq_lens,
+                       cu_tokens, workspace, stream)
+
+
+def pa_kv4_gather(key_out, value_out, kv_cache, block_tables, seq_lens, cu_tokens: torch.Tensor | None = None,
+                  workspace: torch.Tensor | None = None, stream=None):
+    """Read each sequence's last tokens of a 4-bit cache back as fp16 or bf16
+    rows (shapes as for :func:`pa_kv4_append`).  Returns the workspace used."""
+    return _kv4_tokens("pa_kv4_gather", lib().pa_kv4_gather, False, kv_cache, key_out, value_out, block_tables,
+                       seq_lens, cu_tokens, workspace, stream)
 
 
 def host_io_workspace_bytes(num_seqs, num_heads, num_kv_heads, head_size, max_blocks_per_seq,

@@ -106,6 +106,31 @@ bool ws_layout(int S, int H, int KH, int D, int MB, int BS, int P, WsLayout* w) 
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
+// The 4-bit family's launch, dispatched on the head size.
+cudaError_t launch_kv4_f16(const KParams& prm, int D, int BS, int kvu, int max_ctas, cudaStream_t st) {
+  switch (D) {
+    case 64: return launch_kv4_d64_f16(prm, BS, kvu, max_ctas, st);
+    case 80: return launch_kv4_d80_f16(prm, BS, kvu, max_ctas, st);
+    case 96: return launch_kv4_d96_f16(prm, BS, kvu, max_ctas, st);
+    case 112: return launch_kv4_d112_f16(prm, BS, kvu, max_ctas, st);
+    case 128: return launch_kv4_d128_f16(prm, BS, kvu, max_ctas, st);
+    case 256: return launch_kv4_d256_f16(prm, BS, kvu, max_ctas, st);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+cudaError_t launch_kv4_bf16(const KParams& prm, int D, int BS, int kvu, int max_ctas, cudaStream_t st) {
+  switch (D) {
+    case 64: return launch_kv4_d64_bf16(prm, BS, kvu, max_ctas, st);
+    case 80: return launch_kv4_d80_bf16(prm, BS, kvu, max_ctas, st);
+    case 96: return launch_kv4_d96_bf16(prm, BS, kvu, max_ctas, st);
+    case 112: return launch_kv4_d112_bf16(prm, BS, kvu, max_ctas, st);
+    case 128: return launch_kv4_d128_bf16(prm, BS, kvu, max_ctas, st);
+    case 256: return launch_kv4_d256_bf16(prm, BS, kvu, max_ctas, st);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*,
                                   CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
@@ -184,7 +209,8 @@ int decode_impl(void* out, float* lse, const void* query, const void* key_cache,
                 float scale, int num_seqs, int q_len, int num_heads, int num_kv_heads, int head_size,
                 int block_size, int partition_size, int dtype, void* stream, int max_blocks_per_seq,
                 int num_blocks, void* workspace, size_t workspace_bytes, int variant, int max_ctas,
-                long long timeout_ns, bool kv_fp8 = false, float k_scale = 1.f, float v_scale = 1.f) {
+                long long timeout_ns, bool kv_fp8 = false, float k_scale = 1.f, float v_scale = 1.f,
+                bool kv4 = false) {
   // Multi-query: the kernel sees q_len "row heads" per caller head (H below
   // counts them), q_len * G per kv head, all sharing the kv head's blocks.
   if (q_len < 1 || q_len > kMaxSeqsPerLaunch || num_heads <= 0 ||
@@ -207,7 +233,7 @@ int decode_impl(void* out, float* lse, const void* query, const void* key_cache,
   if (variant == PA_VARIANT_SIMT && !simt_ok) return PA_ERR_UNSUPPORTED;
   // fp32 runs on the CUDA-core family only (its shapes; multi-query rows on
   // its causal instances).
-  if (dtype == PA_DTYPE_FP32 && (kv_fp8 || variant == PA_VARIANT_MMA || !simt_ok))
+  if (dtype == PA_DTYPE_FP32 && (kv_fp8 || kv4 || variant == PA_VARIANT_MMA || !simt_ok))
     return PA_ERR_UNSUPPORTED;
   if (S == 0) return PA_OK;
   if (!out || !query || !key_cache || !value_cache || !block_tables || !seq_lens)
@@ -222,12 +248,12 @@ int decode_impl(void* out, float* lse, const void* query, const void* key_cache,
 
   const int G = H / KH;
   if (variant == PA_VARIANT_AUTO)
-    variant = ((G == 1 || dtype == PA_DTYPE_FP32) && !kv_fp8 && simt_ok) ? PA_VARIANT_SIMT : PA_VARIANT_MMA;
+    variant = ((G == 1 || dtype == PA_DTYPE_FP32) && !kv_fp8 && !kv4 && simt_ok) ? PA_VARIANT_SIMT : PA_VARIANT_MMA;
   // More than 8 query rows per kv head: the tensor-core instances for units
   // of 16 rows (the rows on the M side of the products) read each K/V block
   // once for 16 rows (head sizes 64 and 128, blocks of 16 or 32 tokens,
   // 16-bit caches).
-  const bool wide = variant == PA_VARIANT_MMA && G > kMmaGroup && !kv_fp8 && D <= 128 &&
+  const bool wide = variant == PA_VARIANT_MMA && G > kMmaGroup && !kv_fp8 && !kv4 && D <= 128 &&
                     base_shape(D, BS);
   const int gt = (variant == PA_VARIANT_MMA) ? (wide ? kMmaGroupWide : kMmaGroup) : kSimtGroup;
   // Four query rows per kv head (query heads, or multi-query row heads): a
@@ -235,7 +261,9 @@ int decode_impl(void* out, float* lse, const void* query, const void* key_cache,
   // values covers both), head sizes up to 128 and blocks of 8, 16 or 32 tokens.
   const bool pairs = variant == PA_VARIANT_MMA && !wide && G * 2 == kMmaGroup && KH % 2 == 0 &&
                      D <= 128 && (BS == 8 || BS == 16 || BS == 32);
-  const int kvu = pairs ? 2 : 1;
+  // Over a 4-bit cache a unit takes two kv heads wherever their rows fit the
+  // 8 columns (the tile's scores, softmax and weights then serve both).
+  const int kvu = kv4 ? (G * 2 <= kMmaGroup && KH % 2 == 0 ? 2 : 1) : pairs ? 2 : 1;
   const int hg_per_kv = (G + gt - 1) / gt;
   const int n_hg = KH * hg_per_kv / kvu;
   const int rows_per_launch = kMaxSeqsPerLaunch;  // sequences per launch
@@ -243,7 +271,7 @@ int decode_impl(void* out, float* lse, const void* query, const void* key_cache,
   if ((long long)chunk * w.pmax * n_hg > INT_MAX / 2) return PA_ERR_UNSUPPORTED;
   // The tensor-core kernels over 16-bit caches in blocks of 16 tokens or more
   // stage value blocks by swizzled tensor copies (z coordinates are int32).
-  const bool tma_values = variant == PA_VARIANT_MMA && !kv_fp8 && BS >= 16;
+  const bool tma_values = variant == PA_VARIANT_MMA && !kv_fp8 && !kv4 && BS >= 16;
   KParams maps;
   std::memset(&maps, 0, sizeof maps);
   if (tma_values) {
@@ -300,7 +328,10 @@ int decode_impl(void* out, float* lse, const void* query, const void* key_cache,
     prm.n_hg = n_hg;
     prm.timeout_ns = timeout_ns > 0 ? timeout_ns : (1LL << 31);
     cudaError_t e;
-    if (kv_fp8 && pairs && BS == 8)
+    if (kv4)
+      e = dtype == PA_DTYPE_FP16 ? launch_kv4_f16(prm, D, BS, kvu, max_ctas, st)
+                                 : launch_kv4_bf16(prm, D, BS, kvu, max_ctas, st);
+    else if (kv_fp8 && pairs && BS == 8)
       e = dtype == PA_DTYPE_FP16 ? launch_mma8_gb8_f16(prm, D, max_ctas, st)
                                  : launch_mma8_gb8_bf16(prm, D, max_ctas, st);
     else if (kv_fp8 && pairs && (D == 64 || D == 128))
@@ -387,6 +418,29 @@ int decode_impl(void* out, float* lse, const void* query, const void* key_cache,
 }
 
 }  // namespace
+
+extern "C" int pa_decode_v2_kv4(void* out, float* lse, const void* query, const void* kv_cache,
+                                const int32_t* block_tables, const int32_t* seq_lens, float scale,
+                                int num_seqs, int num_heads, int num_kv_heads, int head_size,
+                                int block_size, int partition_size, int dtype, void* stream,
+                                int max_blocks_per_seq, int num_blocks, void* workspace,
+                                size_t workspace_bytes) {
+  return pa_decode_v2_mq_kv4(out, lse, query, kv_cache, block_tables, seq_lens, scale, num_seqs, 1, num_heads,
+                             num_kv_heads, head_size, block_size, partition_size, dtype, stream,
+                             max_blocks_per_seq, num_blocks, workspace, workspace_bytes);
+}
+
+extern "C" int pa_decode_v2_mq_kv4(void* out, float* lse, const void* query, const void* kv_cache,
+                                   const int32_t* block_tables, const int32_t* seq_lens, float scale,
+                                   int num_seqs, int q_len, int num_heads, int num_kv_heads, int head_size,
+                                   int block_size, int partition_size, int dtype, void* stream,
+                                   int max_blocks_per_seq, int num_blocks, void* workspace,
+                                   size_t workspace_bytes) {
+  return decode_impl(out, lse, query, kv_cache, kv_cache, block_tables, seq_lens, scale, num_seqs, q_len,
+                     num_heads, num_kv_heads, head_size, block_size, partition_size, dtype, stream,
+                     max_blocks_per_seq, num_blocks, workspace, workspace_bytes, PA_VARIANT_AUTO, 0, 0, false,
+                     1.f, 1.f, true);
+}
 
 extern "C" int pa_decode_v2_ex(void* out, const void* query, const void* key_cache,
                                const void* value_cache, const int32_t* block_tables,

@@ -1,0 +1,11 @@
+// pa_kv4d112_f16.cu -- instances of the paged decode kernel over a 4-bit
+// cache, head size 112, queries and output __half.
+#include "pa_kv4_launch.cuh"
+
+namespace pa {
+
+cudaError_t launch_kv4_d112_f16(const KParams& prm, int BS, int kvu, int max_ctas, cudaStream_t st) {
+  return kv4_go_bs<__half, 112>(prm, BS, kvu, max_ctas, st);
+}
+
+}  // namespace pa

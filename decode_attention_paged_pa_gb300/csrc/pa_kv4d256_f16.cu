@@ -1,0 +1,11 @@
+// pa_kv4d256_f16.cu -- instances of the paged decode kernel over a 4-bit
+// cache, head size 256, queries and output __half.
+#include "pa_kv4_launch.cuh"
+
+namespace pa {
+
+cudaError_t launch_kv4_d256_f16(const KParams& prm, int BS, int kvu, int max_ctas, cudaStream_t st) {
+  return kv4_go_bs<__half, 256>(prm, BS, kvu, max_ctas, st);
+}
+
+}  // namespace pa

@@ -271,6 +271,97 @@ int pa_decode_v2_mq_fp8(void* out, float* lse, const void* query, const void* ke
                         int num_blocks, void* workspace, size_t workspace_bytes);
 
 /*
+ * Caches held in 4 bits.  The pages' launcher takes a kv_cache_dtype (page
+ * "paged_attention_v2_triton.py -- Triton PagedAttention V2 for BI-V100"); the
+ * format here is this library's own: a block of one kv head is one record of
+ * pa_kv4_block_bytes(head_size, block_size) = block_size * (head_size + 8)
+ * bytes, and the cache is
+ *   kv_cache [num_blocks, num_kv_heads, block_size * (head_size + 8)] uint8
+ * A record holds, with x = min(head_size, 128),
+ *   key codes    [head_size/x][block_size][x/2]   two codes a byte, the even
+ *                                                 dim in the low four bits
+ *   value codes  [head_size/x][block_size][x/2]
+ *   parameters   [block_size][4] of the dtype     key scale, key zero, value
+ *                                                 scale, value zero of a token
+ * and a code c stands for scale * c + zero.  The dtype (fp16 or bf16) is that
+ * of the queries and of the rows that are written: a cache is used with one.
+ * Returns 0 for a head or block size outside the supported ones (head_size 64,
+ * 80, 96, 112, 128 or 256, block_size 8, 16, 32 or 64).
+ */
+size_t pa_kv4_block_bytes(int head_size, int block_size);
+
+/*
+ * Decode attention over a 4-bit cache: pa_decode_v2_lse with
+ *   K_t[d] = k_scale_t * ck_t[d] + k_zero_t,  V_t[d] = v_scale_t * cv_t[d] + v_zero_t
+ * of the sequence's cached tokens (nothing is rounded to the dtype before the
+ * products).  lse may be NULL.  dtype PA_DTYPE_FP16 or PA_DTYPE_BF16
+ * (PA_ERR_UNSUPPORTED for fp32); head sizes, block sizes, partitions, the
+ * workspace (pa_decode_v2_workspace_bytes), ownership and errors are those of
+ * pa_decode_v2.  |scale * query| is expected below 2^100.
+ */
+int pa_decode_v2_kv4(void* out, float* lse, const void* query, const void* kv_cache,
+                     const int32_t* block_tables, const int32_t* seq_lens, float scale, int num_seqs,
+                     int num_heads, int num_kv_heads, int head_size, int block_size, int partition_size,
+                     int dtype, void* stream, int max_blocks_per_seq, int num_blocks, void* workspace,
+                     size_t workspace_bytes);
+
+/*
+ * Multi-query decode over a 4-bit cache: the causal query rows of
+ * pa_decode_v2_mq with the cache of pa_decode_v2_kv4.
+ */
+int pa_decode_v2_mq_kv4(void* out, float* lse, const void* query, const void* kv_cache,
+                        const int32_t* block_tables, const int32_t* seq_lens, float scale, int num_seqs,
+                        int q_len, int num_heads, int num_kv_heads, int head_size, int block_size,
+                        int partition_size, int dtype, void* stream, int max_blocks_per_seq,
+                        int num_blocks, void* workspace, size_t workspace_bytes);
+
+/*
+ * Writes new tokens into a 4-bit cache.  Sequence s has the rows
+ * cu_tokens[s] .. cu_tokens[s+1] - 1 of key and value, and they are its last
+ * cached tokens: with n of them, row cu_tokens[s] + i goes to position
+ * seq_lens[s] - n + i (seq_lens counts the new tokens, as for pa_decode_v2_mq).
+ * Per token and kv head, for the key and the value x[0 .. head_size):
+ *   zero  = min x (+0 for a zero of either sign)
+ *   scale = (max x - min x) / 15, computed in fp32, rounded to the dtype
+ *   code  = (x - zero) / scale in fp32, rounded to the nearest integer (ties
+ *           to even), at most 15; 0 where the scale is 0
+ * A vector with a NaN or an infinity, or whose spread is not finite in fp32,
+ * gets NaN for scale and zero and reads back as NaN.
+ *   kv_cache     as above, written: only the slots of the new tokens
+ *   key, value   [num_tokens, num_kv_heads, head_size] dtype, rows
+ *                key_stride / value_stride elements apart (multiples of 8, at
+ *                least num_kv_heads * head_size), 16-byte aligned
+ *   cu_tokens    DEVICE [num_seqs + 1] int32, ascending from 0; NULL: every
+ *                sequence has num_tokens / num_seqs rows.  Rows at or behind
+ *                cu_tokens[num_seqs] are not read.
+ *   workspace    >= 256 bytes, 16-byte aligned, required; holds the status
+ *                (pa_decode_v2_device_status), whatever it held before
+ * A position of several sequences (a shared block) must not be written by two
+ * of them.  A length below the sequence's row count or above the table's
+ * capacity, offsets that descend or pass num_tokens, and block ids outside
+ * the pool are recorded as PA_ERR_DEVICE_BOUNDS; the rows concerned are
+ * skipped.  One launch on `stream`; it can be captured into a CUDA graph.
+ */
+int pa_kv4_append(void* kv_cache, const void* key, const void* value, const int32_t* block_tables,
+                  const int32_t* seq_lens, const int32_t* cu_tokens, int num_seqs, int num_tokens,
+                  int num_kv_heads, int head_size, int block_size, long long key_stride,
+                  long long value_stride, int dtype, void* stream, int max_blocks_per_seq,
+                  int num_blocks, void* workspace, size_t workspace_bytes);
+
+/*
+ * The reverse: the last cu_tokens[s+1] - cu_tokens[s] cached tokens of each
+ * sequence as rows of the dtype, each value scale * code + zero in fp32 rounded
+ * once (for prefill attention over earlier context, or to leave the format).
+ * Arguments as for pa_kv4_append; rows that belong to no sequence, or whose
+ * length or block id is refused, keep what they held.
+ */
+int pa_kv4_gather(void* key_out, void* value_out, const void* kv_cache, const int32_t* block_tables,
+                  const int32_t* seq_lens, const int32_t* cu_tokens, int num_seqs, int num_tokens,
+                  int num_kv_heads, int head_size, int block_size, long long key_stride,
+                  long long value_stride, int dtype, void* stream, int max_blocks_per_seq,
+                  int num_blocks, void* workspace, size_t workspace_bytes);
+
+/*
  * Bytes of device workspace pa_decode_v2_host_io needs: the workspace of
  * pa_decode_v2 plus device staging for query, out (room for 4-byte elements,
  * whatever the dtype), block_tables and seq_lens.  Returns 0 for invalid sizes.
