@@ -25,6 +25,7 @@ PA_ERR_WORKSPACE = 3
 PA_ERR_CUDA = 4
 PA_ERR_DEVICE_BOUNDS = 5
 PA_ERR_TIMEOUT = 6
+PA_ERR_NO_BLOCKS = 7
 
 PA_DTYPE_FP16 = 0
 PA_DTYPE_BF16 = 1
@@ -51,6 +52,10 @@ EXPORTED_SYMBOLS = (
     "pa_kv4_append",
     "pa_kv4_gather",
     "pa_kv4_block_bytes",
+    "pa_pages_fork",
+    "pa_pages_resize",
+    "pa_pages_compact",
+    "pa_pages_workspace_bytes",
     "pa_decode_v2_workspace_bytes",
     "pa_decode_v2_workspace_layout",
     "pa_decode_v2_host_io",
@@ -107,6 +112,14 @@ def _declare(lib):
         fn.restype = ci
     lib.pa_kv4_block_bytes.argtypes = [ci, ci]
     lib.pa_kv4_block_bytes.restype = cs
+    lib.pa_pages_workspace_bytes.argtypes = [ci] * 3
+    lib.pa_pages_workspace_bytes.restype = cs
+    lib.pa_pages_fork.argtypes = [vp] * 8 + [ci] * 6 + [vp, vp, cs]
+    lib.pa_pages_fork.restype = ci
+    lib.pa_pages_resize.argtypes = [vp] * 6 + [ci] * 5 + [vp, vp, cs]
+    lib.pa_pages_resize.restype = ci
+    lib.pa_pages_compact.argtypes = [vp] * 6 + [ci] * 5 + [vp, vp, cs]
+    lib.pa_pages_compact.restype = ci
     lib.pa_decode_v2_host_io.argtypes = base
     lib.pa_decode_v2_host_io.restype = ci
     lib.pa_decode_v2_host_io_workspace_bytes.argtypes = [ci] * 7
@@ -553,6 +566,117 @@ def pa_kv4_gather(key_out, value_out, kv_cache, block_tables, seq_lens, cu_token
     rows (shapes as for :func:`pa_kv4_append`).  Returns the workspace used."""
     return _kv4_tokens("pa_kv4_gather", lib().pa_kv4_gather, False, kv_cache, key_out, value_out, block_tables,
                        seq_lens, cu_tokens, workspace, stream)
+
+
+def pages_workspace_bytes(num_rows: int, max_blocks_per_seq: int, num_blocks: int) -> int:
+    """Bytes of workspace a pages call needs (rows: children or sequences)."""
+    return int(lib().pa_pages_workspace_bytes(int(num_rows), int(max_blocks_per_seq), int(num_blocks)))
+
+
+def _pages_args(refcounts, caches, rows, MB, workspace, **tensors):
+    """(caches array, page bytes array, count, workspace) after the checks all pages calls share."""
+    _check_tensor("refcounts", refcounts, torch.int32, 1)
+    NB = refcounts.shape[0]
+    if NB == 0:
+        raise ValueError("refcounts must have num_blocks >= 1 entries")
+    caches = [caches] if isinstance(caches, torch.Tensor) else list(caches)
+    n = len(caches)
+    ptrs, sizes = (ctypes.c_void_p * max(n, 1))(), (ctypes.c_size_t * max(n, 1))()
+    for i, c in enumerate(caches):
+        _check_tensor("cache", c)
+        if c.dim() < 1 or c.shape[0] != NB:
+            raise ValueError("every cache's first dimension must be the pool's num_blocks (refcounts' length)")
+        if c.device != refcounts.device:
+            raise ValueError(f"every cache must be on {refcounts.device}, got {c.device}")
+        ptrs[i] = c.data_ptr()
+        sizes[i] = c.numel() * c.element_size() // NB
+    if workspace is None:
+        workspace = torch.empty(max(pages_workspace_bytes(rows, MB, NB), 256), dtype=torch.uint8,
+                                device=refcounts.device)
+    _check_tensor("workspace", workspace, torch.uint8)
+    _same_device(refcounts, workspace=workspace, **tensors)
+    return ptrs, sizes, n, workspace
+
+
+def pa_pages_fork(block_tables_out, seq_lens_out, block_tables, seq_lens, parents, refcounts, caches,
+                  block_size: int, workspace: torch.Tensor | None = None, stream=None):
+    """Child rows that share their parents' full blocks and own a copy of the
+    partly filled last one (see include/pa_decode.h): block_tables_out int32
+    [n, MB], seq_lens_out int32 [n] written; block_tables [S, MB], seq_lens [S];
+    parents int32 [n] (-1: an empty row); refcounts int32 [num_blocks] updated;
+    ``caches`` the tensors [num_blocks, ...] whose pages follow the tables.
+    Returns the workspace used (its status: :func:`device_status`)."""
+    _check_tensor("block_tables_out", block_tables_out, torch.int32, 2)
+    _check_tensor("seq_lens_out", seq_lens_out, torch.int32, 1)
+    _check_tensor("block_tables", block_tables, torch.int32, 2)
+    _check_tensor("seq_lens", seq_lens, torch.int32, 1)
+    _check_tensor("parents", parents, torch.int32, 1)
+    (S, MB), n = block_tables.shape, parents.shape[0]
+    if tuple(block_tables_out.shape) != (n, MB) or seq_lens_out.shape[0] != n or seq_lens.shape[0] != S:
+        raise ValueError("inconsistent table / length / parents shapes")
+    ptrs, sizes, nc, workspace = _pages_args(
+        refcounts, caches, n, MB, workspace, block_tables_out=block_tables_out, seq_lens_out=seq_lens_out,
+        block_tables=block_tables, seq_lens=seq_lens, parents=parents)
+    with _current(refcounts):
+        st = lib().pa_pages_fork(
+            _ptr(block_tables_out), _ptr(seq_lens_out), _ptr(block_tables), _ptr(seq_lens), _ptr(parents),
+            _ptr(refcounts), ptrs, sizes, nc, S, n, MB, int(block_size), refcounts.shape[0],
+            _stream_handle(stream, refcounts), _ptr(workspace), workspace.numel())
+    if st != PA_OK:
+        raise PaError(st, "pa_pages_fork")
+    return workspace
+
+
+def pa_pages_resize(block_tables, seq_lens, new_lens, refcounts, caches, block_size: int,
+                    workspace: torch.Tensor | None = None, stream=None):
+    """Sequences grown, truncated or (new length 0) freed (see
+    include/pa_decode.h): block_tables int32 [S, MB], seq_lens int32 [S] and
+    refcounts int32 [num_blocks] updated in place; new_lens int32 [S].
+    Returns the workspace used."""
+    _check_tensor("block_tables", block_tables, torch.int32, 2)
+    _check_tensor("seq_lens", seq_lens, torch.int32, 1)
+    _check_tensor("new_lens", new_lens, torch.int32, 1)
+    S, MB = block_tables.shape
+    if seq_lens.shape[0] != S or new_lens.shape[0] != S:
+        raise ValueError("block_tables / seq_lens / new_lens must have num_seqs rows")
+    ptrs, sizes, nc, workspace = _pages_args(refcounts, caches, S, MB, workspace, block_tables=block_tables,
+                                             seq_lens=seq_lens, new_lens=new_lens)
+    with _current(refcounts):
+        st = lib().pa_pages_resize(
+            _ptr(block_tables), _ptr(seq_lens), _ptr(new_lens), _ptr(refcounts), ptrs, sizes, nc, S, MB,
+            int(block_size), refcounts.shape[0], _stream_handle(stream, refcounts), _ptr(workspace),
+            workspace.numel())
+    if st != PA_OK:
+        raise PaError(st, "pa_pages_resize")
+    return workspace
+
+
+def pa_pages_compact(block_tables, seq_lens, refcounts, caches, block_size: int,
+                     workspace: torch.Tensor | None = None, stream=None, new_ids: torch.Tensor | None = None):
+    """The blocks in use moved to the front of the pool (see
+    include/pa_decode.h): block_tables int32 [S, MB] and refcounts int32
+    [num_blocks] updated in place, pages moved in every cache; ``new_ids``
+    (int32 [num_blocks], optional) receives each block's new id.  Returns the
+    workspace used."""
+    _check_tensor("block_tables", block_tables, torch.int32, 2)
+    _check_tensor("seq_lens", seq_lens, torch.int32, 1)
+    S, MB = block_tables.shape
+    if seq_lens.shape[0] != S:
+        raise ValueError("block_tables / seq_lens must have num_seqs rows")
+    if new_ids is not None:
+        _check_tensor("new_ids", new_ids, torch.int32, 1)
+        if new_ids.shape != refcounts.shape:
+            raise ValueError("new_ids must have num_blocks entries")
+    ptrs, sizes, nc, workspace = _pages_args(refcounts, caches, S, MB, workspace, block_tables=block_tables,
+                                             seq_lens=seq_lens, new_ids=new_ids)
+    with _current(refcounts):
+        st = lib().pa_pages_compact(
+            _ptr(block_tables), _ptr(seq_lens), _ptr(refcounts), _ptr(new_ids), ptrs, sizes, nc, S, MB,
+            int(block_size), refcounts.shape[0], _stream_handle(stream, refcounts), _ptr(workspace),
+            workspace.numel())
+    if st != PA_OK:
+        raise PaError(st, "pa_pages_compact")
+    return workspace
 
 
 def host_io_workspace_bytes(num_seqs, num_heads, num_kv_heads, head_size, max_blocks_per_seq,

@@ -601,6 +601,7 @@ extern "C" const char* pa_decode_v2_status_string(int status) {
     case PA_ERR_CUDA: return "CUDA runtime error";
     case PA_ERR_DEVICE_BOUNDS: return "device-side bounds violation (block id or sequence length)";
     case PA_ERR_TIMEOUT: return "device-side wait timed out";
+    case PA_ERR_NO_BLOCKS: return "too few free blocks in the pool";
     default: return "unknown status";
   }
 }

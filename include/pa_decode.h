@@ -70,7 +70,8 @@ enum {
     PA_ERR_WORKSPACE = 3,     /* workspace smaller than pa_decode_v2_workspace_bytes() */
     PA_ERR_CUDA = 4,          /* a CUDA runtime call failed (launch, memset, ...) */
     PA_ERR_DEVICE_BOUNDS = 5, /* device-side: bad block id or sequence length */
-    PA_ERR_TIMEOUT = 6        /* device-side: a bounded wait gave up */
+    PA_ERR_TIMEOUT = 6,       /* device-side: a bounded wait gave up */
+    PA_ERR_NO_BLOCKS = 7      /* device-side: the pool has too few free blocks */
 };
 
 /* Kernel families (pa_decode_v2_ex's `variant`). */
@@ -360,6 +361,91 @@ int pa_kv4_gather(void* key_out, void* value_out, const void* kv_cache, const in
                   int num_kv_heads, int head_size, int block_size, long long key_stride,
                   long long value_stride, int dtype, void* stream, int max_blocks_per_seq,
                   int num_blocks, void* workspace, size_t workspace_bytes);
+
+/*
+ * Pages of a pool.  For callers that keep block tables, lengths and the pool's
+ * state on the device: sequences share, take and give back blocks without a
+ * round trip to the host.  The state is
+ *   refcounts [num_blocks] int32, read and written: the number of table rows
+ *   that hold a block within their length; 0 (or less) is a free block
+ * and the blocks of a row are its first ceil(seq_lens / block_size) entries.
+ * Blocks are taken lowest free id first, in row order and within a row in table
+ * order, so the result does not depend on timing.  Blocks given back by a call
+ * are free for the calls after it.  After a fork or a resize a row's partly
+ * filled last block is held by that row alone, so that appending to one
+ * sequence never writes another's tokens.
+ *
+ * Arguments shared by the three calls:
+ *   caches       HOST array of num_caches DEVICE pointers: every cache whose
+ *                pages follow the tables (keys, values, of every layer; any
+ *                layout whose first dimension is the block).  16-byte aligned.
+ *   page_bytes   HOST array: bytes of one block in each cache, multiples of 16
+ *   block_size   tokens per block, any positive number
+ *   workspace    >= pa_pages_workspace_bytes(rows, ...) bytes (rows:
+ *                num_children or num_seqs), 16-byte aligned, required; holds
+ *                the status (pa_decode_v2_device_status)
+ * Calls enqueue two launches on `stream` (one more per further 128 caches),
+ * never synchronise and can be captured into a CUDA graph.  The arrays caches
+ * and page_bytes are read before the call returns.  Calls on one pool must be
+ * ordered on one stream, also with those that read its tables and caches.
+ *
+ * Errors on the device: a call that needs more blocks than are free records
+ * PA_ERR_NO_BLOCKS and changes nothing.  Rows with a parent, length or new
+ * length out of range, or whose partly filled block has an id outside the
+ * pool, are recorded as PA_ERR_DEVICE_BOUNDS and left as they were (a child
+ * becomes an empty row); other ids outside the pool are recorded and counted
+ * nowhere; a count that would fall below 0 is recorded and stays.
+ * Returns 0 for invalid sizes.
+ */
+size_t pa_pages_workspace_bytes(int num_rows, int max_blocks_per_seq, int num_blocks);
+
+/*
+ * Forks: row i of the outputs becomes a copy of sequence parents[i] (parallel
+ * samples, beams).  It shares the parent's full blocks (their counts go up) and
+ * gets a copy of its partly filled last block in a block of its own; the
+ * parents keep theirs.  Table entries past the child's blocks keep what they
+ * held.
+ *   block_tables_out [num_children, max_blocks_per_seq], seq_lens_out
+ *                [num_children]: written, must not overlap the inputs
+ *   block_tables [num_seqs, max_blocks_per_seq], seq_lens [num_seqs]
+ *   parents      [num_children] int32 in [0, num_seqs), in any order, with
+ *                repeats; -1 makes an empty row
+ */
+int pa_pages_fork(int32_t* block_tables_out, int32_t* seq_lens_out, const int32_t* block_tables,
+                  const int32_t* seq_lens, const int32_t* parents, int32_t* refcounts,
+                  void* const* caches, const size_t* page_bytes, int num_caches, int num_seqs,
+                  int num_children, int max_blocks_per_seq, int block_size, int num_blocks,
+                  void* stream, void* workspace, size_t workspace_bytes);
+
+/*
+ * Resizes: sequence s gets room for new_lens[s] tokens, and seq_lens[s] becomes
+ * new_lens[s].  A longer sequence takes blocks, a shorter one gives back those
+ * past its new end, 0 frees it; the same length leaves it as it is.  Where the
+ * last token kept lies in a partly filled block that other rows hold too
+ * (a sequence cut back into a part it shares), the row gets a copy of it.
+ *   block_tables [num_seqs, max_blocks_per_seq], seq_lens [num_seqs]: updated
+ *   new_lens     [num_seqs] int32 in [0, max_blocks_per_seq * block_size]
+ */
+int pa_pages_resize(int32_t* block_tables, int32_t* seq_lens, const int32_t* new_lens,
+                    int32_t* refcounts, void* const* caches, const size_t* page_bytes, int num_caches,
+                    int num_seqs, int max_blocks_per_seq, int block_size, int num_blocks, void* stream,
+                    void* workspace, size_t workspace_bytes);
+
+/*
+ * Compacts: with U blocks in use, those with ids of U and up move, in ascending
+ * order, into the free ids below U, ascending; pages, counts and table entries
+ * follow, and the blocks U .. num_blocks - 1 are free afterwards (so the
+ * caches' tails can be given up or used otherwise).  A pool without holes is
+ * left as it is.
+ *   block_tables [num_seqs, max_blocks_per_seq]: updated; every row that holds
+ *                blocks has to be among them (or follow new_ids)
+ *   new_ids      NULL, or DEVICE [num_blocks] int32, written: the block's id
+ *                after the call, -1 for a block that was free
+ */
+int pa_pages_compact(int32_t* block_tables, const int32_t* seq_lens, int32_t* refcounts,
+                     int32_t* new_ids, void* const* caches, const size_t* page_bytes, int num_caches,
+                     int num_seqs, int max_blocks_per_seq, int block_size, int num_blocks, void* stream,
+                     void* workspace, size_t workspace_bytes);
 
 /*
  * Bytes of device workspace pa_decode_v2_host_io needs: the workspace of
