@@ -19,8 +19,7 @@
 //     size)-byte run in the page's layouts -- into shared memory, completing
 //     on mbarriers: the key block by a 1-D bulk async copy, the value block by
 //     a 1-D bulk copy or (tensor-core consumer over 16-bit caches, C::kTma) a
-//     3-D tensor copy that lays its rows out in the swizzle of their width
-//     (4-bit caches, C::kRecord: one bulk copy takes the block's record);
+//     3-D tensor copy that lays its rows out in the swizzle of their width;
 //   * warps 0..NC-1 (consumers): work item j of unit (p, hg) (a block, or two
 //     consecutive blocks: C::kItemBlocks) goes to warp (j + p * n_hg + hg) % NC
 //     (a fixed grouping, so results do not depend on scheduling), which folds
@@ -410,21 +409,16 @@ __device__ __forceinline__ void producer_loop(const KParams& prm, uint8_t* smem,
         while (true) {
           if (!done && mbar_test_wait(bar_empty + 8 * st, ph ^ 1u)) {
             const uint32_t dst = sbase + st * LY::STAGE;
+            const size_t off = ((size_t)bi * prm.KH + U.kv) * (size_t)(D * C::BS) * C::KV_ESZ;
             mbar_arrive_expect_tx(bar_full + 8 * st, LY::STAGE_TX);
-            if constexpr (C::kRecord) {
-              bulk_copy_g2s(dst, static_cast<const uint8_t*>(prm.kc) + ((size_t)bi * prm.KH + U.kv) * C::REC,
-                            LY::KBYTES, bar_full + 8 * st, pol_stream);
+            bulk_copy_g2s(dst, static_cast<const uint8_t*>(prm.kc) + off, LY::KBYTES, bar_full + 8 * st,
+                          pol_stream);
+            if constexpr (C::kTma) {
+              // The whole value block (x = 0: the 16-byte alignment rule holds).
+              tma_load_3d(dst + LY::VOFF, &prm.tmv, 0, 0, bi * prm.KH + U.kv, bar_full + 8 * st, pol_stream);
             } else {
-              const size_t off = ((size_t)bi * prm.KH + U.kv) * (size_t)(D * C::BS) * C::KV_ESZ;
-              bulk_copy_g2s(dst, static_cast<const uint8_t*>(prm.kc) + off, LY::KBYTES, bar_full + 8 * st,
-                            pol_stream);
-              if constexpr (C::kTma) {
-                // The whole value block (x = 0: the 16-byte alignment rule holds).
-                tma_load_3d(dst + LY::VOFF, &prm.tmv, 0, 0, bi * prm.KH + U.kv, bar_full + 8 * st, pol_stream);
-              } else {
-                bulk_copy_g2s(dst + LY::VOFF, static_cast<const uint8_t*>(prm.vc) + off, LY::KBYTES,
-                              bar_full + 8 * st, pol_stream);
-              }
+              bulk_copy_g2s(dst + LY::VOFF, static_cast<const uint8_t*>(prm.vc) + off, LY::KBYTES,
+                            bar_full + 8 * st, pol_stream);
             }
             done = true;
           }

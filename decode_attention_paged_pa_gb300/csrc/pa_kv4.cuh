@@ -1,5 +1,5 @@
-// pa_kv4.cuh -- tensor-core consumer for the paged decode kernel over a cache
-// held in 4 bits.
+// pa_kv4.cuh -- persistent, warp-specialised paged decode attention over a
+// cache held in 4 bits (phase 1; the partitions are combined by pa_combine.cuh).
 //
 // Cache record of one (block, kv head), BS * (D + 8) bytes (x = min(D, 128)):
 //
@@ -27,9 +27,14 @@
 // zero; it is kept to the spread of the codes (c - 8) by summing the rounded
 // weights themselves (one more product, with rows of code 8) and putting
 // 8 p_t vs_t back in fp32 with the zeros.  The weights are scaled by the power
-// of two 2^12 / vb, vb above every value scale the warp has met (raised, with
+// of two 2^7 / vb, vb above every value scale the warp has met (raised, with
 // the accumulators, when a larger one comes), so they stay in fp16's range
 // whatever the cache's magnitude.
+//
+// Softmax without a reduction per item: each column keeps a reference (a
+// maximum it has met) and raises it only when a score passes it by more than
+// 2^8, which one vote per item finds out; weights stay below 2^8, sums and
+// accumulators in fp32.  Most items need no shuffle, no rescaling.
 //
 // Rows and slots.  MMA row i of a 16-token score tile holds token kTok(i):
 // 0 7 1 6 2 5 3 4, then 8 more of the same.  The 4-byte words of a token row
@@ -42,424 +47,831 @@
 // of 64 run padded: the words past a row's end are other bytes of the record,
 // which the zeroed query slots, or leaving the accumulator rows out, ignore
 // (every nibble is a finite number).
+//
+// Work unit = (sequence, partition, kv head, GT of its query rows), taken by a
+// team of TW warps of one CTA (TW = 1, 2, 4 ..: as many as make enough teams'
+// worth of units, choose_team); each warp takes a contiguous run of the
+// partition's tokens.  One CTA of NC equal warps per SM, no producer: a warp
+// owns a ring of a few 32-token stages and refills a stage itself, by one bulk
+// copy per block, right after it has used it, so no warp waits for another
+// while it streams.  What was measured on the way to this: a team of all the
+// SM's warps with one warp that merges their states (the scheme of
+// pa_kernel.cuh) spends more on set-ups, hand-overs and the merging warp than
+// on the tokens, as a 4-bit partition holds a quarter of the bytes.  A warp of
+// a team of one writes its unit itself; larger teams meet once per unit, leave
+// their states in their rings and each merge a slice of the rows.
 #pragma once
 
 #include "pa_common.cuh"
+#include "pa_kernel.cuh"
 
 namespace pa {
 
-template <typename T_, int D_, int BS_, int KVU_>
-struct Kv4Consumer {
+#ifndef PA_KV4_UNITS
+#define PA_KV4_UNITS 5
+#endif
+
+template <typename T_, int D_, int NT_>
+struct Kv4 {
   using T = T_;
-  static constexpr bool kTma = false;
-  static constexpr bool kRecord = true;  // keys, values and parameters of a block are one run of bytes
-  static constexpr int D = D_, BS = BS_, GT = 8;
-  static constexpr int KVU = KVU_;  // kv heads per unit (G * KVU <= 8 columns)
-  static constexpr bool kMma = true;
-  static constexpr bool kCausal = false;
-  static constexpr uint32_t X = D_ < 128 ? D_ : 128;  // dims per slab
-  static constexpr int NSLAB = D_ / (int)X;
-  static constexpr uint32_t XB = X / 2;               // bytes of a token row in a slab
-  static constexpr uint32_t SLAB = (uint32_t)BS_ * XB;
-  static constexpr uint32_t VOFFSET = (uint32_t)BS_ * D_ / 2;  // value codes in a record
-  static constexpr uint32_t POFFSET = (uint32_t)BS_ * D_;      // parameters in a record
-  static constexpr uint32_t REC = (uint32_t)BS_ * (D_ + 8);
-  static constexpr uint32_t KBLK = (uint32_t)KVU_ * REC;
-  static constexpr uint32_t KREGION = 0;
-  static constexpr uint32_t STAGE_BYTES = KBLK;
-  static constexpr uint32_t STAGE_TX = KBLK;
-  static_assert(D_ % (int)X == 0 && X % 16 == 0 && KBLK % 16 == 0, "whole slabs, 16-byte units");
-  static constexpr int KV_ESZ = 1;
-  static constexpr int kIssueBatch = (KBLK <= 2304) ? 32 : 16;
-  static constexpr int kItemBlocks = BS_ <= 16 ? 2 : 1;
-  static constexpr int SCRATCH_FLOATS = 0;
-  static constexpr int QROW = D_ + 8;
-  static constexpr int AROW = D_ + 4;
+  static constexpr int D = D_, NT = NT_, GT = 8 * NT_;
+  // Warps per CTA: as many as the accumulators' registers allow (128 or 255 a thread).
+  static constexpr int NC = (D_ <= 128 && NT_ == 1) ? 16 : 8;
+  static constexpr int THREADS = NC * 32;
+  static constexpr int X = D_ < 128 ? D_ : 128;  // dims per slab
+  static constexpr int NSLAB = D_ / X;
+  static constexpr int XB = X / 2;               // bytes of a token row in a slab
+  static_assert(D_ % X == 0 && X % 16 == 0, "whole slabs");
   // 4-byte words of a slab row per lane quad member (keys) and per lane group (values).
-  static constexpr int KW = ((int)X / 8 + 3) / 4;
-  static constexpr int VW = ((int)X / 8 + 7) / 8;
-  static constexpr int NK = NSLAB * KW * 2;   // k-steps of the score product
-  static constexpr int MTS = VW * 4;          // 16-dim tiles of a slab's value product
+  static constexpr int KW = (X / 8 + 3) / 4;
+  static constexpr int VW = (X / 8 + 7) / 8;
+  static constexpr int NK = NSLAB * KW * 2;      // k-steps of the score product
+  static constexpr int MTS = VW * 4;             // 16-dim tiles of a slab's value product
   static constexpr int NMT = NSLAB * MTS;
+  static constexpr int NSMAX = 8;                // ring stages per warp
+  static constexpr int AROW = D_ + 4;            // floats of a handed-over row (16 bytes past it, for the banks)
+  static constexpr uint32_t STATE = GT * AROW * 4 + GT * 2 * 4;
+  static constexpr uint32_t SZ_BAR = NC * NSMAX * 8;
+  static constexpr uint32_t SZ_PREF = (kMaxSeqsPerLaunch + 1) * 4;
+  static constexpr uint32_t FIXED = al16(SZ_BAR) + 64 + 256 + al16(SZ_PREF);
+  static constexpr uint32_t BUDGET = 227 * 1024;
+  static constexpr uint32_t RING = (BUDGET - FIXED) / NC / 128 * 128;  // bytes per warp
+  static constexpr uint32_t OFF_BAR = NC * RING, OFF_FLAGS = OFF_BAR + al16(SZ_BAR), OFF_NEXT = OFF_FLAGS + 64,
+                            OFF_PREF = OFF_NEXT + 256, BYTES = OFF_PREF + al16(SZ_PREF);
+  static_assert(BYTES <= BUDGET, "shared memory over budget");
+  static_assert(STATE <= RING && 64 * (D_ + 8) <= RING, "a warp's state and its largest stage fit its ring");
+};
+
+// What a CTA derives from the launch and the lengths.
+struct Kv4Plan {
+  int TW;             // warps per unit
+  int n_hg;           // units per partition: KH * hg_per_kv
+  int TS, NBLK;       // tokens and blocks per stage
+  uint32_t rec;       // bytes of a record
+  uint32_t stage;     // bytes of a ring stage
+  int NS;             // ring stages per warp
+  int total;          // units
+};
+
+// Warps per unit: the fewest that give the grid's teams about five units each
+// (an even end), but no more than a partition has stages.
+template <class K>
+__device__ __forceinline__ Kv4Plan make_plan(const KParams& prm, int BS, int partitions) {
+  Kv4Plan pl;
+  pl.NBLK = BS < 32 ? 32 / BS : 1;
+  pl.TS = pl.NBLK * BS;
+  pl.rec = (uint32_t)BS * (K::D + 8);
+  pl.stage = pl.rec * pl.NBLK;
+  pl.NS = min((int)(K::RING / pl.stage), K::NSMAX);
+  pl.n_hg = prm.KH * prm.hg_per_kv;
+  pl.total = partitions * pl.n_hg;
+  const long long want = (long long)PA_KV4_UNITS * gridDim.x * K::NC;
+  int tw = 1;
+  while (tw < K::NC && tw * pl.TS < prm.P && (long long)pl.total * tw < want) tw *= 2;
+  pl.TW = tw;
+  return pl;
+}
+
+// ---------------------------------------------------------------- small pieces
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t lds_b32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ void lds_b64(uint32_t a, uint32_t& x, uint32_t& y) {
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(x), "=r"(y) : "r"(a));
+}
+__device__ __forceinline__ void lds_b128(uint32_t a, uint32_t* v) {
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+               : "r"(a));
+}
+// fp16 products, accumulated in fp32; `first`: from zero.
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_f16_first(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %10, %10, %10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+// Offsets within a stage that depend on the block size only (warp-uniform).
+struct Kv4Offsets {
+  uint32_t hd, td;    // codes: tokens 8..15 of a tile after 0..7; tile 1 after tile 0
+  uint32_t hdp, tdp;  // parameters: the same
+  uint32_t slab, voff, poff;
+};
+template <class K>
+__device__ __forceinline__ Kv4Offsets make_offsets(const Kv4Plan& pl, int BS) {
+  Kv4Offsets o;
+  o.hd = BS == 8 ? pl.rec : 8 * K::XB;
+  o.hdp = BS == 8 ? pl.rec : 64;
+  o.td = BS == 8 ? 2 * pl.rec : BS == 16 ? pl.rec : 16 * K::XB;
+  o.tdp = BS == 8 ? 2 * pl.rec : BS == 16 ? pl.rec : 128;
+  o.slab = (uint32_t)BS * K::XB;
+  o.voff = (uint32_t)BS * K::D / 2;
+  o.poff = (uint32_t)BS * K::D;
+  return o;
+}
+
+// ---------------------------------------------------------------- a consumer warp's state
+template <class K, bool MQ>
+struct Kv4State {
+  using T = typename K::T;
+  static constexpr int NT = K::NT, NK = K::NK, NMT = K::NMT, KW = K::KW, VW = K::VW, NSLAB = K::NSLAB;
   static constexpr uint32_t LO = 0x000f000fu, HI = 0x00f000f0u;
 
-  uint32_t qb[NK][2];  // Q^T fragments: the query row of column lane / 4
-  float m[2], l[2];    // columns 2 (lane % 4) and + 1
-  float zs[2];         // sum of weight * (value zero + 8 value scale)
-  float acc[NMT][4], acc8[4];
-  float kf, qz[2];     // score factors: scale_log2 over the operands' powers of two; times sum(q)
-  float vb, vinv;      // see above: vb a power of two, vinv = 2^12 / vb
-  int lim[2];
-  int own[2], ub;      // kv head (0 .. KVU - 1) of the lane's columns, and of column lane / 4
+  uint32_t qb[NT][NK][2];          // Q^T fragments: the query row of column lane / 4
+  float ms[NT][2], thr[NT][2];     // reference (0 until set) and reference + 8 (-inf until set)
+  float l[NT][2], zs[NT][2];       // sums of weights; of weight * (value zero + 8 value scale)
+  float qz[NT][2];                 // scale_log2 * sum(q)
+  float acc[NMT][NT][4], acc8[NT][4];
+  float kf;                        // score factor: scale_log2 over the operands' powers of two
+  float vb, vinv;                  // see the top: a power of two, and 2^7 / vb
+  int lim[NT][2], minlim;          // MQ: positions the lane's columns see; the warp's least
 
   __device__ __forceinline__ static int tok_lo(int i) { return (i & 1) ? 7 - (i >> 1) : (i >> 1); }
 
-  __device__ __forceinline__ static uint32_t lds32(uint32_t a) {
-    uint32_t v;
-    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a));
-    return v;
-  }
-  __device__ __forceinline__ static void lds64(uint32_t a, uint32_t& x, uint32_t& y) {
-    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(x), "=r"(y) : "r"(a));
-  }
-  __device__ __forceinline__ static void lds128(uint32_t a, uint32_t* v) {
-    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
-                 : "r"(a));
-  }
-  // KW words of a key row from word c * KW on (row strides: 32, 40, 48, 56 or 64 bytes).
   __device__ __forceinline__ static void key_words(uint32_t a, uint32_t (&w)[KW]) {
-    if constexpr (KW == 4 && XB % 16 == 0) {
-      lds128(a, w);
+    if constexpr (KW == 4 && K::XB % 16 == 0) {
+      lds_b128(a, w);
     } else if constexpr (KW % 2 == 0) {
 #pragma unroll
-      for (int i = 0; i < KW; i += 2) lds64(a + 4 * i, w[i], w[i + 1]);
+      for (int i = 0; i < KW; i += 2) lds_b64(a + 4 * i, w[i], w[i + 1]);
     } else {
 #pragma unroll
-      for (int i = 0; i < KW; ++i) w[i] = lds32(a + 4 * i);
-    }
-  }
-  __device__ __forceinline__ static float2 params2(uint32_t w) { return F16Traits<T>::to_float2(w); }
-
-  template <class F>
-  __device__ __forceinline__ void set_limits(F limit_of, int lane) {
-#pragma unroll
-    for (int j = 0; j < 2; ++j) lim[j] = limit_of((lane & 3) * 2 + j);
-  }
-
-  __device__ __forceinline__ void begin_unit(const T* qs, int nh, float sl2, int lane, int G) {
-    const int n = lane >> 2, c = lane & 3;
-    ub = KVU_ > 1 ? n / G : 0;
-#pragma unroll
-    for (int j = 0; j < 2; ++j) own[j] = KVU_ > 1 ? min((2 * c + j) / G, KVU_ - 1) : 0;
-    const uint16_t* q16 = reinterpret_cast<const uint16_t*>(qs) + n * QROW;
-    // Dims 8w .. 8w + 7 of head n are word w of a slab; this lane holds words
-    // c * KW .. of each slab.
-    float amax = 0.f, sum = 0.f;
-#pragma unroll
-    for (int sl = 0; sl < NSLAB; ++sl)
-#pragma unroll
-      for (int i = 0; i < KW; ++i) {
-        const int w = c * KW + i;
-        if (n < nh && w < (int)X / 8) {
-          const uint4 v = *reinterpret_cast<const uint4*>(q16 + sl * X + w * 8);
-          const uint32_t e[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float2 f = F16Traits<T>::to_float2(e[k]);
-            amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
-            sum += f.x + f.y;
-          }
-        }
-      }
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-    // 2^s brings the unit's largest |q| below 2^15; zero, subnormal, Inf or
-    // NaN leave the query unscaled.
-    const int E = (__float_as_int(amax) >> 23) & 0xff;
-    const int s = (E == 0 || E == 255) ? 0 : max(-113, min(110, 141 - E));
-    const float up = __int_as_float((127 + s) << 23), up16 = up * 0.0625f;
-#pragma unroll
-    for (int sl = 0; sl < NSLAB; ++sl)
-#pragma unroll
-      for (int i = 0; i < KW; ++i) {
-        const int w = c * KW + i;
-        float f[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) f[k] = 0.f;
-        if (n < nh && w < (int)X / 8)
-          unpack_chunk<T>(*reinterpret_cast<const uint4*>(q16 + sl * X + w * 8), f);
-        const int ks = (sl * KW + i) * 2;
-        qb[ks][0] = F16Traits<__half>::pack(f[0] * up, f[4] * up);
-        qb[ks][1] = F16Traits<__half>::pack(f[1] * up16, f[5] * up16);
-        qb[ks + 1][0] = F16Traits<__half>::pack(f[2] * up, f[6] * up);
-        qb[ks + 1][1] = F16Traits<__half>::pack(f[3] * up16, f[7] * up16);
-      }
-    kf = sl2 * __int_as_float((127 - s) << 23) * 16777216.f;
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      qz[j] = sl2 * __shfl_sync(0xffffffffu, sum, (2 * c + j) * 4);
-      m[j] = -INFINITY;
-      l[j] = zs[j] = 0.f;
-    }
-#pragma unroll
-    for (int mt = 0; mt < NMT; ++mt)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[mt][i] = 0.f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) acc8[i] = 0.f;
-    vb = 7.888609052210118e-31f;  // 2^-100
-    vinv = 4096.f / vb;
-  }
-
-  __device__ __forceinline__ void block(const uint8_t* s, const uint8_t*, int ntok, int lane, float*, int tok0) {
-    const uint32_t a = smem_addr(s);
-    if constexpr (BS == 8) {
-      // Half a tile: rows 8..15 read the block again and are masked.
-      const uint32_t lo[1] = {a}, hi[1] = {a};
-      const int tl[1] = {0}, th[1] = {0};
-      tiles<1>(lo, hi, tl, th, ntok, lane, tok0);
-    } else {
-      constexpr int NTT = BS / 16, NTU = NTT < 2 ? NTT : 2;
-#pragma unroll
-      for (int h = 0; h < NTT / NTU; ++h) {
-        if (h > 0 && ntok <= h * 16 * NTU) break;
-        uint32_t lo[NTU], hi[NTU];
-        int tl[NTU], th[NTU];
-#pragma unroll
-        for (int t = 0; t < NTU; ++t) {
-          lo[t] = hi[t] = a;
-          tl[t] = (h * NTU + t) * 16;
-          th[t] = tl[t] + 8;
-        }
-        tiles<NTU>(lo, hi, tl, th, ntok - h * 16 * NTU, lane, tok0 + h * 16 * NTU);
-      }
-    }
-  }
-
-  __device__ __forceinline__ void block_pair(const uint8_t* sA, const uint8_t*, const uint8_t* sB, const uint8_t*,
-                                             int ntok, int lane, int tok0) {
-    const uint32_t a = smem_addr(sA), b = smem_addr(sB);
-    if constexpr (BS == 8) {
-      const uint32_t lo[1] = {a}, hi[1] = {b};
-      const int tl[1] = {0}, th[1] = {0};
-      tiles<1>(lo, hi, tl, th, ntok, lane, tok0);
-    } else {
-      static_assert(BS == 8 || BS == 16 || kItemBlocks == 1, "pairs are 8- or 16-token blocks");
-      const uint32_t lo[2] = {a, b}, hi[2] = {a, b};
-      const int tl[2] = {0, 0}, th[2] = {8, 8};
-      tiles<2>(lo, hi, tl, th, ntok, lane, tok0);
-    }
-  }
-
-  // NT 16-token tiles: tokens 0..7 of tile t are tokens tl[t].. of the record
-  // at lo[t], tokens 8..15 tokens th[t].. of the record at hi[t]; ntok of the
-  // item's tokens lie before the sequence end, and its first is token tok0.
-  template <int NT>
-  __device__ __forceinline__ void tiles(const uint32_t (&lo)[NT], const uint32_t (&hi)[NT], const int (&tl)[NT],
-                                        const int (&th)[NT], int ntok, int lane, int tok0) {
-    const int r = lane >> 2, c = lane & 3;
-    const int trow = tok_lo(r);
-    float sc[NT][4];
-    float2 pv[NT][2][2];  // (value scale, value zero) of the lane's two score rows, per column
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      float dot[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int u = 0; u < KVU; ++u) {
-        float c0[4] = {0.f, 0.f, 0.f, 0.f}, c1[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int sl = 0; sl < NSLAB; ++sl) {
-          uint32_t wl[KW], wh[KW];
-          key_words(lo[t] + u * REC + sl * SLAB + (tl[t] + trow) * XB + c * (KW * 4), wl);
-          key_words(hi[t] + u * REC + sl * SLAB + (th[t] + trow) * XB + c * (KW * 4), wh);
-#pragma unroll
-          for (int i = 0; i < KW; ++i) {
-            const int ks = (sl * KW + i) * 2;
-            const uint32_t a[4] = {wl[i] & LO, wh[i] & LO, wl[i] & HI, wh[i] & HI};
-            Mma<__half>::run(c0, a, qb[ks][0], qb[ks][1]);
-            const uint32_t xl = wl[i] >> 8, xh = wh[i] >> 8;
-            const uint32_t b[4] = {xl & LO, xh & LO, xl & HI, xh & HI};
-            Mma<__half>::run(c1, b, qb[ks + 1][0], qb[ks + 1][1]);
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float v = c0[i] + c1[i];
-          dot[i] = (KVU == 1 || own[i & 1] == u) ? v : dot[i];
-        }
-      }
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {  // score rows r and r + 8
-        const int tt = t * 16 + 8 * h + trow;
-        const uint32_t pa = (h ? hi[t] + (th[t] + trow) * 8 : lo[t] + (tl[t] + trow) * 8) + POFFSET;
-        float2 k = make_float2(0.f, 0.f);
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          if (j == 0 || KVU > 1) {
-            uint32_t wk, wv;
-            lds64(pa + (KVU > 1 ? own[j] * REC : 0u), wk, wv);
-            k = params2(wk);
-            pv[t][h][j] = params2(wv);
-          } else {
-            pv[t][h][1] = pv[t][h][0];
-          }
-          const float z = fmaf(k.x * kf, dot[2 * h + j], k.y * qz[j]);
-          // Slots past the sequence end hold arbitrary parameters: cleared.
-          if (tt >= ntok) pv[t][h][j] = make_float2(0.f, 0.f);
-          sc[t][2 * h + j] = (tt < ntok && tok0 + tt < lim[j]) ? z : -INFINITY;
-        }
-      }
-    }
-    // Weights and running statistics.
-    float alpha[2];
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      float bm = fmaxf(sc[0][j], sc[0][j + 2]);
-#pragma unroll
-      for (int t = 1; t < NT; ++t) bm = fmaxf(bm, fmaxf(sc[t][j], sc[t][j + 2]));
-      bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 4));
-      bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 8));
-      bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 16));
-      const float mn = fmaxf(m[j], bm);
-      const float ms = (mn == -INFINITY) ? 0.f : mn;  // a row that has seen no position yet
-      alpha[j] = exp2f(m[j] - ms);
-      m[j] = mn;
-      float ps = 0.f;
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          // A row's masked positions weigh nothing, whatever their parameters hold.
-          const bool seen = sc[t][2 * h + j] != -INFINITY;
-          sc[t][2 * h + j] = exp2f(sc[t][2 * h + j] - ms);
-          ps += sc[t][2 * h + j];
-          if (!seen) pv[t][h][j] = make_float2(0.f, 0.f);
-        }
-      l[j] = fmaf(l[j], alpha[j], ps);
-      zs[j] *= alpha[j];
-    }
-    // The value scales' bound (finite scales only: a NaN or Inf goes through
-    // to the output whatever the bound is).
-    float vm = 0.f;
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const float a = fabsf(pv[t][h][j].x);
-          vm = a < INFINITY ? fmaxf(vm, a) : vm;
-        }
-    float down = 1.f;
-    if (__any_sync(0xffffffffu, vm >= vb)) {
-      // The power of two above the largest scale (both positive: ordered as integers).
-      const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(vm));
-      const float nb = __uint_as_float(min((top >> 23) + 1u, 254u) << 23);
-      down = vb / nb;
-      vb = nb;
-      vinv = 4096.f / nb;
-    }
-    const float a0 = alpha[0] * down, a1 = alpha[1] * down;
-#pragma unroll
-    for (int mt = 0; mt < NMT; ++mt) {
-      acc[mt][0] *= a0;
-      acc[mt][1] *= a1;
-      acc[mt][2] *= a0;
-      acc[mt][3] *= a1;
-    }
-    acc8[0] *= a0;
-    acc8[1] *= a1;
-    acc8[2] *= a0;
-    acc8[3] *= a1;
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      float w[4];
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const float p = sc[t][2 * h + j];
-          const float2 v = pv[t][h][j];
-          zs[j] = fmaf(p, fmaf(8.f, v.x, v.y), zs[j]);
-          w[2 * h + j] = p * (v.x * vinv);
-        }
-      const uint32_t b0 = movmatrix_trans(F16Traits<__half>::pack(w[0], w[1]));
-      const uint32_t b1 = movmatrix_trans(F16Traits<__half>::pack(w[2], w[3]));
-      const uint32_t eight[4] = {0x00080008u, 0x00080008u, 0x00080008u, 0x00080008u};
-      Mma<__half>::run(acc8, eight, b0, b1);
-#pragma unroll
-      for (int u = 0; u < KVU; ++u) {
-        // kv head u's product takes the weight columns of its own query heads.
-        const bool mine = KVU == 1 || ub == u;
-        const uint32_t m0 = mine ? b0 : 0u, m1 = mine ? b1 : 0u;
-#pragma unroll
-        for (int sl = 0; sl < NSLAB; ++sl) {
-          // Slots 2c, 2c + 1 and 2c + 8, 2c + 9 hold tokens c, 7 - c, 8 + c, 15 - c.
-          const uint32_t base = u * REC + VOFFSET + sl * SLAB + r * (VW * 4);
-          uint32_t wa[2], wb[2], wc[2], wd[2];
-          value_words(lo[t] + base + (tl[t] + c) * XB, wa);
-          value_words(lo[t] + base + (tl[t] + 7 - c) * XB, wb);
-          value_words(hi[t] + base + (th[t] + c) * XB, wc);
-          value_words(hi[t] + base + (th[t] + 7 - c) * XB, wd);
-#pragma unroll
-          for (int half = 0; half < VW; ++half) {
-            // VW = 2: rows r and r + 8 of tile mt hold nibble mt of the two
-            // words (nibbles 0-3, then 4-7); VW = 1: nibbles mt and mt + 4 of the one.
-            const uint32_t sel = half ? 0x7632u : 0x5410u;
-            uint32_t x0, x1, x2, x3;
-            if constexpr (VW == 2) {
-              x0 = __byte_perm(wa[0], wb[0], sel);
-              x1 = __byte_perm(wa[1], wb[1], sel);
-              x2 = __byte_perm(wc[0], wd[0], sel);
-              x3 = __byte_perm(wc[1], wd[1], sel);
-            } else {
-              x0 = __byte_perm(wa[0], wb[0], 0x5410u);
-              x1 = __byte_perm(wa[0], wb[0], 0x7632u);
-              x2 = __byte_perm(wc[0], wd[0], 0x5410u);
-              x3 = __byte_perm(wc[0], wd[0], 0x7632u);
-            }
-            const int mt = sl * MTS + half * 4;
-            const uint32_t f0[4] = {x0 & LO, x1 & LO, x2 & LO, x3 & LO};
-            Mma<__half>::run(acc[mt], f0, m0, m1);
-            const uint32_t f1[4] = {x0 & HI, x1 & HI, x2 & HI, x3 & HI};
-            Mma<__half>::run(acc[mt + 1], f1, m0, m1);
-            x0 >>= 8; x1 >>= 8; x2 >>= 8; x3 >>= 8;
-            const uint32_t f2[4] = {x0 & LO, x1 & LO, x2 & LO, x3 & LO};
-            Mma<__half>::run(acc[mt + 2], f2, m0, m1);
-            const uint32_t f3[4] = {x0 & HI, x1 & HI, x2 & HI, x3 & HI};
-            Mma<__half>::run(acc[mt + 3], f3, m0, m1);
-          }
-        }
-      }
+      for (int i = 0; i < KW; ++i) w[i] = lds_b32(a + 4 * i);
     }
   }
   __device__ __forceinline__ static void value_words(uint32_t a, uint32_t (&w)[2]) {
     if constexpr (VW == 2) {
-      lds64(a, w[0], w[1]);
+      lds_b64(a, w[0], w[1]);
     } else {
-      w[0] = lds32(a);
+      w[0] = lds_b32(a);
       w[1] = 0u;
     }
   }
 
-  __device__ __forceinline__ void finish(float* acc_out, float* ml, int lane) {
-    const int r = lane >> 2, c = lane & 3;
+  // row(i): the unit's query row i (of nh), in global memory.
+  template <class F>
+  __device__ __forceinline__ void begin_unit(F row, int nh, float sl2, int lane) {
+    const int n = lane >> 2, c = lane & 3;
+    // Dims 8w .. 8w + 7 of a slab are word w; this lane holds words c * KW ...
+    uint4 v[NT][NSLAB * KW];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      float ls = l[j], z = zs[j];
-#pragma unroll
-      for (int o = 4; o < 32; o <<= 1) {
-        ls += __shfl_xor_sync(0xffffffffu, ls, o);
-        z += __shfl_xor_sync(0xffffffffu, z, o);
-      }
-      if (r == 0) {
-        ml[(2 * c + j) * 2] = m[j];
-        ml[(2 * c + j) * 2 + 1] = ls;
-      }
-      float* o = acc_out + (2 * c + j) * AROW;
-      // Tiles of odd nibbles carry 2^-20 instead of 2^-24.
-      const float e8 = acc8[j], e16 = 16.f * e8;
+    for (int t = 0; t < NT; ++t) {
+      const T* q = 8 * t + n < nh ? row(8 * t + n) : nullptr;
 #pragma unroll
       for (int sl = 0; sl < NSLAB; ++sl)
 #pragma unroll
-        for (int h = 0; h < 2; ++h)   // rows r and r + 8
+        for (int i = 0; i < KW; ++i) {
+          const int w = c * KW + i;
+          v[t][sl * KW + i] = make_uint4(0, 0, 0, 0);
+          if (q && w < K::X / 8) v[t][sl * KW + i] = __ldg(reinterpret_cast<const uint4*>(q + sl * K::X + w * 8));
+        }
+    }
+    float amax = 0.f;
 #pragma unroll
-          for (int q = 0; q < VW; ++q) {
-            // Dims of row half h: VW = 2: 16 r + 8 h + 4 q ..; VW = 1: 8 r + 4 h ..
-            const int d = VW == 2 ? 16 * r + 8 * h + 4 * q : 8 * r + 4 * h;
-            const int mt = sl * MTS + 4 * q;
-            float4 v;
-            v.x = fmaf((acc[mt][2 * h + j] - e8) * 4096.f, vb, z);
-            v.y = fmaf((acc[mt + 1][2 * h + j] - e16) * 256.f, vb, z);
-            v.z = fmaf((acc[mt + 2][2 * h + j] - e8) * 4096.f, vb, z);
-            v.w = fmaf((acc[mt + 3][2 * h + j] - e16) * 256.f, vb, z);
-            if (d < (int)X) *reinterpret_cast<float4*>(o + sl * X + d) = v;
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int i = 0; i < NSLAB * KW; ++i) {
+        float f[8];
+        unpack_chunk<T>(v[t][i], f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(f[e]));
+      }
+    // 2^s brings the unit's largest |q| below 2^15; zero, subnormal, Inf or
+    // NaN leave the query unscaled.  (Positive floats are ordered as integers.)
+    const int E = (int)(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)) >> 23);
+    const int s = (E == 0 || E == 255) ? 0 : max(-113, min(110, 141 - E));
+    const float up = __int_as_float((127 + s) << 23), up16 = up * 0.0625f;
+    kf = sl2 * __int_as_float((127 - s) << 23) * 16777216.f;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < NSLAB * KW; ++i) {
+        float f[8];
+        unpack_chunk<T>(v[t][i], f);
+        const int ks = 2 * i;
+        qb[t][ks][0] = F16Traits<__half>::pack(f[0] * up, f[4] * up);
+        qb[t][ks][1] = F16Traits<__half>::pack(f[1] * up16, f[5] * up16);
+        qb[t][ks + 1][0] = F16Traits<__half>::pack(f[2] * up, f[6] * up);
+        qb[t][ks + 1][1] = F16Traits<__half>::pack(f[3] * up16, f[7] * up16);
+      }
+      // sum(q): the product with keys of code 1.
+      const uint32_t one[4] = {0x00010001u, 0x00010001u, 0x00100010u, 0x00100010u};
+#pragma unroll
+      for (int ks = 0; ks < NK; ++ks) mma_f16(sum, one, qb[t][ks][0], qb[t][ks][1]);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        qz[t][j] = kf * sum[j];
+        ms[t][j] = 0.f;
+        thr[t][j] = -INFINITY;
+        l[t][j] = zs[t][j] = 0.f;
+      }
+#pragma unroll
+      for (int mt = 0; mt < NMT; ++mt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[mt][t][i] = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc8[t][i] = 0.f;
+    }
+    vb = 7.888609052210118e-31f;  // 2^-100
+    vinv = 128.f / vb;
+  }
+
+  template <class F>
+  __device__ __forceinline__ void set_limits(F limit_of, int lane) {
+    int least = INT_MAX_;
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        lim[t][j] = limit_of(8 * t + (lane & 3) * 2 + j);
+        least = min(least, lim[t][j]);
+      }
+    minlim = __reduce_min_sync(0xffffffffu, least);
+  }
+  static constexpr int INT_MAX_ = 0x7fffffff;
+
+  // 32 tokens whose first tile starts at `codes` / `params` (the record's
+  // start plus the token offset of either); ntok of them lie before the
+  // sequence end, the first is token tok0.
+  __device__ __forceinline__ void pass(uint32_t codes, uint32_t params, const Kv4Offsets& o, int ntok, int tok0,
+                                       int lane) {
+    const int r = lane >> 2, c = lane & 3;
+    const int trow = tok_lo(r);
+    float z[2][NT][4];
+    float2 pv[2][2];  // (value scale, value zero) of the lane's score rows r, r + 8 of each tile
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      float c0[NT][4], c1[NT][4];
+      const uint32_t ka = codes + t * o.td + trow * K::XB + c * (KW * 4);
+#pragma unroll
+      for (int sl = 0; sl < NSLAB; ++sl) {
+        uint32_t wl[KW], wh[KW];
+        key_words(ka + sl * o.slab, wl);
+        key_words(ka + sl * o.slab + o.hd, wh);
+#pragma unroll
+        for (int i = 0; i < KW; ++i) {
+          const int ks = (sl * KW + i) * 2;
+          const uint32_t a[4] = {wl[i] & LO, wh[i] & LO, wl[i] & HI, wh[i] & HI};
+          const uint32_t xl = wl[i] >> 8, xh = wh[i] >> 8;
+          const uint32_t b[4] = {xl & LO, xh & LO, xl & HI, xh & HI};
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            if (ks == 0) {
+              mma_f16_first(c0[n], a, qb[n][ks][0], qb[n][ks][1]);
+              mma_f16_first(c1[n], b, qb[n][ks + 1][0], qb[n][ks + 1][1]);
+            } else {
+              mma_f16(c0[n], a, qb[n][ks][0], qb[n][ks][1]);
+              mma_f16(c1[n], b, qb[n][ks + 1][0], qb[n][ks + 1][1]);
+            }
           }
+        }
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t wk, wv;
+        lds_b64(params + t * o.tdp + (h ? o.hdp : 0u) + trow * 8, wk, wv);
+        const float2 k = F16Traits<T>::to_float2(wk);
+        pv[t][h] = F16Traits<T>::to_float2(wv);
+        const float kx = k.x * kf;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            z[t][n][2 * h + j] = fmaf(kx, c0[n][2 * h + j] + c1[n][2 * h + j], k.y * qz[n][j]);
+      }
+    }
+    // Slots past the sequence end hold arbitrary parameters, and causal rows
+    // stop earlier: their scores become -inf, and (below) their weights 0.
+    const bool full = ntok >= 32 && (!MQ || tok0 + 32 <= minlim);
+    if (!full) {
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int tt = 16 * t + 8 * h + trow;
+          if (tt >= ntok) pv[t][h] = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+              if (tt >= ntok || (MQ && tok0 + tt >= lim[n][j])) z[t][n][2 * h + j] = -INFINITY;
+        }
+    }
+    float vm = fmaxf(fmaxf(fabsf(pv[0][0].x), fabsf(pv[0][1].x)), fmaxf(fabsf(pv[1][0].x), fabsf(pv[1][1].x)));
+    bool raise = vm >= vb;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        raise |= fmaxf(fmaxf(z[0][n][j], z[0][n][j + 2]), fmaxf(z[1][n][j], z[1][n][j + 2])) > thr[n][j];
+    if (__any_sync(0xffffffffu, raise)) raise_bounds(z, pv);
+    if (full) weigh<false>(z, pv, codes + o.voff, o, r, c);
+    else weigh<true>(z, pv, codes + o.voff, o, r, c);
+  }
+
+  // New references, and a new bound on the value scales (finite ones: a NaN
+  // or Inf goes through to the output whatever the bound is); the sums and
+  // accumulators follow.
+  __device__ __forceinline__ void raise_bounds(const float (&z)[2][NT][4], const float2 (&pv)[2][2]) {
+    float vm = 0.f;
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float a = fabsf(pv[t][h].x);
+        vm = a < INFINITY ? fmaxf(vm, a) : vm;
+      }
+    const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(vm));
+    float down = 1.f;
+    if (__uint_as_float(top) >= vb) {
+      const float nb = __uint_as_float(min((top >> 23) + 1u, 254u) << 23);  // the power of two above
+      down = vb / nb;
+      vb = nb;
+      vinv = 128.f / nb;
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      float a[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        float bm = fmaxf(fmaxf(z[0][n][j], z[0][n][j + 2]), fmaxf(z[1][n][j], z[1][n][j + 2]));
+        bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 4));
+        bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 8));
+        bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 16));
+        const bool set = thr[n][j] != -INFINITY;
+        a[j] = 1.f;
+        if (bm != -INFINITY) {  // (a row that has seen no position yet stays unset)
+          const float nm = set ? fmaxf(ms[n][j], bm) : bm;
+          if (set) a[j] = ex2(ms[n][j] - nm);
+          ms[n][j] = nm;
+          thr[n][j] = nm + 8.f;
+        }
+        l[n][j] *= a[j];
+        zs[n][j] *= a[j];
+        a[j] *= down;
+      }
+#pragma unroll
+      for (int mt = 0; mt < NMT; ++mt) {
+        acc[mt][n][0] *= a[0];
+        acc[mt][n][1] *= a[1];
+        acc[mt][n][2] *= a[0];
+        acc[mt][n][3] *= a[1];
+      }
+      acc8[n][0] *= a[0];
+      acc8[n][1] *= a[1];
+      acc8[n][2] *= a[0];
+      acc8[n][3] *= a[1];
+    }
+  }
+
+  template <bool MASK>
+  __device__ __forceinline__ void weigh(const float (&z)[2][NT][4], const float2 (&pv)[2][2], uint32_t values,
+                                        const Kv4Offsets& o, int r, int c) {
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      uint32_t b0[NT], b1[NT];
+      const float zc[2] = {fmaf(8.f, pv[t][0].x, pv[t][0].y), fmaf(8.f, pv[t][1].x, pv[t][1].y)};
+      const float vw[2] = {pv[t][0].x * vinv, pv[t][1].x * vinv};
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        float w[4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const float x = z[t][n][2 * h + j];
+            const float p = ex2(x - ms[n][j]);
+            l[n][j] += p;
+            // A masked position weighs nothing, whatever its parameters hold.
+            const bool out = MASK && x == -INFINITY;
+            zs[n][j] = out ? zs[n][j] : fmaf(p, zc[h], zs[n][j]);
+            w[2 * h + j] = out ? 0.f : p * vw[h];
+          }
+        b0[n] = movmatrix_trans(F16Traits<__half>::pack(w[0], w[1]));
+        b1[n] = movmatrix_trans(F16Traits<__half>::pack(w[2], w[3]));
+        const uint32_t eight[4] = {0x00080008u, 0x00080008u, 0x00080008u, 0x00080008u};
+        mma_f16(acc8[n], eight, b0[n], b1[n]);
+      }
+      // Slots 2c, 2c + 1 and 2c + 8, 2c + 9 hold tokens c, 7 - c, 8 + c, 15 - c.
+      const uint32_t va = values + t * o.td + c * K::XB + r * (VW * 4);
+      const uint32_t vd = (7 - 2 * c) * K::XB;
+#pragma unroll
+      for (int sl = 0; sl < NSLAB; ++sl) {
+        uint32_t wa[2], wb[2], wc[2], wd[2];
+        value_words(va + sl * o.slab, wa);
+        value_words(va + sl * o.slab + vd, wb);
+        value_words(va + sl * o.slab + o.hd, wc);
+        value_words(va + sl * o.slab + o.hd + vd, wd);
+#pragma unroll
+        for (int half = 0; half < VW; ++half) {
+          // VW = 2: rows r and r + 8 of tile mt hold nibble mt of the two
+          // words (nibbles 0-3, then 4-7); VW = 1: nibbles mt and mt + 4 of the one.
+          uint32_t x0, x1, x2, x3;
+          if constexpr (VW == 2) {
+            const uint32_t sel = half ? 0x7632u : 0x5410u;
+            x0 = __byte_perm(wa[0], wb[0], sel);
+            x1 = __byte_perm(wa[1], wb[1], sel);
+            x2 = __byte_perm(wc[0], wd[0], sel);
+            x3 = __byte_perm(wc[1], wd[1], sel);
+          } else {
+            x0 = __byte_perm(wa[0], wb[0], 0x5410u);
+            x1 = __byte_perm(wa[0], wb[0], 0x7632u);
+            x2 = __byte_perm(wc[0], wd[0], 0x5410u);
+            x3 = __byte_perm(wc[0], wd[0], 0x7632u);
+          }
+          const int mt = sl * K::MTS + half * 4;
+          const uint32_t f0[4] = {x0 & LO, x1 & LO, x2 & LO, x3 & LO};
+          const uint32_t f1[4] = {x0 & HI, x1 & HI, x2 & HI, x3 & HI};
+          x0 >>= 8; x1 >>= 8; x2 >>= 8; x3 >>= 8;
+          const uint32_t f2[4] = {x0 & LO, x1 & LO, x2 & LO, x3 & LO};
+          const uint32_t f3[4] = {x0 & HI, x1 & HI, x2 & HI, x3 & HI};
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            mma_f16(acc[mt][n], f0, b0[n], b1[n]);
+            mma_f16(acc[mt + 1][n], f1, b0[n], b1[n]);
+            mma_f16(acc[mt + 2][n], f2, b0[n], b1[n]);
+            mma_f16(acc[mt + 3][n], f3, b0[n], b1[n]);
+          }
+        }
+      }
+    }
+  }
+
+  // The warp's state of the unit, four dims at a time: sink(col, d, v) with
+  // the unnormalised sums of column col's dims d .. d + 3, and stat(col, m, l)
+  // once per column.
+  template <class Sink, class Stat>
+  __device__ __forceinline__ void finish(Sink sink, Stat stat, int lane) {
+    const int r = lane >> 2, c = lane & 3;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        float ls = l[n][j], zz = zs[n][j];
+#pragma unroll
+        for (int k = 4; k < 32; k <<= 1) {
+          ls += __shfl_xor_sync(0xffffffffu, ls, k);
+          zz += __shfl_xor_sync(0xffffffffu, zz, k);
+        }
+        const int col = 8 * n + 2 * c + j;
+        stat(col, thr[n][j] == -INFINITY ? -INFINITY : ms[n][j], ls);
+        // Tiles of odd nibbles carry 2^-20 instead of 2^-24.
+        const float e8 = acc8[n][j], e16 = 16.f * e8;
+#pragma unroll
+        for (int sl = 0; sl < NSLAB; ++sl)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)   // rows r and r + 8
+#pragma unroll
+            for (int q = 0; q < VW; ++q) {
+              // Dims of row half h: VW = 2: 16 r + 8 h + 4 q ..; VW = 1: 8 r + 4 h ..
+              const int d = VW == 2 ? 16 * r + 8 * h + 4 * q : 8 * r + 4 * h;
+              const int mt = sl * K::MTS + 4 * q;
+              float4 v;
+              v.x = fmaf((acc[mt][n][2 * h + j] - e8) * 131072.f, vb, zz);
+              v.y = fmaf((acc[mt + 1][n][2 * h + j] - e16) * 8192.f, vb, zz);
+              v.z = fmaf((acc[mt + 2][n][2 * h + j] - e8) * 131072.f, vb, zz);
+              v.w = fmaf((acc[mt + 3][n][2 * h + j] - e16) * 8192.f, vb, zz);
+              if (d < K::X) sink(col, sl * K::X + d, v, ls);
+            }
+      }
+  }
+};
+
+// ---------------------------------------------------------------- units
+// Unit u = (partition, kv head, row group), partitions numbered in batch
+// order: sequence s holds pref[s] .. pref[s + 1] - 1.
+struct Kv4Unit {
+  int s, p, np, L, t0, t1, nb, kv, h0, nh;
+};
+template <class K, bool MQ>
+__device__ __forceinline__ Kv4Unit kv4_unit(const KParams& prm, const Kv4Plan& pl, const int* pref, int BS, int u) {
+  Kv4Unit U;
+  const int pair = u / pl.n_hg, hg = u - pair * pl.n_hg;
+  int lo = 0, hi = prm.S;  // pref[lo] <= pair < pref[lo + 1]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (pref[mid] <= pair) lo = mid; else hi = mid;
+  }
+  bool bad = false;  // flagged by the prologue already
+  U.s = lo;
+  U.p = pair - pref[lo];
+  U.np = pref[lo + 1] - pref[lo];
+  U.L = seq_tokens<MQ>(prm, lo, prm.MB * BS, &bad);
+  U.t0 = U.p * prm.P;
+  U.t1 = min(U.t0 + prm.P, U.L);
+  U.nb = (U.t1 - U.t0 + BS - 1) / BS;
+  U.kv = hg / prm.hg_per_kv;
+  const int part = hg - U.kv * prm.hg_per_kv;
+  U.h0 = U.kv * prm.G + part * K::GT;
+  U.nh = min(K::GT, prm.G - part * K::GT);
+  return U;
+}
+
+// One finished row piece: the partition's normalised output in the workspace,
+// or the output itself where the sequence has one partition.
+template <class K>
+__device__ __forceinline__ void put_row(const KParams& prm, const Kv4Unit& U, int col, int d, const float4& v,
+                                        uint64_t keep) {
+  using T = typename K::T;
+  const int h = U.h0 + col;
+  if (U.np == 1) {
+    store4<T>(static_cast<T*>(prm.out) + out_row_rt(prm, U.s, h) * K::D + d, v);
+  } else {
+    const size_t at = ((size_t)U.s * prm.H + h) * prm.Pmax + U.p;
+    st_f4_policy(reinterpret_cast<float4*>(prm.ws_o + at * K::D + d), v, keep);
+  }
+}
+__device__ __forceinline__ void put_stat(const KParams& prm, const Kv4Unit& U, int col, float m, float l,
+                                         uint64_t keep) {
+  const int h = U.h0 + col;
+  const size_t at = ((size_t)U.s * prm.H + h) * prm.Pmax + U.p;
+  st_f32_policy(prm.ws_m + at, m * kLn2, keep);
+  st_f32_policy(prm.ws_l + at, l, keep);
+  if (U.np == 1 && prm.lse) prm.lse[out_row_rt(prm, U.s, h)] = m * kLn2 + logf(l);
+}
+// (A NaN sum stays NaN: only an empty row divides by nothing.)
+__device__ __forceinline__ float inverse(float l) { return l == 0.f ? 0.f : 1.f / l; }
+
+// Unused partitions: sentinels (m = -inf, l = 0).  Empty sequences: zeros (a
+// multi-query sequence is never empty: it holds its new tokens).
+template <class K, bool MQ>
+__device__ __forceinline__ void kv4_sentinels(const KParams& prm, int BS) {
+  using T = typename K::T;
+  const int S = prm.S, H = prm.H, Pmax = prm.Pmax;
+  const long long me = (long long)blockIdx.x * K::THREADS + threadIdx.x, n = (long long)gridDim.x * K::THREADS;
+  auto parts_of = [&](int s) {
+    bool bad = false;  // flagged by the prologue already
+    return (seq_tokens<MQ>(prm, s, prm.MB * BS, &bad) + prm.P - 1) / prm.P;
+  };
+  for (long long i = me; i < (long long)S * H * Pmax; i += n) {
+    const int s = (int)(i / ((long long)H * Pmax)), p = (int)(i % Pmax);
+    if (p >= parts_of(s)) {
+      prm.ws_m[i] = -INFINITY;
+      prm.ws_l[i] = 0.f;
+    }
+  }
+  if constexpr (!MQ) {
+    constexpr int D16 = K::D * 2 / 16;
+    uint4* out = static_cast<uint4*>(prm.out);
+    for (long long i = me; i < (long long)S * H * D16; i += n)
+      if (parts_of((int)(i / ((long long)H * D16))) == 0) out[i] = make_uint4(0, 0, 0, 0);
+    if (prm.lse)
+      for (long long i = me; i < (long long)S * H; i += n)
+        if (parts_of((int)(i / H)) == 0) prm.lse[i] = -INFINITY;
+  }
+}
+
+// A warp's run of a unit's stages: refills its own ring.
+template <class K>
+struct Kv4Stream {
+  const KParams& prm;
+  const Kv4Plan& pl;
+  uint32_t ring, bars;   // shared addresses of the warp's ring and barriers
+  uint32_t slot_in, slot_out, ph_out;  // next stage to fill; next to use, and its phase
+  const int32_t* row;    // the run's block ids
+  const uint8_t* base;   // the kv head's record of block 0
+  int nb, nst, next;     // blocks and stages of the run, stages issued
+  int ids, ids_next;     // lane's ids of the current window of 32 blocks, and of the one after
+  int lane;
+  uint64_t policy;
+
+  __device__ __forceinline__ Kv4Stream(const KParams& p, const Kv4Plan& l, uint32_t r, uint32_t b, int ln)
+      : prm(p), pl(l), ring(r), bars(b), slot_in(0), slot_out(0), ph_out(0), nst(0), next(0), lane(ln),
+        policy(l2_policy_evict_first()) {}
+
+  __device__ __forceinline__ int fetch(int b0) const { return b0 + lane < nb ? __ldg(row + b0 + lane) : 0; }
+
+  __device__ __forceinline__ void start(const int32_t* table, const uint8_t* cache_kv, int blocks) {
+    row = table;
+    base = cache_kv;
+    nb = blocks;
+    nst = (blocks + pl.NBLK - 1) / pl.NBLK;
+    next = 0;
+    ids = fetch(0);
+    ids_next = fetch(32);
+    ids = check_block_id(prm, ids);
+    const int n = min(nst, pl.NS);
+    for (int i = 0; i < n; ++i) issue();
+  }
+  // Fills the next stage (it is free: this warp has used it, or never filled it).
+  __device__ __forceinline__ void issue() {
+    if (next >= nst) return;
+    const int b0 = next * pl.NBLK;
+    if (b0 > 0 && b0 % 32 == 0) {
+      ids = check_block_id(prm, ids_next);
+      ids_next = fetch(b0 + 32);
+    }
+    const int n = min(pl.NBLK, nb - b0);
+    const int id = __shfl_sync(0xffffffffu, ids, b0 % 32 + (lane < n ? lane : 0));
+    const uint32_t bar = bars + 8 * slot_in;
+    if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)n * pl.rec);
+    __syncwarp();
+    if (lane < n)
+      bulk_copy_g2s(ring + slot_in * pl.stage + lane * pl.rec, base + (size_t)id * prm.KH * pl.rec, pl.rec, bar,
+                    policy);
+    slot_in = slot_in + 1 == (uint32_t)pl.NS ? 0 : slot_in + 1;
+    ++next;
+  }
+  // The next stage to use, once it has landed; 0: gave up.
+  __device__ __forceinline__ bool wait(volatile int* abort_flag) const {
+    const uint32_t bar = bars + 8 * slot_out;
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, ph_out))) return true;
+    return __all_sync(0xffffffffu, wait_bounded(bar, ph_out, abort_flag, prm.hdr + kHdrError, prm.timeout_ns,
+                                                kSiteFull, (int)slot_out));
+  }
+  __device__ __forceinline__ void used() {
+    // The stage is refilled by bulk copies (async proxy): every lane's reads
+    // of it are ordered before that by a proxy fence.
+    fence_proxy_async_smem();
+    __syncwarp();
+    slot_out = slot_out + 1 == (uint32_t)pl.NS ? 0 : slot_out + 1;
+    ph_out ^= slot_out == 0 ? 1u : 0u;
+  }
+  // After a wait that gave up: no copy of this warp stays in flight (bounded).
+  __device__ __forceinline__ void drain(int done) {
+    for (; done < next; ++done) {
+      const uint64_t t0 = global_timer_ns();
+      while (!mbar_try_wait(bars + 8 * slot_out, ph_out) && (long long)(global_timer_ns() - t0) < 100000000LL) {
+      }
+      used();
     }
   }
 };
+
+template <class K, bool MQ>
+__global__ void __launch_bounds__(K::THREADS, 1) kv4_decode_kernel(const __grid_constant__ KParams prm, int BS) {
+  using T = typename K::T;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t sbase = smem_addr(smem);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + K::OFF_FLAGS);
+  int* bad_len = reinterpret_cast<int*>(smem + K::OFF_FLAGS + 16);
+  volatile int* team_next = reinterpret_cast<volatile int*>(smem + K::OFF_NEXT);
+  int* pref = reinterpret_cast<int*>(smem + K::OFF_PREF);
+  if (tid == 0) {
+    *abort_flag = 0;
+    *bad_len = 0;
+  }
+  if (lane < K::NSMAX) mbar_init(sbase + K::OFF_BAR + (warp * K::NSMAX + lane) * 8, 1);
+  fence_mbarrier_init();
+  __syncthreads();
+  // pref[s]: partitions of the sequences before s (an exclusive scan; the warp
+  // totals are kept in the ring, not filled yet).
+  {
+    constexpr int NW = K::NC;
+    int* scan = reinterpret_cast<int*>(smem);
+    const int S = prm.S, per = (S + K::THREADS - 1) / K::THREADS;
+    const int beg = min(tid * per, S), end = min(beg + per, S);
+    bool bad = false;
+    int sum = 0;
+    for (int s = beg; s < end; ++s) {
+      const int np = (seq_tokens<MQ>(prm, s, prm.MB * BS, &bad) + prm.P - 1) / prm.P;
+      pref[s] = sum;
+      sum += np;
+    }
+    if (bad) *bad_len = 1;
+    int incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int n = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += n;
+    }
+    if (lane == 31) scan[warp] = incl;
+    __syncthreads();
+    int before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+      const int v = scan[w];
+      if (w < warp) before += v;
+      all += v;
+    }
+    for (int s = beg; s < end; ++s) pref[s] += before + incl - sum;
+    if (tid == 0) pref[S] = all;
+    fence_proxy_async_smem();  // the ring is filled by bulk copies from here on
+  }
+  __syncthreads();
+  const Kv4Plan pl = make_plan<K>(prm, BS, pref[prm.S]);
+  // A programmatic dependent of the kernel that clears the workspace header:
+  // nothing below may touch the header before it has completed.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (tid == 0 && *bad_len) atomicCAS(prm.hdr + kHdrError, 0, kErrDeviceBounds);
+
+  const Kv4Offsets off = make_offsets<K>(pl, BS);
+  const int teams = K::NC / pl.TW, team = warp / pl.TW, tw = warp % pl.TW;
+  const uint64_t keep = l2_policy_evict_last();
+  Kv4Stream<K> in(prm, pl, sbase + warp * K::RING, sbase + K::OFF_BAR + warp * K::NSMAX * 8, lane);
+  Kv4State<K, MQ> st;
+  // The first units are dealt out over the CTAs; the counter hands out the rest.
+  int u = blockIdx.x + (int)gridDim.x * team;
+  bool alive = true;
+  // The sentinels are written while the first copies fly.
+  bool sentinels = false;
+  while (u < pl.total) {
+    const Kv4Unit U = kv4_unit<K, MQ>(prm, pl, pref, BS, u);
+    const int nst = (U.nb + pl.NBLK - 1) / pl.NBLK, per = (nst + pl.TW - 1) / pl.TW;
+    const int i0 = min(tw * per, nst), b0 = i0 * pl.NBLK, nb = min(per * pl.NBLK, U.nb - b0);
+    int u_next = 0;
+    if (tw == 0 && lane == 0) u_next = atomicAdd(prm.hdr + kHdrWork, 1) + (int)gridDim.x * teams;
+    in.start(prm.bt + (size_t)U.s * prm.MB + U.t0 / BS + b0,
+             static_cast<const uint8_t*>(prm.kc) + (size_t)U.kv * pl.rec, alive ? max(nb, 0) : 0);
+    if (!sentinels) {
+      sentinels = true;
+      kv4_sentinels<K, MQ>(prm, BS);
+    }
+    st.begin_unit([&](int i) { return static_cast<const T*>(prm.q) + out_row<MQ>(prm, U.s, U.h0 + i) * K::D; }, U.nh,
+                  prm.scale_log2, lane);
+    if constexpr (MQ) st.set_limits([&](int h) { return row_limit<MQ>(prm, U.L, U.h0 + h); }, lane);
+    for (int i = 0; i < in.nst; ++i) {
+      if (!in.wait(abort_flag)) {
+        in.drain(i);
+        alive = false;
+        break;
+      }
+      const int tok = (i0 + i) * pl.TS, n = U.t1 - U.t0 - tok;
+      const uint32_t rec = in.ring + in.slot_out * pl.stage;
+      st.pass(rec, rec + off.poff, off, n, U.t0 + tok, lane);
+      if (BS == 64 && n > 32)
+        st.pass(rec + 32 * K::XB, rec + off.poff + 256, off, n - 32, U.t0 + tok + 32, lane);
+      in.used();
+      in.issue();
+    }
+    if (pl.TW == 1) {
+      if (!alive) break;
+      st.finish(
+          [&](int col, int d, const float4& v, float ls) {
+            const float inv = inverse(ls);
+            if (col < U.nh)
+              put_row<K>(prm, U, col, d, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv), keep);
+          },
+          [&](int col, float m, float ls) {
+            if (lane < 4 && col < U.nh) put_stat(prm, U, col, m, ls, keep);
+          },
+          lane);
+      u = __shfl_sync(0xffffffffu, u_next, 0);
+    } else {
+      // The team's states, each in its warp's ring (whose stages are all used).
+      float* acc = reinterpret_cast<float*>(smem + warp * K::RING);
+      float* ml = acc + K::GT * K::AROW;
+      st.finish([&](int col, int d, const float4& v, float) { *reinterpret_cast<float4*>(acc + col * K::AROW + d) = v; },
+                [&](int col, float m, float ls) {
+                  if (lane < 4) {
+                    ml[2 * col] = m;
+                    ml[2 * col + 1] = ls;
+                  }
+                },
+                lane);
+      if (tw == 0 && lane == 0) team_next[team] = *abort_flag ? pl.total : u_next;
+      named_barrier_sync(1 + team, pl.TW * 32);
+      // A slice of the rows each; the warps' states in warp order.
+      const float* first = reinterpret_cast<const float*>(smem + (warp - tw) * K::RING);
+      constexpr int D4 = K::D / 4, WR = K::RING / 4;
+      for (int i = tw * 32 + lane; i < U.nh * D4; i += pl.TW * 32) {
+        const int col = i / D4, d4 = i - col * D4;
+        float M = -INFINITY;
+        for (int w = 0; w < pl.TW; ++w) M = fmaxf(M, first[w * WR + K::GT * K::AROW + 2 * col]);
+        // (A row that sees nothing in this partition has M = -inf: its weights are 0.)
+        const float Ms = M == -INFINITY ? 0.f : M;
+        float den = 0.f;
+        float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int w = 0; w < pl.TW; ++w) {
+          const float2 s2 = *reinterpret_cast<const float2*>(first + w * WR + K::GT * K::AROW + 2 * col);
+          const float f = ex2(s2.x - Ms);
+          const float4 v = *reinterpret_cast<const float4*>(first + w * WR + col * K::AROW + 4 * d4);
+          den = fmaf(f, s2.y, den);
+          num.x = fmaf(f, v.x, num.x);
+          num.y = fmaf(f, v.y, num.y);
+          num.z = fmaf(f, v.z, num.z);
+          num.w = fmaf(f, v.w, num.w);
+        }
+        const float inv = inverse(den);
+        put_row<K>(prm, U, col, 4 * d4, make_float4(num.x * inv, num.y * inv, num.z * inv, num.w * inv), keep);
+        if (d4 == 0) put_stat(prm, U, col, M, den, keep);
+      }
+      u = team_next[team];
+      fence_proxy_async_smem();  // the rings are filled by bulk copies again
+      named_barrier_sync(1 + team, pl.TW * 32);
+    }
+    if (*abort_flag && pl.TW == 1) break;
+  }
+  if (!sentinels) kv4_sentinels<K, MQ>(prm, BS);
+  // Phase 2 may be launched once every CTA has said so or ended (it waits for
+  // this grid to complete before it reads anything).
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
 
 }  // namespace pa

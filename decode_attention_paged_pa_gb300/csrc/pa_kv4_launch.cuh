@@ -1,6 +1,5 @@
-// pa_kv4_launch.cuh -- instances of the paged decode kernel over a 4-bit cache
-// for one head size and element type: every block size, units of one or two
-// kv heads.
+// pa_kv4_launch.cuh -- launch of the 4-bit kernel's instances of one head size
+// and element type.
 #pragma once
 
 #include "pa_kv4.cuh"
@@ -8,24 +7,43 @@
 
 namespace pa {
 
-// Consumer warps: eight, as over an fp8 cache, where their registers fit under
-// the ten-warp cap (D <= 128), six otherwise.
-template <typename T, int D, int BS>
-static cudaError_t kv4_go(const KParams& prm, int kvu, int max_ctas, cudaStream_t st) {
-  constexpr int NC = D <= 128 ? 8 : 6;
-  return kvu == 2 ? launch_one<Kv4Consumer<T, D, BS, 2>, NC>(prm, max_ctas, st)
-                  : launch_one<Kv4Consumer<T, D, BS, 1>, NC>(prm, max_ctas, st);
+template <class K, bool MQ>
+static cudaError_t kv4_go(const KParams& prm, int BS, int max_ctas, cudaStream_t st) {
+  // The shared-memory opt-in is set once per kernel instance and device.
+  static std::atomic<uint64_t> opted_in{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = (dev >= 0 && dev < 64) ? (1ull << dev) : 0ull;
+  if (!bit || !(opted_in.load(std::memory_order_acquire) & bit)) {
+    e = cudaFuncSetAttribute(kv4_decode_kernel<K, MQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)K::BYTES);
+    if (e != cudaSuccess) return e;
+    opted_in.fetch_or(bit, std::memory_order_acq_rel);
+  }
+  int grid = device_sm_count();
+  if (max_ctas > 0 && max_ctas < grid) grid = max_ctas;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid, 1, 1);
+  cfg.blockDim = dim3(K::THREADS, 1, 1);
+  cfg.dynamicSmemBytes = K::BYTES;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kv4_decode_kernel<K, MQ>, prm, BS);
 }
 
 template <typename T, int D>
-static cudaError_t kv4_go_bs(const KParams& prm, int BS, int kvu, int max_ctas, cudaStream_t st) {
-  switch (BS) {
-    case 8: return kv4_go<T, D, 8>(prm, kvu, max_ctas, st);
-    case 16: return kv4_go<T, D, 16>(prm, kvu, max_ctas, st);
-    case 32: return kv4_go<T, D, 32>(prm, kvu, max_ctas, st);
-    case 64: return kv4_go<T, D, 64>(prm, kvu, max_ctas, st);
-    default: return cudaErrorInvalidValue;
+static cudaError_t kv4_go_d(const KParams& prm, int BS, int nt, int max_ctas, cudaStream_t st) {
+  if constexpr (D <= 128) {
+    if (nt == 2)
+      return prm.q_len > 1 ? kv4_go<Kv4<T, D, 2>, true>(prm, BS, max_ctas, st)
+                           : kv4_go<Kv4<T, D, 2>, false>(prm, BS, max_ctas, st);
   }
+  return prm.q_len > 1 ? kv4_go<Kv4<T, D, 1>, true>(prm, BS, max_ctas, st)
+                       : kv4_go<Kv4<T, D, 1>, false>(prm, BS, max_ctas, st);
 }
 
 }  // namespace pa

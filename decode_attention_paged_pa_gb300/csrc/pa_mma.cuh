@@ -72,7 +72,6 @@ struct MmaConsumer {
   static constexpr int NT = 1;  // 8-head column tiles per unit
   // kTma: the value block is staged by a swizzled tensor copy.
   static constexpr bool kTma = !FP8_ && BS_ >= 16;
-  static constexpr bool kRecord = false;
   static constexpr int D = D_, BS = BS_, GT = 8 * NT;
   static constexpr int KVU = KVU_;
   static_assert(KVU_ == 1 || 8 % KVU_ == 0, "kv-head groups share one 8-column tile");

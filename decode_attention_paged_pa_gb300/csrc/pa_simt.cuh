@@ -31,7 +31,6 @@ struct SimtConsumer {
   static constexpr int KV_ESZ = (int)sizeof(T_);  // bytes per cached element
   // A ring stage holds one whole block, key then value, each one bulk copy.
   static constexpr bool kTma = false;
-  static constexpr bool kRecord = false;
   static constexpr uint32_t KTILE = (uint32_t)D_ * BS_ * sizeof(T_);
   static constexpr uint32_t KREGION = KTILE, STAGE_BYTES = 2 * KTILE, STAGE_TX = 2 * KTILE;
   static constexpr int KVU = 1;  // kv heads per unit
