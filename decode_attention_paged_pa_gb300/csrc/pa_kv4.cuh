@@ -71,12 +71,18 @@ namespace pa {
 #define PA_KV4_UNITS 5
 #endif
 
-template <typename T_, int D_, int NT_>
+// TB: tokens per block, 8, 16 or 32; the last serves 64-token blocks too, as
+// two halves (the block size itself is then a launch argument).
+template <typename T_, int D_, int NT_, int TB_>
 struct Kv4 {
   using T = T_;
-  static constexpr int D = D_, NT = NT_, GT = 8 * NT_;
+  static constexpr int D = D_, NT = NT_, GT = 8 * NT_, TB = TB_;
+  static constexpr int NBLK = 32 / TB_;          // blocks per stage
   // Warps per CTA: as many as the accumulators' registers allow (128 or 255 a thread).
-  static constexpr int NC = (D_ <= 128 && NT_ == 1) ? 16 : 8;
+#ifndef PA_KV4_NC
+#define PA_KV4_NC 16
+#endif
+  static constexpr int NC = (D_ <= 128 && NT_ == 1) ? PA_KV4_NC : 8;
   static constexpr int THREADS = NC * 32;
   static constexpr int X = D_ < 128 ? D_ : 128;  // dims per slab
   static constexpr int NSLAB = D_ / X;
@@ -106,7 +112,7 @@ struct Kv4 {
 struct Kv4Plan {
   int TW;             // warps per unit
   int n_hg;           // units per partition: KH * hg_per_kv
-  int TS, NBLK;       // tokens and blocks per stage
+  int TS;             // tokens per stage
   uint32_t rec;       // bytes of a record
   uint32_t stage;     // bytes of a ring stage
   int NS;             // ring stages per warp
@@ -118,10 +124,9 @@ struct Kv4Plan {
 template <class K>
 __device__ __forceinline__ Kv4Plan make_plan(const KParams& prm, int BS, int partitions) {
   Kv4Plan pl;
-  pl.NBLK = BS < 32 ? 32 / BS : 1;
-  pl.TS = pl.NBLK * BS;
+  pl.TS = K::NBLK * BS;
   pl.rec = (uint32_t)BS * (K::D + 8);
-  pl.stage = pl.rec * pl.NBLK;
+  pl.stage = pl.rec * K::NBLK;
   pl.NS = min((int)(K::RING / pl.stage), K::NSMAX);
   pl.n_hg = prm.KH * prm.hg_per_kv;
   pl.total = partitions * pl.n_hg;
@@ -151,6 +156,17 @@ __device__ __forceinline__ void lds_b128(uint32_t a, uint32_t* v) {
                : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
                : "r"(a));
 }
+// One lane of the warp (the compiler issues what it does from uniform
+// registers; copies by several lanes would be a loop over them).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
 // fp16 products, accumulated in fp32; `first`: from zero.
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
@@ -165,40 +181,53 @@ __device__ __forceinline__ void mma_f16_first(float (&c)[4], const uint32_t (&a)
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 
-// Offsets within a stage that depend on the block size only (warp-uniform).
-struct Kv4Offsets {
-  uint32_t hd, td;    // codes: tokens 8..15 of a tile after 0..7; tile 1 after tile 0
-  uint32_t hdp, tdp;  // parameters: the same
-  uint32_t slab, voff, poff;
-};
+// Offsets within a stage: constants but for the ones that 64-token blocks
+// stretch.
 template <class K>
-__device__ __forceinline__ Kv4Offsets make_offsets(const Kv4Plan& pl, int BS) {
-  Kv4Offsets o;
-  o.hd = BS == 8 ? pl.rec : 8 * K::XB;
-  o.hdp = BS == 8 ? pl.rec : 64;
-  o.td = BS == 8 ? 2 * pl.rec : BS == 16 ? pl.rec : 16 * K::XB;
-  o.tdp = BS == 8 ? 2 * pl.rec : BS == 16 ? pl.rec : 128;
-  o.slab = (uint32_t)BS * K::XB;
-  o.voff = (uint32_t)BS * K::D / 2;
-  o.poff = (uint32_t)BS * K::D;
-  return o;
-}
+struct Kv4Offsets {
+  static constexpr uint32_t REC = (uint32_t)K::TB * (K::D + 8);
+  // Codes: tokens 8..15 of a tile after 0..7, and tile 1 after tile 0; parameters the same.
+  static constexpr uint32_t hd = K::TB == 8 ? REC : 8 * K::XB;
+  static constexpr uint32_t td = K::TB == 8 ? 2 * REC : K::TB == 16 ? REC : 16 * K::XB;
+  static constexpr uint32_t hdp = K::TB == 8 ? REC : 64;
+  static constexpr uint32_t tdp = K::TB == 8 ? 2 * REC : K::TB == 16 ? REC : 128;
+  uint32_t bs;
+  __device__ __forceinline__ explicit Kv4Offsets(int BS) : bs(K::TB < 32 ? K::TB : BS) {}
+  __device__ __forceinline__ uint32_t slab() const { return (K::TB < 32 ? K::TB : bs) * K::XB; }
+  __device__ __forceinline__ uint32_t voff() const { return (K::TB < 32 ? K::TB : bs) * (K::D / 2); }
+  __device__ __forceinline__ uint32_t poff() const { return (K::TB < 32 ? K::TB : bs) * K::D; }
+};
 
 // ---------------------------------------------------------------- a consumer warp's state
-template <class K, bool MQ>
+template <class K>
 struct Kv4State {
   using T = typename K::T;
   static constexpr int NT = K::NT, NK = K::NK, NMT = K::NMT, KW = K::KW, VW = K::VW, NSLAB = K::NSLAB;
   static constexpr uint32_t LO = 0x000f000fu, HI = 0x00f000f0u;
 
   uint32_t qb[NT][NK][2];          // Q^T fragments: the query row of column lane / 4
-  float ms[NT][2], thr[NT][2];     // reference (0 until set) and reference + 8 (-inf until set)
+  float ms[NT][2], thr[NT][2];     // reference (0 until set); 8, or -inf until it is set
   float l[NT][2], zs[NT][2];       // sums of weights; of weight * (value zero + 8 value scale)
   float qz[NT][2];                 // scale_log2 * sum(q)
   float acc[NMT][NT][4], acc8[NT][4];
   float kf;                        // score factor: scale_log2 over the operands' powers of two
   float vb, vinv;                  // see the top: a power of two, and 2^7 / vb
-  int lim[NT][2], minlim;          // MQ: positions the lane's columns see; the warp's least
+  int lim[NT][2], minlim;          // positions the lane's columns see; the warp's least
+  // The lane's offsets in a tile: key words, parameters, values of the first
+  // and second token of its slots.
+  uint32_t ko, po, vo, vo2;
+
+  __device__ __forceinline__ explicit Kv4State(int lane) {
+    const int r = lane >> 2, c = lane & 3;
+    ko = tok_lo(r) * K::XB + c * (KW * 4);
+    po = tok_lo(r) * 8;
+    // Slots 2c, 2c + 1 and 2c + 8, 2c + 9 hold tokens c, 7 - c, 8 + c, 15 - c.
+    vo = c * K::XB + r * (VW * 4);
+    vo2 = (7 - c) * K::XB + r * (VW * 4);
+    // (Opaque: kept in registers rather than computed again for every stage,
+    // which cost 30 instructions of 500.)
+    asm volatile("" : "+r"(ko), "+r"(po), "+r"(vo), "+r"(vo2));
+  }
 
   __device__ __forceinline__ static int tok_lo(int i) { return (i & 1) ? 7 - (i >> 1) : (i >> 1); }
 
@@ -240,19 +269,21 @@ struct Kv4State {
           if (q && w < K::X / 8) v[t][sl * KW + i] = __ldg(reinterpret_cast<const uint4*>(q + sl * K::X + w * 8));
         }
     }
-    float amax = 0.f;
+    // The largest |q|, as 16-bit patterns (ordered as the values are).
+    uint32_t top = 0;
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int i = 0; i < NSLAB * KW; ++i) {
-        float f[8];
-        unpack_chunk<T>(v[t][i], f);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(f[e]));
+        top = __vmaxu2(top, v[t][i].x & 0x7fff7fffu);
+        top = __vmaxu2(top, v[t][i].y & 0x7fff7fffu);
+        top = __vmaxu2(top, v[t][i].z & 0x7fff7fffu);
+        top = __vmaxu2(top, v[t][i].w & 0x7fff7fffu);
       }
+    top = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
     // 2^s brings the unit's largest |q| below 2^15; zero, subnormal, Inf or
-    // NaN leave the query unscaled.  (Positive floats are ordered as integers.)
-    const int E = (int)(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)) >> 23);
+    // NaN leave the query unscaled.
+    const int E = (__float_as_int(F16Traits<T>::to_float2(top).x) >> 23) & 0xff;
     const int s = (E == 0 || E == 255) ? 0 : max(-113, min(110, 141 - E));
     const float up = __int_as_float((127 + s) << 23), up16 = up * 0.0625f;
     kf = sl2 * __int_as_float((127 - s) << 23) * 16777216.f;
@@ -293,7 +324,7 @@ struct Kv4State {
 
   template <class F>
   __device__ __forceinline__ void set_limits(F limit_of, int lane) {
-    int least = INT_MAX_;
+    int least = 0x7fffffff;
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -303,48 +334,53 @@ struct Kv4State {
       }
     minlim = __reduce_min_sync(0xffffffffu, least);
   }
-  static constexpr int INT_MAX_ = 0x7fffffff;
 
   // 32 tokens whose first tile starts at `codes` / `params` (the record's
   // start plus the token offset of either); ntok of them lie before the
   // sequence end, the first is token tok0.
-  __device__ __forceinline__ void pass(uint32_t codes, uint32_t params, const Kv4Offsets& o, int ntok, int tok0,
+  __device__ __forceinline__ void pass(uint32_t codes, uint32_t params, const Kv4Offsets<K>& o, int ntok, int tok0,
                                        int lane) {
-    const int r = lane >> 2, c = lane & 3;
-    const int trow = tok_lo(r);
-    float z[2][NT][4];
-    float2 pv[2][2];  // (value scale, value zero) of the lane's score rows r, r + 8 of each tile
+    using O = Kv4Offsets<K>;
+    float y[2][NT][4];  // scores, less the columns' references
+    float2 pv[2][2];    // (value scale, value zero) of the lane's score rows r, r + 8 of each tile
+    const uint32_t ka = codes + ko, pa = params + po;
+    float dot[2][NT][4];
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      float c0[NT][4], c1[NT][4];
-      const uint32_t ka = codes + t * o.td + trow * K::XB + c * (KW * 4);
+    for (int sl = 0; sl < NSLAB; ++sl) {
+      uint32_t wl[2][KW], wh[2][KW];
 #pragma unroll
-      for (int sl = 0; sl < NSLAB; ++sl) {
-        uint32_t wl[KW], wh[KW];
-        key_words(ka + sl * o.slab, wl);
-        key_words(ka + sl * o.slab + o.hd, wh);
+      for (int t = 0; t < 2; ++t) {
+        key_words(ka + t * O::td + sl * o.slab(), wl[t]);
+        key_words(ka + t * O::td + sl * o.slab() + O::hd, wh[t]);
+      }
+      // (The tiles' chains of dependent products run side by side.)
 #pragma unroll
-        for (int i = 0; i < KW; ++i) {
-          const int ks = (sl * KW + i) * 2;
-          const uint32_t a[4] = {wl[i] & LO, wh[i] & LO, wl[i] & HI, wh[i] & HI};
-          const uint32_t xl = wl[i] >> 8, xh = wh[i] >> 8;
-          const uint32_t b[4] = {xl & LO, xh & LO, xl & HI, xh & HI};
+      for (int i = 0; i < KW; ++i) {
+        const int ks = (sl * KW + i) * 2;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const uint32_t a[4] = {wl[t][i] & LO, wh[t][i] & LO, wl[t][i] & HI, wh[t][i] & HI};
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-            if (ks == 0) {
-              mma_f16_first(c0[n], a, qb[n][ks][0], qb[n][ks][1]);
-              mma_f16_first(c1[n], b, qb[n][ks + 1][0], qb[n][ks + 1][1]);
-            } else {
-              mma_f16(c0[n], a, qb[n][ks][0], qb[n][ks][1]);
-              mma_f16(c1[n], b, qb[n][ks + 1][0], qb[n][ks + 1][1]);
-            }
+            if (ks == 0) mma_f16_first(dot[t][n], a, qb[n][ks][0], qb[n][ks][1]);
+            else mma_f16(dot[t][n], a, qb[n][ks][0], qb[n][ks][1]);
           }
         }
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const uint32_t xl = wl[t][i] >> 8, xh = wh[t][i] >> 8;
+          const uint32_t b[4] = {xl & LO, xh & LO, xl & HI, xh & HI};
+#pragma unroll
+          for (int n = 0; n < NT; ++n) mma_f16(dot[t][n], b, qb[n][ks + 1][0], qb[n][ks + 1][1]);
+        }
       }
+    }
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         uint32_t wk, wv;
-        lds_b64(params + t * o.tdp + (h ? o.hdp : 0u) + trow * 8, wk, wv);
+        lds_b64(pa + t * O::tdp + (h ? O::hdp : 0u), wk, wv);
         const float2 k = F16Traits<T>::to_float2(wk);
         pv[t][h] = F16Traits<T>::to_float2(wv);
         const float kx = k.x * kf;
@@ -352,13 +388,14 @@ struct Kv4State {
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int j = 0; j < 2; ++j)
-            z[t][n][2 * h + j] = fmaf(kx, c0[n][2 * h + j] + c1[n][2 * h + j], k.y * qz[n][j]);
+            y[t][n][2 * h + j] = fmaf(kx, dot[t][n][2 * h + j], fmaf(k.y, qz[n][j], -ms[n][j]));
       }
     }
     // Slots past the sequence end hold arbitrary parameters, and causal rows
     // stop earlier: their scores become -inf, and (below) their weights 0.
-    const bool full = ntok >= 32 && (!MQ || tok0 + 32 <= minlim);
+    const bool full = ntok >= 32 && tok0 + 32 <= minlim;
     if (!full) {
+      const int trow = tok_lo(lane >> 2);
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -369,7 +406,7 @@ struct Kv4State {
           for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int j = 0; j < 2; ++j)
-              if (tt >= ntok || (MQ && tok0 + tt >= lim[n][j])) z[t][n][2 * h + j] = -INFINITY;
+              if (tt >= ntok || tok0 + tt >= lim[n][j]) y[t][n][2 * h + j] = -INFINITY;
         }
     }
     float vm = fmaxf(fmaxf(fabsf(pv[0][0].x), fabsf(pv[0][1].x)), fmaxf(fabsf(pv[1][0].x), fabsf(pv[1][1].x)));
@@ -378,16 +415,17 @@ struct Kv4State {
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int j = 0; j < 2; ++j)
-        raise |= fmaxf(fmaxf(z[0][n][j], z[0][n][j + 2]), fmaxf(z[1][n][j], z[1][n][j + 2])) > thr[n][j];
-    if (__any_sync(0xffffffffu, raise)) raise_bounds(z, pv);
-    if (full) weigh<false>(z, pv, codes + o.voff, o, r, c);
-    else weigh<true>(z, pv, codes + o.voff, o, r, c);
+        raise |= fmaxf(fmaxf(y[0][n][j], y[0][n][j + 2]), fmaxf(y[1][n][j], y[1][n][j + 2])) > thr[n][j];
+    if (__any_sync(0xffffffffu, raise)) raise_bounds(y, pv);
+    if (full) weigh<false>(y, pv);
+    else weigh<true>(y, pv);
+    values(y, codes + o.voff(), o);
   }
 
   // New references, and a new bound on the value scales (finite ones: a NaN
-  // or Inf goes through to the output whatever the bound is); the sums and
-  // accumulators follow.
-  __device__ __forceinline__ void raise_bounds(const float (&z)[2][NT][4], const float2 (&pv)[2][2]) {
+  // or Inf goes through to the output whatever the bound is; four times the
+  // largest, so that few items raise it); the sums and accumulators follow.
+  __device__ __forceinline__ void raise_bounds(float (&y)[2][NT][4], const float2 (&pv)[2][2]) {
     float vm = 0.f;
 #pragma unroll
     for (int t = 0; t < 2; ++t)
@@ -399,7 +437,7 @@ struct Kv4State {
     const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(vm));
     float down = 1.f;
     if (__uint_as_float(top) >= vb) {
-      const float nb = __uint_as_float(min((top >> 23) + 1u, 254u) << 23);  // the power of two above
+      const float nb = __uint_as_float(min((top >> 23) + 3u, 254u) << 23);
       down = vb / nb;
       vb = nb;
       vinv = 128.f / nb;
@@ -409,17 +447,22 @@ struct Kv4State {
       float a[2];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        float bm = fmaxf(fmaxf(z[0][n][j], z[0][n][j + 2]), fmaxf(z[1][n][j], z[1][n][j + 2]));
+        float bm = fmaxf(fmaxf(y[0][n][j], y[0][n][j + 2]), fmaxf(y[1][n][j], y[1][n][j + 2]));
         bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 4));
         bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 8));
         bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 16));
         const bool set = thr[n][j] != -INFINITY;
         a[j] = 1.f;
-        if (bm != -INFINITY) {  // (a row that has seen no position yet stays unset)
-          const float nm = set ? fmaxf(ms[n][j], bm) : bm;
-          if (set) a[j] = ex2(ms[n][j] - nm);
-          ms[n][j] = nm;
-          thr[n][j] = nm + 8.f;
+        // (A row that has seen no position yet stays unset; a set reference only rises.)
+        if (bm != -INFINITY && (!set || bm > 0.f)) {
+          if (set) a[j] = ex2(-bm);
+          ms[n][j] += bm;
+          thr[n][j] = 8.f;
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            y[t][n][j] -= bm;
+            y[t][n][j + 2] -= bm;
+          }
         }
         l[n][j] *= a[j];
         zs[n][j] *= a[j];
@@ -439,44 +482,49 @@ struct Kv4State {
     }
   }
 
+  // Scores into weights (over the value scales' bound), and their sums.
   template <bool MASK>
-  __device__ __forceinline__ void weigh(const float (&z)[2][NT][4], const float2 (&pv)[2][2], uint32_t values,
-                                        const Kv4Offsets& o, int r, int c) {
+  __device__ __forceinline__ void weigh(float (&y)[2][NT][4], const float2 (&pv)[2][2]) {
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      uint32_t b0[NT], b1[NT];
-      const float zc[2] = {fmaf(8.f, pv[t][0].x, pv[t][0].y), fmaf(8.f, pv[t][1].x, pv[t][1].y)};
-      const float vw[2] = {pv[t][0].x * vinv, pv[t][1].x * vinv};
+    for (int t = 0; t < 2; ++t)
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        float w[4];
+      for (int h = 0; h < 2; ++h) {
+        const float zc = fmaf(8.f, pv[t][h].x, pv[t][h].y), vw = pv[t][h].x * vinv;
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            const float x = z[t][n][2 * h + j];
-            const float p = ex2(x - ms[n][j]);
+            const float x = y[t][n][2 * h + j];
+            const float p = ex2(x);
             l[n][j] += p;
             // A masked position weighs nothing, whatever its parameters hold.
             const bool out = MASK && x == -INFINITY;
-            zs[n][j] = out ? zs[n][j] : fmaf(p, zc[h], zs[n][j]);
-            w[2 * h + j] = out ? 0.f : p * vw[h];
+            zs[n][j] = out ? zs[n][j] : fmaf(p, zc, zs[n][j]);
+            y[t][n][2 * h + j] = out ? 0.f : p * vw;
           }
-        b0[n] = movmatrix_trans(F16Traits<__half>::pack(w[0], w[1]));
-        b1[n] = movmatrix_trans(F16Traits<__half>::pack(w[2], w[3]));
+      }
+  }
+
+  __device__ __forceinline__ void values(const float (&w)[2][NT][4], uint32_t codes, const Kv4Offsets<K>& o) {
+    using O = Kv4Offsets<K>;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      uint32_t b0[NT], b1[NT];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        b0[n] = movmatrix_trans(F16Traits<__half>::pack(w[t][n][0], w[t][n][1]));
+        b1[n] = movmatrix_trans(F16Traits<__half>::pack(w[t][n][2], w[t][n][3]));
         const uint32_t eight[4] = {0x00080008u, 0x00080008u, 0x00080008u, 0x00080008u};
         mma_f16(acc8[n], eight, b0[n], b1[n]);
       }
-      // Slots 2c, 2c + 1 and 2c + 8, 2c + 9 hold tokens c, 7 - c, 8 + c, 15 - c.
-      const uint32_t va = values + t * o.td + c * K::XB + r * (VW * 4);
-      const uint32_t vd = (7 - 2 * c) * K::XB;
+      const uint32_t va = codes + vo + t * O::td, vd = codes + vo2 + t * O::td;
 #pragma unroll
       for (int sl = 0; sl < NSLAB; ++sl) {
         uint32_t wa[2], wb[2], wc[2], wd[2];
-        value_words(va + sl * o.slab, wa);
-        value_words(va + sl * o.slab + vd, wb);
-        value_words(va + sl * o.slab + o.hd, wc);
-        value_words(va + sl * o.slab + o.hd + vd, wd);
+        value_words(va + sl * o.slab(), wa);
+        value_words(vd + sl * o.slab(), wb);
+        value_words(va + sl * o.slab() + O::hd, wc);
+        value_words(vd + sl * o.slab() + O::hd, wd);
 #pragma unroll
         for (int half = 0; half < VW; ++half) {
           // VW = 2: rows r and r + 8 of tile mt hold nibble mt of the two
@@ -513,10 +561,10 @@ struct Kv4State {
   }
 
   // The warp's state of the unit, four dims at a time: sink(col, d, v) with
-  // the unnormalised sums of column col's dims d .. d + 3, and stat(col, m, l)
-  // once per column.
-  template <class Sink, class Stat>
-  __device__ __forceinline__ void finish(Sink sink, Stat stat, int lane) {
+  // the sums of column col's dims d .. d + 3, times scale(l), and
+  // stat(col, m, l) once per column.
+  template <class Scale, class Sink, class Stat>
+  __device__ __forceinline__ void finish(Scale scale, Sink sink, Stat stat, int lane) {
     const int r = lane >> 2, c = lane & 3;
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -532,6 +580,7 @@ struct Kv4State {
         stat(col, thr[n][j] == -INFINITY ? -INFINITY : ms[n][j], ls);
         // Tiles of odd nibbles carry 2^-20 instead of 2^-24.
         const float e8 = acc8[n][j], e16 = 16.f * e8;
+        const float f = scale(ls), vbf = vb * f, zf = zz * f;
 #pragma unroll
         for (int sl = 0; sl < NSLAB; ++sl)
 #pragma unroll
@@ -542,23 +591,28 @@ struct Kv4State {
               const int d = VW == 2 ? 16 * r + 8 * h + 4 * q : 8 * r + 4 * h;
               const int mt = sl * K::MTS + 4 * q;
               float4 v;
-              v.x = fmaf((acc[mt][n][2 * h + j] - e8) * 131072.f, vb, zz);
-              v.y = fmaf((acc[mt + 1][n][2 * h + j] - e16) * 8192.f, vb, zz);
-              v.z = fmaf((acc[mt + 2][n][2 * h + j] - e8) * 131072.f, vb, zz);
-              v.w = fmaf((acc[mt + 3][n][2 * h + j] - e16) * 8192.f, vb, zz);
-              if (d < K::X) sink(col, sl * K::X + d, v, ls);
+              v.x = fmaf((acc[mt][n][2 * h + j] - e8) * 131072.f, vbf, zf);
+              v.y = fmaf((acc[mt + 1][n][2 * h + j] - e16) * 8192.f, vbf, zf);
+              v.z = fmaf((acc[mt + 2][n][2 * h + j] - e8) * 131072.f, vbf, zf);
+              v.w = fmaf((acc[mt + 3][n][2 * h + j] - e16) * 8192.f, vbf, zf);
+              if (d < K::X) sink(col, sl * K::X + d, v);
             }
       }
   }
 };
 
 // ---------------------------------------------------------------- units
+// Cached tokens of sequence s, clamped to what its table row can hold (out of
+// range lengths are recorded by the prologue).
+__device__ __forceinline__ int kv4_tokens(const KParams& prm, int s, int BS) {
+  return min(max(prm.lens[s], 0), prm.MB * BS);
+}
 // Unit u = (partition, kv head, row group), partitions numbered in batch
 // order: sequence s holds pref[s] .. pref[s + 1] - 1.
 struct Kv4Unit {
   int s, p, np, L, t0, t1, nb, kv, h0, nh;
 };
-template <class K, bool MQ>
+template <class K>
 __device__ __forceinline__ Kv4Unit kv4_unit(const KParams& prm, const Kv4Plan& pl, const int* pref, int BS, int u) {
   Kv4Unit U;
   const int pair = u / pl.n_hg, hg = u - pair * pl.n_hg;
@@ -567,14 +621,13 @@ __device__ __forceinline__ Kv4Unit kv4_unit(const KParams& prm, const Kv4Plan& p
     const int mid = (lo + hi) >> 1;
     if (pref[mid] <= pair) lo = mid; else hi = mid;
   }
-  bool bad = false;  // flagged by the prologue already
   U.s = lo;
   U.p = pair - pref[lo];
   U.np = pref[lo + 1] - pref[lo];
-  U.L = seq_tokens<MQ>(prm, lo, prm.MB * BS, &bad);
+  U.L = kv4_tokens(prm, lo, BS);
   U.t0 = U.p * prm.P;
   U.t1 = min(U.t0 + prm.P, U.L);
-  U.nb = (U.t1 - U.t0 + BS - 1) / BS;
+  U.nb = (U.t1 - U.t0 + BS - 1) >> (__ffs(BS) - 1);
   U.kv = hg / prm.hg_per_kv;
   const int part = hg - U.kv * prm.hg_per_kv;
   U.h0 = U.kv * prm.G + part * K::GT;
@@ -609,15 +662,12 @@ __device__ __forceinline__ float inverse(float l) { return l == 0.f ? 0.f : 1.f 
 
 // Unused partitions: sentinels (m = -inf, l = 0).  Empty sequences: zeros (a
 // multi-query sequence is never empty: it holds its new tokens).
-template <class K, bool MQ>
+template <class K>
 __device__ __forceinline__ void kv4_sentinels(const KParams& prm, int BS) {
   using T = typename K::T;
   const int S = prm.S, H = prm.H, Pmax = prm.Pmax;
   const long long me = (long long)blockIdx.x * K::THREADS + threadIdx.x, n = (long long)gridDim.x * K::THREADS;
-  auto parts_of = [&](int s) {
-    bool bad = false;  // flagged by the prologue already
-    return (seq_tokens<MQ>(prm, s, prm.MB * BS, &bad) + prm.P - 1) / prm.P;
-  };
+  auto parts_of = [&](int s) { return (kv4_tokens(prm, s, BS) + prm.P - 1) / prm.P; };
   for (long long i = me; i < (long long)S * H * Pmax; i += n) {
     const int s = (int)(i / ((long long)H * Pmax)), p = (int)(i % Pmax);
     if (p >= parts_of(s)) {
@@ -625,7 +675,7 @@ __device__ __forceinline__ void kv4_sentinels(const KParams& prm, int BS) {
       prm.ws_l[i] = 0.f;
     }
   }
-  if constexpr (!MQ) {
+  if (prm.q_len == 1) {
     constexpr int D16 = K::D * 2 / 16;
     uint4* out = static_cast<uint4*>(prm.out);
     for (long long i = me; i < (long long)S * H * D16; i += n)
@@ -636,88 +686,118 @@ __device__ __forceinline__ void kv4_sentinels(const KParams& prm, int BS) {
   }
 }
 
-// A warp's run of a unit's stages: refills its own ring.
+// (Out of line: a wait that does not succeed at once has time for a call.)
+static __device__ __noinline__ bool kv4_wait_slow(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* err_word,
+                                           long long timeout_ns, int slot) {
+  return __all_sync(0xffffffffu, wait_bounded(bar, parity, abort_flag, err_word, timeout_ns, kSiteFull, slot));
+}
+
+// A bulk copy into this CTA's own shared memory (bulk_copy_g2s names its
+// destination in the cluster's address space, which costs a few instructions).
+__device__ __forceinline__ void bulk_copy_cta(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar,
+                                              uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1], %2, [%3], %4;" ::"r"(dst),
+      "l"(src), "r"(bytes), "r"(bar), "l"(policy)
+      : "memory");
+}
+
+// A warp's run of a unit's stages: refills its own ring.  (Everything but the
+// ids is the same in all lanes.)
 template <class K>
 struct Kv4Stream {
-  const KParams& prm;
-  const Kv4Plan& pl;
-  uint32_t ring, bars;   // shared addresses of the warp's ring and barriers
-  uint32_t slot_in, slot_out, ph_out;  // next stage to fill; next to use, and its phase
+  uint32_t in, out;      // byte offsets in the ring of the next stage to fill, and of the next to use
+  uint32_t bar_in, bar_out, ph_out;  // their barriers, and the phase of the latter
+  int nb, left;          // blocks of the run; those not asked for yet
+  int ids, ids_next;     // lane's ids of the current window of 32 blocks, and of the one after
+  uint32_t ring, ring_bytes, bars;   // shared addresses of the warp's ring and barriers; bytes in use
+  uint32_t rec, stage;
   const int32_t* row;    // the run's block ids
   const uint8_t* base;   // the kv head's record of block 0
-  int nb, nst, next;     // blocks and stages of the run, stages issued
-  int ids, ids_next;     // lane's ids of the current window of 32 blocks, and of the one after
-  int lane;
+  size_t block_bytes;    // of all kv heads
   uint64_t policy;
 
-  __device__ __forceinline__ Kv4Stream(const KParams& p, const Kv4Plan& l, uint32_t r, uint32_t b, int ln)
-      : prm(p), pl(l), ring(r), bars(b), slot_in(0), slot_out(0), ph_out(0), nst(0), next(0), lane(ln),
+  __device__ __forceinline__ Kv4Stream(const KParams& prm, const Kv4Plan& pl, uint32_t r, uint32_t b)
+      : in(0), out(0), bar_in(b), bar_out(b), ph_out(0), nb(0), left(0), ring(r), ring_bytes(pl.NS * pl.stage),
+        bars(b), rec(pl.rec), stage(pl.stage), block_bytes((size_t)prm.KH * pl.rec),
         policy(l2_policy_evict_first()) {}
 
-  __device__ __forceinline__ int fetch(int b0) const { return b0 + lane < nb ? __ldg(row + b0 + lane) : 0; }
+  __device__ __forceinline__ int fetch(int b0, int lane) const { return b0 + lane < nb ? __ldg(row + b0 + lane) : 0; }
 
-  __device__ __forceinline__ void start(const int32_t* table, const uint8_t* cache_kv, int blocks) {
+  __device__ __forceinline__ void start(const KParams& prm, const int32_t* table, const uint8_t* cache_kv, int blocks,
+                                        int NS, int lane) {
     row = table;
     base = cache_kv;
-    nb = blocks;
-    nst = (blocks + pl.NBLK - 1) / pl.NBLK;
-    next = 0;
-    ids = fetch(0);
-    ids_next = fetch(32);
+    nb = left = blocks;
+    ids = fetch(0, lane);
+    ids_next = fetch(32, lane);
     ids = check_block_id(prm, ids);
-    const int n = min(nst, pl.NS);
-    for (int i = 0; i < n; ++i) issue();
+    for (int i = 0; i < NS; ++i) issue(prm, lane);
   }
   // Fills the next stage (it is free: this warp has used it, or never filled it).
-  __device__ __forceinline__ void issue() {
-    if (next >= nst) return;
-    const int b0 = next * pl.NBLK;
-    if (b0 > 0 && b0 % 32 == 0) {
+  __device__ __forceinline__ void issue(const KParams& prm, int lane) {
+    if (left <= 0) return;
+    const int b0 = nb - left, w = b0 & 31;
+    if (w == 0 && b0 > 0) {
       ids = check_block_id(prm, ids_next);
-      ids_next = fetch(b0 + 32);
+      ids_next = fetch(b0 + 32, lane);
     }
-    const int n = min(pl.NBLK, nb - b0);
-    const int id = __shfl_sync(0xffffffffu, ids, b0 % 32 + (lane < n ? lane : 0));
-    const uint32_t bar = bars + 8 * slot_in;
-    if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)n * pl.rec);
-    __syncwarp();
-    if (lane < n)
-      bulk_copy_g2s(ring + slot_in * pl.stage + lane * pl.rec, base + (size_t)id * prm.KH * pl.rec, pl.rec, bar,
-                    policy);
-    slot_in = slot_in + 1 == (uint32_t)pl.NS ? 0 : slot_in + 1;
-    ++next;
+    int id[K::NBLK];
+#pragma unroll
+    for (int k = 0; k < K::NBLK; ++k) id[k] = __shfl_sync(0xffffffffu, ids, w + k);
+    const int n = min(K::NBLK, left);
+    if (elect_one()) {
+      mbar_arrive_expect_tx(bar_in, (uint32_t)n * rec);
+#pragma unroll
+      for (int k = 0; k < K::NBLK; ++k)
+        if (k < n) bulk_copy_cta(ring + in + k * rec, base + (uint32_t)id[k] * block_bytes, rec, bar_in, policy);
+    }
+    left -= K::NBLK;
+    in += stage;
+    bar_in += 8;
+    if (in == ring_bytes) {
+      in = 0;
+      bar_in = bars;
+    }
   }
-  // The next stage to use, once it has landed; 0: gave up.
-  __device__ __forceinline__ bool wait(volatile int* abort_flag) const {
-    const uint32_t bar = bars + 8 * slot_out;
-    if (__all_sync(0xffffffffu, mbar_try_wait(bar, ph_out))) return true;
-    return __all_sync(0xffffffffu, wait_bounded(bar, ph_out, abort_flag, prm.hdr + kHdrError, prm.timeout_ns,
-                                                kSiteFull, (int)slot_out));
+  // Waits for the next stage to land; false: gave up.
+  __device__ __forceinline__ bool wait(const KParams& prm, volatile int* abort_flag) const {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar_out, ph_out))) return true;
+    return kv4_wait_slow(bar_out, ph_out, abort_flag, prm.hdr + kHdrError, prm.timeout_ns, (int)(out / stage));
   }
   __device__ __forceinline__ void used() {
     // The stage is refilled by bulk copies (async proxy): every lane's reads
     // of it are ordered before that by a proxy fence.
     fence_proxy_async_smem();
     __syncwarp();
-    slot_out = slot_out + 1 == (uint32_t)pl.NS ? 0 : slot_out + 1;
-    ph_out ^= slot_out == 0 ? 1u : 0u;
+    out += stage;
+    bar_out += 8;
+    if (out == ring_bytes) {
+      out = 0;
+      bar_out = bars;
+      ph_out ^= 1u;
+    }
   }
-  // After a wait that gave up: no copy of this warp stays in flight (bounded).
+  // After a wait that gave up at stage `done` of the run: no copy of this warp
+  // stays in flight (bounded).
   __device__ __forceinline__ void drain(int done) {
-    for (; done < next; ++done) {
+    const int asked = (nb - max(left, 0) + K::NBLK - 1) / K::NBLK;
+    for (; done < asked; ++done) {
       const uint64_t t0 = global_timer_ns();
-      while (!mbar_try_wait(bars + 8 * slot_out, ph_out) && (long long)(global_timer_ns() - t0) < 100000000LL) {
+      while (!mbar_try_wait(bar_out, ph_out) && (long long)(global_timer_ns() - t0) < 100000000LL) {
       }
       used();
     }
   }
 };
 
-template <class K, bool MQ>
+template <class K>
 __global__ void __launch_bounds__(K::THREADS, 1) kv4_decode_kernel(const __grid_constant__ KParams prm, int BS) {
   using T = typename K::T;
   extern __shared__ __align__(1024) uint8_t smem[];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // (The warp index by a shuffle: known to be the same in all lanes.)
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const uint32_t sbase = smem_addr(smem);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + K::OFF_FLAGS);
   int* bad_len = reinterpret_cast<int*>(smem + K::OFF_FLAGS + 16);
@@ -740,7 +820,9 @@ __global__ void __launch_bounds__(K::THREADS, 1) kv4_decode_kernel(const __grid_
     bool bad = false;
     int sum = 0;
     for (int s = beg; s < end; ++s) {
-      const int np = (seq_tokens<MQ>(prm, s, prm.MB * BS, &bad) + prm.P - 1) / prm.P;
+      // (A multi-query sequence holds its q_len new tokens.)
+      bad |= prm.lens[s] < (prm.q_len > 1 ? prm.q_len : 0) || prm.lens[s] > prm.MB * BS;
+      const int np = (kv4_tokens(prm, s, BS) + prm.P - 1) / prm.P;
       pref[s] = sum;
       sum += np;
     }
@@ -771,52 +853,53 @@ __global__ void __launch_bounds__(K::THREADS, 1) kv4_decode_kernel(const __grid_
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (tid == 0 && *bad_len) atomicCAS(prm.hdr + kHdrError, 0, kErrDeviceBounds);
 
-  const Kv4Offsets off = make_offsets<K>(pl, BS);
-  const int teams = K::NC / pl.TW, team = warp / pl.TW, tw = warp % pl.TW;
+  const Kv4Offsets<K> off(BS);
+  const int ltw = __ffs(pl.TW) - 1, lbs = __ffs(BS) - 1;
+  const int teams = K::NC >> ltw, team = warp >> ltw, tw = warp & (pl.TW - 1);
   const uint64_t keep = l2_policy_evict_last();
-  Kv4Stream<K> in(prm, pl, sbase + warp * K::RING, sbase + K::OFF_BAR + warp * K::NSMAX * 8, lane);
-  Kv4State<K, MQ> st;
+  Kv4Stream<K> in(prm, pl, sbase + warp * K::RING, sbase + K::OFF_BAR + warp * K::NSMAX * 8);
+  Kv4State<K> st(lane);
   // The first units are dealt out over the CTAs; the counter hands out the rest.
   int u = blockIdx.x + (int)gridDim.x * team;
   bool alive = true;
   // The sentinels are written while the first copies fly.
   bool sentinels = false;
   while (u < pl.total) {
-    const Kv4Unit U = kv4_unit<K, MQ>(prm, pl, pref, BS, u);
-    const int nst = (U.nb + pl.NBLK - 1) / pl.NBLK, per = (nst + pl.TW - 1) / pl.TW;
-    const int i0 = min(tw * per, nst), b0 = i0 * pl.NBLK, nb = min(per * pl.NBLK, U.nb - b0);
+    const Kv4Unit U = kv4_unit<K>(prm, pl, pref, BS, u);
+    const int nst = (U.nb + K::NBLK - 1) / K::NBLK, per = (nst + pl.TW - 1) >> ltw;
+    const int i0 = min(tw * per, nst), b0 = i0 * K::NBLK, nb = min(per * K::NBLK, U.nb - b0);
     int u_next = 0;
     if (tw == 0 && lane == 0) u_next = atomicAdd(prm.hdr + kHdrWork, 1) + (int)gridDim.x * teams;
-    in.start(prm.bt + (size_t)U.s * prm.MB + U.t0 / BS + b0,
-             static_cast<const uint8_t*>(prm.kc) + (size_t)U.kv * pl.rec, alive ? max(nb, 0) : 0);
+    const int blocks = alive ? max(nb, 0) : 0, stages = (blocks + K::NBLK - 1) / K::NBLK;
+    in.start(prm, prm.bt + (size_t)U.s * prm.MB + (U.t0 >> lbs) + b0,
+             static_cast<const uint8_t*>(prm.kc) + (size_t)U.kv * pl.rec, blocks, pl.NS, lane);
     if (!sentinels) {
       sentinels = true;
-      kv4_sentinels<K, MQ>(prm, BS);
+      kv4_sentinels<K>(prm, BS);
     }
-    st.begin_unit([&](int i) { return static_cast<const T*>(prm.q) + out_row<MQ>(prm, U.s, U.h0 + i) * K::D; }, U.nh,
+    st.begin_unit([&](int i) { return static_cast<const T*>(prm.q) + out_row_rt(prm, U.s, U.h0 + i) * K::D; }, U.nh,
                   prm.scale_log2, lane);
-    if constexpr (MQ) st.set_limits([&](int h) { return row_limit<MQ>(prm, U.L, U.h0 + h); }, lane);
-    for (int i = 0; i < in.nst; ++i) {
-      if (!in.wait(abort_flag)) {
+    if (prm.q_len > 1) st.set_limits([&](int h) { return row_limit<true>(prm, U.L, U.h0 + h); }, lane);
+    else st.set_limits([&](int) { return U.L; }, lane);
+    int n = U.t1 - U.t0 - i0 * pl.TS, tok = U.t0 + i0 * pl.TS;  // tokens from the stage on; its first
+    for (int i = 0; i < stages; ++i, n -= pl.TS, tok += pl.TS) {
+      if (!in.wait(prm, abort_flag)) {
         in.drain(i);
         alive = false;
         break;
       }
-      const int tok = (i0 + i) * pl.TS, n = U.t1 - U.t0 - tok;
-      const uint32_t rec = in.ring + in.slot_out * pl.stage;
-      st.pass(rec, rec + off.poff, off, n, U.t0 + tok, lane);
-      if (BS == 64 && n > 32)
-        st.pass(rec + 32 * K::XB, rec + off.poff + 256, off, n - 32, U.t0 + tok + 32, lane);
+      const uint32_t rec = in.ring + in.out;
+      st.pass(rec, rec + off.poff(), off, n, tok, lane);
+      if (K::TB == 32 && BS == 64 && n > 32)
+        st.pass(rec + 32 * K::XB, rec + off.poff() + 256, off, n - 32, tok + 32, lane);
       in.used();
-      in.issue();
+      in.issue(prm, lane);
     }
     if (pl.TW == 1) {
       if (!alive) break;
-      st.finish(
-          [&](int col, int d, const float4& v, float ls) {
-            const float inv = inverse(ls);
-            if (col < U.nh)
-              put_row<K>(prm, U, col, d, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv), keep);
+      st.finish([](float ls) { return inverse(ls); },
+          [&](int col, int d, const float4& v) {
+            if (col < U.nh) put_row<K>(prm, U, col, d, v, keep);
           },
           [&](int col, float m, float ls) {
             if (lane < 4 && col < U.nh) put_stat(prm, U, col, m, ls, keep);
@@ -827,7 +910,8 @@ __global__ void __launch_bounds__(K::THREADS, 1) kv4_decode_kernel(const __grid_
       // The team's states, each in its warp's ring (whose stages are all used).
       float* acc = reinterpret_cast<float*>(smem + warp * K::RING);
       float* ml = acc + K::GT * K::AROW;
-      st.finish([&](int col, int d, const float4& v, float) { *reinterpret_cast<float4*>(acc + col * K::AROW + d) = v; },
+      st.finish([](float) { return 1.f; },
+                [&](int col, int d, const float4& v) { *reinterpret_cast<float4*>(acc + col * K::AROW + d) = v; },
                 [&](int col, float m, float ls) {
                   if (lane < 4) {
                     ml[2 * col] = m;
@@ -868,7 +952,7 @@ __global__ void __launch_bounds__(K::THREADS, 1) kv4_decode_kernel(const __grid_
     }
     if (*abort_flag && pl.TW == 1) break;
   }
-  if (!sentinels) kv4_sentinels<K, MQ>(prm, BS);
+  if (!sentinels) kv4_sentinels<K>(prm, BS);
   // Phase 2 may be launched once every CTA has said so or ended (it waits for
   // this grid to complete before it reads anything).
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

@@ -7,7 +7,7 @@
 
 namespace pa {
 
-template <class K, bool MQ>
+template <class K>
 static cudaError_t kv4_go(const KParams& prm, int BS, int max_ctas, cudaStream_t st) {
   // The shared-memory opt-in is set once per kernel instance and device.
   static std::atomic<uint64_t> opted_in{0};
@@ -16,7 +16,7 @@ static cudaError_t kv4_go(const KParams& prm, int BS, int max_ctas, cudaStream_t
   if (e != cudaSuccess) return e;
   const uint64_t bit = (dev >= 0 && dev < 64) ? (1ull << dev) : 0ull;
   if (!bit || !(opted_in.load(std::memory_order_acquire) & bit)) {
-    e = cudaFuncSetAttribute(kv4_decode_kernel<K, MQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)K::BYTES);
+    e = cudaFuncSetAttribute(kv4_decode_kernel<K>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)K::BYTES);
     if (e != cudaSuccess) return e;
     opted_in.fetch_or(bit, std::memory_order_acq_rel);
   }
@@ -32,18 +32,26 @@ static cudaError_t kv4_go(const KParams& prm, int BS, int max_ctas, cudaStream_t
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv4_decode_kernel<K, MQ>, prm, BS);
+  return cudaLaunchKernelEx(&cfg, kv4_decode_kernel<K>, prm, BS);
+}
+
+template <typename T, int D, int NT>
+static cudaError_t kv4_go_bs(const KParams& prm, int BS, int max_ctas, cudaStream_t st) {
+  switch (BS) {
+    case 8: return kv4_go<Kv4<T, D, NT, 8>>(prm, BS, max_ctas, st);
+    case 16: return kv4_go<Kv4<T, D, NT, 16>>(prm, BS, max_ctas, st);
+    case 32:
+    case 64: return kv4_go<Kv4<T, D, NT, 32>>(prm, BS, max_ctas, st);
+    default: return cudaErrorInvalidValue;
+  }
 }
 
 template <typename T, int D>
 static cudaError_t kv4_go_d(const KParams& prm, int BS, int nt, int max_ctas, cudaStream_t st) {
   if constexpr (D <= 128) {
-    if (nt == 2)
-      return prm.q_len > 1 ? kv4_go<Kv4<T, D, 2>, true>(prm, BS, max_ctas, st)
-                           : kv4_go<Kv4<T, D, 2>, false>(prm, BS, max_ctas, st);
+    if (nt == 2) return kv4_go_bs<T, D, 2>(prm, BS, max_ctas, st);
   }
-  return prm.q_len > 1 ? kv4_go<Kv4<T, D, 1>, true>(prm, BS, max_ctas, st)
-                       : kv4_go<Kv4<T, D, 1>, false>(prm, BS, max_ctas, st);
+  return kv4_go_bs<T, D, 1>(prm, BS, max_ctas, st);
 }
 
 }  // namespace pa
