@@ -71,18 +71,26 @@ namespace pa {
 #define PA_KV4_UNITS 5
 #endif
 
-// TB: tokens per block, 8, 16 or 32; the last serves 64-token blocks too, as
-// two halves (the block size itself is then a launch argument).
+// TB: tokens per block.
 template <typename T_, int D_, int NT_, int TB_>
 struct Kv4 {
   using T = T_;
   static constexpr int D = D_, NT = NT_, GT = 8 * NT_, TB = TB_;
-  static constexpr int NBLK = 32 / TB_;          // blocks per stage
+#ifndef PA_KV4_TILES
+#define PA_KV4_TILES 4
+#endif
+  // 16-token tiles per stage (two at head size 256, for three stages in the ring).
+  static constexpr int NTI = D_ > 128 && TB_ < 64 ? 2 : PA_KV4_TILES;
+  static constexpr int TS = 16 * NTI;            // tokens per stage
+  static constexpr int NBLK = TS / TB_;          // blocks per stage
+  static_assert(NBLK >= 1, "a stage holds whole blocks");
+  static constexpr uint32_t REC = (uint32_t)TB_ * (D_ + 8), STAGE = REC * NBLK;
   // Warps per CTA: as many as the accumulators' registers allow (128 or 255 a thread).
 #ifndef PA_KV4_NC
-#define PA_KV4_NC 16
+#define PA_KV4_NC 8
 #endif
-  static constexpr int NC = (D_ <= 128 && NT_ == 1) ? PA_KV4_NC : 8;
+  static constexpr int NC = D_ > 128 && TB_ == 64 ? 4 : (D_ <= 128 && NT_ == 1) ? PA_KV4_NC : 8;
+  static_assert((NC & (NC - 1)) == 0, "teams of a power of two");
   static constexpr int THREADS = NC * 32;
   static constexpr int X = D_ < 128 ? D_ : 128;  // dims per slab
   static constexpr int NSLAB = D_ / X;
@@ -105,34 +113,27 @@ struct Kv4 {
   static constexpr uint32_t OFF_BAR = NC * RING, OFF_FLAGS = OFF_BAR + al16(SZ_BAR), OFF_NEXT = OFF_FLAGS + 64,
                             OFF_PREF = OFF_NEXT + 256, BYTES = OFF_PREF + al16(SZ_PREF);
   static_assert(BYTES <= BUDGET, "shared memory over budget");
-  static_assert(STATE <= RING && 64 * (D_ + 8) <= RING, "a warp's state and its largest stage fit its ring");
+  static constexpr int NS = RING / STAGE < NSMAX ? RING / STAGE : NSMAX;  // ring stages per warp
+  static_assert(STATE <= RING && NS >= 1, "a warp's state and a stage fit its ring");
 };
 
 // What a CTA derives from the launch and the lengths.
 struct Kv4Plan {
   int TW;             // warps per unit
   int n_hg;           // units per partition: KH * hg_per_kv
-  int TS;             // tokens per stage
-  uint32_t rec;       // bytes of a record
-  uint32_t stage;     // bytes of a ring stage
-  int NS;             // ring stages per warp
   int total;          // units
 };
 
-// Warps per unit: the fewest that give the grid's teams about five units each
-// (an even end), but no more than a partition has stages.
+// Warps per unit: the fewest that give the grid's teams a few units each (an
+// even end), but no more than a partition has stages.
 template <class K>
-__device__ __forceinline__ Kv4Plan make_plan(const KParams& prm, int BS, int partitions) {
+__device__ __forceinline__ Kv4Plan make_plan(const KParams& prm, int partitions) {
   Kv4Plan pl;
-  pl.TS = K::NBLK * BS;
-  pl.rec = (uint32_t)BS * (K::D + 8);
-  pl.stage = pl.rec * K::NBLK;
-  pl.NS = min((int)(K::RING / pl.stage), K::NSMAX);
   pl.n_hg = prm.KH * prm.hg_per_kv;
   pl.total = partitions * pl.n_hg;
   const long long want = (long long)PA_KV4_UNITS * gridDim.x * K::NC;
   int tw = 1;
-  while (tw < K::NC && tw * pl.TS < prm.P && (long long)pl.total * tw < want) tw *= 2;
+  while (tw < K::NC && tw * K::TS < prm.P && (long long)pl.total * tw < want) tw *= 2;
   pl.TW = tw;
   return pl;
 }
@@ -181,28 +182,29 @@ __device__ __forceinline__ void mma_f16_first(float (&c)[4], const uint32_t (&a)
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 
-// Offsets within a stage: constants but for the ones that 64-token blocks
-// stretch.
+// Offsets within a stage (a constant each).
 template <class K>
 struct Kv4Offsets {
-  static constexpr uint32_t REC = (uint32_t)K::TB * (K::D + 8);
-  // Codes: tokens 8..15 of a tile after 0..7, and tile 1 after tile 0; parameters the same.
-  static constexpr uint32_t hd = K::TB == 8 ? REC : 8 * K::XB;
-  static constexpr uint32_t td = K::TB == 8 ? 2 * REC : K::TB == 16 ? REC : 16 * K::XB;
-  static constexpr uint32_t hdp = K::TB == 8 ? REC : 64;
-  static constexpr uint32_t tdp = K::TB == 8 ? 2 * REC : K::TB == 16 ? REC : 128;
-  uint32_t bs;
-  __device__ __forceinline__ explicit Kv4Offsets(int BS) : bs(K::TB < 32 ? K::TB : BS) {}
-  __device__ __forceinline__ uint32_t slab() const { return (K::TB < 32 ? K::TB : bs) * K::XB; }
-  __device__ __forceinline__ uint32_t voff() const { return (K::TB < 32 ? K::TB : bs) * (K::D / 2); }
-  __device__ __forceinline__ uint32_t poff() const { return (K::TB < 32 ? K::TB : bs) * K::D; }
+  static constexpr uint32_t slab = K::TB * K::XB;     // slab 1 after slab 0
+  static constexpr uint32_t voff = K::TB * K::D / 2;  // value codes in a record
+  static constexpr uint32_t poff = K::TB * K::D;      // parameters in a record
+  // Tokens 8..15 of a tile after 0..7: codes, parameters.
+  static constexpr uint32_t hd = K::TB == 8 ? K::REC : 8 * K::XB;
+  static constexpr uint32_t hdp = K::TB == 8 ? K::REC : 64;
+  // Tile t.
+  __device__ static constexpr uint32_t tile(int t) {
+    return (uint32_t)(16 * t / K::TB) * K::REC + (uint32_t)(16 * t % K::TB) * K::XB;
+  }
+  __device__ static constexpr uint32_t tilep(int t) {
+    return (uint32_t)(16 * t / K::TB) * K::REC + (uint32_t)(16 * t % K::TB) * 8;
+  }
 };
 
 // ---------------------------------------------------------------- a consumer warp's state
 template <class K>
 struct Kv4State {
   using T = typename K::T;
-  static constexpr int NT = K::NT, NK = K::NK, NMT = K::NMT, KW = K::KW, VW = K::VW, NSLAB = K::NSLAB;
+  static constexpr int NT = K::NT, NK = K::NK, NMT = K::NMT, KW = K::KW, VW = K::VW, NSLAB = K::NSLAB, NTI = K::NTI;
   static constexpr uint32_t LO = 0x000f000fu, HI = 0x00f000f0u;
 
   uint32_t qb[NT][NK][2];          // Q^T fragments: the query row of column lane / 4
@@ -335,52 +337,52 @@ struct Kv4State {
     minlim = __reduce_min_sync(0xffffffffu, least);
   }
 
-  // 32 tokens whose first tile starts at `codes` / `params` (the record's
-  // start plus the token offset of either); ntok of them lie before the
-  // sequence end, the first is token tok0.
-  __device__ __forceinline__ void pass(uint32_t codes, uint32_t params, const Kv4Offsets<K>& o, int ntok, int tok0,
-                                       int lane) {
+  // The stage at `codes`: ntok of its tokens lie before the sequence end, the
+  // first is token tok0.
+  __device__ __forceinline__ void pass(uint32_t codes, int ntok, int tok0, int lane) {
     using O = Kv4Offsets<K>;
-    float y[2][NT][4];  // scores, less the columns' references
-    float2 pv[2][2];    // (value scale, value zero) of the lane's score rows r, r + 8 of each tile
-    const uint32_t ka = codes + ko, pa = params + po;
-    float dot[2][NT][4];
+    float y[NTI][NT][4];  // scores, less the columns' references
+    float2 pv[NTI][2];    // (value scale, value zero) of the lane's score rows r, r + 8 of each tile
+    const uint32_t ka = codes + ko, pa = codes + O::poff + po;
+    float dot[NTI][NT][4];
 #pragma unroll
-    for (int sl = 0; sl < NSLAB; ++sl) {
-      uint32_t wl[2][KW], wh[2][KW];
+    for (int t0 = 0; t0 < NTI; t0 += 2)
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        key_words(ka + t * O::td + sl * o.slab(), wl[t]);
-        key_words(ka + t * O::td + sl * o.slab() + O::hd, wh[t]);
-      }
-      // (The tiles' chains of dependent products run side by side.)
-#pragma unroll
-      for (int i = 0; i < KW; ++i) {
-        const int ks = (sl * KW + i) * 2;
+      for (int sl = 0; sl < NSLAB; ++sl) {
+        uint32_t wl[2][KW], wh[2][KW];
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-          const uint32_t a[4] = {wl[t][i] & LO, wh[t][i] & LO, wl[t][i] & HI, wh[t][i] & HI};
+          key_words(ka + O::tile(t0 + t) + sl * O::slab, wl[t]);
+          key_words(ka + O::tile(t0 + t) + sl * O::slab + O::hd, wh[t]);
+        }
+        // (Two tiles' chains of dependent products run side by side.)
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            if (ks == 0) mma_f16_first(dot[t][n], a, qb[n][ks][0], qb[n][ks][1]);
-            else mma_f16(dot[t][n], a, qb[n][ks][0], qb[n][ks][1]);
+        for (int i = 0; i < KW; ++i) {
+          const int ks = (sl * KW + i) * 2;
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            const uint32_t a[4] = {wl[t][i] & LO, wh[t][i] & LO, wl[t][i] & HI, wh[t][i] & HI};
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              if (ks == 0) mma_f16_first(dot[t0 + t][n], a, qb[n][ks][0], qb[n][ks][1]);
+              else mma_f16(dot[t0 + t][n], a, qb[n][ks][0], qb[n][ks][1]);
+            }
+          }
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            const uint32_t xl = wl[t][i] >> 8, xh = wh[t][i] >> 8;
+            const uint32_t b[4] = {xl & LO, xh & LO, xl & HI, xh & HI};
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mma_f16(dot[t0 + t][n], b, qb[n][ks + 1][0], qb[n][ks + 1][1]);
           }
         }
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          const uint32_t xl = wl[t][i] >> 8, xh = wh[t][i] >> 8;
-          const uint32_t b[4] = {xl & LO, xh & LO, xl & HI, xh & HI};
-#pragma unroll
-          for (int n = 0; n < NT; ++n) mma_f16(dot[t][n], b, qb[n][ks + 1][0], qb[n][ks + 1][1]);
-        }
       }
-    }
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
+    for (int t = 0; t < NTI; ++t) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         uint32_t wk, wv;
-        lds_b64(pa + t * O::tdp + (h ? O::hdp : 0u), wk, wv);
+        lds_b64(pa + O::tilep(t) + (h ? O::hdp : 0u), wk, wv);
         const float2 k = F16Traits<T>::to_float2(wk);
         pv[t][h] = F16Traits<T>::to_float2(wv);
         const float kx = k.x * kf;
@@ -393,11 +395,11 @@ struct Kv4State {
     }
     // Slots past the sequence end hold arbitrary parameters, and causal rows
     // stop earlier: their scores become -inf, and (below) their weights 0.
-    const bool full = ntok >= 32 && tok0 + 32 <= minlim;
+    const bool full = ntok >= K::TS && tok0 + K::TS <= minlim;
     if (!full) {
       const int trow = tok_lo(lane >> 2);
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
+      for (int t = 0; t < NTI; ++t)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int tt = 16 * t + 8 * h + trow;
@@ -409,26 +411,34 @@ struct Kv4State {
               if (tt >= ntok || tok0 + tt >= lim[n][j]) y[t][n][2 * h + j] = -INFINITY;
         }
     }
-    float vm = fmaxf(fmaxf(fabsf(pv[0][0].x), fabsf(pv[0][1].x)), fmaxf(fabsf(pv[1][0].x), fabsf(pv[1][1].x)));
+    float vm = 0.f;
+#pragma unroll
+    for (int t = 0; t < NTI; ++t) vm = fmaxf(vm, fmaxf(fabsf(pv[t][0].x), fabsf(pv[t][1].x)));
     bool raise = vm >= vb;
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
-        raise |= fmaxf(fmaxf(y[0][n][j], y[0][n][j + 2]), fmaxf(y[1][n][j], y[1][n][j + 2])) > thr[n][j];
+      for (int j = 0; j < 2; ++j) raise |= column_max(y, n, j) > thr[n][j];
     if (__any_sync(0xffffffffu, raise)) raise_bounds(y, pv);
     if (full) weigh<false>(y, pv);
     else weigh<true>(y, pv);
-    values(y, codes + o.voff(), o);
+    values(y, codes + O::voff);
+  }
+
+  __device__ __forceinline__ static float column_max(const float (&y)[NTI][NT][4], int n, int j) {
+    float b = fmaxf(y[0][n][j], y[0][n][j + 2]);
+#pragma unroll
+    for (int t = 1; t < NTI; ++t) b = fmaxf(b, fmaxf(y[t][n][j], y[t][n][j + 2]));
+    return b;
   }
 
   // New references, and a new bound on the value scales (finite ones: a NaN
   // or Inf goes through to the output whatever the bound is; four times the
   // largest, so that few items raise it); the sums and accumulators follow.
-  __device__ __forceinline__ void raise_bounds(float (&y)[2][NT][4], const float2 (&pv)[2][2]) {
+  __device__ __forceinline__ void raise_bounds(float (&y)[NTI][NT][4], const float2 (&pv)[NTI][2]) {
     float vm = 0.f;
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
+    for (int t = 0; t < NTI; ++t)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const float a = fabsf(pv[t][h].x);
@@ -447,7 +457,7 @@ struct Kv4State {
       float a[2];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        float bm = fmaxf(fmaxf(y[0][n][j], y[0][n][j + 2]), fmaxf(y[1][n][j], y[1][n][j + 2]));
+        float bm = column_max(y, n, j);
         bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 4));
         bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 8));
         bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 16));
@@ -459,7 +469,7 @@ struct Kv4State {
           ms[n][j] += bm;
           thr[n][j] = 8.f;
 #pragma unroll
-          for (int t = 0; t < 2; ++t) {
+          for (int t = 0; t < NTI; ++t) {
             y[t][n][j] -= bm;
             y[t][n][j + 2] -= bm;
           }
@@ -484,9 +494,9 @@ struct Kv4State {
 
   // Scores into weights (over the value scales' bound), and their sums.
   template <bool MASK>
-  __device__ __forceinline__ void weigh(float (&y)[2][NT][4], const float2 (&pv)[2][2]) {
+  __device__ __forceinline__ void weigh(float (&y)[NTI][NT][4], const float2 (&pv)[NTI][2]) {
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
+    for (int t = 0; t < NTI; ++t)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const float zc = fmaf(8.f, pv[t][h].x, pv[t][h].y), vw = pv[t][h].x * vinv;
@@ -505,10 +515,10 @@ struct Kv4State {
       }
   }
 
-  __device__ __forceinline__ void values(const float (&w)[2][NT][4], uint32_t codes, const Kv4Offsets<K>& o) {
+  __device__ __forceinline__ void values(const float (&w)[NTI][NT][4], uint32_t codes) {
     using O = Kv4Offsets<K>;
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
+    for (int t = 0; t < NTI; ++t) {
       uint32_t b0[NT], b1[NT];
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
@@ -517,14 +527,14 @@ struct Kv4State {
         const uint32_t eight[4] = {0x00080008u, 0x00080008u, 0x00080008u, 0x00080008u};
         mma_f16(acc8[n], eight, b0[n], b1[n]);
       }
-      const uint32_t va = codes + vo + t * O::td, vd = codes + vo2 + t * O::td;
+      const uint32_t va = codes + vo + O::tile(t), vd = codes + vo2 + O::tile(t);
 #pragma unroll
       for (int sl = 0; sl < NSLAB; ++sl) {
         uint32_t wa[2], wb[2], wc[2], wd[2];
-        value_words(va + sl * o.slab(), wa);
-        value_words(vd + sl * o.slab(), wb);
-        value_words(va + sl * o.slab() + O::hd, wc);
-        value_words(vd + sl * o.slab() + O::hd, wd);
+        value_words(va + sl * O::slab, wa);
+        value_words(vd + sl * O::slab, wb);
+        value_words(va + sl * O::slab + O::hd, wc);
+        value_words(vd + sl * O::slab + O::hd, wd);
 #pragma unroll
         for (int half = 0; half < VW; ++half) {
           // VW = 2: rows r and r + 8 of tile mt hold nibble mt of the two
@@ -613,7 +623,7 @@ struct Kv4Unit {
   int s, p, np, L, t0, t1, nb, kv, h0, nh;
 };
 template <class K>
-__device__ __forceinline__ Kv4Unit kv4_unit(const KParams& prm, const Kv4Plan& pl, const int* pref, int BS, int u) {
+__device__ __forceinline__ Kv4Unit kv4_unit(const KParams& prm, const Kv4Plan& pl, const int* pref, int u) {
   Kv4Unit U;
   const int pair = u / pl.n_hg, hg = u - pair * pl.n_hg;
   int lo = 0, hi = prm.S;  // pref[lo] <= pair < pref[lo + 1]
@@ -624,10 +634,10 @@ __device__ __forceinline__ Kv4Unit kv4_unit(const KParams& prm, const Kv4Plan& p
   U.s = lo;
   U.p = pair - pref[lo];
   U.np = pref[lo + 1] - pref[lo];
-  U.L = kv4_tokens(prm, lo, BS);
+  U.L = kv4_tokens(prm, lo, K::TB);
   U.t0 = U.p * prm.P;
   U.t1 = min(U.t0 + prm.P, U.L);
-  U.nb = (U.t1 - U.t0 + BS - 1) >> (__ffs(BS) - 1);
+  U.nb = (U.t1 - U.t0 + K::TB - 1) / K::TB;
   U.kv = hg / prm.hg_per_kv;
   const int part = hg - U.kv * prm.hg_per_kv;
   U.h0 = U.kv * prm.G + part * K::GT;
@@ -663,11 +673,11 @@ __device__ __forceinline__ float inverse(float l) { return l == 0.f ? 0.f : 1.f 
 // Unused partitions: sentinels (m = -inf, l = 0).  Empty sequences: zeros (a
 // multi-query sequence is never empty: it holds its new tokens).
 template <class K>
-__device__ __forceinline__ void kv4_sentinels(const KParams& prm, int BS) {
+__device__ __forceinline__ void kv4_sentinels(const KParams& prm) {
   using T = typename K::T;
   const int S = prm.S, H = prm.H, Pmax = prm.Pmax;
   const long long me = (long long)blockIdx.x * K::THREADS + threadIdx.x, n = (long long)gridDim.x * K::THREADS;
-  auto parts_of = [&](int s) { return (kv4_tokens(prm, s, BS) + prm.P - 1) / prm.P; };
+  auto parts_of = [&](int s) { return (kv4_tokens(prm, s, K::TB) + prm.P - 1) / prm.P; };
   for (long long i = me; i < (long long)S * H * Pmax; i += n) {
     const int s = (int)(i / ((long long)H * Pmax)), p = (int)(i % Pmax);
     if (p >= parts_of(s)) {
@@ -711,29 +721,27 @@ struct Kv4Stream {
   uint32_t bar_in, bar_out, ph_out;  // their barriers, and the phase of the latter
   int nb, left;          // blocks of the run; those not asked for yet
   int ids, ids_next;     // lane's ids of the current window of 32 blocks, and of the one after
-  uint32_t ring, ring_bytes, bars;   // shared addresses of the warp's ring and barriers; bytes in use
-  uint32_t rec, stage;
+  uint32_t ring, bars;   // shared addresses of the warp's ring and barriers
   const int32_t* row;    // the run's block ids
   const uint8_t* base;   // the kv head's record of block 0
   size_t block_bytes;    // of all kv heads
   uint64_t policy;
 
-  __device__ __forceinline__ Kv4Stream(const KParams& prm, const Kv4Plan& pl, uint32_t r, uint32_t b)
-      : in(0), out(0), bar_in(b), bar_out(b), ph_out(0), nb(0), left(0), ring(r), ring_bytes(pl.NS * pl.stage),
-        bars(b), rec(pl.rec), stage(pl.stage), block_bytes((size_t)prm.KH * pl.rec),
-        policy(l2_policy_evict_first()) {}
+  __device__ __forceinline__ Kv4Stream(const KParams& prm, uint32_t r, uint32_t b)
+      : in(0), out(0), bar_in(b), bar_out(b), ph_out(0), nb(0), left(0), ring(r), bars(b),
+        block_bytes((size_t)prm.KH * K::REC), policy(l2_policy_evict_first()) {}
 
   __device__ __forceinline__ int fetch(int b0, int lane) const { return b0 + lane < nb ? __ldg(row + b0 + lane) : 0; }
 
   __device__ __forceinline__ void start(const KParams& prm, const int32_t* table, const uint8_t* cache_kv, int blocks,
-                                        int NS, int lane) {
+                                        int lane) {
     row = table;
     base = cache_kv;
     nb = left = blocks;
     ids = fetch(0, lane);
     ids_next = fetch(32, lane);
     ids = check_block_id(prm, ids);
-    for (int i = 0; i < NS; ++i) issue(prm, lane);
+    for (int i = 0; i < K::NS; ++i) issue(prm, lane);
   }
   // Fills the next stage (it is free: this warp has used it, or never filled it).
   __device__ __forceinline__ void issue(const KParams& prm, int lane) {
@@ -748,15 +756,15 @@ struct Kv4Stream {
     for (int k = 0; k < K::NBLK; ++k) id[k] = __shfl_sync(0xffffffffu, ids, w + k);
     const int n = min(K::NBLK, left);
     if (elect_one()) {
-      mbar_arrive_expect_tx(bar_in, (uint32_t)n * rec);
+      mbar_arrive_expect_tx(bar_in, (uint32_t)n * K::REC);
 #pragma unroll
       for (int k = 0; k < K::NBLK; ++k)
-        if (k < n) bulk_copy_cta(ring + in + k * rec, base + (uint32_t)id[k] * block_bytes, rec, bar_in, policy);
+        if (k < n) bulk_copy_cta(ring + in + k * K::REC, base + (uint32_t)id[k] * block_bytes, K::REC, bar_in, policy);
     }
     left -= K::NBLK;
-    in += stage;
+    in += K::STAGE;
     bar_in += 8;
-    if (in == ring_bytes) {
+    if (in == K::NS * K::STAGE) {
       in = 0;
       bar_in = bars;
     }
@@ -764,16 +772,16 @@ struct Kv4Stream {
   // Waits for the next stage to land; false: gave up.
   __device__ __forceinline__ bool wait(const KParams& prm, volatile int* abort_flag) const {
     if (__all_sync(0xffffffffu, mbar_try_wait(bar_out, ph_out))) return true;
-    return kv4_wait_slow(bar_out, ph_out, abort_flag, prm.hdr + kHdrError, prm.timeout_ns, (int)(out / stage));
+    return kv4_wait_slow(bar_out, ph_out, abort_flag, prm.hdr + kHdrError, prm.timeout_ns, (int)(out / K::STAGE));
   }
   __device__ __forceinline__ void used() {
     // The stage is refilled by bulk copies (async proxy): every lane's reads
     // of it are ordered before that by a proxy fence.
     fence_proxy_async_smem();
     __syncwarp();
-    out += stage;
+    out += K::STAGE;
     bar_out += 8;
-    if (out == ring_bytes) {
+    if (out == K::NS * K::STAGE) {
       out = 0;
       bar_out = bars;
       ph_out ^= 1u;
@@ -793,7 +801,7 @@ struct Kv4Stream {
 };
 
 template <class K>
-__global__ void __launch_bounds__(K::THREADS, 1) kv4_decode_kernel(const __grid_constant__ KParams prm, int BS) {
+__global__ void __launch_bounds__(K::THREADS, 1) kv4_decode_kernel(const __grid_constant__ KParams prm) {
   using T = typename K::T;
   extern __shared__ __align__(1024) uint8_t smem[];
   // (The warp index by a shuffle: known to be the same in all lanes.)
@@ -821,8 +829,8 @@ __global__ void __launch_bounds__(K::THREADS, 1) kv4_decode_kernel(const __grid_
     int sum = 0;
     for (int s = beg; s < end; ++s) {
       // (A multi-query sequence holds its q_len new tokens.)
-      bad |= prm.lens[s] < (prm.q_len > 1 ? prm.q_len : 0) || prm.lens[s] > prm.MB * BS;
-      const int np = (kv4_tokens(prm, s, BS) + prm.P - 1) / prm.P;
+      bad |= prm.lens[s] < (prm.q_len > 1 ? prm.q_len : 0) || prm.lens[s] > prm.MB * K::TB;
+      const int np = (kv4_tokens(prm, s, K::TB) + prm.P - 1) / prm.P;
       pref[s] = sum;
       sum += np;
     }
@@ -847,17 +855,16 @@ __global__ void __launch_bounds__(K::THREADS, 1) kv4_decode_kernel(const __grid_
     fence_proxy_async_smem();  // the ring is filled by bulk copies from here on
   }
   __syncthreads();
-  const Kv4Plan pl = make_plan<K>(prm, BS, pref[prm.S]);
+  const Kv4Plan pl = make_plan<K>(prm, pref[prm.S]);
   // A programmatic dependent of the kernel that clears the workspace header:
   // nothing below may touch the header before it has completed.
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (tid == 0 && *bad_len) atomicCAS(prm.hdr + kHdrError, 0, kErrDeviceBounds);
 
-  const Kv4Offsets<K> off(BS);
-  const int ltw = __ffs(pl.TW) - 1, lbs = __ffs(BS) - 1;
+  const int ltw = __ffs(pl.TW) - 1;
   const int teams = K::NC >> ltw, team = warp >> ltw, tw = warp & (pl.TW - 1);
   const uint64_t keep = l2_policy_evict_last();
-  Kv4Stream<K> in(prm, pl, sbase + warp * K::RING, sbase + K::OFF_BAR + warp * K::NSMAX * 8);
+  Kv4Stream<K> in(prm, sbase + warp * K::RING, sbase + K::OFF_BAR + warp * K::NSMAX * 8);
   Kv4State<K> st(lane);
   // The first units are dealt out over the CTAs; the counter hands out the rest.
   int u = blockIdx.x + (int)gridDim.x * team;
@@ -865,33 +872,30 @@ __global__ void __launch_bounds__(K::THREADS, 1) kv4_decode_kernel(const __grid_
   // The sentinels are written while the first copies fly.
   bool sentinels = false;
   while (u < pl.total) {
-    const Kv4Unit U = kv4_unit<K>(prm, pl, pref, BS, u);
+    const Kv4Unit U = kv4_unit<K>(prm, pl, pref, u);
     const int nst = (U.nb + K::NBLK - 1) / K::NBLK, per = (nst + pl.TW - 1) >> ltw;
     const int i0 = min(tw * per, nst), b0 = i0 * K::NBLK, nb = min(per * K::NBLK, U.nb - b0);
     int u_next = 0;
     if (tw == 0 && lane == 0) u_next = atomicAdd(prm.hdr + kHdrWork, 1) + (int)gridDim.x * teams;
     const int blocks = alive ? max(nb, 0) : 0, stages = (blocks + K::NBLK - 1) / K::NBLK;
-    in.start(prm, prm.bt + (size_t)U.s * prm.MB + (U.t0 >> lbs) + b0,
-             static_cast<const uint8_t*>(prm.kc) + (size_t)U.kv * pl.rec, blocks, pl.NS, lane);
+    in.start(prm, prm.bt + (size_t)U.s * prm.MB + U.t0 / K::TB + b0,
+             static_cast<const uint8_t*>(prm.kc) + (size_t)U.kv * K::REC, blocks, lane);
     if (!sentinels) {
       sentinels = true;
-      kv4_sentinels<K>(prm, BS);
+      kv4_sentinels<K>(prm);
     }
     st.begin_unit([&](int i) { return static_cast<const T*>(prm.q) + out_row_rt(prm, U.s, U.h0 + i) * K::D; }, U.nh,
                   prm.scale_log2, lane);
     if (prm.q_len > 1) st.set_limits([&](int h) { return row_limit<true>(prm, U.L, U.h0 + h); }, lane);
     else st.set_limits([&](int) { return U.L; }, lane);
-    int n = U.t1 - U.t0 - i0 * pl.TS, tok = U.t0 + i0 * pl.TS;  // tokens from the stage on; its first
-    for (int i = 0; i < stages; ++i, n -= pl.TS, tok += pl.TS) {
+    int n = U.t1 - U.t0 - i0 * K::TS, tok = U.t0 + i0 * K::TS;  // tokens from the stage on; its first
+    for (int i = 0; i < stages; ++i, n -= K::TS, tok += K::TS) {
       if (!in.wait(prm, abort_flag)) {
         in.drain(i);
         alive = false;
         break;
       }
-      const uint32_t rec = in.ring + in.out;
-      st.pass(rec, rec + off.poff(), off, n, tok, lane);
-      if (K::TB == 32 && BS == 64 && n > 32)
-        st.pass(rec + 32 * K::XB, rec + off.poff() + 256, off, n - 32, tok + 32, lane);
+      st.pass(in.ring + in.out, n, tok, lane);
       in.used();
       in.issue(prm, lane);
     }
@@ -952,7 +956,7 @@ __global__ void __launch_bounds__(K::THREADS, 1) kv4_decode_kernel(const __grid_
     }
     if (*abort_flag && pl.TW == 1) break;
   }
-  if (!sentinels) kv4_sentinels<K>(prm, BS);
+  if (!sentinels) kv4_sentinels<K>(prm);
   // Phase 2 may be launched once every CTA has said so or ended (it waits for
   // this grid to complete before it reads anything).
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

@@ -8,7 +8,7 @@
 namespace pa {
 
 template <class K>
-static cudaError_t kv4_go(const KParams& prm, int BS, int max_ctas, cudaStream_t st) {
+static cudaError_t kv4_go(const KParams& prm, int max_ctas, cudaStream_t st) {
   // The shared-memory opt-in is set once per kernel instance and device.
   static std::atomic<uint64_t> opted_in{0};
   int dev = 0;
@@ -32,16 +32,16 @@ static cudaError_t kv4_go(const KParams& prm, int BS, int max_ctas, cudaStream_t
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv4_decode_kernel<K>, prm, BS);
+  return cudaLaunchKernelEx(&cfg, kv4_decode_kernel<K>, prm);
 }
 
 template <typename T, int D, int NT>
 static cudaError_t kv4_go_bs(const KParams& prm, int BS, int max_ctas, cudaStream_t st) {
   switch (BS) {
-    case 8: return kv4_go<Kv4<T, D, NT, 8>>(prm, BS, max_ctas, st);
-    case 16: return kv4_go<Kv4<T, D, NT, 16>>(prm, BS, max_ctas, st);
-    case 32:
-    case 64: return kv4_go<Kv4<T, D, NT, 32>>(prm, BS, max_ctas, st);
+    case 8: return kv4_go<Kv4<T, D, NT, 8>>(prm, max_ctas, st);
+    case 16: return kv4_go<Kv4<T, D, NT, 16>>(prm, max_ctas, st);
+    case 32: return kv4_go<Kv4<T, D, NT, 32>>(prm, max_ctas, st);
+    case 64: return kv4_go<Kv4<T, D, NT, 64>>(prm, max_ctas, st);
     default: return cudaErrorInvalidValue;
   }
 }
