@@ -48,28 +48,30 @@
 // which the zeroed query slots, or leaving the accumulator rows out, ignore
 // (every nibble is a finite number).
 //
-// Work unit = (sequence, partition, kv head, GT of its query rows), taken by a
-// team of TW warps of one CTA (TW = 1, 2, 4 ..: as many as make enough teams'
-// worth of units, choose_team); each warp takes a contiguous run of the
-// partition's tokens.  One CTA of NC equal warps per SM, no producer: a warp
-// owns a ring of a few 32-token stages and refills a stage itself, by one bulk
-// copy per block, right after it has used it, so no warp waits for another
-// while it streams.  What was measured on the way to this: a team of all the
-// SM's warps with one warp that merges their states (the scheme of
-// pa_kernel.cuh) spends more on set-ups, hand-overs and the merging warp than
-// on the tokens, as a 4-bit partition holds a quarter of the bytes.  A warp of
-// a team of one writes its unit itself; larger teams meet once per unit, leave
-// their states in their rings and each merge a slice of the rows.
+// Work.  A unit is (sequence, partition, kv head, GT of its query rows), a run
+// of stages of 64 tokens (32 at head size 256).  One CTA of NC equal warps per
+// SM, no producer: a warp takes whole units from a global counter, owns a ring
+// of a few stages and refills a stage itself, by one bulk copy per block, right
+// after it has used it; what it asks for runs ahead into its next unit.  Units
+// are numbered with the kv heads of a partition next to each other, so the
+// records of one block, neighbours in memory, are read at about the same time
+// by different SMs (contiguous shares per warp instead, which end together,
+// took 160 us where this takes 118 for the copies of a batch alone).  The units
+// left over when every warp has taken as many as the others are shared by
+// teams of TW warps of a CTA, each a part of the tokens; the team merges the
+// parts through shared memory.
+//
+// Measured on the way (128 sequences of 2048 to 8192 tokens, 32 heads over 8
+// kv heads, D = 128): the scheme of pa_kernel.cuh 239 us (a 4-bit partition
+// holds a quarter of the bytes, so set-ups, hand-overs and the one merging warp
+// outweigh the tokens); whole units without run-ahead 177 us (16 warps of 128
+// registers, 32-token stages) and 158 us (8 of 200, 64).
 #pragma once
 
 #include "pa_common.cuh"
 #include "pa_kernel.cuh"
 
 namespace pa {
-
-#ifndef PA_KV4_UNITS
-#define PA_KV4_UNITS 5
-#endif
 
 // TB: tokens per block.
 template <typename T_, int D_, int NT_, int TB_>
@@ -79,8 +81,8 @@ struct Kv4 {
 #ifndef PA_KV4_TILES
 #define PA_KV4_TILES 4
 #endif
-  // 16-token tiles per stage (two at head size 256, for three stages in the ring).
-  static constexpr int NTI = D_ > 128 && TB_ < 64 ? 2 : PA_KV4_TILES;
+  // 16-token tiles per stage (two at head size 256, for two stages in the ring).
+  static constexpr int NTI = TB_ == 64 ? 4 : D_ > 128 ? 2 : PA_KV4_TILES;
   static constexpr int TS = 16 * NTI;            // tokens per stage
   static constexpr int NBLK = TS / TB_;          // blocks per stage
   static_assert(NBLK >= 1, "a stage holds whole blocks");
@@ -90,7 +92,7 @@ struct Kv4 {
 #define PA_KV4_NC 8
 #endif
   static constexpr int NC = D_ > 128 && TB_ == 64 ? 4 : (D_ <= 128 && NT_ == 1) ? PA_KV4_NC : 8;
-  static_assert((NC & (NC - 1)) == 0, "teams of a power of two");
+
   static constexpr int THREADS = NC * 32;
   static constexpr int X = D_ < 128 ? D_ : 128;  // dims per slab
   static constexpr int NSLAB = D_ / X;
@@ -106,37 +108,16 @@ struct Kv4 {
   static constexpr int AROW = D_ + 4;            // floats of a handed-over row (16 bytes past it, for the banks)
   static constexpr uint32_t STATE = GT * AROW * 4 + GT * 2 * 4;
   static constexpr uint32_t SZ_BAR = NC * NSMAX * 8;
-  static constexpr uint32_t SZ_PREF = (kMaxSeqsPerLaunch + 1) * 4;
-  static constexpr uint32_t FIXED = al16(SZ_BAR) + 64 + 256 + al16(SZ_PREF);
+  static constexpr uint32_t SZ_PREF = (2 * kMaxSeqsPerLaunch + 1) * 4;  // partition prefix, lengths
+  static constexpr uint32_t FIXED = al16(SZ_BAR) + 64 + al16(SZ_PREF);
   static constexpr uint32_t BUDGET = 227 * 1024;
   static constexpr uint32_t RING = (BUDGET - FIXED) / NC / 128 * 128;  // bytes per warp
-  static constexpr uint32_t OFF_BAR = NC * RING, OFF_FLAGS = OFF_BAR + al16(SZ_BAR), OFF_NEXT = OFF_FLAGS + 64,
-                            OFF_PREF = OFF_NEXT + 256, BYTES = OFF_PREF + al16(SZ_PREF);
+  static constexpr uint32_t OFF_BAR = NC * RING, OFF_FLAGS = OFF_BAR + al16(SZ_BAR),
+                            OFF_PREF = OFF_FLAGS + 64, BYTES = OFF_PREF + al16(SZ_PREF);
   static_assert(BYTES <= BUDGET, "shared memory over budget");
   static constexpr int NS = RING / STAGE < NSMAX ? RING / STAGE : NSMAX;  // ring stages per warp
-  static_assert(STATE <= RING && NS >= 1, "a warp's state and a stage fit its ring");
+  static_assert(STATE <= RING && NS >= 2, "a warp's state or two stages fit its ring");
 };
-
-// What a CTA derives from the launch and the lengths.
-struct Kv4Plan {
-  int TW;             // warps per unit
-  int n_hg;           // units per partition: KH * hg_per_kv
-  int total;          // units
-};
-
-// Warps per unit: the fewest that give the grid's teams a few units each (an
-// even end), but no more than a partition has stages.
-template <class K>
-__device__ __forceinline__ Kv4Plan make_plan(const KParams& prm, int partitions) {
-  Kv4Plan pl;
-  pl.n_hg = prm.KH * prm.hg_per_kv;
-  pl.total = partitions * pl.n_hg;
-  const long long want = (long long)PA_KV4_UNITS * gridDim.x * K::NC;
-  int tw = 1;
-  while (tw < K::NC && tw * K::TS < prm.P && (long long)pl.total * tw < want) tw *= 2;
-  pl.TW = tw;
-  return pl;
-}
 
 // ---------------------------------------------------------------- small pieces
 __device__ __forceinline__ float ex2(float x) {
@@ -253,34 +234,39 @@ struct Kv4State {
     }
   }
 
-  // row(i): the unit's query row i (of nh), in global memory.
-  template <class F>
-  __device__ __forceinline__ void begin_unit(F row, int nh, float sl2, int lane) {
-    const int n = lane >> 2, c = lane & 3;
-    // Dims 8w .. 8w + 7 of a slab are word w; this lane holds words c * KW ...
+  // The unit's query rows as this lane needs them: row(i) is row i (of nh) in
+  // global memory.  Dims 8w .. 8w + 7 of a slab are word w; this lane holds
+  // words c * KW ...
+  struct Rows {
     uint4 v[NT][NSLAB * KW];
+  };
+  template <class F>
+  __device__ __forceinline__ static void load_rows(Rows& q, F row, int nh, int lane) {
+    const int n = lane >> 2, c = lane & 3;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      const T* q = 8 * t + n < nh ? row(8 * t + n) : nullptr;
+      const T* p = 8 * t + n < nh ? row(8 * t + n) : nullptr;
 #pragma unroll
       for (int sl = 0; sl < NSLAB; ++sl)
 #pragma unroll
         for (int i = 0; i < KW; ++i) {
           const int w = c * KW + i;
-          v[t][sl * KW + i] = make_uint4(0, 0, 0, 0);
-          if (q && w < K::X / 8) v[t][sl * KW + i] = __ldg(reinterpret_cast<const uint4*>(q + sl * K::X + w * 8));
+          q.v[t][sl * KW + i] = make_uint4(0, 0, 0, 0);
+          if (p && w < K::X / 8) q.v[t][sl * KW + i] = __ldg(reinterpret_cast<const uint4*>(p + sl * K::X + w * 8));
         }
     }
+  }
+  __device__ __forceinline__ void begin_unit(const Rows& q, float sl2) {
     // The largest |q|, as 16-bit patterns (ordered as the values are).
     uint32_t top = 0;
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int i = 0; i < NSLAB * KW; ++i) {
-        top = __vmaxu2(top, v[t][i].x & 0x7fff7fffu);
-        top = __vmaxu2(top, v[t][i].y & 0x7fff7fffu);
-        top = __vmaxu2(top, v[t][i].z & 0x7fff7fffu);
-        top = __vmaxu2(top, v[t][i].w & 0x7fff7fffu);
+        top = __vmaxu2(top, q.v[t][i].x & 0x7fff7fffu);
+        top = __vmaxu2(top, q.v[t][i].y & 0x7fff7fffu);
+        top = __vmaxu2(top, q.v[t][i].z & 0x7fff7fffu);
+        top = __vmaxu2(top, q.v[t][i].w & 0x7fff7fffu);
       }
     top = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
     // 2^s brings the unit's largest |q| below 2^15; zero, subnormal, Inf or
@@ -295,7 +281,7 @@ struct Kv4State {
 #pragma unroll
       for (int i = 0; i < NSLAB * KW; ++i) {
         float f[8];
-        unpack_chunk<T>(v[t][i], f);
+        unpack_chunk<T>(q.v[t][i], f);
         const int ks = 2 * i;
         qb[t][ks][0] = F16Traits<__half>::pack(f[0] * up, f[4] * up);
         qb[t][ks][1] = F16Traits<__half>::pack(f[1] * up16, f[5] * up16);
@@ -570,11 +556,10 @@ struct Kv4State {
     }
   }
 
-  // The warp's state of the unit, four dims at a time: sink(col, d, v) with
-  // the sums of column col's dims d .. d + 3, times scale(l), and
-  // stat(col, m, l) once per column.
-  template <class Scale, class Sink, class Stat>
-  __device__ __forceinline__ void finish(Scale scale, Sink sink, Stat stat, int lane) {
+  // The unit's sums: row col (< nh) at rows + col * stride, over the row's
+  // weight sum where `divide`; stat(col, reference, weight sum) for each row.
+  template <class Stat>
+  __device__ __forceinline__ void finish(float* rows, size_t stride, int nh, bool divide, Stat stat, int lane) {
     const int r = lane >> 2, c = lane & 3;
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -587,10 +572,14 @@ struct Kv4State {
           zz += __shfl_xor_sync(0xffffffffu, zz, k);
         }
         const int col = 8 * n + 2 * c + j;
-        stat(col, thr[n][j] == -INFINITY ? -INFINITY : ms[n][j], ls);
+        if (col >= nh) continue;
+        if (r == 0) stat(col, thr[n][j] == -INFINITY ? -INFINITY : ms[n][j], ls);
+        // (A NaN sum stays NaN: only an empty row divides by nothing.)
+        const float f = divide ? (ls == 0.f ? 0.f : 1.f / ls) : 1.f;
+        const float vbf = vb * f, zf = zz * f;
+        float* o = rows + col * stride;
         // Tiles of odd nibbles carry 2^-20 instead of 2^-24.
         const float e8 = acc8[n][j], e16 = 16.f * e8;
-        const float f = scale(ls), vbf = vb * f, zf = zz * f;
 #pragma unroll
         for (int sl = 0; sl < NSLAB; ++sl)
 #pragma unroll
@@ -605,27 +594,24 @@ struct Kv4State {
               v.y = fmaf((acc[mt + 1][n][2 * h + j] - e16) * 8192.f, vbf, zf);
               v.z = fmaf((acc[mt + 2][n][2 * h + j] - e8) * 131072.f, vbf, zf);
               v.w = fmaf((acc[mt + 3][n][2 * h + j] - e16) * 8192.f, vbf, zf);
-              if (d < K::X) sink(col, sl * K::X + d, v);
+              if (d < K::X) *reinterpret_cast<float4*>(o + sl * K::X + d) = v;
             }
       }
   }
 };
 
 // ---------------------------------------------------------------- units
-// Cached tokens of sequence s, clamped to what its table row can hold (out of
-// range lengths are recorded by the prologue).
-__device__ __forceinline__ int kv4_tokens(const KParams& prm, int s, int BS) {
-  return min(max(prm.lens[s], 0), prm.MB * BS);
-}
-// Unit u = (partition, kv head, row group), partitions numbered in batch
-// order: sequence s holds pref[s] .. pref[s + 1] - 1.
+// Unit u = (partition, head group), partitions numbered in batch order:
+// sequence s holds pref[s] .. pref[s + 1] - 1 (pref and the clamped lengths in
+// shared memory).
 struct Kv4Unit {
-  int s, p, np, L, t0, t1, nb, kv, h0, nh;
+  int s, p, np, L, t0, t1, kv, h0, nh;
+  int nb, stages;  // blocks, stages
 };
 template <class K>
-__device__ __forceinline__ Kv4Unit kv4_unit(const KParams& prm, const Kv4Plan& pl, const int* pref, int u) {
+__device__ __forceinline__ Kv4Unit kv4_unit(const KParams& prm, const int* pref, const int* lens, int u) {
   Kv4Unit U;
-  const int pair = u / pl.n_hg, hg = u - pair * pl.n_hg;
+  const int n_hg = prm.KH * prm.hg_per_kv, pair = u / n_hg, hg = u - pair * n_hg;
   int lo = 0, hi = prm.S;  // pref[lo] <= pair < pref[lo + 1]
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -634,65 +620,68 @@ __device__ __forceinline__ Kv4Unit kv4_unit(const KParams& prm, const Kv4Plan& p
   U.s = lo;
   U.p = pair - pref[lo];
   U.np = pref[lo + 1] - pref[lo];
-  U.L = kv4_tokens(prm, lo, K::TB);
+  U.L = lens[lo];
   U.t0 = U.p * prm.P;
   U.t1 = min(U.t0 + prm.P, U.L);
   U.nb = (U.t1 - U.t0 + K::TB - 1) / K::TB;
-  U.kv = hg / prm.hg_per_kv;
+  U.stages = (U.nb + K::NBLK - 1) / K::NBLK;
+  U.kv = prm.hg_per_kv == 1 ? hg : hg / prm.hg_per_kv;
   const int part = hg - U.kv * prm.hg_per_kv;
   U.h0 = U.kv * prm.G + part * K::GT;
   U.nh = min(K::GT, prm.G - part * K::GT);
   return U;
 }
 
-// One finished row piece: the partition's normalised output in the workspace,
-// or the output itself where the sequence has one partition.
+// Warps per unit among the `rest` units that are left when every warp of the
+// grid has taken the same number: the time of a round falls with the warps, a
+// set-up and a merge (about 0.15 of a unit) comes with every round.
 template <class K>
-__device__ __forceinline__ void put_row(const KParams& prm, const Kv4Unit& U, int col, int d, const float4& v,
-                                        uint64_t keep) {
-  using T = typename K::T;
-  const int h = U.h0 + col;
-  if (U.np == 1) {
-    store4<T>(static_cast<T*>(prm.out) + out_row_rt(prm, U.s, h) * K::D + d, v);
-  } else {
-    const size_t at = ((size_t)U.s * prm.H + h) * prm.Pmax + U.p;
-    st_f4_policy(reinterpret_cast<float4*>(prm.ws_o + at * K::D + d), v, keep);
+__device__ __forceinline__ int tail_team(const KParams& prm, int rest, int warps) {
+  int best = 1;
+  float cost = 1.f;
+#pragma unroll
+  for (int tw = 2; tw <= K::NC; tw *= 2) {
+    if (K::NC % tw != 0 || (tw / 2) * K::TS >= prm.P) break;
+    const float rounds = (float)((rest + warps / tw - 1) / (warps / tw));
+    const float c = rounds / tw + 0.15f * rounds;
+    if (c < cost) {
+      cost = c;
+      best = tw;
+    }
   }
+  return best;
+}
+
+// Place of row head h's partition p in the workspace's m and l (o: times D).
+__device__ __forceinline__ size_t ws_row(const KParams& prm, int s, int h, int p) {
+  return ((size_t)s * prm.H + h) * prm.Pmax + p;
 }
 __device__ __forceinline__ void put_stat(const KParams& prm, const Kv4Unit& U, int col, float m, float l,
                                          uint64_t keep) {
-  const int h = U.h0 + col;
-  const size_t at = ((size_t)U.s * prm.H + h) * prm.Pmax + U.p;
+  const size_t at = ws_row(prm, U.s, U.h0 + col, U.p);
   st_f32_policy(prm.ws_m + at, m * kLn2, keep);
   st_f32_policy(prm.ws_l + at, l, keep);
-  if (U.np == 1 && prm.lse) prm.lse[out_row_rt(prm, U.s, h)] = m * kLn2 + logf(l);
+  if (U.np == 1 && prm.lse) prm.lse[out_row_rt(prm, U.s, U.h0 + col)] = m * kLn2 + logf(l);
 }
-// (A NaN sum stays NaN: only an empty row divides by nothing.)
-__device__ __forceinline__ float inverse(float l) { return l == 0.f ? 0.f : 1.f / l; }
 
 // Unused partitions: sentinels (m = -inf, l = 0).  Empty sequences: zeros (a
-// multi-query sequence is never empty: it holds its new tokens).
+// multi-query sequence is never empty: it holds its new tokens).  A warp takes
+// a row (s, h) at a time.
 template <class K>
-__device__ __forceinline__ void kv4_sentinels(const KParams& prm) {
+__device__ __forceinline__ void kv4_sentinels(const KParams& prm, const int* lens, int warp, int lane) {
   using T = typename K::T;
-  const int S = prm.S, H = prm.H, Pmax = prm.Pmax;
-  const long long me = (long long)blockIdx.x * K::THREADS + threadIdx.x, n = (long long)gridDim.x * K::THREADS;
-  auto parts_of = [&](int s) { return (kv4_tokens(prm, s, K::TB) + prm.P - 1) / prm.P; };
-  for (long long i = me; i < (long long)S * H * Pmax; i += n) {
-    const int s = (int)(i / ((long long)H * Pmax)), p = (int)(i % Pmax);
-    if (p >= parts_of(s)) {
-      prm.ws_m[i] = -INFINITY;
-      prm.ws_l[i] = 0.f;
+  const int rows = prm.S * prm.H, step = gridDim.x * K::NC;
+  for (int row = blockIdx.x + gridDim.x * warp; row < rows; row += step) {
+    const int np = (lens[row / prm.H] + prm.P - 1) / prm.P;
+    for (int p = np + lane; p < prm.Pmax; p += 32) {
+      prm.ws_m[(size_t)row * prm.Pmax + p] = -INFINITY;
+      prm.ws_l[(size_t)row * prm.Pmax + p] = 0.f;
     }
-  }
-  if (prm.q_len == 1) {
-    constexpr int D16 = K::D * 2 / 16;
-    uint4* out = static_cast<uint4*>(prm.out);
-    for (long long i = me; i < (long long)S * H * D16; i += n)
-      if (parts_of((int)(i / ((long long)H * D16))) == 0) out[i] = make_uint4(0, 0, 0, 0);
-    if (prm.lse)
-      for (long long i = me; i < (long long)S * H; i += n)
-        if (parts_of((int)(i / H)) == 0) prm.lse[i] = -INFINITY;
+    if (np == 0 && prm.q_len == 1) {
+      uint4* out = reinterpret_cast<uint4*>(static_cast<T*>(prm.out) + (size_t)row * K::D);
+      for (int i = lane; i < K::D / 8; i += 32) out[i] = make_uint4(0, 0, 0, 0);
+      if (prm.lse && lane == 0) prm.lse[row] = -INFINITY;
+    }
   }
 }
 
@@ -713,64 +702,82 @@ __device__ __forceinline__ void bulk_copy_cta(uint32_t dst, const void* src, uin
       : "memory");
 }
 
-// A warp's run of a unit's stages: refills its own ring.  (Everything but the
-// ids is the same in all lanes.)
+// A warp's stages, asked for ahead of their use: those of a run of blocks, then
+// those of the run that `queue` named.  (Everything but the ids is the same in
+// all lanes.)
 template <class K>
 struct Kv4Stream {
+  struct Run {
+    const int32_t* row;  // block ids
+    const uint8_t* base; // the kv head's record of block 0
+    int blocks;
+  };
+  const KParams& prm;
   uint32_t in, out;      // byte offsets in the ring of the next stage to fill, and of the next to use
   uint32_t bar_in, bar_out, ph_out;  // their barriers, and the phase of the latter
-  int nb, left;          // blocks of the run; those not asked for yet
-  int ids, ids_next;     // lane's ids of the current window of 32 blocks, and of the one after
   uint32_t ring, bars;   // shared addresses of the warp's ring and barriers
-  const int32_t* row;    // the run's block ids
-  const uint8_t* base;   // the kv head's record of block 0
+  Run cur, next;
+  int blk;               // blocks of the current run asked for
+  int ahead;             // stages asked for and not used
+  int ids, ids_after;    // lane's ids of the current window of 32 blocks, and of the one after
+  int ids_next;          // ... and of the next run's first window
   size_t block_bytes;    // of all kv heads
   uint64_t policy;
 
-  __device__ __forceinline__ Kv4Stream(const KParams& prm, uint32_t r, uint32_t b)
-      : in(0), out(0), bar_in(b), bar_out(b), ph_out(0), nb(0), left(0), ring(r), bars(b),
-        block_bytes((size_t)prm.KH * K::REC), policy(l2_policy_evict_first()) {}
+  __device__ __forceinline__ Kv4Stream(const KParams& p, uint32_t r, uint32_t b)
+      : prm(p), in(0), out(0), bar_in(b), bar_out(b), ph_out(0), ring(r), bars(b), cur{nullptr, nullptr, 0},
+        next{nullptr, nullptr, 0}, blk(0), ahead(0), ids(0), ids_after(0), ids_next(0),
+        block_bytes((size_t)p.KH * K::REC), policy(l2_policy_evict_first()) {}
 
-  __device__ __forceinline__ int fetch(int b0, int lane) const { return b0 + lane < nb ? __ldg(row + b0 + lane) : 0; }
-
-  __device__ __forceinline__ void start(const KParams& prm, const int32_t* table, const uint8_t* cache_kv, int blocks,
-                                        int lane) {
-    row = table;
-    base = cache_kv;
-    nb = left = blocks;
-    ids = fetch(0, lane);
-    ids_next = fetch(32, lane);
-    ids = check_block_id(prm, ids);
-    for (int i = 0; i < K::NS; ++i) issue(prm, lane);
+  __device__ __forceinline__ static int fetch(const Run& r, int b0, int lane) {
+    return b0 + lane < r.blocks ? __ldg(r.row + b0 + lane) : 0;
   }
-  // Fills the next stage (it is free: this warp has used it, or never filled it).
-  __device__ __forceinline__ void issue(const KParams& prm, int lane) {
-    if (left <= 0) return;
-    const int b0 = nb - left, w = b0 & 31;
-    if (w == 0 && b0 > 0) {
+  // The run to follow the current one.
+  __device__ __forceinline__ void queue(const Run& r, int lane) {
+    next = r;
+    ids_next = fetch(r, 0, lane);
+  }
+  __device__ __forceinline__ void fill(int lane) {
+    while (ahead < K::NS && issue(lane)) {
+    }
+  }
+  // Fills the next stage (it is free: this warp has used it, or never filled
+  // it); false: nothing is left to ask for.
+  __device__ __forceinline__ bool issue(int lane) {
+    if (blk >= cur.blocks) {
+      if (next.blocks == 0) return false;
+      cur = next;
+      next.blocks = 0;
+      blk = 0;
       ids = check_block_id(prm, ids_next);
-      ids_next = fetch(b0 + 32, lane);
+      ids_after = fetch(cur, 32, lane);
+    } else if ((blk & 31) == 0) {
+      ids = check_block_id(prm, ids_after);
+      ids_after = fetch(cur, blk + 32, lane);
     }
     int id[K::NBLK];
 #pragma unroll
-    for (int k = 0; k < K::NBLK; ++k) id[k] = __shfl_sync(0xffffffffu, ids, w + k);
-    const int n = min(K::NBLK, left);
+    for (int k = 0; k < K::NBLK; ++k) id[k] = __shfl_sync(0xffffffffu, ids, (blk + k) & 31);
+    const int n = min(K::NBLK, cur.blocks - blk);
     if (elect_one()) {
       mbar_arrive_expect_tx(bar_in, (uint32_t)n * K::REC);
 #pragma unroll
       for (int k = 0; k < K::NBLK; ++k)
-        if (k < n) bulk_copy_cta(ring + in + k * K::REC, base + (uint32_t)id[k] * block_bytes, K::REC, bar_in, policy);
+        if (k < n)
+          bulk_copy_cta(ring + in + k * K::REC, cur.base + (uint32_t)id[k] * block_bytes, K::REC, bar_in, policy);
     }
-    left -= K::NBLK;
+    blk += K::NBLK;
+    ++ahead;
     in += K::STAGE;
     bar_in += 8;
     if (in == K::NS * K::STAGE) {
       in = 0;
       bar_in = bars;
     }
+    return true;
   }
   // Waits for the next stage to land; false: gave up.
-  __device__ __forceinline__ bool wait(const KParams& prm, volatile int* abort_flag) const {
+  __device__ __forceinline__ bool wait(volatile int* abort_flag) const {
     if (__all_sync(0xffffffffu, mbar_try_wait(bar_out, ph_out))) return true;
     return kv4_wait_slow(bar_out, ph_out, abort_flag, prm.hdr + kHdrError, prm.timeout_ns, (int)(out / K::STAGE));
   }
@@ -779,6 +786,7 @@ struct Kv4Stream {
     // of it are ordered before that by a proxy fence.
     fence_proxy_async_smem();
     __syncwarp();
+    --ahead;
     out += K::STAGE;
     bar_out += 8;
     if (out == K::NS * K::STAGE) {
@@ -787,41 +795,40 @@ struct Kv4Stream {
       ph_out ^= 1u;
     }
   }
-  // After a wait that gave up at stage `done` of the run: no copy of this warp
-  // stays in flight (bounded).
-  __device__ __forceinline__ void drain(int done) {
-    const int asked = (nb - max(left, 0) + K::NBLK - 1) / K::NBLK;
-    for (; done < asked; ++done) {
+  // After a wait that gave up: nothing more is asked for, and no copy of this
+  // warp stays in flight (bounded).
+  __device__ __forceinline__ void drain() {
+    while (ahead > 0) {
       const uint64_t t0 = global_timer_ns();
       while (!mbar_try_wait(bar_out, ph_out) && (long long)(global_timer_ns() - t0) < 100000000LL) {
       }
       used();
     }
+    cur.blocks = next.blocks = 0;
   }
 };
 
 template <class K>
 __global__ void __launch_bounds__(K::THREADS, 1) kv4_decode_kernel(const __grid_constant__ KParams prm) {
   using T = typename K::T;
+  using Run = typename Kv4Stream<K>::Run;
   extern __shared__ __align__(1024) uint8_t smem[];
   // (The warp index by a shuffle: known to be the same in all lanes.)
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const uint32_t sbase = smem_addr(smem);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + K::OFF_FLAGS);
   int* bad_len = reinterpret_cast<int*>(smem + K::OFF_FLAGS + 16);
-  volatile int* team_next = reinterpret_cast<volatile int*>(smem + K::OFF_NEXT);
   int* pref = reinterpret_cast<int*>(smem + K::OFF_PREF);
+  int* lens = pref + kMaxSeqsPerLaunch + 1;
   if (tid == 0) {
     *abort_flag = 0;
     *bad_len = 0;
   }
-  if (lane < K::NSMAX) mbar_init(sbase + K::OFF_BAR + (warp * K::NSMAX + lane) * 8, 1);
+  if (lane < K::NS) mbar_init(sbase + K::OFF_BAR + (warp * K::NSMAX + lane) * 8, 1);
   fence_mbarrier_init();
   __syncthreads();
-  // pref[s]: partitions of the sequences before s (an exclusive scan; the warp
-  // totals are kept in the ring, not filled yet).
+  // pref: an exclusive scan (the warp totals are kept in the ring, not filled yet).
   {
-    constexpr int NW = K::NC;
     int* scan = reinterpret_cast<int*>(smem);
     const int S = prm.S, per = (S + K::THREADS - 1) / K::THREADS;
     const int beg = min(tid * per, S), end = min(beg + per, S);
@@ -829,10 +836,11 @@ __global__ void __launch_bounds__(K::THREADS, 1) kv4_decode_kernel(const __grid_
     int sum = 0;
     for (int s = beg; s < end; ++s) {
       // (A multi-query sequence holds its q_len new tokens.)
-      bad |= prm.lens[s] < (prm.q_len > 1 ? prm.q_len : 0) || prm.lens[s] > prm.MB * K::TB;
-      const int np = (kv4_tokens(prm, s, K::TB) + prm.P - 1) / prm.P;
+      const int L = prm.lens[s], cap = prm.MB * K::TB;
+      bad |= L < (prm.q_len > 1 ? prm.q_len : 0) || L > cap;
+      lens[s] = min(max(L, 0), cap);
       pref[s] = sum;
-      sum += np;
+      sum += (lens[s] + prm.P - 1) / prm.P;
     }
     if (bad) *bad_len = 1;
     int incl = sum;
@@ -845,7 +853,7 @@ __global__ void __launch_bounds__(K::THREADS, 1) kv4_decode_kernel(const __grid_
     __syncthreads();
     int before = 0, all = 0;
 #pragma unroll
-    for (int w = 0; w < NW; ++w) {
+    for (int w = 0; w < K::NC; ++w) {
       const int v = scan[w];
       if (w < warp) before += v;
       all += v;
@@ -855,88 +863,131 @@ __global__ void __launch_bounds__(K::THREADS, 1) kv4_decode_kernel(const __grid_
     fence_proxy_async_smem();  // the ring is filled by bulk copies from here on
   }
   __syncthreads();
-  const Kv4Plan pl = make_plan<K>(prm, pref[prm.S]);
+  // Units [0, solo) go to single warps, the rest to teams of TW.
+  const int total = pref[prm.S] * prm.KH * prm.hg_per_kv, warps = (int)gridDim.x * K::NC;
+  int solo = total / warps * warps;
+  const int TW = tail_team<K>(prm, total - solo, warps);
+  if (TW == 1) solo = total;
   // A programmatic dependent of the kernel that clears the workspace header:
   // nothing below may touch the header before it has completed.
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (tid == 0 && *bad_len) atomicCAS(prm.hdr + kHdrError, 0, kErrDeviceBounds);
 
-  const int ltw = __ffs(pl.TW) - 1;
-  const int teams = K::NC >> ltw, team = warp >> ltw, tw = warp & (pl.TW - 1);
   const uint64_t keep = l2_policy_evict_last();
   Kv4Stream<K> in(prm, sbase + warp * K::RING, sbase + K::OFF_BAR + warp * K::NSMAX * 8);
   Kv4State<K> st(lane);
+  typename Kv4State<K>::Rows q;
+  auto run_of = [&](const Kv4Unit& U, int b0, int blocks) {
+    return Run{prm.bt + (size_t)U.s * prm.MB + U.t0 / K::TB + b0,
+               static_cast<const uint8_t*>(prm.kc) + (size_t)U.kv * K::REC, blocks};
+  };
+  auto load_rows = [&](const Kv4Unit& U) {
+    st.load_rows(q, [&](int i) { return static_cast<const T*>(prm.q) + out_row_rt(prm, U.s, U.h0 + i) * K::D; }, U.nh,
+                 lane);
+  };
+  // The next unit's query rows are loaded a stage ahead where registers allow.
+  constexpr bool kAhead = K::NT == 1 && K::D <= 128;
+
   // The first units are dealt out over the CTAs; the counter hands out the rest.
-  int u = blockIdx.x + (int)gridDim.x * team;
-  bool alive = true;
-  // The sentinels are written while the first copies fly.
-  bool sentinels = false;
-  while (u < pl.total) {
-    const Kv4Unit U = kv4_unit<K>(prm, pl, pref, u);
-    const int nst = (U.nb + K::NBLK - 1) / K::NBLK, per = (nst + pl.TW - 1) >> ltw;
-    const int i0 = min(tw * per, nst), b0 = i0 * K::NBLK, nb = min(per * K::NBLK, U.nb - b0);
-    int u_next = 0;
-    if (tw == 0 && lane == 0) u_next = atomicAdd(prm.hdr + kHdrWork, 1) + (int)gridDim.x * teams;
-    const int blocks = alive ? max(nb, 0) : 0, stages = (blocks + K::NBLK - 1) / K::NBLK;
-    in.start(prm, prm.bt + (size_t)U.s * prm.MB + U.t0 / K::TB + b0,
-             static_cast<const uint8_t*>(prm.kc) + (size_t)U.kv * K::REC, blocks, lane);
-    if (!sentinels) {
-      sentinels = true;
-      kv4_sentinels<K>(prm);
+  const int ltw = __ffs(TW) - 1, team = warp >> ltw, tw = warp & (TW - 1);
+  bool alone = true, alive = true;
+  int u = blockIdx.x + (int)gridDim.x * warp;
+  Kv4Unit U{};
+  if (u < solo) {
+    U = kv4_unit<K>(prm, pref, lens, u);
+    in.queue(run_of(U, 0, U.nb), lane);
+    in.fill(lane);
+    load_rows(U);
+  }
+  kv4_sentinels<K>(prm, lens, warp, lane);  // (while the first copies fly)
+  while (true) {
+    if (alone && u >= solo) {
+      // On to the teams' units, dealt out like the first ones.
+      if (TW == 1) break;
+      alone = false;
+      u = solo + blockIdx.x + (int)gridDim.x * team;
     }
-    st.begin_unit([&](int i) { return static_cast<const T*>(prm.q) + out_row_rt(prm, U.s, U.h0 + i) * K::D; }, U.nh,
-                  prm.scale_log2, lane);
+    if (u >= total) break;
+    int i0 = 0, n = U.stages, u_next = total;
+    if (alone) {
+      if (lane == 0) u_next = atomicAdd(prm.hdr + kHdrWork, 1) + warps;
+    } else {
+      U = kv4_unit<K>(prm, pref, lens, u);
+      const int per = (U.stages + TW - 1) >> ltw;
+      i0 = min(tw * per, U.stages);
+      n = min(per, U.stages - i0);
+      if (alive && n > 0) {
+        in.queue(run_of(U, i0 * K::NBLK, min(n * K::NBLK, U.nb - i0 * K::NBLK)), lane);
+        in.fill(lane);
+      }
+      load_rows(U);
+      u_next = u + (int)gridDim.x * (K::NC >> ltw);
+    }
+    st.begin_unit(q, prm.scale_log2);
     if (prm.q_len > 1) st.set_limits([&](int h) { return row_limit<true>(prm, U.L, U.h0 + h); }, lane);
     else st.set_limits([&](int) { return U.L; }, lane);
-    int n = U.t1 - U.t0 - i0 * K::TS, tok = U.t0 + i0 * K::TS;  // tokens from the stage on; its first
-    for (int i = 0; i < stages; ++i, n -= K::TS, tok += K::TS) {
-      if (!in.wait(prm, abort_flag)) {
-        in.drain(i);
+    Kv4Unit V = U;
+    int tok = U.t0 + i0 * K::TS;
+    for (int i = 0; i < n && alive; ++i, tok += K::TS) {
+      if (!in.wait(abort_flag)) {
+        in.drain();
         alive = false;
         break;
       }
-      st.pass(in.ring + in.out, n, tok, lane);
+      if (alone && i == (n > 1 ? 1 : 0)) {
+        // The claim has been answered: what is asked for runs on into the next unit.
+        u_next = __shfl_sync(0xffffffffu, u_next, 0);
+        if (u_next < solo) {
+          V = kv4_unit<K>(prm, pref, lens, u_next);
+          in.queue(run_of(V, 0, V.nb), lane);
+        }
+      }
+      if (kAhead && alone && i == n - 1 && u_next < solo) load_rows(V);
+      st.pass(in.ring + in.out, U.t1 - tok, tok, lane);
       in.used();
-      in.issue(prm, lane);
+      in.fill(lane);
     }
-    if (pl.TW == 1) {
-      if (!alive) break;
-      st.finish([](float ls) { return inverse(ls); },
-          [&](int col, int d, const float4& v) {
-            if (col < U.nh) put_row<K>(prm, U, col, d, v, keep);
-          },
-          [&](int col, float m, float ls) {
-            if (lane < 4 && col < U.nh) put_stat(prm, U, col, m, ls, keep);
-          },
-          lane);
-      u = __shfl_sync(0xffffffffu, u_next, 0);
+    if (alone) {
+      if (!alive) {
+        u = solo;
+        continue;
+      }
+      // The partition's normalised output, into the workspace; from there on
+      // to the output where the sequence has one partition.
+      float* rows = prm.ws_o + ws_row(prm, U.s, U.h0, U.p) * K::D;
+      const size_t stride = (size_t)prm.Pmax * K::D;
+      st.finish(rows, stride, U.nh, true, [&](int col, float m, float l) { put_stat(prm, U, col, m, l, keep); }, lane);
+      if (U.np == 1) {
+        __syncwarp();
+        for (int i = lane; i < U.nh * (K::D / 4); i += 32) {
+          const int col = i / (K::D / 4), d = 4 * (i - col * (K::D / 4));
+          store4<T>(static_cast<T*>(prm.out) + out_row_rt(prm, U.s, U.h0 + col) * K::D + d,
+                    *reinterpret_cast<const float4*>(rows + col * stride + d));
+        }
+      }
+      if (!kAhead && u_next < solo) load_rows(V);
+      U = V;
     } else {
       // The team's states, each in its warp's ring (whose stages are all used).
-      float* acc = reinterpret_cast<float*>(smem + warp * K::RING);
-      float* ml = acc + K::GT * K::AROW;
-      st.finish([](float) { return 1.f; },
-                [&](int col, int d, const float4& v) { *reinterpret_cast<float4*>(acc + col * K::AROW + d) = v; },
-                [&](int col, float m, float ls) {
-                  if (lane < 4) {
-                    ml[2 * col] = m;
-                    ml[2 * col + 1] = ls;
-                  }
+      float* state = reinterpret_cast<float*>(smem + warp * K::RING);
+      st.finish(state, K::AROW, K::GT, false,
+                [&](int col, float m, float l) {
+                  *reinterpret_cast<float2*>(state + K::GT * K::AROW + 2 * col) = make_float2(m, l);
                 },
                 lane);
-      if (tw == 0 && lane == 0) team_next[team] = *abort_flag ? pl.total : u_next;
-      named_barrier_sync(1 + team, pl.TW * 32);
+      named_barrier_sync(1 + team, TW * 32);
       // A slice of the rows each; the warps' states in warp order.
       const float* first = reinterpret_cast<const float*>(smem + (warp - tw) * K::RING);
       constexpr int D4 = K::D / 4, WR = K::RING / 4;
-      for (int i = tw * 32 + lane; i < U.nh * D4; i += pl.TW * 32) {
+      for (int i = tw * 32 + lane; i < U.nh * D4; i += TW * 32) {
         const int col = i / D4, d4 = i - col * D4;
         float M = -INFINITY;
-        for (int w = 0; w < pl.TW; ++w) M = fmaxf(M, first[w * WR + K::GT * K::AROW + 2 * col]);
+        for (int w = 0; w < TW; ++w) M = fmaxf(M, first[w * WR + K::GT * K::AROW + 2 * col]);
         // (A row that sees nothing in this partition has M = -inf: its weights are 0.)
         const float Ms = M == -INFINITY ? 0.f : M;
         float den = 0.f;
         float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int w = 0; w < pl.TW; ++w) {
+        for (int w = 0; w < TW; ++w) {
           const float2 s2 = *reinterpret_cast<const float2*>(first + w * WR + K::GT * K::AROW + 2 * col);
           const float f = ex2(s2.x - Ms);
           const float4 v = *reinterpret_cast<const float4*>(first + w * WR + col * K::AROW + 4 * d4);
@@ -946,17 +997,20 @@ __global__ void __launch_bounds__(K::THREADS, 1) kv4_decode_kernel(const __grid_
           num.z = fmaf(f, v.z, num.z);
           num.w = fmaf(f, v.w, num.w);
         }
-        const float inv = inverse(den);
-        put_row<K>(prm, U, col, 4 * d4, make_float4(num.x * inv, num.y * inv, num.z * inv, num.w * inv), keep);
+        const float inv = den == 0.f ? 0.f : 1.f / den;
+        const float4 val = make_float4(num.x * inv, num.y * inv, num.z * inv, num.w * inv);
+        if (U.np == 1) {
+          store4<T>(static_cast<T*>(prm.out) + out_row_rt(prm, U.s, U.h0 + col) * K::D + 4 * d4, val);
+        } else {
+          st_f4_policy(reinterpret_cast<float4*>(prm.ws_o + ws_row(prm, U.s, U.h0 + col, U.p) * K::D) + d4, val, keep);
+        }
         if (d4 == 0) put_stat(prm, U, col, M, den, keep);
       }
-      u = team_next[team];
       fence_proxy_async_smem();  // the rings are filled by bulk copies again
-      named_barrier_sync(1 + team, pl.TW * 32);
+      named_barrier_sync(1 + team, TW * 32);
     }
-    if (*abort_flag && pl.TW == 1) break;
+    u = u_next;
   }
-  if (!sentinels) kv4_sentinels<K>(prm);
   // Phase 2 may be launched once every CTA has said so or ended (it waits for
   // this grid to complete before it reads anything).
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
