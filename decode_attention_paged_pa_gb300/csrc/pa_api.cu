@@ -107,26 +107,26 @@ bool ws_layout(int S, int H, int KH, int D, int MB, int BS, int P, WsLayout* w) 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 // The 4-bit family's launch, dispatched on the head size.
-cudaError_t launch_kv4_f16(const KParams& prm, int D, int BS, int nt, int max_ctas, cudaStream_t st) {
+cudaError_t launch_kv4_f16(const KParams& prm, int D, int BS, int nt, int kvu, int max_ctas, cudaStream_t st) {
   switch (D) {
-    case 64: return launch_kv4_d64_f16(prm, BS, nt, max_ctas, st);
-    case 80: return launch_kv4_d80_f16(prm, BS, nt, max_ctas, st);
-    case 96: return launch_kv4_d96_f16(prm, BS, nt, max_ctas, st);
-    case 112: return launch_kv4_d112_f16(prm, BS, nt, max_ctas, st);
-    case 128: return launch_kv4_d128_f16(prm, BS, nt, max_ctas, st);
-    case 256: return launch_kv4_d256_f16(prm, BS, nt, max_ctas, st);
+    case 64: return launch_kv4_d64_f16(prm, BS, nt, kvu, max_ctas, st);
+    case 80: return launch_kv4_d80_f16(prm, BS, nt, kvu, max_ctas, st);
+    case 96: return launch_kv4_d96_f16(prm, BS, nt, kvu, max_ctas, st);
+    case 112: return launch_kv4_d112_f16(prm, BS, nt, kvu, max_ctas, st);
+    case 128: return launch_kv4_d128_f16(prm, BS, nt, kvu, max_ctas, st);
+    case 256: return launch_kv4_d256_f16(prm, BS, nt, kvu, max_ctas, st);
     default: return cudaErrorInvalidValue;
   }
 }
 
-cudaError_t launch_kv4_bf16(const KParams& prm, int D, int BS, int nt, int max_ctas, cudaStream_t st) {
+cudaError_t launch_kv4_bf16(const KParams& prm, int D, int BS, int nt, int kvu, int max_ctas, cudaStream_t st) {
   switch (D) {
-    case 64: return launch_kv4_d64_bf16(prm, BS, nt, max_ctas, st);
-    case 80: return launch_kv4_d80_bf16(prm, BS, nt, max_ctas, st);
-    case 96: return launch_kv4_d96_bf16(prm, BS, nt, max_ctas, st);
-    case 112: return launch_kv4_d112_bf16(prm, BS, nt, max_ctas, st);
-    case 128: return launch_kv4_d128_bf16(prm, BS, nt, max_ctas, st);
-    case 256: return launch_kv4_d256_bf16(prm, BS, nt, max_ctas, st);
+    case 64: return launch_kv4_d64_bf16(prm, BS, nt, kvu, max_ctas, st);
+    case 80: return launch_kv4_d80_bf16(prm, BS, nt, kvu, max_ctas, st);
+    case 96: return launch_kv4_d96_bf16(prm, BS, nt, kvu, max_ctas, st);
+    case 112: return launch_kv4_d112_bf16(prm, BS, nt, kvu, max_ctas, st);
+    case 128: return launch_kv4_d128_bf16(prm, BS, nt, kvu, max_ctas, st);
+    case 256: return launch_kv4_d256_bf16(prm, BS, nt, kvu, max_ctas, st);
     default: return cudaErrorInvalidValue;
   }
 }
@@ -264,7 +264,11 @@ int decode_impl(void* out, float* lse, const void* query, const void* key_cache,
   // values covers both), head sizes up to 128 and blocks of 8, 16 or 32 tokens.
   const bool pairs = variant == PA_VARIANT_MMA && !wide && G * 2 == kMmaGroup && KH % 2 == 0 &&
                      D <= 128 && (BS == 8 || BS == 16 || BS == 32) && !kv4;
-  const int kvu = pairs ? 2 : 1;
+  // Over a 4-bit cache, two kv heads a unit where each has at most four rows
+  // (head sizes up to 128, blocks of up to 32 tokens: two stages of both heads
+  // fit a warp's ring).
+  const bool kv4_pairs = kv4 && G * 2 <= kMmaGroup && KH % 2 == 0 && D <= 128 && BS <= 32;
+  const int kvu = pairs || kv4_pairs ? 2 : 1;
   const int hg_per_kv = (G + gt - 1) / gt;
   const int n_hg = KH * hg_per_kv / kvu;
   const int rows_per_launch = kMaxSeqsPerLaunch;  // sequences per launch
@@ -330,8 +334,8 @@ int decode_impl(void* out, float* lse, const void* query, const void* key_cache,
     prm.timeout_ns = timeout_ns > 0 ? timeout_ns : (1LL << 31);
     cudaError_t e;
     if (kv4)
-      e = dtype == PA_DTYPE_FP16 ? launch_kv4_f16(prm, D, BS, nt, max_ctas, st)
-                                 : launch_kv4_bf16(prm, D, BS, nt, max_ctas, st);
+      e = dtype == PA_DTYPE_FP16 ? launch_kv4_f16(prm, D, BS, nt, kvu, max_ctas, st)
+                                 : launch_kv4_bf16(prm, D, BS, nt, kvu, max_ctas, st);
     else if (kv_fp8 && pairs && BS == 8)
       e = dtype == PA_DTYPE_FP16 ? launch_mma8_gb8_f16(prm, D, max_ctas, st)
                                  : launch_mma8_gb8_bf16(prm, D, max_ctas, st);

@@ -73,20 +73,23 @@
 
 namespace pa {
 
-// TB: tokens per block.
-template <typename T_, int D_, int NT_, int TB_>
+// TB: tokens per block.  KVU: kv heads per unit; with two (at most four query
+// rows each), head u's rows are columns 4u .. 4u + 3, so the softmax and the
+// weights of a tile serve both, and a block's copy covers both records.
+template <typename T_, int D_, int NT_, int TB_, int KVU_>
 struct Kv4 {
   using T = T_;
-  static constexpr int D = D_, NT = NT_, GT = 8 * NT_, TB = TB_;
+  static constexpr int D = D_, NT = NT_, GT = 8 * NT_, TB = TB_, KVU = KVU_;
+  static_assert(KVU_ == 1 || (KVU_ == 2 && NT_ == 1), "two heads share one column tile");
 #ifndef PA_KV4_TILES
 #define PA_KV4_TILES 4
 #endif
   // 16-token tiles per stage (two at head size 256, for two stages in the ring).
-  static constexpr int NTI = TB_ == 64 ? 4 : D_ > 128 ? 2 : PA_KV4_TILES;
+  static constexpr int NTI = TB_ == 64 ? 4 : D_ > 128 || KVU_ == 2 ? 2 : PA_KV4_TILES;
   static constexpr int TS = 16 * NTI;            // tokens per stage
   static constexpr int NBLK = TS / TB_;          // blocks per stage
   static_assert(NBLK >= 1, "a stage holds whole blocks");
-  static constexpr uint32_t REC = (uint32_t)TB_ * (D_ + 8), STAGE = REC * NBLK;
+  static constexpr uint32_t REC = (uint32_t)TB_ * (D_ + 8), BLOCK = REC * KVU_, STAGE = BLOCK * NBLK;
   // Warps per CTA: as many as the accumulators' registers allow (128 or 255 a thread).
 #ifndef PA_KV4_NC
 #define PA_KV4_NC 8
@@ -170,14 +173,14 @@ struct Kv4Offsets {
   static constexpr uint32_t voff = K::TB * K::D / 2;  // value codes in a record
   static constexpr uint32_t poff = K::TB * K::D;      // parameters in a record
   // Tokens 8..15 of a tile after 0..7: codes, parameters.
-  static constexpr uint32_t hd = K::TB == 8 ? K::REC : 8 * K::XB;
-  static constexpr uint32_t hdp = K::TB == 8 ? K::REC : 64;
+  static constexpr uint32_t hd = K::TB == 8 ? K::BLOCK : 8 * K::XB;
+  static constexpr uint32_t hdp = K::TB == 8 ? K::BLOCK : 64;
   // Tile t.
   __device__ static constexpr uint32_t tile(int t) {
-    return (uint32_t)(16 * t / K::TB) * K::REC + (uint32_t)(16 * t % K::TB) * K::XB;
+    return (uint32_t)(16 * t / K::TB) * K::BLOCK + (uint32_t)(16 * t % K::TB) * K::XB;
   }
   __device__ static constexpr uint32_t tilep(int t) {
-    return (uint32_t)(16 * t / K::TB) * K::REC + (uint32_t)(16 * t % K::TB) * 8;
+    return (uint32_t)(16 * t / K::TB) * K::BLOCK + (uint32_t)(16 * t % K::TB) * 8;
   }
 };
 
@@ -185,7 +188,7 @@ struct Kv4Offsets {
 template <class K>
 struct Kv4State {
   using T = typename K::T;
-  static constexpr int NT = K::NT, NK = K::NK, NMT = K::NMT, KW = K::KW, VW = K::VW, NSLAB = K::NSLAB, NTI = K::NTI;
+  static constexpr int NT = K::NT, NK = K::NK, NMT = K::NMT, KW = K::KW, VW = K::VW, NSLAB = K::NSLAB, NTI = K::NTI, KVU = K::KVU;
   static constexpr uint32_t LO = 0x000f000fu, HI = 0x00f000f0u;
 
   uint32_t qb[NT][NK][2];          // Q^T fragments: the query row of column lane / 4
@@ -203,7 +206,7 @@ struct Kv4State {
   __device__ __forceinline__ explicit Kv4State(int lane) {
     const int r = lane >> 2, c = lane & 3;
     ko = tok_lo(r) * K::XB + c * (KW * 4);
-    po = tok_lo(r) * 8;
+    po = tok_lo(r) * 8 + (KVU == 2 ? (c >> 1) * K::REC : 0u);  // (of its columns' kv head)
     // Slots 2c, 2c + 1 and 2c + 8, 2c + 9 hold tokens c, 7 - c, 8 + c, 15 - c.
     vo = c * K::XB + r * (VW * 4);
     vo2 = (7 - c) * K::XB + r * (VW * 4);
@@ -234,8 +237,18 @@ struct Kv4State {
     }
   }
 
-  // The unit's query rows as this lane needs them: row(i) is row i (of nh) in
-  // global memory.  Dims 8w .. 8w + 7 of a slab are word w; this lane holds
+  // Column `col` holds query row row_of(col, nh) of the unit, where it holds
+  // one; nh: rows of a kv head.
+  __device__ __forceinline__ static bool has_row(int col, int nh) { return (KVU == 2 ? col & 3 : col) < nh; }
+  __device__ __forceinline__ static int row_of(int col, int nh) {
+    return KVU == 2 ? (col >> 2) * nh + (col & 3) : col;
+  }
+  __device__ __forceinline__ static int column_of(int row, int nh) {
+    return KVU == 2 && row >= nh ? 4 + row - nh : row;
+  }
+
+  // The unit's query rows as this lane needs them: row(i) is row i in global
+  // memory.  Dims 8w .. 8w + 7 of a slab are word w; this lane holds
   // words c * KW ...
   struct Rows {
     uint4 v[NT][NSLAB * KW];
@@ -245,7 +258,7 @@ struct Kv4State {
     const int n = lane >> 2, c = lane & 3;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      const T* p = 8 * t + n < nh ? row(8 * t + n) : nullptr;
+      const T* p = has_row(8 * t + n, nh) ? row(row_of(8 * t + n, nh)) : nullptr;
 #pragma unroll
       for (int sl = 0; sl < NSLAB; ++sl)
 #pragma unroll
@@ -311,13 +324,14 @@ struct Kv4State {
   }
 
   template <class F>
-  __device__ __forceinline__ void set_limits(F limit_of, int lane) {
+  __device__ __forceinline__ void set_limits(F limit_of, int nh, int lane) {
     int least = 0x7fffffff;
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        lim[t][j] = limit_of(8 * t + (lane & 3) * 2 + j);
+        const int col = 8 * t + (lane & 3) * 2 + j;
+        lim[t][j] = has_row(col, nh) ? limit_of(row_of(col, nh)) : 0x7fffffff;
         least = min(least, lim[t][j]);
       }
     minlim = __reduce_min_sync(0xffffffffu, least);
@@ -330,39 +344,53 @@ struct Kv4State {
     float y[NTI][NT][4];  // scores, less the columns' references
     float2 pv[NTI][2];    // (value scale, value zero) of the lane's score rows r, r + 8 of each tile
     const uint32_t ka = codes + ko, pa = codes + O::poff + po;
+    const bool second = (lane & 2) != 0;  // KVU = 2: the lane's score columns are the second head's
     float dot[NTI][NT][4];
 #pragma unroll
-    for (int t0 = 0; t0 < NTI; t0 += 2)
+    for (int t0 = 0; t0 < NTI; t0 += 2) {
+      float du[KVU][2][NT][4];
 #pragma unroll
       for (int sl = 0; sl < NSLAB; ++sl) {
-        uint32_t wl[2][KW], wh[2][KW];
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          key_words(ka + O::tile(t0 + t) + sl * O::slab, wl[t]);
-          key_words(ka + O::tile(t0 + t) + sl * O::slab + O::hd, wh[t]);
-        }
-        // (Two tiles' chains of dependent products run side by side.)
-#pragma unroll
-        for (int i = 0; i < KW; ++i) {
-          const int ks = (sl * KW + i) * 2;
+        for (int u = 0; u < KVU; ++u) {
+          uint32_t wl[2][KW], wh[2][KW];
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
-            const uint32_t a[4] = {wl[t][i] & LO, wh[t][i] & LO, wl[t][i] & HI, wh[t][i] & HI};
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              if (ks == 0) mma_f16_first(dot[t0 + t][n], a, qb[n][ks][0], qb[n][ks][1]);
-              else mma_f16(dot[t0 + t][n], a, qb[n][ks][0], qb[n][ks][1]);
-            }
+            key_words(ka + u * K::REC + O::tile(t0 + t) + sl * O::slab, wl[t]);
+            key_words(ka + u * K::REC + O::tile(t0 + t) + sl * O::slab + O::hd, wh[t]);
           }
+          // (Two tiles' chains of dependent products run side by side.)
 #pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            const uint32_t xl = wl[t][i] >> 8, xh = wh[t][i] >> 8;
-            const uint32_t b[4] = {xl & LO, xh & LO, xl & HI, xh & HI};
+          for (int i = 0; i < KW; ++i) {
+            const int ks = (sl * KW + i) * 2;
 #pragma unroll
-            for (int n = 0; n < NT; ++n) mma_f16(dot[t0 + t][n], b, qb[n][ks + 1][0], qb[n][ks + 1][1]);
+            for (int t = 0; t < 2; ++t) {
+              const uint32_t a[4] = {wl[t][i] & LO, wh[t][i] & LO, wl[t][i] & HI, wh[t][i] & HI};
+#pragma unroll
+              for (int n = 0; n < NT; ++n) {
+                if (ks == 0) mma_f16_first(du[u][t][n], a, qb[n][ks][0], qb[n][ks][1]);
+                else mma_f16(du[u][t][n], a, qb[n][ks][0], qb[n][ks][1]);
+              }
+            }
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              const uint32_t xl = wl[t][i] >> 8, xh = wh[t][i] >> 8;
+              const uint32_t b[4] = {xl & LO, xh & LO, xl & HI, xh & HI};
+#pragma unroll
+              for (int n = 0; n < NT; ++n) mma_f16(du[u][t][n], b, qb[n][ks + 1][0], qb[n][ks + 1][1]);
+            }
           }
         }
       }
+      // (Every column meets both heads' keys; its own head's product counts.)
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            dot[t0 + t][n][i] = KVU == 2 && second ? du[KVU - 1][t][n][i] : du[0][t][n][i];
+    }
 #pragma unroll
     for (int t = 0; t < NTI; ++t) {
 #pragma unroll
@@ -408,7 +436,7 @@ struct Kv4State {
     if (__any_sync(0xffffffffu, raise)) raise_bounds(y, pv);
     if (full) weigh<false>(y, pv);
     else weigh<true>(y, pv);
-    values(y, codes + O::voff);
+    values(y, codes + O::voff, lane);
   }
 
   __device__ __forceinline__ static float column_max(const float (&y)[NTI][NT][4], int n, int j) {
@@ -501,7 +529,7 @@ struct Kv4State {
       }
   }
 
-  __device__ __forceinline__ void values(const float (&w)[NTI][NT][4], uint32_t codes) {
+  __device__ __forceinline__ void values(const float (&w)[NTI][NT][4], uint32_t codes, int lane) {
     using O = Kv4Offsets<K>;
 #pragma unroll
     for (int t = 0; t < NTI; ++t) {
@@ -513,7 +541,17 @@ struct Kv4State {
         const uint32_t eight[4] = {0x00080008u, 0x00080008u, 0x00080008u, 0x00080008u};
         mma_f16(acc8[n], eight, b0[n], b1[n]);
       }
-      const uint32_t va = codes + vo + O::tile(t), vd = codes + vo2 + O::tile(t);
+#pragma unroll
+      for (int u = 0; u < KVU; ++u) {
+      // Head u's product takes the weights of its own columns.
+      const bool mine = KVU == 1 || (lane >> 4) == u;
+      uint32_t m0[NT], m1[NT];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        m0[n] = mine ? b0[n] : 0u;
+        m1[n] = mine ? b1[n] : 0u;
+      }
+      const uint32_t va = codes + vo + u * K::REC + O::tile(t), vd = codes + vo2 + u * K::REC + O::tile(t);
 #pragma unroll
       for (int sl = 0; sl < NSLAB; ++sl) {
         uint32_t wa[2], wb[2], wc[2], wd[2];
@@ -546,20 +584,22 @@ struct Kv4State {
           const uint32_t f3[4] = {x0 & HI, x1 & HI, x2 & HI, x3 & HI};
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-            mma_f16(acc[mt][n], f0, b0[n], b1[n]);
-            mma_f16(acc[mt + 1][n], f1, b0[n], b1[n]);
-            mma_f16(acc[mt + 2][n], f2, b0[n], b1[n]);
-            mma_f16(acc[mt + 3][n], f3, b0[n], b1[n]);
+            mma_f16(acc[mt][n], f0, m0[n], m1[n]);
+            mma_f16(acc[mt + 1][n], f1, m0[n], m1[n]);
+            mma_f16(acc[mt + 2][n], f2, m0[n], m1[n]);
+            mma_f16(acc[mt + 3][n], f3, m0[n], m1[n]);
           }
         }
+      }
       }
     }
   }
 
-  // The unit's sums: row col (< nh) at rows + col * stride, over the row's
-  // weight sum where `divide`; stat(col, reference, weight sum) for each row.
+  // The unit's sums: its row i at rows + i * stride, over the row's weight sum,
+  // and stat(i, reference, weight sum); or, by_column, all columns' sums as
+  // they are, and stat by column.
   template <class Stat>
-  __device__ __forceinline__ void finish(float* rows, size_t stride, int nh, bool divide, Stat stat, int lane) {
+  __device__ __forceinline__ void finish(float* rows, size_t stride, int nh, bool by_column, Stat stat, int lane) {
     const int r = lane >> 2, c = lane & 3;
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -571,13 +611,13 @@ struct Kv4State {
           ls += __shfl_xor_sync(0xffffffffu, ls, k);
           zz += __shfl_xor_sync(0xffffffffu, zz, k);
         }
-        const int col = 8 * n + 2 * c + j;
-        if (col >= nh) continue;
-        if (r == 0) stat(col, thr[n][j] == -INFINITY ? -INFINITY : ms[n][j], ls);
+        const int col = 8 * n + 2 * c + j, row = by_column ? col : row_of(col, nh);
+        if (!by_column && !has_row(col, nh)) continue;
+        if (r == 0) stat(row, thr[n][j] == -INFINITY ? -INFINITY : ms[n][j], ls);
         // (A NaN sum stays NaN: only an empty row divides by nothing.)
-        const float f = divide ? (ls == 0.f ? 0.f : 1.f / ls) : 1.f;
+        const float f = by_column ? 1.f : ls == 0.f ? 0.f : 1.f / ls;
         const float vbf = vb * f, zf = zz * f;
-        float* o = rows + col * stride;
+        float* o = rows + row * stride;
         // Tiles of odd nibbles carry 2^-20 instead of 2^-24.
         const float e8 = acc8[n][j], e16 = 16.f * e8;
 #pragma unroll
@@ -605,13 +645,14 @@ struct Kv4State {
 // sequence s holds pref[s] .. pref[s + 1] - 1 (pref and the clamped lengths in
 // shared memory).
 struct Kv4Unit {
-  int s, p, np, L, t0, t1, kv, h0, nh;
+  int s, p, np, L, t0, t1;
+  int kv, h0, nh;  // first kv head and row head; rows per kv head
   int nb, stages;  // blocks, stages
 };
 template <class K>
 __device__ __forceinline__ Kv4Unit kv4_unit(const KParams& prm, const int* pref, const int* lens, int u) {
   Kv4Unit U;
-  const int n_hg = prm.KH * prm.hg_per_kv, pair = u / n_hg, hg = u - pair * n_hg;
+  const int n_hg = prm.KH / K::KVU * prm.hg_per_kv, pair = u / n_hg, hg = u - pair * n_hg;
   int lo = 0, hi = prm.S;  // pref[lo] <= pair < pref[lo + 1]
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -625,10 +666,16 @@ __device__ __forceinline__ Kv4Unit kv4_unit(const KParams& prm, const int* pref,
   U.t1 = min(U.t0 + prm.P, U.L);
   U.nb = (U.t1 - U.t0 + K::TB - 1) / K::TB;
   U.stages = (U.nb + K::NBLK - 1) / K::NBLK;
-  U.kv = prm.hg_per_kv == 1 ? hg : hg / prm.hg_per_kv;
-  const int part = hg - U.kv * prm.hg_per_kv;
-  U.h0 = U.kv * prm.G + part * K::GT;
-  U.nh = min(K::GT, prm.G - part * K::GT);
+  if constexpr (K::KVU == 2) {
+    U.kv = 2 * hg;
+    U.h0 = U.kv * prm.G;
+    U.nh = prm.G;
+  } else {
+    U.kv = prm.hg_per_kv == 1 ? hg : hg / prm.hg_per_kv;
+    const int part = hg - U.kv * prm.hg_per_kv;
+    U.h0 = U.kv * prm.G + part * K::GT;
+    U.nh = min(K::GT, prm.G - part * K::GT);
+  }
   return U;
 }
 
@@ -656,12 +703,12 @@ __device__ __forceinline__ int tail_team(const KParams& prm, int rest, int warps
 __device__ __forceinline__ size_t ws_row(const KParams& prm, int s, int h, int p) {
   return ((size_t)s * prm.H + h) * prm.Pmax + p;
 }
-__device__ __forceinline__ void put_stat(const KParams& prm, const Kv4Unit& U, int col, float m, float l,
+__device__ __forceinline__ void put_stat(const KParams& prm, const Kv4Unit& U, int row, float m, float l,
                                          uint64_t keep) {
-  const size_t at = ws_row(prm, U.s, U.h0 + col, U.p);
+  const size_t at = ws_row(prm, U.s, U.h0 + row, U.p);
   st_f32_policy(prm.ws_m + at, m * kLn2, keep);
   st_f32_policy(prm.ws_l + at, l, keep);
-  if (U.np == 1 && prm.lse) prm.lse[out_row_rt(prm, U.s, U.h0 + col)] = m * kLn2 + logf(l);
+  if (U.np == 1 && prm.lse) prm.lse[out_row_rt(prm, U.s, U.h0 + row)] = m * kLn2 + logf(l);
 }
 
 // Unused partitions: sentinels (m = -inf, l = 0).  Empty sequences: zeros (a
@@ -760,11 +807,11 @@ struct Kv4Stream {
     for (int k = 0; k < K::NBLK; ++k) id[k] = __shfl_sync(0xffffffffu, ids, (blk + k) & 31);
     const int n = min(K::NBLK, cur.blocks - blk);
     if (elect_one()) {
-      mbar_arrive_expect_tx(bar_in, (uint32_t)n * K::REC);
+      mbar_arrive_expect_tx(bar_in, (uint32_t)n * K::BLOCK);
 #pragma unroll
       for (int k = 0; k < K::NBLK; ++k)
         if (k < n)
-          bulk_copy_cta(ring + in + k * K::REC, cur.base + (uint32_t)id[k] * block_bytes, K::REC, bar_in, policy);
+          bulk_copy_cta(ring + in + k * K::BLOCK, cur.base + (uint32_t)id[k] * block_bytes, K::BLOCK, bar_in, policy);
     }
     blk += K::NBLK;
     ++ahead;
@@ -864,7 +911,7 @@ __global__ void __launch_bounds__(K::THREADS, 1) kv4_decode_kernel(const __grid_
   }
   __syncthreads();
   // Units [0, solo) go to single warps, the rest to teams of TW.
-  const int total = pref[prm.S] * prm.KH * prm.hg_per_kv, warps = (int)gridDim.x * K::NC;
+  const int total = pref[prm.S] * (prm.KH / K::KVU) * prm.hg_per_kv, warps = (int)gridDim.x * K::NC;
   int solo = total / warps * warps;
   const int TW = tail_team<K>(prm, total - solo, warps);
   if (TW == 1) solo = total;
@@ -924,8 +971,8 @@ __global__ void __launch_bounds__(K::THREADS, 1) kv4_decode_kernel(const __grid_
       u_next = u + (int)gridDim.x * (K::NC >> ltw);
     }
     st.begin_unit(q, prm.scale_log2);
-    if (prm.q_len > 1) st.set_limits([&](int h) { return row_limit<true>(prm, U.L, U.h0 + h); }, lane);
-    else st.set_limits([&](int) { return U.L; }, lane);
+    if (prm.q_len > 1) st.set_limits([&](int h) { return row_limit<true>(prm, U.L, U.h0 + h); }, U.nh, lane);
+    else st.set_limits([&](int) { return U.L; }, U.nh, lane);
     Kv4Unit V = U;
     int tok = U.t0 + i0 * K::TS;
     for (int i = 0; i < n && alive; ++i, tok += K::TS) {
@@ -956,10 +1003,10 @@ __global__ void __launch_bounds__(K::THREADS, 1) kv4_decode_kernel(const __grid_
       // to the output where the sequence has one partition.
       float* rows = prm.ws_o + ws_row(prm, U.s, U.h0, U.p) * K::D;
       const size_t stride = (size_t)prm.Pmax * K::D;
-      st.finish(rows, stride, U.nh, true, [&](int col, float m, float l) { put_stat(prm, U, col, m, l, keep); }, lane);
+      st.finish(rows, stride, U.nh, false, [&](int col, float m, float l) { put_stat(prm, U, col, m, l, keep); }, lane);
       if (U.np == 1) {
         __syncwarp();
-        for (int i = lane; i < U.nh * (K::D / 4); i += 32) {
+        for (int i = lane; i < U.nh * K::KVU * (K::D / 4); i += 32) {
           const int col = i / (K::D / 4), d = 4 * (i - col * (K::D / 4));
           store4<T>(static_cast<T*>(prm.out) + out_row_rt(prm, U.s, U.h0 + col) * K::D + d,
                     *reinterpret_cast<const float4*>(rows + col * stride + d));
@@ -970,7 +1017,7 @@ __global__ void __launch_bounds__(K::THREADS, 1) kv4_decode_kernel(const __grid_
     } else {
       // The team's states, each in its warp's ring (whose stages are all used).
       float* state = reinterpret_cast<float*>(smem + warp * K::RING);
-      st.finish(state, K::AROW, K::GT, false,
+      st.finish(state, K::AROW, U.nh, true,
                 [&](int col, float m, float l) {
                   *reinterpret_cast<float2*>(state + K::GT * K::AROW + 2 * col) = make_float2(m, l);
                 },
@@ -979,8 +1026,8 @@ __global__ void __launch_bounds__(K::THREADS, 1) kv4_decode_kernel(const __grid_
       // A slice of the rows each; the warps' states in warp order.
       const float* first = reinterpret_cast<const float*>(smem + (warp - tw) * K::RING);
       constexpr int D4 = K::D / 4, WR = K::RING / 4;
-      for (int i = tw * 32 + lane; i < U.nh * D4; i += TW * 32) {
-        const int col = i / D4, d4 = i - col * D4;
+      for (int i = tw * 32 + lane; i < U.nh * K::KVU * D4; i += TW * 32) {
+        const int row = i / D4, d4 = i - row * D4, col = Kv4State<K>::column_of(row, U.nh);
         float M = -INFINITY;
         for (int w = 0; w < TW; ++w) M = fmaxf(M, first[w * WR + K::GT * K::AROW + 2 * col]);
         // (A row that sees nothing in this partition has M = -inf: its weights are 0.)
@@ -1000,11 +1047,11 @@ __global__ void __launch_bounds__(K::THREADS, 1) kv4_decode_kernel(const __grid_
         const float inv = den == 0.f ? 0.f : 1.f / den;
         const float4 val = make_float4(num.x * inv, num.y * inv, num.z * inv, num.w * inv);
         if (U.np == 1) {
-          store4<T>(static_cast<T*>(prm.out) + out_row_rt(prm, U.s, U.h0 + col) * K::D + 4 * d4, val);
+          store4<T>(static_cast<T*>(prm.out) + out_row_rt(prm, U.s, U.h0 + row) * K::D + 4 * d4, val);
         } else {
-          st_f4_policy(reinterpret_cast<float4*>(prm.ws_o + ws_row(prm, U.s, U.h0 + col, U.p) * K::D) + d4, val, keep);
+          st_f4_policy(reinterpret_cast<float4*>(prm.ws_o + ws_row(prm, U.s, U.h0 + row, U.p) * K::D) + d4, val, keep);
         }
-        if (d4 == 0) put_stat(prm, U, col, M, den, keep);
+        if (d4 == 0) put_stat(prm, U, row, M, den, keep);
       }
       fence_proxy_async_smem();  // the rings are filled by bulk copies again
       named_barrier_sync(1 + team, TW * 32);

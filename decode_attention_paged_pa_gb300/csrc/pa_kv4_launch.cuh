@@ -35,23 +35,28 @@ static cudaError_t kv4_go(const KParams& prm, int max_ctas, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, kv4_decode_kernel<K>, prm);
 }
 
-template <typename T, int D, int NT>
+template <typename T, int D, int NT, int KVU>
 static cudaError_t kv4_go_bs(const KParams& prm, int BS, int max_ctas, cudaStream_t st) {
   switch (BS) {
-    case 8: return kv4_go<Kv4<T, D, NT, 8>>(prm, max_ctas, st);
-    case 16: return kv4_go<Kv4<T, D, NT, 16>>(prm, max_ctas, st);
-    case 32: return kv4_go<Kv4<T, D, NT, 32>>(prm, max_ctas, st);
-    case 64: return kv4_go<Kv4<T, D, NT, 64>>(prm, max_ctas, st);
-    default: return cudaErrorInvalidValue;
+    case 8: return kv4_go<Kv4<T, D, NT, 8, KVU>>(prm, max_ctas, st);
+    case 16: return kv4_go<Kv4<T, D, NT, 16, KVU>>(prm, max_ctas, st);
+    case 32: return kv4_go<Kv4<T, D, NT, 32, KVU>>(prm, max_ctas, st);
+    default: break;
   }
+  if constexpr (KVU == 1) {
+    if (BS == 64) return kv4_go<Kv4<T, D, NT, 64, KVU>>(prm, max_ctas, st);
+  }
+  return cudaErrorInvalidValue;
 }
 
+// nt: 8-row column tiles per unit; kvu: kv heads per unit.
 template <typename T, int D>
-static cudaError_t kv4_go_d(const KParams& prm, int BS, int nt, int max_ctas, cudaStream_t st) {
+static cudaError_t kv4_go_d(const KParams& prm, int BS, int nt, int kvu, int max_ctas, cudaStream_t st) {
   if constexpr (D <= 128) {
-    if (nt == 2) return kv4_go_bs<T, D, 2>(prm, BS, max_ctas, st);
+    if (nt == 2) return kv4_go_bs<T, D, 2, 1>(prm, BS, max_ctas, st);
+    if (kvu == 2) return kv4_go_bs<T, D, 1, 2>(prm, BS, max_ctas, st);
   }
-  return kv4_go_bs<T, D, 1>(prm, BS, max_ctas, st);
+  return kv4_go_bs<T, D, 1, 1>(prm, BS, max_ctas, st);
 }
 
 }  // namespace pa

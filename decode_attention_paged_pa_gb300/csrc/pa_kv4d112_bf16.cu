@@ -4,8 +4,8 @@
 
 namespace pa {
 
-cudaError_t launch_kv4_d112_bf16(const KParams& prm, int BS, int nt, int max_ctas, cudaStream_t st) {
-  return kv4_go_d<__nv_bfloat16, 112>(prm, BS, nt, max_ctas, st);
+cudaError_t launch_kv4_d112_bf16(const KParams& prm, int BS, int nt, int kvu, int max_ctas, cudaStream_t st) {
+  return kv4_go_d<__nv_bfloat16, 112>(prm, BS, nt, kvu, max_ctas, st);
 }
 
 }  // namespace pa

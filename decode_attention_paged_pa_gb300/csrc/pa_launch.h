@@ -71,20 +71,21 @@ cudaError_t launch_mma8_gb8_f16(const KParams& prm, int D, int max_ctas, cudaStr
 cudaError_t launch_mma8_gb8_bf16(const KParams& prm, int D, int max_ctas, cudaStream_t st);
 
 // Over a 4-bit cache (queries and output fp16 / bf16), by head size: blocks of
-// 8, 16, 32 or 64 tokens, units of nt * 8 query rows of a kv head (nt = 2: head
-// sizes up to 128).
-cudaError_t launch_kv4_d64_f16(const KParams& prm, int BS, int nt, int max_ctas, cudaStream_t st);
-cudaError_t launch_kv4_d64_bf16(const KParams& prm, int BS, int nt, int max_ctas, cudaStream_t st);
-cudaError_t launch_kv4_d80_f16(const KParams& prm, int BS, int nt, int max_ctas, cudaStream_t st);
-cudaError_t launch_kv4_d80_bf16(const KParams& prm, int BS, int nt, int max_ctas, cudaStream_t st);
-cudaError_t launch_kv4_d96_f16(const KParams& prm, int BS, int nt, int max_ctas, cudaStream_t st);
-cudaError_t launch_kv4_d96_bf16(const KParams& prm, int BS, int nt, int max_ctas, cudaStream_t st);
-cudaError_t launch_kv4_d112_f16(const KParams& prm, int BS, int nt, int max_ctas, cudaStream_t st);
-cudaError_t launch_kv4_d112_bf16(const KParams& prm, int BS, int nt, int max_ctas, cudaStream_t st);
-cudaError_t launch_kv4_d128_f16(const KParams& prm, int BS, int nt, int max_ctas, cudaStream_t st);
-cudaError_t launch_kv4_d128_bf16(const KParams& prm, int BS, int nt, int max_ctas, cudaStream_t st);
-cudaError_t launch_kv4_d256_f16(const KParams& prm, int BS, int nt, int max_ctas, cudaStream_t st);
-cudaError_t launch_kv4_d256_bf16(const KParams& prm, int BS, int nt, int max_ctas, cudaStream_t st);
+// 8, 16, 32 or 64 tokens, units of nt * 8 query rows of a kv head, or (kvu = 2, up
+// to four rows each) of two kv heads; either 2: head sizes up to 128, and kvu = 2:
+// blocks of up to 32 tokens.
+cudaError_t launch_kv4_d64_f16(const KParams& prm, int BS, int nt, int kvu, int max_ctas, cudaStream_t st);
+cudaError_t launch_kv4_d64_bf16(const KParams& prm, int BS, int nt, int kvu, int max_ctas, cudaStream_t st);
+cudaError_t launch_kv4_d80_f16(const KParams& prm, int BS, int nt, int kvu, int max_ctas, cudaStream_t st);
+cudaError_t launch_kv4_d80_bf16(const KParams& prm, int BS, int nt, int kvu, int max_ctas, cudaStream_t st);
+cudaError_t launch_kv4_d96_f16(const KParams& prm, int BS, int nt, int kvu, int max_ctas, cudaStream_t st);
+cudaError_t launch_kv4_d96_bf16(const KParams& prm, int BS, int nt, int kvu, int max_ctas, cudaStream_t st);
+cudaError_t launch_kv4_d112_f16(const KParams& prm, int BS, int nt, int kvu, int max_ctas, cudaStream_t st);
+cudaError_t launch_kv4_d112_bf16(const KParams& prm, int BS, int nt, int kvu, int max_ctas, cudaStream_t st);
+cudaError_t launch_kv4_d128_f16(const KParams& prm, int BS, int nt, int kvu, int max_ctas, cudaStream_t st);
+cudaError_t launch_kv4_d128_bf16(const KParams& prm, int BS, int nt, int kvu, int max_ctas, cudaStream_t st);
+cudaError_t launch_kv4_d256_f16(const KParams& prm, int BS, int nt, int kvu, int max_ctas, cudaStream_t st);
+cudaError_t launch_kv4_d256_bf16(const KParams& prm, int BS, int nt, int kvu, int max_ctas, cudaStream_t st);
 // Phase 2: the cross-partition combine of every multi-partition row, launched
 // as a programmatic dependent of the phase-1 launch before it on `st`.
 cudaError_t launch_combine(const CParams& prm, int elem_bytes, bool bf16, int D, cudaStream_t st);
