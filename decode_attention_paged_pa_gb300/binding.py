@@ -410,9 +410,9 @@ def kv4_block_bytes(head_size: int, block_size: int) -> int:
     return int(lib().pa_kv4_block_bytes(int(head_size), int(block_size)))
 
 
-def _kv4_shape(kv_cache, D):
+def _kv4_shape(kv_cache, D, device):
     """(num_blocks, KH, block_size) of a 4-bit cache for head size D."""
-    _check_tensor("kv_cache", kv_cache, torch.uint8, 3)
+    _need("kv_cache", kv_cache, torch.uint8, 3, device)
     NB, KH, rec = kv_cache.shape
     if rec % (D + 8) != 0 or rec == 0:
         raise ValueError("kv_cache must be [num_blocks, KH, block_size * (head_size + 8)]")
@@ -420,36 +420,33 @@ def _kv4_shape(kv_cache, D):
 
 
 def _decode_kv4(name, out, query, kv_cache, block_tables, seq_lens, scale, partition_size, workspace, stream, lse):
-    rows = query.shape[:-1]  # [S, H] or [S, q_len, H]
+    ndim = query.dim()  # [S, H, D] or [S, q_len, H, D]
     dt = query.dtype
     if dt not in _DTYPE_CODE:
         raise TypeError("query must be float16 or bfloat16")
-    _check_tensor("out", out, dt, query.dim())
-    _check_tensor("block_tables", block_tables, torch.int32, 2)
-    _check_tensor("seq_lens", seq_lens, torch.int32, 1)
-    S, H, D = query.shape[0], query.shape[-2], query.shape[-1]
-    QL = query.shape[1] if query.dim() == 4 else 1
-    NB, KH, BS = _kv4_shape(kv_cache, D)
-    if out.shape != query.shape:
+    dev = query.get_device()
+    _need("out", out, dt, ndim, dev)
+    _need("block_tables", block_tables, torch.int32, 2, dev)
+    _need("seq_lens", seq_lens, torch.int32, 1, dev)
+    shape = query.shape
+    S, H, D = shape[0], shape[-2], shape[-1]
+    QL = shape[1] if ndim == 4 else 1
+    NB, KH, BS = _kv4_shape(kv_cache, D, dev)
+    if out.shape != shape:
         raise ValueError("out must have query's shape")
-    if block_tables.shape[0] != S or seq_lens.shape[0] != S:
+    rows, MB = block_tables.shape
+    if rows != S or seq_lens.shape[0] != S:
         raise ValueError("block_tables / seq_lens must have num_seqs rows")
     if lse is not None:
-        _check_tensor("lse", lse, torch.float32, query.dim() - 1)
-        if lse.shape != rows:
+        _need("lse", lse, torch.float32, ndim - 1, dev)
+        if lse.shape != shape[:-1]:
             raise ValueError("lse must be query's shape without the head size")
-    MB = block_tables.shape[1]
-    if workspace is None:  # (a caller's workspace is checked by the library: PA_ERR_WORKSPACE)
-        workspace = torch.empty(max(workspace_bytes(S * QL, H, KH, D, MB, BS, partition_size), 256),
-                                dtype=torch.uint8, device=query.device)
-    _check_tensor("workspace", workspace, torch.uint8)
-    _same_device(query, out=out, kv_cache=kv_cache, block_tables=block_tables, seq_lens=seq_lens,
-                 workspace=workspace, lse=lse)
-    with _current(query):
+    workspace = _need_workspace(workspace, dev, lambda: workspace_bytes(S * QL, H, KH, D, MB, BS, partition_size))
+    with _current(dev):
         st = lib().pa_decode_v2_mq_kv4(
-            _ptr(out), _ptr(lse), _ptr(query), _ptr(kv_cache), _ptr(block_tables), _ptr(seq_lens), float(scale),
-            S, QL, H, KH, D, BS, int(partition_size), _DTYPE_CODE[dt], _stream_handle(stream, query), MB, NB,
-            _ptr(workspace), workspace.numel())
+            out.data_ptr(), _ptr(lse), query.data_ptr(), kv_cache.data_ptr(), block_tables.data_ptr(),
+            seq_lens.data_ptr(), float(scale), S, QL, H, KH, D, BS, int(partition_size), _DTYPE_CODE[dt],
+            _stream_handle(stream, query), MB, NB, workspace.data_ptr(), workspace.numel())
     if st != PA_OK:
         raise PaError(st, name)
     return workspace
@@ -478,21 +475,37 @@ def pa_decode_v2_mq_kv4(out, query, kv_cache, block_tables, seq_lens, scale: flo
 
 
 _no_switch = contextlib.nullcontext()
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
-def _current(like: torch.Tensor):
-    """A context in which ``like``'s device is the current one (nothing to do,
-    and nothing paid for a switch, where it is already)."""
-    return _no_switch if like.get_device() == torch.cuda.current_device() else torch.cuda.device(like.device)
+def _current(device: int):
+    """A context in which CUDA device ``device`` is the current one (nothing to
+    do, and nothing paid for a switch, where it is already)."""
+    return _no_switch if device == _current_device() else torch.cuda.device(device)
 
 
-def _same_device(like, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != like.device:
-            raise ValueError(f"{name} must be on {like.device}, got {t.device}")
+def _need(name, t, dtype, ndim, device):
+    """The checks of :func:`_check_tensor`, and the device: one expression where
+    they hold (these calls are made every step)."""
+    if (t.__class__ is torch.Tensor and t.dtype is dtype and t.dim() == ndim and t.get_device() == device
+            and t.is_contiguous()):
+        return
+    _check_tensor(name, t, dtype, ndim)
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be on cuda:{device}, got {t.device}")
 
 
-def _token_rows(name, t, kv_cache):
+def _need_workspace(workspace, device, nbytes):
+    """The caller's workspace, checked (its size by the library), or a new one."""
+    if workspace is None:
+        return torch.empty(max(nbytes(), 256), dtype=torch.uint8, device=torch.device("cuda", device))
+    _check_tensor("workspace", workspace, torch.uint8)
+    if workspace.get_device() != device:
+        raise ValueError(f"workspace must be on cuda:{device}, got {workspace.device}")
+    return workspace
+
+
+def _token_rows(name, t, device):
     """(rows, KH, D, row stride) of [N, KH, D] or [S, q_len, KH, D] rows: the
     heads of a token are contiguous, tokens a constant stride apart."""
     if not isinstance(t, torch.Tensor):
@@ -501,48 +514,50 @@ def _token_rows(name, t, kv_cache):
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype not in _DTYPE_CODE:
         raise TypeError(f"{name} must be float16 or bfloat16")
-    if t.dim() == 4:
-        if t.shape[1] != 1 and t.shape[0] != 1 and t.stride(0) != t.shape[1] * t.stride(1):
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be on cuda:{device}, got {t.device}")
+    shape, strides = t.shape, t.stride()
+    if len(shape) == 4:
+        if shape[1] != 1 and shape[0] != 1 and strides[0] != shape[1] * strides[1]:
             raise ValueError(f"{name}: tokens must be a constant stride apart")
-        N, stride = t.shape[0] * t.shape[1], t.stride(1) if t.shape[1] != 1 else t.stride(0)
-    elif t.dim() == 3:
-        N, stride = t.shape[0], t.stride(0)
+        N, stride = shape[0] * shape[1], strides[1] if shape[1] != 1 else strides[0]
+    elif len(shape) == 3:
+        N, stride = shape[0], strides[0]
     else:
-        raise ValueError(f"{name} must have 3 or 4 dims, got shape {tuple(t.shape)}")
-    KH, D = t.shape[-2], t.shape[-1]
-    if (D != 1 and t.stride(-1) != 1) or (KH != 1 and t.stride(-2) != D):
+        raise ValueError(f"{name} must have 3 or 4 dims, got shape {tuple(shape)}")
+    KH, D = shape[-2], shape[-1]
+    if (D != 1 and strides[-1] != 1) or (KH != 1 and strides[-2] != D):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
     return N, KH, D, (stride if N > 1 else KH * D)
 
 
 def _kv4_tokens(name, fn, first, kv_cache, key, value, block_tables, seq_lens, cu_tokens, workspace, stream):
-    N, KH, D, ks = _token_rows("key", key, kv_cache)
-    Nv, KHv, Dv, vs = _token_rows("value", value, kv_cache)
-    if (N, KH, D) != (Nv, KHv, Dv) or key.dtype != value.dtype:
+    dev = kv_cache.get_device() if isinstance(kv_cache, torch.Tensor) else -1
+    N, KH, D, ks = _token_rows("key", key, dev)
+    Nv, KHv, Dv, vs = _token_rows("value", value, dev)
+    if N != Nv or KH != KHv or D != Dv or key.dtype is not value.dtype:
         raise ValueError("key and value must have the same shape and dtype")
-    NB, KHc, BS = _kv4_shape(kv_cache, D)
+    NB, KHc, BS = _kv4_shape(kv_cache, D, dev)
     if KHc != KH:
         raise ValueError("key / value and kv_cache must have the same kv heads")
-    _check_tensor("block_tables", block_tables, torch.int32, 2)
-    _check_tensor("seq_lens", seq_lens, torch.int32, 1)
+    _need("block_tables", block_tables, torch.int32, 2, dev)
+    _need("seq_lens", seq_lens, torch.int32, 1, dev)
     S, MB = block_tables.shape
     if seq_lens.shape[0] != S:
         raise ValueError("block_tables / seq_lens must have num_seqs rows")
+    cu = None
     if cu_tokens is not None:
-        _check_tensor("cu_tokens", cu_tokens, torch.int32, 1)
+        _need("cu_tokens", cu_tokens, torch.int32, 1, dev)
         if cu_tokens.shape[0] != S + 1:
             raise ValueError("cu_tokens must have num_seqs + 1 entries")
-    if workspace is None:
-        workspace = torch.empty(256, dtype=torch.uint8, device=kv_cache.device)
-    _check_tensor("workspace", workspace, torch.uint8)
-    _same_device(kv_cache, key=key, value=value, block_tables=block_tables, seq_lens=seq_lens, cu_tokens=cu_tokens,
-                 workspace=workspace)
-    args = [_ptr(kv_cache), _ptr(key), _ptr(value)]
-    if not first:
-        args = args[1:] + args[:1]
-    with _current(kv_cache):
-        st = fn(*args, _ptr(block_tables), _ptr(seq_lens), _ptr(cu_tokens), S, N, KH, D, BS, ks, vs,
-                _DTYPE_CODE[key.dtype], _stream_handle(stream, kv_cache), MB, NB, _ptr(workspace), workspace.numel())
+        cu = cu_tokens.data_ptr()
+    workspace = _need_workspace(workspace, dev, lambda: 256)
+    c, k, v = kv_cache.data_ptr(), key.data_ptr(), value.data_ptr()
+    args = (c, k, v) if first else (k, v, c)
+    with _current(dev):
+        st = fn(*args, block_tables.data_ptr(), seq_lens.data_ptr(), cu, S, N, KH, D, BS, ks, vs,
+                _DTYPE_CODE[key.dtype], _stream_handle(stream, kv_cache), MB, NB, workspace.data_ptr(),
+                workspace.numel())
     if st != PA_OK:
         raise PaError(st, name)
     return workspace
@@ -573,29 +588,25 @@ def pages_workspace_bytes(num_rows: int, max_blocks_per_seq: int, num_blocks: in
     return int(lib().pa_pages_workspace_bytes(int(num_rows), int(max_blocks_per_seq), int(num_blocks)))
 
 
-def _pages_args(refcounts, caches, rows, MB, workspace, **tensors):
+def _pages_args(refcounts, caches, rows, MB, workspace):
     """(caches array, page bytes array, count, workspace) after the checks all pages calls share."""
-    _check_tensor("refcounts", refcounts, torch.int32, 1)
-    NB = refcounts.shape[0]
+    NB, dev = refcounts.shape[0], refcounts.get_device()
     if NB == 0:
         raise ValueError("refcounts must have num_blocks >= 1 entries")
-    caches = [caches] if isinstance(caches, torch.Tensor) else list(caches)
-    n = len(caches)
-    ptrs, sizes = (ctypes.c_void_p * max(n, 1))(), (ctypes.c_size_t * max(n, 1))()
-    for i, c in enumerate(caches):
-        _check_tensor("cache", c)
+    caches = (caches,) if isinstance(caches, torch.Tensor) else caches
+    ptrs, sizes = [], []
+    for c in caches:
+        if not (c.__class__ is torch.Tensor and c.get_device() == dev and c.is_contiguous()):
+            _check_tensor("cache", c)
+            if c.get_device() != dev:
+                raise ValueError(f"every cache must be on {refcounts.device}, got {c.device}")
         if c.dim() < 1 or c.shape[0] != NB:
             raise ValueError("every cache's first dimension must be the pool's num_blocks (refcounts' length)")
-        if c.device != refcounts.device:
-            raise ValueError(f"every cache must be on {refcounts.device}, got {c.device}")
-        ptrs[i] = c.data_ptr()
-        sizes[i] = c.numel() * c.element_size() // NB
-    if workspace is None:
-        workspace = torch.empty(max(pages_workspace_bytes(rows, MB, NB), 256), dtype=torch.uint8,
-                                device=refcounts.device)
-    _check_tensor("workspace", workspace, torch.uint8)
-    _same_device(refcounts, workspace=workspace, **tensors)
-    return ptrs, sizes, n, workspace
+        ptrs.append(c.data_ptr())
+        sizes.append(c.numel() * c.element_size() // NB)
+    n = len(ptrs)
+    ptrs, sizes = (ctypes.c_void_p * max(n, 1))(*ptrs), (ctypes.c_size_t * max(n, 1))(*sizes)
+    return ptrs, sizes, n, _need_workspace(workspace, dev, lambda: pages_workspace_bytes(rows, MB, NB))
 
 
 def pa_pages_fork(block_tables_out, seq_lens_out, block_tables, seq_lens, parents, refcounts, caches,
@@ -606,18 +617,18 @@ def pa_pages_fork(block_tables_out, seq_lens_out, block_tables, seq_lens, parent
     parents int32 [n] (-1: an empty row); refcounts int32 [num_blocks] updated;
     ``caches`` the tensors [num_blocks, ...] whose pages follow the tables.
     Returns the workspace used (its status: :func:`device_status`)."""
-    _check_tensor("block_tables_out", block_tables_out, torch.int32, 2)
-    _check_tensor("seq_lens_out", seq_lens_out, torch.int32, 1)
-    _check_tensor("block_tables", block_tables, torch.int32, 2)
-    _check_tensor("seq_lens", seq_lens, torch.int32, 1)
-    _check_tensor("parents", parents, torch.int32, 1)
+    _check_tensor("refcounts", refcounts, torch.int32, 1)
+    dev = refcounts.get_device()
+    _need("block_tables_out", block_tables_out, torch.int32, 2, dev)
+    _need("seq_lens_out", seq_lens_out, torch.int32, 1, dev)
+    _need("block_tables", block_tables, torch.int32, 2, dev)
+    _need("seq_lens", seq_lens, torch.int32, 1, dev)
+    _need("parents", parents, torch.int32, 1, dev)
     (S, MB), n = block_tables.shape, parents.shape[0]
     if tuple(block_tables_out.shape) != (n, MB) or seq_lens_out.shape[0] != n or seq_lens.shape[0] != S:
         raise ValueError("inconsistent table / length / parents shapes")
-    ptrs, sizes, nc, workspace = _pages_args(
-        refcounts, caches, n, MB, workspace, block_tables_out=block_tables_out, seq_lens_out=seq_lens_out,
-        block_tables=block_tables, seq_lens=seq_lens, parents=parents)
-    with _current(refcounts):
+    ptrs, sizes, nc, workspace = _pages_args(refcounts, caches, n, MB, workspace)
+    with _current(dev):
         st = lib().pa_pages_fork(
             _ptr(block_tables_out), _ptr(seq_lens_out), _ptr(block_tables), _ptr(seq_lens), _ptr(parents),
             _ptr(refcounts), ptrs, sizes, nc, S, n, MB, int(block_size), refcounts.shape[0],
@@ -633,15 +644,16 @@ def pa_pages_resize(block_tables, seq_lens, new_lens, refcounts, caches, block_s
     include/pa_decode.h): block_tables int32 [S, MB], seq_lens int32 [S] and
     refcounts int32 [num_blocks] updated in place; new_lens int32 [S].
     Returns the workspace used."""
-    _check_tensor("block_tables", block_tables, torch.int32, 2)
-    _check_tensor("seq_lens", seq_lens, torch.int32, 1)
-    _check_tensor("new_lens", new_lens, torch.int32, 1)
+    _check_tensor("refcounts", refcounts, torch.int32, 1)
+    dev = refcounts.get_device()
+    _need("block_tables", block_tables, torch.int32, 2, dev)
+    _need("seq_lens", seq_lens, torch.int32, 1, dev)
+    _need("new_lens", new_lens, torch.int32, 1, dev)
     S, MB = block_tables.shape
     if seq_lens.shape[0] != S or new_lens.shape[0] != S:
         raise ValueError("block_tables / seq_lens / new_lens must have num_seqs rows")
-    ptrs, sizes, nc, workspace = _pages_args(refcounts, caches, S, MB, workspace, block_tables=block_tables,
-                                             seq_lens=seq_lens, new_lens=new_lens)
-    with _current(refcounts):
+    ptrs, sizes, nc, workspace = _pages_args(refcounts, caches, S, MB, workspace)
+    with _current(dev):
         st = lib().pa_pages_resize(
             _ptr(block_tables), _ptr(seq_lens), _ptr(new_lens), _ptr(refcounts), ptrs, sizes, nc, S, MB,
             int(block_size), refcounts.shape[0], _stream_handle(stream, refcounts), _ptr(workspace),
@@ -658,18 +670,19 @@ def pa_pages_compact(block_tables, seq_lens, refcounts, caches, block_size: int,
     [num_blocks] updated in place, pages moved in every cache; ``new_ids``
     (int32 [num_blocks], optional) receives each block's new id.  Returns the
     workspace used."""
-    _check_tensor("block_tables", block_tables, torch.int32, 2)
-    _check_tensor("seq_lens", seq_lens, torch.int32, 1)
+    _check_tensor("refcounts", refcounts, torch.int32, 1)
+    dev = refcounts.get_device()
+    _need("block_tables", block_tables, torch.int32, 2, dev)
+    _need("seq_lens", seq_lens, torch.int32, 1, dev)
     S, MB = block_tables.shape
     if seq_lens.shape[0] != S:
         raise ValueError("block_tables / seq_lens must have num_seqs rows")
     if new_ids is not None:
-        _check_tensor("new_ids", new_ids, torch.int32, 1)
+        _need("new_ids", new_ids, torch.int32, 1, dev)
         if new_ids.shape != refcounts.shape:
             raise ValueError("new_ids must have num_blocks entries")
-    ptrs, sizes, nc, workspace = _pages_args(refcounts, caches, S, MB, workspace, block_tables=block_tables,
-                                             seq_lens=seq_lens, new_ids=new_ids)
-    with _current(refcounts):
+    ptrs, sizes, nc, workspace = _pages_args(refcounts, caches, S, MB, workspace)
+    with _current(dev):
         st = lib().pa_pages_compact(
             _ptr(block_tables), _ptr(seq_lens), _ptr(refcounts), _ptr(new_ids), ptrs, sizes, nc, S, MB,
             int(block_size), refcounts.shape[0], _stream_handle(stream, refcounts), _ptr(workspace),

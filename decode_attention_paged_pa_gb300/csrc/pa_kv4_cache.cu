@@ -4,14 +4,23 @@
 //
 // One vector is one token's key or value of one kv head: D elements of T next
 // to each other in the token rows, D/2 bytes of codes and two parameters in
-// the cache.  D/8 lanes (a power of two of them, the last ones idle at head
-// sizes 80, 96 and 112) take a vector with one 16-byte access each on the row
-// side and one 4-byte access on the cache side.  A CTA takes a run of
-// consecutive tokens; its warps first find each token's sequence (a 32-way
-// search of the row offsets), block and slot.
+// the cache.  D/16 lanes (of a power of two, the last ones idle at head sizes
+// 80, 96 and 112) take a vector with two 16-byte accesses each on the row side
+// and one 8-byte access on the cache side, a few vectors at a time so that
+// enough loads are in flight.  A CTA takes a run of consecutive tokens; its
+// first warp finds each token's sequence (a 32-way search of the row offsets
+// for the first, steps from there for the others), block and slot, while the
+// others' rows are on their way.
 //
 // Both kernels are bound by memory: 2 D bytes on the row side and D/2 + 4 on
-// the cache side per vector, each touched once.
+// the cache side per vector, each touched once.  A first form with eight
+// elements a lane, fp32 minima and a division per element was bound by issue
+// (80% of the slots); so minima and maxima are taken on packed pairs (they are
+// exact in T), the lowest and the negated highest in one word through the
+// shuffles; the quotient (x - zero) / scale by a reciprocal, and only where it
+// lies so close to a tie that the reciprocal's error could decide, by the
+// division that defines the code; and read-back is one packed multiply-add per
+// pair (rounded once).
 #include <cstring>
 
 #include "pa_common.cuh"
@@ -23,8 +32,7 @@ namespace {
 
 struct Kv4Params {
   uint8_t* cache;
-  const void* in[2];   // key, value rows (append)
-  void* out[2];        // key, value rows (gather)
+  void* row[2];        // key, value rows (append: only read)
   const int32_t* bt;
   const int32_t* lens;
   const int32_t* cu;   // [S + 1], or null: every sequence has `per` tokens
@@ -34,8 +42,9 @@ struct Kv4Params {
   int tpc;             // tokens per CTA
 };
 
-constexpr int kThreads = 256;
+constexpr int kWorkers = 128, kThreads = kWorkers + 32;
 constexpr int kMaxTokens = 16;  // per CTA
+constexpr int kBatch = 2;       // vectors a lane group has in flight
 
 // New (or wanted) tokens of sequence s: rows [first, first + n) of N.
 __device__ __forceinline__ void seq_rows(const Kv4Params& p, int s, int* first, int* n) {
@@ -48,32 +57,32 @@ __device__ __forceinline__ void seq_rows(const Kv4Params& p, int s, int* first, 
   }
 }
 
-// Warp: block (-1: skip the token) and slot of row t.
-__device__ __forceinline__ void place(const Kv4Params& p, int t, int lane, int* blk, int* slot) {
+// Warp: block (-1: skip the token) and slot of rows t0 + lane (lane < nt).
+__device__ __forceinline__ void place(const Kv4Params& p, int t0, int nt, int lane, int* blk, int* slot) {
+  *blk = -1;
+  *slot = 0;
+  const int t = t0 + lane;
   int s = -1;
   if (!p.cu) {
     s = t / p.per;
   } else {
-    // The last s in [0, S) with cu[s] <= t, 32 pivots a step.
+    // The last s in [0, S) with cu[s] <= t0, 32 pivots a step.
     int lo = 0, n = p.S;
     while (true) {
       const int step = (n + 31) / 32;
       const int i = lo + lane * step;
-      const bool le = lane * step < n && p.cu[i] <= t;
+      const bool le = lane * step < n && p.cu[i] <= t0;
       const unsigned m = __ballot_sync(0xffffffffu, le);
-      if (m == 0) break;  // t lies before the first row
-      const int k = 31 - __clz(m);
+      const int k = m ? 31 - __clz(m) : 0;  // (t0 before the first row: from sequence 0 on)
       lo += k * step;
       n = min(step, n - k * step);
-      if (step == 1) {
-        s = lo;
-        break;
-      }
+      if (step == 1) break;
     }
+    if (lane >= nt) return;
+    s = lo;
+    while (s + 1 < p.S && p.cu[s + 1] <= t) ++s;
   }
-  *blk = -1;
-  *slot = 0;
-  if (s < 0 || s >= p.S) return;
+  if (lane >= nt || s < 0 || s >= p.S) return;
   int first, n;
   seq_rows(p, s, &first, &n);
   const int i = t - first, L = p.lens[s];
@@ -109,102 +118,200 @@ __device__ __forceinline__ void write_status(const Kv4Params& p) {
 
 template <int D>
 constexpr int lanes_per_vector() {
-  return D <= 64 ? 8 : D <= 128 ? 16 : 32;
+  return D <= 64 ? 4 : D <= 128 ? 8 : 16;
 }
 
+// Packed pairs of T.
+template <typename T> struct Pair;
+template <> struct Pair<__half> {
+  using V = __half2;
+  static constexpr uint32_t kBase = 0x64006400u;  // 1024: a code in the low bits adds exactly
+  static constexpr uint32_t kSmallest = 0x0400u;  // smallest normal number
+  static constexpr uint32_t kInf = 0x7c007c00u;
+  __device__ __forceinline__ static V fma(V a, V b, V c) { return __hfma2(a, b, c); }
+};
+template <> struct Pair<__nv_bfloat16> {
+  using V = __nv_bfloat162;
+  static constexpr uint32_t kBase = 0x43004300u;  // 128
+  static constexpr uint32_t kSmallest = 0x0080u;
+  static constexpr uint32_t kInf = 0x7f807f80u;
+  __device__ __forceinline__ static V fma(V a, V b, V c) { return __hfma2(a, b, c); }
+};
+template <typename V>
+__device__ __forceinline__ V as_pair(uint32_t w) { return *reinterpret_cast<V*>(&w); }
+template <typename V>
+__device__ __forceinline__ uint32_t as_word(V v) { return *reinterpret_cast<uint32_t*>(&v); }
+
 // The codes of 8 elements (element e in bits 4e ..) of a vector of lowest
-// value lo and scale s (the scale that is stored: already rounded to T).
-__device__ __forceinline__ uint32_t quantise8(const float (&f)[8], float lo, float s) {
+// value lo and scale s (the scale that is stored: already rounded to T);
+// r: about 1 / s.  `fast`: s is a normal number of T.
+__device__ __forceinline__ uint32_t quantise8(const float (&f)[8], float lo, float s, float r, bool fast) {
+  // x + 1.5 * 2^23 holds the nearest integer to x (ties to even) in its low bits.
+  constexpr float kMagic = 12582912.f;
+  float far = 0.f;  // largest distance of a quotient from its integer
   uint32_t w = 0;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const int c = s > 0.f ? min(15, __float2int_rn(__fdiv_rn(f[e] - lo, s))) : 0;
-    w |= (uint32_t)c << (4 * e);
+  for (int e = 7; e >= 0; --e) {
+    const float t = (f[e] - lo) * r;
+    const float m = t + kMagic;
+    far = fmaxf(far, fabsf(t - (m - kMagic)));
+    w = w * 16u + __float_as_uint(m);
+  }
+  w -= 0x4b400000u * 0x11111111u;
+  // t is within 2^-17 of the quotient (the reciprocal and three roundings at a
+  // value below 16), and at most 15.1 as s is rounded to 8 bits or more: a
+  // distance that far from a half decides nothing else.
+  if (!fast || !(far < 0.5f - 1.f / 65536.f)) {
+    w = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int c = s > 0.f ? min(15, __float2int_rn(__fdiv_rn(f[e] - lo, s))) : 0;
+      w |= (uint32_t)c << (4 * e);
+    }
   }
   return w;
 }
 
 template <typename T, int D, bool GATHER>
-__global__ void __launch_bounds__(kThreads) kv4_tokens_kernel(const __grid_constant__ Kv4Params p) {
-  constexpr int LPV = lanes_per_vector<D>(), NG = kThreads / LPV;
+__global__ void __launch_bounds__(kThreads, 7) kv4_tokens_kernel(const __grid_constant__ Kv4Params p) {
+  using P = Pair<T>;
+  using V = typename P::V;
+  constexpr int LPV = lanes_per_vector<D>(), NG = kWorkers / LPV;
   constexpr int X = D < 128 ? D : 128, XB = X / 2;
   __shared__ int s_blk[kMaxTokens], s_slot[kMaxTokens];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31;
   const long long t0 = (long long)blockIdx.x * p.tpc;
   const int nt = (int)min((long long)p.tpc, (long long)p.N - t0);
-  for (int i = warp; i < nt; i += kThreads / 32) {
-    int blk, slot;
-    place(p, (int)t0 + i, lane, &blk, &slot);
-    if (lane == 0) {
-      s_blk[i] = blk;
-      s_slot[i] = slot;
+  if (threadIdx.x >= kWorkers) {
+    if (nt > 0) {
+      int blk, slot;
+      place(p, (int)t0, nt, lane, &blk, &slot);
+      if (lane < nt) {
+        s_blk[lane] = blk;
+        s_slot[lane] = slot;
+      }
+      named_barrier_sync(1, kThreads);
     }
-  }
-  __syncthreads();
-  const int grp = threadIdx.x / LPV, gl = threadIdx.x % LPV;
-  const bool act = gl < D / 8;
-  const int per_tok = 2 * p.KH, nv = nt * per_tok;
-  const size_t rec_bytes = (size_t)p.BS * (D + 8);
-  // The loop bounds are the warp's, not the group's: its shuffles take whole warps.
-  for (int v0 = 0; v0 < nv; v0 += NG) {
-    const int v = v0 + grp;
-    const bool on = v < nv;
-    const int i = on ? v / per_tok : 0, k = on ? v - i * per_tok : 0;
-    const int sel = k / p.KH, h = k - sel * p.KH;
-    const int blk = on ? s_blk[i] : -1, slot = s_slot[i];
-    const bool go = act && blk >= 0;
-    uint8_t* rec = p.cache + ((size_t)max(blk, 0) * p.KH + h) * rec_bytes;
-    uint32_t* code = reinterpret_cast<uint32_t*>(rec + (size_t)sel * p.BS * (D / 2) +
-                                                 (size_t)(gl / (X / 8)) * p.BS * XB + (size_t)slot * XB +
-                                                 (gl % (X / 8)) * 4);
-    uint32_t* par = reinterpret_cast<uint32_t*>(rec + (size_t)p.BS * D + (size_t)slot * 8 + sel * 4);
-    const size_t row = (size_t)(t0 + i) * (size_t)p.stride[sel] + (size_t)h * D + gl * 8;
-    if constexpr (GATHER) {
-      if (!go) continue;
-      const uint32_t w = *code;
-      const float2 sz = F16Traits<T>::to_float2(*par);
-      uint32_t o[4];
+  } else {
+    const int grp = threadIdx.x / LPV, gl = threadIdx.x % LPV;
+    const bool act = gl < D / 16;
+    const int per_tok = 2 * p.KH;
+    const uint32_t rec_bytes = (uint32_t)p.BS * (D + 8), half = (uint32_t)p.BS * (D / 2);
+    const uint32_t code_at = (uint32_t)(gl / (X / 16)) * p.BS * XB + (uint32_t)(gl % (X / 16)) * 8;
+    // This group's next vector: token i, and k = (key or value, head) within it.
+    int i = grp / per_tok, k = grp - i * per_tok;
+    bool placed = false;
+    // The loop bound is the CTA's, not the group's: shuffles take whole warps.
+    for (int v0 = 0; v0 < nt * per_tok; v0 += NG * kBatch) {
+      uint4 x[kBatch][2];
+      T* row[kBatch];
+      int vi[kBatch], vk[kBatch];
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        o[e] = F16Traits<T>::pack(fmaf((float)((w >> (8 * e)) & 15u), sz.x, sz.y),
-                                  fmaf((float)((w >> (8 * e + 4)) & 15u), sz.x, sz.y));
-      *reinterpret_cast<uint4*>(static_cast<T*>(p.out[sel]) + row) = make_uint4(o[0], o[1], o[2], o[3]);
-    } else {
-      float f[8];
-      float lo = INFINITY, hi = -INFINITY;
-      bool odd = false;  // a NaN or an infinity among the elements
+      for (int j = 0; j < kBatch; ++j) {
+        const int sel = k >= p.KH;
+        vi[j] = i;
+        vk[j] = k;
+        row[j] = static_cast<T*>(p.row[sel]) + (t0 + i) * p.stride[sel] + (k - sel * p.KH) * D + gl * 16;
+        if constexpr (!GATHER) {
+          x[j][0] = x[j][1] = make_uint4(0, 0, 0, 0);
+          if (act && i < nt) {
+            x[j][0] = reinterpret_cast<const uint4*>(row[j])[0];
+            x[j][1] = reinterpret_cast<const uint4*>(row[j])[1];
+          }
+        }
+        for (k += NG; k >= per_tok; k -= per_tok) ++i;
+      }
+      if (!placed) {
+        named_barrier_sync(1, kThreads);
+        placed = true;
+      }
+      // This lane's code words, and the vector's parameters.
+      uint8_t *code[kBatch], *par[kBatch];
+      bool go[kBatch];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = 0.f;
-      if (go) {
-        unpack_chunk<T>(*reinterpret_cast<const uint4*>(static_cast<const T*>(p.in[sel]) + row), f);
+      for (int j = 0; j < kBatch; ++j) {
+        const bool in = vi[j] < nt;
+        const int blk = in ? s_blk[vi[j]] : -1;
+        const uint32_t slot = in ? s_slot[vi[j]] : 0, sel = vk[j] >= p.KH;
+        uint8_t* rec = p.cache + ((size_t)max(blk, 0) * p.KH + (vk[j] - (int)sel * p.KH)) * rec_bytes;
+        code[j] = rec + (sel * half + slot * XB + code_at);
+        par[j] = rec + (2 * half + slot * 8 + sel * 4);
+        go[j] = act && blk >= 0;
+      }
+      if constexpr (GATHER) {
+        uint2 w[kBatch];
+        uint32_t sz[kBatch];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          lo = fminf(lo, f[e]);
-          hi = fmaxf(hi, f[e]);
-          odd |= !(fabsf(f[e]) < INFINITY);
+        for (int j = 0; j < kBatch; ++j) {
+          w[j] = go[j] ? *reinterpret_cast<const uint2*>(code[j]) : make_uint2(0, 0);
+          sz[j] = go[j] ? *reinterpret_cast<const uint32_t*>(par[j]) : 0u;
+        }
+        const V base = as_pair<V>(P::kBase);
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+          const V s = as_pair<V>(__byte_perm(sz[j], 0, 0x1010)), z = as_pair<V>(__byte_perm(sz[j], 0, 0x3232));
+          uint32_t o[8];
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            const uint32_t c = q ? w[j].y : w[j].x;
+            uint32_t v[4];  // elements e and e + 4
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              v[e] = as_word(P::fma(__hsub2(as_pair<V>(((c >> (4 * e)) & 0x000f000fu) | P::kBase), base), s, z));
+            o[4 * q] = __byte_perm(v[0], v[1], 0x5410);
+            o[4 * q + 1] = __byte_perm(v[2], v[3], 0x5410);
+            o[4 * q + 2] = __byte_perm(v[0], v[1], 0x7632);
+            o[4 * q + 3] = __byte_perm(v[2], v[3], 0x7632);
+          }
+          if (go[j]) {
+            reinterpret_cast<uint4*>(row[j])[0] = make_uint4(o[0], o[1], o[2], o[3]);
+            reinterpret_cast<uint4*>(row[j])[1] = make_uint4(o[4], o[5], o[6], o[7]);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+          // Lowest and highest, a NaN going through (idle lanes: no influence).
+          const uint32_t e[8] = {x[j][0].x, x[j][0].y, x[j][0].z, x[j][0].w, x[j][1].x, x[j][1].y, x[j][1].z, x[j][1].w};
+          V lo = as_pair<V>(e[0]), hi = lo;
+#pragma unroll
+          for (int q = 1; q < 8; ++q) {
+            lo = __hmin2_nan(lo, as_pair<V>(e[q]));
+            hi = __hmax2_nan(hi, as_pair<V>(e[q]));
+          }
+          // (low, -high) in one word.
+          const uint32_t nh = as_word(hi) ^ 0x80008000u;
+          V m = __hmin2_nan(as_pair<V>(__byte_perm(as_word(lo), nh, 0x5410)), as_pair<V>(__byte_perm(as_word(lo), nh, 0x7632)));
+          if (!act) m = as_pair<V>(P::kInf);
+#pragma unroll
+          for (int o = 1; o < LPV; o <<= 1) m = __hmin2_nan(m, as_pair<V>(__shfl_xor_sync(0xffffffffu, as_word(m), o)));
+          if (!go[j]) continue;
+          const float2 mf = F16Traits<T>::to_float2(as_word(m));
+          // scale = (hi - lo) / 15, rounded to T, which the codes are taken
+          // against; zero = lo, an element and so exact in T (a zero of either
+          // sign is stored as +0).
+          const float low = mf.x + 0.f, spread = -mf.y - low;
+          uint32_t sz = F16Traits<T>::pack(__fdiv_rn(spread, 15.f), low);
+          uint2 w = make_uint2(0, 0);
+          if (!(spread < INFINITY)) {
+            sz = 0x7fff7fffu;  // NaN in fp16 and in bf16
+          } else {
+            const float s = F16Traits<T>::to_float2(sz).x;
+            float r;
+            asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+            const bool fast = (sz & 0xffffu) >= P::kSmallest;
+            float f[8];
+            unpack_chunk<T>(x[j][0], f);
+            w.x = quantise8(f, low, s, r, fast);
+            unpack_chunk<T>(x[j][1], f);
+            w.y = quantise8(f, low, s, r, fast);
+          }
+          *reinterpret_cast<uint2*>(code[j]) = w;
+          if (gl == 0) *reinterpret_cast<uint32_t*>(par[j]) = sz;
         }
       }
-#pragma unroll
-      for (int o = 1; o < LPV; o <<= 1) {
-        lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-        hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-      }
-      const unsigned odds = __ballot_sync(0xffffffffu, odd);
-      const unsigned mine = (LPV == 32 ? 0xffffffffu : ((1u << LPV) - 1u) << (lane / LPV * LPV));
-      if (!go) continue;
-      // scale = (hi - lo) / 15, rounded to T, which the codes are taken
-      // against; zero = lo, an element and so exact in T (a zero of either
-      // sign is stored as +0).
-      lo += 0.f;
-      const float spread = hi - lo;
-      const bool poison = (odds & mine) || !(spread < INFINITY);
-      uint32_t sz = F16Traits<T>::pack(__fdiv_rn(spread, 15.f), lo), w = 0;
-      if (poison) sz = 0x7fff7fffu;  // NaN in fp16 and in bf16
-      else w = quantise8(f, lo, F16Traits<T>::to_float2(sz).x);
-      *code = w;
-      if (gl == 0) *par = sz;
     }
   }
   if (blockIdx.x == 0) write_status(p);
@@ -212,12 +319,12 @@ __global__ void __launch_bounds__(kThreads) kv4_tokens_kernel(const __grid_const
 
 template <typename T, bool GATHER>
 cudaError_t launch_tokens(const Kv4Params& p, int D, cudaStream_t st) {
-  // Tokens per CTA: one while the call is too small to give every SM four
+  // Tokens per CTA: one while the call is too small to give every SM eight
   // CTAs, then as many as still do, up to kMaxTokens.
-  const int want = device_sm_count() * 4;
+  const int want = device_sm_count() * 8;
   Kv4Params q = p;
   q.tpc = p.N / want < 1 ? 1 : p.N / want > kMaxTokens ? kMaxTokens : p.N / want;
-  const int grid = p.N == 0 ? 1 : (p.N + q.tpc - 1) / q.tpc;
+  const int grid = p.N == 0 ? 1 : (int)(((long long)p.N + q.tpc - 1) / q.tpc);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid, 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
@@ -267,8 +374,8 @@ int tokens_impl(bool gather, void* kv_cache, void* key, void* value, const int32
   Kv4Params p;
   std::memset(&p, 0, sizeof p);
   p.cache = static_cast<uint8_t*>(kv_cache);
-  p.in[0] = p.out[0] = key;
-  p.in[1] = p.out[1] = value;
+  p.row[0] = key;
+  p.row[1] = value;
   p.bt = block_tables;
   p.lens = seq_lens;
   p.cu = num_seqs > 0 ? cu_tokens : nullptr;

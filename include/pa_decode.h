@@ -334,7 +334,7 @@ int pa_decode_v2_mq_kv4(void* out, float* lse, const void* query, const void* kv
  *                least num_kv_heads * head_size), 16-byte aligned
  *   cu_tokens    DEVICE [num_seqs + 1] int32, ascending from 0; NULL: every
  *                sequence has num_tokens / num_seqs rows.  Rows at or behind
- *                cu_tokens[num_seqs] are not read.
+ *                cu_tokens[num_seqs] count for nothing.
  *   workspace    >= 256 bytes, 16-byte aligned, required; holds the status
  *                (pa_decode_v2_device_status), whatever it held before
  * A position of several sequences (a shared block) must not be written by two
@@ -351,8 +351,8 @@ int pa_kv4_append(void* kv_cache, const void* key, const void* value, const int3
 
 /*
  * The reverse: the last cu_tokens[s+1] - cu_tokens[s] cached tokens of each
- * sequence as rows of the dtype, each value scale * code + zero in fp32 rounded
- * once (for prefill attention over earlier context, or to leave the format).
+ * sequence as rows of the dtype, each value scale * code + zero rounded once
+ * (for prefill attention over earlier context, or to leave the format).
  * Arguments as for pa_kv4_append; rows that belong to no sequence, or whose
  * length or block id is refused, keep what they held.
  */

@@ -1,7 +1,8 @@
 """Tokens written into a 4-bit cache and read back (pa_kv4_append,
-pa_kv4_gather), bit for bit against the definition in 64 bits (every step of it
-is an fp32 operation or a rounding to T, and the quotients' 64-bit values round
-to fp32 as the fp32 division does)."""
+pa_kv4_gather).  What is stored is compared bit for bit with the definition in
+64 bits (every step of it is an fp32 operation or a rounding to T, and the
+quotients' 64-bit values round to fp32 as the fp32 division does); what is read
+back has to be the nearest value of the type."""
 import pytest
 import torch
 
@@ -56,6 +57,14 @@ def rows(g, N, KH, D, dtype):
     return x.to(dtype)
 
 
+def nearest(got, ref):
+    """Every value is the nearest of its type to scale * code + zero (rounded once)."""
+    err = (got.double() - ref).abs()
+    for step in (1, -1):  # the neighbouring patterns
+        near = (got.view(torch.int16) + step).view(got.dtype).double()
+        assert bool((err <= (near - ref).abs())[near.isfinite()].all())
+
+
 @pytest.mark.parametrize("dtype", [F16, BF16], ids=["fp16", "bf16"])
 @pytest.mark.parametrize("BS", [8, 16, 32, 64])
 @pytest.mark.parametrize("D", [64, 80, 96, 112, 128, 256])
@@ -79,8 +88,7 @@ def test_append_and_gather(D, BS, dtype):
     at = [(s, int(L[s]) - m + i) for s, m in enumerate(new) for i in range(m)]
     for got, ref in ((ko, K), (vo, V)):
         w = torch.stack([ref[int(bt[s, p // BS]), :, p % BS] for s, p in at])
-        # scale * code + zero: one fp32 rounding, then the rounding to T
-        assert torch.equal(got[: len(at)].cpu(), w.float().to(dtype))
+        nearest(got[: len(at)].cpu(), w)
         assert bool((got[len(at):] == 7).all())  # rows behind the last sequence
 
 
