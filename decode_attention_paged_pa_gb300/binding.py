@@ -9,6 +9,7 @@ if that is impossible the call fails.
 """
 from __future__ import annotations
 
+import array
 import contextlib
 import ctypes
 import os
@@ -589,7 +590,7 @@ def pages_workspace_bytes(num_rows: int, max_blocks_per_seq: int, num_blocks: in
 
 
 def _pages_args(refcounts, caches, rows, MB, workspace):
-    """(caches array, page bytes array, count, workspace) after the checks all pages calls share."""
+    """(cache pointers, page bytes, count, workspace) after the checks all pages calls share."""
     NB, dev = refcounts.shape[0], refcounts.get_device()
     if NB == 0:
         raise ValueError("refcounts must have num_blocks >= 1 entries")
@@ -604,9 +605,9 @@ def _pages_args(refcounts, caches, rows, MB, workspace):
             raise ValueError("every cache's first dimension must be the pool's num_blocks (refcounts' length)")
         ptrs.append(c.data_ptr())
         sizes.append(c.numel() * c.element_size() // NB)
-    n = len(ptrs)
-    ptrs, sizes = (ctypes.c_void_p * max(n, 1))(*ptrs), (ctypes.c_size_t * max(n, 1))(*sizes)
-    return ptrs, sizes, n, _need_workspace(workspace, dev, lambda: pages_workspace_bytes(rows, MB, NB))
+    # (Arrays of 64-bit words, passed by address: a third of ctypes arrays' cost.)
+    workspace = _need_workspace(workspace, dev, lambda: pages_workspace_bytes(rows, MB, NB))
+    return array.array("Q", ptrs), array.array("Q", sizes), len(ptrs), workspace
 
 
 def pa_pages_fork(block_tables_out, seq_lens_out, block_tables, seq_lens, parents, refcounts, caches,
@@ -631,8 +632,8 @@ def pa_pages_fork(block_tables_out, seq_lens_out, block_tables, seq_lens, parent
     with _current(dev):
         st = lib().pa_pages_fork(
             _ptr(block_tables_out), _ptr(seq_lens_out), _ptr(block_tables), _ptr(seq_lens), _ptr(parents),
-            _ptr(refcounts), ptrs, sizes, nc, S, n, MB, int(block_size), refcounts.shape[0],
-            _stream_handle(stream, refcounts), _ptr(workspace), workspace.numel())
+            _ptr(refcounts), ptrs.buffer_info()[0], sizes.buffer_info()[0], nc, S, n, MB, int(block_size),
+            refcounts.shape[0], _stream_handle(stream, refcounts), _ptr(workspace), workspace.numel())
     if st != PA_OK:
         raise PaError(st, "pa_pages_fork")
     return workspace
@@ -655,9 +656,9 @@ def pa_pages_resize(block_tables, seq_lens, new_lens, refcounts, caches, block_s
     ptrs, sizes, nc, workspace = _pages_args(refcounts, caches, S, MB, workspace)
     with _current(dev):
         st = lib().pa_pages_resize(
-            _ptr(block_tables), _ptr(seq_lens), _ptr(new_lens), _ptr(refcounts), ptrs, sizes, nc, S, MB,
-            int(block_size), refcounts.shape[0], _stream_handle(stream, refcounts), _ptr(workspace),
-            workspace.numel())
+            _ptr(block_tables), _ptr(seq_lens), _ptr(new_lens), _ptr(refcounts), ptrs.buffer_info()[0],
+            sizes.buffer_info()[0], nc, S, MB, int(block_size), refcounts.shape[0],
+            _stream_handle(stream, refcounts), _ptr(workspace), workspace.numel())
     if st != PA_OK:
         raise PaError(st, "pa_pages_resize")
     return workspace
@@ -684,7 +685,8 @@ def pa_pages_compact(block_tables, seq_lens, refcounts, caches, block_size: int,
     ptrs, sizes, nc, workspace = _pages_args(refcounts, caches, S, MB, workspace)
     with _current(dev):
         st = lib().pa_pages_compact(
-            _ptr(block_tables), _ptr(seq_lens), _ptr(refcounts), _ptr(new_ids), ptrs, sizes, nc, S, MB,
+            _ptr(block_tables), _ptr(seq_lens), _ptr(refcounts), _ptr(new_ids), ptrs.buffer_info()[0],
+            sizes.buffer_info()[0], nc, S, MB,
             int(block_size), refcounts.shape[0], _stream_handle(stream, refcounts), _ptr(workspace),
             workspace.numel())
     if st != PA_OK:

@@ -7,12 +7,14 @@
 //
 //   plan   one thread-block cluster.  Its first CTA works out what each row
 //          needs and numbers the needs in row order (a block scan); the whole
-//          cluster looks through the counts, 32 ids a thread as a bit mask,
-//          numbers the free ids (counts exchanged through distributed shared
-//          memory) and lists the lowest ones.  It stops at the last id needed.
+//          cluster looks through the counts, up to 1024 ids a warp as bit masks
+//          of 32 (one a lane), numbers the free ids (counts exchanged through distributed shared
+//          memory) and lists the lowest ones, a warp a mask at a time so that
+//          what it writes is contiguous.  It stops at the last id needed.  The
+//          counts are on their way while the rows are looked at.
 //          It also leaves the call's status: a call that the pool cannot serve
 //          changes nothing.
-//   apply  the whole GPU: table entries and counts, 256 entries a warp, and
+//   apply  the whole GPU: table entries and counts, 128 entries a warp, and
 //          the pages to be copied, 4 KB a warp and step.
 //
 // What bounds them: a call that copies many pages, the memory (each page read
@@ -44,7 +46,7 @@ enum Mode { kFork, kResize, kCompact };
 
 constexpr int kCluster = 8, kPlanThreads = 1024;
 constexpr int kApplyThreads = 256;
-constexpr int kEntries = 256;                     // table entries per warp job
+constexpr int kPer = 4, kEntries = 32 * kPer;      // table entries per lane and warp job
 constexpr int kCopyUnroll = 8;                    // 16-byte words per lane and job
 constexpr uint32_t kCopyBytes = 32 * 16 * kCopyUnroll;
 constexpr int kMaxCaches = 128;                   // per launch
@@ -108,27 +110,62 @@ __device__ __forceinline__ V block_scan(V v, V* total, V* tmp) {
   return tmp[warp] + incl - v;
 }
 
-// Bit i: block id0 + i exists and is in use.
-__device__ __forceinline__ uint32_t used_mask(const PagesParams& p, long long id0) {
-  uint32_t m = 0;
-  if (id0 + 32 <= p.NB && (reinterpret_cast<uintptr_t>(p.refs) & 15) == 0) {
-    int4 v[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = reinterpret_cast<const int4*>(p.refs + id0)[i];
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      m |= (uint32_t)(v[i].x > 0) << (4 * i) | (uint32_t)(v[i].y > 0) << (4 * i + 1) |
-           (uint32_t)(v[i].z > 0) << (4 * i + 2) | (uint32_t)(v[i].w > 0) << (4 * i + 3);
-  } else {
-    for (int i = 0; i < 32 && id0 + i < p.NB; ++i) m |= (uint32_t)(p.refs[id0 + i] > 0) << i;
+// Ids are looked through in rounds; in a round a warp has `steps` groups of 32
+// ids from its first on, and lane l < steps holds group l's mask (bit i: the
+// i-th block is in use).  Eight groups' counts are loaded at a time.
+struct Groups {
+  int steps;
+  __device__ __forceinline__ explicit Groups(int NB) {
+    constexpr int warps = kCluster * kPlanThreads / 32;
+    steps = min(32, max(1, (NB + warps * 32 - 1) / (warps * 32)));
   }
-  return m;
-}
-// Bit i: block id0 + i exists.
-__device__ __forceinline__ uint32_t valid_mask(const PagesParams& p, long long id0) {
-  const long long n = p.NB - id0;
-  return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
-}
+  __device__ __forceinline__ long long ids_per_warp() const { return 32ll * steps; }
+  __device__ __forceinline__ void load(const PagesParams& p, long long first, int s0, int lane, int (&v)[8]) const {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const long long id = first + 32 * (s0 + j) + lane;
+      v[j] = s0 + j < steps && id < p.NB ? p.refs[id] : 0;
+    }
+  }
+  // (v: the first eight groups, loaded already, or null.)
+  __device__ __forceinline__ uint32_t used(const PagesParams& p, long long first, int lane, const int (*ready)[8]) const {
+    uint32_t m = 0;
+    for (int s0 = 0; s0 < steps; s0 += 8) {
+      int v[8];
+      if (ready && s0 == 0) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = (*ready)[j];
+      } else {
+        load(p, first, s0, lane, v);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t b = __ballot_sync(0xffffffffu, v[j] > 0);
+        if (lane == s0 + j) m = b;
+      }
+    }
+    return m;
+  }
+  // Bit i: the lane's group has an i-th block.
+  __device__ __forceinline__ uint32_t valid(const PagesParams& p, long long first, int lane) const {
+    const long long n = lane < steps ? p.NB - (first + 32 * lane) : 0;
+    return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
+  }
+  // Warp: the ids of the lanes' masks into list[number], the lane's first one
+  // being number `pos`, numbers below `end` only.
+  __device__ __forceinline__ void list(int* out, uint32_t mask, long long pos, long long end, long long first,
+                                       int lane) const {
+    const uint32_t before = (1u << lane) - 1u;
+    for (uint32_t left = __ballot_sync(0xffffffffu, mask != 0); left; left &= left - 1) {
+      const int l = __ffs(left) - 1;
+      const uint32_t m = __shfl_sync(0xffffffffu, mask, l);
+      const long long at = __shfl_sync(0xffffffffu, pos, l);
+      if (at >= end) break;
+      const long long k = at + __popc(m & before);
+      if (((m >> lane) & 1u) && k < end) out[k] = (int)first + 32 * l + lane;
+    }
+  }
+};
 
 // What row i needs: *n new blocks, *src the block to copy (-1: none).
 // Returns false for a row that is refused.
@@ -176,12 +213,16 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads,
     pages_plan_kernel(const __grid_constant__ PagesParams p) {
   __shared__ unsigned long long tmp[33];
   __shared__ unsigned long long shared_count[2];
-  __shared__ long long shared_need;
+  __shared__ long long shared_need;  // (of the first CTA)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   cg::cluster_group cl = cg::this_cluster();
-  const int rank = (int)cl.block_rank(), tid = threadIdx.x;
-  const long long round = (long long)kCluster * kPlanThreads * 32;
+  const int rank = (int)cl.block_rank(), tid = threadIdx.x, lane = tid & 31;
+  const Groups groups(p.NB);
+  const long long round = groups.ids_per_warp() * (kCluster * kPlanThreads / 32);
+  const long long warp_first = groups.ids_per_warp() * (rank * (kPlanThreads / 32) + (tid >> 5));
+  int ready[8];
+  groups.load(p, warp_first, 0, lane, ready);
 
   if constexpr (MODE != kCompact) {
     int bad = 0, copies = 0;
@@ -211,24 +252,24 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads,
       if (tid == 0) shared_need = need;
       bad = __syncthreads_or(bad);
     }
-    cl.sync();
-    const long long need = *cl.map_shared_rank(&shared_need, 0);
-    long long found = 0;
+    long long need = LLONG_MAX, found = 0;
     int par = 0;
     for (long long base = 0; base < p.NB && found < need; base += round, par ^= 1) {
-      const long long id0 = base + ((long long)rank * kPlanThreads + tid) * 32;
-      uint32_t m = id0 < p.NB ? ~used_mask(p, id0) & valid_mask(p, id0) : 0u;
+      const long long first = base + warp_first;
+      const uint32_t m = ~groups.used(p, first, lane, base == 0 ? &ready : nullptr) & groups.valid(p, first, lane);
       unsigned long long total;
       const unsigned long long before = block_scan((unsigned long long)__popc(m), &total, tmp);
       if (tid == 0) shared_count[par] = total;
       cl.sync();
+      need = *cl.map_shared_rank(&shared_need, 0);
       long long pos = found + (long long)before;
+#pragma unroll
       for (int q = 0; q < kCluster; ++q) {
         const long long c = (long long)*cl.map_shared_rank(&shared_count[par], q);
         if (q < rank) pos += c;
         found += c;
       }
-      for (; m && pos < need; m &= m - 1, ++pos) p.ids[pos] = (int)(id0 + __ffs(m) - 1);
+      groups.list(p.ids, m, pos, need, first, lane);
     }
     if (rank == 0 && tid == 0) {
       const bool enough = found >= need;
@@ -239,27 +280,30 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads,
   } else {
     // Blocks in use, then the free ids below that number and the used ones
     // from it on (equally many), both ascending.
-    unsigned long long n = 0, total;
-    for (long long id0 = ((long long)rank * kPlanThreads + tid) * 32; id0 < p.NB; id0 += round)
-      n += __popc(used_mask(p, id0));
+    const uint32_t u_first = groups.used(p, warp_first, lane, &ready);
+    unsigned long long n = __popc(u_first), total;
+    for (long long base = round; base < p.NB; base += round)
+      n += __popc(groups.used(p, base + warp_first, lane, nullptr));
     block_scan(n, &total, tmp);
     if (tid == 0) shared_count[1] = total;
     cl.sync();
     long long used = 0;
+#pragma unroll
     for (int q = 0; q < kCluster; ++q) used += (long long)*cl.map_shared_rank(&shared_count[1], q);
     long long below = 0, above = 0;
     int par = 0;
     for (long long base = 0; base < p.NB; base += round, par ^= 1) {
-      const long long id0 = base + ((long long)rank * kPlanThreads + tid) * 32;
-      const uint32_t valid = valid_mask(p, id0), u = id0 < p.NB ? used_mask(p, id0) : 0u;
-      const long long nb = used - id0;
+      const long long first = base + warp_first;
+      const uint32_t u = base == 0 ? u_first : groups.used(p, first, lane, nullptr);
+      const long long nb = used - (first + 32 * lane);
       const uint32_t front = nb >= 32 ? 0xffffffffu : nb <= 0 ? 0u : (1u << nb) - 1u;  // ids below `used`
-      uint32_t holes = ~u & valid & front, movers = u & ~front;
+      const uint32_t holes = ~u & groups.valid(p, first, lane) & front, movers = u & ~front;
       const unsigned long long mine = (unsigned long long)__popc(holes) << 32 | __popc(movers);
       const unsigned long long before = block_scan(mine, &total, tmp);
       if (tid == 0) shared_count[par] = total;
       cl.sync();
       long long h = below + (long long)(before >> 32), m = above + (long long)(before & 0xffffffffu);
+#pragma unroll
       for (int q = 0; q < kCluster; ++q) {
         const unsigned long long c = *cl.map_shared_rank(&shared_count[par], q);
         if (q < rank) {
@@ -269,12 +313,18 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads,
         below += (long long)(c >> 32);
         above += (long long)(c & 0xffffffffu);
       }
-      for (; holes; holes &= holes - 1) p.ids[h++] = (int)(id0 + __ffs(holes) - 1);
-      for (int i = 0; i < 32 && id0 + i < p.NB; ++i) {
-        const bool is_used = (u >> i) & 1u, is_front = (front >> i) & 1u;
-        if (!is_front) p.rank_of[id0 + i] = is_used ? (int)m : -1;
-        if (p.new_ids && (is_front || !is_used)) p.new_ids[id0 + i] = is_used ? (int)(id0 + i) : -1;
-        if (!is_front && is_used) p.copy_src[m++] = (int)(id0 + i);
+      groups.list(p.ids, holes, h, LLONG_MAX, first, lane);
+      groups.list(p.copy_src, movers, m, LLONG_MAX, first, lane);
+      // Numbers of the moves, and (but for the moved blocks) the new ids.
+      for (int l = 0; l < groups.steps && first + 32 * l < p.NB; ++l) {
+        if (!p.new_ids && first + 32 * l + 31 < used) continue;
+        const long long id = first + 32 * l + lane;
+        const uint32_t mv = __shfl_sync(0xffffffffu, movers, l), us = __shfl_sync(0xffffffffu, u, l);
+        const long long at = __shfl_sync(0xffffffffu, m, l);
+        if (id >= p.NB) continue;
+        const bool is_used = (us >> lane) & 1u;
+        if (id >= used) p.rank_of[id] = is_used ? (int)at + __popc(mv & ((1u << lane) - 1u)) : -1;
+        if (p.new_ids && !(id >= used && is_used)) p.new_ids[id] = is_used ? (int)id : -1;
       }
     }
     if (rank == 0 && tid == 0) {
@@ -296,14 +346,14 @@ __device__ __forceinline__ void apply_row(const PagesParams& p, int i, int j0, i
     if (j0 >= full + part) return;
     const int32_t* src = p.bt + (size_t)p.arg[i] * p.MB;
     int32_t* dst = p.bt_out + (size_t)i * p.MB;
-    int id[kEntries / 32];
+    int id[kPer];
 #pragma unroll
-    for (int k = 0; k < kEntries / 32; ++k) {
+    for (int k = 0; k < kPer; ++k) {
       const int j = j0 + k * 32 + lane;
       id[k] = j < full ? src[j] : 0;
     }
 #pragma unroll
-    for (int k = 0; k < kEntries / 32; ++k) {
+    for (int k = 0; k < kPer; ++k) {
       const int j = j0 + k * 32 + lane;
       if (j < full) {
         if ((unsigned)id[k] < (unsigned)p.NB) atomicAdd(p.refs + id[k], 1);
@@ -322,11 +372,23 @@ __device__ __forceinline__ void apply_row(const PagesParams& p, int i, int j0, i
     if (j0 == 0 && lane == 0) p.lens[i] = N;
     const int oldB = (L + p.BS - 1) / p.BS, newB = (N + p.BS - 1) / p.BS;
     const int lo = min(oldB, newB) - cow, hi = max(oldB, newB);
+    if (lo + j0 >= hi) return;
     int32_t* row = p.bt + (size_t)i * p.MB;
-    for (int j = lo + j0 + lane; j < min(hi, lo + j0 + kEntries); j += 32) {
+    // (The loads of all entries first.)
+    int old[kPer], fresh[kPer];
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      const int j = lo + j0 + k * 32 + lane;
       const bool edge = cow && j == lo;
-      if (edge || j < oldB) {  // given back
-        const int b = row[j];
+      old[k] = j < hi && (edge || j < oldB) ? row[j] : -2;                                   // given back
+      fresh[k] = j < hi && (edge || j >= oldB) ? p.ids[first + (edge ? 0 : cow + j - oldB)] : -1;  // taken
+    }
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      const int j = lo + j0 + k * 32 + lane;
+      const bool edge = cow && j == lo;
+      if (j < hi && (edge || j < oldB)) {
+        const int b = old[k];
         if ((unsigned)b >= (unsigned)p.NB) {
           record(p);
         } else if (atomicSub(p.refs + b, 1) <= 0) {
@@ -334,10 +396,9 @@ __device__ __forceinline__ void apply_row(const PagesParams& p, int i, int j0, i
           record(p);
         }
       }
-      if (edge || j >= oldB) {  // taken
-        const int b = p.ids[first + (edge ? 0 : cow + j - oldB)];
-        p.refs[b] = 1;
-        row[j] = b;
+      if (fresh[k] >= 0) {
+        p.refs[fresh[k]] = 1;
+        row[j] = fresh[k];
       }
     }
   } else {
@@ -345,16 +406,24 @@ __device__ __forceinline__ void apply_row(const PagesParams& p, int i, int j0, i
     if ((L < 0 || L > cap) && j0 == 0 && lane == 0) record(p);
     const int n = (min(max(L, 0), cap) + p.BS - 1) / p.BS;
     int32_t* row = p.bt + (size_t)i * p.MB;
-    for (int j = j0 + lane; j < min(n, j0 + kEntries); j += 32) {
-      const int b = row[j];
-      if ((unsigned)b >= (unsigned)p.NB) {
-        record(p);
-      } else if (b >= used) {
-        const int r = p.rank_of[b];
-        if (r < 0) record(p);  // a table holds a free block
-        else row[j] = p.ids[r];
-      }
+    if (j0 >= n) return;
+    int b[kPer], r[kPer];
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      const int j = j0 + k * 32 + lane;
+      b[k] = j < n ? row[j] : 0;
     }
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      const int j = j0 + k * 32 + lane;
+      const bool in = (unsigned)b[k] < (unsigned)p.NB;
+      r[k] = j < n && in && b[k] >= used ? p.rank_of[b[k]] : -2;
+      // An id outside the pool, or a free block.
+      if (j < n && (!in || r[k] == -1)) record(p);
+    }
+#pragma unroll
+    for (int k = 0; k < kPer; ++k)
+      if (r[k] >= 0) row[j0 + k * 32 + lane] = p.ids[r[k]];
   }
 }
 
