@@ -81,20 +81,15 @@ struct Kv4 {
   using T = T_;
   static constexpr int D = D_, NT = NT_, GT = 8 * NT_, TB = TB_, KVU = KVU_;
   static_assert(KVU_ == 1 || (KVU_ == 2 && NT_ == 1), "two heads share one column tile");
-#ifndef PA_KV4_TILES
-#define PA_KV4_TILES 4
-#endif
   // 16-token tiles per stage (two at head size 256, for two stages in the ring).
-  static constexpr int NTI = TB_ == 64 ? 4 : D_ > 128 || KVU_ == 2 ? 2 : PA_KV4_TILES;
+  static constexpr int NTI = TB_ == 64 ? 4 : D_ > 128 || KVU_ == 2 ? 2 : 4;
   static constexpr int TS = 16 * NTI;            // tokens per stage
   static constexpr int NBLK = TS / TB_;          // blocks per stage
   static_assert(NBLK >= 1, "a stage holds whole blocks");
   static constexpr uint32_t REC = (uint32_t)TB_ * (D_ + 8), BLOCK = REC * KVU_, STAGE = BLOCK * NBLK;
   // Warps per CTA: as many as the accumulators' registers allow (128 or 255 a thread).
-#ifndef PA_KV4_NC
-#define PA_KV4_NC 8
-#endif
-  static constexpr int NC = D_ > 128 && TB_ == 64 ? 4 : (D_ <= 128 && NT_ == 1) ? PA_KV4_NC : 8;
+  // (With two kv heads a unit 12 of 168, with a few spills: 135 us against 138.)
+  static constexpr int NC = D_ > 128 && TB_ == 64 ? 4 : KVU_ == 2 ? 12 : 8;
 
   static constexpr int THREADS = NC * 32;
   static constexpr int X = D_ < 128 ? D_ : 128;  // dims per slab
@@ -932,8 +927,6 @@ __global__ void __launch_bounds__(K::THREADS, 1) kv4_decode_kernel(const __grid_
     st.load_rows(q, [&](int i) { return static_cast<const T*>(prm.q) + out_row_rt(prm, U.s, U.h0 + i) * K::D; }, U.nh,
                  lane);
   };
-  // The next unit's query rows are loaded a stage ahead where registers allow.
-  constexpr bool kAhead = K::NT == 1 && K::D <= 128;
 
   // The first units are dealt out over the CTAs; the counter hands out the rest.
   const int ltw = __ffs(TW) - 1, team = warp >> ltw, tw = warp & (TW - 1);
@@ -989,7 +982,6 @@ __global__ void __launch_bounds__(K::THREADS, 1) kv4_decode_kernel(const __grid_
           in.queue(run_of(V, 0, V.nb), lane);
         }
       }
-      if (kAhead && alone && i == n - 1 && u_next < solo) load_rows(V);
       st.pass(in.ring + in.out, U.t1 - tok, tok, lane);
       in.used();
       in.fill(lane);
@@ -1012,7 +1004,7 @@ __global__ void __launch_bounds__(K::THREADS, 1) kv4_decode_kernel(const __grid_
                     *reinterpret_cast<const float4*>(rows + col * stride + d));
         }
       }
-      if (!kAhead && u_next < solo) load_rows(V);
+      if (u_next < solo) load_rows(V);
       U = V;
     } else {
       // The team's states, each in its warp's ring (whose stages are all used).
