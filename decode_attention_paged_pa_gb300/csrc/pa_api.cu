@@ -327,7 +327,9 @@ int decode_impl(void* out, float* lse, const void* query, const void* key_cache,
     prm.G = G;
     prm.MB = MB;
     prm.num_blocks = num_blocks;
-    prm.P = P;
+    // (A partition past the table's capacity is the capacity: sums of lengths
+    // and partition sizes stay in 32 bits.)
+    prm.P = kv4 && P > MB * BS ? MB * BS : P;
     prm.Pmax = w.pmax;
     prm.hg_per_kv = hg_per_kv;
     prm.n_hg = n_hg;

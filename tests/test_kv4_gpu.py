@@ -66,6 +66,62 @@ def test_more_sequences_than_a_launch_takes():
     check(*kv4_case(8, 530, 4, 2, 64, 16, lens, F16, NB=700), 0.125, P=64)
 
 
+@pytest.mark.parametrize("S,H,KH,D,BS,q_len,dtype", [
+    (420, 32, 8, 64, 16, 1, BF16),     # two kv heads a unit
+    (300, 16, 2, 128, 8, 1, F16),      # eight rows a kv head
+    (300, 16, 4, 80, 32, 4, BF16),     # sixteen rows
+    (300, 3, 3, 256, 16, 1, F16),      # head size 256
+    (300, 5, 5, 128, 64, 1, BF16),     # 64-token blocks
+    (300, 20, 4, 112, 16, 1, F16),     # five rows
+])
+def test_batches_of_many_units(S, H, KH, D, BS, q_len, dtype):
+    """Thousands of units: warps take whole ones, the rest goes to teams.  A
+    sample of the sequences is checked, and that a second run is bitwise the same."""
+    g = torch.Generator().manual_seed(S + D)
+    lens = [int(v) for v in torch.randint(q_len, 900, (S,), generator=g)]
+    lens[5], lens[6] = q_len, 899
+    if q_len == 1:
+        lens[7] = 0
+    q, cache, bt, L = kv4_case(S + D, S, H, KH, D, BS, lens, dtype, q_len=q_len, NB=1500)
+    out, lse = run(q, cache, bt, L, 0.1, P=64)
+    again, lse2 = run(q, cache, bt, L, 0.1, P=64)
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
+    pick = [0, 5, 6, 7, S - 1] + [int(v) for v in torch.randint(0, S, (9,), generator=g)]
+    ref, bound, rl, rb = attend64(q[pick], cache, bt[pick], L[pick], 0.1, dtype)
+    err = (out[pick].double() - ref).abs()
+    assert bool((err <= bound).all()), f"worst {float((err / bound.clamp(min=1e-30)).max()):.2f} of the bound"
+    same = (lse[pick].double() == rl) | ((lse[pick].double() - rl).abs() <= rb)
+    assert bool(same.all())
+
+
+def test_partition_sizes_from_one_block_to_past_the_table():
+    case = kv4_case(21, 3, 8, 2, 128, 16, [300, 17, 64], BF16)
+    for P in (16, 48, 80, 4096, 2 ** 31 - 16):
+        check(*case, 0.09, P=P)
+
+
+def test_another_stream_and_two_calls_at_once():
+    """Calls on two streams at a time, each with a workspace of its own."""
+    dev = torch.device("cuda")
+    cases = [[t.to(dev) for t in kv4_case(30 + i, 40, 8, 2, 128, 16, [(37 * j) % 700 for j in range(40)], F16)]
+             for i in range(2)]
+    want = []
+    for q, c, b, l in cases:
+        o = torch.empty_like(q)
+        binding.pa_decode_v2_kv4(o, q, c, b, l, 0.1, partition_size=64)
+        want.append(o)
+    torch.cuda.synchronize()
+    streams, outs = [torch.cuda.Stream() for _ in cases], [torch.empty_like(c[0]) for c in cases]
+    keep = []
+    for _ in range(5):
+        for s, o, (q, c, b, l) in zip(streams, outs, cases):
+            keep.append(binding.pa_decode_v2_kv4(o, q, c, b, l, 0.1, partition_size=64, stream=s,
+                                                 workspace=torch.empty(1 << 24, dtype=torch.uint8, device=dev)))
+    torch.cuda.synchronize()
+    for o, w in zip(outs, want):
+        assert torch.equal(o, w)
+
+
 @pytest.mark.parametrize("dtype", [F16, BF16], ids=["fp16", "bf16"])
 def test_value_scales_of_every_magnitude(dtype):
     """Value scales over eight orders of magnitude in one sequence: the bound
