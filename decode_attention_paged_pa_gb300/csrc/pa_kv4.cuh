@@ -61,11 +61,21 @@
 // teams of TW warps of a CTA, each a part of the tokens; the team merges the
 // parts through shared memory.
 //
-// Measured on the way (128 sequences of 2048 to 8192 tokens, 32 heads over 8
-// kv heads, D = 128): the scheme of pa_kernel.cuh 239 us (a 4-bit partition
-// holds a quarter of the bytes, so set-ups, hand-overs and the one merging warp
-// outweigh the tokens); whole units without run-ahead 177 us (16 warps of 128
-// registers, 32-token stages) and 158 us (8 of 200, 64).
+// Measured (GB300, 2070 MHz; 6766 GB/s is the measured copy rate):
+//   128 sequences of 2048 to 8192 tokens, 32 heads over 8 kv heads, D = 128:
+//     133 us for 715 MB, 79% of the copy rate (the copies alone, without the
+//     arithmetic, 118 us); 140 with eight warps of 255 registers, 158 with one
+//     kv head a unit and the units handed out whole (177 with 16 warps of 128
+//     registers and 32-token stages), 239 in the scheme of pa_kernel.cuh: a
+//     4-bit partition holds a quarter of the bytes, so set-ups, hand-overs and
+//     the one merging warp outweigh the tokens.
+//   A batch with a few long sequences among short ones, 64 heads over 8:
+//     47 us, 76 without teams for the units left over.
+//   Four new tokens a sequence, 32 heads over 8 (16 rows a unit): 68 us for
+//     160 MB.  The tensor pipe and the issue slots are each under half used;
+//     two warps a scheduler (255 registers) leave the chains of a tile, scores
+//     to weights to values, in the open.  32-token stages 69 us; 10 and 12
+//     warps, which spill, 115 and 97.
 #pragma once
 
 #include "pa_common.cuh"
@@ -183,7 +193,8 @@ struct Kv4Offsets {
 template <class K>
 struct Kv4State {
   using T = typename K::T;
-  static constexpr int NT = K::NT, NK = K::NK, NMT = K::NMT, KW = K::KW, VW = K::VW, NSLAB = K::NSLAB, NTI = K::NTI, KVU = K::KVU;
+  static constexpr int NT = K::NT, NK = K::NK, NMT = K::NMT, KW = K::KW, VW = K::VW, NSLAB = K::NSLAB;
+  static constexpr int NTI = K::NTI, KVU = K::KVU;
   static constexpr uint32_t LO = 0x000f000fu, HI = 0x00f000f0u;
 
   uint32_t qb[NT][NK][2];          // Q^T fragments: the query row of column lane / 4
@@ -538,54 +549,54 @@ struct Kv4State {
       }
 #pragma unroll
       for (int u = 0; u < KVU; ++u) {
-      // Head u's product takes the weights of its own columns.
-      const bool mine = KVU == 1 || (lane >> 4) == u;
-      uint32_t m0[NT], m1[NT];
+        // Head u's product takes the weights of its own columns.
+        const bool mine = KVU == 1 || (lane >> 4) == u;
+        uint32_t m0[NT], m1[NT];
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        m0[n] = mine ? b0[n] : 0u;
-        m1[n] = mine ? b1[n] : 0u;
-      }
-      const uint32_t va = codes + vo + u * K::REC + O::tile(t), vd = codes + vo2 + u * K::REC + O::tile(t);
+        for (int n = 0; n < NT; ++n) {
+          m0[n] = mine ? b0[n] : 0u;
+          m1[n] = mine ? b1[n] : 0u;
+        }
+        const uint32_t va = codes + vo + u * K::REC + O::tile(t), vd = codes + vo2 + u * K::REC + O::tile(t);
 #pragma unroll
-      for (int sl = 0; sl < NSLAB; ++sl) {
-        uint32_t wa[2], wb[2], wc[2], wd[2];
-        value_words(va + sl * O::slab, wa);
-        value_words(vd + sl * O::slab, wb);
-        value_words(va + sl * O::slab + O::hd, wc);
-        value_words(vd + sl * O::slab + O::hd, wd);
+        for (int sl = 0; sl < NSLAB; ++sl) {
+          uint32_t wa[2], wb[2], wc[2], wd[2];
+          value_words(va + sl * O::slab, wa);
+          value_words(vd + sl * O::slab, wb);
+          value_words(va + sl * O::slab + O::hd, wc);
+          value_words(vd + sl * O::slab + O::hd, wd);
 #pragma unroll
-        for (int half = 0; half < VW; ++half) {
-          // VW = 2: rows r and r + 8 of tile mt hold nibble mt of the two
-          // words (nibbles 0-3, then 4-7); VW = 1: nibbles mt and mt + 4 of the one.
-          uint32_t x0, x1, x2, x3;
-          if constexpr (VW == 2) {
-            const uint32_t sel = half ? 0x7632u : 0x5410u;
-            x0 = __byte_perm(wa[0], wb[0], sel);
-            x1 = __byte_perm(wa[1], wb[1], sel);
-            x2 = __byte_perm(wc[0], wd[0], sel);
-            x3 = __byte_perm(wc[1], wd[1], sel);
-          } else {
-            x0 = __byte_perm(wa[0], wb[0], 0x5410u);
-            x1 = __byte_perm(wa[0], wb[0], 0x7632u);
-            x2 = __byte_perm(wc[0], wd[0], 0x5410u);
-            x3 = __byte_perm(wc[0], wd[0], 0x7632u);
-          }
-          const int mt = sl * K::MTS + half * 4;
-          const uint32_t f0[4] = {x0 & LO, x1 & LO, x2 & LO, x3 & LO};
-          const uint32_t f1[4] = {x0 & HI, x1 & HI, x2 & HI, x3 & HI};
-          x0 >>= 8; x1 >>= 8; x2 >>= 8; x3 >>= 8;
-          const uint32_t f2[4] = {x0 & LO, x1 & LO, x2 & LO, x3 & LO};
-          const uint32_t f3[4] = {x0 & HI, x1 & HI, x2 & HI, x3 & HI};
+          for (int half = 0; half < VW; ++half) {
+            // VW = 2: rows r and r + 8 of tile mt hold nibble mt of the two
+            // words (nibbles 0-3, then 4-7); VW = 1: nibbles mt and mt + 4 of the one.
+            uint32_t x0, x1, x2, x3;
+            if constexpr (VW == 2) {
+              const uint32_t sel = half ? 0x7632u : 0x5410u;
+              x0 = __byte_perm(wa[0], wb[0], sel);
+              x1 = __byte_perm(wa[1], wb[1], sel);
+              x2 = __byte_perm(wc[0], wd[0], sel);
+              x3 = __byte_perm(wc[1], wd[1], sel);
+            } else {
+              x0 = __byte_perm(wa[0], wb[0], 0x5410u);
+              x1 = __byte_perm(wa[0], wb[0], 0x7632u);
+              x2 = __byte_perm(wc[0], wd[0], 0x5410u);
+              x3 = __byte_perm(wc[0], wd[0], 0x7632u);
+            }
+            const int mt = sl * K::MTS + half * 4;
+            const uint32_t f0[4] = {x0 & LO, x1 & LO, x2 & LO, x3 & LO};
+            const uint32_t f1[4] = {x0 & HI, x1 & HI, x2 & HI, x3 & HI};
+            x0 >>= 8; x1 >>= 8; x2 >>= 8; x3 >>= 8;
+            const uint32_t f2[4] = {x0 & LO, x1 & LO, x2 & LO, x3 & LO};
+            const uint32_t f3[4] = {x0 & HI, x1 & HI, x2 & HI, x3 & HI};
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            mma_f16(acc[mt][n], f0, m0[n], m1[n]);
-            mma_f16(acc[mt + 1][n], f1, m0[n], m1[n]);
-            mma_f16(acc[mt + 2][n], f2, m0[n], m1[n]);
-            mma_f16(acc[mt + 3][n], f3, m0[n], m1[n]);
+            for (int n = 0; n < NT; ++n) {
+              mma_f16(acc[mt][n], f0, m0[n], m1[n]);
+              mma_f16(acc[mt + 1][n], f1, m0[n], m1[n]);
+              mma_f16(acc[mt + 2][n], f2, m0[n], m1[n]);
+              mma_f16(acc[mt + 3][n], f3, m0[n], m1[n]);
+            }
           }
         }
-      }
       }
     }
   }
@@ -728,8 +739,8 @@ __device__ __forceinline__ void kv4_sentinels(const KParams& prm, const int* len
 }
 
 // (Out of line: a wait that does not succeed at once has time for a call.)
-static __device__ __noinline__ bool kv4_wait_slow(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* err_word,
-                                           long long timeout_ns, int slot) {
+static __device__ __noinline__ bool kv4_wait_slow(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                                  int* err_word, long long timeout_ns, int slot) {
   return __all_sync(0xffffffffu, wait_bounded(bar, parity, abort_flag, err_word, timeout_ns, kSiteFull, slot));
 }
 

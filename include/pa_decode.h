@@ -3,7 +3,10 @@
  * ("PagedAttention V2": partitioned online softmax followed by a
  * cross-partition log-sum-exp combine): single-query decode (pa_decode_v2,
  * pa_decode_v2_ex, pa_decode_v2_lse), multi-query decode (pa_decode_v2_mq),
- * E4M3 (fp8) caches (pa_decode_v2_fp8), host-resident per-step inputs
+ * E4M3 (fp8) caches (pa_decode_v2_fp8), 4-bit caches (pa_decode_v2_kv4,
+ * pa_decode_v2_mq_kv4; written and read back with pa_kv4_append and
+ * pa_kv4_gather), the pages of a pool managed on the device (pa_pages_fork,
+ * pa_pages_resize, pa_pages_compact), host-resident per-step inputs
  * (pa_decode_v2_host_io) and a no-allocation variant
  * (pa_decode_v2_static_scratch).
  *
@@ -298,7 +301,9 @@ size_t pa_kv4_block_bytes(int head_size, int block_size);
  * products).  lse may be NULL.  dtype PA_DTYPE_FP16 or PA_DTYPE_BF16
  * (PA_ERR_UNSUPPORTED for fp32); head sizes, block sizes, partitions, the
  * workspace (pa_decode_v2_workspace_bytes), ownership and errors are those of
- * pa_decode_v2.  |scale * query| is expected below 2^100.
+ * pa_decode_v2; but the m_p left in the workspace may lie below the
+ * partition's maximum, by up to 8 ln 2, l_p and o_p being relative to it.
+ * |scale * query| is expected below 2^100.
  */
 int pa_decode_v2_kv4(void* out, float* lse, const void* query, const void* kv_cache,
                      const int32_t* block_tables, const int32_t* seq_lens, float scale, int num_seqs,
@@ -379,11 +384,12 @@ int pa_kv4_gather(void* key_out, void* value_out, const void* kv_cache, const in
  *   caches       HOST array of num_caches DEVICE pointers: every cache whose
  *                pages follow the tables (keys, values, of every layer; any
  *                layout whose first dimension is the block).  16-byte aligned.
- *   page_bytes   HOST array: bytes of one block in each cache, multiples of 16
+ *   page_bytes   HOST array: bytes of one block in each cache, multiples of 16,
+ *                at most 2^35
  *   block_size   tokens per block, any positive number
  *   workspace    >= pa_pages_workspace_bytes(rows, ...) bytes (rows:
- *                num_children or num_seqs), 16-byte aligned, required; holds
- *                the status (pa_decode_v2_device_status)
+ *                num_children or num_seqs, below 2^24), 16-byte aligned,
+ *                required; holds the status (pa_decode_v2_device_status)
  * Calls enqueue two launches on `stream` (one more per further 128 caches),
  * never synchronise and can be captured into a CUDA graph.  The arrays caches
  * and page_bytes are read before the call returns.  Calls on one pool must be

@@ -216,6 +216,45 @@ def test_many_sequences_large_rows_and_empty_calls():
     assert torch.equal(cd.cpu(), expected(cache, bt, L, new, key, value))
 
 
+def test_replays_from_a_cuda_graph():
+    """A step captured once (append, then the context read back), replayed as the lengths grow."""
+    D, KH, BS, S, dev = 128, 2, 16, 4, torch.device("cuda")
+    lens = [15, 1, 40, 64]
+    cache, bt, L, g = pool(12, S, KH, D, BS, [v + 4 for v in lens])
+    L = torch.tensor(lens, dtype=torch.int32)
+    cd, bd, ld = cache.to(dev), bt.to(dev), L.to(dev)
+    k, v = (torch.zeros((S, KH, D), dtype=BF16, device=dev) for _ in range(2))
+    ko, vo = torch.empty_like(k), torch.empty_like(k)
+    ws, ws2 = (torch.empty(256, dtype=torch.uint8, device=dev) for _ in range(2))
+
+    def step():
+        binding.pa_kv4_append(cd, k, v, bd, ld, workspace=ws)
+        binding.pa_kv4_gather(ko, vo, cd, bd, ld, workspace=ws2)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    want = expected(cache, bt, L, [1] * S, k.cpu(), v.cpu())
+    for i in range(4):
+        key, value = rows(g, S, KH, D, BF16), rows(g, S, KH, D, BF16)
+        k.copy_(key)
+        v.copy_(value)
+        L += 1
+        ld.copy_(L)
+        graph.replay()
+        assert binding.device_status(ws) == binding.device_status(ws2) == binding.PA_OK
+        want = expected(want, bt, L, [1] * S, key, value)
+        assert torch.equal(cd.cpu(), want)
+        K, V, _ = read_records(want, D, BF16)
+        for got, ref in ((ko, K), (vo, V)):
+            nearest(got.cpu(), torch.stack([ref[int(bt[s, p // BS]), :, p % BS] for s, p in enumerate((L - 1).tolist())]))
+
+
 def test_refusals():
     dev = torch.device("cuda")
     D, KH, BS = 128, 2, 16

@@ -48,7 +48,8 @@ def call(fn, **kw):
     (dict(S=-1), BAD), (dict(MB=0), BAD), (dict(BS=0), BAD), (dict(NB=0), BAD), (dict(MB=1 << 28, BS=8), BAD),
     (dict(refs=None), BAD), (dict(refs=FAKE + 2), BAD), (dict(bt=None), BAD), (dict(lens=FAKE + 1), BAD),
     (dict(nc=-1), BAD), (dict(no_array=True), BAD), (dict(caches=[None]), BAD), (dict(caches=[FAKE + 8]), BAD),
-    (dict(sizes=[0]), BAD), (dict(sizes=[24]), BAD), (dict(ws=None), BAD), (dict(ws=FAKE + 8), BAD),
+    (dict(sizes=[0]), BAD), (dict(sizes=[24]), BAD), (dict(sizes=[2 ** 35 + 16]), BAD),
+    (dict(ws=None), BAD), (dict(ws=FAKE + 8), BAD),
     (dict(bytes=256), binding.PA_ERR_WORKSPACE),
 ])
 def test_rejects(fn, kw, status):
@@ -56,7 +57,7 @@ def test_rejects(fn, kw, status):
 
 
 @pytest.mark.parametrize("fn,kw", [
-    ("pa_pages_fork", dict(arg=None)), ("pa_pages_fork", dict(n=-1)), ("pa_pages_fork", dict(out=None)),
+    ("pa_pages_fork", dict(arg=None)), ("pa_pages_fork", dict(n=-1)), ("pa_pages_fork", dict(n=1 << 24)), ("pa_pages_fork", dict(out=None)),
     ("pa_pages_fork", dict(lo=FAKE * 3 + 2)), ("pa_pages_fork", dict(out=FAKE)),
     ("pa_pages_fork", dict(out=FAKE + 2 * 16 - 4)), ("pa_pages_fork", dict(lo=FAKE * 4 + 4)),
     ("pa_pages_resize", dict(arg=None)), ("pa_pages_compact", dict(ids=FAKE + 2)),
