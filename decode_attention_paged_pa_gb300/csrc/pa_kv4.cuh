@@ -98,7 +98,7 @@ struct Kv4 {
   static_assert(NBLK >= 1, "a stage holds whole blocks");
   static constexpr uint32_t REC = (uint32_t)TB_ * (D_ + 8), BLOCK = REC * KVU_, STAGE = BLOCK * NBLK;
   // Warps per CTA: as many as the accumulators' registers allow (128 or 255 a thread).
-  // (With two kv heads a unit 12 of 168, with a few spills: 135 us against 138.)
+  // (With two kv heads a unit 12 of 168: 133 us against 138.)
   static constexpr int NC = D_ > 128 && TB_ == 64 ? 4 : KVU_ == 2 ? 12 : 8;
 
   static constexpr int THREADS = NC * 32;
@@ -117,11 +117,13 @@ struct Kv4 {
   static constexpr uint32_t STATE = GT * AROW * 4 + GT * 2 * 4;
   static constexpr uint32_t SZ_BAR = NC * NSMAX * 8;
   static constexpr uint32_t SZ_PREF = (2 * kMaxSeqsPerLaunch + 1) * 4;  // partition prefix, lengths
-  static constexpr uint32_t FIXED = al16(SZ_BAR) + 64 + al16(SZ_PREF);
+  static constexpr uint32_t SZ_UNIT = NC * 2 * 48;                      // each warp's unit and the one after it
+  static constexpr uint32_t FIXED = al16(SZ_BAR) + 64 + al16(SZ_PREF) + SZ_UNIT;
   static constexpr uint32_t BUDGET = 227 * 1024;
   static constexpr uint32_t RING = (BUDGET - FIXED) / NC / 128 * 128;  // bytes per warp
   static constexpr uint32_t OFF_BAR = NC * RING, OFF_FLAGS = OFF_BAR + al16(SZ_BAR),
-                            OFF_PREF = OFF_FLAGS + 64, BYTES = OFF_PREF + al16(SZ_PREF);
+                            OFF_PREF = OFF_FLAGS + 64, OFF_UNIT = OFF_PREF + al16(SZ_PREF),
+                            BYTES = OFF_UNIT + SZ_UNIT;
   static_assert(BYTES <= BUDGET, "shared memory over budget");
   static constexpr int NS = RING / STAGE < NSMAX ? RING / STAGE : NSMAX;  // ring stages per warp
   static_assert(STATE <= RING && NS >= 2, "a warp's state or two stages fit its ring");
@@ -198,13 +200,13 @@ struct Kv4State {
   static constexpr uint32_t LO = 0x000f000fu, HI = 0x00f000f0u;
 
   uint32_t qb[NT][NK][2];          // Q^T fragments: the query row of column lane / 4
-  float ms[NT][2], thr[NT][2];     // reference (0 until set); 8, or -inf until it is set
+  float ms[NT][2];                 // reference (0 until set)
+  uint32_t set;                    // bit 2n + j: column j of tile n has one
   float l[NT][2], zs[NT][2];       // sums of weights; of weight * (value zero + 8 value scale)
   float qz[NT][2];                 // scale_log2 * sum(q)
   float acc[NMT][NT][4], acc8[NT][4];
   float kf;                        // score factor: scale_log2 over the operands' powers of two
   float vb, vinv;                  // see the top: a power of two, and 2^7 / vb
-  int lim[NT][2], minlim;          // positions the lane's columns see; the warp's least
   // The lane's offsets in a tile: key words, parameters, values of the first
   // and second token of its slots.
   uint32_t ko, po, vo, vo2;
@@ -221,6 +223,7 @@ struct Kv4State {
     asm volatile("" : "+r"(ko), "+r"(po), "+r"(vo), "+r"(vo2));
   }
 
+  __device__ __forceinline__ bool has_ref(int n, int j) const { return (set >> (2 * n + j)) & 1u; }
   __device__ __forceinline__ static int tok_lo(int i) { return (i & 1) ? 7 - (i >> 1) : (i >> 1); }
 
   __device__ __forceinline__ static void key_words(uint32_t a, uint32_t (&w)[KW]) {
@@ -315,7 +318,6 @@ struct Kv4State {
       for (int j = 0; j < 2; ++j) {
         qz[t][j] = kf * sum[j];
         ms[t][j] = 0.f;
-        thr[t][j] = -INFINITY;
         l[t][j] = zs[t][j] = 0.f;
       }
 #pragma unroll
@@ -325,27 +327,16 @@ struct Kv4State {
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc8[t][i] = 0.f;
     }
+    set = 0;
     vb = 7.888609052210118e-31f;  // 2^-100
     vinv = 128.f / vb;
   }
 
-  template <class F>
-  __device__ __forceinline__ void set_limits(F limit_of, int nh, int lane) {
-    int least = 0x7fffffff;
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int col = 8 * t + (lane & 3) * 2 + j;
-        lim[t][j] = has_row(col, nh) ? limit_of(row_of(col, nh)) : 0x7fffffff;
-        least = min(least, lim[t][j]);
-      }
-    minlim = __reduce_min_sync(0xffffffffu, least);
-  }
-
   // The stage at `codes`: ntok of its tokens lie before the sequence end, the
-  // first is token tok0.
-  __device__ __forceinline__ void pass(uint32_t codes, int ntok, int tok0, int lane) {
+  // first is token tok0; rows see at least `least` positions, and column `col`
+  // sees limit_of(col).
+  template <class F>
+  __device__ __forceinline__ void pass(uint32_t codes, int ntok, int tok0, int least, F limit_of, int lane) {
     using O = Kv4Offsets<K>;
     float y[NTI][NT][4];  // scores, less the columns' references
     float2 pv[NTI][2];    // (value scale, value zero) of the lane's score rows r, r + 8 of each tile
@@ -415,9 +406,14 @@ struct Kv4State {
     }
     // Slots past the sequence end hold arbitrary parameters, and causal rows
     // stop earlier: their scores become -inf, and (below) their weights 0.
-    const bool full = ntok >= K::TS && tok0 + K::TS <= minlim;
+    const bool full = ntok >= K::TS && tok0 + K::TS <= least;
     if (!full) {
       const int trow = tok_lo(lane >> 2);
+      int lim[NT][2];
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) lim[n][j] = limit_of(8 * n + (lane & 3) * 2 + j) - tok0;
 #pragma unroll
       for (int t = 0; t < NTI; ++t)
 #pragma unroll
@@ -428,7 +424,7 @@ struct Kv4State {
           for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int j = 0; j < 2; ++j)
-              if (tt >= ntok || tok0 + tt >= lim[n][j]) y[t][n][2 * h + j] = -INFINITY;
+              if (tt >= ntok || tt >= lim[n][j]) y[t][n][2 * h + j] = -INFINITY;
         }
     }
     float vm = 0.f;
@@ -438,7 +434,7 @@ struct Kv4State {
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) raise |= column_max(y, n, j) > thr[n][j];
+      for (int j = 0; j < 2; ++j) raise |= column_max(y, n, j) > (has_ref(n, j) ? 8.f : -INFINITY);
     if (__any_sync(0xffffffffu, raise)) raise_bounds(y, pv);
     if (full) weigh<false>(y, pv);
     else weigh<true>(y, pv);
@@ -481,13 +477,13 @@ struct Kv4State {
         bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 4));
         bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 8));
         bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 16));
-        const bool set = thr[n][j] != -INFINITY;
+        const bool old = has_ref(n, j);
         a[j] = 1.f;
         // (A row that has seen no position yet stays unset; a set reference only rises.)
-        if (bm != -INFINITY && (!set || bm > 0.f)) {
-          if (set) a[j] = ex2(-bm);
+        if (bm != -INFINITY && (!old || bm > 0.f)) {
+          if (old) a[j] = ex2(-bm);
           ms[n][j] += bm;
-          thr[n][j] = 8.f;
+          set |= 1u << (2 * n + j);
 #pragma unroll
           for (int t = 0; t < NTI; ++t) {
             y[t][n][j] -= bm;
@@ -619,7 +615,7 @@ struct Kv4State {
         }
         const int col = 8 * n + 2 * c + j, row = by_column ? col : row_of(col, nh);
         if (!by_column && !has_row(col, nh)) continue;
-        if (r == 0) stat(row, thr[n][j] == -INFINITY ? -INFINITY : ms[n][j], ls);
+        if (r == 0) stat(row, has_ref(n, j) ? ms[n][j] : -INFINITY, ls);
         // (A NaN sum stays NaN: only an empty row divides by nothing.)
         const float f = by_column ? 1.f : ls == 0.f ? 0.f : 1.f / ls;
         const float vbf = vb * f, zf = zz * f;
@@ -650,11 +646,12 @@ struct Kv4State {
 // Unit u = (partition, head group), partitions numbered in batch order:
 // sequence s holds pref[s] .. pref[s + 1] - 1 (pref and the clamped lengths in
 // shared memory).
-struct Kv4Unit {
+struct __align__(16) Kv4Unit {
   int s, p, np, L, t0, t1;
-  int kv, h0, nh;  // first kv head and row head; rows per kv head
+  int kv, h0, nh, pad;  // first kv head and row head; rows per kv head
   int nb, stages;  // blocks, stages
 };
+static_assert(sizeof(Kv4Unit) == 48, "units in shared memory");
 template <class K>
 __device__ __forceinline__ Kv4Unit kv4_unit(const KParams& prm, const int* pref, const int* lens, int u) {
   Kv4Unit U;
@@ -943,9 +940,14 @@ __global__ void __launch_bounds__(K::THREADS, 1) kv4_decode_kernel(const __grid_
   const int ltw = __ffs(TW) - 1, team = warp >> ltw, tw = warp & (TW - 1);
   bool alone = true, alive = true;
   int u = blockIdx.x + (int)gridDim.x * warp;
-  Kv4Unit U{};
+  // A warp's unit and the next one wait in shared memory while the stages are
+  // worked on: registers that spill cost more (beside 227 KB of shared memory
+  // little is left of the L1 cache, so a spilled value comes from L2).
+  Kv4Unit* at = reinterpret_cast<Kv4Unit*>(smem + K::OFF_UNIT) + 2 * warp;
+  int par = 0;
   if (u < solo) {
-    U = kv4_unit<K>(prm, pref, lens, u);
+    const Kv4Unit U = kv4_unit<K>(prm, pref, lens, u);
+    at[0] = U;
     in.queue(run_of(U, 0, U.nb), lane);
     in.fill(lane);
     load_rows(U);
@@ -959,26 +961,31 @@ __global__ void __launch_bounds__(K::THREADS, 1) kv4_decode_kernel(const __grid_
       u = solo + blockIdx.x + (int)gridDim.x * team;
     }
     if (u >= total) break;
-    int i0 = 0, n = U.stages, u_next = total;
-    if (alone) {
-      if (lane == 0) u_next = atomicAdd(prm.hdr + kHdrWork, 1) + warps;
-    } else {
-      U = kv4_unit<K>(prm, pref, lens, u);
-      const int per = (U.stages + TW - 1) >> ltw;
-      i0 = min(tw * per, U.stages);
-      n = min(per, U.stages - i0);
-      if (alive && n > 0) {
-        in.queue(run_of(U, i0 * K::NBLK, min(n * K::NBLK, U.nb - i0 * K::NBLK)), lane);
-        in.fill(lane);
+    int i0 = 0, n, u_next = total, tok, end, least;
+    {
+      Kv4Unit U;
+      if (alone) {
+        if (lane == 0) u_next = atomicAdd(prm.hdr + kHdrWork, 1) + warps;
+        U = at[par];
+        n = U.stages;
+      } else {
+        U = kv4_unit<K>(prm, pref, lens, u);
+        at[par] = U;
+        const int per = (U.stages + TW - 1) >> ltw;
+        i0 = min(tw * per, U.stages);
+        n = min(per, U.stages - i0);
+        if (alive && n > 0) {
+          in.queue(run_of(U, i0 * K::NBLK, min(n * K::NBLK, U.nb - i0 * K::NBLK)), lane);
+          in.fill(lane);
+        }
+        load_rows(U);
+        u_next = u + (int)gridDim.x * (K::NC >> ltw);
       }
-      load_rows(U);
-      u_next = u + (int)gridDim.x * (K::NC >> ltw);
+      tok = U.t0 + i0 * K::TS;
+      end = U.t1;
+      least = U.L - prm.q_len + 1;
     }
     st.begin_unit(q, prm.scale_log2);
-    if (prm.q_len > 1) st.set_limits([&](int h) { return row_limit<true>(prm, U.L, U.h0 + h); }, U.nh, lane);
-    else st.set_limits([&](int) { return U.L; }, U.nh, lane);
-    Kv4Unit V = U;
-    int tok = U.t0 + i0 * K::TS;
     for (int i = 0; i < n && alive; ++i, tok += K::TS) {
       if (!in.wait(abort_flag)) {
         in.drain();
@@ -989,14 +996,22 @@ __global__ void __launch_bounds__(K::THREADS, 1) kv4_decode_kernel(const __grid_
         // The claim has been answered: what is asked for runs on into the next unit.
         u_next = __shfl_sync(0xffffffffu, u_next, 0);
         if (u_next < solo) {
-          V = kv4_unit<K>(prm, pref, lens, u_next);
+          const Kv4Unit V = kv4_unit<K>(prm, pref, lens, u_next);
+          at[par ^ 1] = V;
           in.queue(run_of(V, 0, V.nb), lane);
         }
       }
-      st.pass(in.ring + in.out, U.t1 - tok, tok, lane);
+      st.pass(in.ring + in.out, end - tok, tok, least,
+              [&](int col) {
+                const Kv4Unit& U = at[par];
+                if (prm.q_len == 1 || !st.has_row(col, U.nh)) return U.L;
+                return row_limit<true>(prm, U.L, U.h0 + st.row_of(col, U.nh));
+              },
+              lane);
       in.used();
       in.fill(lane);
     }
+    const Kv4Unit U = at[par];
     if (alone) {
       if (!alive) {
         u = solo;
@@ -1015,8 +1030,8 @@ __global__ void __launch_bounds__(K::THREADS, 1) kv4_decode_kernel(const __grid_
                     *reinterpret_cast<const float4*>(rows + col * stride + d));
         }
       }
-      if (u_next < solo) load_rows(V);
-      U = V;
+      par ^= 1;
+      if (u_next < solo) load_rows(at[par]);
     } else {
       // The team's states, each in its warp's ring (whose stages are all used).
       float* state = reinterpret_cast<float*>(smem + warp * K::RING);
