@@ -63,19 +63,21 @@
 //
 // Measured (GB300, 2070 MHz; 6766 GB/s is the measured copy rate):
 //   128 sequences of 2048 to 8192 tokens, 32 heads over 8 kv heads, D = 128:
-//     133 us for 715 MB, 79% of the copy rate (the copies alone, without the
+//     131 us for 715 MB, 81% of the copy rate (the copies alone, without the
 //     arithmetic, 118 us); 140 with eight warps of 255 registers, 158 with one
 //     kv head a unit and the units handed out whole (177 with 16 warps of 128
 //     registers and 32-token stages), 239 in the scheme of pa_kernel.cuh: a
 //     4-bit partition holds a quarter of the bytes, so set-ups, hand-overs and
 //     the one merging warp outweigh the tokens.
 //   A batch with a few long sequences among short ones, 64 heads over 8:
-//     47 us, 76 without teams for the units left over.
-//   Four new tokens a sequence, 32 heads over 8 (16 rows a unit): 68 us for
-//     160 MB.  The tensor pipe and the issue slots are each under half used;
-//     two warps a scheduler (255 registers) leave the chains of a tile, scores
-//     to weights to values, in the open.  32-token stages 69 us; 10 and 12
-//     warps, which spill, 115 and 97.
+//     45 us, 76 without teams for the units left over.
+//   Four new tokens a sequence, 32 heads over 8 (16 rows a unit): 60 us for
+//     160 MB.  The tensor pipe is a third used, the issue slots 40%: two warps a
+//     scheduler (255 registers) leave the chains of a tile, scores to weights to
+//     values, in the open.  32-token stages 64 to 67 us.  What cost most before
+//     that were spilled registers: 227 KB of shared memory leave next to no L1,
+//     so they come from L2 (68 us with ten reloads a stage; 10 and 12 warps of
+//     168 registers, 13 a tile, 115 and 90).
 #pragma once
 
 #include "pa_common.cuh"
@@ -97,9 +99,13 @@ struct Kv4 {
   static constexpr int NBLK = TS / TB_;          // blocks per stage
   static_assert(NBLK >= 1, "a stage holds whole blocks");
   static constexpr uint32_t REC = (uint32_t)TB_ * (D_ + 8), BLOCK = REC * KVU_, STAGE = BLOCK * NBLK;
-  // Warps per CTA: as many as the accumulators' registers allow (128 or 255 a thread).
-  // (With two kv heads a unit 12 of 168: 133 us against 138.)
-  static constexpr int NC = D_ > 128 && TB_ == 64 ? 4 : KVU_ == 2 ? 12 : 8;
+  // Warps per CTA: as many as the accumulators' registers allow without a
+  // spill: 12 of 168 a thread where a unit has 8 columns, 8 of 255 where it has
+  // 16 or the head 256 dims, 4 where two stages of 64-token blocks of such a
+  // head fill the ring.  (12 against 8: 128 sequences of 32 heads over 8 133
+  // against 138 us, 64 of 64 over 8 74 against 86, long skew 45 against 47; 16
+  // columns, spilling: 90 against 60.)
+  static constexpr int NC = NT_ == 2 ? 8 : D_ <= 128 ? 12 : TB_ == 64 ? 4 : 8;
 
   static constexpr int THREADS = NC * 32;
   static constexpr int X = D_ < 128 ? D_ : 128;  // dims per slab
