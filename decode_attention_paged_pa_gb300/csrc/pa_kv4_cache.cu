@@ -6,8 +6,11 @@
 // to each other in the token rows, D/2 bytes of codes and two parameters in
 // the cache.  D/16 lanes (of a power of two, the last ones idle at head sizes
 // 80, 96 and 112) take a vector with two 16-byte accesses each on the row side
-// and one 8-byte access on the cache side, a few vectors at a time so that
-// enough loads are in flight.  A CTA takes a run of consecutive tokens; its
+// and two 4-byte accesses on the cache side, two vectors at a time so that
+// enough loads are in flight.  A lane's two groups of 8 elements lie half a
+// vector apart: each access is contiguous over the lanes (16 elements next to
+// each other and 8-byte codes instead wrote half sectors, 115 us for the
+// prompts below where this took 111).  A CTA takes a run of consecutive tokens; its
 // first warp finds each token's sequence (a 32-way search of the row offsets
 // for the first, steps from there for the others), block and slot, while the
 // others' rows are on their way.
@@ -23,7 +26,7 @@
 // pair (rounded once).
 //
 // Measured (GB300): chunks of 24 prompts written and their contexts read back
-// (8 kv heads, D = 128), 115 us for 542 MB, 70% of the measured copy rate of
+// (8 kv heads, D = 128), 104 us for 542 MB, 77% of the measured copy rate of
 // 6766 GB/s (247 in the first form; 137 with a persistent grid whose first warp
 // looked ahead: many small CTAs hide the placing as well).  One token each of
 // 128 sequences, written and read back: 7 us, two launches of three dependent
@@ -50,7 +53,8 @@ struct Kv4Params {
 };
 
 constexpr int kWorkers = 128, kThreads = kWorkers + 32;
-constexpr int kMaxTokens = 16;  // per CTA
+constexpr int kMaxTokens = 32;   // per CTA
+constexpr int kElements = 16384;  // per CTA, about
 constexpr int kBatch = 2;       // vectors a lane group has in flight
 
 // New (or wanted) tokens of sequence s: rows [first, first + n) of N.
@@ -180,7 +184,7 @@ __device__ __forceinline__ uint32_t quantise8(const float (&f)[8], float lo, flo
 }
 
 template <typename T, int D, bool GATHER>
-__global__ void __launch_bounds__(kThreads, 7) kv4_tokens_kernel(const __grid_constant__ Kv4Params p) {
+__global__ void __launch_bounds__(kThreads, GATHER ? 9 : 7) kv4_tokens_kernel(const __grid_constant__ Kv4Params p) {
   using P = Pair<T>;
   using V = typename P::V;
   constexpr int LPV = lanes_per_vector<D>(), NG = kWorkers / LPV;
@@ -206,7 +210,10 @@ __global__ void __launch_bounds__(kThreads, 7) kv4_tokens_kernel(const __grid_co
     const bool act = gl < D / 16;
     const int per_tok = 2 * p.KH;
     const uint32_t rec_bytes = (uint32_t)p.BS * (D + 8), half = (uint32_t)p.BS * (D / 2);
-    const uint32_t code_at = (uint32_t)(gl / (X / 16)) * p.BS * XB + (uint32_t)(gl % (X / 16)) * 8;
+    // This lane's two groups of 8 elements (each access is contiguous over the lanes).
+    constexpr int HALF = D / 16;
+    const uint32_t at0 = (uint32_t)(gl / (X / 8)) * p.BS * XB + (uint32_t)(gl % (X / 8)) * 4;
+    const uint32_t at1 = (uint32_t)((gl + HALF) / (X / 8)) * p.BS * XB + (uint32_t)((gl + HALF) % (X / 8)) * 4;
     // This group's next vector: token i, and k = (key or value, head) within it.
     int i = grp / per_tok, k = grp - i * per_tok;
     bool placed = false;
@@ -220,12 +227,12 @@ __global__ void __launch_bounds__(kThreads, 7) kv4_tokens_kernel(const __grid_co
         const int sel = k >= p.KH;
         vi[j] = i;
         vk[j] = k;
-        row[j] = static_cast<T*>(p.row[sel]) + (t0 + i) * p.stride[sel] + (k - sel * p.KH) * D + gl * 16;
+        row[j] = static_cast<T*>(p.row[sel]) + (t0 + i) * p.stride[sel] + (k - sel * p.KH) * D + gl * 8;
         if constexpr (!GATHER) {
           x[j][0] = x[j][1] = make_uint4(0, 0, 0, 0);
           if (act && i < nt) {
             x[j][0] = reinterpret_cast<const uint4*>(row[j])[0];
-            x[j][1] = reinterpret_cast<const uint4*>(row[j])[1];
+            x[j][1] = reinterpret_cast<const uint4*>(row[j])[HALF];
           }
         }
         for (k += NG; k >= per_tok; k -= per_tok) ++i;
@@ -243,7 +250,7 @@ __global__ void __launch_bounds__(kThreads, 7) kv4_tokens_kernel(const __grid_co
         const int blk = in ? s_blk[vi[j]] : -1;
         const uint32_t slot = in ? s_slot[vi[j]] : 0, sel = vk[j] >= p.KH;
         uint8_t* rec = p.cache + ((size_t)max(blk, 0) * p.KH + (vk[j] - (int)sel * p.KH)) * rec_bytes;
-        code[j] = rec + (sel * half + slot * XB + code_at);
+        code[j] = rec + (sel * half + slot * XB);
         par[j] = rec + (2 * half + slot * 8 + sel * 4);
         go[j] = act && blk >= 0;
       }
@@ -252,7 +259,8 @@ __global__ void __launch_bounds__(kThreads, 7) kv4_tokens_kernel(const __grid_co
         uint32_t sz[kBatch];
 #pragma unroll
         for (int j = 0; j < kBatch; ++j) {
-          w[j] = go[j] ? *reinterpret_cast<const uint2*>(code[j]) : make_uint2(0, 0);
+          w[j].x = go[j] ? *reinterpret_cast<const uint32_t*>(code[j] + at0) : 0u;
+          w[j].y = go[j] ? *reinterpret_cast<const uint32_t*>(code[j] + at1) : 0u;
           sz[j] = go[j] ? *reinterpret_cast<const uint32_t*>(par[j]) : 0u;
         }
         const V base = as_pair<V>(P::kBase);
@@ -274,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, 7) kv4_tokens_kernel(const __grid_co
           }
           if (go[j]) {
             reinterpret_cast<uint4*>(row[j])[0] = make_uint4(o[0], o[1], o[2], o[3]);
-            reinterpret_cast<uint4*>(row[j])[1] = make_uint4(o[4], o[5], o[6], o[7]);
+            reinterpret_cast<uint4*>(row[j])[HALF] = make_uint4(o[4], o[5], o[6], o[7]);
           }
         }
       } else {
@@ -317,7 +325,8 @@ __global__ void __launch_bounds__(kThreads, 7) kv4_tokens_kernel(const __grid_co
             unpack_chunk<T>(x[j][1], f);
             w.y = quantise8(f, low, s, r, fast);
           }
-          *reinterpret_cast<uint2*>(code[j]) = w;
+          *reinterpret_cast<uint32_t*>(code[j] + at0) = w.x;
+          *reinterpret_cast<uint32_t*>(code[j] + at1) = w.y;
           if (gl == 0) *reinterpret_cast<uint32_t*>(par[j]) = sz;
         }
       }
@@ -329,10 +338,13 @@ __global__ void __launch_bounds__(kThreads, 7) kv4_tokens_kernel(const __grid_co
 template <typename T, bool GATHER>
 cudaError_t launch_tokens(const Kv4Params& p, int D, cudaStream_t st) {
   // Tokens per CTA: one while the call is too small to give every SM eight
-  // CTAs, then as many as still do, up to kMaxTokens.
-  const int want = device_sm_count() * 8;
+  // CTAs, then as many as still do, up to kElements' worth (8 tokens of 8 heads
+  // of 128 dims: 104 us for the prompts above, 111 with 16 tokens, 105 with 4;
+  // 8 tokens whatever the heads: 162 against 140 us at 32 heads, 122 against 47
+  // at one head of 64 dims).
+  const int want = device_sm_count() * 8, most = kElements / (2 * p.KH * D);
   Kv4Params q = p;
-  q.tpc = p.N / want < 1 ? 1 : p.N / want > kMaxTokens ? kMaxTokens : p.N / want;
+  q.tpc = max(1, min(min(most, kMaxTokens), p.N / want));
   const int grid = p.N == 0 ? 1 : (int)(((long long)p.N + q.tpc - 1) / q.tpc);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid, 1, 1);
