@@ -49,7 +49,8 @@
 // (every nibble is a finite number).
 //
 // Work.  A unit is (sequence, partition, kv head, GT of its query rows), a run
-// of stages of 64 tokens (32 at head size 256).  One CTA of NC equal warps per
+// of stages of 64 tokens (32 at head size 256, and where a unit is two kv heads:
+// GT = 8 columns of four rows each).  One CTA of NC equal warps per
 // SM, no producer: a warp takes whole units from a global counter, owns a ring
 // of a few stages and refills a stage itself, by one bulk copy per block, right
 // after it has used it; what it asks for runs ahead into its next unit.  Units
@@ -93,7 +94,8 @@ struct Kv4 {
   using T = T_;
   static constexpr int D = D_, NT = NT_, GT = 8 * NT_, TB = TB_, KVU = KVU_;
   static_assert(KVU_ == 1 || (KVU_ == 2 && NT_ == 1), "two heads share one column tile");
-  // 16-token tiles per stage (two at head size 256, for two stages in the ring).
+  // 16-token tiles per stage (two at head size 256 and of two kv heads, for two
+  // stages in the ring).
   static constexpr int NTI = TB_ == 64 ? 4 : D_ > 128 || KVU_ == 2 ? 2 : 4;
   static constexpr int TS = 16 * NTI;            // tokens per stage
   static constexpr int NBLK = TS / TB_;          // blocks per stage
