@@ -21,7 +21,10 @@
 //
 // Two launch shapes, both programmatic dependents of phase 1 that read the
 // lengths first and wait for phase 1 to complete (griddepcontrol.wait) before
-// they read any state:
+// they read any state.  Every CTA waits, also one without a row to combine:
+// what follows on the stream may be a programmatic dependent of this launch
+// (the next call's header clear, pages being moved, tokens being written), and
+// this launch's completion has to stand for that of phase 1.
 //  - pa_combine_rows_kernel (up to kRowsMaxSeqs sequences, when the table
 //    allows more than 16 partitions): one CTA of 16
 //    warps per SM, persistent over the batch's row groups, each sequence's WPR
@@ -193,9 +196,10 @@ __global__ void __launch_bounds__(NW * 32) pa_combine_kernel(const __grid_consta
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int s = blockIdx.x;
   const int np = seq_partitions(prm, s);
-  if (np <= 1) return;  // finished by phase 1 (or empty: zeros written there)
-  // Partition states are phase 1's output.
+  // Partition states are phase 1's output; and no CTA ends before phase 1 has
+  // (see the top).
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (np <= 1) return;  // finished by phase 1 (or empty: zeros written there)
   const int rpc = NW / prm.wpr;
   combine_rows<T, D, NW>(prm, s, np, prm.wpr, blockIdx.y * rpc, warp, lane, s_acc, s_m, s_t);
 }
@@ -241,8 +245,8 @@ __global__ void __launch_bounds__(kRowsWarps * 32, 1) pa_combine_rows_kernel(con
   }
   __syncthreads();
   const int total = s_pref[S];
-  if ((int)blockIdx.x >= total) return;
-  // Partition states are phase 1's output.
+  // Partition states are phase 1's output; and no CTA ends before phase 1 has
+  // (see the top).
   asm volatile("griddepcontrol.wait;" ::: "memory");
   for (int v = blockIdx.x; v < total; v += gridDim.x) {
     int lo = 0, hi = S;  // s_pref[lo] <= v < s_pref[lo + 1]
