@@ -97,8 +97,9 @@ __device__ __forceinline__ void place(const Kv4Params& p, int t0, int nt, int la
   int first, n;
   seq_rows(p, s, &first, &n);
   const int i = t - first, L = p.lens[s];
-  // Rows behind the last sequence (and rows of a malformed offset list) are left alone.
-  if (i < 0 || i >= n || L < n || L > p.MB * p.BS) return;
+  // Rows behind the last sequence are left alone, and so are those of a sequence
+  // that write_status refuses.
+  if (i < 0 || i >= n || first < 0 || first + (long long)n > p.N || L < n || L > p.MB * p.BS) return;
   const int pos = L - n + i;
   const int b = p.bt[(size_t)s * p.MB + pos / p.BS];
   if ((unsigned)b >= (unsigned)p.num_blocks) return;

@@ -344,9 +344,12 @@ int pa_decode_v2_mq_kv4(void* out, float* lse, const void* query, const void* kv
  *                (pa_decode_v2_device_status), whatever it held before
  * A position of several sequences (a shared block) must not be written by two
  * of them.  A length below the sequence's row count or above the table's
- * capacity, offsets that descend or pass num_tokens, and block ids outside
- * the pool are recorded as PA_ERR_DEVICE_BOUNDS; the rows concerned are
- * skipped.  One launch on `stream`; it can be captured into a CUDA graph.
+ * capacity, offsets of a sequence that descend, start below 0 or pass
+ * num_tokens, and block ids outside the pool are recorded as
+ * PA_ERR_DEVICE_BOUNDS; all rows of such a sequence (of a bad block id: those
+ * of its block) are skipped.  Where offsets descend, rows of other sequences may
+ * be skipped too, and one that several claim goes to one of them.  One launch on
+ * `stream`; it can be captured into a CUDA graph.
  */
 int pa_kv4_append(void* kv_cache, const void* key, const void* value, const int32_t* block_tables,
                   const int32_t* seq_lens, const int32_t* cu_tokens, int num_seqs, int num_tokens,

@@ -276,3 +276,62 @@ def test_refusals():
         binding.pa_kv4_append(c, wide[:, :KH * D].unflatten(1, (KH, D)), k, b, l)
     with pytest.raises(binding.PaError):
         binding.pa_kv4_append(c, k, k, b, l, workspace=torch.empty(64, dtype=torch.uint8, device=dev))
+
+
+def slots(rec, D):
+    """Records [KH, BS * (D + 8)] as the bytes of each token: [BS, KH, D + 8]."""
+    KH, BS, x = rec.shape[0], rec.shape[-1] // (D + 8), min(D, 128)
+    n = BS * D // 2
+    codes = rec[:, :2 * n].view(KH, 2, D // x, BS, x // 2).permute(3, 0, 1, 2, 4).reshape(BS, KH, D)
+    return torch.cat([codes, rec[:, 2 * n:].view(KH, BS, 8).transpose(0, 1)], -1)
+
+
+@pytest.mark.parametrize("cu,refused", [
+    ([0, 4, 6, 12], [2]),           # passes the nine rows
+    ([-2, 4, 6, 9], [0]),           # starts below 0
+    ([0, 4, 2 ** 31 - 1, 2 ** 31 - 1], [1, 2]),
+    ([0, 6, 4, 9], [1]),            # descend
+    ([0, 4, -2 ** 31, 9], [1, 2]),
+    ([7, 5, 6, 3], [0, 2]),
+])
+def test_rows_of_refused_offsets_are_skipped(cu, refused):
+    """Every slot of a refused sequence keeps its bytes, its rows what they held.
+    The other sequences get their rows; where offsets descend, some or none of them."""
+    D, KH, BS = 128, 2, 16
+    lens = [20, 9, 18]
+    cache, bt, L, g = pool(6, 3, KH, D, BS, lens)
+    key, value = rows(g, 9, KH, D, F16), rows(g, 9, KH, D, F16)
+    dev = torch.device("cuda")
+    cd, cud = cache.to(dev), torch.tensor(cu, dtype=torch.int32, device=dev)
+    ws = binding.pa_kv4_append(cd, key.to(dev), value.to(dev), bt.to(dev), L.to(dev), cu_tokens=cud)
+    assert binding.device_status(ws) == binding.PA_ERR_DEVICE_BOUNDS
+    ko = torch.full_like(key, 9.0, device=dev)
+    vo = ko.clone()
+    ws = binding.pa_kv4_gather(ko, vo, cd, bt.to(dev), L.to(dev), cu_tokens=cud)
+    assert binding.device_status(ws) == binding.PA_ERR_DEVICE_BOUNDS
+    descend = any(a > b for a, b in zip(cu, cu[1:]))
+    claims = {}  # row -> (sequence, position)
+    for s in range(3):
+        if s not in refused:
+            for t in range(cu[s], cu[s + 1]):
+                claims.setdefault(t, []).append((s, lens[s] - (cu[s + 1] - cu[s]) + t - cu[s]))
+    allowed = {(s, p): t for t, c in claims.items() for s, p in c}
+    got = cd.cpu()
+    for s in range(3):
+        for p in range(lens[s]):
+            b, o = int(bt[s, p // BS]), p % BS
+            now, old = slots(got[b], D)[o], slots(cache[b], D)[o]
+            if (s, p) not in allowed:
+                assert torch.equal(now, old), (s, p)
+                continue
+            t = allowed[s, p]
+            at, one = torch.zeros(3, dtype=torch.int32), [int(i == s) for i in range(3)]
+            at[s] = p + 1
+            new = slots(expected(cache, bt, at, one, key[t:t + 1], value[t:t + 1])[b], D)[o]
+            assert torch.equal(now, new) or (descend and torch.equal(now, old)), (s, p)
+    held = {int(bt[s, j]) for s in range(3) for j in range(-(-lens[s] // BS))}
+    for b in set(range(cache.shape[0])) - held:
+        assert torch.equal(got[b], cache[b])
+    for t in range(9):
+        kept = bool((ko[t] == 9).all()) and bool((vo[t] == 9).all())
+        assert kept if t not in claims else descend or not kept
