@@ -26,15 +26,19 @@
 // fp16.  A weight's rounding error meets the code, whose mean is far from
 // zero; it is kept to the spread of the codes (c - 8) by summing the rounded
 // weights themselves (one more product, with rows of code 8) and putting
-// 8 p_t vs_t back in fp32 with the zeros.  The weights are scaled by the power
-// of two 2^7 / vb, vb above every value scale the warp has met (raised, with
-// the accumulators, when a larger one comes), so they stay in fp16's range
-// whatever the cache's magnitude.
+// 8 p_t vs_t back in fp32 with the zeros.
 //
-// Softmax without a reduction per item: each column keeps a reference (a
-// maximum it has met) and raises it only when a score passes it by more than
-// 2^8, which one vote per item finds out; weights stay below 2^8, sums and
-// accumulators in fp32.  Most items need no shuffle, no rescaling.
+// Softmax without a reduction per item: each column subtracts a reference from
+// its scores that brings the largest p_t vs_t it has met to 2^6, so that what is
+// rounded to fp16 has its range whatever the cache's magnitude and however far
+// its value scales differ: a large scale at a position of no weight takes nothing
+// from the others.  (p_t itself stays below 2^40, and the sums in fp32.)  The
+// reference is raised, with the sums and accumulators, only where a product may
+// pass 2^15, which one vote per item finds out from a bound (the lane's largest
+// p times its largest scale); most items need no shuffle, no rescaling.
+// (References of the scores alone and one factor for the scales, above the
+// largest met by the warp, cost as much and lost the others' bits: 2^28 below
+// that scale nothing was left.)
 //
 // Rows and slots.  MMA row i of a 16-token score tile holds token kTok(i):
 // 0 7 1 6 2 5 3 4, then 8 more of the same.  The 4-byte words of a token row
@@ -143,6 +147,11 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 __device__ __forceinline__ uint32_t lds_b32(uint32_t a) {
   uint32_t v;
   asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a));
@@ -214,7 +223,9 @@ struct Kv4State {
   float qz[NT][2];                 // scale_log2 * sum(q)
   float acc[NMT][NT][4], acc8[NT][4];
   float kf;                        // score factor: scale_log2 over the operands' powers of two
-  float vb, vinv;                  // see the top: a power of two, and 2^7 / vb
+  // Weights (log2) and their products with the value scales: the most there may
+  // be, and where a new reference puts them.
+  static constexpr float kTopP = 40.f, kNewP = 36.f, kTopW = 32768.f, kNewW = 6.f;
   // The lane's offsets in a tile: key words, parameters, values of the first
   // and second token of its slots.
   uint32_t ko, po, vo, vo2;
@@ -336,8 +347,6 @@ struct Kv4State {
       for (int i = 0; i < 4; ++i) acc8[t][i] = 0.f;
     }
     set = 0;
-    vb = 7.888609052210118e-31f;  // 2^-100
-    vinv = 128.f / vb;
   }
 
   // The stage at `codes`: ntok of its tokens lie before the sequence end, the
@@ -438,12 +447,15 @@ struct Kv4State {
     float vm = 0.f;
 #pragma unroll
     for (int t = 0; t < NTI; ++t) vm = fmaxf(vm, fmaxf(fabsf(pv[t][0].x), fabsf(pv[t][1].x)));
-    bool raise = vm >= vb;
+    float top = column_max(y, 0, 0);
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int i = 1; i < 2 * NT; ++i) top = fmaxf(top, column_max(y, i >> 1, i & 1));
+    bool raise = top > kTopP || vm * ex2(top) > kTopW;
+    if (set != (1u << (2 * NT)) - 1u) {
 #pragma unroll
-      for (int j = 0; j < 2; ++j) raise |= column_max(y, n, j) > (has_ref(n, j) ? 8.f : -INFINITY);
-    if (__any_sync(0xffffffffu, raise)) raise_bounds(y, pv);
+      for (int i = 0; i < 2 * NT; ++i) raise |= !has_ref(i >> 1, i & 1) && column_max(y, i >> 1, i & 1) > -INFINITY;
+    }
+    if (__any_sync(0xffffffffu, raise)) raise_references(y, pv);
     if (full) weigh<false>(y, pv);
     else weigh<true>(y, pv);
     values(y, codes + O::voff, lane);
@@ -456,51 +468,48 @@ struct Kv4State {
     return b;
   }
 
-  // New references, and a new bound on the value scales (finite ones: a NaN
-  // or Inf goes through to the output whatever the bound is; four times the
-  // largest, so that few items raise it); the sums and accumulators follow.
-  __device__ __forceinline__ void raise_bounds(float (&y)[NTI][NT][4], const float2 (&pv)[NTI][2]) {
-    float vm = 0.f;
+  // New references for the columns that have none, or whose weights or products
+  // pass their bounds; the sums and accumulators follow.  (Scales that are not
+  // finite count for nothing here: they go through to the output whatever the
+  // reference is.)
+  __device__ __forceinline__ void raise_references(float (&y)[NTI][NT][4], const float2 (&pv)[NTI][2]) {
+    float lv[NTI][2];
 #pragma unroll
     for (int t = 0; t < NTI; ++t)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const float a = fabsf(pv[t][h].x);
-        vm = a < INFINITY ? fmaxf(vm, a) : vm;
+        lv[t][h] = a < INFINITY ? lg2(a) : -INFINITY;
       }
-    const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(vm));
-    float down = 1.f;
-    if (__uint_as_float(top) >= vb) {
-      const float nb = __uint_as_float(min((top >> 23) + 3u, 254u) << 23);
-      down = vb / nb;
-      vb = nb;
-      vinv = 128.f / nb;
-    }
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       float a[2];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        float bm = column_max(y, n, j);
-        bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 4));
-        bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 8));
-        bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 16));
+        float top = column_max(y, n, j), prod = -INFINITY;  // log2 of the largest weight, and product
+#pragma unroll
+        for (int t = 0; t < NTI; ++t) prod = fmaxf(prod, fmaxf(y[t][n][j] + lv[t][0], y[t][n][j + 2] + lv[t][1]));
+#pragma unroll
+        for (int k = 4; k < 32; k <<= 1) {
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
+          prod = fmaxf(prod, __shfl_xor_sync(0xffffffffu, prod, k));
+        }
         const bool old = has_ref(n, j);
         a[j] = 1.f;
         // (A row that has seen no position yet stays unset; a set reference only rises.)
-        if (bm != -INFINITY && (!old || bm > 0.f)) {
-          if (old) a[j] = ex2(-bm);
-          ms[n][j] += bm;
+        if (top != -INFINITY && (!old || top > kTopP || prod > 15.f)) {
+          const float up = fmaxf(prod - kNewW, top - kNewP);
+          if (old) a[j] = ex2(-up);
+          ms[n][j] += up;
           set |= 1u << (2 * n + j);
 #pragma unroll
           for (int t = 0; t < NTI; ++t) {
-            y[t][n][j] -= bm;
-            y[t][n][j + 2] -= bm;
+            y[t][n][j] -= up;
+            y[t][n][j + 2] -= up;
           }
         }
         l[n][j] *= a[j];
         zs[n][j] *= a[j];
-        a[j] *= down;
       }
 #pragma unroll
       for (int mt = 0; mt < NMT; ++mt) {
@@ -516,14 +525,14 @@ struct Kv4State {
     }
   }
 
-  // Scores into weights (over the value scales' bound), and their sums.
+  // Scores into weights, their sums, and their products with the value scales.
   template <bool MASK>
   __device__ __forceinline__ void weigh(float (&y)[NTI][NT][4], const float2 (&pv)[NTI][2]) {
 #pragma unroll
     for (int t = 0; t < NTI; ++t)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const float zc = fmaf(8.f, pv[t][h].x, pv[t][h].y), vw = pv[t][h].x * vinv;
+        const float zc = fmaf(8.f, pv[t][h].x, pv[t][h].y);
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -534,7 +543,7 @@ struct Kv4State {
             // A masked position weighs nothing, whatever its parameters hold.
             const bool out = MASK && x == -INFINITY;
             zs[n][j] = out ? zs[n][j] : fmaf(p, zc, zs[n][j]);
-            y[t][n][2 * h + j] = out ? 0.f : p * vw;
+            y[t][n][2 * h + j] = out ? 0.f : p * pv[t][h].x;
           }
       }
   }
@@ -606,8 +615,10 @@ struct Kv4State {
   }
 
   // The unit's sums: its row i at rows + i * stride, over the row's weight sum,
-  // and stat(i, reference, weight sum); or, by_column, all columns' sums as
-  // they are, and stat by column.
+  // and stat(i, reference, weight sum); or, by_column, all columns' sums, and stat
+  // by column.  What leaves the warp is relative to a reference that brings the
+  // weight sum to [1, 2): those of other warps and partitions may lie far apart,
+  // as their value scales do.
   template <class Stat>
   __device__ __forceinline__ void finish(float* rows, size_t stride, int nh, bool by_column, Stat stat, int lane) {
     const int r = lane >> 2, c = lane & 3;
@@ -623,10 +634,12 @@ struct Kv4State {
         }
         const int col = 8 * n + 2 * c + j, row = by_column ? col : row_of(col, nh);
         if (!by_column && !has_row(col, nh)) continue;
-        if (r == 0) stat(row, has_ref(n, j) ? ms[n][j] : -INFINITY, ls);
-        // (A NaN sum stays NaN: only an empty row divides by nothing.)
-        const float f = by_column ? 1.f : ls == 0.f ? 0.f : 1.f / ls;
-        const float vbf = vb * f, zf = zz * f;
+        // (A NaN or infinite sum stays what it is; only an empty row divides by nothing.)
+        const int e = ls > 0.f && ls < INFINITY ? (int)(__float_as_uint(ls) >> 23) - 127 : 0;
+        const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+        if (r == 0) stat(row, has_ref(n, j) ? ms[n][j] + (float)e : -INFINITY, ls * down);
+        const float f = by_column ? down : ls == 0.f ? 0.f : 1.f / ls;
+        const float zf = zz * f;
         float* o = rows + row * stride;
         // Tiles of odd nibbles carry 2^-20 instead of 2^-24.
         const float e8 = acc8[n][j], e16 = 16.f * e8;
@@ -640,10 +653,10 @@ struct Kv4State {
               const int d = VW == 2 ? 16 * r + 8 * h + 4 * q : 8 * r + 4 * h;
               const int mt = sl * K::MTS + 4 * q;
               float4 v;
-              v.x = fmaf((acc[mt][n][2 * h + j] - e8) * 131072.f, vbf, zf);
-              v.y = fmaf((acc[mt + 1][n][2 * h + j] - e16) * 8192.f, vbf, zf);
-              v.z = fmaf((acc[mt + 2][n][2 * h + j] - e8) * 131072.f, vbf, zf);
-              v.w = fmaf((acc[mt + 3][n][2 * h + j] - e16) * 8192.f, vbf, zf);
+              v.x = fmaf((acc[mt][n][2 * h + j] - e8) * 16777216.f, f, zf);
+              v.y = fmaf((acc[mt + 1][n][2 * h + j] - e16) * 1048576.f, f, zf);
+              v.z = fmaf((acc[mt + 2][n][2 * h + j] - e8) * 16777216.f, f, zf);
+              v.w = fmaf((acc[mt + 3][n][2 * h + j] - e16) * 1048576.f, f, zf);
               if (d < K::X) *reinterpret_cast<float4*>(o + sl * K::X + d) = v;
             }
       }

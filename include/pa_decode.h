@@ -301,9 +301,12 @@ size_t pa_kv4_block_bytes(int head_size, int block_size);
  * products).  lse may be NULL.  dtype PA_DTYPE_FP16 or PA_DTYPE_BF16
  * (PA_ERR_UNSUPPORTED for fp32); head sizes, block sizes, partitions, the
  * workspace (pa_decode_v2_workspace_bytes), ownership and errors are those of
- * pa_decode_v2; but the m_p left in the workspace may lie below the
- * partition's maximum, by up to 8 ln 2, l_p and o_p being relative to it.
- * |scale * query| is expected below 2^100.
+ * pa_decode_v2; but the m_p left in the workspace is not the partition's
+ * maximum: it lies near the log of its sum, l_p between 1 and 16.
+ * Value scales may differ by any factor: a token's precision depends on what it
+ * adds to a row, not on other tokens' scales.  For full precision |scale * query|
+ * is expected below 2^100, and in bf16 caches value scales of 2^-50 or more (or
+ * 0) and value zeros below 2^64.
  */
 int pa_decode_v2_kv4(void* out, float* lse, const void* query, const void* kv_cache,
                      const int32_t* block_tables, const int32_t* seq_lens, float scale, int num_seqs,
