@@ -22,7 +22,7 @@
 //
 // Roundings below 32 bits, besides the codes: the query is scaled by a power
 // of two into fp16's range (exact, except for elements more than 2^24 below
-// the unit's largest), and the weights p_t vs_t enter the value product as
+// the unit's largest finite one), and the weights p_t vs_t enter the value product as
 // fp16.  A weight's rounding error meets the code, whose mean is far from
 // zero; it is kept to the spread of the codes (c - 8) by summing the rounded
 // weights themselves (one more product, with rows of code 8) and putting
@@ -84,6 +84,8 @@
 //     so they come from L2 (68 us with ten reloads a stage; 10 and 12 warps of
 //     168 registers, 13 a tile, 115 and 90).
 #pragma once
+
+#include <type_traits>
 
 #include "pa_common.cuh"
 #include "pa_kernel.cuh"
@@ -297,23 +299,34 @@ struct Kv4State {
         }
     }
   }
-  __device__ __forceinline__ void begin_unit(const Rows& q, float sl2) {
-    // The largest |q|, as 16-bit patterns (ordered as the values are).
+  // The unit's largest |q| (FINITE: of its finite elements) as a pattern.
+  static constexpr uint32_t kInf16 = std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u;
+  template <bool FINITE>
+  __device__ __forceinline__ static uint32_t largest(const Rows& q) {
     uint32_t top = 0;
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int i = 0; i < NSLAB * KW; ++i) {
-        top = __vmaxu2(top, q.v[t][i].x & 0x7fff7fffu);
-        top = __vmaxu2(top, q.v[t][i].y & 0x7fff7fffu);
-        top = __vmaxu2(top, q.v[t][i].z & 0x7fff7fffu);
-        top = __vmaxu2(top, q.v[t][i].w & 0x7fff7fffu);
+        const uint32_t w[4] = {q.v[t][i].x, q.v[t][i].y, q.v[t][i].z, q.v[t][i].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t a = w[k] & 0x7fff7fffu;
+          top = __vmaxu2(top, FINITE ? a & __vcmpltu2(a, kInf16 * 0x10001u) : a);
+        }
       }
-    top = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
-    // 2^s brings the unit's largest |q| below 2^15; zero, subnormal, Inf or
-    // NaN leave the query unscaled.
+    return __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
+  }
+  __device__ __forceinline__ void begin_unit(const Rows& q, float sl2) {
+    // The largest |q|, as 16-bit patterns (ordered as the values are); where a
+    // row holds infinities or NaN (patterns from kInf16 on), the largest finite
+    // one: the scale is the other rows' too.
+    uint32_t top = largest<false>(q);
+    if (top >= kInf16) top = largest<true>(q);
+    // 2^s brings the unit's largest |q| below 2^15; zero or subnormal leave the
+    // query unscaled.
     const int E = (__float_as_int(F16Traits<T>::to_float2(top).x) >> 23) & 0xff;
-    const int s = (E == 0 || E == 255) ? 0 : max(-113, min(110, 141 - E));
+    const int s = E == 0 ? 0 : max(-113, min(110, 141 - E));
     const float up = __int_as_float((127 + s) << 23), up16 = up * 0.0625f;
     kf = sl2 * __int_as_float((127 - s) << 23) * 16777216.f;
 #pragma unroll

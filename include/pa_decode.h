@@ -305,8 +305,10 @@ size_t pa_kv4_block_bytes(int head_size, int block_size);
  * maximum: it lies near the log of its sum, l_p between 1 and 16.
  * Value scales may differ by any factor: a token's precision depends on what it
  * adds to a row, not on other tokens' scales.  For full precision |scale * query|
- * is expected below 2^100, and in bf16 caches value scales of 2^-50 or more (or
- * 0) and value zeros below 2^64.
+ * is expected below 2^100, the largest elements of the query rows of a kv head
+ * and its neighbour within 2^16 of one another, and in bf16 caches value scales
+ * of 2^-50 or more (or 0) and value zeros below 2^64.  A query row with an
+ * infinity or NaN leaves the other rows' results alone.
  */
 int pa_decode_v2_kv4(void* out, float* lse, const void* query, const void* kv_cache,
                      const int32_t* block_tables, const int32_t* seq_lens, float scale, int num_seqs,

@@ -1,5 +1,6 @@
 """Decode over 4-bit caches whose value scales differ by many orders of
-magnitude: what one token holds leaves the others' precision alone.
+magnitude, or whose query has infinities and NaN: what one token or row holds
+leaves the others' results alone.
 
 Bound of an output element o = sum P_t v_t (P the softmax): half a step of the
 type, |o| u; the weights P_t vs_t go through fp16, which multiplies the code's
@@ -193,3 +194,20 @@ def test_scores_that_rise_by_hundreds(form, dtype):
             par[b, :, o, 0] = 0.01
             par[b, :, o, 1] = pos // 5 * 0.5  # scores of about 0.09 * 0.8 D * that
     check(q, cache, bt, L, 0.09, 1024, [0, 1, 2])
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("mag,dtype", [(1.0, F16), (1.0, BF16), (1e7, BF16), (1e-8, BF16), (2e-5, F16)])
+@pytest.mark.parametrize("form", FORMS[:4], ids=str)
+def test_a_row_of_infinities_or_nan_leaves_the_others(form, mag, dtype, bad):
+    """Query rows that hold one: NaN; every other row of the sequence keeps its bits."""
+    q, cache, bt, L = case(form, dtype)
+    q = (q.float() * mag).to(dtype)
+    q[:, ..., 1, 5] = 0
+    base, lse = run(q, cache, bt, L, 0.09 / mag, 64)
+    check(q, cache, bt, L, 0.09 / mag, 64)
+    q[:, ..., 1, 5] = bad
+    out, lse2 = run(q, cache, bt, L, 0.09 / mag, 64)
+    keep = [h for h in range(form[1]) if h != 1]
+    assert torch.equal(out[..., keep, :], base[..., keep, :]) and torch.equal(lse[..., keep], lse2[..., keep])
+    if math.isnan(bad):
+        assert bool(out[..., 1, :].isnan().all())
