@@ -190,6 +190,26 @@ def _stream_handle(stream, like: torch.Tensor | None = None) -> int | None:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _new_workspace(nbytes: int, device: int, stream) -> torch.Tensor:
+    """A workspace for a call on ``stream`` (None: the current one), allocated
+    there: PyTorch's allocator gives memory that was dropped to later work of the
+    stream that it was allocated on, which has to be the call's."""
+    def empty():
+        return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=torch.device("cuda", device))
+
+    if stream is None:
+        return empty()
+    handle = _stream_handle(stream)
+    current = _raw_stream(device) if _raw_stream is not None else torch.cuda.current_stream(device).cuda_stream
+    if handle == current:
+        return empty()
+    if not isinstance(stream, torch.cuda.Stream):
+        # (1 names the legacy default stream, as 0 does.)
+        stream = torch.cuda.ExternalStream(0 if handle == 1 else handle, device=torch.device("cuda", device))
+    with torch.cuda.stream(stream):
+        return empty()
+
+
 def _check_tensor(name, t, dtype=None, ndim=None):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -236,8 +256,7 @@ def pa_decode_v2(out, query, key_cache, value_cache, block_tables, seq_lens, sca
         raise ValueError("block_tables / seq_lens must have num_seqs rows")
     MB = block_tables.shape[1]
     if workspace is None:  # (a caller's workspace is checked by the library: PA_ERR_WORKSPACE)
-        workspace = torch.empty(max(workspace_bytes(S, H, KH, D, MB, BS, partition_size), 256), dtype=torch.uint8,
-                                device=query.device)
+        workspace = _new_workspace(workspace_bytes(S, H, KH, D, MB, BS, partition_size), query.get_device(), stream)
     _check_tensor("workspace", workspace, torch.uint8)
     if lse is not None:
         _check_tensor("lse", lse, torch.float32, 2)
@@ -293,8 +312,8 @@ def pa_decode_v2_mq(out, query, key_cache, value_cache, block_tables, seq_lens, 
             raise ValueError("lse must be [num_seqs, q_len, num_heads]")
     MB = block_tables.shape[1]
     if workspace is None:  # (a caller's workspace is checked by the library: PA_ERR_WORKSPACE)
-        workspace = torch.empty(max(workspace_bytes(S * QL, H, KH, D, MB, BS, partition_size), 256), dtype=torch.uint8,
-                                device=query.device)
+        workspace = _new_workspace(workspace_bytes(S * QL, H, KH, D, MB, BS, partition_size), query.get_device(),
+                                   stream)
     _check_tensor("workspace", workspace, torch.uint8)
     st = lib().pa_decode_v2_mq(
         _ptr(out), _ptr(lse), _ptr(query), _ptr(key_cache), _ptr(value_cache), _ptr(block_tables),
@@ -349,8 +368,7 @@ def pa_decode_v2_fp8(out, query, key_cache, value_cache, block_tables, seq_lens,
             raise ValueError("lse must be [num_seqs, num_heads]")
     MB = block_tables.shape[1]
     if workspace is None:  # (a caller's workspace is checked by the library: PA_ERR_WORKSPACE)
-        workspace = torch.empty(max(workspace_bytes(S, H, KH, D, MB, BS, partition_size), 256), dtype=torch.uint8,
-                                device=query.device)
+        workspace = _new_workspace(workspace_bytes(S, H, KH, D, MB, BS, partition_size), query.get_device(), stream)
     _check_tensor("workspace", workspace, torch.uint8)
     st = lib().pa_decode_v2_fp8(
         _ptr(out), _ptr(lse), _ptr(query), _ptr(key_cache), _ptr(value_cache), _ptr(block_tables),
@@ -393,8 +411,8 @@ def pa_decode_v2_mq_fp8(out, query, key_cache, value_cache, block_tables, seq_le
             raise ValueError("lse must be [num_seqs, q_len, num_heads]")
     MB = block_tables.shape[1]
     if workspace is None:  # (a caller's workspace is checked by the library: PA_ERR_WORKSPACE)
-        workspace = torch.empty(max(workspace_bytes(S * QL, H, KH, D, MB, BS, partition_size), 256), dtype=torch.uint8,
-                                device=query.device)
+        workspace = _new_workspace(workspace_bytes(S * QL, H, KH, D, MB, BS, partition_size), query.get_device(),
+                                   stream)
     _check_tensor("workspace", workspace, torch.uint8)
     st = lib().pa_decode_v2_mq_fp8(
         _ptr(out), _ptr(lse), _ptr(query), _ptr(key_cache), _ptr(value_cache), _ptr(block_tables),
@@ -442,7 +460,8 @@ def _decode_kv4(name, out, query, kv_cache, block_tables, seq_lens, scale, parti
         _need("lse", lse, torch.float32, ndim - 1, dev)
         if lse.shape != shape[:-1]:
             raise ValueError("lse must be query's shape without the head size")
-    workspace = _need_workspace(workspace, dev, lambda: workspace_bytes(S * QL, H, KH, D, MB, BS, partition_size))
+    workspace = _need_workspace(workspace, dev, lambda: workspace_bytes(S * QL, H, KH, D, MB, BS, partition_size),
+                                stream)
     with _current(dev):
         st = lib().pa_decode_v2_mq_kv4(
             out.data_ptr(), _ptr(lse), query.data_ptr(), kv_cache.data_ptr(), block_tables.data_ptr(),
@@ -496,10 +515,10 @@ def _need(name, t, dtype, ndim, device):
         raise ValueError(f"{name} must be on cuda:{device}, got {t.device}")
 
 
-def _need_workspace(workspace, device, nbytes):
+def _need_workspace(workspace, device, nbytes, stream):
     """The caller's workspace, checked (its size by the library), or a new one."""
     if workspace is None:
-        return torch.empty(max(nbytes(), 256), dtype=torch.uint8, device=torch.device("cuda", device))
+        return _new_workspace(nbytes(), device, stream)
     _check_tensor("workspace", workspace, torch.uint8)
     if workspace.get_device() != device:
         raise ValueError(f"workspace must be on cuda:{device}, got {workspace.device}")
@@ -552,7 +571,7 @@ def _kv4_tokens(name, fn, first, kv_cache, key, value, block_tables, seq_lens, c
         if cu_tokens.shape[0] != S + 1:
             raise ValueError("cu_tokens must have num_seqs + 1 entries")
         cu = cu_tokens.data_ptr()
-    workspace = _need_workspace(workspace, dev, lambda: 256)
+    workspace = _need_workspace(workspace, dev, lambda: 256, stream)
     c, k, v = kv_cache.data_ptr(), key.data_ptr(), value.data_ptr()
     args = (c, k, v) if first else (k, v, c)
     with _current(dev):
@@ -589,7 +608,7 @@ def pages_workspace_bytes(num_rows: int, max_blocks_per_seq: int, num_blocks: in
     return int(lib().pa_pages_workspace_bytes(int(num_rows), int(max_blocks_per_seq), int(num_blocks)))
 
 
-def _pages_args(refcounts, caches, rows, MB, workspace):
+def _pages_args(refcounts, caches, rows, MB, workspace, stream):
     """(cache pointers, page bytes, count, workspace) after the checks all pages calls share."""
     NB, dev = refcounts.shape[0], refcounts.get_device()
     if NB == 0:
@@ -606,7 +625,7 @@ def _pages_args(refcounts, caches, rows, MB, workspace):
         ptrs.append(c.data_ptr())
         sizes.append(c.numel() * c.element_size() // NB)
     # (Arrays of 64-bit words, passed by address: a third of ctypes arrays' cost.)
-    workspace = _need_workspace(workspace, dev, lambda: pages_workspace_bytes(rows, MB, NB))
+    workspace = _need_workspace(workspace, dev, lambda: pages_workspace_bytes(rows, MB, NB), stream)
     return array.array("Q", ptrs), array.array("Q", sizes), len(ptrs), workspace
 
 
@@ -628,7 +647,7 @@ def pa_pages_fork(block_tables_out, seq_lens_out, block_tables, seq_lens, parent
     (S, MB), n = block_tables.shape, parents.shape[0]
     if tuple(block_tables_out.shape) != (n, MB) or seq_lens_out.shape[0] != n or seq_lens.shape[0] != S:
         raise ValueError("inconsistent table / length / parents shapes")
-    ptrs, sizes, nc, workspace = _pages_args(refcounts, caches, n, MB, workspace)
+    ptrs, sizes, nc, workspace = _pages_args(refcounts, caches, n, MB, workspace, stream)
     with _current(dev):
         st = lib().pa_pages_fork(
             _ptr(block_tables_out), _ptr(seq_lens_out), _ptr(block_tables), _ptr(seq_lens), _ptr(parents),
@@ -653,7 +672,7 @@ def pa_pages_resize(block_tables, seq_lens, new_lens, refcounts, caches, block_s
     S, MB = block_tables.shape
     if seq_lens.shape[0] != S or new_lens.shape[0] != S:
         raise ValueError("block_tables / seq_lens / new_lens must have num_seqs rows")
-    ptrs, sizes, nc, workspace = _pages_args(refcounts, caches, S, MB, workspace)
+    ptrs, sizes, nc, workspace = _pages_args(refcounts, caches, S, MB, workspace, stream)
     with _current(dev):
         st = lib().pa_pages_resize(
             _ptr(block_tables), _ptr(seq_lens), _ptr(new_lens), _ptr(refcounts), ptrs.buffer_info()[0],
@@ -682,7 +701,7 @@ def pa_pages_compact(block_tables, seq_lens, refcounts, caches, block_size: int,
         _need("new_ids", new_ids, torch.int32, 1, dev)
         if new_ids.shape != refcounts.shape:
             raise ValueError("new_ids must have num_blocks entries")
-    ptrs, sizes, nc, workspace = _pages_args(refcounts, caches, S, MB, workspace)
+    ptrs, sizes, nc, workspace = _pages_args(refcounts, caches, S, MB, workspace, stream)
     with _current(dev):
         st = lib().pa_pages_compact(
             _ptr(block_tables), _ptr(seq_lens), _ptr(refcounts), _ptr(new_ids), ptrs.buffer_info()[0],
