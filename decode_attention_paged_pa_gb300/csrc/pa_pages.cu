@@ -501,9 +501,42 @@ bool pages_layout(int rows, int MB, int NB, PagesLayout* l) {
   return true;
 }
 
-bool overlap(const void* a, size_t na, const void* b, size_t nb) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return x < y + nb && y < x + na;
+struct Span {
+  const void* p;
+  size_t n;      // bytes
+  bool written;  // by the call
+};
+bool overlap(const Span& a, const Span& b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  return a.n > 0 && b.n > 0 && x < y + b.n && y < x + a.n;
+}
+
+// Whether something that the call writes lies in another of its arrays.  The
+// plan is checked, and applied by a second launch that reads the lengths,
+// parents and tables again: they must not change in between.
+template <int MODE>
+bool written_overlaps(const PagesParams& p, void* const* caches, const size_t* page_bytes, int num_caches,
+                      const void* workspace, size_t workspace_bytes) {
+  const size_t row = (size_t)p.MB * 4, S = (size_t)p.S, rows = (size_t)p.rows, NB = (size_t)p.NB;
+  const Span spans[] = {{p.bt, S * row, MODE != kFork},
+                        {p.lens, S * 4, MODE == kResize},
+                        {p.arg, MODE == kCompact ? 0 : rows * 4, false},
+                        {p.bt_out, MODE == kFork ? rows * row : 0, true},
+                        {p.lens_out, MODE == kFork ? rows * 4 : 0, true},
+                        {p.refs, NB * 4, true},
+                        {p.new_ids, p.new_ids ? NB * 4 : 0, true},
+                        {workspace, workspace_bytes, true}};
+  constexpr int n = sizeof spans / sizeof spans[0];
+  for (int i = 0; i < n; ++i)
+    for (int j = 0; j < i; ++j) {
+      // (New lengths that are the lengths: every row keeps its own, and is written as it is.)
+      if (MODE == kResize && i == 2 && j == 1 && p.arg == p.lens) continue;
+      if ((spans[i].written || spans[j].written) && overlap(spans[i], spans[j])) return true;
+    }
+  for (int k = 0; k < num_caches; ++k)
+    for (int i = 0; i < n; ++i)
+      if (overlap(Span{caches[k], NB * page_bytes[k], true}, spans[i])) return true;
+  return false;
 }
 
 template <int MODE>
@@ -517,10 +550,6 @@ int pages_impl(PagesParams p, void* const* caches, const size_t* page_bytes, int
   if (MODE != kCompact && p.rows > 0 && (!p.arg || !aligned(p.arg, 4))) return PA_ERR_INVALID_ARG;
   if (MODE == kFork && p.rows > 0) {
     if (!p.bt_out || !p.lens_out || !aligned(p.bt_out, 4) || !aligned(p.lens_out, 4)) return PA_ERR_INVALID_ARG;
-    const size_t row = (size_t)p.MB * 4;
-    if (p.S > 0 && (overlap(p.bt, p.S * row, p.bt_out, p.rows * row) ||
-                    overlap(p.lens, (size_t)p.S * 4, p.lens_out, (size_t)p.rows * 4)))
-      return PA_ERR_INVALID_ARG;
   }
   if (num_caches > 0 && (!caches || !page_bytes)) return PA_ERR_INVALID_ARG;
   for (int i = 0; i < num_caches; ++i)
@@ -531,6 +560,7 @@ int pages_impl(PagesParams p, void* const* caches, const size_t* page_bytes, int
   if (!pages_layout(p.rows, p.MB, p.NB, &l)) return PA_ERR_INVALID_ARG;
   if (!workspace || !aligned(workspace, 16)) return PA_ERR_INVALID_ARG;
   if (workspace_bytes < l.total) return PA_ERR_WORKSPACE;
+  if (written_overlaps<MODE>(p, caches, page_bytes, num_caches, workspace, l.total)) return PA_ERR_INVALID_ARG;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.hdr = reinterpret_cast<int*>(ws);
   p.row_old = reinterpret_cast<int*>(ws + l.old);

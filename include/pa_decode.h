@@ -400,7 +400,9 @@ int pa_kv4_gather(void* key_out, void* value_out, const void* kv_cache, const in
  *                required; holds the status (pa_decode_v2_device_status)
  * Calls enqueue two launches on `stream` (one more per further 128 caches),
  * never synchronise and can be captured into a CUDA graph.  The arrays caches
- * and page_bytes are read before the call returns.  Calls on one pool must be
+ * and page_bytes are read before the call returns.  No array that a call writes
+ * may overlap another of its arrays (PA_ERR_INVALID_ARG; the new lengths of a
+ * resize may be the lengths themselves).  Calls on one pool must be
  * ordered on one stream, also with those that read its tables and caches.
  *
  * Errors on the device: a call that needs more blocks than are free records
@@ -420,7 +422,7 @@ size_t pa_pages_workspace_bytes(int num_rows, int max_blocks_per_seq, int num_bl
  * parents keep theirs.  Table entries past the child's blocks keep what they
  * held.
  *   block_tables_out [num_children, max_blocks_per_seq], seq_lens_out
- *                [num_children]: written, must not overlap the inputs
+ *                [num_children]: written
  *   block_tables [num_seqs, max_blocks_per_seq], seq_lens [num_seqs]
  *   parents      [num_children] int32 in [0, num_seqs), in any order, with
  *                repeats; -1 makes an empty row

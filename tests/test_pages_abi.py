@@ -68,3 +68,34 @@ def test_rejects_of_one_call(fn, kw):
 
 def test_status_string_of_a_full_pool():
     assert "free blocks" in binding.status_string(binding.PA_ERR_NO_BLOCKS)
+
+
+# Arrays that lie apart: two rows of four blocks, three children, a pool of eight blocks.
+APART = dict(bt=FAKE, lens=FAKE * 2, arg=FAKE * 3, out=FAKE * 4, lo=FAKE * 5, refs=FAKE * 6, caches=[FAKE * 7],
+             ws=FAKE * 8)
+SIZE = dict(bt=32, lens=8, arg=8, out=48, lo=12, refs=32, ids=32, caches=8 * 1024, ws=binding.pages_workspace_bytes(2, 4, 8))
+
+
+@pytest.mark.parametrize("fn,written,other", [
+    # The children's rows and lengths, over what the call reads and over one another.
+    *[("pa_pages_fork", w, o) for w in ("out", "lo") for o in ("bt", "lens", "arg", "refs", "caches", "ws")],
+    ("pa_pages_fork", "out", "lo"),
+    ("pa_pages_fork", "refs", "bt"), ("pa_pages_fork", "refs", "arg"), ("pa_pages_fork", "ws", "arg"),
+    # The tables and lengths in place; new lengths that overlap the lengths in part.
+    *[("pa_pages_resize", w, o) for w in ("bt", "lens", "refs", "ws") for o in ("arg", "caches")],
+    ("pa_pages_resize", "bt", "lens"), ("pa_pages_resize", "bt", "refs"), ("pa_pages_resize", "lens", "refs"),
+    *[("pa_pages_compact", w, o) for w in ("bt", "refs", "ids") for o in ("lens", "caches", "ws")],
+    ("pa_pages_compact", "ids", "refs"), ("pa_pages_compact", "ids", "bt"),
+])
+@pytest.mark.parametrize("end", ["first", "last"])
+def test_rejects_what_is_written_over_another_array(fn, written, other, end):
+    """`other` begins at the last word of `written`, or ends at its first one."""
+    a = dict(APART)
+    base = FAKE * 32
+    off = SIZE[written] - 4 if end == "last" else 4 - SIZE[other]
+    if other in ("ws", "caches") or written in ("ws", "caches"):
+        off = off // 16 * 16 if end == "last" else -(-off // 16) * 16
+        off = off if end == "last" else min(off, 0)
+    a[written] = [base] if written == "caches" else base
+    a[other] = [base + off] if other == "caches" else base + off
+    assert call(fn, **a) == BAD

@@ -341,3 +341,20 @@ def test_refusals():
     with pytest.raises(binding.PaError):
         binding.pa_pages_compact(tables, ld, refs, caches, 0)
     p.equals(tables, ld, refs, caches)
+
+
+def test_new_lengths_that_are_the_lengths():
+    """A resize to the lengths themselves (the same array) changes nothing."""
+    p = Pool(10, [30, 20, 0, 64], 4, 40, 16)
+    tables, ld, refs, caches = p.on_gpu()
+    status(binding.pa_pages_resize(tables, ld, ld, refs, caches, 16))
+    assert p.resize(list(p.lens))
+    p.equals(tables, ld, refs, caches)
+    with pytest.raises(binding.PaError):  # an array that is the lengths' but for the first
+        both = i32([30, 20, 0, 64, 64])
+        binding.pa_pages_resize(tables, both[:4], both[1:], refs, caches, 16)
+    with pytest.raises(binding.PaError):  # parents in the array that takes the children's lengths
+        out = torch.zeros((4, 4), dtype=torch.int32, device="cuda")
+        par = i32([0, 1, 2, 3])
+        binding.pa_pages_fork(out, par, tables, ld, par, refs, caches, 16)
+    p.equals(tables, ld, refs, caches)
