@@ -50,6 +50,7 @@ EXPORTED_SYMBOLS = (
     "pa_decode_v2_mq_fp8",
     "pa_decode_v2_kv4",
     "pa_decode_v2_mq_kv4",
+    "pa_decode_v2_kv4_ex",
     "pa_kv4_append",
     "pa_kv4_gather",
     "pa_kv4_block_bytes",
@@ -108,6 +109,8 @@ def _declare(lib):
     lib.pa_decode_v2_kv4.restype = ci
     lib.pa_decode_v2_mq_kv4.argtypes = [vp] * 6 + base[6:8] + [ci] + base[8:]
     lib.pa_decode_v2_mq_kv4.restype = ci
+    lib.pa_decode_v2_kv4_ex.argtypes = lib.pa_decode_v2_mq_kv4.argtypes + [ci, cll]
+    lib.pa_decode_v2_kv4_ex.restype = ci
     for fn in (lib.pa_kv4_append, lib.pa_kv4_gather):
         fn.argtypes = [vp] * 6 + [ci] * 5 + [cll, cll, ci, vp, ci, ci, vp, cs]
         fn.restype = ci
@@ -438,7 +441,8 @@ def _kv4_shape(kv_cache, D, device):
     return NB, KH, rec // (D + 8)
 
 
-def _decode_kv4(name, out, query, kv_cache, block_tables, seq_lens, scale, partition_size, workspace, stream, lse):
+def _decode_kv4(name, out, query, kv_cache, block_tables, seq_lens, scale, partition_size, workspace, stream, lse,
+                max_ctas, timeout_ns):
     ndim = query.dim()  # [S, H, D] or [S, q_len, H, D]
     dt = query.dtype
     if dt not in _DTYPE_CODE:
@@ -463,35 +467,39 @@ def _decode_kv4(name, out, query, kv_cache, block_tables, seq_lens, scale, parti
     workspace = _need_workspace(workspace, dev, lambda: workspace_bytes(S * QL, H, KH, D, MB, BS, partition_size),
                                 stream)
     with _current(dev):
-        st = lib().pa_decode_v2_mq_kv4(
+        st = lib().pa_decode_v2_kv4_ex(
             out.data_ptr(), _ptr(lse), query.data_ptr(), kv_cache.data_ptr(), block_tables.data_ptr(),
             seq_lens.data_ptr(), float(scale), S, QL, H, KH, D, BS, int(partition_size), _DTYPE_CODE[dt],
-            _stream_handle(stream, query), MB, NB, workspace.data_ptr(), workspace.numel())
+            _stream_handle(stream, query), MB, NB, workspace.data_ptr(), workspace.numel(), int(max_ctas),
+            int(timeout_ns))
     if st != PA_OK:
         raise PaError(st, name)
     return workspace
 
 
 def pa_decode_v2_kv4(out, query, kv_cache, block_tables, seq_lens, scale: float, partition_size: int = 512,
-                     workspace: torch.Tensor | None = None, stream=None, lse: torch.Tensor | None = None):
+                     workspace: torch.Tensor | None = None, stream=None, lse: torch.Tensor | None = None,
+                     max_ctas: int = 0, timeout_ns: int = 0):
     """Decode over a cache held in 4 bits (see include/pa_decode.h): query/out
     [S, H, D] fp16 or bf16; kv_cache uint8 [NB, KH, BS * (D + 8)] as
-    :func:`pa_kv4_append` writes it.  ``lse`` (float32 [S, H]) is optional.
+    :func:`pa_kv4_append` writes it.  ``lse`` (float32 [S, H]) is optional;
+    ``max_ctas`` and ``timeout_ns`` are the controls of ``pa_decode_v2_kv4_ex``.
     Returns the workspace used."""
     _check_tensor("query", query, ndim=3)
     return _decode_kv4("pa_decode_v2_kv4", out, query, kv_cache, block_tables, seq_lens, scale, partition_size,
-                       workspace, stream, lse)
+                       workspace, stream, lse, max_ctas, timeout_ns)
 
 
 def pa_decode_v2_mq_kv4(out, query, kv_cache, block_tables, seq_lens, scale: float, partition_size: int = 512,
-                        workspace: torch.Tensor | None = None, stream=None, lse: torch.Tensor | None = None):
+                        workspace: torch.Tensor | None = None, stream=None, lse: torch.Tensor | None = None,
+                        max_ctas: int = 0, timeout_ns: int = 0):
     """Multi-query decode over a cache held in 4 bits: query/out
     [S, q_len, H, D], rows causal as for :func:`pa_decode_v2_mq`, the cache of
     :func:`pa_decode_v2_kv4`.  ``lse`` (float32 [S, q_len, H]) is optional.
     Returns the workspace used."""
     _check_tensor("query", query, ndim=4)
     return _decode_kv4("pa_decode_v2_mq_kv4", out, query, kv_cache, block_tables, seq_lens, scale, partition_size,
-                       workspace, stream, lse)
+                       workspace, stream, lse, max_ctas, timeout_ns)
 
 
 _no_switch = contextlib.nullcontext()

@@ -443,10 +443,21 @@ extern "C" int pa_decode_v2_mq_kv4(void* out, float* lse, const void* query, con
                                    int block_size, int partition_size, int dtype, void* stream,
                                    int max_blocks_per_seq, int num_blocks, void* workspace,
                                    size_t workspace_bytes) {
+  return pa_decode_v2_kv4_ex(out, lse, query, kv_cache, block_tables, seq_lens, scale, num_seqs, q_len, num_heads,
+                             num_kv_heads, head_size, block_size, partition_size, dtype, stream,
+                             max_blocks_per_seq, num_blocks, workspace, workspace_bytes, 0, 0);
+}
+
+extern "C" int pa_decode_v2_kv4_ex(void* out, float* lse, const void* query, const void* kv_cache,
+                                   const int32_t* block_tables, const int32_t* seq_lens, float scale,
+                                   int num_seqs, int q_len, int num_heads, int num_kv_heads, int head_size,
+                                   int block_size, int partition_size, int dtype, void* stream,
+                                   int max_blocks_per_seq, int num_blocks, void* workspace,
+                                   size_t workspace_bytes, int max_ctas, long long timeout_ns) {
   return decode_impl(out, lse, query, kv_cache, kv_cache, block_tables, seq_lens, scale, num_seqs, q_len,
                      num_heads, num_kv_heads, head_size, block_size, partition_size, dtype, stream,
-                     max_blocks_per_seq, num_blocks, workspace, workspace_bytes, PA_VARIANT_AUTO, 0, 0, false,
-                     1.f, 1.f, true);
+                     max_blocks_per_seq, num_blocks, workspace, workspace_bytes, PA_VARIANT_AUTO, max_ctas,
+                     timeout_ns, false, 1.f, 1.f, true);
 }
 
 extern "C" int pa_decode_v2_ex(void* out, const void* query, const void* key_cache,

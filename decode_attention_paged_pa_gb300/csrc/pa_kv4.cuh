@@ -770,9 +770,26 @@ __device__ __forceinline__ void kv4_sentinels(const KParams& prm, const int* len
 }
 
 // (Out of line: a wait that does not succeed at once has time for a call.)
+// try_wait sleeps for longer than a copy takes, and the global timer ticks about
+// as seldom as copies land: a short limit is met by looking at the barrier and
+// the SM's clock (two cycles a nanosecond or so) in turn.
+constexpr long long kShortWaitNs = 1 << 20;
 static __device__ __noinline__ bool kv4_wait_slow(uint32_t bar, uint32_t parity, volatile int* abort_flag,
                                                   int* err_word, long long timeout_ns, int slot) {
-  return __all_sync(0xffffffffu, wait_bounded(bar, parity, abort_flag, err_word, timeout_ns, kSiteFull, slot));
+  bool ok = true;
+  if (timeout_ns >= kShortWaitNs) {
+    ok = wait_bounded(bar, parity, abort_flag, err_word, timeout_ns, kSiteFull, slot);
+  } else {
+    const long long t0 = clock64();
+    while (ok && !mbar_test_wait(bar, parity)) {
+      ok = !*abort_flag;
+      if (ok && clock64() - t0 > 2 * timeout_ns) {
+        record_timeout(abort_flag, err_word, kSiteFull, slot);
+        ok = false;
+      }
+    }
+  }
+  return __all_sync(0xffffffffu, ok);
 }
 
 // A bulk copy into this CTA's own shared memory (bulk_copy_g2s names its
@@ -862,7 +879,7 @@ struct Kv4Stream {
   }
   // Waits for the next stage to land; false: gave up.
   __device__ __forceinline__ bool wait(volatile int* abort_flag) const {
-    if (__all_sync(0xffffffffu, mbar_try_wait(bar_out, ph_out))) return true;
+    if (__all_sync(0xffffffffu, mbar_test_wait(bar_out, ph_out))) return true;
     return kv4_wait_slow(bar_out, ph_out, abort_flag, prm.hdr + kHdrError, prm.timeout_ns, (int)(out / K::STAGE));
   }
   __device__ __forceinline__ void used() {

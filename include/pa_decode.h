@@ -327,6 +327,21 @@ int pa_decode_v2_mq_kv4(void* out, float* lse, const void* query, const void* kv
                         int num_blocks, void* workspace, size_t workspace_bytes);
 
 /*
+ * pa_decode_v2_mq_kv4 with the controls of pa_decode_v2_ex, for tests and
+ * measurement: max_ctas bounds the persistent grid (0 = one CTA per SM),
+ * timeout_ns every device-side wait (0 = 2^31 ns); a wait that runs out is
+ * recorded as PA_ERR_TIMEOUT.  The units left over at the end are shared by as
+ * many warps as the grid leaves to them, so outputs for two grids may differ by
+ * the roundings of fp32 sums (for one grid they are bitwise the same).
+ */
+int pa_decode_v2_kv4_ex(void* out, float* lse, const void* query, const void* kv_cache,
+                        const int32_t* block_tables, const int32_t* seq_lens, float scale, int num_seqs,
+                        int q_len, int num_heads, int num_kv_heads, int head_size, int block_size,
+                        int partition_size, int dtype, void* stream, int max_blocks_per_seq,
+                        int num_blocks, void* workspace, size_t workspace_bytes, int max_ctas,
+                        long long timeout_ns);
+
+/*
  * Writes new tokens into a 4-bit cache.  Sequence s has the rows
  * cu_tokens[s] .. cu_tokens[s+1] - 1 of key and value, and they are its last
  * cached tokens: with n of them, row cu_tokens[s] + i goes to position

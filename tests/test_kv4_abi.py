@@ -86,3 +86,16 @@ def tokens(fn, **kw):
 ])
 def test_tokens_rejects(fn, kw, status):
     assert tokens(fn, **kw) == status
+
+
+@pytest.mark.parametrize("max_ctas,timeout_ns,kw,status", [
+    (-1, 0, {}, binding.PA_ERR_INVALID_ARG),
+    (0, -1, {}, binding.PA_ERR_INVALID_ARG),
+    (4, 1000, dict(S=0), binding.PA_OK),
+    (4, 1000, dict(n=1024), binding.PA_ERR_WORKSPACE),
+])
+def test_decode_ex_rejects(max_ctas, timeout_ns, kw, status):
+    a = dict(out=FAKE, lse=None, query=FAKE, cache=FAKE, bt=FAKE, lens=FAKE, scale=0.125, S=2, q_len=2, H=4, KH=2,
+             D=128, BS=16, P=512, dtype=0, stream=None, MB=4, NB=8, ws=FAKE, n=1 << 30)
+    a.update(kw)
+    assert binding.lib().pa_decode_v2_kv4_ex(*a.values(), max_ctas, timeout_ns) == status
