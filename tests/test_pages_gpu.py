@@ -358,3 +358,41 @@ def test_new_lengths_that_are_the_lengths():
         par = i32([0, 1, 2, 3])
         binding.pa_pages_fork(out, par, tables, ld, par, refs, caches, 16)
     p.equals(tables, ld, refs, caches)
+
+
+def test_an_unchanged_length_in_a_shared_block_gets_a_copy():
+    """Rows that end in a partly filled block that others hold: a copy each, at the same length
+    too; a row that ends on a block's edge, or holds its last block alone, is left as it is."""
+    p = Pool(11, [24, 24, 32, 24, 7], 4, 30, 16)
+    for s in (1, 3):  # rows 0, 1 and 3 hold the same two blocks
+        for j in range(2):
+            p.refs[int(p.tables[s, j])] -= 1
+            p.tables[s, j] = p.tables[0, j]
+            p.refs[int(p.tables[0, j])] += 1
+    tables, ld, refs, caches = p.on_gpu()
+    shared, before = int(p.tables[0, 1]), p.tables.clone()
+    status(binding.pa_pages_resize(tables, ld, i32([24, 24, 32, 24, 7]), refs, caches, 16))
+    assert p.resize([24, 24, 32, 24, 7])
+    p.equals(tables, ld, refs, caches)
+    last = [int(tables[s, 1]) for s in (0, 1, 3)]
+    assert len({shared, *last}) == 4 and refs[shared] == 0 and all(refs[b] == 1 for b in last)
+    assert all(torch.equal(c[shared], c[b]) for c in caches for b in last)
+    assert torch.equal(tables[2].cpu(), before[2]) and torch.equal(tables[4].cpu(), before[4])
+    # Now each holds its own: the same call again changes nothing.
+    status(binding.pa_pages_resize(tables, ld, i32([24, 24, 32, 24, 7]), refs, caches, 16))
+    p.equals(tables, ld, refs, caches)
+
+
+def test_every_holder_cut_back_needs_a_block_of_its_own():
+    """Two rows cut back into the block that they alone share: two copies, so a pool with one
+    free block refuses both at once and takes them one after the other."""
+    p = Pool(12, [32, 32], 3, 4, 16, share=2)
+    assert sum(x == 0 for x in p.refs) == 2
+    p.refs[[b for b in range(4) if p.refs[b] == 0][0]] = 1  # (someone else's)
+    tables, ld, refs, caches = p.on_gpu()
+    status(binding.pa_pages_resize(tables, ld, i32([20, 20]), refs, caches, 16), binding.PA_ERR_NO_BLOCKS)
+    p.equals(tables, ld, refs, caches)
+    for new in ([20, 32], [20, 20]):
+        status(binding.pa_pages_resize(tables, ld, i32(new), refs, caches, 16))
+        assert p.resize(new)
+        p.equals(tables, ld, refs, caches)
