@@ -362,8 +362,10 @@ int pa_decode_v2_kv4_ex(void* out, float* lse, const void* query, const void* kv
  *                cu_tokens[num_seqs] count for nothing.
  *   workspace    >= 256 bytes, 16-byte aligned, required; holds the status
  *                (pa_decode_v2_device_status), whatever it held before
- * A position of several sequences (a shared block) must not be written by two
- * of them.  A length below the sequence's row count or above the table's
+ * The lengths have to count the new tokens already: after a pa_pages_resize that
+ * was refused (PA_ERR_NO_BLOCKS) they do not, and the rows would go over cached
+ * tokens.  A position of several sequences (a shared block) must not be written
+ * by two of them.  A length below the sequence's row count or above the table's
  * capacity, offsets of a sequence that descend, start below 0 or pass
  * num_tokens, and block ids outside the pool are recorded as
  * PA_ERR_DEVICE_BOUNDS; all rows of such a sequence (of a bad block id: those
@@ -421,7 +423,10 @@ int pa_kv4_gather(void* key_out, void* value_out, const void* kv_cache, const in
  * ordered on one stream, also with those that read its tables and caches.
  *
  * Errors on the device: a call that needs more blocks than are free records
- * PA_ERR_NO_BLOCKS and changes nothing.  Rows with a parent, length or new
+ * PA_ERR_NO_BLOCKS and changes nothing.  What is enqueued behind it runs all the
+ * same: a pa_kv4_append finds the old lengths and writes its rows over each
+ * sequence's last tokens.  So the status is to be read before it, unless the host
+ * knows that enough blocks are free.  Rows with a parent, length or new
  * length out of range, or whose partly filled block has an id outside the
  * pool, are recorded as PA_ERR_DEVICE_BOUNDS and left as they were (a child
  * becomes an empty row); other ids outside the pool are recorded and counted
@@ -451,9 +456,12 @@ int pa_pages_fork(int32_t* block_tables_out, int32_t* seq_lens_out, const int32_
 /*
  * Resizes: sequence s gets room for new_lens[s] tokens, and seq_lens[s] becomes
  * new_lens[s].  A longer sequence takes blocks, a shorter one gives back those
- * past its new end, 0 frees it; the same length leaves it as it is.  Where the
- * last token kept lies in a partly filled block that other rows hold too
- * (a sequence cut back into a part it shares), the row gets a copy of it.
+ * past its new end, 0 frees it.  Where the last token kept lies in a partly
+ * filled block that other rows hold too (a sequence cut back into a part it
+ * shares, or that ends there already, whatever its new length), the row gets a
+ * copy of it.  So does every such row of a call: where they are all the holders,
+ * the block that they shared becomes free, and the call has needed one block more
+ * than they hold in the end.
  *   block_tables [num_seqs, max_blocks_per_seq], seq_lens [num_seqs]: updated
  *   new_lens     [num_seqs] int32 in [0, max_blocks_per_seq * block_size]
  */
