@@ -76,13 +76,23 @@
 //     the one merging warp outweigh the tokens.
 //   A batch with a few long sequences among short ones, 64 heads over 8:
 //     45 us, 76 without teams for the units left over.
-//   Four new tokens a sequence, 32 heads over 8 (16 rows a unit): 60 us for
-//     160 MB.  The tensor pipe is a third used, the issue slots 40%: two warps a
+//   Four new tokens a sequence, 32 heads over 8 (16 rows a unit): 61 us for
+//     160 MB.  The tensor pipe is a third used, the issue slots 37%: two warps a
 //     scheduler (255 registers) leave the chains of a tile, scores to weights to
 //     values, in the open.  32-token stages 64 to 67 us.  What cost most before
 //     that were spilled registers: 227 KB of shared memory leave next to no L1,
 //     so they come from L2 (68 us with ten reloads a stage; 10 and 12 warps of
-//     168 registers, 13 a tile, 115 and 90).
+//     168 registers, 13 a tile, 115 and 90; the four to six words a thread that
+//     still spill lie outside the tiles, as the references are raised).
+//   More rows a kv head than a unit takes (16; 8 at head size 256) read and
+//     unpack its records again: 48 sequences as above with 32 rows a kv head 135 us
+//     for 177 MB, 64 of 2048 to 8192 tokens with 16 rows a head (64 heads over 4)
+//     76 us for 190 MB.
+//   Head size 256, 64 sequences of 2048 to 8192 tokens, 8 kv heads, 730 MB: 139 us
+//     with one row a head, 143 with four, 150 with eight (8 warps); 166 in blocks of
+//     64 tokens (4 warps).  The first batch in blocks of 8 tokens 135 us, of 64 tokens
+//     138; with one row a kv head (64 sequences, 32 heads, 735 MB) 125; at head size 64
+//     91 us for 393 MB.
 #pragma once
 
 #include <type_traits>

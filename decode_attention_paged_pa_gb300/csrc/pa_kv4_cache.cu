@@ -15,10 +15,11 @@
 // for the first, steps from there for the others), block and slot, while the
 // others' rows are on their way.
 //
-// Both kernels are bound by memory: 2 D bytes on the row side and D/2 + 4 on
-// the cache side per vector, each touched once.  A first form with eight
-// elements a lane, fp32 minima and a division per element was bound by issue
-// (80% of the slots); so minima and maxima are taken on packed pairs (they are
+// Per vector 2 D bytes on the row side and D/2 + 4 on the cache side are touched
+// once.  Read-back is bound by memory (loads in flight); the append by issue (76%
+// of the slots, 43% of the memory's rate: about seven single-precision
+// instructions an element for its code).  A first form with eight elements a
+// lane, fp32 minima and a division per element took twice as long; so minima and maxima are taken on packed pairs (they are
 // exact in T), the lowest and the negated highest in one word through the
 // shuffles; the quotient (x - zero) / scale by a reciprocal, and only where it
 // lies so close to a tie that the reciprocal's error could decide, by the
@@ -28,9 +29,16 @@
 // Measured (GB300): chunks of 24 prompts written and their contexts read back
 // (8 kv heads, D = 128), 104 us for 542 MB, 77% of the measured copy rate of
 // 6766 GB/s (247 in the first form; 137 with a persistent grid whose first warp
-// looked ahead: many small CTAs hide the placing as well).  One token each of
-// 128 sequences, written and read back: 7 us, two launches of three dependent
-// loads each.
+// looked ahead: many small CTAs hide the placing as well); alone, the append
+// takes 41 us for 164 MB (60% of that rate), the read-back 65 for 406 MB (92%).
+// One token each of 128 sequences, written and read back: 7 us, two launches of
+// three dependent loads each.
+//
+// The status check takes a thread a sequence: of a single sequence of thousands
+// of blocks it takes longer than the rows do.  One context of 131072 tokens read
+// back, D = 128: 143 us with one kv head (floor 12.6), 233 with eight (floor 100),
+// blocks of 16; 274 and 414 with twice as many blocks, of 8; written, 196 us with
+// eight (floor 100).
 #include <cstring>
 
 #include "pa_common.cuh"
@@ -107,8 +115,8 @@ __device__ __forceinline__ void place(const Kv4Params& p, int t0, int nt, int la
   *slot = pos % p.BS;
 }
 
-// CTA 0 checks every sequence and leaves the call's status in the header, so
-// that no other launch has to clear it.
+// CTA 0 checks every sequence, a thread each, and leaves the call's status in the
+// header, so that no other launch has to clear it.
 __device__ __forceinline__ void write_status(const Kv4Params& p) {
   int bad = 0;
   if (p.cu && threadIdx.x == 0 && p.cu[0] < 0) bad = 1;
