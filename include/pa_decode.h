@@ -384,7 +384,7 @@ int pa_kv4_append(void* kv_cache, const void* key, const void* value, const int3
  * sequence as rows of the dtype, each value scale * code + zero rounded once
  * (for prefill attention over earlier context, or to leave the format).
  * Arguments as for pa_kv4_append; rows that belong to no sequence, or whose
- * length or block id is refused, keep what they held.
+ * length, offsets or block id are refused, keep what they held.
  */
 int pa_kv4_gather(void* key_out, void* value_out, const void* kv_cache, const int32_t* block_tables,
                   const int32_t* seq_lens, const int32_t* cu_tokens, int num_seqs, int num_tokens,

@@ -195,6 +195,42 @@ def test_scores_that_rise_by_hundreds(form, dtype):
             par[b, :, o, 1] = pos // 5 * 0.5  # scores of about 0.09 * 0.8 D * that
     check(q, cache, bt, L, 0.09, 1024, [0, 1, 2])
 
+@pytest.mark.parametrize("form", FORMS, ids=str)
+def test_states_of_partitions(form):
+    """What is left of a partition in the workspace: its weight sum lies in [1, 16),
+    and with its reference gives the log of its sum; unused ones are (-inf, 0)."""
+    q, cache, bt, L = case(form, BF16)
+    S, H, KH, D, BS, ql = form
+    params(cache, D, BF16)[..., 2:] *= 1000.0
+    dev, P = torch.device("cuda"), 64
+    qd, cd, bd, ld = (t.to(dev) for t in (q, cache, bt, L))
+    out = torch.empty_like(qd)
+    call = binding.pa_decode_v2_kv4 if ql == 1 else binding.pa_decode_v2_mq_kv4
+    ws = call(out, qd, cd, bd, ld, 0.09, partition_size=P)
+    assert binding.device_status(ws) == binding.PA_OK
+    (om, ol, _, _, _), pmax = binding.workspace_layout(S * ql, H, KH, D, bt.shape[1], BS, P)
+    m, l = (ws[o:o + S * ql * H * pmax * 4].view(torch.float32).view(S, ql * H, pmax).cpu() for o in (om, ol))
+    G = H // KH
+    for s in range(3):
+        n = int(L[s])
+        np = -(-n // P)
+        assert bool((m[s, :, np:] == -math.inf).all()) and not bool(l[s, :, np:].any())
+        k, _, _ = read_records(cache[bt[s, : -(-n // BS)].long()], D, BF16)
+        for r in range(H * ql):  # row head r: kv head, token, head of the group
+            kv, i, g = r // (G * ql), r % (G * ql) // G, r % G
+            row = (q[s] if ql == 1 else q[s, i])[kv * G + g].double()
+            z = float(torch.tensor(0.09)) * (k[:, kv].reshape(-1, D)[: n - ql + 1 + i] @ row)
+            for p in range(np):
+                part = z[p * P:(p + 1) * P]
+                if part.numel() == 0:
+                    assert m[s, r, p] == -math.inf and l[s, r, p] == 0
+                    continue
+                assert 1 <= float(l[s, r, p]) < 16
+                got = float(m[s, r, p]) + math.log(float(l[s, r, p]))
+                # (The scores' fp32 error, as in the bound above with M below 400; one of fp32 for m.)
+                assert abs(got - float(torch.logsumexp(part, 0))) <= 400 * (D + 8) * 2.0 ** -23 + 2.0 ** -15
+
+
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
 @pytest.mark.parametrize("mag,dtype", [(1.0, F16), (1.0, BF16), (1e7, BF16), (1e-8, BF16), (2e-5, F16)])
 @pytest.mark.parametrize("form", FORMS[:4], ids=str)
