@@ -100,8 +100,8 @@ def draw(rng):
         e4m3 = rng.random() < 0.25
         dtype = rng.choice(["fp16", "bf16"] if e4m3 else ["fp16", "fp16", "bf16", "bf16", "fp32"])
         n = rng.choice([1, 1, 1, 2, 4, 7, 16, 61, 128]) if op == "window" else _logint(rng, 1, 100)
-        if dtype == "fp32":
-            n = min(n, 16)
+        if dtype == "fp32":  # (whose blocks hold at most 32 tokens of 256 dims)
+            n, BS = min(n, 16), min(BS, 32) if D == 256 else BS
         S = _logint(rng, 1, 128)
         if op == "window" or rng.random() < 0.3:
             window, sinks = max(_logint(rng, 1, 4096), n if op == "tree" else 1), rng.choice([0, 0, 1, 4, 4, 33, 128])
