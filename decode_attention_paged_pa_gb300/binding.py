@@ -31,6 +31,7 @@ PA_ERR_NO_BLOCKS = 7
 PA_DTYPE_FP16 = 0
 PA_DTYPE_BF16 = 1
 PA_DTYPE_FP32 = 2
+PA_DTYPE_E4M3 = 3  # caches alone
 
 PA_VARIANT_AUTO = 0
 PA_VARIANT_SIMT = 1
@@ -58,6 +59,15 @@ EXPORTED_SYMBOLS = (
     "pa_pages_resize",
     "pa_pages_compact",
     "pa_pages_workspace_bytes",
+    "pa_decode_v2_window",
+    "pa_decode_v2_window_fp8",
+    "pa_decode_v2_tree",
+    "pa_decode_v2_tree_fp8",
+    "pa_decode_v2_view_workspace_bytes",
+    "pa_tree_masks",
+    "pa_tree_accept",
+    "pa_pages_slots",
+    "pa_cache_write",
     "pa_decode_v2_workspace_bytes",
     "pa_decode_v2_workspace_layout",
     "pa_decode_v2_host_io",
@@ -124,6 +134,24 @@ def _declare(lib):
     lib.pa_pages_resize.restype = ci
     lib.pa_pages_compact.argtypes = [vp] * 6 + [ci] * 5 + [vp, vp, cs]
     lib.pa_pages_compact.restype = ci
+    # out, lse, query .. seq_lens, scale, [scales,] window, sinks, num_seqs, q_len, then pa_decode_v2's from num_heads on
+    lib.pa_decode_v2_window.argtypes = [vp, vp] + base[1:7] + [ci] * 4 + base[8:]
+    lib.pa_decode_v2_window_fp8.argtypes = [vp, vp] + base[1:7] + [cf, cf] + [ci] * 4 + base[8:]
+    # ... with the masks after the lengths
+    lib.pa_decode_v2_tree.argtypes = [vp, vp] + base[1:6] + [vp, cf] + [ci] * 4 + base[8:]
+    lib.pa_decode_v2_tree_fp8.argtypes = [vp, vp] + base[1:6] + [vp, cf, cf, cf] + [ci] * 4 + base[8:]
+    for fn in (lib.pa_decode_v2_window, lib.pa_decode_v2_window_fp8, lib.pa_decode_v2_tree, lib.pa_decode_v2_tree_fp8):
+        fn.restype = ci
+    lib.pa_decode_v2_view_workspace_bytes.argtypes = [ci] * 10
+    lib.pa_decode_v2_view_workspace_bytes.restype = cs
+    lib.pa_tree_masks.argtypes = [vp] * 4 + [ci, ci, vp, vp, cs]
+    lib.pa_tree_masks.restype = ci
+    lib.pa_tree_accept.argtypes = [vp] * 3 + [ci] + [vp] * 4 + [ci] * 7 + [vp, ci, ci, vp, cs]
+    lib.pa_tree_accept.restype = ci
+    lib.pa_pages_slots.argtypes = [vp] * 7 + [ci] * 4 + [vp, vp, cs]
+    lib.pa_pages_slots.restype = ci
+    lib.pa_cache_write.argtypes = [vp] * 5 + [cf, cf] + [ci] * 4 + [cll, cll, ci, ci, vp, ci, vp, cs]
+    lib.pa_cache_write.restype = ci
     lib.pa_decode_v2_host_io.argtypes = base
     lib.pa_decode_v2_host_io.restype = ci
     lib.pa_decode_v2_host_io_workspace_bytes.argtypes = [ci] * 7
@@ -718,6 +746,296 @@ def pa_pages_compact(block_tables, seq_lens, refcounts, caches, block_size: int,
             workspace.numel())
     if st != PA_OK:
         raise PaError(st, "pa_pages_compact")
+    return workspace
+
+
+def view_workspace_bytes(num_seqs, q_len, num_heads, num_kv_heads, head_size, max_blocks_per_seq, block_size,
+                         partition_size, window, sinks) -> int:
+    """Bytes of workspace for windowed or tree attention (a tree's ``q_len``: its
+    nodes; ``window`` 0: a tree without one)."""
+    return int(lib().pa_decode_v2_view_workspace_bytes(num_seqs, q_len, num_heads, num_kv_heads, head_size,
+                                                       max_blocks_per_seq, block_size, partition_size, window,
+                                                       sinks))
+
+
+def _decode_view(name, out, query, key_cache, value_cache, block_tables, seq_lens, masks, scale, scales, window, sinks,
+                 partition_size, workspace, stream, lse):
+    fp8 = scales is not None
+    dt, ndim = query.dtype, query.dim()
+    if dt not in (_DTYPE_CODE if fp8 else _DTYPE_CODE_F32):
+        raise TypeError("query must be float16 or bfloat16" if fp8 else "query must be float16, bfloat16 or float32")
+    dev = query.get_device()
+    _need("out", out, dt, ndim, dev)
+    cdt = torch.uint8 if fp8 else dt
+    _need("key_cache", key_cache, cdt, 5, dev)
+    _need("value_cache", value_cache, cdt, 4, dev)
+    _need("block_tables", block_tables, torch.int32, 2, dev)
+    _need("seq_lens", seq_lens, torch.int32, 1, dev)
+    shape = query.shape
+    S, H, D = shape[0], shape[-2], shape[-1]
+    QL = shape[1] if ndim == 4 else 1
+    NB, KH, DX, BS, X = key_cache.shape
+    if out.shape != shape or X * key_cache.element_size() != 16 or DX * X != D:
+        raise ValueError("inconsistent query / out / key_cache shapes")
+    if value_cache.shape != (NB, KH, D, BS):
+        raise ValueError("value_cache must be [num_blocks, KH, D, BS]")
+    rows, MB = block_tables.shape
+    if rows != S or seq_lens.shape[0] != S:
+        raise ValueError("block_tables / seq_lens must have num_seqs rows")
+    if masks is not None:
+        _need("masks", masks, torch.int32, 3, dev)
+        if masks.shape != (S, QL, (QL + 31) // 32):
+            raise ValueError("masks must be [num_seqs, num_nodes, ceil(num_nodes / 32)]")
+    if lse is not None:
+        _need("lse", lse, torch.float32, ndim - 1, dev)
+        if lse.shape != shape[:-1]:
+            raise ValueError("lse must be query's shape without the head size")
+    # (The library takes 32-bit numbers; a longer window is all tokens.)
+    window, sinks = min(int(window), 1 << 30), min(int(sinks), 1 << 30)
+    if window < 0 or sinks < 0:
+        raise PaError(PA_ERR_INVALID_ARG, name)
+    workspace = _need_workspace(
+        workspace, dev, lambda: view_workspace_bytes(S, QL, H, KH, D, MB, BS, partition_size, window, sinks), stream)
+    fn = getattr(lib(), name + ("_fp8" if fp8 else ""))
+    args = (out.data_ptr(), _ptr(lse), query.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(),
+            block_tables.data_ptr(), seq_lens.data_ptr())
+    if masks is not None:
+        args += (masks.data_ptr(),)
+    args += (float(scale),) + (scales if fp8 else ())
+    with _current(dev):
+        st = fn(*args, window, sinks, S, QL, H, KH, D, BS, int(partition_size), _DTYPE_CODE_F32[dt],
+                _stream_handle(stream, query), MB, NB, workspace.data_ptr(), workspace.numel())
+    if st != PA_OK:
+        raise PaError(st, name)
+    return workspace
+
+
+def _need_query(query, *ndims):
+    _check_tensor("query", query)
+    if query.dim() not in ndims:
+        raise ValueError(f"query must have {' or '.join(map(str, ndims))} dims, got shape {tuple(query.shape)}")
+
+
+def pa_decode_v2_window(out, query, key_cache, value_cache, block_tables, seq_lens, scale: float, window: int,
+                        sinks: int = 0, partition_size: int = 512, workspace: torch.Tensor | None = None,
+                        stream=None, lse: torch.Tensor | None = None):
+    """Attention to a sliding window and the first ``sinks`` tokens (see
+    include/pa_decode.h): query/out [S, H, D] or [S, q_len, H, D]; a row at
+    position p sees t <= p with t > p - window or t < sinks.  Caches, tables and
+    ``lse`` as for :func:`pa_decode_v2` and :func:`pa_decode_v2_mq`.  Table entries
+    of blocks that no row sees are not read.  Returns the workspace used."""
+    _need_query(query, 3, 4)
+    return _decode_view("pa_decode_v2_window", out, query, key_cache, value_cache, block_tables, seq_lens, None, scale,
+                        None, window, sinks, partition_size, workspace, stream, lse)
+
+
+def pa_decode_v2_window_fp8(out, query, key_cache, value_cache, block_tables, seq_lens, scale: float, window: int,
+                            sinks: int = 0, k_scale: float = 1.0, v_scale: float = 1.0, partition_size: int = 512,
+                            workspace: torch.Tensor | None = None, stream=None, lse: torch.Tensor | None = None):
+    """:func:`pa_decode_v2_window` over an E4M3 cache (caches and scales of
+    :func:`pa_decode_v2_fp8`).  Returns the workspace used."""
+    _need_query(query, 3, 4)
+    return _decode_view("pa_decode_v2_window", out, query, key_cache, value_cache, block_tables, seq_lens, None, scale,
+                        (float(k_scale), float(v_scale)), window, sinks, partition_size, workspace, stream, lse)
+
+
+def pa_decode_v2_tree(out, query, key_cache, value_cache, block_tables, seq_lens, masks, scale: float, window: int = 0,
+                      sinks: int = 0, partition_size: int = 512, workspace: torch.Tensor | None = None, stream=None,
+                      lse: torch.Tensor | None = None):
+    """Attention for a tree of drafted tokens, each sequence's last ``n`` cached
+    ones (see include/pa_decode.h): query/out [S, n, H, D]; masks int32
+    [S, n, ceil(n / 32)] as :func:`pa_tree_masks` makes them; every node sees the
+    tokens before the tree (within ``window``, if it is not 0, and the first
+    ``sinks``) and the nodes of its mask; a node without a bit is padding.
+    Returns the workspace used."""
+    _need_query(query, 4)
+    _check_tensor("masks", masks)
+    return _decode_view("pa_decode_v2_tree", out, query, key_cache, value_cache, block_tables, seq_lens, masks, scale,
+                        None, window, sinks, partition_size, workspace, stream, lse)
+
+
+def pa_decode_v2_tree_fp8(out, query, key_cache, value_cache, block_tables, seq_lens, masks, scale: float,
+                          window: int = 0, sinks: int = 0, k_scale: float = 1.0, v_scale: float = 1.0,
+                          partition_size: int = 512, workspace: torch.Tensor | None = None, stream=None,
+                          lse: torch.Tensor | None = None):
+    """:func:`pa_decode_v2_tree` over an E4M3 cache (caches and scales of
+    :func:`pa_decode_v2_fp8`).  Returns the workspace used."""
+    _need_query(query, 4)
+    _check_tensor("masks", masks)
+    return _decode_view("pa_decode_v2_tree", out, query, key_cache, value_cache, block_tables, seq_lens, masks, scale,
+                        (float(k_scale), float(v_scale)), window, sinks, partition_size, workspace, stream, lse)
+
+
+def pa_tree_masks(masks, positions, parents, seq_lens, workspace: torch.Tensor | None = None, stream=None):
+    """Masks and positions of trees from their nodes' parents (see
+    include/pa_decode.h): parents int32 [S, n] (-1: a child of the tokens before
+    the tree; below -1: padding); masks int32 [S, n, ceil(n / 32)] and positions
+    int32 [S, n] (or None) written; seq_lens int32 [S].  ``workspace`` (uint8,
+    >= 256 bytes) holds the status.  Returns the workspace used."""
+    _check_tensor("parents", parents, torch.int32, 2)
+    dev = parents.get_device()
+    _need("masks", masks, torch.int32, 3, dev)
+    _need("seq_lens", seq_lens, torch.int32, 1, dev)
+    S, n = parents.shape
+    if masks.shape != (S, n, (n + 31) // 32) or seq_lens.shape[0] != S:
+        raise ValueError("masks must be [num_seqs, num_nodes, ceil(num_nodes / 32)], seq_lens [num_seqs]")
+    if positions is not None:
+        _need("positions", positions, torch.int32, 2, dev)
+        if positions.shape != (S, n):
+            raise ValueError("positions must have parents' shape")
+    workspace = _need_workspace(workspace, dev, lambda: 256, stream)
+    with _current(dev):
+        st = lib().pa_tree_masks(masks.data_ptr(), _ptr(positions), parents.data_ptr(), seq_lens.data_ptr(), S, n,
+                                 _stream_handle(stream, parents), workspace.data_ptr(), workspace.numel())
+    if st != PA_OK:
+        raise PaError(st, "pa_tree_masks")
+    return workspace
+
+
+_CACHE_CODE = {**_DTYPE_CODE_F32, torch.uint8: PA_DTYPE_E4M3}
+
+
+def _cache_shape(name, key_cache, value_cache, dev):
+    """(num_blocks, KH, D, BS) of a pair of paged caches, fp16, bf16, fp32 or (uint8) E4M3."""
+    _need("key_cache", key_cache, key_cache.dtype, 5, dev)
+    _need("value_cache", value_cache, key_cache.dtype, 4, dev)
+    if key_cache.dtype not in _CACHE_CODE:
+        raise TypeError("caches must be float16, bfloat16, float32 or uint8 (E4M3)")
+    NB, KH, DX, BS, X = key_cache.shape
+    if X * key_cache.element_size() != 16 or value_cache.shape != (NB, KH, DX * X, BS):
+        raise ValueError(f"{name}: key_cache must be [num_blocks, KH, D/x, BS, x], value_cache [num_blocks, KH, D, BS]")
+    return NB, KH, DX * X, BS
+
+
+def pa_tree_accept(new_lens, key_caches, value_caches, block_tables, seq_lens, accepted, num_accepted, num_nodes: int,
+                   workspace: torch.Tensor | None = None, stream=None):
+    """The accepted nodes of each tree moved to the front of its part of the cache
+    (see include/pa_decode.h): ``key_caches`` / ``value_caches`` the tensors of
+    every layer (one shape and type; a tensor is one layer); accepted int32
+    [S, A], ascending, num_accepted int32 [S]; new_lens int32 [S] written.
+    Returns the workspace used."""
+    _check_tensor("seq_lens", seq_lens, torch.int32, 1)
+    dev = seq_lens.get_device()
+    key_caches = (key_caches,) if isinstance(key_caches, torch.Tensor) else key_caches
+    value_caches = (value_caches,) if isinstance(value_caches, torch.Tensor) else value_caches
+    if len(key_caches) != len(value_caches) or not key_caches:
+        raise ValueError("as many value caches as key caches, and one at least")
+    shape = _cache_shape("pa_tree_accept", key_caches[0], value_caches[0], dev)
+    cdt = key_caches[0].dtype
+    for k, v in zip(key_caches[1:], value_caches[1:]):
+        if k.dtype is not cdt or k.shape != key_caches[0].shape or v.shape != value_caches[0].shape:
+            raise ValueError("caches must have one shape and type")
+        _need("key_cache", k, cdt, 5, dev)
+        _need("value_cache", v, cdt, 4, dev)
+    NB, KH, D, BS = shape
+    _need("new_lens", new_lens, torch.int32, 1, dev)
+    _need("block_tables", block_tables, torch.int32, 2, dev)
+    _need("accepted", accepted, torch.int32, 2, dev)
+    _need("num_accepted", num_accepted, torch.int32, 1, dev)
+    S, MB = block_tables.shape
+    if not (new_lens.shape[0] == seq_lens.shape[0] == accepted.shape[0] == num_accepted.shape[0] == S):
+        raise ValueError("block_tables / seq_lens / accepted / num_accepted / new_lens must have num_seqs rows")
+    workspace = _need_workspace(workspace, dev, lambda: 256, stream)
+    ks = array.array("Q", [t.data_ptr() for t in key_caches])
+    vs = array.array("Q", [t.data_ptr() for t in value_caches])
+    with _current(dev):
+        st = lib().pa_tree_accept(
+            new_lens.data_ptr(), ks.buffer_info()[0], vs.buffer_info()[0], len(ks), block_tables.data_ptr(),
+            seq_lens.data_ptr(), accepted.data_ptr(), num_accepted.data_ptr(), S, int(num_nodes), accepted.shape[1],
+            KH, D, BS, _CACHE_CODE[cdt], _stream_handle(stream, seq_lens), MB, NB, workspace.data_ptr(),
+            workspace.numel())
+    if st != PA_OK:
+        raise PaError(st, "pa_tree_accept")
+    return workspace
+
+
+def pa_pages_slots(slots, positions, seq_ids, cu_tokens, block_tables, seq_lens, num_new, block_size: int,
+                   workspace: torch.Tensor | None = None, stream=None):
+    """The rows of a step numbered from its requests' lengths (see
+    include/pa_decode.h): num_new int32 [S] new tokens of each sequence, counted
+    by seq_lens already; slots int64 [N] (-1 behind the last row), positions and
+    seq_ids int32 [N] (or None) and cu_tokens int32 [S + 1] written.
+    ``workspace`` (uint8, >= 256 bytes) holds the status.  Returns the workspace
+    used."""
+    _check_tensor("slots", slots, torch.int64, 1)
+    dev, N = slots.get_device(), slots.shape[0]
+    for name, t in (("positions", positions), ("seq_ids", seq_ids)):
+        if t is not None:
+            _need(name, t, torch.int32, 1, dev)
+            if t.shape[0] != N:
+                raise ValueError(f"{name} must have slots' shape")
+    _need("cu_tokens", cu_tokens, torch.int32, 1, dev)
+    _need("block_tables", block_tables, torch.int32, 2, dev)
+    _need("seq_lens", seq_lens, torch.int32, 1, dev)
+    _need("num_new", num_new, torch.int32, 1, dev)
+    S, MB = block_tables.shape
+    if seq_lens.shape[0] != S or num_new.shape[0] != S or cu_tokens.shape[0] != S + 1:
+        raise ValueError("block_tables / seq_lens / num_new must have num_seqs rows, cu_tokens one more")
+    workspace = _need_workspace(workspace, dev, lambda: 256, stream)
+    with _current(dev):
+        st = lib().pa_pages_slots(slots.data_ptr(), _ptr(positions), _ptr(seq_ids), cu_tokens.data_ptr(),
+                                  block_tables.data_ptr(), seq_lens.data_ptr(), num_new.data_ptr(), S, N, MB,
+                                  int(block_size), _stream_handle(stream, slots), workspace.data_ptr(),
+                                  workspace.numel())
+    if st != PA_OK:
+        raise PaError(st, "pa_pages_slots")
+    return workspace
+
+
+def _rows_of(name, t, device, KH, D):
+    """(rows, row stride) of [N, KH, D] or [S, q_len, KH, D] token rows: the heads of
+    a token are contiguous, tokens a constant stride apart."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be on cuda:{device}, got {t.device}")
+    if t.dtype not in _DTYPE_CODE_F32:
+        raise TypeError(f"{name} must be float16, bfloat16 or float32")
+    shape, strides = t.shape, t.stride()
+    if len(shape) == 4:
+        if shape[1] != 1 and shape[0] != 1 and strides[0] != shape[1] * strides[1]:
+            raise ValueError(f"{name}: tokens must be a constant stride apart")
+        N, stride = shape[0] * shape[1], strides[1] if shape[1] != 1 else strides[0]
+    elif len(shape) == 3:
+        N, stride = shape[0], strides[0]
+    else:
+        raise ValueError(f"{name} must have 3 or 4 dims, got shape {tuple(shape)}")
+    if shape[-2] != KH or shape[-1] != D:
+        raise ValueError(f"{name} must have the caches' kv heads and head size, got shape {tuple(shape)}")
+    if strides[-1] != 1 or (KH != 1 and strides[-2] != D):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return N, (stride if N > 1 else KH * D)
+
+
+def pa_cache_write(key_cache, value_cache, key, value, slots, k_scale: float = 1.0, v_scale: float = 1.0,
+                   workspace: torch.Tensor | None = None, stream=None):
+    """New tokens written into paged caches by their slots (see
+    include/pa_decode.h): key / value [N, KH, D] (or [S, q_len, KH, D]) fp16, bf16
+    or fp32, slices of wider token rows allowed; caches of the same type, or uint8
+    ones that get the E4M3 codes of x / k_scale and x / v_scale; slots int64 [N],
+    negative ones skipped.  ``workspace`` (uint8, >= 256 bytes) holds the status.
+    Returns the workspace used."""
+    _check_tensor("slots", slots, torch.int64, 1)
+    dev = slots.get_device()
+    if not isinstance(key_cache, torch.Tensor):
+        raise TypeError("key_cache must be a torch.Tensor")
+    NB, KH, D, BS = _cache_shape("pa_cache_write", key_cache, value_cache, dev)
+    N, ks = _rows_of("key", key, dev, KH, D)
+    Nv, vs = _rows_of("value", value, dev, KH, D)
+    if N != Nv or key.dtype is not value.dtype or slots.shape[0] != N:
+        raise ValueError("key, value and slots must have the same rows, key and value one dtype")
+    if key_cache.dtype is not torch.uint8 and key_cache.dtype is not key.dtype:
+        raise TypeError("caches must have the rows' dtype, or be uint8 (E4M3)")
+    workspace = _need_workspace(workspace, dev, lambda: 256, stream)
+    with _current(dev):
+        st = lib().pa_cache_write(key_cache.data_ptr(), value_cache.data_ptr(), key.data_ptr(), value.data_ptr(),
+                                  slots.data_ptr(), float(k_scale), float(v_scale), N, KH, D, BS, ks, vs,
+                                  _DTYPE_CODE_F32[key.dtype], _CACHE_CODE[key_cache.dtype],
+                                  _stream_handle(stream, slots), NB, workspace.data_ptr(), workspace.numel())
+    if st != PA_OK:
+        raise PaError(st, "pa_cache_write")
     return workspace
 
 

@@ -104,6 +104,35 @@ bool ws_layout(int S, int H, int KH, int D, int MB, int BS, int P, WsLayout* w) 
   return true;
 }
 
+// Blocks of a sequence that view rows (pa_decode_v2_window, pa_decode_v2_tree) can
+// be worked on in one call: all of the table, or the first tokens' and as many as
+// a window and the rows behind its start can touch.
+int view_blocks(int q_len, int MB, int BS, int window, int sinks) {
+  if (window <= 0) return MB;
+  const long long n = ((long long)sinks + BS - 1) / BS + ((long long)window + q_len - 1 + BS - 1) / BS + 1;
+  return n < MB ? (int)n : MB;
+}
+
+// What view rows see (null in decode_impl: plain decode).
+struct ViewArgs {
+  int window, sinks;
+  const int32_t* masks;
+  bool tree;
+};
+
+// The view kernels' launch.
+cudaError_t launch_views(const KParams& prm, int dtype, bool kv_fp8, bool pairs, int D, int BS, int max_ctas,
+                         cudaStream_t st) {
+  const bool half = dtype == PA_DTYPE_FP16, b = BS == 8 || BS == 64;
+  if (dtype == PA_DTYPE_FP32) return b ? launch_view_x_f32(prm, D, BS, max_ctas, st) : launch_view_f32(prm, D, BS, max_ctas, st);
+  if (kv_fp8 && pairs) return half ? launch_view8_g_f16(prm, D, BS, max_ctas, st) : launch_view8_g_bf16(prm, D, BS, max_ctas, st);
+  if (kv_fp8 && b) return half ? launch_view8_b_f16(prm, D, BS, max_ctas, st) : launch_view8_b_bf16(prm, D, BS, max_ctas, st);
+  if (kv_fp8) return half ? launch_view8_f16(prm, D, BS, max_ctas, st) : launch_view8_bf16(prm, D, BS, max_ctas, st);
+  if (pairs) return half ? launch_view_g_f16(prm, D, BS, max_ctas, st) : launch_view_g_bf16(prm, D, BS, max_ctas, st);
+  if (b) return half ? launch_view_b_f16(prm, D, BS, max_ctas, st) : launch_view_b_bf16(prm, D, BS, max_ctas, st);
+  return half ? launch_view_f16(prm, D, BS, max_ctas, st) : launch_view_bf16(prm, D, BS, max_ctas, st);
+}
+
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 // The 4-bit family's launch, dispatched on the head size.
@@ -210,7 +239,7 @@ int decode_impl(void* out, float* lse, const void* query, const void* key_cache,
                 int block_size, int partition_size, int dtype, void* stream, int max_blocks_per_seq,
                 int num_blocks, void* workspace, size_t workspace_bytes, int variant, int max_ctas,
                 long long timeout_ns, bool kv_fp8 = false, float k_scale = 1.f, float v_scale = 1.f,
-                bool kv4 = false) {
+                bool kv4 = false, const ViewArgs* view = nullptr) {
   // Multi-query: the kernel sees q_len "row heads" per caller head (H below
   // counts them), q_len * G per kv head, all sharing the kv head's blocks.
   if (q_len < 1 || q_len > kMaxSeqsPerLaunch || num_heads <= 0 ||
@@ -218,7 +247,7 @@ int decode_impl(void* out, float* lse, const void* query, const void* key_cache,
     return PA_ERR_INVALID_ARG;
   const int S = num_seqs, H = num_heads * q_len, KH = num_kv_heads, D = head_size, BS = block_size,
             P = partition_size, MB = max_blocks_per_seq;
-  if (!valid_sizes(S, H, KH, D, MB, BS, P) || num_blocks <= 0) return PA_ERR_INVALID_ARG;
+  if (!valid_sizes(S, H, KH, D, MB, BS, P) || num_heads % KH != 0 || num_blocks <= 0) return PA_ERR_INVALID_ARG;
   if (dtype != PA_DTYPE_FP16 && dtype != PA_DTYPE_BF16 && dtype != PA_DTYPE_FP32) return PA_ERR_INVALID_ARG;
   if (variant < PA_VARIANT_AUTO || variant > PA_VARIANT_MMA || max_ctas < 0 || timeout_ns < 0)
     return PA_ERR_INVALID_ARG;
@@ -226,6 +255,12 @@ int decode_impl(void* out, float* lse, const void* query, const void* key_cache,
   if (!(k_scale == k_scale) || k_scale == INFINITY || k_scale == -INFINITY || !(v_scale == v_scale) ||
       v_scale == INFINITY || v_scale == -INFINITY)
     return PA_ERR_INVALID_ARG;
+  if (view) {
+    // (A tree's ancestors never lie before its window.)
+    if (view->sinks < 0 || view->window < (view->tree ? 0 : 1) ||
+        (view->tree && view->window > 0 && view->window < q_len))
+      return PA_ERR_INVALID_ARG;
+  }
   if (!supported(D, BS, P)) return PA_ERR_UNSUPPORTED;
   if (kv_fp8 && variant == PA_VARIANT_SIMT) return PA_ERR_UNSUPPORTED;  // fp8 runs on tensor cores
   // (8-token blocks on the CUDA cores: fp32 only; the 16-bit types take the tensor cores there.)
@@ -242,18 +277,21 @@ int decode_impl(void* out, float* lse, const void* query, const void* key_cache,
       !aligned(value_cache, 16) || !aligned(block_tables, 4) || !aligned(seq_lens, 4) ||
       (workspace && !aligned(workspace, 16)) || (lse && !aligned(lse, 4)))
     return PA_ERR_INVALID_ARG;
+  if (view && view->tree && (!view->masks || !aligned(view->masks, 4))) return PA_ERR_INVALID_ARG;
   WsLayout w;
-  if (!ws_layout(S, H, KH, D, MB, BS, P, &w)) return PA_ERR_INVALID_ARG;
+  if (!ws_layout(S, H, KH, D, view ? view_blocks(q_len, MB, BS, view->window, view->sinks) : MB, BS, P, &w))
+    return PA_ERR_INVALID_ARG;
   if (workspace && workspace_bytes < w.total) return PA_ERR_WORKSPACE;
 
   const int G = H / KH;
   if (variant == PA_VARIANT_AUTO)
-    variant = ((G == 1 || dtype == PA_DTYPE_FP32) && !kv_fp8 && !kv4 && simt_ok) ? PA_VARIANT_SIMT : PA_VARIANT_MMA;
+    variant = view ? (dtype == PA_DTYPE_FP32 ? PA_VARIANT_SIMT : PA_VARIANT_MMA)
+              : ((G == 1 || dtype == PA_DTYPE_FP32) && !kv_fp8 && !kv4 && simt_ok) ? PA_VARIANT_SIMT : PA_VARIANT_MMA;
   // More than 8 query rows per kv head: the tensor-core instances for units
   // of 16 rows (the rows on the M side of the products) read each K/V block
   // once for 16 rows (head sizes 64 and 128, blocks of 16 or 32 tokens,
   // 16-bit caches).
-  const bool wide = variant == PA_VARIANT_MMA && G > kMmaGroup && !kv_fp8 && !kv4 && D <= 128 &&
+  const bool wide = !view && variant == PA_VARIANT_MMA && G > kMmaGroup && !kv_fp8 && !kv4 && D <= 128 &&
                     base_shape(D, BS);
   // Over a 4-bit cache, 16 rows a unit where a kv head has more than 8: its
   // codes are unpacked once for both halves.
@@ -329,13 +367,21 @@ int decode_impl(void* out, float* lse, const void* query, const void* key_cache,
     prm.num_blocks = num_blocks;
     // (A partition past the table's capacity is the capacity: sums of lengths
     // and partition sizes stay in 32 bits.)
-    prm.P = kv4 && P > MB * BS ? MB * BS : P;
+    prm.P = (kv4 || view) && P > MB * BS ? MB * BS : P;
     prm.Pmax = w.pmax;
     prm.hg_per_kv = hg_per_kv;
     prm.n_hg = n_hg;
     prm.timeout_ns = timeout_ns > 0 ? timeout_ns : (1LL << 31);
+    if (view) {
+      prm.window = view->window;
+      prm.sinks = view->sinks;
+      prm.words = (q_len + 31) / 32;
+      prm.masks = view->tree ? reinterpret_cast<const uint32_t*>(view->masks) + (size_t)s0 * q_len * prm.words : nullptr;
+    }
     cudaError_t e;
-    if (kv4)
+    if (view)
+      e = launch_views(prm, dtype, kv_fp8, pairs, D, BS, max_ctas, st);
+    else if (kv4)
       e = dtype == PA_DTYPE_FP16 ? launch_kv4_f16(prm, D, BS, nt, kvu, max_ctas, st)
                                  : launch_kv4_bf16(prm, D, BS, nt, kvu, max_ctas, st);
     else if (kv_fp8 && pairs && BS == 8)
@@ -411,8 +457,14 @@ int decode_impl(void* out, float* lse, const void* query, const void* key_cache,
     cp.S = S;
     cp.H = H;
     cp.Pmax = w.pmax;
-    cp.P = P;
+    cp.P = view && P > MB * BS ? MB * BS : P;
     cp.max_len = MB * BS;
+    cp.BS = BS;
+    if (view) {
+      cp.view = 1;
+      cp.window = view->window;
+      cp.sinks = view->sinks;
+    }
     cp.wpr = w.pmax > 64 ? 8 : w.pmax > 32 ? 4 : w.pmax > 16 ? 2 : 1;
     cp.q_len = q_len;
     cp.Hu = num_heads;
@@ -458,6 +510,80 @@ extern "C" int pa_decode_v2_kv4_ex(void* out, float* lse, const void* query, con
                      num_heads, num_kv_heads, head_size, block_size, partition_size, dtype, stream,
                      max_blocks_per_seq, num_blocks, workspace, workspace_bytes, PA_VARIANT_AUTO, max_ctas,
                      timeout_ns, false, 1.f, 1.f, true);
+}
+
+namespace {
+
+// Lengths stay far below 2^30: a longer window, or more first tokens, is all of them.
+int view_tokens_arg(int n) { return n < (1 << 30) ? n : 1 << 30; }
+
+}  // namespace
+
+extern "C" size_t pa_decode_v2_view_workspace_bytes(int num_seqs, int q_len, int num_heads, int num_kv_heads,
+                                                    int head_size, int max_blocks_per_seq, int block_size,
+                                                    int partition_size, int window, int sinks) {
+  WsLayout w;
+  if (q_len < 1 || q_len > kMaxSeqsPerLaunch || num_heads <= 0 || (long long)num_heads * q_len > 65535 ||
+      num_kv_heads <= 0 || num_heads % num_kv_heads != 0 || window < 0 || sinks < 0 || block_size <= 0)
+    return 0;
+  if (!ws_layout(num_seqs, num_heads * q_len, num_kv_heads, head_size,
+                 view_blocks(q_len, max_blocks_per_seq, block_size, window, sinks), block_size, partition_size, &w))
+    return 0;
+  return w.total;
+}
+
+extern "C" int pa_decode_v2_window(void* out, float* lse, const void* query, const void* key_cache,
+                                   const void* value_cache, const int32_t* block_tables, const int32_t* seq_lens,
+                                   float scale, int window, int sinks, int num_seqs, int q_len, int num_heads,
+                                   int num_kv_heads, int head_size, int block_size, int partition_size, int dtype,
+                                   void* stream, int max_blocks_per_seq, int num_blocks, void* workspace,
+                                   size_t workspace_bytes) {
+  const ViewArgs view = {view_tokens_arg(window), view_tokens_arg(sinks), nullptr, false};
+  return decode_impl(out, lse, query, key_cache, value_cache, block_tables, seq_lens, scale, num_seqs, q_len,
+                     num_heads, num_kv_heads, head_size, block_size, partition_size, dtype, stream,
+                     max_blocks_per_seq, num_blocks, workspace, workspace_bytes, PA_VARIANT_AUTO, 0, 0, false, 1.f,
+                     1.f, false, &view);
+}
+
+extern "C" int pa_decode_v2_window_fp8(void* out, float* lse, const void* query, const void* key_cache,
+                                       const void* value_cache, const int32_t* block_tables,
+                                       const int32_t* seq_lens, float scale, float k_scale, float v_scale,
+                                       int window, int sinks, int num_seqs, int q_len, int num_heads,
+                                       int num_kv_heads, int head_size, int block_size, int partition_size,
+                                       int dtype, void* stream, int max_blocks_per_seq, int num_blocks,
+                                       void* workspace, size_t workspace_bytes) {
+  const ViewArgs view = {view_tokens_arg(window), view_tokens_arg(sinks), nullptr, false};
+  return decode_impl(out, lse, query, key_cache, value_cache, block_tables, seq_lens, scale, num_seqs, q_len,
+                     num_heads, num_kv_heads, head_size, block_size, partition_size, dtype, stream,
+                     max_blocks_per_seq, num_blocks, workspace, workspace_bytes, PA_VARIANT_AUTO, 0, 0, true,
+                     k_scale, v_scale, false, &view);
+}
+
+extern "C" int pa_decode_v2_tree(void* out, float* lse, const void* query, const void* key_cache,
+                                 const void* value_cache, const int32_t* block_tables, const int32_t* seq_lens,
+                                 const int32_t* masks, float scale, int window, int sinks, int num_seqs,
+                                 int num_nodes, int num_heads, int num_kv_heads, int head_size, int block_size,
+                                 int partition_size, int dtype, void* stream, int max_blocks_per_seq,
+                                 int num_blocks, void* workspace, size_t workspace_bytes) {
+  const ViewArgs view = {view_tokens_arg(window), view_tokens_arg(sinks), masks, true};
+  return decode_impl(out, lse, query, key_cache, value_cache, block_tables, seq_lens, scale, num_seqs, num_nodes,
+                     num_heads, num_kv_heads, head_size, block_size, partition_size, dtype, stream,
+                     max_blocks_per_seq, num_blocks, workspace, workspace_bytes, PA_VARIANT_AUTO, 0, 0, false, 1.f,
+                     1.f, false, &view);
+}
+
+extern "C" int pa_decode_v2_tree_fp8(void* out, float* lse, const void* query, const void* key_cache,
+                                     const void* value_cache, const int32_t* block_tables,
+                                     const int32_t* seq_lens, const int32_t* masks, float scale, float k_scale,
+                                     float v_scale, int window, int sinks, int num_seqs, int num_nodes,
+                                     int num_heads, int num_kv_heads, int head_size, int block_size,
+                                     int partition_size, int dtype, void* stream, int max_blocks_per_seq,
+                                     int num_blocks, void* workspace, size_t workspace_bytes) {
+  const ViewArgs view = {view_tokens_arg(window), view_tokens_arg(sinks), masks, true};
+  return decode_impl(out, lse, query, key_cache, value_cache, block_tables, seq_lens, scale, num_seqs, num_nodes,
+                     num_heads, num_kv_heads, head_size, block_size, partition_size, dtype, stream,
+                     max_blocks_per_seq, num_blocks, workspace, workspace_bytes, PA_VARIANT_AUTO, 0, 0, true,
+                     k_scale, v_scale, false, &view);
 }
 
 extern "C" int pa_decode_v2_ex(void* out, const void* query, const void* key_cache,

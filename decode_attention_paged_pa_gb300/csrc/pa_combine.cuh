@@ -37,6 +37,7 @@
 #pragma once
 
 #include "pa_common.cuh"
+#include "pa_view.cuh"
 
 namespace pa {
 
@@ -50,6 +51,7 @@ struct CParams {
   int S, H, Pmax, P, max_len;
   int wpr;             // pa_combine_kernel: warps per row, 1, 2, 4 or 8
   int q_len, Hu, Gu, G;  // multi-query rows (q_len > 1): row head -> output row
+  int view, window, sinks, BS;  // view rows (1): see ViewSpan
 };
 
 // pa_combine_kernel: 8 warps where a row takes 8 of them, 4 otherwise (with
@@ -69,7 +71,8 @@ __device__ __forceinline__ size_t combine_out_row(const CParams& prm, int s, int
 }
 
 __device__ __forceinline__ int seq_partitions(const CParams& prm, int s) {
-  const int L = min(max(prm.lens[s], 0), prm.max_len);
+  int L = min(max(prm.lens[s], 0), prm.max_len);
+  if (prm.view) L = view_tokens(L, prm.q_len, prm.window, prm.sinks, prm.BS);
   return (L + prm.P - 1) / prm.P;
 }
 

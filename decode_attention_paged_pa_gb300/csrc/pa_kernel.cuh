@@ -44,6 +44,7 @@
 #pragma once
 
 #include "pa_common.cuh"
+#include "pa_view.cuh"
 
 namespace pa {
 
@@ -55,6 +56,13 @@ namespace pa {
 #endif
 constexpr int kMaxSeqsPerLaunch = PA_MAX_SEQS_PER_LAUNCH;
 static_assert(kMaxSeqsPerLaunch <= 65536, "ranks are kept as 16-bit sequence indices");
+
+// What the rows of a launch see.
+enum Mode {
+  kSingle = 0,  // one row a head: every cached token
+  kMulti = 1,   // q_len causal rows a head
+  kView = 2     // q_len rows a head that see a window and the first tokens, or the nodes of a tree
+};
 
 struct KParams {
   // Tensor map of the value cache (C::kTma consumers only): [NB * KH][D][BS]
@@ -82,16 +90,31 @@ struct KParams {
   int hg_per_kv;  // ceil(G / GT)
   int n_hg;       // head groups per partition: KH * hg_per_kv, or KH / KVU
   long long timeout_ns;
+  // View rows (kView): a window of `window` tokens (0: no window) and the first
+  // `sinks` ones; masks: the trees' masks [S, q_len, words], or null.
+  int window, sinks, words;
+  const uint32_t* masks;
 };
 
 // Cached tokens of sequence s, clamped to [0, max_len].  A length outside
-// [MQ ? q_len : 0, max_len] is flagged (*bad): a multi-query sequence holds
+// [q_len (one row: 0), max_len] is flagged (*bad): a multi-query sequence holds
 // its q_len new tokens.
-template <bool MQ>
+template <int MODE>
 __device__ __forceinline__ int seq_tokens(const KParams& prm, int s, int max_len, bool* bad) {
   const int L = prm.lens[s];
-  if (L < (MQ ? prm.q_len : 0) || L > max_len) *bad = true;
+  if constexpr (MODE == kView) {
+    // (Without masks a single row may find an empty sequence.)
+    if ((L < prm.q_len && !(L == 0 && prm.q_len == 1 && !prm.masks)) || L > max_len) *bad = true;
+  } else {
+    if (L < (MODE == kMulti ? prm.q_len : 0) || L > max_len) *bad = true;
+  }
   return min(max(L, 0), max_len);
+}
+// ... and those of them that a launch works on (see ViewSpan).
+template <int MODE>
+__device__ __forceinline__ int work_tokens(const KParams& prm, int L, int BS) {
+  if constexpr (MODE == kView) return view_tokens(L, prm.q_len, prm.window, prm.sinks, BS);
+  else return L;
 }
 
 // Multi-query decode keeps the single-query work decomposition and gives the
@@ -101,9 +124,9 @@ __device__ __forceinline__ int seq_tokens(const KParams& prm, int s, int max_len
 // load serves q_len * Gu rows); token i sits at position L - q_len + i and
 // sees positions 0 .. L - q_len + i.  (Multi-query kernels are separate
 // instances: carrying q_len through the single-query kernel cost it 5%.)
-template <bool MQ>
+template <int MODE>
 __device__ __forceinline__ size_t out_row(const KParams& prm, int s, int h) {
-  if constexpr (!MQ) {
+  if constexpr (MODE == kSingle) {
     return (size_t)s * prm.H + h;
   } else {
     const int kv = h / prm.G, l = h - kv * prm.G, i = l / prm.Gu;
@@ -112,22 +135,41 @@ __device__ __forceinline__ size_t out_row(const KParams& prm, int s, int h) {
 }
 // out_row for code shared by both kernel kinds (final writes only).
 __device__ __forceinline__ size_t out_row_rt(const KParams& prm, int s, int h) {
-  return prm.q_len > 1 ? out_row<true>(prm, s, h) : out_row<false>(prm, s, h);
+  return prm.q_len > 1 ? out_row<kMulti>(prm, s, h) : out_row<kSingle>(prm, s, h);
 }
 // Positions [0, limit) that row head h of a sequence of L tokens sees.
-template <bool MQ>
+template <int MODE>
 __device__ __forceinline__ int row_limit(const KParams& prm, int L, int h) {
-  if constexpr (!MQ) {
+  if constexpr (MODE == kSingle) {
     return L;
   } else {
     return L - prm.q_len + (h % prm.G) / prm.Gu + 1;
   }
 }
 
+// (See RowView.)
+__device__ __forceinline__ RowView row_view(const KParams& prm, int s, int L, int h) {
+  const int i = (h % prm.G) / prm.Gu, first = L - prm.q_len;
+  RowView v;
+  int at = first + i;
+  v.bits = nullptr;
+  v.hi = v.base = at + 1;
+  if (prm.masks) {
+    v.bits = prm.masks + ((size_t)s * prm.q_len + i) * prm.words;
+    int n = 0;
+    for (int w = 0; w < prm.words; ++w) n += __popc(__ldg(v.bits + w));
+    at = first + n - 1;
+    v.base = first;
+    v.hi = n > 0 ? L : 0;
+  }
+  v.lo = prm.window > 0 ? at - prm.window + 1 : 0;
+  return v;
+}
+
 struct UnitInfo {
   int s, p, hg, t0, t1, nb, np, nh, h0;
   int L;  // the sequence's tokens
-  int pad[2];
+  int sink_blocks, skip;  // (kView only: see ViewSpan)
 };
 
 constexpr uint32_t al16(uint32_t x) { return (x + 15u) & ~15u; }
@@ -213,6 +255,7 @@ __device__ __forceinline__ bool wait_issued(const volatile uint32_t* issued, uin
 // A work unit as the producer sees it.
 struct UnitPlan {
   int s, p, hg, t0, t1, nb, np, nh, h0, kv, L;
+  ViewSpan span;  // (kView)
 };
 
 // Unit u = (partition pair, head group): pairs are numbered over the
@@ -220,7 +263,7 @@ struct UnitPlan {
 // partitions pref[r] .. pref[r + 1] - 1), so the sequences with the most
 // partitions, whose combines are the longest chains, start first, and the
 // last units handed out belong to the shortest sequences.
-template <class C, bool MQ>
+template <class C, int MODE>
 __device__ __forceinline__ UnitPlan plan_unit(const KParams& prm, const int* pref, const uint16_t* perm, int u) {
   constexpr int BS = C::BS, GT = C::GT;
   UnitPlan U;
@@ -235,10 +278,12 @@ __device__ __forceinline__ UnitPlan plan_unit(const KParams& prm, const int* pre
   U.s = perm[lo];
   U.p = pair - pref[lo];
   U.np = pref[lo + 1] - pref[lo];
-  const int L = seq_tokens<MQ>(prm, U.s, prm.MB * C::BS, &bad);
+  const int L = seq_tokens<MODE>(prm, U.s, prm.MB * C::BS, &bad);
   U.L = L;
   U.t0 = U.p * prm.P;
-  U.t1 = min(U.t0 + prm.P, L);
+  U.t1 = min(U.t0 + prm.P, work_tokens<MODE>(prm, L, BS));
+  U.span = ViewSpan{0, 0};
+  if constexpr (MODE == kView) U.span = view_span(L, prm.q_len, prm.window, prm.sinks, BS);
   U.nb = (U.t1 - U.t0 + BS - 1) / BS;
   if constexpr (C::KVU > 1) {
     // Head group hg: kv heads KVU hg .. KVU hg + KVU - 1, their G * KVU query heads.
@@ -258,9 +303,11 @@ __device__ __forceinline__ UnitPlan plan_unit(const KParams& prm, const int* pre
 // loaded (0 past the unit's end): issuing the load and checking the entry
 // (check_block_id) are split so that the load's latency can overlap other
 // work.
-template <class C>
+template <class C, int MODE>
 __device__ __forceinline__ int fetch_block_id(const KParams& prm, const UnitPlan& U, int c0, int lane) {
-  return (c0 + lane < U.nb) ? __ldg(prm.bt + (size_t)U.s * prm.MB + U.t0 / C::BS + c0 + lane) : 0;
+  int j = U.t0 / C::BS + c0 + lane;
+  if constexpr (MODE == kView) j += j < U.span.sink_blocks ? 0 : U.span.skip;
+  return (c0 + lane < U.nb) ? __ldg(prm.bt + (size_t)U.s * prm.MB + j) : 0;
 }
 // An id outside the pool is recorded and replaced by 0, so nothing is read
 // out of bounds.
@@ -271,12 +318,12 @@ __device__ __forceinline__ int check_block_id(const KParams& prm, int b) {
   }
   return b;
 }
-template <class C>
+template <class C, int MODE>
 __device__ __forceinline__ int load_block_id(const KParams& prm, const UnitPlan& U, int c0, int lane) {
-  return check_block_id(prm, fetch_block_id<C>(prm, U, c0, lane));
+  return check_block_id(prm, fetch_block_id<C, MODE>(prm, U, c0, lane));
 }
 
-template <class C, class LY, bool MQ>
+template <class C, class LY, int MODE>
 __device__ __forceinline__ void producer_loop(const KParams& prm, uint8_t* smem, const int* pref,
                                               const uint16_t* perm, UnitInfo* info, volatile int* abort_flag,
                                               volatile uint32_t* issued, int lane) {
@@ -294,7 +341,7 @@ __device__ __forceinline__ void producer_loop(const KParams& prm, uint8_t* smem,
   const int total = pref[prm.S] * prm.n_hg;
   auto plan_next = [&](int u, UnitPlan& Up) -> bool {
     if (u >= total) return false;
-    Up = plan_unit<C, MQ>(prm, pref, perm, u);
+    Up = plan_unit<C, MODE>(prm, pref, perm, u);
     return true;
   };
 
@@ -322,22 +369,26 @@ __device__ __forceinline__ void producer_loop(const KParams& prm, uint8_t* smem,
         UnitInfo& I = info[slot];
         I.s = Up.s; I.p = Up.p; I.hg = Up.hg; I.t0 = Up.t0; I.t1 = Up.t1; I.nb = Up.nb;
         I.np = Up.np; I.nh = Up.nh; I.h0 = Up.h0; I.L = Up.L;
+        if constexpr (MODE == kView) {
+          I.sink_blocks = Up.span.sink_blocks;
+          I.skip = Up.span.skip;
+        }
         const uint32_t qbytes = (uint32_t)(Up.nh * D * sizeof(T));
         mbar_arrive_expect_tx(bar_ufull + 8 * slot, qbytes);
-        if constexpr (!MQ && C::QROW == D)
+        if constexpr (MODE == kSingle && C::QROW == D)
           bulk_copy_g2s(sbase + LY::OFF_Q + slot * LY::QSLOT,
                         static_cast<const T*>(prm.q) + ((size_t)Up.s * prm.H + Up.h0) * D, qbytes,
                         bar_ufull + 8 * slot, pol_keep);
       }
     }
     okp = __shfl_sync(0xffffffffu, (int)okp, 0) != 0;
-    if constexpr (MQ || C::QROW != D) {
+    if constexpr (MODE != kSingle || C::QROW != D) {
       // One row copy per lane: the row heads of a multi-query unit are
       // scattered over the caller's [S, q_len, H] rows, and padded rows
       // (QROW > D) are not contiguous in the slot.
       if (okp && have && lane < Up.nh)
         bulk_copy_g2s(sbase + LY::OFF_Q + slot * LY::QSLOT + lane * LY::QROW_BYTES,
-                      static_cast<const T*>(prm.q) + out_row<MQ>(prm, Up.s, Up.h0 + lane) * D,
+                      static_cast<const T*>(prm.q) + out_row<MODE>(prm, Up.s, Up.h0 + lane) * D,
                       (uint32_t)(D * sizeof(T)), bar_ufull + 8 * slot, pol_keep);
     }
     if (okp) ++kq;
@@ -360,7 +411,7 @@ __device__ __forceinline__ void producer_loop(const KParams& prm, uint8_t* smem,
   UnitPlan U{};
   bool have = plan_next(u_cur, U);
   int bids = 0;  // this lane's block id among the unit's first 32 blocks
-  if (have) bids = load_block_id<C>(prm, U, 0, lane);
+  if (have) bids = load_block_id<C, MODE>(prm, U, 0, lane);
   ok = publish(U, have);
   while (have && ok) {
     int u_req = 0;
@@ -375,14 +426,14 @@ __device__ __forceinline__ void producer_loop(const KParams& prm, uint8_t* smem,
     auto plan_fetch_next = [&]() {
       const int u_nx = __shfl_sync(0xffffffffu, u_req, 0);
       have_next = plan_next(u_nx, Un);
-      if (have_next) bids_next = fetch_block_id<C>(prm, Un, 0, lane);
+      if (have_next) bids_next = fetch_block_id<C, MODE>(prm, Un, 0, lane);
       planned_next = true;
     };
     // Batches of the unit: those of its 32-block chunks (a batch never crosses one).
     const int nbatch = (U.nb / 32) * ((32 + BATCH - 1) / BATCH) + (U.nb % 32 + BATCH - 1) / BATCH;
     int ib = 0;
     for (int c0 = 0; c0 < U.nb && ok; c0 += 32) {
-      const int b32 = (c0 == 0) ? bids : load_block_id<C>(prm, U, c0, lane);
+      const int b32 = (c0 == 0) ? bids : load_block_id<C, MODE>(prm, U, c0, lane);
       const int cend = min(c0 + 32, U.nb);
       for (int jb = c0; jb < cend && ok; jb += BATCH, ++ib) {
         if (!claimed && ib + 2 >= nbatch) {
@@ -522,7 +573,7 @@ __device__ __forceinline__ bool wait_handover(const KParams& prm, uint32_t bar_e
 // Consumer warp: stream the blocks of every unit assigned to it and hand its
 // online-softmax state for each unit to the epilogue warp through shared
 // memory.  Consumer warps never wait for each other.
-template <class C, class LY, bool MQ>
+template <class C, class LY, int MODE>
 __device__ __forceinline__ void consumer_loop(const KParams& prm, uint8_t* smem, const UnitInfo* info,
                                               volatile int* abort_flag, const volatile uint32_t* issued, int warp,
                                               int lane) {
@@ -544,10 +595,21 @@ __device__ __forceinline__ void consumer_loop(const KParams& prm, uint8_t* smem,
 
   // Unused partitions: sentinels (m = -inf, l = 0).  Empty sequences: zeros
   // (a multi-query sequence is never empty: it holds its new tokens).
-  {
+  if constexpr (MODE == kView) {
+    // (Nothing reads the states of unused partitions: phase 2 knows their number.)
+    for (int s = blockIdx.x; s < S; s += gridDim.x) {
+      bool bad = false;
+      if (work_tokens<MODE>(prm, seq_tokens<MODE>(prm, s, prm.MB * C::BS, &bad), BS) > 0) continue;
+      constexpr int D16 = D * (int)sizeof(T) / 16;
+      uint4* o = reinterpret_cast<uint4*>(out) + (size_t)s * H * D16;
+      for (int i = ctid; i < H * D16; i += NCT) o[i] = make_uint4(0, 0, 0, 0);
+      if (prm.lse)
+        for (int i = ctid; i < H; i += NCT) prm.lse[(size_t)s * H + i] = -INFINITY;
+    }
+  } else {
     auto parts_of = [&](int s) {
       bool bad = false;  // flagged by the prologue already
-      return (seq_tokens<MQ>(prm, s, prm.MB * C::BS, &bad) + prm.P - 1) / prm.P;
+      return (seq_tokens<MODE>(prm, s, prm.MB * C::BS, &bad) + prm.P - 1) / prm.P;
     };
     const long long n1 = (long long)S * H * Pmax;
     for (long long i = (long long)blockIdx.x * NCT + ctid; i < n1; i += (long long)gridDim.x * NCT) {
@@ -558,7 +620,7 @@ __device__ __forceinline__ void consumer_loop(const KParams& prm, uint8_t* smem,
         prm.ws_l[i] = 0.f;
       }
     }
-    if constexpr (!MQ) {
+    if constexpr (MODE == kSingle) {
       constexpr int D16 = D * (int)sizeof(T) / 16;  // 16-byte words per output row
       const long long n2 = (long long)S * H * D16;
       for (long long i = (long long)blockIdx.x * NCT + ctid; i < n2; i += (long long)gridDim.x * NCT) {
@@ -593,8 +655,10 @@ __device__ __forceinline__ void consumer_loop(const KParams& prm, uint8_t* smem,
     }
     cons.begin_unit(reinterpret_cast<const T*>(smem + LY::OFF_Q + slot * LY::QSLOT), I.nh,
                     prm.scale_log2, lane, prm.G);
-    if constexpr (C::kMma || MQ)
-      cons.set_limits([&](int h) { return row_limit<MQ>(prm, I.L, I.h0 + h); }, lane);
+    if constexpr (MODE == kView)
+      cons.set_views([&](int h) { return row_view(prm, I.s, I.L, I.h0 + h); }, I.nh, prm.sinks, lane);
+    else if constexpr (C::kMma || MODE == kMulti)
+      cons.set_limits([&](int h) { return row_limit<MODE>(prm, I.L, I.h0 + h); }, lane);
     fence_proxy_async_smem();  // the query slot is refilled by a bulk copy: same ordering as a stage
     __syncwarp();
     if (lane == 0) mbar_arrive(bar_uempty + 8 * slot);
@@ -624,15 +688,24 @@ __device__ __forceinline__ void consumer_loop(const KParams& prm, uint8_t* smem,
       if (!__all_sync(0xffffffffu, okb)) break;
       const int ntok = min(nbi * BS, I.t1 - I.t0 - j * BS);
       uint8_t* sa = smem + st * LY::STAGE;
+      int tok0 = I.t0 + j * BS;
+      if constexpr (MODE == kView) {
+        // Positions: the item's first token, and how much further on than one
+        // block its second block lies.
+        const int b0 = tok0 / BS;
+        const bool over = b0 >= I.sink_blocks;
+        tok0 += over ? I.skip * BS : 0;
+        cons.set_gap(!over && b0 + 1 >= I.sink_blocks ? I.skip * BS : 0);
+      }
       if constexpr (PB == 2) {
         if (nbi == 2) {
           uint8_t* sb = smem + stage_of<LY>(gj + 1) * LY::STAGE;
-          cons.block_pair(sa, sa + LY::VOFF, sb, sb + LY::VOFF, ntok, lane, I.t0 + j * BS);
+          cons.block_pair(sa, sa + LY::VOFF, sb, sb + LY::VOFF, ntok, lane, tok0);
         } else {
-          cons.block(sa, sa + LY::VOFF, ntok, lane, scr, I.t0 + j * BS);
+          cons.block(sa, sa + LY::VOFF, ntok, lane, scr, tok0);
         }
       } else {
-        cons.block(sa, sa + LY::VOFF, ntok, lane, scr, I.t0 + j * BS);
+        cons.block(sa, sa + LY::VOFF, ntok, lane, scr, tok0);
       }
       // The stage is refilled by a bulk copy (async proxy) once released:
       // every lane's reads of it (generic proxy) are ordered before that
@@ -660,7 +733,7 @@ __device__ __forceinline__ void consumer_loop(const KParams& prm, uint8_t* smem,
 // Epilogue warp: for every unit, merge the consumer warps' states into the
 // partition's (m_p, l_p, o_p) in the workspace, or, for a sequence with one
 // partition, into the output and its log-sum-exp (single pass).
-template <class C, class LY>
+template <class C, class LY, int MODE>
 __device__ __forceinline__ void epilogue_loop(const KParams& prm, uint8_t* smem, volatile int* abort_flag,
                                               int lane) {
   using T = typename C::T;
@@ -729,7 +802,9 @@ __device__ __forceinline__ void epilogue_loop(const KParams& prm, uint8_t* smem,
       }
       const float den = ef[NC * GT + gh];
       const float inv = (den > 0.f ? 1.f / den : 0.f) * prm.v_scale;
-      const float4 val = make_float4(num.x * inv, num.y * inv, num.z * inv, num.w * inv);
+      float4 val = make_float4(num.x * inv, num.y * inv, num.z * inv, num.w * inv);
+      // (A view row that saw nothing here may have met values that no row sees.)
+      if (MODE == kView && den == 0.f) val = make_float4(0.f, 0.f, 0.f, 0.f);
       const size_t sh = (size_t)I.s * H + I.h0 + gh;
       if (single) {
         store4<T>(out + out_row_rt(prm, I.s, I.h0 + gh) * D + d4 * 4, val);
@@ -749,7 +824,7 @@ __device__ __forceinline__ void epilogue_loop(const KParams& prm, uint8_t* smem,
   }
 }
 
-template <class C, int NC, int NSTAGE, int CTAS_PER_SM, bool MQ>
+template <class C, int NC, int NSTAGE, int CTAS_PER_SM, int MODE>
 __global__ void __launch_bounds__(Layout<C, NC, NSTAGE>::THREADS, CTAS_PER_SM)
     pa_decode_kernel(const __grid_constant__ KParams prm) {
   using LY = Layout<C, NC, NSTAGE>;
@@ -800,7 +875,7 @@ __global__ void __launch_bounds__(Layout<C, NC, NSTAGE>::THREADS, CTAS_PER_SM)
     __syncthreads();
     for (int s = tid; s < S; s += nthr) {
       bool bad = false;
-      const int L = seq_tokens<MQ>(prm, s, max_len, &bad);
+      const int L = work_tokens<MODE>(prm, seq_tokens<MODE>(prm, s, max_len, &bad), C::BS);
       if (bad) *bad_len = 1;
       const int np = (L + prm.P - 1) / prm.P;
       parts[s] = np;
@@ -884,11 +959,11 @@ __global__ void __launch_bounds__(Layout<C, NC, NSTAGE>::THREADS, CTAS_PER_SM)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (tid == 0 && *bad_len) atomicCAS(prm.hdr + kHdrError, 0, kErrDeviceBounds);
   if (warp == NC) {
-    producer_loop<C, LY, MQ>(prm, smem, pref, perm, info, abort_flag, issued, lane);
+    producer_loop<C, LY, MODE>(prm, smem, pref, perm, info, abort_flag, issued, lane);
   } else if (warp == NC + 1) {
-    epilogue_loop<C, LY>(prm, smem, abort_flag, lane);
+    epilogue_loop<C, LY, MODE>(prm, smem, abort_flag, lane);
   } else {
-    consumer_loop<C, LY, MQ>(prm, smem, info, abort_flag, issued, warp, lane);
+    consumer_loop<C, LY, MODE>(prm, smem, info, abort_flag, issued, warp, lane);
   }
 }
 

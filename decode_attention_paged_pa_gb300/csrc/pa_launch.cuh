@@ -61,23 +61,26 @@ cudaError_t launch_one(const KParams& prm, int max_ctas, cudaStream_t stream) {
   using LY = typename SZ::LY;
   // Multi-query rows run on the tensor-core consumer, and on the CUDA-core
   // consumer's causal instances (fp32); those have no single-query kernel.
+  // View consumers take any number of rows.
   void (*kern)(KParams) = nullptr;
-  if constexpr (C::kMma) {
-    kern = prm.q_len > 1 ? pa_decode_kernel<C, NC, SZ::NS, kCtasPerSm, true>
-                         : pa_decode_kernel<C, NC, SZ::NS, kCtasPerSm, false>;
+  if constexpr (C::kView) {
+    kern = pa_decode_kernel<C, NC, SZ::NS, kCtasPerSm, kView>;
+  } else if constexpr (C::kMma) {
+    kern = prm.q_len > 1 ? pa_decode_kernel<C, NC, SZ::NS, kCtasPerSm, kMulti>
+                         : pa_decode_kernel<C, NC, SZ::NS, kCtasPerSm, kSingle>;
   } else if constexpr (C::kCausal) {
     if (prm.q_len <= 1) return cudaErrorInvalidValue;
-    kern = pa_decode_kernel<C, NC, SZ::NS, kCtasPerSm, true>;
+    kern = pa_decode_kernel<C, NC, SZ::NS, kCtasPerSm, kMulti>;
   } else {
     if (prm.q_len > 1) return cudaErrorInvalidValue;
-    kern = pa_decode_kernel<C, NC, SZ::NS, kCtasPerSm, false>;
+    kern = pa_decode_kernel<C, NC, SZ::NS, kCtasPerSm, kSingle>;
   }
   // The shared-memory opt-in is set once per kernel instance and device.
   static std::atomic<uint64_t> opted_in[2] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  const int mq = prm.q_len > 1 ? 1 : 0;
+  const int mq = !C::kView && prm.q_len > 1 ? 1 : 0;  // (a view consumer has one instance)
   const uint64_t bit = (dev >= 0 && dev < 64) ? (1ull << dev) : 0ull;
   if (!bit || !(opted_in[mq].load(std::memory_order_acquire) & bit)) {
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)LY::bytes(kMaxSeqsPerLaunch));

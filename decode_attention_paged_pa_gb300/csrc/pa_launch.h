@@ -70,6 +70,24 @@ cudaError_t launch_mma8_gx_bf16(const KParams& prm, int D, int BS, int max_ctas,
 cudaError_t launch_mma8_gb8_f16(const KParams& prm, int D, int max_ctas, cudaStream_t st);
 cudaError_t launch_mma8_gb8_bf16(const KParams& prm, int D, int max_ctas, cudaStream_t st);
 
+// View rows (windows, trees): 16-bit caches by units of one kv head, in blocks of
+// 16 or 32 tokens, of 8 or 64 (_b), and of pairs of kv heads (_g: up to 128 dims,
+// blocks of up to 32 tokens); the same over E4M3 caches (8); fp32 caches.
+cudaError_t launch_view_f16(const KParams& prm, int D, int BS, int max_ctas, cudaStream_t st);
+cudaError_t launch_view_bf16(const KParams& prm, int D, int BS, int max_ctas, cudaStream_t st);
+cudaError_t launch_view_b_f16(const KParams& prm, int D, int BS, int max_ctas, cudaStream_t st);
+cudaError_t launch_view_b_bf16(const KParams& prm, int D, int BS, int max_ctas, cudaStream_t st);
+cudaError_t launch_view_g_f16(const KParams& prm, int D, int BS, int max_ctas, cudaStream_t st);
+cudaError_t launch_view_g_bf16(const KParams& prm, int D, int BS, int max_ctas, cudaStream_t st);
+cudaError_t launch_view8_f16(const KParams& prm, int D, int BS, int max_ctas, cudaStream_t st);
+cudaError_t launch_view8_bf16(const KParams& prm, int D, int BS, int max_ctas, cudaStream_t st);
+cudaError_t launch_view8_b_f16(const KParams& prm, int D, int BS, int max_ctas, cudaStream_t st);
+cudaError_t launch_view8_b_bf16(const KParams& prm, int D, int BS, int max_ctas, cudaStream_t st);
+cudaError_t launch_view8_g_f16(const KParams& prm, int D, int BS, int max_ctas, cudaStream_t st);
+cudaError_t launch_view8_g_bf16(const KParams& prm, int D, int BS, int max_ctas, cudaStream_t st);
+cudaError_t launch_view_f32(const KParams& prm, int D, int BS, int max_ctas, cudaStream_t st);
+cudaError_t launch_view_x_f32(const KParams& prm, int D, int BS, int max_ctas, cudaStream_t st);
+
 // Over a 4-bit cache (queries and output fp16 / bf16), by head size: blocks of
 // 8, 16, 32 or 64 tokens, units of nt * 8 query rows of a kv head, or (kvu = 2, up
 // to four rows each) of two kv heads; either 2: head sizes up to 128, and kvu = 2:

@@ -33,9 +33,11 @@
 
 #include <cuda_fp8.h>
 
+#include <climits>
 #include <type_traits>
 
 #include "pa_common.cuh"
+#include "pa_view.cuh"
 
 namespace pa {
 
@@ -65,7 +67,12 @@ constexpr uint32_t al1024(uint32_t x) { return (x + 1023u) & ~1023u; }
 // weight (values) columns of the other kv heads zeroed, into the same
 // accumulators.  The softmax, the weights and the stage's waits then serve
 // KVU kv heads at once, and the copies are KVU times larger.
-template <typename T_, int D_, int BS_, bool FP8_ = false, int KVU_ = 1>
+// VIEW_: rows that see a window and the first tokens, or the nodes of a tree
+// (RowView): most work items are seen whole by every row of the unit and go
+// the same way as a causal unit's; in the others each score is masked by its
+// row's view, and a value that is not finite reaches only the rows that see it
+// (its product with another row's zero weight would be NaN).
+template <typename T_, int D_, int BS_, bool FP8_ = false, int KVU_ = 1, bool VIEW_ = false>
 struct MmaConsumer {
   using T = T_;
   using MT = typename std::conditional<FP8_, __half, T_>::type;  // operand type of the products
@@ -77,6 +84,7 @@ struct MmaConsumer {
   static_assert(KVU_ == 1 || 8 % KVU_ == 0, "kv-head groups share one 8-column tile");
   static constexpr bool kMma = true;
   static constexpr bool kCausal = false;  // (every unit is masked by its limits)
+  static constexpr bool kView = VIEW_;
   static constexpr bool kFp8 = FP8_;
   static constexpr int KV_ESZ = FP8_ ? 1 : 2;  // bytes per cached element
   // A stage: the key blocks of the unit's KVU kv heads (KTILE bytes each,
@@ -135,6 +143,122 @@ struct MmaConsumer {
   float acc[NMT][NT][4];
   float scale_log2;
   int lim[NT][2];  // positions [0, lim) the lane's heads see (causal rows of multi-query decode)
+
+  // View rows: the lane's two columns' windows and masks (RowView), the first
+  // tokens that stay visible, the positions [full_lo, full_hi) that every row of
+  // the unit sees (rows that see nothing apart: hi = 0), and how much further on
+  // than one block a work item's second block lies.
+  struct NoViews {};
+  struct Views {
+    int lo[2];
+    const uint32_t* bits[2];
+    int base, sinks, full_lo, full_hi, gap;
+  };
+  typename std::conditional<VIEW_, Views, NoViews>::type vw;
+
+  template <class F>
+  __device__ __forceinline__ void set_views(F view_of, int nh, int sinks, int lane) {
+    static_assert(NT == 1, "one column tile");
+    vw.full_lo = 0;
+    vw.full_hi = INT_MAX;
+    vw.base = INT_MAX;
+    vw.sinks = sinks;
+    vw.gap = 0;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int h = (lane & 3) * 2 + j;
+      lim[0][j] = 0;
+      vw.lo[j] = 0;
+      vw.bits[j] = nullptr;
+      if (h < nh) {
+        const RowView r = view_of(h);
+        lim[0][j] = r.hi;
+        vw.lo[j] = r.lo;
+        if (r.bits) {
+          vw.bits[j] = r.bits;
+          vw.base = r.base;
+        }
+        if (r.hi > 0) {
+          vw.full_lo = max(vw.full_lo, r.lo);
+          vw.full_hi = min(vw.full_hi, min(r.hi, r.base));
+        }
+      }
+    }
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) {
+      vw.full_lo = max(vw.full_lo, __shfl_xor_sync(0xffffffffu, vw.full_lo, o));
+      vw.full_hi = min(vw.full_hi, __shfl_xor_sync(0xffffffffu, vw.full_hi, o));
+    }
+  }
+  __device__ __forceinline__ void set_gap(int gap) {
+    if constexpr (VIEW_) vw.gap = gap;
+  }
+  // Position of the item's token t (tok0: its first token's).
+  __device__ __forceinline__ int pos_of(int tok0, int t) const {
+    if constexpr (VIEW_ && kItemBlocks == 2) return tok0 + t + (t >= BS ? vw.gap : 0);
+    else return tok0 + t;
+  }
+  // Whether some row of the unit does not see some token of the item (rows that
+  // see nothing at all apart).
+  __device__ __forceinline__ bool is_partial(int tok0, int ntok) const {
+    if constexpr (!VIEW_) return false;
+    else {
+      const int last = tok0 + ntok - 1;
+      return (kItemBlocks == 2 && vw.gap > 0) || last >= vw.full_hi || (tok0 < vw.full_lo && last >= vw.sinks);
+    }
+  }
+  // Whether the lane's column j sees position p.
+  __device__ __forceinline__ bool sees(int p, int j, bool partial) const {
+    if constexpr (!VIEW_) return p < lim[0][j];
+    else {
+      bool v = p < lim[0][j];
+      if (partial) {
+        v = v && (p >= vw.lo[j] || p < vw.sinks);
+        if (v && p >= vw.base) v = (__ldg(vw.bits[j] + ((p - vw.base) >> 5)) >> ((p - vw.base) & 31)) & 1u;
+      }
+      return v;
+    }
+  }
+
+  // The 16-bit value fragment `a` (dims x tokens, one k-step) of a partial item:
+  // elements that are not finite are taken out, and the accumulators of the rows
+  // that see their tokens (weights w of the score fragment not 0) become what the
+  // sums would: +-infinity, or NaN.  Infinities are counted by products with
+  // 0 / 1 operands; a NaN counts as one of each sign.
+  __device__ __forceinline__ static void value_guard(uint32_t (&a)[4], float (&acc4)[4], const float (&w)[4],
+                                                     bool mine) {
+    constexpr uint32_t kExp = std::is_same<MT, __half>::value ? 0x7c00u : 0x7f80u;
+    constexpr uint32_t kOne = std::is_same<MT, __half>::value ? 0x3c00u : 0x3f80u;
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      bad |= (a[i] & kExp) == kExp || ((a[i] >> 16) & kExp) == kExp;
+    if (!__any_sync(0xffffffffu, bad)) return;
+    uint32_t up[4], down[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      up[i] = down[i] = 0u;
+#pragma unroll
+      for (int s = 0; s < 32; s += 16) {
+        const uint32_t e = (a[i] >> s) & 0xffffu;
+        if ((e & kExp) != kExp) continue;
+        const bool nan = (e & 0x7fffu) != kExp;
+        if (nan || !(e & 0x8000u)) up[i] |= kOne << s;
+        if (nan || (e & 0x8000u)) down[i] |= kOne << s;
+        a[i] &= ~(0xffffu << s);
+      }
+    }
+    const uint32_t f0 = movmatrix_trans((w[0] != 0.f ? kOne : 0u) | (w[1] != 0.f ? kOne << 16 : 0u));
+    const uint32_t f1 = movmatrix_trans((w[2] != 0.f ? kOne : 0u) | (w[3] != 0.f ? kOne << 16 : 0u));
+    float nu[4] = {0.f, 0.f, 0.f, 0.f}, nd[4] = {0.f, 0.f, 0.f, 0.f};
+    Mma<MT>::run(nu, up, mine ? f0 : 0u, mine ? f1 : 0u);
+    Mma<MT>::run(nd, down, mine ? f0 : 0u, mine ? f1 : 0u);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (nu[i] > 0.f) acc4[i] += INFINITY;
+      if (nd[i] > 0.f) acc4[i] -= INFINITY;
+    }
+  }
 
   // fp8 caches: the token (within its 16-token tile) that MMA row i holds.
   // Rows 2c, 2c+1 and 2c+8, 2c+9 -- the score rows that become the weight
@@ -322,6 +446,7 @@ struct MmaConsumer {
   __device__ __forceinline__ void tiles(const uint32_t (&kt)[NTI], const uint32_t (&vt)[NTI], const int (&vc)[NTI],
                                         bool has_b, int ntok, int lane, int tok0) {
     const int r = lane >> 2;
+    const bool partial = is_partial(tok0, ntok);
     float sc[NTI][NT][4];
 #pragma unroll
     for (int tt = 0; tt < NTI; ++tt) {
@@ -352,6 +477,14 @@ struct MmaConsumer {
       for (int t = 0; t < NT; ++t) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) c[t][i] += c2[t][i];
+        if constexpr (VIEW_) {
+          const int p_lo = pos_of(tok0, t_lo), p_hi = pos_of(tok0, t_hi);
+          sc[tt][t][0] = t_lo < ntok && sees(p_lo, 0, partial) ? c[t][0] * scale_log2 : -INFINITY;
+          sc[tt][t][1] = t_lo < ntok && sees(p_lo, 1, partial) ? c[t][1] * scale_log2 : -INFINITY;
+          sc[tt][t][2] = t_hi < ntok && sees(p_hi, 0, partial) ? c[t][2] * scale_log2 : -INFINITY;
+          sc[tt][t][3] = t_hi < ntok && sees(p_hi, 1, partial) ? c[t][3] * scale_log2 : -INFINITY;
+          continue;
+        }
         sc[tt][t][0] = (t_lo < ntok && tok0 + t_lo < lim[t][0]) ? c[t][0] * scale_log2 : -INFINITY;
         sc[tt][t][1] = (t_lo < ntok && tok0 + t_lo < lim[t][1]) ? c[t][1] * scale_log2 : -INFINITY;
         sc[tt][t][2] = (t_hi < ntok && tok0 + t_hi < lim[t][0]) ? c[t][2] * scale_log2 : -INFINITY;
@@ -438,6 +571,9 @@ struct MmaConsumer {
             const uint32_t k1 = (t + 8 < ntok ? 0xffffu : 0u) | (t + 9 < ntok ? 0xffff0000u : 0u);
             a[0] &= k0; a[1] &= k0; a[2] &= k1; a[3] &= k1;
           }
+          if constexpr (VIEW_) {
+            if (partial) value_guard(a, acc[mt][0], sc[tt][0], mine);
+          }
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
             Mma<T>::run(acc[mt][t], a, mine ? b0[t] : 0u, mine ? b1[t] : 0u);
@@ -480,6 +616,7 @@ struct MmaConsumer {
                                             const uint32_t (&vv)[NT2], int ntok, int lane, int tok0) {
     const int r = lane >> 2, c = lane & 3;
     const int trow_lo = kTok(r), trow_hi = kTok(r + 8);
+    const bool partial = is_partial(tok0, ntok);
     float sc[NT2][4];
 #pragma unroll
     for (int tt = 0; tt < NT2; ++tt) {
@@ -504,10 +641,11 @@ struct MmaConsumer {
 #pragma unroll
       for (int i = 0; i < 4; ++i) c0[i] += c1[i];
       const int t_lo = tt * 16 + trow_lo, t_hi = tt * 16 + trow_hi;
-      sc[tt][0] = (t_lo < ntok && tok0 + t_lo < lim[0][0]) ? c0[0] * scale_log2 : -INFINITY;
-      sc[tt][1] = (t_lo < ntok && tok0 + t_lo < lim[0][1]) ? c0[1] * scale_log2 : -INFINITY;
-      sc[tt][2] = (t_hi < ntok && tok0 + t_hi < lim[0][0]) ? c0[2] * scale_log2 : -INFINITY;
-      sc[tt][3] = (t_hi < ntok && tok0 + t_hi < lim[0][1]) ? c0[3] * scale_log2 : -INFINITY;
+      const int p_lo = pos_of(tok0, t_lo), p_hi = pos_of(tok0, t_hi);
+      sc[tt][0] = t_lo < ntok && sees(p_lo, 0, partial) ? c0[0] * scale_log2 : -INFINITY;
+      sc[tt][1] = t_lo < ntok && sees(p_lo, 1, partial) ? c0[1] * scale_log2 : -INFINITY;
+      sc[tt][2] = t_hi < ntok && sees(p_hi, 0, partial) ? c0[2] * scale_log2 : -INFINITY;
+      sc[tt][3] = t_hi < ntok && sees(p_hi, 1, partial) ? c0[3] * scale_log2 : -INFINITY;
     }
     // Value words (dims mt*16 + r and + 8, tokens tt*16 + 4c .. +3) do not
     // depend on the weights: read them before the softmax.
@@ -583,11 +721,45 @@ struct MmaConsumer {
 #pragma unroll
         for (int mt = 0; mt < NMT; ++mt) {
           const uint32_t v0 = wv[tt][mt][0] & vmask[tt], v1 = wv[tt][mt][1] & vmask[tt];
-          const uint32_t a[4] = {e4m3x2(v0), e4m3x2(v1), e4m3x2(v0 >> 16), e4m3x2(v1 >> 16)};
+          uint32_t a[4] = {e4m3x2(v0), e4m3x2(v1), e4m3x2(v0 >> 16), e4m3x2(v1 >> 16)};
+          if constexpr (VIEW_) {
+            // (The guard's products take the weights' rows in the tile's order: quads
+            // c >= 2 find their tokens 4c, 4c + 1 in score rows 2c + 8, 2c + 9.)
+            if (partial) fp8_value_guard(a, acc[mt][0], sc[tt], mine, c);
+          }
           Mma<__half>::run(acc[mt][0], a, b0, b1);
         }
       }
     }
+  }
+
+  // value_guard for a tile of E4M3 values (of which only NaN is not finite).
+  __device__ __forceinline__ static void fp8_value_guard(uint32_t (&a)[4], float (&acc4)[4], const float (&w)[4],
+                                                         bool mine, int c) {
+    constexpr uint32_t kExp = 0x7c00u, kOne = 0x3c00u;
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) bad |= (a[i] & kExp) == kExp || ((a[i] >> 16) & kExp) == kExp;
+    if (!__any_sync(0xffffffffu, bad)) return;
+    uint32_t is[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      is[i] = 0u;
+#pragma unroll
+      for (int s = 0; s < 32; s += 16) {
+        if (((a[i] >> s) & kExp) != kExp) continue;
+        is[i] |= kOne << s;
+        a[i] &= ~(0xffffu << s);
+      }
+    }
+    const uint32_t f0 = movmatrix_trans((w[0] != 0.f ? kOne : 0u) | (w[1] != 0.f ? kOne << 16 : 0u));
+    const uint32_t f1 = movmatrix_trans((w[2] != 0.f ? kOne : 0u) | (w[3] != 0.f ? kOne << 16 : 0u));
+    const uint32_t b0 = c >= 2 ? f1 : f0, b1 = c >= 2 ? f0 : f1;
+    float n[4] = {0.f, 0.f, 0.f, 0.f};
+    Mma<__half>::run(n, is, mine ? b0 : 0u, mine ? b1 : 0u);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (n[i] > 0.f) acc4[i] = __int_as_float(0x7fffffff);
   }
 
   __device__ __forceinline__ void finish(float* acc_out, float* ml, int lane) {

@@ -39,6 +39,7 @@ struct MmaRowConsumer {
   static constexpr bool kTma = true;
   static constexpr bool kMma = true;
   static constexpr bool kCausal = false;  // (every unit is masked by its limits)
+  static constexpr bool kView = false;
   static constexpr bool kFp8 = false;
   static constexpr int KVU = 1;
   static constexpr int KV_ESZ = 2;

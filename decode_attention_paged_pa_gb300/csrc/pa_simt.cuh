@@ -12,18 +12,24 @@
 #pragma once
 
 #include "pa_common.cuh"
+#include "pa_view.cuh"
 
 namespace pa {
 
 // CAUSAL_: the instance for the causal rows of multi-query decode (each
 // head masked to the positions it may see; used for fp32 elements, whose
 // multi-query rows run on this family).
-template <typename T_, int D_, int BS_, int GT_, bool CAUSAL_ = false>
+// VIEW_: the instance for rows that see a window and the first tokens, or the
+// nodes of a tree (RowView; one row a unit): tokens that the row does not see get
+// no weight, and their values are cleared, as those past the sequence's end are.
+template <typename T_, int D_, int BS_, int GT_, bool CAUSAL_ = false, bool VIEW_ = false>
 struct SimtConsumer {
   using T = T_;
   static constexpr int D = D_, BS = BS_, GT = GT_;
   static constexpr bool kMma = false;
-  static constexpr bool kCausal = CAUSAL_;
+  static constexpr bool kCausal = CAUSAL_ || VIEW_;
+  static constexpr bool kView = VIEW_;
+  static_assert(!VIEW_ || (GT_ == 1 && BS_ <= 64), "a view unit has one row; a block's view fits 64 bits");
   // Blocks the producer warp issues together (MHA batch: 8 / 24 / 32 blocks
   // 363.5 / 355.3 / 359.4 us).
   static constexpr int kIssueBatch = 24;
@@ -95,6 +101,22 @@ struct SimtConsumer {
     }
   }
 
+  RowView view;  // view instances
+  int sinks;
+
+  template <class F>
+  __device__ __forceinline__ void set_views(F view_of, int, int n_sinks, int) {
+    view = view_of(0);
+    sinks = n_sinks;
+    lim[0] = view.hi;
+  }
+  __device__ __forceinline__ void set_gap(int) {}
+  __device__ __forceinline__ bool sees(int p) const {
+    bool v = p < view.hi && (p >= view.lo || p < sinks);
+    if (v && p >= view.base) v = (__ldg(view.bits + ((p - view.base) >> 5)) >> ((p - view.base) & 31)) & 1u;
+    return v;
+  }
+
   // Positions each head of the unit may see (causal instances only).
   template <class F>
   __device__ __forceinline__ void set_limits(F limit_of, int) {
@@ -110,6 +132,13 @@ struct SimtConsumer {
   __device__ __forceinline__ void block(const uint8_t* ks, uint8_t* vs, int ntok, int lane,
                                         float* pw, int tok0) {
     const int tl = lane % TPP, slice = lane / TPP;
+    // View rows: the block's tokens that the row sees (bit t).
+    uint64_t seen = ~0ull;
+    if constexpr (VIEW_) {
+      seen = __ballot_sync(0xffffffffu, lane < ntok && sees(tok0 + lane));
+      if constexpr (BS > 32) seen |= (uint64_t)__ballot_sync(0xffffffffu, lane + 32 < ntok && sees(tok0 + lane + 32)) << 32;
+      if (seen == 0) return;
+    }
     float sc[NPASS][GT];
 #pragma unroll
     for (int ps = 0; ps < NPASS; ++ps) {
@@ -145,7 +174,9 @@ struct SimtConsumer {
 #pragma unroll
         for (int off = TPP; off < 32; off <<= 1) sc[ps][g] += __shfl_xor_sync(0xffffffffu, sc[ps][g], off);
         if (t >= ntok) sc[ps][g] = -INFINITY;
-        if constexpr (kCausal) {
+        if constexpr (VIEW_) {
+          if (!((seen >> t) & 1u)) sc[ps][g] = -INFINITY;
+        } else if constexpr (kCausal) {
           if (tok0 + t >= lim[g]) sc[ps][g] = -INFINITY;
         }
       }
@@ -179,7 +210,20 @@ struct SimtConsumer {
         for (int ps = 0; ps < NPASS; ++ps) pw[g * BS + ps * TPP + tl] = sc[ps][g];
       }
     }
-    if (ntok < BS) {
+    constexpr uint64_t kAll = BS_ >= 64 ? ~0ull : (1ull << (BS_ % 64)) - 1;
+    if (VIEW_ && (seen & kAll) != kAll) {
+      // Values of tokens that the row does not see, and slots past the end: cleared
+      // like those below (few blocks of a row: at its window's start, among the first
+      // tokens, in a tree, and the last one).
+      for (uint64_t hid = ~seen & kAll; hid; hid &= hid - 1) {
+        const int t = __ffsll((long long)hid) - 1;
+        for (int d = lane; d < D; d += 32) {
+          if constexpr (sizeof(T) == 4) reinterpret_cast<uint32_t*>(vs)[d * BS + t] = 0u;
+          else reinterpret_cast<uint16_t*>(vs)[d * BS + t] = 0;
+        }
+      }
+      fence_proxy_async_smem();
+    } else if (!VIEW_ && ntok < BS) {
       // Slots past the sequence end hold arbitrary cache contents; zero them
       // so that 0 * (NaN or Inf) cannot reach the accumulator.  Rows of up to
       // 32 tokens: a lane clears its dims' tails (no index division; the

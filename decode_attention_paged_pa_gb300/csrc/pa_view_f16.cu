@@ -1,0 +1,26 @@
+// pa_view_f16.cu -- view instances (windows, trees) of the paged decode kernel
+// with the tensor-core (mma.sync) consumer, blocks of 16 or 32 tokens, element type
+// __half.
+#include "pa_launch.cuh"
+#include "pa_mma.cuh"
+
+namespace pa {
+
+template <int D>
+static cudaError_t go(const KParams& prm, int BS, int max_ctas, cudaStream_t st) {
+  if (BS == 16) return launch_one<MmaConsumer<__half, D, 16, false, 1, true>, kMmaConsumerWarps>(prm, max_ctas, st);
+  return launch_one<MmaConsumer<__half, D, 32, false, 1, true>, kMmaConsumerWarps>(prm, max_ctas, st);
+}
+
+cudaError_t launch_view_f16(const KParams& prm, int D, int BS, int max_ctas, cudaStream_t st) {
+  switch (D) {
+    case 64: return go<64>(prm, BS, max_ctas, st);
+    case 80: return go<80>(prm, BS, max_ctas, st);
+    case 96: return go<96>(prm, BS, max_ctas, st);
+    case 112: return go<112>(prm, BS, max_ctas, st);
+    case 128: return go<128>(prm, BS, max_ctas, st);
+    default: return go<256>(prm, BS, max_ctas, st);
+  }
+}
+
+}  // namespace pa

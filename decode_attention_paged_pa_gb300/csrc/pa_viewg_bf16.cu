@@ -1,0 +1,27 @@
+// pa_viewg_bf16.cu -- view instances (windows, trees) of the paged decode kernel
+// with the tensor-core (mma.sync) consumer over pairs of kv heads (four query
+// rows each), blocks of 8, 16 or 32 tokens, element type
+// __nv_bfloat16, head sizes up to 128.
+#include "pa_launch.cuh"
+#include "pa_mma.cuh"
+
+namespace pa {
+
+template <int D>
+static cudaError_t go(const KParams& prm, int BS, int max_ctas, cudaStream_t st) {
+  if (BS == 8) return launch_one<MmaConsumer<__nv_bfloat16, D, 8, false, 2, true>, kMmaConsumerWarps>(prm, max_ctas, st);
+  if (BS == 16) return launch_one<MmaConsumer<__nv_bfloat16, D, 16, false, 2, true>, kMmaConsumerWarps>(prm, max_ctas, st);
+  return launch_one<MmaConsumer<__nv_bfloat16, D, 32, false, 2, true>, kMmaConsumerWarps>(prm, max_ctas, st);
+}
+
+cudaError_t launch_view_g_bf16(const KParams& prm, int D, int BS, int max_ctas, cudaStream_t st) {
+  switch (D) {
+    case 64: return go<64>(prm, BS, max_ctas, st);
+    case 80: return go<80>(prm, BS, max_ctas, st);
+    case 96: return go<96>(prm, BS, max_ctas, st);
+    case 112: return go<112>(prm, BS, max_ctas, st);
+    default: return go<128>(prm, BS, max_ctas, st);
+  }
+}
+
+}  // namespace pa

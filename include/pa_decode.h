@@ -3,6 +3,9 @@
  * ("PagedAttention V2": partitioned online softmax followed by a
  * cross-partition log-sum-exp combine): single-query decode (pa_decode_v2,
  * pa_decode_v2_ex, pa_decode_v2_lse), multi-query decode (pa_decode_v2_mq),
+ * sliding windows (pa_decode_v2_window), trees of drafted tokens
+ * (pa_decode_v2_tree; pa_tree_masks, pa_tree_accept), slot maps and the writing of
+ * new tokens (pa_pages_slots, pa_cache_write),
  * E4M3 (fp8) caches (pa_decode_v2_fp8), 4-bit caches (pa_decode_v2_kv4,
  * pa_decode_v2_mq_kv4; written and read back with pa_kv4_append and
  * pa_kv4_gather), the pages of a pool managed on the device (pa_pages_fork,
@@ -61,6 +64,8 @@ extern "C" {
 
 /* Element types of query, caches and output. */
 enum { PA_DTYPE_FP16 = 0, PA_DTYPE_BF16 = 1, PA_DTYPE_FP32 = 2 };
+/* ... and of caches alone (pa_cache_write, pa_tree_accept). */
+enum { PA_DTYPE_E4M3 = 3 };
 
 /* Status codes. */
 enum {
@@ -273,6 +278,193 @@ int pa_decode_v2_mq_fp8(void* out, float* lse, const void* query, const void* ke
                         int num_heads, int num_kv_heads, int head_size, int block_size,
                         int partition_size, int dtype, void* stream, int max_blocks_per_seq,
                         int num_blocks, void* workspace, size_t workspace_bytes);
+
+/*
+ * Attention to a sliding window and to the first tokens, for layers that look
+ * back a fixed number of tokens.  Rows, tables and lengths are those of
+ * pa_decode_v2_mq (q_len = 1: of pa_decode_v2_lse): row i of sequence s is at
+ * position p = L - q_len + i, and sees position t where
+ *     t <= p   and   (t > p - window  or  t < sinks)
+ * so a window counts the row's own token.  A window of L or more is
+ * pa_decode_v2_mq's rule.
+ *   window      1 or more
+ *   sinks       first tokens that stay visible, 0 or more
+ *   seq_lens    [num_seqs] int32, each in [q_len, max_blocks_per_seq*block_size];
+ *               a single row (q_len = 1) also takes 0.  Other lengths are recorded
+ *               as PA_ERR_DEVICE_BOUNDS; a length below q_len then gives zeros and
+ *               -INFINITY, as an empty sequence does.
+ *   block_tables  only the entries of blocks with a position that some row of
+ *               the sequence sees are read: blocks between the first tokens and
+ *               the window may have been given back
+ *   q_len       1 .. 512
+ *   workspace   >= pa_decode_v2_view_workspace_bytes(num_seqs, q_len, ...) bytes,
+ *               or NULL.  Partitions count the visible blocks only.
+ * Elements, shapes, lse, ownership and errors are those of pa_decode_v2_mq (fp32:
+ * not blocks of 64 tokens at head size 256, PA_ERR_UNSUPPORTED).  A key or value
+ * that is not finite reaches the rows that see it, no others.
+ */
+int pa_decode_v2_window(void* out, float* lse, const void* query, const void* key_cache,
+                        const void* value_cache, const int32_t* block_tables, const int32_t* seq_lens,
+                        float scale, int window, int sinks, int num_seqs, int q_len, int num_heads,
+                        int num_kv_heads, int head_size, int block_size, int partition_size, int dtype,
+                        void* stream, int max_blocks_per_seq, int num_blocks, void* workspace,
+                        size_t workspace_bytes);
+
+/* pa_decode_v2_window over an E4M3 cache (caches and scales of pa_decode_v2_mq_fp8). */
+int pa_decode_v2_window_fp8(void* out, float* lse, const void* query, const void* key_cache,
+                            const void* value_cache, const int32_t* block_tables, const int32_t* seq_lens,
+                            float scale, float k_scale, float v_scale, int window, int sinks, int num_seqs,
+                            int q_len, int num_heads, int num_kv_heads, int head_size, int block_size,
+                            int partition_size, int dtype, void* stream, int max_blocks_per_seq,
+                            int num_blocks, void* workspace, size_t workspace_bytes);
+
+/*
+ * Attention for a tree of drafted tokens.  The last num_nodes cached tokens of
+ * each sequence are the nodes (their K and V are in the cache, in any order that
+ * puts a parent before its children): node i's K and V are those of position
+ * L - num_nodes + i.  Node i sees
+ *     position t < L - num_nodes: the tokens before the tree, and
+ *     node j where bit j % 32 of masks[s][i][j / 32] is set
+ * and a node whose mask has no bit is padding: it sees nothing, its row is zeros
+ * and its lse -INFINITY.  A chain (node i sees nodes 0 .. i) is pa_decode_v2_mq.
+ * With a window, node i is at position p = L - num_nodes + (bits of its mask) - 1
+ * (its depth in the tree) and sees of the tokens before the tree those with
+ * t > p - window or t < sinks.
+ *   query, out  [num_seqs, num_nodes, num_heads, head_size]   dtype
+ *   lse         NULL, or DEVICE [num_seqs, num_nodes, num_heads] fp32
+ *   masks       DEVICE [num_seqs, num_nodes, ceil(num_nodes / 32)] int32, as
+ *               pa_tree_masks makes them (once for all layers of a step).  Any masks
+ *               will do; bits past num_nodes have to be 0.
+ *   window      0: no window (sinks then says nothing), or num_nodes or more
+ *   seq_lens    each in [num_nodes, max_blocks_per_seq*block_size] (others:
+ *               PA_ERR_DEVICE_BOUNDS; below num_nodes: zeros)
+ *   num_nodes   1 .. 512
+ *   workspace   >= pa_decode_v2_view_workspace_bytes(num_seqs, num_nodes, ...)
+ * All else is as for pa_decode_v2_window.
+ */
+int pa_decode_v2_tree(void* out, float* lse, const void* query, const void* key_cache,
+                      const void* value_cache, const int32_t* block_tables, const int32_t* seq_lens,
+                      const int32_t* masks, float scale, int window, int sinks, int num_seqs, int num_nodes,
+                      int num_heads, int num_kv_heads, int head_size, int block_size, int partition_size,
+                      int dtype, void* stream, int max_blocks_per_seq, int num_blocks, void* workspace,
+                      size_t workspace_bytes);
+
+/* pa_decode_v2_tree over an E4M3 cache (caches and scales of pa_decode_v2_mq_fp8). */
+int pa_decode_v2_tree_fp8(void* out, float* lse, const void* query, const void* key_cache,
+                          const void* value_cache, const int32_t* block_tables, const int32_t* seq_lens,
+                          const int32_t* masks, float scale, float k_scale, float v_scale, int window,
+                          int sinks, int num_seqs, int num_nodes, int num_heads, int num_kv_heads,
+                          int head_size, int block_size, int partition_size, int dtype, void* stream,
+                          int max_blocks_per_seq, int num_blocks, void* workspace, size_t workspace_bytes);
+
+/*
+ * Bytes of workspace for pa_decode_v2_window and pa_decode_v2_tree (q_len:
+ * num_nodes; window 0: a tree without one).  0 for invalid sizes.
+ */
+size_t pa_decode_v2_view_workspace_bytes(int num_seqs, int q_len, int num_heads, int num_kv_heads,
+                                         int head_size, int max_blocks_per_seq, int block_size,
+                                         int partition_size, int window, int sinks);
+
+/*
+ * The masks of trees given by their nodes' parents:
+ *   parents     [num_seqs, num_nodes] int32: the parent's number, below the node's
+ *               own; -1 for a child of the tokens before the tree; below -1 for
+ *               padding
+ *   masks       [num_seqs, num_nodes, ceil(num_nodes / 32)] int32, written: a
+ *               node's bits are its own and its ancestors'; padding has none
+ *   positions   NULL, or [num_seqs, num_nodes] int32, written: seq_lens[s] -
+ *               num_nodes + depth (a child of the tokens before the tree has
+ *               depth 0), for rotary embeddings; -1 for padding
+ *   seq_lens    [num_seqs] int32, counting the nodes
+ *   num_nodes   1 .. 512
+ *   workspace   >= 256 bytes, 16-byte aligned, required; holds the status, whatever
+ *               it held before
+ * A parent that is not below its node, a child of padding (both become padding),
+ * and a length below num_nodes (positions of -1) are recorded as
+ * PA_ERR_DEVICE_BOUNDS.  What is written may not overlap another array
+ * (PA_ERR_INVALID_ARG).
+ */
+int pa_tree_masks(int32_t* masks, int32_t* positions, const int32_t* parents, const int32_t* seq_lens,
+                  int num_seqs, int num_nodes, void* stream, void* workspace, size_t workspace_bytes);
+
+/*
+ * After verification: the accepted nodes' K and V move to the front of the tree's
+ * part of the cache, in the caches of every layer, and lengths follow.  Sequence
+ * s keeps nodes accepted[s][0 .. num_accepted[s]), ascending: node accepted[s][i]
+ * goes to position L - num_nodes + i, and new_lens[s] = L - num_nodes +
+ * num_accepted[s] (what pa_pages_resize takes).  Positions from there on hold
+ * what they held or a moved token.
+ *   key_caches, value_caches   HOST arrays of num_caches DEVICE pointers, 16-byte
+ *               aligned: caches of one shape and element type (layouts of
+ *               pa_decode_v2 and pa_decode_v2_fp8); read before the call returns
+ *   accepted    [num_seqs, max_accepted] int32 (entries past num_accepted are not
+ *               read); max_accepted 0 .. 512
+ *   num_accepted  [num_seqs] int32, each in [0, max_accepted]
+ *   new_lens    [num_seqs] int32, written; may not overlap another array
+ *   num_nodes   1 .. 512
+ *   cache_dtype PA_DTYPE_FP16, _BF16, _FP32 or _E4M3
+ *   workspace   >= 256 bytes, 16-byte aligned, required; holds the status
+ * The positions from L - num_nodes on must not be shared with another sequence (as
+ * pa_pages_resize leaves them).  A length out of range, a count or path that is
+ * not as above, and block ids outside the pool are recorded as
+ * PA_ERR_DEVICE_BOUNDS: such a sequence keeps its cache, and new_lens[s] is L.
+ * One launch (one more per further 64 caches).
+ */
+int pa_tree_accept(int32_t* new_lens, void* const* key_caches, void* const* value_caches, int num_caches,
+                   const int32_t* block_tables, const int32_t* seq_lens, const int32_t* accepted,
+                   const int32_t* num_accepted, int num_seqs, int num_nodes, int max_accepted,
+                   int num_kv_heads, int head_size, int block_size, int cache_dtype, void* stream,
+                   int max_blocks_per_seq, int num_blocks, void* workspace, size_t workspace_bytes);
+
+/*
+ * The rows of a step, numbered from its requests' lengths.  Sequence s has
+ * num_new[s] new tokens, its last ones (seq_lens counts them already, as after
+ * pa_pages_resize).  With cu[s] the sum of num_new before s, row cu[s] + i of the
+ * step is sequence s at position seq_lens[s] - num_new[s] + i.
+ *   cu_tokens   [num_seqs + 1] int32, written: cu (at most 2^31 - 1), as
+ *               pa_kv4_append takes it
+ *   slots       [num_tokens] int64, written: block * block_size + offset of each
+ *               row, as pa_cache_write takes it; -1 for rows of no sequence
+ *   positions, seq_ids   NULL, or [num_tokens] int32, written: -1 for rows of no
+ *               sequence
+ *   num_tokens  rows there is room for: more than the step has, where a captured
+ *               graph keeps its size
+ *   block_size  any positive number
+ *   workspace   >= 256 bytes, 16-byte aligned, required; holds the status
+ * A negative count (taken as 0), more rows than num_tokens (those behind are left
+ * out), a length below the count or above the table's capacity (slots and
+ * positions of -1) and a negative block id (slots of -1) are recorded as
+ * PA_ERR_DEVICE_BOUNDS.  What is written may not overlap another array
+ * (PA_ERR_INVALID_ARG).
+ */
+int pa_pages_slots(int64_t* slots, int32_t* positions, int32_t* seq_ids, int32_t* cu_tokens,
+                   const int32_t* block_tables, const int32_t* seq_lens, const int32_t* num_new,
+                   int num_seqs, int num_tokens, int max_blocks_per_seq, int block_size, void* stream,
+                   void* workspace, size_t workspace_bytes);
+
+/*
+ * Writes new tokens into the caches that pa_decode_v2 and pa_decode_v2_fp8 read.
+ *   key, value   [num_tokens, num_kv_heads, head_size] dtype (fp16, bf16 or fp32),
+ *                rows key_stride / value_stride elements apart (whole 16 bytes, at
+ *                least num_kv_heads * head_size), 16-byte aligned
+ *   slots        [num_tokens] int64: row r goes to offset slots[r] % block_size of
+ *                block slots[r] / block_size; a negative slot skips the row.  Slots
+ *                of a call differ (of two rows with one slot, either's bytes may
+ *                stay).  Slots past the pool are recorded as PA_ERR_DEVICE_BOUNDS and
+ *                skipped.
+ *   cache_dtype  dtype: rows are copied (k_scale and v_scale are 1); or
+ *                PA_DTYPE_E4M3: codes of x / k_scale and x / v_scale, computed in
+ *                fp32, rounded to the nearest E4M3 (ties to even) and kept within
+ *                +-448 (infinities too; NaN becomes NaN), so that a code c stands for
+ *                scale * c as pa_decode_v2_fp8 reads it; scales positive and finite
+ *   workspace    >= 256 bytes, 16-byte aligned, required; holds the status
+ * Only the rows' slots are written.  One launch on `stream`; it can be captured
+ * into a CUDA graph.
+ */
+int pa_cache_write(void* key_cache, void* value_cache, const void* key, const void* value,
+                   const int64_t* slots, float k_scale, float v_scale, int num_tokens, int num_kv_heads,
+                   int head_size, int block_size, long long key_stride, long long value_stride, int dtype,
+                   int cache_dtype, void* stream, int num_blocks, void* workspace, size_t workspace_bytes);
 
 /*
  * Caches held in 4 bits.  The pages' launcher takes a kv_cache_dtype (page

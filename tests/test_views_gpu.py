@@ -1,0 +1,302 @@
+"""Windowed and tree attention (pa_decode_v2_window, pa_decode_v2_tree and their
+forms over E4M3 caches) against plain 64-bit attention over the tokens each row
+sees, within bounds derived in view_testutil."""
+import math
+
+import pytest
+import torch
+
+from decode_attention_paged_pa_gb300 import PaError, binding
+from view_testutil import ancestors, attend64, caches, pack, tree_parents, visible
+
+pytestmark = pytest.mark.gpu
+
+K_SCALE, V_SCALE = 0.5, 1.25
+NAN_E4M3 = 0x7F
+
+
+def make(seed, dtype, cache, n, H, KH, D, BS, lens, window, sinks, see=None, poison=True):
+    """Inputs on the CPU: shuffled pages; table entries of blocks that no row sees
+    are -1, and every slot that no row sees holds NaN."""
+    S, MB = len(lens), max(1, max(-(-v // BS) for v in lens) + 1)
+    g = torch.Generator().manual_seed(seed)
+    q = torch.randn((S, n, H, D), generator=g).to(dtype)
+    kc, vc = caches(seed + 1, S * MB, KH, D, BS, torch.uint8 if cache == "e4m3" else dtype)
+    bt = torch.randperm(S * MB, generator=g).view(S, MB).to(torch.int32)
+    if poison:
+        bad = NAN_E4M3 if cache == "e4m3" else float("nan")
+        for s, L in enumerate(lens):
+            seen = visible(L, n, window, sinks, None if see is None else see[s]).any(0)
+            for b in range(MB):
+                part = seen[b * BS:(b + 1) * BS]
+                for o in range(BS):
+                    if o >= part.numel() or not bool(part[o]):
+                        kc[bt[s, b], :, :, o] = bad
+                        vc[bt[s, b], :, :, o] = bad
+                if not bool(part.any()) and not (see is not None and L - n < (b + 1) * BS and b * BS < L):
+                    bt[s, b] = -1  # (blocks of a tree's nodes are all there)
+    return q, kc, vc, bt, torch.tensor(lens, dtype=torch.int32)
+
+
+def run(q, kc, vc, bt, lens, scale, window, sinks, see=None, P=64, single=False, status=binding.PA_OK, ws=None):
+    dev = torch.device("cuda")
+    d = [t.to(dev) for t in (q, kc, vc, bt, lens)]
+    if single:
+        d[0] = d[0].squeeze(1)
+    out = torch.full_like(d[0], float("nan"))
+    lse = torch.full(d[0].shape[:-1], float("nan"), device=dev)
+    more = dict(partition_size=P, lse=lse, workspace=ws)
+    fp8 = kc.dtype == torch.uint8
+    if fp8:
+        more |= dict(k_scale=K_SCALE, v_scale=V_SCALE)
+    if see is None:
+        call = binding.pa_decode_v2_window_fp8 if fp8 else binding.pa_decode_v2_window
+        ws = call(out, *d, scale, window, sinks, **more)
+    else:
+        call = binding.pa_decode_v2_tree_fp8 if fp8 else binding.pa_decode_v2_tree
+        ws = call(out, *d, pack(see).to(dev), scale, window=window, sinks=sinks, **more)
+    assert binding.device_status(ws) == status
+    return out.cpu().view(q.shape), lse.cpu().view(q.shape[:-1])
+
+
+def check(got, lse, q, kc, vc, bt, lens, scale, window, sinks, see=None):
+    ref, ref_lse, bound = attend64(q, kc, vc, bt, lens, scale, window, sinks, see, K_SCALE, V_SCALE)
+    err = (got.double() - ref).abs()
+    assert bool((err <= bound).all()), f"worst excess {float((err - bound).max()):.3e}, NaN {int(got.isnan().sum())}"
+    empty = ref_lse.isinf()
+    assert bool((lse[empty] == -math.inf).all())
+    assert bool((got[empty] == 0).all())
+    # fp32 sums of at most a few thousand terms, and scores of about 10 or less.
+    assert bool(((lse.double() - ref_lse)[~empty].abs() <= 1e-4 + 1e-5 * ref_lse[~empty].abs()).all())
+
+
+LENS = [1, 15, 16, 17, 64, 65, 127, 300, 5]
+SHAPES = [("fp16", "same", 4, 4, 64, 16), ("bf16", "same", 8, 2, 128, 16), ("fp16", "same", 4, 1, 128, 32),
+          ("bf16", "same", 6, 2, 96, 8), ("fp16", "same", 8, 2, 80, 8), ("bf16", "same", 5, 1, 256, 16),
+          ("fp16", "same", 2, 2, 112, 64), ("bf16", "same", 12, 1, 64, 32), ("fp32", "same", 2, 1, 64, 16),
+          ("fp32", "same", 2, 2, 128, 64), ("fp32", "same", 1, 1, 256, 8), ("fp16", "e4m3", 8, 2, 128, 16),
+          ("bf16", "e4m3", 4, 4, 64, 8), ("fp16", "e4m3", 6, 2, 112, 32), ("bf16", "e4m3", 3, 1, 256, 64),
+          ("bf16", "e4m3", 8, 2, 64, 8)]
+T = {"fp16": torch.float16, "bf16": torch.bfloat16, "fp32": torch.float32}
+IDS = ["-".join(map(str, s)) for s in SHAPES]
+
+
+@pytest.mark.parametrize("window,sinks", [(1, 0), (2, 1), (16, 4), (17, 33), (100, 0), (64, 300), (1 << 31, 7)])
+@pytest.mark.parametrize("shape", SHAPES, ids=IDS)
+def test_window_single(shape, window, sinks):
+    dtype, cache, H, KH, D, BS = shape
+    lens = LENS + [0, 200]
+    case = make(7 + D + window % 1000, T[dtype], cache, 1, H, KH, D, BS, lens, window, sinks)
+    got, lse = run(*case, 0.11, window, sinks, single=True)
+    check(got, lse, *case, 0.11, window, sinks)
+
+
+@pytest.mark.parametrize("n,window,sinks", [(2, 1, 0), (4, 3, 2), (7, 40, 20), (33, 17, 4), (3, 1000, 4)])
+@pytest.mark.parametrize("shape", SHAPES, ids=IDS)
+def test_window_rows(shape, n, window, sinks):
+    dtype, cache, H, KH, D, BS = shape
+    lens = [n + v for v in (0, 1, 15, 16, 60, 190)]
+    case = make(70 + D + n, T[dtype], cache, n, H, KH, D, BS, lens, window, sinks)
+    got, lse = run(*case, 0.11, window, sinks)
+    check(got, lse, *case, 0.11, window, sinks)
+
+
+@pytest.mark.parametrize("n,window,sinks", [(1, 0, 0), (2, 0, 0), (7, 0, 0), (7, 7, 3), (16, 40, 20), (33, 0, 0),
+                                            (65, 70, 0)])
+@pytest.mark.parametrize("shape", SHAPES, ids=IDS)
+def test_tree(shape, n, window, sinks):
+    dtype, cache, H, KH, D, BS = shape
+    lens = [n + v for v in (0, 1, 16, 47, 190)]
+    see = torch.stack([ancestors(tree_parents(n + s, n, max(1, n - s))) for s in range(len(lens))])
+    case = make(700 + D + n, T[dtype], cache, n, H, KH, D, BS, lens, window, sinks, see)
+    got, lse = run(*case, 0.11, window, sinks, see)
+    check(got, lse, *case, 0.11, window, sinks, see)
+
+
+@pytest.mark.parametrize("shape", SHAPES, ids=IDS)
+def test_values_that_are_not_finite_reach_the_rows_that_see_them(shape):
+    """Nodes 1 and 2 are siblings: 1's key and value are NaN, 2's value has an
+    infinity of each sign; neither reaches the other's row, nor node 3's below 0."""
+    dtype, cache, H, KH, D, BS = shape
+    n, lens = 4, [40, 21]
+    see = ancestors([-1, 0, 0, 0]).expand(2, 4, 4).clone()
+    q, kc, vc, bt, L = make(5, T[dtype], cache, n, H, KH, D, BS, lens, 0, 0, see, poison=False)
+    clean = kc.clone(), vc.clone()
+    for s, length in enumerate(lens):
+        b1, o1 = bt[s, (length - 3) // BS], (length - 3) % BS
+        b2, o2 = bt[s, (length - 2) // BS], (length - 2) % BS
+        kc[b1, :, :, o1] = NAN_E4M3 if cache == "e4m3" else float("nan")
+        vc[b1, :, :, o1] = NAN_E4M3 if cache == "e4m3" else float("nan")
+        if cache != "e4m3":
+            vc[b2, :, 0, o2], vc[b2, :, 1, o2] = float("inf"), -float("inf")
+    got, lse = run(q, kc, vc, bt, L, 0.11, 0, 0, see)
+    ref, ref_lse, bound = attend64(q, *clean, bt, L, 0.11, 0, 0, see, K_SCALE, V_SCALE)
+    assert bool(got[:, 1].isnan().all()) and bool(lse[:, 1].isnan().all())
+    rows = [0, 3]
+    assert bool(((got.double() - ref).abs() <= bound)[:, rows].all())
+    if cache != "e4m3":
+        assert bool((got[:, 2, :, 0] == math.inf).all()) and bool((got[:, 2, :, 1] == -math.inf).all())
+        assert bool(((got.double() - ref).abs() <= bound)[:, 2, :, 2:].all())
+
+
+@pytest.mark.parametrize("cache", ["same", "e4m3"])
+def test_window_of_everything_is_multi_query_decode(cache):
+    q, kc, vc, bt, L = make(3, torch.float16, cache, 4, 8, 2, 128, 16, [4, 90, 700], 1000, 0, poison=False)
+    got, lse = run(q, kc, vc, bt, L, 0.1, 1000, 0, P=128)
+    dev = torch.device("cuda")
+    out = torch.empty_like(q, device=dev)
+    d = [t.to(dev) for t in (q, kc, vc, bt, L)]
+    if cache == "e4m3":
+        binding.pa_decode_v2_mq_fp8(out, *d, 0.1, k_scale=K_SCALE, v_scale=V_SCALE, partition_size=128)
+    else:
+        binding.pa_decode_v2_mq(out, *d, 0.1, partition_size=128)
+    # Two orders of the same fp32 sums, each rounded to fp16 (and its weights).
+    assert bool(((got - out.cpu()).abs() <= 2.0 ** -9 * (1 + got.abs())).all())
+
+
+@pytest.mark.parametrize("P", [16, 64, 512, 1 << 30])
+def test_partitions(P):
+    """Windows over long sequences: one or many partitions, the same workspace
+    reused with a larger one's contents."""
+    lens, window, sinks = [5000, 4097, 1030, 64, 1], 1024, 20
+    case = make(9, torch.bfloat16, "same", 1, 8, 2, 128, 16, lens, window, sinks)
+    for _ in range(2):
+        got, lse = run(*case, 0.09, window, sinks, P=P, single=True)
+        check(got, lse, *case, 0.09, window, sinks)
+
+
+def test_many_sequences_and_a_poisoned_workspace():
+    """More sequences than one launch takes; the workspace starts as 0x7f bytes."""
+    g = torch.Generator().manual_seed(4)
+    lens = torch.randint(3, 120, (600,), generator=g).tolist()
+    case = make(11, torch.float16, "same", 3, 4, 2, 64, 16, lens, 24, 2)
+    n = binding.view_workspace_bytes(600, 3, 4, 2, 64, case[3].shape[1], 16, 16, 24, 2)
+    ws = torch.full((n,), 0x7F, dtype=torch.uint8, device="cuda")
+    got, lse = run(*case, 0.12, 24, 2, P=16, ws=ws)
+    check(got, lse, *case, 0.12, 24, 2)
+
+
+def test_bad_lengths_and_ids_are_recorded():
+    q, kc, vc, bt, L = make(13, torch.float16, "same", 4, 4, 2, 64, 16, [50, 3, 40], 16, 0, poison=False)
+    got, lse = run(q, kc, vc, bt, L, 0.1, 16, 0, status=binding.PA_ERR_DEVICE_BOUNDS)
+    assert bool((got[1] == 0).all()) and bool((lse[1] == -math.inf).all())
+    ref, _, bound = attend64(q, kc, vc, bt, L, 0.1, 16, 0)
+    assert bool(((got.double() - ref).abs() <= bound)[[0, 2]].all())
+    L2 = torch.tensor([50, 60, 40], dtype=torch.int32)
+    bt2 = bt.clone()
+    bt2[2, 2] = kc.shape[0]
+    got, _ = run(q, kc, vc, bt2, L2, 0.1, 16, 0, status=binding.PA_ERR_DEVICE_BOUNDS)
+    ref, _, bound = attend64(q, kc, vc, bt, L2, 0.1, 16, 0)
+    assert bool(((got.double() - ref).abs() <= bound)[:2].all())
+    see = ancestors([-1, 0, 0, 1]).expand(3, 4, 4).clone()
+    got, lse = run(q, kc, vc, bt, torch.tensor([50, 0, 40], dtype=torch.int32), 0.1, 0, 0, see,
+                   status=binding.PA_ERR_DEVICE_BOUNDS)
+    assert bool((got[1] == 0).all())
+
+
+@pytest.mark.parametrize("op", ["window", "tree"])
+def test_captured_and_on_another_stream(op):
+    """A captured call replayed with other lengths, masks and queries; then two
+    calls at once on two streams with workspaces of their own."""
+    dev = torch.device("cuda")
+    n, H, KH, D, BS, P = 5, 8, 2, 128, 16, 64
+    see_a = ancestors([-1, 0, 1, 0, 3]).expand(3, n, n).clone()
+    see_b = ancestors([-1, -1, 1, 2, 3]).expand(3, n, n).clone()
+    window, sinks = (32, 4) if op == "window" else (0, 0)
+    see = (None, None) if op == "window" else (see_a, see_b)
+    a = make(1, torch.float16, "same", n, H, KH, D, BS, [200, 30, 7], window, sinks, see[0], poison=False)
+    b = make(1, torch.float16, "same", n, H, KH, D, BS, [40, 190, 111], window, sinks, see[1], poison=False)
+    q2, lens2 = torch.flip(a[0], [0]), b[4]
+    d = [t.to(dev) for t in a]
+    masks = pack(see_a).to(dev)
+    out = torch.empty_like(d[0])
+    ws = torch.empty(binding.view_workspace_bytes(3, n, H, KH, D, a[3].shape[1], BS, P, window, sinks),
+                     dtype=torch.uint8, device=dev)
+
+    def call(o, x, w, stream=None):
+        if op == "window":
+            binding.pa_decode_v2_window(o, *x, 0.1, window, sinks, partition_size=P, workspace=w, stream=stream)
+        else:
+            binding.pa_decode_v2_tree(o, *x, masks, 0.1, partition_size=P, workspace=w, stream=stream)
+
+    call(out, d, ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(out, d, ws)
+    for q, lens, s in ((a[0], a[4], see[0]), (q2, lens2, see[1]), (a[0], a[4], see[0])):
+        d[0].copy_(q)
+        d[4].copy_(lens)
+        if s is not None:
+            masks.copy_(pack(s))
+        out.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert binding.device_status(ws) == binding.PA_OK
+        ref, _, bound = attend64(q, a[1], a[2], a[3], lens, 0.1, window, sinks, s)
+        assert bool(((out.cpu().double() - ref).abs() <= bound).all())
+    outs = [torch.full_like(out, float("nan")) for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(5):
+        for o, st in zip(outs, streams):
+            st.wait_stream(torch.cuda.current_stream())
+            call(o, d, None, st)
+    torch.cuda.synchronize()
+    for o in outs:
+        assert torch.equal(o, out)
+
+
+def test_repeats_are_bitwise_equal():
+    case = make(21, torch.bfloat16, "same", 16, 32, 8, 128, 16, [900, 333, 1500, 64], 0, 0,
+                see := torch.stack([ancestors(tree_parents(s, 16)) for s in range(4)]), poison=False)
+    first = run(*case, 0.09, 0, 0, see, P=256)
+    for _ in range(3):
+        again = run(*case, 0.09, 0, 0, see, P=256)
+        assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+
+
+def test_pool_past_4_gb():
+    """Blocks whose bytes lie past 2^32 of the caches."""
+    dev = torch.device("cuda")
+    KH, D, BS = 8, 128, 16
+    NB = (1 << 32) // (KH * D * BS * 2) * 5 // 4
+    kc = torch.zeros((NB, KH, D // 8, BS, 8), dtype=torch.float16, device=dev)
+    vc = torch.zeros((NB, KH, D, BS), dtype=torch.float16, device=dev)
+    small = make(31, torch.float16, "same", 2, 8, 8, D, BS, [100, 70], 50, 4, poison=False)
+    used = torch.tensor([NB - 1 - 3 * i for i in range(small[1].shape[0])])
+    kc[used.to(dev)] = small[1].to(dev)
+    vc[used.to(dev)] = small[2].to(dev)
+    bt = used[small[3].long()].to(torch.int32)
+    out = torch.empty_like(small[0], device=dev)
+    ws = binding.pa_decode_v2_window(out, small[0].to(dev), kc, vc, bt.to(dev), small[4].to(dev), 0.1, 50, 4)
+    assert binding.device_status(ws) == binding.PA_OK
+    ref, _, bound = attend64(*small, 0.1, 50, 4)
+    assert bool(((out.cpu().double() - ref).abs() <= bound).all())
+
+
+def test_refusals():
+    dev = torch.device("cuda")
+    q, kc, vc, bt, L = (t.to(dev) for t in make(1, torch.float16, "same", 4, 4, 2, 64, 16, [40, 30], 16, 0,
+                                                 poison=False))
+    out = torch.empty_like(q)
+    masks = torch.zeros((2, 4, 1), dtype=torch.int32, device=dev)
+    ok = lambda **kw: binding.pa_decode_v2_tree(out, q, kc, vc, bt, L, masks, 0.1, **kw)
+    ok(window=4)
+    for bad in (dict(window=3), dict(window=-1), dict(sinks=-1), dict(partition_size=24)):
+        with pytest.raises(PaError):
+            ok(**bad)
+    for window, sinks in ((0, 0), (-5, 0), (4, -1)):
+        with pytest.raises(PaError):
+            binding.pa_decode_v2_window(out, q, kc, vc, bt, L, 0.1, window, sinks)
+    with pytest.raises(PaError):
+        binding.pa_decode_v2_window(out, q, kc, vc, bt, L, 0.1, 16, workspace=torch.empty(256, dtype=torch.uint8, device=dev))
+    with pytest.raises(ValueError):
+        binding.pa_decode_v2_tree(out, q, kc, vc, bt, L, masks[:, :3], 0.1)
+    with pytest.raises(TypeError):
+        binding.pa_decode_v2_tree(out, q, kc, vc, bt, L, masks.long(), 0.1)
+    with pytest.raises(ValueError):
+        binding.pa_decode_v2_tree(out[:, 0], q[:, 0], kc, vc, bt, L, masks, 0.1)
+    with pytest.raises(TypeError):
+        binding.pa_decode_v2_window_fp8(out, q, kc, vc, bt, L, 0.1, 16)
+    with pytest.raises(ValueError):
+        binding.pa_decode_v2_window(out, q, kc.cpu(), vc, bt, L, 0.1, 16)
