@@ -76,6 +76,9 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB_PATH)
+    # (Every build compiles all sources, so the objects, as large as the library, are of no more use.)
+    for obj in objs:
+        os.remove(obj)
     return LIB_PATH
 
 
