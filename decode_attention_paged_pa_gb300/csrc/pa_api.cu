@@ -296,7 +296,11 @@ int decode_impl(void* out, float* lse, const void* query, const void* key_cache,
   // Over a 4-bit cache, 16 rows a unit where a kv head has more than 8: its
   // codes are unpacked once for both halves.
   const int nt = kv4 && G > kMmaGroup && D <= 128 ? 2 : 1;
-  const int gt = kv4 ? nt * kMmaGroup : (variant == PA_VARIANT_MMA) ? (wide ? kMmaGroupWide : kMmaGroup) : kSimtGroup;
+  const int gt = view && variant == PA_VARIANT_MMA && !kv_fp8 && G > kMmaGroup ? rows_per_unit(D)
+                 : kv4 ? nt * kMmaGroup : (variant == PA_VARIANT_MMA) ? (wide ? kMmaGroupWide : kMmaGroup) : kSimtGroup;
+  // View rows: with more than eight a kv head, 128 or 256 of them a unit on the
+  // fifth-generation tensor cores (pa_rows.cuh), over 16-bit caches.
+  const bool many = view && variant == PA_VARIANT_MMA && !kv_fp8 && G > kMmaGroup;
   // Four query rows per kv head (query heads, or multi-query row heads): a
   // unit's 8 columns take two kv heads (one block copy each for keys and
   // values covers both), head sizes up to 128 and blocks of 8, 16 or 32 tokens.
@@ -309,7 +313,7 @@ int decode_impl(void* out, float* lse, const void* query, const void* key_cache,
   const int kvu = pairs || kv4_pairs ? 2 : 1;
   const int hg_per_kv = (G + gt - 1) / gt;
   const int n_hg = KH * hg_per_kv / kvu;
-  const int rows_per_launch = kMaxSeqsPerLaunch;  // sequences per launch
+  const int rows_per_launch = many ? kRowsSeqsPerLaunch : kMaxSeqsPerLaunch;  // sequences per launch
   const int chunk = S < rows_per_launch ? S : rows_per_launch;
   if ((long long)chunk * w.pmax * n_hg > INT_MAX / 2) return PA_ERR_UNSUPPORTED;
   // The tensor-core kernels over 16-bit caches in blocks of 16 tokens or more
@@ -379,7 +383,9 @@ int decode_impl(void* out, float* lse, const void* query, const void* key_cache,
       prm.masks = view->tree ? reinterpret_cast<const uint32_t*>(view->masks) + (size_t)s0 * q_len * prm.words : nullptr;
     }
     cudaError_t e;
-    if (view)
+    if (many)
+      e = dtype == PA_DTYPE_FP16 ? launch_rows_f16(prm, D, BS, max_ctas, st) : launch_rows_bf16(prm, D, BS, max_ctas, st);
+    else if (view)
       e = launch_views(prm, dtype, kv_fp8, pairs, D, BS, max_ctas, st);
     else if (kv4)
       e = dtype == PA_DTYPE_FP16 ? launch_kv4_f16(prm, D, BS, nt, kvu, max_ctas, st)

@@ -824,11 +824,113 @@ __device__ __forceinline__ void epilogue_loop(const KParams& prm, uint8_t* smem,
   }
 }
 
+// Longest-first order.  Every CTA computes the same order from the lengths:
+// perm[r] = the sequence of rank r, sequences sorted by partition count,
+// most first (counts of 127 or more as equals), ties in batch order (a
+// stable counting sort); pref[r] = partitions of ranks before r.  Lengths
+// are clamped to [0, MB*BS]; an out-of-range length is recorded as a device
+// error.  Temporaries live in `tmp`: the ring,
+// unused until the producer starts.
+template <int MODE, int BS, int THREADS>
+__device__ __forceinline__ void plan_order(const KParams& prm, uint8_t* tmp, int* pref, uint16_t* perm,
+                                           int* bad_len) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  constexpr int NW = THREADS / 32;
+  constexpr int NBK = 128;  // sort buckets
+  static_assert(THREADS % 32 == 0 && NW <= 32, "whole warps, at most 32");
+  const int S = prm.S, nthr = THREADS, max_len = prm.MB * BS;
+  int* bucket = reinterpret_cast<int*>(tmp);       // [NBK] counts, then next free rank
+  int* parts = bucket + NBK;                          // [S] partitions per sequence
+  int* scan = parts + kMaxSeqsPerLaunch;              // [2 * NW] warp totals, then warp starts
+  for (int i = tid; i < NBK; i += nthr) bucket[i] = 0;
+  __syncthreads();
+  for (int s = tid; s < S; s += nthr) {
+    bool bad = false;
+    const int L = work_tokens<MODE>(prm, seq_tokens<MODE>(prm, s, max_len, &bad), BS);
+    if (bad) *bad_len = 1;
+    const int np = (L + prm.P - 1) / prm.P;
+    parts[s] = np;
+    atomicAdd(&bucket[NBK - 1 - min(np, NBK - 1)], 1);
+  }
+  __syncthreads();
+  if (warp == 0) {
+    constexpr int PER = NBK / 32;  // buckets per lane: exclusive scan of the counts
+    int v[PER], tot = 0;
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+      v[j] = bucket[lane * PER + j];
+      tot += v[j];
+    }
+    int incl = tot;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int n = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += n;
+    }
+    int start = incl - tot;
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+      bucket[lane * PER + j] = start;
+      start += v[j];
+    }
+    __syncwarp();
+    // 32 sequences at a time, in batch order: lanes with the same bucket
+    // take consecutive ranks in lane order.
+    for (int c0 = 0; c0 < S; c0 += 32) {
+      const int s = c0 + lane;
+      const int key = s < S ? NBK - 1 - min(parts[s], NBK - 1) : -1 - lane;
+      const unsigned peers = __match_any_sync(0xffffffffu, key);
+      const int before = __popc(peers & ((1u << lane) - 1u));
+      const int base = s < S ? bucket[key] : 0;
+      __syncwarp();
+      if (s < S) {
+        perm[base + before] = (uint16_t)s;
+        if (before == 0) bucket[key] = base + __popc(peers);
+      }
+      __syncwarp();
+    }
+  }
+  __syncthreads();
+  // pref over ranks: thread t sums a contiguous range of ranks; an exclusive
+  // scan of those sums (within each warp, then over the warp totals).
+  const int per = (S + nthr - 1) / nthr;
+  const int beg = min(tid * per, S), end = min(beg + per, S);
+  int sum = 0;
+  for (int r = beg; r < end; ++r) sum += parts[perm[r]];
+  int incl = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int n = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += n;
+  }
+  if (lane == 31) scan[warp] = incl;
+  __syncthreads();
+  if (warp == 0) {
+    const int t = lane < NW ? scan[lane] : 0;
+    int ti = t;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int n = __shfl_up_sync(0xffffffffu, ti, o);
+      if (lane >= o) ti += n;
+    }
+    if (lane < NW) scan[NW + lane] = ti - t;  // warp starts
+    if (lane == NW - 1) pref[S] = ti;
+  }
+  __syncthreads();
+  int run = scan[NW + warp] + incl - sum;
+  for (int r = beg; r < end; ++r) {
+    pref[r] = run;
+    run += parts[perm[r]];
+  }
+}
+constexpr int kOrderTempBytes = (128 + kMaxSeqsPerLaunch + 64) * 4;  // plan_order's temporaries
+
 template <class C, int NC, int NSTAGE, int CTAS_PER_SM, int MODE>
 __global__ void __launch_bounds__(Layout<C, NC, NSTAGE>::THREADS, CTAS_PER_SM)
     pa_decode_kernel(const __grid_constant__ KParams prm) {
   using LY = Layout<C, NC, NSTAGE>;
   constexpr int NS = LY::NSTAGE, UQ = LY::UQ;
+  static_assert(LY::RING >= kOrderTempBytes, "prologue temporaries fit in the ring");
   extern __shared__ __align__(1024) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t sbase = smem_addr(smem);
@@ -856,102 +958,7 @@ __global__ void __launch_bounds__(Layout<C, NC, NSTAGE>::THREADS, CTAS_PER_SM)
     *bad_len = 0;
     fence_mbarrier_init();
   }
-  // Longest-first order.  Every CTA computes the same order from the lengths:
-  // perm[r] = the sequence of rank r, sequences sorted by partition count,
-  // most first (counts of 127 or more as equals), ties in batch order (a
-  // stable counting sort); pref[r] = partitions of ranks before r.  Lengths
-  // are clamped to [0, MB*BS]; an out-of-range length is recorded as a device
-  // error.  Temporaries live in the ring, unused until the producer starts.
-  {
-    constexpr int NW = LY::THREADS / 32;
-    constexpr int NBK = 128;  // sort buckets
-    static_assert(LY::THREADS % 32 == 0 && NW <= 32, "whole warps, at most 32");
-    static_assert(LY::RING >= (NBK + kMaxSeqsPerLaunch + 2 * NW) * 4, "prologue temporaries fit in the ring");
-    const int S = prm.S, nthr = LY::THREADS, max_len = prm.MB * C::BS;
-    int* bucket = reinterpret_cast<int*>(smem);       // [NBK] counts, then next free rank
-    int* parts = bucket + NBK;                          // [S] partitions per sequence
-    int* scan = parts + kMaxSeqsPerLaunch;              // [2 * NW] warp totals, then warp starts
-    for (int i = tid; i < NBK; i += nthr) bucket[i] = 0;
-    __syncthreads();
-    for (int s = tid; s < S; s += nthr) {
-      bool bad = false;
-      const int L = work_tokens<MODE>(prm, seq_tokens<MODE>(prm, s, max_len, &bad), C::BS);
-      if (bad) *bad_len = 1;
-      const int np = (L + prm.P - 1) / prm.P;
-      parts[s] = np;
-      atomicAdd(&bucket[NBK - 1 - min(np, NBK - 1)], 1);
-    }
-    __syncthreads();
-    if (warp == 0) {
-      constexpr int PER = NBK / 32;  // buckets per lane: exclusive scan of the counts
-      int v[PER], tot = 0;
-#pragma unroll
-      for (int j = 0; j < PER; ++j) {
-        v[j] = bucket[lane * PER + j];
-        tot += v[j];
-      }
-      int incl = tot;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int n = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += n;
-      }
-      int start = incl - tot;
-#pragma unroll
-      for (int j = 0; j < PER; ++j) {
-        bucket[lane * PER + j] = start;
-        start += v[j];
-      }
-      __syncwarp();
-      // 32 sequences at a time, in batch order: lanes with the same bucket
-      // take consecutive ranks in lane order.
-      for (int c0 = 0; c0 < S; c0 += 32) {
-        const int s = c0 + lane;
-        const int key = s < S ? NBK - 1 - min(parts[s], NBK - 1) : -1 - lane;
-        const unsigned peers = __match_any_sync(0xffffffffu, key);
-        const int before = __popc(peers & ((1u << lane) - 1u));
-        const int base = s < S ? bucket[key] : 0;
-        __syncwarp();
-        if (s < S) {
-          perm[base + before] = (uint16_t)s;
-          if (before == 0) bucket[key] = base + __popc(peers);
-        }
-        __syncwarp();
-      }
-    }
-    __syncthreads();
-    // pref over ranks: thread t sums a contiguous range of ranks; an exclusive
-    // scan of those sums (within each warp, then over the warp totals).
-    const int per = (S + nthr - 1) / nthr;
-    const int beg = min(tid * per, S), end = min(beg + per, S);
-    int sum = 0;
-    for (int r = beg; r < end; ++r) sum += parts[perm[r]];
-    int incl = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int n = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += n;
-    }
-    if (lane == 31) scan[warp] = incl;
-    __syncthreads();
-    if (warp == 0) {
-      const int t = lane < NW ? scan[lane] : 0;
-      int ti = t;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int n = __shfl_up_sync(0xffffffffu, ti, o);
-        if (lane >= o) ti += n;
-      }
-      if (lane < NW) scan[NW + lane] = ti - t;  // warp starts
-      if (lane == NW - 1) pref[S] = ti;
-    }
-    __syncthreads();
-    int run = scan[NW + warp] + incl - sum;
-    for (int r = beg; r < end; ++r) {
-      pref[r] = run;
-      run += parts[perm[r]];
-    }
-  }
+  plan_order<MODE, C::BS, LY::THREADS>(prm, smem, pref, perm, bad_len);
   __syncthreads();
   // This launch is a programmatic dependent of the kernel that clears the
   // workspace header: everything above overlaps it, nothing below may touch

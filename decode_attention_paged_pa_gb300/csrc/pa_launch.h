@@ -87,6 +87,14 @@ cudaError_t launch_view8_g_f16(const KParams& prm, int D, int BS, int max_ctas, 
 cudaError_t launch_view8_g_bf16(const KParams& prm, int D, int BS, int max_ctas, cudaStream_t st);
 cudaError_t launch_view_f32(const KParams& prm, int D, int BS, int max_ctas, cudaStream_t st);
 cudaError_t launch_view_x_f32(const KParams& prm, int D, int BS, int max_ctas, cudaStream_t st);
+// ... and with many rows a kv head, over 16-bit caches (_x: head sizes from 112).
+cudaError_t launch_rows_f16(const KParams& prm, int D, int BS, int max_ctas, cudaStream_t st);
+cudaError_t launch_rows_bf16(const KParams& prm, int D, int BS, int max_ctas, cudaStream_t st);
+cudaError_t launch_rows_x_f16(const KParams& prm, int D, int BS, int max_ctas, cudaStream_t st);
+cudaError_t launch_rows_x_bf16(const KParams& prm, int D, int BS, int max_ctas, cudaStream_t st);
+// Sequences of a launch, and rows of a unit at head size D.
+constexpr int kRowsSeqsPerLaunch = 256;
+constexpr int rows_per_unit(int D) { return D <= 128 ? 256 : 128; }
 
 // Over a 4-bit cache (queries and output fp16 / bf16), by head size: blocks of
 // 8, 16, 32 or 64 tokens, units of nt * 8 query rows of a kv head, or (kvu = 2, up

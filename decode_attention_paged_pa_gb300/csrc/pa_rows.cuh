@@ -1,0 +1,704 @@
+// pa_rows.cuh -- view attention (windows, trees) with many query rows a kv head, on
+// the fifth-generation tensor cores (16-bit caches).
+//
+// The rows of a kv head (query tokens x query heads of its group) are the M = 128
+// side of the products, so that a block of the cache is read once for 128 rows (256
+// in a unit of two row tiles), where the units of 8 rows of pa_mma.cuh read it
+// once for 8:
+//
+//   S[rows x tokens] = Q[rows x D] . K^T       tcgen05.mma, Q and K in shared memory
+//   O[rows x D]     += P[rows x tokens] . V    tcgen05.mma, P in tensor memory
+//
+// Both operands of the cache are read as they lie in the page layouts.  A key block
+// [D/8][BS][8] is a column of core matrices (8 tokens x 16 bytes); one instruction
+// takes the same eight tokens of every block of a tile (the stride between rows of
+// core matrices is that between blocks), so the scores of a tile of TN tokens come
+// in BS / 8 instructions a k-step, their columns ordered (group of eight tokens,
+// block, token).  A value block [D][BS] is K-major with rows of 2 BS bytes: the
+// tensor copy stores it in the swizzle of that width.
+//
+// One CTA per SM, persistent over units (sequence, partition, kv head, up to GT
+// rows), which a producer warp takes from the global counter (as in pa_kernel.cuh)
+// and streams through a ring of K and V tiles.  One thread issues the products.
+// Warpgroups of four warps, a row a thread, turn scores into weights: two of them
+// (NP = 2) work in turns.  With at most 128 rows in a unit both have the same rows
+// and take the tiles alternately, each with its own O, joined at the end of the
+// unit; with more, each has a row tile and takes every tile.  At head size 256 (NP
+// = 1) one warpgroup does all, with two buffers of scores.
+//
+// Softmax: scores in fp32; a row keeps a reference (the maximum when it was last
+// set) and sets a new one, rescaling O, only where its maximum has grown by more
+// than 2^8 over it: weights stay below 2^8, whose sums in fp32 and, for fp16,
+// roundings are as exact as those of weights below 1.  Weights are rounded to the
+// element type; bf16 ones as the sum of two terms (two products), as in pa_mma.cuh.
+//
+// Tensor memory (512 columns of 128 lanes): scores of either pipeline, overlaid by
+// its weights once they are read, and O of either.  A product that writes scores
+// over weights is issued behind the one that reads them, by the same thread.
+//
+// A tile that some row does not see whole is masked row by row, eight tokens at a
+// time; values of it that are not finite are cleared in shared memory (their
+// products with other rows' zero weights would be NaN), and the rows that do see
+// them get them added at the end of the unit.
+#pragma once
+
+#include <type_traits>
+
+#include "pa_kernel.cuh"
+#include "pa_tc.cuh"
+
+namespace pa {
+
+constexpr int kRowsMaxUnitSeqs = 256;  // sequences per launch (the order's arrays take shared memory)
+constexpr uint32_t kRowsSmem = 227u * 1024u;
+
+struct RowsUnit {
+  int s, p, kv, t0, t1, nt, np, nh, h0, L, sink_blocks, skip;
+};
+
+template <typename T_, int D_, int BS_>
+struct RowsConfig {
+  using T = T_;
+  static constexpr int D = D_, BS = BS_;
+  static constexpr int NP = D_ <= 128 ? 2 : 1;     // pipelines (warpgroups)
+  static constexpr int TN = D_ <= 128 ? 128 : 64;  // tokens per tile
+  static constexpr int GT = 128 * NP, KVU = 1;     // rows per unit; (plan_unit) kv heads per unit
+  static constexpr int NB = TN / BS, NG = BS / 8;  // blocks of a tile, groups of eight tokens of a block
+  static constexpr bool kTma = BS_ >= 16;
+  static constexpr bool kBf16 = std::is_same<T_, __nv_bfloat16>::value;
+  static constexpr uint32_t BLK = (uint32_t)D_ * BS_ * 2, SLOT = (uint32_t)TN * D_ * 2, QTILE = 128u * D_ * 2;
+  static constexpr int THREADS = NP * 128 + 64, UQ = 2;
+  // Tensor memory columns.
+  static constexpr uint32_t S_COL = 0, O_COL = 2 * TN, O_STEP = 128;
+  static_assert(2 * TN + (NP == 2 ? 256 : 256) <= 512, "tensor memory");
+  // Shared memory: Q tiles, the ring, then barriers, units, flags, order.
+  static constexpr uint32_t QBYTES = NP * QTILE;
+  static constexpr uint32_t small(int ns) {
+    return al16((2 * ns + 2 * UQ + 11) * 8) + al16(UQ * sizeof(RowsUnit)) + 64 + al16((kRowsMaxUnitSeqs + 1) * 4) +
+           al16(kRowsMaxUnitSeqs * 2);
+  }
+  static constexpr int NS = (int)((kRowsSmem - small(16) - QBYTES) / SLOT) < 16
+                                ? (int)((kRowsSmem - small(16) - QBYTES) / SLOT)
+                                : 16;
+  static_assert(NS >= 3, "the ring holds a tile's keys and values and the next keys");
+  static constexpr uint32_t OFF_RING = QBYTES, OFF_BAR = OFF_RING + NS * SLOT;
+  static constexpr uint32_t OFF_INFO = OFF_BAR + al16((2 * NS + 2 * UQ + 11) * 8);
+  static constexpr uint32_t OFF_FLAGS = OFF_INFO + al16(UQ * sizeof(RowsUnit));
+  static constexpr uint32_t OFF_PREF = OFF_FLAGS + 64;
+  static constexpr uint32_t OFF_PERM = OFF_PREF + al16((kRowsMaxUnitSeqs + 1) * 4);
+  static constexpr uint32_t BYTES = OFF_PERM + al16(kRowsMaxUnitSeqs * 2);
+  static_assert(BYTES <= kRowsSmem && QBYTES % 1024 == 0 && SLOT % 1024 == 0, "shared memory");
+  static_assert(NS * SLOT >= kOrderTempBytes, "prologue temporaries fit in the ring");
+  // Barriers.
+  static constexpr uint32_t FULL = 0, EMPTY = NS, UFULL = 2 * NS, UEMPTY = UFULL + UQ, QFULL = UEMPTY + UQ,
+                            QFREE = QFULL + 1, SFULL = QFREE + 1, PREADY = SFULL + 2, PVDONE = PREADY + 2,
+                            OFREE = PVDONE + 2, XBAR = OFREE + 1, DRAIN = XBAR + 1;
+  static_assert(DRAIN + 1 == 2 * NS + 2 * UQ + 11, "barriers");
+};
+
+// Wait sites of this kernel (see WaitSite).
+enum RowsSite {
+  kRowsUnitSlot = 20, kRowsRing = 21, kRowsUnit = 22, kRowsQ = 23, kRowsOFree = 24, kRowsFull = 25, kRowsP = 26,
+  kRowsS = 27, kRowsPv = 28, kRowsQFree = 29, kRowsX = 30
+};
+
+template <class C>
+struct RowsCta {
+  const KParams& prm;
+  uint8_t* smem;
+  uint32_t sbase, bar0;
+  volatile int* abort_flag;
+  int* err;
+
+  __device__ __forceinline__ RowsCta(const KParams& p, uint8_t* sm)
+      : prm(p), smem(sm), sbase(smem_addr(sm)), bar0(sbase + C::OFF_BAR),
+        abort_flag(reinterpret_cast<volatile int*>(sm + C::OFF_FLAGS)), err(p.hdr + kHdrError) {}
+  __device__ __forceinline__ uint32_t bar(uint32_t i) const { return bar0 + 8 * i; }
+  __device__ __forceinline__ bool wait(uint32_t b, uint32_t phase, int site, int detail) const {
+    return wait_bounded(bar(b), phase & 1u, abort_flag, err, prm.timeout_ns, site, detail);
+  }
+  // Ring item g (keys and values of the CTA's tiles in turn).
+  __device__ __forceinline__ uint32_t slot(uint32_t g) const { return g % C::NS; }
+  __device__ __forceinline__ uint32_t phase(uint32_t g) const { return g / C::NS; }
+
+  // Position of block vb of those that the sequence's rows can see.
+  static __device__ __forceinline__ int block_pos(const RowsUnit& U, int vb) {
+    return (vb + (vb < U.sink_blocks ? 0 : U.skip)) * C::BS;
+  }
+
+  // The unit of a plan, cut to the tokens that some row of it sees.
+  __device__ __forceinline__ RowsUnit cut(const UnitPlan& P) const {
+    RowsUnit U{P.s, P.p, P.kv, P.t0, P.t1, 0, P.np, P.nh, P.h0, P.L, P.span.sink_blocks, P.span.skip};
+    if (!prm.masks) {
+      const int l0 = P.h0 - P.kv * prm.G, first = P.L - prm.q_len;
+      const int i0 = l0 / prm.Gu, i1 = (l0 + P.nh - 1) / prm.Gu;  // its first and last query token
+      const int skip = U.skip * C::BS;
+      // (The skipped blocks lie before every row's window, and before its end.)
+      U.t1 = min(U.t1, first + i1 + 1 - skip);
+      const int lo = first + i0 - prm.window + 1 - skip;
+      if (U.t0 >= U.sink_blocks * C::BS && lo > U.t0) {
+        // (Without skipped blocks, the first tokens lie where they are.)
+        if (U.skip > 0 || U.t0 >= prm.sinks) U.t0 += (lo - U.t0) / C::TN * C::TN;
+      }
+    }
+    U.nt = U.t1 > U.t0 ? (U.t1 - U.t0 + C::TN - 1) / C::TN : 0;
+    return U;
+  }
+
+  // ---------------------------------------------------------------- producer warp
+  __device__ __forceinline__ int fetch_ids(const RowsUnit& U, int b0, int lane) const {
+    const int nb = (U.t1 - U.t0 + C::BS - 1) / C::BS;
+    if (b0 + lane >= nb) return 0;
+    int j = U.t0 / C::BS + b0 + lane;
+    j += j < U.sink_blocks ? 0 : U.skip;
+    return __ldg(prm.bt + (size_t)U.s * prm.MB + j);
+  }
+
+  __device__ __forceinline__ void producer(const int* pref, const uint16_t* perm, int lane) {
+    constexpr int NB = C::NB, PER = 32 / NB;  // tiles whose ids a warp holds
+    RowsUnit* info = reinterpret_cast<RowsUnit*>(smem + C::OFF_INFO);
+    const uint64_t pol = l2_policy_evict_first();
+    const int total = pref[prm.S] * prm.n_hg;
+    fence_proxy_async_smem();  // the prologue's temporaries lay in the ring
+    uint32_t g = 0, k = 0;
+    int u = blockIdx.x;
+    bool ok = true;
+    while (ok) {
+      const bool have = u < total;
+      RowsUnit U{};
+      if (have) U = cut(plan_unit<C, kView>(prm, pref, perm, u));
+      else U.s = -1;
+      // Publish it.
+      const uint32_t us = k % C::UQ;
+      ok = __shfl_sync(0xffffffffu, lane == 0 ? (int)wait(C::UEMPTY + us, k / C::UQ + 1, kRowsUnitSlot, (int)k) : 0, 0);
+      if (!ok) break;
+      if (lane == 0) {
+        info[us] = U;
+        mbar_arrive(bar(C::UFULL + us));
+      }
+      ++k;
+      if (!have) break;
+      int ids = fetch_ids(U, 0, lane), ids_next = U.nt > PER ? fetch_ids(U, 32, lane) : 0, claimed = 0;
+      if (U.nt == 0 && lane == 0) claimed = atomicAdd(prm.hdr + kHdrWork, 1);
+      for (int j = 0; j < U.nt && ok; ++j) {
+        if (j > 0 && j % PER == 0) {
+          ids = ids_next;
+          if (j + PER < U.nt) ids_next = fetch_ids(U, (j + PER) * NB, lane);
+        }
+        // (The next unit is taken while this one's last tile is on its way.)
+        if (j + 1 == U.nt && lane == 0) claimed = atomicAdd(prm.hdr + kHdrWork, 1);
+        const int nb = min(NB, (U.t1 - U.t0 - j * C::TN + C::BS - 1) / C::BS);
+        const int id = check_block_id(prm, __shfl_sync(0xffffffffu, ids, (j % PER) * NB + (lane < nb ? lane : 0)));
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {  // keys, values
+          const uint32_t sl = slot(g), fb = bar(C::FULL + sl), dst = sbase + C::OFF_RING + sl * C::SLOT;
+          ok = __shfl_sync(0xffffffffu, lane == 0 ? (int)wait(C::EMPTY + sl, phase(g) + 1, kRowsRing, (int)g) : 0, 0);
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_expect_tx(fb, (uint32_t)nb * C::BLK);
+          __syncwarp();
+          if (lane < nb) {
+            const size_t row = (size_t)id * prm.KH + U.kv;
+            if (w == 0 || !C::kTma)
+              bulk_copy_g2s(dst + lane * C::BLK, static_cast<const uint8_t*>(w ? prm.vc : prm.kc) + row * C::BLK,
+                            C::BLK, fb, pol);
+            else  // (x = 0: the 16-byte alignment rule holds)
+              tma_load_3d(dst + lane * C::BLK, &prm.tmv, 0, 0, (int)row, fb, pol);
+          }
+          ++g;
+        }
+      }
+      u = __shfl_sync(0xffffffffu, claimed, 0) + (int)gridDim.x;
+    }
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    // Copies in flight land before the CTA ends, whatever the others did.
+    if (lane == 0)
+      for (uint32_t i = g > (uint32_t)C::NS ? g - C::NS : 0u; i < g; ++i) {
+        const uint64_t t0 = global_timer_ns();
+        while (!mbar_try_wait(bar(C::FULL + slot(i)), phase(i) & 1u) && global_timer_ns() - t0 < 100000000ull) {
+        }
+      }
+    __syncwarp();
+  }
+
+  // ---------------------------------------------------------------- product thread
+  // Scores of ring slot `sl` against Q tile q, into score buffer b.
+  __device__ __forceinline__ void issue_scores(uint32_t tmem, int q, uint32_t sl, int b, uint32_t idesc) const {
+    const uint32_t qa = sbase + q * C::QTILE, ka = sbase + C::OFF_RING + sl * C::SLOT;
+    constexpr int NI = C::NB == 1 ? 1 : C::NG;         // instructions a k-step
+    constexpr int N = C::TN / NI;                      // columns of each
+    constexpr uint32_t STRIDE = C::NB == 1 ? 128u : C::BLK;
+#pragma unroll
+    for (int kk = 0; kk < C::D / 16; ++kk) {
+      const uint64_t a = smem_desc(qa + kk * 4096, 2048, 128, kSwizzleNone);
+#pragma unroll
+      for (int i = 0; i < NI; ++i)
+        mma_ss(tmem + C::S_COL + b * C::TN + i * N, a,
+               smem_desc(ka + kk * 2 * C::BS * 16 + i * 128, C::BS * 16, STRIDE, kSwizzleNone), idesc, kk > 0);
+    }
+  }
+  // O[o] (+)= weights of buffer b times the values in slot `sl`, `ks` k-steps.
+  __device__ __forceinline__ void issue_values(uint32_t tmem, int o, uint32_t sl, int b, int ks, uint32_t idesc,
+                                               bool add) const {
+    const uint32_t va = sbase + C::OFF_RING + sl * C::SLOT, d = tmem + C::O_COL + o * C::O_STEP;
+    const uint32_t p = tmem + C::S_COL + b * C::TN;
+#pragma unroll
+    for (int h = 0; h < (C::kBf16 ? 2 : 1); ++h) {
+#pragma unroll
+      for (int k = 0; k < C::TN / 16; ++k) {
+        if (k >= ks) break;
+        uint64_t v;
+        if constexpr (C::BS == 8) {
+          v = smem_desc(va + 2 * k * C::BLK, C::BLK, 128, kSwizzleNone);
+        } else {
+          constexpr int KB = C::BS / 16;  // k-steps of a block
+          constexpr uint32_t SW = C::BS == 16 ? kSwizzle32 : C::BS == 32 ? kSwizzle64 : kSwizzle128;
+          v = smem_desc(va + (k / KB) * C::BLK + (k % KB) * 32, 16, C::BS * 16, SW);
+        }
+        mma_ts(d, p + h * (C::TN / 2) + k * 8, v, idesc, add || h > 0 || k > 0);
+      }
+    }
+  }
+  __device__ __forceinline__ void products(uint32_t tmem) {
+    const RowsUnit* info = reinterpret_cast<const RowsUnit*>(smem + C::OFF_INFO);
+    constexpr int N = C::NB == 1 ? C::TN : C::TN / C::NG;
+    const uint32_t id_s = f16_idesc(C::kBf16, N), id_o = f16_idesc(C::kBf16, C::D);
+    uint32_t g = 0, k = 0;          // ring items and units before this unit
+    uint32_t np_[2] = {0, 0};       // weights taken from each buffer
+    bool ok = true;
+    while (ok) {
+      if (!wait(C::UFULL + k % C::UQ, k / C::UQ, kRowsUnit, (int)k)) break;
+      const RowsUnit U = info[k % C::UQ];
+      mbar_arrive(bar(C::UEMPTY + k % C::UQ));
+      if (U.s < 0) break;
+      const bool both = C::NP == 2 && U.nh > 128;  // a row tile for each pipeline
+      const int steps = both ? 2 * U.nt : U.nt;
+      if (!wait(C::QFULL, k, kRowsQ, (int)k)) break;
+      tc_fence_after();
+      // (Scores of step i + 2 go where the weights of step i were.)
+      const auto scores = [&](int i) {
+        const int j = both ? i >> 1 : i;
+        const uint32_t it = g + 2 * j;
+        if (!both || !(i & 1)) {
+          if (!wait(C::FULL + slot(it), phase(it), kRowsFull, (int)it)) return false;
+        }
+        issue_scores(tmem, both ? i & 1 : 0, slot(it), i & 1, id_s);
+        mma_commit(bar(C::SFULL + (i & 1)));
+        if (!both || (i & 1)) mma_commit(bar(C::EMPTY + slot(it)));
+        return true;
+      };
+      for (int i = 0; i < 2 && i < steps && ok; ++i) ok = scores(i);
+      for (int i = 0; i < steps && ok; ++i) {
+        const int j = both ? i >> 1 : i, b = i & 1, o = C::NP == 2 ? b : 0;
+        const uint32_t it = g + 2 * j + 1;
+        ok = wait(C::FULL + slot(it), phase(it), kRowsFull, (int)it);
+        if (ok && i < 2) ok = wait(C::OFREE, k + 1, kRowsOFree, (int)k);  // the last unit's O is read
+        if (ok) ok = wait(C::PREADY + b, np_[b], kRowsP, i);
+        if (!ok) break;
+        ++np_[b];
+        tc_fence_after();
+        const int left = U.t1 - U.t0 - j * C::TN;
+        issue_values(tmem, o, slot(it), b, left >= C::TN ? C::TN / 16 : (left + 15) / 16, id_o,
+                     C::NP == 2 ? i >= 2 : i >= 1);
+        mma_commit(bar(C::PVDONE + o));
+        if (!both || (i & 1)) mma_commit(bar(C::EMPTY + slot(it)));
+        if (i + 2 < steps) ok = scores(i + 2);
+      }
+      if (!ok) break;
+      mma_commit(bar(C::QFREE));
+      g += 2 * U.nt;
+      ++k;
+    }
+    // What has been issued completes before tensor memory is freed.
+    mma_commit(bar(C::DRAIN));
+    const uint64_t t0 = global_timer_ns();
+    while (!mbar_try_wait(bar(C::DRAIN), 0) && global_timer_ns() - t0 < 100000000ull) {
+    }
+  }
+
+  // ---------------------------------------------------------------- softmax warpgroups
+  // The tokens of a group of eight that a row sees: positions p .. p + 7, `n` of them
+  // in the unit.
+  static __device__ __forceinline__ uint32_t first_bits(int n) { return n >= 8 ? 0xffu : n <= 0 ? 0u : (1u << n) - 1u; }
+  __device__ __forceinline__ uint32_t group_seen(const RowView& v, int p, int n) const {
+    uint32_t m = first_bits(min(v.hi - p, n));
+    m &= ~first_bits(v.lo - p) | first_bits(prm.sinks - p);
+    if (v.bits && p + 7 >= v.base) {
+      const int off = p - v.base;
+      uint64_t w;
+      if (off < 0) {
+        w = (uint64_t)__ldg(v.bits) << -off | ((1ull << -off) - 1);
+      } else {
+        const int i = off >> 5;
+        w = i < prm.words ? __ldg(v.bits + i) : 0u;
+        if (i + 1 < prm.words) w |= (uint64_t)__ldg(v.bits + i + 1) << 32;
+        w >>= off & 31;
+      }
+      m &= (uint32_t)w;
+    }
+    return m;
+  }
+
+  // Byte offset of tokens 8c .. 8c + 7 of dim d in a staged value block.
+  static __device__ __forceinline__ uint32_t value_chunk(int d, int c) {
+    constexpr uint32_t ROW = C::BS * 2;
+    if constexpr (C::kTma) return d * ROW + ((c ^ ((d * ROW >> 7) & (ROW / 16 - 1))) << 4);
+    else return d * ROW + c * 16;
+  }
+
+  // A tile's values: those past the unit's end, and of the others those that are
+  // not finite, are cleared.  128 threads.  True if there was one of the latter.
+  __device__ __forceinline__ bool clear_values(uint32_t sl, int left, int tid) const {
+    constexpr uint32_t kExp = C::kBf16 ? 0x7f80u : 0x7c00u;
+    uint8_t* v = smem + C::OFF_RING + sl * C::SLOT;
+    const int groups = min(C::TN / 8, (left + 15) / 16 * 2);
+    bool found = false;
+    for (int i = tid; i < C::D * groups; i += 128) {
+      const int gr = i / C::D, d = i - gr * C::D, b = gr / C::NG, c = gr % C::NG, n = left - gr * 8;
+      uint4* at = reinterpret_cast<uint4*>(v + b * C::BLK + value_chunk(d, c));
+      if (n <= 0) {
+        *at = make_uint4(0, 0, 0, 0);
+        continue;
+      }
+      uint4 x = *at;
+      uint32_t w[4] = {x.x, x.y, x.z, x.w};
+      bool change = false;
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const bool past = 2 * q + h >= n;
+          const bool odd = ((w[q] >> (16 * h)) & kExp) == kExp;
+          if (past || odd) {
+            w[q] &= h ? 0xffffu : 0xffff0000u;
+            change = true;
+          }
+          found |= odd && !past;
+        }
+      if (change) *at = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    return found;
+  }
+
+  // Values that are not finite, of dims d0 .. d0 + 15, added to the row that sees
+  // their tokens (rare; the cache itself is read).
+  __device__ __noinline__ void add_odd(const RowsUnit& U, const RowView& v, int d0, float* o) const {
+    using T = typename C::T;
+    const T* vc = static_cast<const T*>(prm.vc);
+    for (int t = U.t0; t < U.t1; ++t) {
+      const int vb = t / C::BS, pos = block_pos(U, vb) + t % C::BS;
+      if (!(group_seen(v, pos, 1) & 1u)) continue;
+      int id = prm.bt[(size_t)U.s * prm.MB + pos / C::BS];
+      if ((unsigned)id >= (unsigned)prm.num_blocks) id = 0;
+      const T* blk = vc + ((size_t)id * prm.KH + U.kv) * C::D * C::BS;
+      for (int i = 0; i < 16; ++i) {
+        const float x = (float)blk[(d0 + i) * C::BS + t % C::BS];
+        if (!(fabsf(x) < INFINITY)) o[i] += x;
+      }
+    }
+  }
+
+  __device__ __forceinline__ void softmax(uint32_t tmem, int wg, int tid) {
+    using T = typename C::T;
+    constexpr int TN = C::TN, NB = C::NB, NG = C::NG, D = C::D;
+    const RowsUnit* info = reinterpret_cast<const RowsUnit*>(smem + C::OFF_INFO);
+    volatile int* odd_unit = reinterpret_cast<volatile int*>(smem + C::OFF_FLAGS + 16);
+    const int lane = tid & 31;
+    const uint32_t lanes = (uint32_t)(tid & ~31) << 16;  // this warp's lanes of tensor memory
+    // (The sign of the scale goes to Q.)
+    const uint32_t flip = prm.scale_log2 < 0.f ? 0x80008000u : 0u;
+    const float sl2 = fmaxf(fabsf(prm.scale_log2), 1.17549435e-38f);
+    const uint64_t pol_keep = l2_policy_evict_last();
+    uint32_t g = 0, k = 0, ns_[2] = {0, 0}, npv = 0;  // ring items, units, scores read (a buffer), products into O
+    while (true) {
+      const bool okw = wait(C::UFULL + k % C::UQ, k / C::UQ, kRowsUnit, (int)k);
+      if (!__all_sync(0xffffffffu, okw)) break;
+      const RowsUnit U = info[k % C::UQ];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(C::UEMPTY + k % C::UQ));
+      if (U.s < 0) break;
+      const bool both = C::NP == 2 && U.nh > 128;
+      const int row = both ? wg * 128 + tid : tid;  // the thread's row of the unit
+      const bool mine = row < U.nh;
+      RowView v{0, 0, 0, nullptr};
+      if (mine) v = row_view(prm, U.s, U.L, U.h0 + row);
+      // Q: the unit's row tiles, [D/8][128 rows] 16-byte pieces.
+      if (!__all_sync(0xffffffffu, wait(C::QFREE, k + 1, kRowsQFree, (int)k))) break;
+      {
+        const T* q = static_cast<const T*>(prm.q) + (mine ? out_row<kView>(prm, U.s, U.h0 + row) : 0) * D;
+        uint8_t* dst = smem + (both ? wg : 0) * C::QTILE + tid * 16;
+        const bool shared_rows = C::NP == 2 && !both;  // both warpgroups have the rows: half of the pieces each
+        for (int c = shared_rows ? wg : 0; c < D / 8; c += shared_rows ? 2 : 1) {
+          uint4 x = mine ? reinterpret_cast<const uint4*>(q)[c] : make_uint4(0, 0, 0, 0);
+          x.x ^= flip; x.y ^= flip; x.z ^= flip; x.w ^= flip;
+          *reinterpret_cast<uint4*>(dst + c * 2048) = x;
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(bar(C::QFULL));
+      }
+      // Positions that every row of the unit sees (padding apart).
+      int full_lo, full_hi;
+      {
+        const int first = U.L - prm.q_len, l0 = U.h0 - U.kv * prm.G;
+        const int i0 = l0 / prm.Gu, i1 = (l0 + U.nh - 1) / prm.Gu;
+        full_hi = prm.masks ? first : first + i0 + 1;
+        full_lo = prm.window > 0 ? (prm.masks ? U.L - prm.window : first + i1 - prm.window + 1) : 0;
+      }
+      float mref = -INFINITY, l = 0.f;
+      const int steps = both ? 2 * U.nt : U.nt;
+      int done = 0;  // this warpgroup's steps of the unit
+      bool ok = true;
+      for (int i = C::NP == 2 ? wg : 0; i < steps && ok; i += C::NP, ++done) {
+        const int j = both ? i >> 1 : i, b = i & 1;
+        const uint32_t sc = tmem + lanes + C::S_COL + b * TN;
+        const int tile = U.t0 + j * TN, left = U.t1 - tile, vb0 = tile / C::BS;
+        ok = __all_sync(0xffffffffu, wait(C::SFULL + b, ns_[b], kRowsS, i));
+        if (!ok) break;
+        ++ns_[b];
+        tc_fence_after();
+        float s[TN];
+#pragma unroll
+        for (int c = 0; c < TN; c += 32) tmem_ld32(sc + c, s + c);
+        // Whether every row sees the whole tile.
+        const int p0 = block_pos(U, vb0), p1 = block_pos(U, vb0 + (min(left, TN) - 1) / C::BS) + C::BS - 1;
+        const bool jump = vb0 < U.sink_blocks && U.skip > 0;
+        const bool partial = left < TN || jump || p1 >= full_hi || (p0 < full_lo && p1 >= prm.sinks);
+        tmem_wait_ld();
+        if (partial) {
+          // (Values: before the weights of the tile are announced.)
+          const uint32_t it = g + 2 * j + 1;
+          ok = __all_sync(0xffffffffu, wait(C::FULL + slot(it), phase(it), kRowsFull, (int)it));
+          if (!ok) break;
+          if (clear_values(slot(it), left, tid)) *odd_unit = (int)k + 1;
+          fence_proxy_async_smem();
+#pragma unroll
+          for (int gi = 0; gi < NG; ++gi)
+#pragma unroll
+            for (int bi = 0; bi < NB; ++bi) {
+              const uint32_t m = group_seen(v, block_pos(U, vb0 + bi) + gi * 8, left - bi * C::BS - gi * 8);
+#pragma unroll
+              for (int t = 0; t < 8; ++t)
+                if (!((m >> t) & 1u)) s[(gi * NB + bi) * 8 + t] = -INFINITY;
+            }
+          __syncwarp();
+        }
+        float mx = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < TN; ++c) mx = fmaxf(mx, s[c]);
+        mx *= sl2;
+        if (v.hi == 0) mx = -INFINITY;  // (padding, and rows past the unit's: weights of no use)
+        const bool first = C::NP == 2 ? done == 0 : i == 0;
+        if (mx > mref + 8.f || (mref == -INFINITY && mx > -INFINITY)) {
+          const float alpha = exp2_approx(mref - mx);
+          l *= alpha;
+          const bool had = mref > -INFINITY;
+          mref = mx;
+          mx = had ? alpha : 1.f;
+        } else {
+          mx = 1.f;
+        }
+        if (!first && __any_sync(0xffffffffu, mx != 1.f)) {
+          // O by the rows' factors, once the product before is complete.
+          ok = __all_sync(0xffffffffu, wait(C::PVDONE + (C::NP == 2 ? wg : 0), npv - 1, kRowsPv, i));
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t oc = tmem + lanes + C::O_COL + (C::NP == 2 ? wg : 0) * C::O_STEP;
+#pragma unroll 1
+          for (int c = 0; c < D; c += 16) {
+            float o[16];
+            tmem_ld16(oc + c, o);
+            tmem_wait_ld();
+            uint32_t w[16];
+#pragma unroll
+            for (int q = 0; q < 16; ++q) w[q] = __float_as_uint(o[q] * mx);
+            tmem_st16(oc + c, w);
+          }
+        }
+        const float ref = mref == -INFINITY ? 0.f : mref;
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < TN; ++c) {
+          s[c] = exp2_approx(fmaf(s[c], sl2, -ref));
+          sum[c & 3] += s[c];
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        // Weights, in token order: word w holds tokens 2w, 2w + 1 of the tile.
+#pragma unroll
+        for (int w0 = 0; w0 < TN / 2; w0 += 16) {
+          uint32_t hi[16], lo[16];
+#pragma unroll
+          for (int q = 0; q < 16; ++q) {
+            const int t = 2 * (w0 + q), bi = t / C::BS, gi = t % C::BS / 8, e = (gi * NB + bi) * 8 + t % 8;
+            hi[q] = F16Traits<T>::pack(s[e], s[e + 1]);
+            if constexpr (C::kBf16) {
+              const float2 f = F16Traits<T>::to_float2(hi[q]);
+              lo[q] = F16Traits<T>::pack(s[e] - f.x, s[e + 1] - f.y);
+            }
+          }
+          tmem_st16(sc + w0, hi);
+          if constexpr (C::kBf16) tmem_st16(sc + TN / 2 + w0, lo);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(bar(C::PREADY + b));
+        ++npv;
+      }
+      if (!ok) break;
+      // ---- the end of the unit: join the pipelines' states (one row a thread), write.
+      const uint32_t ob = tmem + lanes + C::O_COL;
+      if (done > 0) {
+        ok = __all_sync(0xffffffffu, wait(C::PVDONE + (C::NP == 2 ? wg : 0), npv - 1, kRowsPv, -1));
+        if (!ok) break;
+        tc_fence_after();
+      }
+      // (mref, l) of either warpgroup's thread of a row, by the score columns.
+      if constexpr (C::NP == 2) {
+        tmem_st2(tmem + lanes + C::S_COL + wg * TN, mref, l);
+        tmem_wait_st();
+        tc_fence_before();
+      }
+      mbar_arrive(bar(C::XBAR));
+      ok = __all_sync(0xffffffffu, wait(C::XBAR, k, kRowsX, (int)k));
+      if (!ok) break;
+      tc_fence_after();
+      const bool odd = *odd_unit == (int)k + 1;
+      float f[2] = {1.f, 0.f};
+      bool has[2] = {U.nt > 0, false};  // pipelines with something in O
+      int o0 = 0, d_lo = 0, d_hi = D;
+      if (C::NP == 2 && !both) {
+        // Both warpgroups have every row: each writes half of its dims.
+        float m2, l2;
+        tmem_ld2(tmem + lanes + C::S_COL + (1 - wg) * TN, m2, l2);
+        tmem_wait_ld();
+        float ma = wg ? m2 : mref, la = wg ? l2 : l, mb = wg ? mref : m2, lb = wg ? l : l2;
+        const float M = fmaxf(ma, mb), Ms = M == -INFINITY ? 0.f : M;
+        f[0] = exp2_approx(ma - Ms);
+        f[1] = exp2_approx(mb - Ms);
+        l = f[0] * la + f[1] * lb;
+        mref = M;
+        has[1] = U.nt > 1;
+        constexpr int HALF = D / 32 * 16;
+        d_lo = wg ? HALF : 0;
+        d_hi = wg ? D : HALF;
+      } else if (C::NP == 2) {
+        o0 = wg;
+      }
+      const float inv = l != 0.f ? 1.f / l : 0.f;
+      const bool single = U.np == 1;
+      const size_t sh = (size_t)U.s * prm.H + U.h0 + row;
+      const size_t orow = mine ? out_row<kView>(prm, U.s, U.h0 + row) : 0;
+#pragma unroll 1
+      for (int c = d_lo; c < d_hi; c += 16) {
+        float o[16];
+#pragma unroll
+        for (int q = 0; q < 16; ++q) o[q] = 0.f;
+        if (has[0]) {
+          tmem_ld16(ob + o0 * C::O_STEP + c, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int q = 0; q < 16; ++q) o[q] *= f[0];
+        }
+        if (has[1]) {
+          float o2[16];
+          tmem_ld16(ob + C::O_STEP + c, o2);
+          tmem_wait_ld();
+#pragma unroll
+          for (int q = 0; q < 16; ++q) o[q] = fmaf(o2[q], f[1], o[q]);
+        }
+        if (mine) {
+          if (odd && v.hi > 0) {
+            float x[16];
+#pragma unroll
+            for (int q = 0; q < 16; ++q) x[q] = o[q];
+            add_odd(U, v, c, x);
+#pragma unroll
+            for (int q = 0; q < 16; ++q) o[q] = x[q];
+          }
+#pragma unroll
+          for (int q = 0; q < 16; ++q) o[q] = v.hi > 0 && l != 0.f ? o[q] * inv : 0.f;
+#pragma unroll
+          for (int q = 0; q < 16; q += 4) {
+            const float4 x = make_float4(o[q], o[q + 1], o[q + 2], o[q + 3]);
+            if (single) store4<T>(static_cast<T*>(prm.out) + orow * D + c + q, x);
+            else st_f4_policy(reinterpret_cast<float4*>(prm.ws_o + (sh * prm.Pmax + U.p) * D + c + q), x, pol_keep);
+          }
+        }
+        __syncwarp();
+      }
+      if (mine && d_lo == 0) {
+        const bool none = v.hi == 0 || l == 0.f;
+        const float mn = none ? -INFINITY : mref * kLn2;
+        st_f32_policy(prm.ws_m + sh * prm.Pmax + U.p, mn, pol_keep);
+        st_f32_policy(prm.ws_l + sh * prm.Pmax + U.p, none ? 0.f : l, pol_keep);
+        if (single && prm.lse) prm.lse[orow] = none ? -INFINITY : mn + logf(l);
+      }
+      tc_fence_before();
+      mbar_arrive(bar(C::OFREE));
+      g += 2 * U.nt;
+      ++k;
+    }
+  }
+};
+
+template <class C>
+__global__ void __launch_bounds__(C::THREADS, 1) pa_rows_kernel(const __grid_constant__ KParams prm) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  RowsCta<C> cta(prm, smem);
+  int* flags = reinterpret_cast<int*>(smem + C::OFF_FLAGS);  // abort, bad length, tensor memory, -, odd unit
+  int* pref = reinterpret_cast<int*>(smem + C::OFF_PREF);
+  uint16_t* perm = reinterpret_cast<uint16_t*>(smem + C::OFF_PERM);
+  constexpr int WP = C::NP * 4, WM = WP + 1;  // producer and product warps
+  if (tid == 0) {
+    for (int i = 0; i < C::NS; ++i) {
+      mbar_init(cta.bar(C::FULL + i), 1);
+      mbar_init(cta.bar(C::EMPTY + i), 1);
+    }
+    for (int i = 0; i < C::UQ; ++i) {
+      mbar_init(cta.bar(C::UFULL + i), 1);
+      mbar_init(cta.bar(C::UEMPTY + i), C::NP * 4 + 1);
+    }
+    mbar_init(cta.bar(C::QFULL), C::NP * 128);
+    mbar_init(cta.bar(C::QFREE), 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(cta.bar(C::SFULL + i), 1);
+      mbar_init(cta.bar(C::PREADY + i), 128);
+      mbar_init(cta.bar(C::PVDONE + i), 1);
+    }
+    mbar_init(cta.bar(C::OFREE), C::NP * 128);
+    mbar_init(cta.bar(C::XBAR), C::NP * 128);
+    mbar_init(cta.bar(C::DRAIN), 1);
+    flags[0] = flags[1] = flags[4] = 0;
+    fence_mbarrier_init();
+  }
+  if (warp == WM) tmem_alloc(smem_addr(flags + 2), 512);
+  plan_order<kView, C::BS, C::THREADS>(prm, smem + C::OFF_RING, pref, perm, flags + 1);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = (uint32_t)flags[2];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (tid == 0 && flags[1]) atomicCAS(prm.hdr + kHdrError, 0, kErrDeviceBounds);
+  if (warp == WP) {
+    cta.producer(pref, perm, lane);
+  } else if (warp == WM) {
+    if (lane == 0) cta.products(tmem);
+    __syncwarp();
+  } else {
+    // Sequences with too few tokens: zeros.
+    constexpr int D16 = C::D / 8;
+    for (int s = blockIdx.x; s < prm.S; s += gridDim.x) {
+      bool bad = false;
+      if (work_tokens<kView>(prm, seq_tokens<kView>(prm, s, prm.MB * C::BS, &bad), C::BS) > 0) continue;
+      uint4* o = static_cast<uint4*>(prm.out) + (size_t)s * prm.H * D16;
+      for (int i = tid; i < prm.H * D16; i += C::NP * 128) o[i] = make_uint4(0, 0, 0, 0);
+      if (prm.lse)
+        for (int i = tid; i < prm.H; i += C::NP * 128) prm.lse[(size_t)s * prm.H + i] = -INFINITY;
+    }
+    cta.softmax(tmem, warp >> 2, tid & 127);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == WM) tmem_free(tmem, 512);
+}
+
+}  // namespace pa

@@ -300,3 +300,58 @@ def test_refusals():
         binding.pa_decode_v2_window_fp8(out, q, kc, vc, bt, L, 0.1, 16)
     with pytest.raises(ValueError):
         binding.pa_decode_v2_window(out, q, kc.cpu(), vc, bt, L, 0.1, 16)
+
+
+MANY = [("fp16", 16, 4, 128, 16), ("bf16", 12, 1, 128, 32), ("bf16", 8, 2, 64, 8), ("fp16", 6, 2, 80, 64),
+        ("bf16", 5, 1, 256, 16), ("fp16", 4, 2, 256, 64), ("fp16", 10, 1, 96, 32), ("bf16", 4, 4, 112, 16),
+        ("fp16", 4, 1, 256, 8), ("bf16", 3, 1, 256, 32)]
+
+
+@pytest.mark.parametrize("n,window,sinks,P", [(40, 0, 0, 128), (100, 0, 0, 1024), (130, 200, 10, 256), (70, 70, 300, 192)])
+@pytest.mark.parametrize("shape", MANY, ids=["-".join(map(str, s)) for s in MANY])
+def test_many_rows(shape, n, window, sinks, P):
+    """Row counts that are and are not whole tiles; one, two and more tiles of 128
+    rows a kv head; partitions of one and of several tiles of tokens."""
+    dtype, H, KH, D, BS = shape
+    lens = [n, n + 1, n + 333, n + 700]
+    see = torch.stack([ancestors(tree_parents(n + s, n, n - 9 * s)) for s in range(len(lens))])
+    for tree in (True, False):
+        w = window if tree or window else 150
+        case = make(D + n, T[dtype], "same", n, H, KH, D, BS, lens, w, sinks, see if tree else None)
+        got, lse = run(*case, 0.07 if tree else -0.07, w, sinks, see if tree else None, P=P)
+        check(got, lse, *case, 0.07 if tree else -0.07, w, sinks, see if tree else None)
+
+
+def test_many_rows_that_see_values_that_are_not_finite():
+    """Values of the tree and of a window's edge that are not finite reach the rows
+    that see them; keys that are not finite too."""
+    n, H, KH, D, BS, L = 36, 4, 1, 128, 16, 400
+    for dtype in (torch.float16, torch.bfloat16):
+        q, kc, vc, bt, lens = make(3, dtype, "same", n, H, KH, D, BS, [L], 100, 0, poison=False)
+        vc[bt[0, (L - 5) // BS], :, 3, (L - 5) % BS] = float("inf")        # seen by the last five rows
+        lo = L - n + 1 - 100                                               # the first row's window starts here
+        vc[bt[0, (lo + 2) // BS], :, 7, (lo + 2) % BS] = float("nan")      # seen by the first three rows
+        got, _ = run(q, kc, vc, bt, lens, 0.1, 100, 0)
+        odd = torch.zeros(n, D, dtype=torch.bool)
+        odd[n - 5:, 3] = True
+        odd[:3, 7] = True
+        assert torch.equal(~got[0].isfinite(), odd[:, None].expand(n, H, D))
+        assert bool((got[0, n - 5:, :, 3] == math.inf).all())
+        clean = vc.clone()
+        clean[~clean.isfinite()] = 0
+        ref, _, bound = attend64(q, kc, clean, bt, lens, 0.1, 100, 0)
+        fine = ~odd[None, :, None].expand(1, n, H, D)
+        assert bool(((got.double() - ref).abs() <= bound)[fine].all())
+
+
+def test_many_rows_of_large_scores():
+    """Scores that grow along the sequence: the rows' references are set again and
+    again.  The tokens' keys are one direction times their position."""
+    n, H, KH, D, BS, L = 32, 4, 1, 128, 16, 900
+    for dtype in (torch.float16, torch.bfloat16):
+        q, kc, vc, bt, lens = make(8, dtype, "same", n, H, KH, D, BS, [L], 5000, 0, poison=False)
+        q = (q.abs() + 0.5).to(dtype)
+        for t in range(L):
+            kc[bt[0, t // BS], :, :, t % BS] = (t / 256.0) * (1.0 if t % 7 else -1.0)
+        got, lse = run(q, kc, vc, bt, lens, 0.15, 5000, 0, P=1024)
+        check(got, lse, q, kc, vc, bt, lens, 0.15, 5000, 0)
