@@ -546,6 +546,13 @@ struct RowsCta {
       // ---- the end of the unit: join the pipelines' states (one row a thread), write.
       const uint32_t ob = tmem + lanes + C::O_COL;
       if (done > 0) {
+        // (A parity tells a phase from the one before only: scores that have arrived
+        // say that all products issued before them are complete, with two pipelines the
+        // last but one of this warpgroup among them; with one it may still be open.)
+        if (C::NP == 1 && done > 1) {
+          ok = __all_sync(0xffffffffu, wait(C::PVDONE, npv - 2, kRowsPv, -2));
+          if (!ok) break;
+        }
         ok = __all_sync(0xffffffffu, wait(C::PVDONE + (C::NP == 2 ? wg : 0), npv - 1, kRowsPv, -1));
         if (!ok) break;
         tc_fence_after();
