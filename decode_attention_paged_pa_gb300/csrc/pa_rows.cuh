@@ -14,12 +14,14 @@
 // takes the same eight tokens of every block of a tile (the stride between rows of
 // core matrices is that between blocks), so the scores of a tile of TN tokens come
 // in BS / 8 instructions a k-step, their columns ordered (group of eight tokens,
-// block, token).  A value block [D][BS] is K-major with rows of 2 BS bytes: the
+// block, token); blocks of 32 tokens or more are copied by chunks of eight dims to
+// make one column of core matrices a tile and chunk (kChunks), one instruction.  A value block [D][BS] is K-major with rows of 2 BS bytes: the
 // tensor copy stores it in the swizzle of that width.
 //
 // One CTA per SM, persistent over units (sequence, partition, kv head, up to GT
 // rows), which a producer warp takes from the global counter (as in pa_kernel.cuh)
-// and streams through a ring of K and V tiles.  One thread issues the products.
+// and streams through a ring of K and V tiles; two warps bring Q; one thread issues
+// the products.
 // Warpgroups of four warps, a row a thread, turn scores into weights: two of them
 // (NP = 2) work in turns.  With at most 128 rows in a unit both have the same rows
 // and take the tiles alternately, each with its own O, joined at the end of the
@@ -67,22 +69,35 @@ struct RowsConfig {
   static constexpr bool kTma = BS_ >= 16;
   static constexpr bool kBf16 = std::is_same<T_, __nv_bfloat16>::value;
   static constexpr uint32_t BLK = (uint32_t)D_ * BS_ * 2, SLOT = (uint32_t)TN * D_ * 2, QTILE = 128u * D_ * 2;
-  static constexpr int THREADS = NP * 128 + 64, UQ = 2;
+  static constexpr int THREADS = NP * 128 + 128, UQ = 2;
+  // Keys are copied a chunk of eight dims at a time where a block's chunk is long enough
+  // (512 bytes): the tile then is one column of core matrices a chunk, and its scores
+  // one instruction a k-step.  Of shorter blocks each is one copy.
+  static constexpr bool kChunks = BS_ >= 32 && NB > 1;
+  static constexpr int LOADERS = 64;  // threads that bring Q
+  // Registers: the launch's 168 a thread (384 threads) are dealt out anew, 216 for the
+  // warpgroups of the softmax (whose rows hold TN scores) and 72 for the other one.
+  static constexpr int REGS = 168, SOFT_REGS = 216, REST_REGS = 72;
+  static_assert(NP == 1 || 256 * SOFT_REGS + 128 * REST_REGS == THREADS * REGS, "the launch's registers");
   // Tensor memory columns.
   static constexpr uint32_t S_COL = 0, O_COL = 2 * TN, O_STEP = 128;
   static_assert(2 * TN + (NP == 2 ? 256 : 256) <= 512, "tensor memory");
   // Shared memory: Q tiles, the ring, then barriers, units, flags, order.
   static constexpr uint32_t QBYTES = NP * QTILE;
   static constexpr uint32_t small(int ns) {
-    return al16((2 * ns + 2 * UQ + 11) * 8) + al16(UQ * sizeof(RowsUnit)) + 64 + al16((kRowsMaxUnitSeqs + 1) * 4) +
+    return al16((2 * ns + 2 * UQ + 13) * 8) + al16(UQ * sizeof(RowsUnit)) + 64 + al16((kRowsMaxUnitSeqs + 1) * 4) +
            al16(kRowsMaxUnitSeqs * 2);
   }
   static constexpr int NS = (int)((kRowsSmem - small(16) - QBYTES) / SLOT) < 16
                                 ? (int)((kRowsSmem - small(16) - QBYTES) / SLOT)
                                 : 16;
   static_assert(NS >= 3, "the ring holds a tile's keys and values and the next keys");
+  // The score column of token t of group gi of eight of block bi.
+  static constexpr __device__ __forceinline__ int column(int bi, int gi, int t) {
+    return kChunks ? bi * BS_ + gi * 8 + t : (gi * NB + bi) * 8 + t;
+  }
   static constexpr uint32_t OFF_RING = QBYTES, OFF_BAR = OFF_RING + NS * SLOT;
-  static constexpr uint32_t OFF_INFO = OFF_BAR + al16((2 * NS + 2 * UQ + 11) * 8);
+  static constexpr uint32_t OFF_INFO = OFF_BAR + al16((2 * NS + 2 * UQ + 13) * 8);
   static constexpr uint32_t OFF_FLAGS = OFF_INFO + al16(UQ * sizeof(RowsUnit));
   static constexpr uint32_t OFF_PREF = OFF_FLAGS + 64;
   static constexpr uint32_t OFF_PERM = OFF_PREF + al16((kRowsMaxUnitSeqs + 1) * 4);
@@ -91,9 +106,9 @@ struct RowsConfig {
   static_assert(NS * SLOT >= kOrderTempBytes, "prologue temporaries fit in the ring");
   // Barriers.
   static constexpr uint32_t FULL = 0, EMPTY = NS, UFULL = 2 * NS, UEMPTY = UFULL + UQ, QFULL = UEMPTY + UQ,
-                            QFREE = QFULL + 1, SFULL = QFREE + 1, PREADY = SFULL + 2, PVDONE = PREADY + 2,
-                            OFREE = PVDONE + 2, XBAR = OFREE + 1, DRAIN = XBAR + 1;
-  static_assert(DRAIN + 1 == 2 * NS + 2 * UQ + 11, "barriers");
+                            QFREE = QFULL + 1, SFULL = QFREE + 2, PREADY = SFULL + 2, PVDONE = PREADY + 2,
+                            OFREE = PVDONE + 2, XBAR = OFREE + 1, XFREE = XBAR + 1, DRAIN = XFREE + 1;
+  static_assert(DRAIN + 1 == 2 * NS + 2 * UQ + 13, "barriers");
 };
 
 // Wait sites of this kernel (see WaitSite).
@@ -120,6 +135,20 @@ struct RowsCta {
   // Ring item g (keys and values of the CTA's tiles in turn).
   __device__ __forceinline__ uint32_t slot(uint32_t g) const { return g % C::NS; }
   __device__ __forceinline__ uint32_t phase(uint32_t g) const { return g / C::NS; }
+
+  // Which Q tile a unit of one row tile takes: with two of them, the one that the unit
+  // before did not (a unit of two tiles takes both, `last` = 2).
+  struct QBuffers {
+    int last = 1;
+    __device__ __forceinline__ int next(bool both) {
+      if (C::NP == 1) return last = 0;
+      if (both) {
+        last = 2;
+        return 0;
+      }
+      return last = last == 0 ? 1 : 0;
+    }
+  };
 
   // Position of block vb of those that the sequence's rows can see.
   static __device__ __forceinline__ int block_pos(const RowsUnit& U, int vb) {
@@ -196,7 +225,19 @@ struct RowsCta {
           if (!ok) break;
           if (lane == 0) mbar_arrive_expect_tx(fb, (uint32_t)nb * C::BLK);
           __syncwarp();
-          if (lane < nb) {
+          if (w == 0 && C::kChunks) {
+            // Chunk c of block b: BS * 16 bytes to c * TN * 16 + b * BS * 16.
+            constexpr int CH = C::D / 8;
+            for (int i0 = 0; i0 < nb * CH; i0 += 32) {
+              const int i = i0 + lane, b = min(i / CH, nb - 1), c = i - b * CH;
+              const int idb = __shfl_sync(0xffffffffu, id, b);
+              if (i < nb * CH)
+                bulk_copy_g2s(dst + c * (C::TN * 16) + b * (C::BS * 16),
+                              static_cast<const uint8_t*>(prm.kc) + ((size_t)idb * prm.KH + U.kv) * C::BLK +
+                                  c * (C::BS * 16),
+                              C::BS * 16, fb, pol);
+            }
+          } else if (lane < nb) {
             const size_t row = (size_t)id * prm.KH + U.kv;
             if (w == 0 || !C::kTma)
               bulk_copy_g2s(dst + lane * C::BLK, static_cast<const uint8_t*>(w ? prm.vc : prm.kc) + row * C::BLK,
@@ -220,98 +261,170 @@ struct RowsCta {
     __syncwarp();
   }
 
-  // ---------------------------------------------------------------- product thread
+  // ---------------------------------------------------------------- product warp
+  // The whole warp goes through the loops, so that descriptors are made in uniform
+  // registers; one lane issues (descriptors made by one diverged lane cost 100 cycles
+  // a product, more than the product).
   // Scores of ring slot `sl` against Q tile q, into score buffer b.
   __device__ __forceinline__ void issue_scores(uint32_t tmem, int q, uint32_t sl, int b, uint32_t idesc) const {
-    const uint32_t qa = sbase + q * C::QTILE, ka = sbase + C::OFF_RING + sl * C::SLOT;
-    constexpr int NI = C::NB == 1 ? 1 : C::NG;         // instructions a k-step
+    constexpr bool ONE = C::kChunks || C::NB == 1;     // the tile's tokens lie one behind another
+    constexpr int NI = ONE ? 1 : C::NG;                // instructions a k-step
     constexpr int N = C::TN / NI;                      // columns of each
-    constexpr uint32_t STRIDE = C::NB == 1 ? 128u : C::BLK;
+    constexpr uint32_t STRIDE = ONE ? 128u : C::BLK;   // from eight tokens to the next
+    constexpr uint32_t LEAD = ONE ? C::TN * 16u : C::BS * 16u;  // from a chunk of dims to the next
+    const uint32_t qa = desc_lo(sbase + q * C::QTILE, 2048), ka = desc_lo(sbase + C::OFF_RING + sl * C::SLOT, LEAD);
+    const uint32_t d = tmem + C::S_COL + b * C::TN;
 #pragma unroll
-    for (int kk = 0; kk < C::D / 16; ++kk) {
-      const uint64_t a = smem_desc(qa + kk * 4096, 2048, 128, kSwizzleNone);
+    for (int kk = 0; kk < C::D / 16; ++kk)
 #pragma unroll
       for (int i = 0; i < NI; ++i)
-        mma_ss(tmem + C::S_COL + b * C::TN + i * N, a,
-               smem_desc(ka + kk * 2 * C::BS * 16 + i * 128, C::BS * 16, STRIDE, kSwizzleNone), idesc, kk > 0);
-    }
+        mma_ss(d + i * N, qa + kk * (4096 / 16), desc_hi(128, kSwizzleNone), ka + (kk * 2 * LEAD + i * 128) / 16,
+               desc_hi(STRIDE, kSwizzleNone), idesc, kk > 0);
   }
   // O[o] (+)= weights of buffer b times the values in slot `sl`, `ks` k-steps.
   __device__ __forceinline__ void issue_values(uint32_t tmem, int o, uint32_t sl, int b, int ks, uint32_t idesc,
                                                bool add) const {
-    const uint32_t va = sbase + C::OFF_RING + sl * C::SLOT, d = tmem + C::O_COL + o * C::O_STEP;
-    const uint32_t p = tmem + C::S_COL + b * C::TN;
+    constexpr int KB = C::BS == 8 ? 1 : C::BS / 16;  // k-steps of a block (of two blocks of eight tokens)
+    constexpr uint32_t SW = C::BS == 8 ? kSwizzleNone : C::BS == 16 ? kSwizzle32 : C::BS == 32 ? kSwizzle64 : kSwizzle128;
+    constexpr uint32_t HI = desc_hi(C::BS == 8 ? 128 : C::BS * 16, SW);
+    const uint32_t va = desc_lo(sbase + C::OFF_RING + sl * C::SLOT, C::BS == 8 ? C::BLK : 16);
+    const uint32_t d = tmem + C::O_COL + o * C::O_STEP, p = tmem + C::S_COL + b * C::TN;
 #pragma unroll
     for (int h = 0; h < (C::kBf16 ? 2 : 1); ++h) {
 #pragma unroll
       for (int k = 0; k < C::TN / 16; ++k) {
         if (k >= ks) break;
-        uint64_t v;
-        if constexpr (C::BS == 8) {
-          v = smem_desc(va + 2 * k * C::BLK, C::BLK, 128, kSwizzleNone);
-        } else {
-          constexpr int KB = C::BS / 16;  // k-steps of a block
-          constexpr uint32_t SW = C::BS == 16 ? kSwizzle32 : C::BS == 32 ? kSwizzle64 : kSwizzle128;
-          v = smem_desc(va + (k / KB) * C::BLK + (k % KB) * 32, 16, C::BS * 16, SW);
-        }
-        mma_ts(d, p + h * (C::TN / 2) + k * 8, v, idesc, add || h > 0 || k > 0);
+        constexpr uint32_t STEP = C::BS == 8 ? 2 * C::BLK : C::BLK;
+        mma_ts(d, p + h * (C::TN / 2) + k * 8, va + ((k / KB) * STEP + (k % KB) * 32) / 16, HI, idesc,
+               add || h > 0 || k > 0);
       }
     }
   }
-  __device__ __forceinline__ void products(uint32_t tmem) {
+  __device__ __forceinline__ void products(uint32_t tmem, int lane) {
     const RowsUnit* info = reinterpret_cast<const RowsUnit*>(smem + C::OFF_INFO);
-    constexpr int N = C::NB == 1 ? C::TN : C::TN / C::NG;
+    constexpr int N = C::kChunks || C::NB == 1 ? C::TN : C::TN / C::NG;
     const uint32_t id_s = f16_idesc(C::kBf16, N), id_o = f16_idesc(C::kBf16, C::D);
+    const auto all = [&](uint32_t b, uint32_t ph, int site, int detail) {
+      return __all_sync(0xffffffffu, wait(b, ph, site, detail)) != 0;
+    };
     uint32_t g = 0, k = 0;          // ring items and units before this unit
-    uint32_t np_[2] = {0, 0};       // weights taken from each buffer
+    uint32_t n0 = 0, n1 = 0;        // weights taken from each buffer
+    QBuffers qb;
     bool ok = true;
     while (ok) {
-      if (!wait(C::UFULL + k % C::UQ, k / C::UQ, kRowsUnit, (int)k)) break;
-      const RowsUnit U = info[k % C::UQ];
-      mbar_arrive(bar(C::UEMPTY + k % C::UQ));
-      if (U.s < 0) break;
-      const bool both = C::NP == 2 && U.nh > 128;  // a row tile for each pipeline
-      const int steps = both ? 2 * U.nt : U.nt;
-      if (!wait(C::QFULL, k, kRowsQ, (int)k)) break;
+      if (!all(C::UFULL + k % C::UQ, k / C::UQ, kRowsUnit, (int)k)) break;
+      const RowsUnit* up = info + k % C::UQ;
+      // (Shuffles tell the compiler that these are the same in every lane.)
+      const int us = __shfl_sync(0xffffffffu, up->s, 0), nt = __shfl_sync(0xffffffffu, up->nt, 0);
+      const int nh = __shfl_sync(0xffffffffu, up->nh, 0), tokens = __shfl_sync(0xffffffffu, up->t1 - up->t0, 0);
+      if (lane == 0) mbar_arrive(bar(C::UEMPTY + k % C::UQ));
+      if (us < 0) break;
+      const bool both = C::NP == 2 && nh > 128;  // a row tile for each pipeline
+      const int steps = both ? 2 * nt : nt, q0 = qb.next(both);
+      if (!all(C::QFULL, k, kRowsQ, (int)k)) break;
+      // (The last unit's joining used the score columns; and with this wait neither side
+      // is ever more than a unit ahead, so that a parity tells the phases apart.)
+      if (!all(C::XFREE, k + 1, kRowsX, (int)k)) break;
       tc_fence_after();
       // (Scores of step i + 2 go where the weights of step i were.)
       const auto scores = [&](int i) {
         const int j = both ? i >> 1 : i;
         const uint32_t it = g + 2 * j;
         if (!both || !(i & 1)) {
-          if (!wait(C::FULL + slot(it), phase(it), kRowsFull, (int)it)) return false;
+          if (!all(C::FULL + slot(it), phase(it), kRowsFull, (int)it)) return false;
         }
-        issue_scores(tmem, both ? i & 1 : 0, slot(it), i & 1, id_s);
-        mma_commit(bar(C::SFULL + (i & 1)));
-        if (!both || (i & 1)) mma_commit(bar(C::EMPTY + slot(it)));
+        if (elect_one()) {
+          issue_scores(tmem, both ? i & 1 : q0, slot(it), i & 1, id_s);
+          mma_commit(bar(C::SFULL + (i & 1)));
+          if (!both || (i & 1)) mma_commit(bar(C::EMPTY + slot(it)));
+        }
+        __syncwarp();
         return true;
       };
       for (int i = 0; i < 2 && i < steps && ok; ++i) ok = scores(i);
       for (int i = 0; i < steps && ok; ++i) {
         const int j = both ? i >> 1 : i, b = i & 1, o = C::NP == 2 ? b : 0;
         const uint32_t it = g + 2 * j + 1;
-        ok = wait(C::FULL + slot(it), phase(it), kRowsFull, (int)it);
-        if (ok && i < 2) ok = wait(C::OFREE, k + 1, kRowsOFree, (int)k);  // the last unit's O is read
-        if (ok) ok = wait(C::PREADY + b, np_[b], kRowsP, i);
+        ok = all(C::FULL + slot(it), phase(it), kRowsFull, (int)it);
+        if (ok && i < 2) ok = all(C::OFREE, k + 1, kRowsOFree, (int)k);  // the last unit's O is read
+        if (ok) ok = all(C::PREADY + b, b ? n1 : n0, kRowsP, i);
         if (!ok) break;
-        ++np_[b];
+        if (b) ++n1;
+        else ++n0;
         tc_fence_after();
-        const int left = U.t1 - U.t0 - j * C::TN;
-        issue_values(tmem, o, slot(it), b, left >= C::TN ? C::TN / 16 : (left + 15) / 16, id_o,
-                     C::NP == 2 ? i >= 2 : i >= 1);
-        mma_commit(bar(C::PVDONE + o));
-        if (!both || (i & 1)) mma_commit(bar(C::EMPTY + slot(it)));
+        const int left = tokens - j * C::TN, ks = left >= C::TN ? C::TN / 16 : (left + 15) / 16;
+        if (elect_one()) {
+          issue_values(tmem, o, slot(it), b, ks, id_o, C::NP == 2 ? i >= 2 : i >= 1);
+          mma_commit(bar(C::PVDONE + b));
+          if (!both || (i & 1)) mma_commit(bar(C::EMPTY + slot(it)));
+        }
+        __syncwarp();
         if (i + 2 < steps) ok = scores(i + 2);
       }
       if (!ok) break;
-      mma_commit(bar(C::QFREE));
-      g += 2 * U.nt;
+      if (elect_one()) mma_commit(bar(C::QFREE + (k & 1)));
+      __syncwarp();
+      g += 2 * nt;
       ++k;
     }
     // What has been issued completes before tensor memory is freed.
-    mma_commit(bar(C::DRAIN));
+    if (elect_one()) mma_commit(bar(C::DRAIN));
+    __syncwarp();
     const uint64_t t0 = global_timer_ns();
     while (!mbar_try_wait(bar(C::DRAIN), 0) && global_timer_ns() - t0 < 100000000ull) {
+    }
+    __syncwarp();
+  }
+
+  // ---------------------------------------------------------------- Q warps
+  // The unit's row tiles, [D/8][128 rows] 16-byte pieces; rows past the unit's (up to
+  // whole warps): zeros.  Four lanes a row: 64 bytes of it an instruction.
+  __device__ __forceinline__ void bring_rows(int tid, int lane) {
+    using T = typename C::T;
+    const RowsUnit* info = reinterpret_cast<const RowsUnit*>(smem + C::OFF_INFO);
+    QBuffers qb;
+    for (uint32_t k = 0;; ++k) {
+      const bool okw = wait(C::UFULL + k % C::UQ, k / C::UQ, kRowsUnit, (int)k);
+      if (!__all_sync(0xffffffffu, okw)) break;
+      const RowsUnit U = info[k % C::UQ];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(C::UEMPTY + k % C::UQ));
+      if (U.s < 0) break;
+      const bool both = C::NP == 2 && U.nh > 128;
+      const int before = qb.last;
+      const int q0 = qb.next(both);
+      // The unit before last is done with its tiles; the last one too, where this one
+      // takes a tile of its.
+      // (Units take turns at two barriers, so that neither is waited for two phases late.)
+      bool ok = k < 2 || wait(C::QFREE + (k & 1), (k >> 1) - 1, kRowsQFree, (int)k);
+      if (ok && k >= 1 && (both || before == 2 || before == q0))
+        ok = wait(C::QFREE + ((k - 1) & 1), (k - 1) >> 1, kRowsQFree, (int)k);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      const int rows = (U.nh + 31) / 32 * 32;
+      for (int row = tid >> 2; row < rows; row += C::LOADERS / 4) {
+        const bool in = row < U.nh;
+        const T* q = static_cast<const T*>(prm.q) + (in ? out_row<kView>(prm, U.s, U.h0 + row) : 0) * C::D;
+        const uint32_t dst = sbase + (both ? row >> 7 : q0) * C::QTILE + (row & 127) * 16;
+#pragma unroll
+        for (int c0 = 0; c0 < C::D / 8; c0 += 4) {
+          const int c = c0 + (tid & 3);
+          if (c < C::D / 8)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + c * 2048), "l"(q + c * 8),
+                         "r"(in ? 16 : 0)
+                         : "memory");
+        }
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      if (prm.scale_log2 < 0.f) {
+        // The products get -Q: the softmax works with a scale that is not negative.
+        for (int row = tid >> 2; row < rows; row += C::LOADERS / 4)
+          for (int c = tid & 3; c < C::D / 8; c += 4) {
+            uint4* x = reinterpret_cast<uint4*>(smem + (both ? row >> 7 : q0) * C::QTILE + (row & 127) * 16 + c * 2048);
+            *x = make_uint4(x->x ^ 0x80008000u, x->y ^ 0x80008000u, x->z ^ 0x80008000u, x->w ^ 0x80008000u);
+          }
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(bar(C::QFULL));
     }
   }
 
@@ -397,6 +510,25 @@ struct RowsCta {
     }
   }
 
+  // o[4 i + e] of lane q of four becomes what lane i had in o[4 q + e].
+  static __device__ __forceinline__ void transpose4(float (&o)[16], int lane) {
+#pragma unroll
+    for (int st = 1; st < 4; st <<= 1) {
+      const bool up = lane & st;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (i & st) continue;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float &a = o[4 * i + e], &b = o[4 * (i + st) + e];
+          const float got = __shfl_xor_sync(0xffffffffu, up ? a : b, st);
+          if (up) a = got;
+          else b = got;
+        }
+      }
+    }
+  }
+
   __device__ __forceinline__ void softmax(uint32_t tmem, int wg, int tid) {
     using T = typename C::T;
     constexpr int TN = C::TN, NB = C::NB, NG = C::NG, D = C::D;
@@ -404,11 +536,10 @@ struct RowsCta {
     volatile int* odd_unit = reinterpret_cast<volatile int*>(smem + C::OFF_FLAGS + 16);
     const int lane = tid & 31;
     const uint32_t lanes = (uint32_t)(tid & ~31) << 16;  // this warp's lanes of tensor memory
-    // (The sign of the scale goes to Q.)
-    const uint32_t flip = prm.scale_log2 < 0.f ? 0x80008000u : 0u;
+    // (The sign of the scale went to Q.)
     const float sl2 = fmaxf(fabsf(prm.scale_log2), 1.17549435e-38f);
     const uint64_t pol_keep = l2_policy_evict_last();
-    uint32_t g = 0, k = 0, ns_[2] = {0, 0}, npv = 0;  // ring items, units, scores read (a buffer), products into O
+    uint32_t g = 0, k = 0, n0 = 0, n1 = 0;  // ring items and units; scores read from each buffer
     while (true) {
       const bool okw = wait(C::UFULL + k % C::UQ, k / C::UQ, kRowsUnit, (int)k);
       if (!__all_sync(0xffffffffu, okw)) break;
@@ -419,22 +550,9 @@ struct RowsCta {
       const bool both = C::NP == 2 && U.nh > 128;
       const int row = both ? wg * 128 + tid : tid;  // the thread's row of the unit
       const bool mine = row < U.nh;
+      const bool warp_rows = (row & ~31) < U.nh;
       RowView v{0, 0, 0, nullptr};
       if (mine) v = row_view(prm, U.s, U.L, U.h0 + row);
-      // Q: the unit's row tiles, [D/8][128 rows] 16-byte pieces.
-      if (!__all_sync(0xffffffffu, wait(C::QFREE, k + 1, kRowsQFree, (int)k))) break;
-      {
-        const T* q = static_cast<const T*>(prm.q) + (mine ? out_row<kView>(prm, U.s, U.h0 + row) : 0) * D;
-        uint8_t* dst = smem + (both ? wg : 0) * C::QTILE + tid * 16;
-        const bool shared_rows = C::NP == 2 && !both;  // both warpgroups have the rows: half of the pieces each
-        for (int c = shared_rows ? wg : 0; c < D / 8; c += shared_rows ? 2 : 1) {
-          uint4 x = mine ? reinterpret_cast<const uint4*>(q)[c] : make_uint4(0, 0, 0, 0);
-          x.x ^= flip; x.y ^= flip; x.z ^= flip; x.w ^= flip;
-          *reinterpret_cast<uint4*>(dst + c * 2048) = x;
-        }
-        fence_proxy_async_smem();
-        mbar_arrive(bar(C::QFULL));
-      }
       // Positions that every row of the unit sees (padding apart).
       int full_lo, full_hi;
       {
@@ -451,18 +569,15 @@ struct RowsCta {
         const int j = both ? i >> 1 : i, b = i & 1;
         const uint32_t sc = tmem + lanes + C::S_COL + b * TN;
         const int tile = U.t0 + j * TN, left = U.t1 - tile, vb0 = tile / C::BS;
-        ok = __all_sync(0xffffffffu, wait(C::SFULL + b, ns_[b], kRowsS, i));
+        ok = __all_sync(0xffffffffu, wait(C::SFULL + b, b ? n1 : n0, kRowsS, i));
         if (!ok) break;
-        ++ns_[b];
+        if (b) ++n1;
+        else ++n0;
         tc_fence_after();
-        float s[TN];
-#pragma unroll
-        for (int c = 0; c < TN; c += 32) tmem_ld32(sc + c, s + c);
         // Whether every row sees the whole tile.
         const int p0 = block_pos(U, vb0), p1 = block_pos(U, vb0 + (min(left, TN) - 1) / C::BS) + C::BS - 1;
         const bool jump = vb0 < U.sink_blocks && U.skip > 0;
         const bool partial = left < TN || jump || p1 >= full_hi || (p0 < full_lo && p1 >= prm.sinks);
-        tmem_wait_ld();
         if (partial) {
           // (Values: before the weights of the tile are announced.)
           const uint32_t it = g + 2 * j + 1;
@@ -470,6 +585,18 @@ struct RowsCta {
           if (!ok) break;
           if (clear_values(slot(it), left, tid)) *odd_unit = (int)k + 1;
           fence_proxy_async_smem();
+          __syncwarp();
+        }
+        if (!warp_rows) {  // a warp without rows only keeps the count
+          tc_fence_before();
+          mbar_arrive(bar(C::PREADY + b));
+          continue;
+        }
+        float s[TN];
+#pragma unroll
+        for (int c = 0; c < TN; c += 32) tmem_ld32(sc + c, s + c);
+        tmem_wait_ld();
+        if (partial) {
 #pragma unroll
           for (int gi = 0; gi < NG; ++gi)
 #pragma unroll
@@ -477,14 +604,14 @@ struct RowsCta {
               const uint32_t m = group_seen(v, block_pos(U, vb0 + bi) + gi * 8, left - bi * C::BS - gi * 8);
 #pragma unroll
               for (int t = 0; t < 8; ++t)
-                if (!((m >> t) & 1u)) s[(gi * NB + bi) * 8 + t] = -INFINITY;
+                if (!((m >> t) & 1u)) s[C::column(bi, gi, t)] = -INFINITY;
             }
           __syncwarp();
         }
-        float mx = -INFINITY;
+        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int c = 0; c < TN; ++c) mx = fmaxf(mx, s[c]);
-        mx *= sl2;
+        for (int c = 0; c < TN; ++c) m4[c & 3] = fmaxf(m4[c & 3], s[c]);
+        float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * sl2;
         if (v.hi == 0) mx = -INFINITY;  // (padding, and rows past the unit's: weights of no use)
         const bool first = C::NP == 2 ? done == 0 : i == 0;
         if (mx > mref + 8.f || (mref == -INFINITY && mx > -INFINITY)) {
@@ -498,7 +625,9 @@ struct RowsCta {
         }
         if (!first && __any_sync(0xffffffffu, mx != 1.f)) {
           // O by the rows' factors, once the product before is complete.
-          ok = __all_sync(0xffffffffu, wait(C::PVDONE + (C::NP == 2 ? wg : 0), npv - 1, kRowsPv, i));
+          // (Each buffer's products have a barrier, on which they are never two ahead.)
+          const int pb = C::NP == 2 ? b : b ^ 1;
+          ok = __all_sync(0xffffffffu, wait(C::PVDONE + pb, (pb ? n1 : n0) - (C::NP == 2 ? 2 : 1), kRowsPv, i));
           if (!ok) break;
           tc_fence_after();
           const uint32_t oc = tmem + lanes + C::O_COL + (C::NP == 2 ? wg : 0) * C::O_STEP;
@@ -527,7 +656,7 @@ struct RowsCta {
           uint32_t hi[16], lo[16];
 #pragma unroll
           for (int q = 0; q < 16; ++q) {
-            const int t = 2 * (w0 + q), bi = t / C::BS, gi = t % C::BS / 8, e = (gi * NB + bi) * 8 + t % 8;
+            const int t = 2 * (w0 + q), e = C::column(t / C::BS, t % C::BS / 8, t % 8);
             hi[q] = F16Traits<T>::pack(s[e], s[e + 1]);
             if constexpr (C::kBf16) {
               const float2 f = F16Traits<T>::to_float2(hi[q]);
@@ -540,20 +669,14 @@ struct RowsCta {
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(bar(C::PREADY + b));
-        ++npv;
       }
       if (!ok) break;
       // ---- the end of the unit: join the pipelines' states (one row a thread), write.
       const uint32_t ob = tmem + lanes + C::O_COL;
       if (done > 0) {
-        // (A parity tells a phase from the one before only: scores that have arrived
-        // say that all products issued before them are complete, with two pipelines the
-        // last but one of this warpgroup among them; with one it may still be open.)
-        if (C::NP == 1 && done > 1) {
-          ok = __all_sync(0xffffffffu, wait(C::PVDONE, npv - 2, kRowsPv, -2));
-          if (!ok) break;
-        }
-        ok = __all_sync(0xffffffffu, wait(C::PVDONE + (C::NP == 2 ? wg : 0), npv - 1, kRowsPv, -1));
+        // (Products are complete in their order: the last one's barrier is enough.)
+        const int pb = (steps - 1) & 1, lb = C::NP == 2 ? wg : pb;
+        ok = __all_sync(0xffffffffu, wait(C::PVDONE + lb, (lb ? n1 : n0) - 1, kRowsPv, -1));
         if (!ok) break;
         tc_fence_after();
       }
@@ -562,6 +685,10 @@ struct RowsCta {
         tmem_st2(tmem + lanes + C::S_COL + wg * TN, mref, l);
         tmem_wait_st();
         tc_fence_before();
+      }
+      if (U.nt == 0) {  // (nothing of this unit came from the product thread)
+        ok = __all_sync(0xffffffffu, wait(C::QFREE + (k & 1), k >> 1, kRowsQFree, (int)k));
+        if (!ok) break;
       }
       mbar_arrive(bar(C::XBAR));
       ok = __all_sync(0xffffffffu, wait(C::XBAR, k, kRowsX, (int)k));
@@ -576,6 +703,8 @@ struct RowsCta {
         float m2, l2;
         tmem_ld2(tmem + lanes + C::S_COL + (1 - wg) * TN, m2, l2);
         tmem_wait_ld();
+        tc_fence_before();
+        mbar_arrive(bar(C::XFREE));
         float ma = wg ? m2 : mref, la = wg ? l2 : l, mb = wg ? mref : m2, lb = wg ? l : l2;
         const float M = fmaxf(ma, mb), Ms = M == -INFINITY ? 0.f : M;
         f[0] = exp2_approx(ma - Ms);
@@ -586,50 +715,58 @@ struct RowsCta {
         constexpr int HALF = D / 32 * 16;
         d_lo = wg ? HALF : 0;
         d_hi = wg ? D : HALF;
-      } else if (C::NP == 2) {
+      } else {
+        mbar_arrive(bar(C::XFREE));
         o0 = wg;
       }
       const float inv = l != 0.f ? 1.f / l : 0.f;
       const bool single = U.np == 1;
-      const size_t sh = (size_t)U.s * prm.H + U.h0 + row;
-      const size_t orow = mine ? out_row<kView>(prm, U.s, U.h0 + row) : 0;
+      const size_t sh0 = (size_t)U.s * prm.H + U.h0, sh = sh0 + row;
+      const int orow = mine ? (int)out_row<kView>(prm, U.s, U.h0 + row) : 0;  // (below 2^25: 256 sequences)
 #pragma unroll 1
       for (int c = d_lo; c < d_hi; c += 16) {
         float o[16];
 #pragma unroll
         for (int q = 0; q < 16; ++q) o[q] = 0.f;
+        float o2[16];
+        if (has[0]) tmem_ld16(ob + o0 * C::O_STEP + c, o);
+        if (has[1]) tmem_ld16(ob + C::O_STEP + c, o2);
+        tmem_wait_ld();
         if (has[0]) {
-          tmem_ld16(ob + o0 * C::O_STEP + c, o);
-          tmem_wait_ld();
 #pragma unroll
           for (int q = 0; q < 16; ++q) o[q] *= f[0];
         }
         if (has[1]) {
-          float o2[16];
-          tmem_ld16(ob + C::O_STEP + c, o2);
-          tmem_wait_ld();
 #pragma unroll
           for (int q = 0; q < 16; ++q) o[q] = fmaf(o2[q], f[1], o[q]);
         }
-        if (mine) {
-          if (odd && v.hi > 0) {
-            float x[16];
+        if (odd && mine && v.hi > 0) {
+          float x[16];
 #pragma unroll
-            for (int q = 0; q < 16; ++q) x[q] = o[q];
-            add_odd(U, v, c, x);
+          for (int q = 0; q < 16; ++q) x[q] = o[q];
+          add_odd(U, v, c, x);
 #pragma unroll
-            for (int q = 0; q < 16; ++q) o[q] = x[q];
-          }
-#pragma unroll
-          for (int q = 0; q < 16; ++q) o[q] = v.hi > 0 && l != 0.f ? o[q] * inv : 0.f;
-#pragma unroll
-          for (int q = 0; q < 16; q += 4) {
-            const float4 x = make_float4(o[q], o[q + 1], o[q + 2], o[q + 3]);
-            if (single) store4<T>(static_cast<T*>(prm.out) + orow * D + c + q, x);
-            else st_f4_policy(reinterpret_cast<float4*>(prm.ws_o + (sh * prm.Pmax + U.p) * D + c + q), x, pol_keep);
-          }
+          for (int q = 0; q < 16; ++q) o[q] = x[q];
         }
         __syncwarp();
+        const bool some = v.hi > 0 && l != 0.f;
+#pragma unroll
+        for (int q = 0; q < 16; ++q) o[q] = some ? o[q] * inv : 0.f;
+        // Four lanes exchange their rows' pieces of four dims: then lane q of the four has
+        // piece q of each of their rows, and they store 16 dims of one row at a time (a
+        // lane a row touched 32 lines with every store).
+        transpose4(o, lane);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = (row & ~3) + i;
+          const int orow_i = __shfl_sync(0xffffffffu, orow, (lane & ~3) + i);
+          const float4 x = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          const int d = c + (lane & 3) * 4;
+          if (r < U.nh) {
+            if (single) store4<T>(static_cast<T*>(prm.out) + (size_t)orow_i * D + d, x);
+            else st_f4_policy(reinterpret_cast<float4*>(prm.ws_o + ((sh0 + r) * prm.Pmax + U.p) * D + d), x, pol_keep);
+          }
+        }
       }
       if (mine && d_lo == 0) {
         const bool none = v.hi == 0 || l == 0.f;
@@ -654,7 +791,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) pa_rows_kernel(const __grid_con
   int* flags = reinterpret_cast<int*>(smem + C::OFF_FLAGS);  // abort, bad length, tensor memory, -, odd unit
   int* pref = reinterpret_cast<int*>(smem + C::OFF_PREF);
   uint16_t* perm = reinterpret_cast<uint16_t*>(smem + C::OFF_PERM);
-  constexpr int WP = C::NP * 4, WM = WP + 1;  // producer and product warps
+  constexpr int WP = C::NP * 4, WM = WP + 1, WQ = WP + 2;  // producer, product and Q warps
   if (tid == 0) {
     for (int i = 0; i < C::NS; ++i) {
       mbar_init(cta.bar(C::FULL + i), 1);
@@ -662,10 +799,12 @@ __global__ void __launch_bounds__(C::THREADS, 1) pa_rows_kernel(const __grid_con
     }
     for (int i = 0; i < C::UQ; ++i) {
       mbar_init(cta.bar(C::UFULL + i), 1);
-      mbar_init(cta.bar(C::UEMPTY + i), C::NP * 4 + 1);
+      mbar_init(cta.bar(C::UEMPTY + i), C::NP * 4 + 3);
     }
-    mbar_init(cta.bar(C::QFULL), C::NP * 128);
+    mbar_init(cta.bar(C::QFULL), C::LOADERS);
+    mbar_init(cta.bar(C::XFREE), C::NP * 128);
     mbar_init(cta.bar(C::QFREE), 1);
+    mbar_init(cta.bar(C::QFREE + 1), 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(cta.bar(C::SFULL + i), 1);
       mbar_init(cta.bar(C::PREADY + i), 128);
@@ -685,12 +824,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) pa_rows_kernel(const __grid_con
   const uint32_t tmem = (uint32_t)flags[2];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (tid == 0 && flags[1]) atomicCAS(prm.hdr + kHdrError, 0, kErrDeviceBounds);
-  if (warp == WP) {
-    cta.producer(pref, perm, lane);
-  } else if (warp == WM) {
-    if (lane == 0) cta.products(tmem);
-    __syncwarp();
-  } else {
+  if (warp < WP) {
+    if constexpr (C::NP == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::SOFT_REGS));
     // Sequences with too few tokens: zeros.
     constexpr int D16 = C::D / 8;
     for (int s = blockIdx.x; s < prm.S; s += gridDim.x) {
@@ -701,7 +836,17 @@ __global__ void __launch_bounds__(C::THREADS, 1) pa_rows_kernel(const __grid_con
       if (prm.lse)
         for (int i = tid; i < prm.H; i += C::NP * 128) prm.lse[(size_t)s * prm.H + i] = -INFINITY;
     }
+    __syncwarp();
     cta.softmax(tmem, warp >> 2, tid & 127);
+  } else {
+    if constexpr (C::NP == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REST_REGS));
+    if (warp == WP) {
+      cta.producer(pref, perm, lane);
+    } else if (warp == WM) {
+      cta.products(tmem, lane);
+    } else {
+      cta.bring_rows(tid - WQ * 32, lane);
+    }
   }
   tc_fence_before();
   __syncthreads();

@@ -73,9 +73,12 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* v) {
 // along K, `stride` bytes along the rows.  Swizzled K-major rows of 32, 64 or 128
 // bytes: `stride` bytes from eight rows to the next.
 enum : uint32_t { kSwizzleNone = 0, kSwizzle128 = 2, kSwizzle64 = 4, kSwizzle32 = 6 };
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead, uint32_t stride, uint32_t swizzle) {
-  return (uint64_t)((addr & 0x3ffffu) >> 4) | (uint64_t)((lead & 0x3ffffu) >> 4) << 16 |
-         (uint64_t)((stride & 0x3ffffu) >> 4) << 32 | 1ull << 46 | (uint64_t)swizzle << 61;
+// Low word for an address (add bytes / 16 for others), high word for all.
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lead) {
+  return (addr & 0x3ffffu) >> 4 | ((lead & 0x3ffffu) >> 4) << 16;
+}
+__device__ __forceinline__ constexpr uint32_t desc_hi(uint32_t stride, uint32_t swizzle) {
+  return ((stride & 0x3ffffu) >> 4) | 1u << 14 | swizzle << 29;
 }
 // Instruction descriptor of kind::f16 with fp32 accumulators: M = 128 rows, N
 // columns, both operands K-major.
@@ -84,21 +87,34 @@ __device__ __forceinline__ uint32_t f16_idesc(bool bf16, int n) {
   return 1u << 4 | t << 7 | t << 10 | (uint32_t)(n >> 3) << 17 | 8u << 24;
 }
 // D[128 x N] (+)= A . B, by one thread: A in shared memory, or (ts) in tensor memory.
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi,
+                                       uint32_t idesc, bool add) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+      "mov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\t"
+      "setp.ne.u32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d),
+      "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"((uint32_t)add)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t b_hi, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+      "mov.b64 b, {%2, %3};\n\t"
+      "setp.ne.u32 p, %5, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"((uint32_t)add)
+      : "memory");
+}
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
-      "setp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
-      : "memory");
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(e));
+  return e != 0;
 }
 // Arrives at `bar` once the products that this thread has issued are complete.
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
