@@ -311,6 +311,18 @@ int decode_impl(void* out, float* lse, const void* query, const void* key_cache,
   // fit a warp's ring).
   const bool kv4_pairs = kv4 && G * 2 <= kMmaGroup && KH % 2 == 0 && D <= 128 && BS <= 32;
   const int kvu = pairs || kv4_pairs ? 2 : 1;
+  // With many rows a unit the states of a partition are many too, and each unit has
+  // its start and end: partitions are taken together, in powers of two, as long as
+  // every SM can still have four units (16 nodes a sequence, 48 sequences of 3000
+  // tokens, partitions of 512: 218 us as they are, 168 with four together).
+  int part = view && P > MB * BS ? MB * BS : P;
+  if (many) {
+    const long long cap = (long long)view_blocks(q_len, MB, BS, view->window, view->sinks) * BS;
+    const long long tiles = (long long)S * KH * ((G + gt - 1) / gt), want = 4ll * device_sm_count();
+    while (part < cap && tiles * ((cap + 2ll * part - 1) / (2ll * part)) >= want) part *= 2;
+    if (!ws_layout(S, H, KH, D, view_blocks(q_len, MB, BS, view->window, view->sinks), BS, part, &w))
+      return PA_ERR_INVALID_ARG;
+  }
   const int hg_per_kv = (G + gt - 1) / gt;
   const int n_hg = KH * hg_per_kv / kvu;
   const int rows_per_launch = many ? kRowsSeqsPerLaunch : kMaxSeqsPerLaunch;  // sequences per launch
@@ -371,7 +383,7 @@ int decode_impl(void* out, float* lse, const void* query, const void* key_cache,
     prm.num_blocks = num_blocks;
     // (A partition past the table's capacity is the capacity: sums of lengths
     // and partition sizes stay in 32 bits.)
-    prm.P = (kv4 || view) && P > MB * BS ? MB * BS : P;
+    prm.P = view ? part : kv4 && P > MB * BS ? MB * BS : P;
     prm.Pmax = w.pmax;
     prm.hg_per_kv = hg_per_kv;
     prm.n_hg = n_hg;
@@ -463,7 +475,7 @@ int decode_impl(void* out, float* lse, const void* query, const void* key_cache,
     cp.S = S;
     cp.H = H;
     cp.Pmax = w.pmax;
-    cp.P = view && P > MB * BS ? MB * BS : P;
+    cp.P = view ? part : P;
     cp.max_len = MB * BS;
     cp.BS = BS;
     if (view) {

@@ -148,22 +148,26 @@ __device__ __forceinline__ int row_limit(const KParams& prm, int L, int h) {
 }
 
 // (See RowView.)
-__device__ __forceinline__ RowView row_view(const KParams& prm, int s, int L, int h) {
-  const int i = (h % prm.G) / prm.Gu, first = L - prm.q_len;
+__device__ __forceinline__ RowView row_view_of(const KParams& prm, int s, int L, int i) {  // i: query token or node
+  const int first = L - prm.q_len;
   RowView v;
   int at = first + i;
   v.bits = nullptr;
   v.hi = v.base = at + 1;
   if (prm.masks) {
     v.bits = prm.masks + ((size_t)s * prm.q_len + i) * prm.words;
-    int n = 0;
-    for (int w = 0; w < prm.words; ++w) n += __popc(__ldg(v.bits + w));
+    int n = __popc(__ldg(v.bits));
+    if (prm.words > 1) n += __popc(__ldg(v.bits + 1));
+    for (int w = 2; w < prm.words; ++w) n += __popc(__ldg(v.bits + w));
     at = first + n - 1;
     v.base = first;
     v.hi = n > 0 ? L : 0;
   }
   v.lo = prm.window > 0 ? at - prm.window + 1 : 0;
   return v;
+}
+__device__ __forceinline__ RowView row_view(const KParams& prm, int s, int L, int h) {
+  return row_view_of(prm, s, L, (h % prm.G) / prm.Gu);
 }
 
 struct UnitInfo {

@@ -151,8 +151,8 @@ struct RowsCta {
   };
 
   // Position of block vb of those that the sequence's rows can see.
-  static __device__ __forceinline__ int block_pos(const RowsUnit& U, int vb) {
-    return (vb + (vb < U.sink_blocks ? 0 : U.skip)) * C::BS;
+  static __device__ __forceinline__ int block_pos(int sink_blocks, int skip, int vb) {
+    return (vb + (vb < sink_blocks ? 0 : skip)) * C::BS;
   }
 
   // The unit of a plan, cut to the tokens that some row of it sees.
@@ -416,7 +416,7 @@ struct RowsCta {
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
       if (prm.scale_log2 < 0.f) {
-        // The products get -Q: the softmax works with a scale that is not negative.
+        // The products get -Q: the softmax works with a scale that is not negativ.
         for (int row = tid >> 2; row < rows; row += C::LOADERS / 4)
           for (int c = tid & 3; c < C::D / 8; c += 4) {
             uint4* x = reinterpret_cast<uint4*>(smem + (both ? row >> 7 : q0) * C::QTILE + (row & 127) * 16 + c * 2048);
@@ -492,20 +492,23 @@ struct RowsCta {
     return found;
   }
 
-  // Values that are not finite, of dims d0 .. d0 + 15, added to the row that sees
-  // their tokens (rare; the cache itself is read).
-  __device__ __noinline__ void add_odd(const RowsUnit& U, const RowView& v, int d0, float* o) const {
+  // Values that are not finite (rare; the cache itself is read): dims [d0, d1) of a
+  // row that has been written get those of the tokens it sees added.  `at`: the row's
+  // output or state.
+  template <typename E>
+  __device__ __noinline__ void add_odd(int s, int kv, int t0, int t1, int sink_blocks, int skip, int lo, int hi, int base,
+                                       const uint32_t* bits, int d0, int d1, E* at) const {
     using T = typename C::T;
     const T* vc = static_cast<const T*>(prm.vc);
-    for (int t = U.t0; t < U.t1; ++t) {
-      const int vb = t / C::BS, pos = block_pos(U, vb) + t % C::BS;
-      if (!(group_seen(v, pos, 1) & 1u)) continue;
-      int id = prm.bt[(size_t)U.s * prm.MB + pos / C::BS];
+    for (int t = t0; t < t1; ++t) {
+      const int pos = t + (t / C::BS < sink_blocks ? 0 : skip * C::BS);
+      if (!(group_seen(RowView{lo, hi, base, bits}, pos, 1) & 1u)) continue;
+      int id = prm.bt[(size_t)s * prm.MB + pos / C::BS];
       if ((unsigned)id >= (unsigned)prm.num_blocks) id = 0;
-      const T* blk = vc + ((size_t)id * prm.KH + U.kv) * C::D * C::BS;
-      for (int i = 0; i < 16; ++i) {
-        const float x = (float)blk[(d0 + i) * C::BS + t % C::BS];
-        if (!(fabsf(x) < INFINITY)) o[i] += x;
+      const T* blk = vc + ((size_t)id * prm.KH + kv) * C::D * C::BS + t % C::BS;
+      for (int d = d0; d < d1; ++d) {
+        const float x = (float)blk[d * C::BS];
+        if (!(fabsf(x) < INFINITY)) at[d] = (E)((float)at[d] + x);
       }
     }
   }
@@ -540,43 +543,46 @@ struct RowsCta {
     const float sl2 = fmaxf(fabsf(prm.scale_log2), 1.17549435e-38f);
     const uint64_t pol_keep = l2_policy_evict_last();
     uint32_t g = 0, k = 0, n0 = 0, n1 = 0;  // ring items and units; scores read from each buffer
+    // (The unit's description stays in its slot while it is worked on, and what a row
+    // sees is worked out where a tile is partly seen and at the end: registers hold
+    // the row's scores.)
     while (true) {
       const bool okw = wait(C::UFULL + k % C::UQ, k / C::UQ, kRowsUnit, (int)k);
       if (!__all_sync(0xffffffffu, okw)) break;
-      const RowsUnit U = info[k % C::UQ];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(C::UEMPTY + k % C::UQ));
+      const volatile RowsUnit& U = info[k % C::UQ];
       if (U.s < 0) break;
-      const bool both = C::NP == 2 && U.nh > 128;
+      const int nh = U.nh, nt = U.nt;
+      const bool both = C::NP == 2 && nh > 128;
       const int row = both ? wg * 128 + tid : tid;  // the thread's row of the unit
-      const bool mine = row < U.nh;
-      const bool warp_rows = (row & ~31) < U.nh;
-      RowView v{0, 0, 0, nullptr};
-      if (mine) v = row_view(prm, U.s, U.L, U.h0 + row);
+      const bool mine = row < nh;
+      const int qi = mine ? (U.h0 - U.kv * prm.G + row) / prm.Gu : -1;  // its query token
+      const auto view = [&]() { return qi >= 0 ? row_view_of(prm, U.s, U.L, qi) : RowView{0, 0, 0, nullptr}; };
+      const bool warp_rows = (row & ~31) < nh;
       // Positions that every row of the unit sees (padding apart).
       int full_lo, full_hi;
       {
         const int first = U.L - prm.q_len, l0 = U.h0 - U.kv * prm.G;
-        const int i0 = l0 / prm.Gu, i1 = (l0 + U.nh - 1) / prm.Gu;
+        const int i0 = l0 / prm.Gu, i1 = (l0 + nh - 1) / prm.Gu;
         full_hi = prm.masks ? first : first + i0 + 1;
         full_lo = prm.window > 0 ? (prm.masks ? U.L - prm.window : first + i1 - prm.window + 1) : 0;
       }
       float mref = -INFINITY, l = 0.f;
-      const int steps = both ? 2 * U.nt : U.nt;
+      const int steps = both ? 2 * nt : nt, t0 = U.t0, t1 = U.t1, sink_blocks = U.sink_blocks, skip = U.skip;
       int done = 0;  // this warpgroup's steps of the unit
       bool ok = true;
       for (int i = C::NP == 2 ? wg : 0; i < steps && ok; i += C::NP, ++done) {
         const int j = both ? i >> 1 : i, b = i & 1;
         const uint32_t sc = tmem + lanes + C::S_COL + b * TN;
-        const int tile = U.t0 + j * TN, left = U.t1 - tile, vb0 = tile / C::BS;
+        const int tile = t0 + j * TN, left = t1 - tile, vb0 = tile / C::BS;
         ok = __all_sync(0xffffffffu, wait(C::SFULL + b, b ? n1 : n0, kRowsS, i));
         if (!ok) break;
         if (b) ++n1;
         else ++n0;
         tc_fence_after();
         // Whether every row sees the whole tile.
-        const int p0 = block_pos(U, vb0), p1 = block_pos(U, vb0 + (min(left, TN) - 1) / C::BS) + C::BS - 1;
-        const bool jump = vb0 < U.sink_blocks && U.skip > 0;
+        const int p0 = block_pos(sink_blocks, skip, vb0);
+        const int p1 = block_pos(sink_blocks, skip, vb0 + (min(left, TN) - 1) / C::BS) + C::BS - 1;
+        const bool jump = vb0 < sink_blocks && skip > 0;
         const bool partial = left < TN || jump || p1 >= full_hi || (p0 < full_lo && p1 >= prm.sinks);
         if (partial) {
           // (Values: before the weights of the tile are announced.)
@@ -597,11 +603,12 @@ struct RowsCta {
         for (int c = 0; c < TN; c += 32) tmem_ld32(sc + c, s + c);
         tmem_wait_ld();
         if (partial) {
+          const RowView v = view();
 #pragma unroll
           for (int gi = 0; gi < NG; ++gi)
 #pragma unroll
             for (int bi = 0; bi < NB; ++bi) {
-              const uint32_t m = group_seen(v, block_pos(U, vb0 + bi) + gi * 8, left - bi * C::BS - gi * 8);
+              const uint32_t m = group_seen(v, block_pos(sink_blocks, skip, vb0 + bi) + gi * 8, left - bi * C::BS - gi * 8);
 #pragma unroll
               for (int t = 0; t < 8; ++t)
                 if (!((m >> t) & 1u)) s[C::column(bi, gi, t)] = -INFINITY;
@@ -612,7 +619,6 @@ struct RowsCta {
 #pragma unroll
         for (int c = 0; c < TN; ++c) m4[c & 3] = fmaxf(m4[c & 3], s[c]);
         float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * sl2;
-        if (v.hi == 0) mx = -INFINITY;  // (padding, and rows past the unit's: weights of no use)
         const bool first = C::NP == 2 ? done == 0 : i == 0;
         if (mx > mref + 8.f || (mref == -INFINITY && mx > -INFINITY)) {
           const float alpha = exp2_approx(mref - mx);
@@ -673,6 +679,7 @@ struct RowsCta {
       if (!ok) break;
       // ---- the end of the unit: join the pipelines' states (one row a thread), write.
       const uint32_t ob = tmem + lanes + C::O_COL;
+      const RowView v = view();
       if (done > 0) {
         // (Products are complete in their order: the last one's barrier is enough.)
         const int pb = (steps - 1) & 1, lb = C::NP == 2 ? wg : pb;
@@ -686,7 +693,7 @@ struct RowsCta {
         tmem_wait_st();
         tc_fence_before();
       }
-      if (U.nt == 0) {  // (nothing of this unit came from the product thread)
+      if (nt == 0) {  // (nothing of this unit came from the product warp)
         ok = __all_sync(0xffffffffu, wait(C::QFREE + (k & 1), k >> 1, kRowsQFree, (int)k));
         if (!ok) break;
       }
@@ -695,8 +702,8 @@ struct RowsCta {
       if (!ok) break;
       tc_fence_after();
       const bool odd = *odd_unit == (int)k + 1;
-      float f[2] = {1.f, 0.f};
-      bool has[2] = {U.nt > 0, false};  // pipelines with something in O
+      float f0 = 1.f, f1 = 0.f;
+      bool has0 = nt > 0, has1 = false;  // pipelines with something in O
       int o0 = 0, d_lo = 0, d_hi = D;
       if (C::NP == 2 && !both) {
         // Both warpgroups have every row: each writes half of its dims.
@@ -705,13 +712,13 @@ struct RowsCta {
         tmem_wait_ld();
         tc_fence_before();
         mbar_arrive(bar(C::XFREE));
-        float ma = wg ? m2 : mref, la = wg ? l2 : l, mb = wg ? mref : m2, lb = wg ? l : l2;
+        const float ma = wg ? m2 : mref, la = wg ? l2 : l, mb = wg ? mref : m2, lb = wg ? l : l2;
         const float M = fmaxf(ma, mb), Ms = M == -INFINITY ? 0.f : M;
-        f[0] = exp2_approx(ma - Ms);
-        f[1] = exp2_approx(mb - Ms);
-        l = f[0] * la + f[1] * lb;
+        f0 = exp2_approx(ma - Ms);
+        f1 = exp2_approx(mb - Ms);
+        l = f0 * la + f1 * lb;
         mref = M;
-        has[1] = U.nt > 1;
+        has1 = nt > 1;
         constexpr int HALF = D / 32 * 16;
         d_lo = wg ? HALF : 0;
         d_hi = wg ? D : HALF;
@@ -719,65 +726,88 @@ struct RowsCta {
         mbar_arrive(bar(C::XFREE));
         o0 = wg;
       }
-      const float inv = l != 0.f ? 1.f / l : 0.f;
-      const bool single = U.np == 1;
-      const size_t sh0 = (size_t)U.s * prm.H + U.h0, sh = sh0 + row;
-      const int orow = mine ? (int)out_row<kView>(prm, U.s, U.h0 + row) : 0;  // (below 2^25: 256 sequences)
-#pragma unroll 1
-      for (int c = d_lo; c < d_hi; c += 16) {
-        float o[16];
-#pragma unroll
-        for (int q = 0; q < 16; ++q) o[q] = 0.f;
-        float o2[16];
-        if (has[0]) tmem_ld16(ob + o0 * C::O_STEP + c, o);
-        if (has[1]) tmem_ld16(ob + C::O_STEP + c, o2);
-        tmem_wait_ld();
-        if (has[0]) {
-#pragma unroll
-          for (int q = 0; q < 16; ++q) o[q] *= f[0];
-        }
-        if (has[1]) {
-#pragma unroll
-          for (int q = 0; q < 16; ++q) o[q] = fmaf(o2[q], f[1], o[q]);
-        }
-        if (odd && mine && v.hi > 0) {
-          float x[16];
-#pragma unroll
-          for (int q = 0; q < 16; ++q) x[q] = o[q];
-          add_odd(U, v, c, x);
-#pragma unroll
-          for (int q = 0; q < 16; ++q) o[q] = x[q];
-        }
-        __syncwarp();
+      if (warp_rows) {
         const bool some = v.hi > 0 && l != 0.f;
-#pragma unroll
-        for (int q = 0; q < 16; ++q) o[q] = some ? o[q] * inv : 0.f;
-        // Four lanes exchange their rows' pieces of four dims: then lane q of the four has
-        // piece q of each of their rows, and they store 16 dims of one row at a time (a
-        // lane a row touched 32 lines with every store).
-        transpose4(o, lane);
+        const float inv = some ? 1.f / l : 0.f;
+        f0 *= inv;
+        f1 *= inv;
+        const bool single = U.np == 1;
+        const size_t sh0 = (size_t)U.s * prm.H + U.h0, sh = sh0 + row;
+        const int orow = mine ? (int)out_row<kView>(prm, U.s, U.h0 + row) : 0;  // (below 2^25: 256 sequences)
+        // Where the lane stores: its piece of four dims of each of its four lanes' rows.
+        uint8_t* to[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int r = (row & ~3) + i;
-          const int orow_i = __shfl_sync(0xffffffffu, orow, (lane & ~3) + i);
-          const float4 x = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-          const int d = c + (lane & 3) * 4;
-          if (r < U.nh) {
-            if (single) store4<T>(static_cast<T*>(prm.out) + (size_t)orow_i * D + d, x);
-            else st_f4_policy(reinterpret_cast<float4*>(prm.ws_o + ((sh0 + r) * prm.Pmax + U.p) * D + d), x, pol_keep);
+          const int r = (row & ~3) + i, ri = __shfl_sync(0xffffffffu, orow, (lane & ~3) + i);
+          to[i] = r >= nh ? nullptr
+                  : single  ? static_cast<uint8_t*>(prm.out) + ((size_t)ri * D + (lane & 3) * 4) * sizeof(T)
+                            : reinterpret_cast<uint8_t*>(prm.ws_o + ((sh0 + r) * prm.Pmax + U.p) * D + (lane & 3) * 4);
+        }
+        constexpr int NCH = 2;  // pieces of 16 dims at a time
+#pragma unroll 1
+        for (int c0 = d_lo; c0 < d_hi; c0 += NCH * 16) {
+          float a[NCH][16], b[NCH][16];
+#pragma unroll
+          for (int h = 0; h < NCH; ++h) {
+            if (c0 + h * 16 >= d_hi) break;
+            if (has0) tmem_ld16(ob + o0 * C::O_STEP + c0 + h * 16, a[h]);
+            if (has1) tmem_ld16(ob + C::O_STEP + c0 + h * 16, b[h]);
+          }
+          tmem_wait_ld();
+#pragma unroll
+          for (int h = 0; h < NCH; ++h) {
+            if (c0 + h * 16 >= d_hi) break;
+            float (&o)[16] = a[h];
+            if (has1) {
+#pragma unroll
+              for (int q = 0; q < 16; ++q) o[q] = fmaf(b[h][q], f1, o[q] * f0);
+            } else {
+#pragma unroll
+              for (int q = 0; q < 16; ++q) o[q] *= f0;
+            }
+            if (!some || !has0) {
+#pragma unroll
+              for (int q = 0; q < 16; ++q) o[q] = 0.f;
+            }
+            // Four lanes exchange their rows' pieces of four dims: then lane q of the four has
+            // piece q of each of their rows, and they store 16 dims of one row at a time (a
+            // lane a row touched 32 lines with every store).
+            __syncwarp();
+            transpose4(o, lane);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float4 x = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+              if (!to[i]) continue;
+              if (single) store4<T>(reinterpret_cast<T*>(to[i]) + c0 + 16 * h, x);
+              else st_f4_policy(reinterpret_cast<float4*>(to[i]) + (c0 + 16 * h) / 4, x, pol_keep);
+            }
           }
         }
-      }
-      if (mine && d_lo == 0) {
-        const bool none = v.hi == 0 || l == 0.f;
-        const float mn = none ? -INFINITY : mref * kLn2;
-        st_f32_policy(prm.ws_m + sh * prm.Pmax + U.p, mn, pol_keep);
-        st_f32_policy(prm.ws_l + sh * prm.Pmax + U.p, none ? 0.f : l, pol_keep);
-        if (single && prm.lse) prm.lse[orow] = none ? -INFINITY : mn + logf(l);
+        if (odd) {
+          __syncwarp();
+          if (mine && some) {
+            if (single)
+              add_odd(U.s, U.kv, t0, t1, sink_blocks, skip, v.lo, v.hi, v.base, v.bits, d_lo, d_hi,
+                      static_cast<T*>(prm.out) + (size_t)orow * D);
+            else
+              add_odd(U.s, U.kv, t0, t1, sink_blocks, skip, v.lo, v.hi, v.base, v.bits, d_lo, d_hi,
+                      prm.ws_o + (sh * prm.Pmax + U.p) * D);
+          }
+          __syncwarp();
+        }
+        if (mine && d_lo == 0) {
+          const float mn = some ? mref * kLn2 : -INFINITY;
+          st_f32_policy(prm.ws_m + sh * prm.Pmax + U.p, mn, pol_keep);
+          st_f32_policy(prm.ws_l + sh * prm.Pmax + U.p, some ? l : 0.f, pol_keep);
+          if (single && prm.lse) prm.lse[orow] = some ? mn + logf(l) : -INFINITY;
+        }
+        __syncwarp();
       }
       tc_fence_before();
       mbar_arrive(bar(C::OFREE));
-      g += 2 * U.nt;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(C::UEMPTY + k % C::UQ));
+      g += 2 * nt;
       ++k;
     }
   }
