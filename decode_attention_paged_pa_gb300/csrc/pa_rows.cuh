@@ -10,12 +10,12 @@
 //   O[rows x D]     += P[rows x tokens] . V    tcgen05.mma, P in tensor memory
 //
 // Both operands of the cache are read as they lie in the page layouts.  A key block
-// [D/8][BS][8] is a column of core matrices (8 tokens x 16 bytes); one instruction
-// takes the same eight tokens of every block of a tile (the stride between rows of
-// core matrices is that between blocks), so the scores of a tile of TN tokens come
-// in BS / 8 instructions a k-step, their columns ordered (group of eight tokens,
-// block, token); blocks of 32 tokens or more are copied by chunks of eight dims to
-// make one column of core matrices a tile and chunk (kChunks), one instruction.  A value block [D][BS] is K-major with rows of 2 BS bytes: the
+// [D/8][BS][8] is a column of core matrices (8 tokens x 16 bytes) for each chunk of
+// eight dims; one instruction takes a block's tokens, or the same eight tokens of
+// every block of a tile (the stride between rows of core matrices is then that
+// between blocks).  (Blocks copied chunk by chunk, to make one column of core
+// matrices of a tile and one instruction of it, took 450 us where whole blocks take
+// 160: a bulk copy of 256 bytes takes as long as one of 4 KB.)  A value block [D][BS] is K-major with rows of 2 BS bytes: the
 // tensor copy stores it in the swizzle of that width.
 //
 // One CTA per SM, persistent over units (sequence, partition, kv head, up to GT
@@ -34,9 +34,11 @@
 // roundings are as exact as those of weights below 1.  Weights are rounded to the
 // element type; bf16 ones as the sum of two terms (two products), as in pa_mma.cuh.
 //
-// Tensor memory (512 columns of 128 lanes): scores of either pipeline, overlaid by
-// its weights once they are read, and O of either.  A product that writes scores
-// over weights is issued behind the one that reads them, by the same thread.
+// Tensor memory (512 columns of 128 lanes): two buffers of scores, two of weights, O
+// of either pipeline.  The scores of a pipeline's next tile are computed as soon as
+// those of its last are read: they and the values' products run beside the softmax.
+// (Tiles of 128 tokens whose weights took the scores' place had each step wait for
+// both products: 16 nodes 157 us where this form takes 110.)
 //
 // A tile that some row does not see whole is masked row by row, eight tokens at a
 // time; values of it that are not finite are cleared in shared memory (their
@@ -63,41 +65,38 @@ struct RowsConfig {
   using T = T_;
   static constexpr int D = D_, BS = BS_;
   static constexpr int NP = D_ <= 128 ? 2 : 1;     // pipelines (warpgroups)
-  static constexpr int TN = D_ <= 128 ? 128 : 64;  // tokens per tile
+  static constexpr int TN = 64;                    // tokens per tile
   static constexpr int GT = 128 * NP, KVU = 1;     // rows per unit; (plan_unit) kv heads per unit
   static constexpr int NB = TN / BS, NG = BS / 8;  // blocks of a tile, groups of eight tokens of a block
   static constexpr bool kTma = BS_ >= 16;
   static constexpr bool kBf16 = std::is_same<T_, __nv_bfloat16>::value;
   static constexpr uint32_t BLK = (uint32_t)D_ * BS_ * 2, SLOT = (uint32_t)TN * D_ * 2, QTILE = 128u * D_ * 2;
   static constexpr int THREADS = NP * 128 + 128, UQ = 2;
-  // Keys are copied a chunk of eight dims at a time where a block's chunk is long enough
-  // (512 bytes): the tile then is one column of core matrices a chunk, and its scores
-  // one instruction a k-step.  Of shorter blocks each is one copy.
-  static constexpr bool kChunks = BS_ >= 32 && NB > 1;
+  // A tile's scores take NI instructions a k-step of N columns each: one a block, or
+  // (kGroups) one for each group of eight tokens, of every block, whichever are fewer.
+  static constexpr bool kGroups = NG < NB;
+  static constexpr int NI = kGroups ? NG : NB, N = TN / NI;
   static constexpr int LOADERS = 64;  // threads that bring Q
-  // Registers: the launch's 168 a thread (384 threads) are dealt out anew, 216 for the
-  // warpgroups of the softmax (whose rows hold TN scores) and 72 for the other one.
-  static constexpr int REGS = 168, SOFT_REGS = 216, REST_REGS = 72;
-  static_assert(NP == 1 || 256 * SOFT_REGS + 128 * REST_REGS == THREADS * REGS, "the launch's registers");
   // Tensor memory columns.
-  static constexpr uint32_t S_COL = 0, O_COL = 2 * TN, O_STEP = 128;
-  static_assert(2 * TN + (NP == 2 ? 256 : 256) <= 512, "tensor memory");
+  // Two buffers of scores, two of weights (bf16: two words of 16 bits each), O.
+  static constexpr uint32_t S_COL = 0, P_COL = 2 * TN, O_COL = 4 * TN, O_STEP = 128;
+  static_assert(4 * TN + 256 <= 512, "tensor memory");
   // Shared memory: Q tiles, the ring, then barriers, units, flags, order.
   static constexpr uint32_t QBYTES = NP * QTILE;
   static constexpr uint32_t small(int ns) {
-    return al16((2 * ns + 2 * UQ + 13) * 8) + al16(UQ * sizeof(RowsUnit)) + 64 + al16((kRowsMaxUnitSeqs + 1) * 4) +
+    return al16((2 * ns + 2 * UQ + 15) * 8) + al16(UQ * sizeof(RowsUnit)) + 64 + al16((kRowsMaxUnitSeqs + 1) * 4) +
            al16(kRowsMaxUnitSeqs * 2);
   }
   static constexpr int NS = (int)((kRowsSmem - small(16) - QBYTES) / SLOT) < 16
                                 ? (int)((kRowsSmem - small(16) - QBYTES) / SLOT)
                                 : 16;
-  static_assert(NS >= 3, "the ring holds a tile's keys and values and the next keys");
+  static_assert(NS >= 5, "the ring holds three tiles' keys and two tiles' values");
   // The score column of token t of group gi of eight of block bi.
   static constexpr __device__ __forceinline__ int column(int bi, int gi, int t) {
-    return kChunks ? bi * BS_ + gi * 8 + t : (gi * NB + bi) * 8 + t;
+    return kGroups ? (gi * NB + bi) * 8 + t : bi * BS_ + gi * 8 + t;
   }
   static constexpr uint32_t OFF_RING = QBYTES, OFF_BAR = OFF_RING + NS * SLOT;
-  static constexpr uint32_t OFF_INFO = OFF_BAR + al16((2 * NS + 2 * UQ + 13) * 8);
+  static constexpr uint32_t OFF_INFO = OFF_BAR + al16((2 * NS + 2 * UQ + 15) * 8);
   static constexpr uint32_t OFF_FLAGS = OFF_INFO + al16(UQ * sizeof(RowsUnit));
   static constexpr uint32_t OFF_PREF = OFF_FLAGS + 64;
   static constexpr uint32_t OFF_PERM = OFF_PREF + al16((kRowsMaxUnitSeqs + 1) * 4);
@@ -106,15 +105,15 @@ struct RowsConfig {
   static_assert(NS * SLOT >= kOrderTempBytes, "prologue temporaries fit in the ring");
   // Barriers.
   static constexpr uint32_t FULL = 0, EMPTY = NS, UFULL = 2 * NS, UEMPTY = UFULL + UQ, QFULL = UEMPTY + UQ,
-                            QFREE = QFULL + 1, SFULL = QFREE + 2, PREADY = SFULL + 2, PVDONE = PREADY + 2,
+                            QFREE = QFULL + 1, SFULL = QFREE + 2, SREAD = SFULL + 2, PREADY = SREAD + 2, PVDONE = PREADY + 2,
                             OFREE = PVDONE + 2, XBAR = OFREE + 1, XFREE = XBAR + 1, DRAIN = XFREE + 1;
-  static_assert(DRAIN + 1 == 2 * NS + 2 * UQ + 13, "barriers");
+  static_assert(DRAIN + 1 == 2 * NS + 2 * UQ + 15, "barriers");
 };
 
 // Wait sites of this kernel (see WaitSite).
 enum RowsSite {
   kRowsUnitSlot = 20, kRowsRing = 21, kRowsUnit = 22, kRowsQ = 23, kRowsOFree = 24, kRowsFull = 25, kRowsP = 26,
-  kRowsS = 27, kRowsPv = 28, kRowsQFree = 29, kRowsX = 30
+  kRowsS = 27, kRowsPv = 28, kRowsQFree = 29, kRowsX = 30, kRowsRead = 31
 };
 
 template <class C>
@@ -132,7 +131,15 @@ struct RowsCta {
   __device__ __forceinline__ bool wait(uint32_t b, uint32_t phase, int site, int detail) const {
     return wait_bounded(bar(b), phase & 1u, abort_flag, err, prm.timeout_ns, site, detail);
   }
-  // Ring item g (keys and values of the CTA's tiles in turn).
+  // Ring items, in the order in which they are done with: where the pipelines take the
+  // tiles in turn, keys are two tiles ahead of the values (K0 K1 K2 V0 K3 V1 ..), else
+  // one (K0 K1 V0 K2 V1 ..).  The items of the keys and values of tile j of nt.
+  static __device__ __forceinline__ uint32_t key_item(bool both, int j) {
+    return both ? (j == 0 ? 0 : 2 * j - 1) : (j < 2 ? j : 2 * j - 2);
+  }
+  static __device__ __forceinline__ uint32_t value_item(bool both, int j, int nt) {
+    return both ? min(2 * j + 2, 2 * nt - 1) : min(2 * j + 3, nt + j);
+  }
   __device__ __forceinline__ uint32_t slot(uint32_t g) const { return g % C::NS; }
   __device__ __forceinline__ uint32_t phase(uint32_t g) const { return g / C::NS; }
 
@@ -209,44 +216,36 @@ struct RowsCta {
       if (!have) break;
       int ids = fetch_ids(U, 0, lane), ids_next = U.nt > PER ? fetch_ids(U, 32, lane) : 0, claimed = 0;
       if (U.nt == 0 && lane == 0) claimed = atomicAdd(prm.hdr + kHdrWork, 1);
-      for (int j = 0; j < U.nt && ok; ++j) {
-        if (j > 0 && j % PER == 0) {
+      const bool both = C::NP == 2 && U.nh > 128;
+      int ids_v = ids, jk = 0, jv = 0;  // the next keys' and values' tiles
+      for (int i = 0; i < 2 * U.nt && ok; ++i) {
+        // (Whichever of the next keys and the next values is item i.)
+        const bool value = jk == U.nt || key_item(both, jk) != (uint32_t)i;
+        const int j = value ? jv++ : jk++;
+        if (!value && j > 0 && j % PER == 0) {
           ids = ids_next;
           if (j + PER < U.nt) ids_next = fetch_ids(U, (j + PER) * NB, lane);
         }
+        if (value && j % PER == 0) ids_v = ids;  // (PER is 4 or more: the keys are in the same 32 blocks)
         // (The next unit is taken while this one's last tile is on its way.)
-        if (j + 1 == U.nt && lane == 0) claimed = atomicAdd(prm.hdr + kHdrWork, 1);
+        if (!value && j + 1 == U.nt && lane == 0) claimed = atomicAdd(prm.hdr + kHdrWork, 1);
         const int nb = min(NB, (U.t1 - U.t0 - j * C::TN + C::BS - 1) / C::BS);
-        const int id = check_block_id(prm, __shfl_sync(0xffffffffu, ids, (j % PER) * NB + (lane < nb ? lane : 0)));
-#pragma unroll
-        for (int w = 0; w < 2; ++w) {  // keys, values
-          const uint32_t sl = slot(g), fb = bar(C::FULL + sl), dst = sbase + C::OFF_RING + sl * C::SLOT;
-          ok = __shfl_sync(0xffffffffu, lane == 0 ? (int)wait(C::EMPTY + sl, phase(g) + 1, kRowsRing, (int)g) : 0, 0);
-          if (!ok) break;
-          if (lane == 0) mbar_arrive_expect_tx(fb, (uint32_t)nb * C::BLK);
-          __syncwarp();
-          if (w == 0 && C::kChunks) {
-            // Chunk c of block b: BS * 16 bytes to c * TN * 16 + b * BS * 16.
-            constexpr int CH = C::D / 8;
-            for (int i0 = 0; i0 < nb * CH; i0 += 32) {
-              const int i = i0 + lane, b = min(i / CH, nb - 1), c = i - b * CH;
-              const int idb = __shfl_sync(0xffffffffu, id, b);
-              if (i < nb * CH)
-                bulk_copy_g2s(dst + c * (C::TN * 16) + b * (C::BS * 16),
-                              static_cast<const uint8_t*>(prm.kc) + ((size_t)idb * prm.KH + U.kv) * C::BLK +
-                                  c * (C::BS * 16),
-                              C::BS * 16, fb, pol);
-            }
-          } else if (lane < nb) {
-            const size_t row = (size_t)id * prm.KH + U.kv;
-            if (w == 0 || !C::kTma)
-              bulk_copy_g2s(dst + lane * C::BLK, static_cast<const uint8_t*>(w ? prm.vc : prm.kc) + row * C::BLK,
-                            C::BLK, fb, pol);
-            else  // (x = 0: the 16-byte alignment rule holds)
-              tma_load_3d(dst + lane * C::BLK, &prm.tmv, 0, 0, (int)row, fb, pol);
-          }
-          ++g;
+        const int id = check_block_id(
+            prm, __shfl_sync(0xffffffffu, value ? ids_v : ids, (j % PER) * NB + (lane < nb ? lane : 0)));
+        const uint32_t sl = slot(g), fb = bar(C::FULL + sl), dst = sbase + C::OFF_RING + sl * C::SLOT;
+        ok = __shfl_sync(0xffffffffu, lane == 0 ? (int)wait(C::EMPTY + sl, phase(g) + 1, kRowsRing, (int)g) : 0, 0);
+        if (!ok) break;
+        if (lane == 0) mbar_arrive_expect_tx(fb, (uint32_t)nb * C::BLK);
+        __syncwarp();
+        if (lane < nb) {
+          const size_t row = (size_t)id * prm.KH + U.kv;
+          if (!value || !C::kTma)
+            bulk_copy_g2s(dst + lane * C::BLK, static_cast<const uint8_t*>(value ? prm.vc : prm.kc) + row * C::BLK,
+                          C::BLK, fb, pol);
+          else  // (x = 0: the 16-byte alignment rule holds)
+            tma_load_3d(dst + lane * C::BLK, &prm.tmv, 0, 0, (int)row, fb, pol);
         }
+        ++g;
       }
       u = __shfl_sync(0xffffffffu, claimed, 0) + (int)gridDim.x;
     }
@@ -267,18 +266,16 @@ struct RowsCta {
   // a product, more than the product).
   // Scores of ring slot `sl` against Q tile q, into score buffer b.
   __device__ __forceinline__ void issue_scores(uint32_t tmem, int q, uint32_t sl, int b, uint32_t idesc) const {
-    constexpr bool ONE = C::kChunks || C::NB == 1;     // the tile's tokens lie one behind another
-    constexpr int NI = ONE ? 1 : C::NG;                // instructions a k-step
-    constexpr int N = C::TN / NI;                      // columns of each
-    constexpr uint32_t STRIDE = ONE ? 128u : C::BLK;   // from eight tokens to the next
-    constexpr uint32_t LEAD = ONE ? C::TN * 16u : C::BS * 16u;  // from a chunk of dims to the next
+    constexpr uint32_t STEP = C::kGroups ? 128u : C::BLK;    // from one instruction's tokens to the next one's
+    constexpr uint32_t STRIDE = C::kGroups ? C::BLK : 128u;  // from eight tokens of an instruction to the next
+    constexpr uint32_t LEAD = C::BS * 16u;                   // from a chunk of dims to the next
     const uint32_t qa = desc_lo(sbase + q * C::QTILE, 2048), ka = desc_lo(sbase + C::OFF_RING + sl * C::SLOT, LEAD);
     const uint32_t d = tmem + C::S_COL + b * C::TN;
 #pragma unroll
     for (int kk = 0; kk < C::D / 16; ++kk)
 #pragma unroll
-      for (int i = 0; i < NI; ++i)
-        mma_ss(d + i * N, qa + kk * (4096 / 16), desc_hi(128, kSwizzleNone), ka + (kk * 2 * LEAD + i * 128) / 16,
+      for (int i = 0; i < C::NI; ++i)
+        mma_ss(d + i * C::N, qa + kk * (4096 / 16), desc_hi(128, kSwizzleNone), ka + (kk * 2 * LEAD + i * STEP) / 16,
                desc_hi(STRIDE, kSwizzleNone), idesc, kk > 0);
   }
   // O[o] (+)= weights of buffer b times the values in slot `sl`, `ks` k-steps.
@@ -288,7 +285,7 @@ struct RowsCta {
     constexpr uint32_t SW = C::BS == 8 ? kSwizzleNone : C::BS == 16 ? kSwizzle32 : C::BS == 32 ? kSwizzle64 : kSwizzle128;
     constexpr uint32_t HI = desc_hi(C::BS == 8 ? 128 : C::BS * 16, SW);
     const uint32_t va = desc_lo(sbase + C::OFF_RING + sl * C::SLOT, C::BS == 8 ? C::BLK : 16);
-    const uint32_t d = tmem + C::O_COL + o * C::O_STEP, p = tmem + C::S_COL + b * C::TN;
+    const uint32_t d = tmem + C::O_COL + o * C::O_STEP, p = tmem + C::P_COL + b * C::TN;
 #pragma unroll
     for (int h = 0; h < (C::kBf16 ? 2 : 1); ++h) {
 #pragma unroll
@@ -302,13 +299,13 @@ struct RowsCta {
   }
   __device__ __forceinline__ void products(uint32_t tmem, int lane) {
     const RowsUnit* info = reinterpret_cast<const RowsUnit*>(smem + C::OFF_INFO);
-    constexpr int N = C::kChunks || C::NB == 1 ? C::TN : C::TN / C::NG;
-    const uint32_t id_s = f16_idesc(C::kBf16, N), id_o = f16_idesc(C::kBf16, C::D);
+    const uint32_t id_s = f16_idesc(C::kBf16, C::N), id_o = f16_idesc(C::kBf16, C::D);
     const auto all = [&](uint32_t b, uint32_t ph, int site, int detail) {
       return __all_sync(0xffffffffu, wait(b, ph, site, detail)) != 0;
     };
     uint32_t g = 0, k = 0;          // ring items and units before this unit
     uint32_t n0 = 0, n1 = 0;        // weights taken from each buffer
+    uint32_t r0 = 0, r1 = 0;        // scores that were read from each buffer
     QBuffers qb;
     bool ok = true;
     while (ok) {
@@ -326,10 +323,10 @@ struct RowsCta {
       // is ever more than a unit ahead, so that a parity tells the phases apart.)
       if (!all(C::XFREE, k + 1, kRowsX, (int)k)) break;
       tc_fence_after();
-      // (Scores of step i + 2 go where the weights of step i were.)
+      // (Scores of step i + 2 go where those of step i were, once they are read.)
       const auto scores = [&](int i) {
         const int j = both ? i >> 1 : i;
-        const uint32_t it = g + 2 * j;
+        const uint32_t it = g + key_item(both, j);
         if (!both || !(i & 1)) {
           if (!all(C::FULL + slot(it), phase(it), kRowsFull, (int)it)) return false;
         }
@@ -344,8 +341,13 @@ struct RowsCta {
       for (int i = 0; i < 2 && i < steps && ok; ++i) ok = scores(i);
       for (int i = 0; i < steps && ok; ++i) {
         const int j = both ? i >> 1 : i, b = i & 1, o = C::NP == 2 ? b : 0;
-        const uint32_t it = g + 2 * j + 1;
-        ok = all(C::FULL + slot(it), phase(it), kRowsFull, (int)it);
+        const uint32_t it = g + value_item(both, j, nt);
+        if (i + 2 < steps) {
+          ok = all(C::SREAD + b, (b ? r1 : r0)++, kRowsRead, i);
+          tc_fence_after();
+          ok = ok && scores(i + 2);
+        }
+        if (ok) ok = all(C::FULL + slot(it), phase(it), kRowsFull, (int)it);
         if (ok && i < 2) ok = all(C::OFREE, k + 1, kRowsOFree, (int)k);  // the last unit's O is read
         if (ok) ok = all(C::PREADY + b, b ? n1 : n0, kRowsP, i);
         if (!ok) break;
@@ -359,8 +361,10 @@ struct RowsCta {
           if (!both || (i & 1)) mma_commit(bar(C::EMPTY + slot(it)));
         }
         __syncwarp();
-        if (i + 2 < steps) ok = scores(i + 2);
       }
+      if (!ok) break;
+      // (Scores that nothing followed have been read, too.)
+      for (int i = max(0, steps - 2); i < steps && ok; ++i) ok = all(C::SREAD + (i & 1), (i & 1 ? r1 : r0)++, kRowsRead, i);
       if (!ok) break;
       if (elect_one()) mma_commit(bar(C::QFREE + (k & 1)));
       __syncwarp();
@@ -586,15 +590,21 @@ struct RowsCta {
         const bool partial = left < TN || jump || p1 >= full_hi || (p0 < full_lo && p1 >= prm.sinks);
         if (partial) {
           // (Values: before the weights of the tile are announced.)
-          const uint32_t it = g + 2 * j + 1;
+          const uint32_t it = g + value_item(both, j, nt);
           ok = __all_sync(0xffffffffu, wait(C::FULL + slot(it), phase(it), kRowsFull, (int)it));
           if (!ok) break;
           if (clear_values(slot(it), left, tid)) *odd_unit = (int)k + 1;
           fence_proxy_async_smem();
           __syncwarp();
         }
-        if (!warp_rows) {  // a warp without rows only keeps the count
-          tc_fence_before();
+        if (!warp_rows) {
+          // A warp without rows only keeps the counts; it waits as the others do, or its
+          // next arrival would stand for one that theirs lack.
+          mbar_arrive(bar(C::SREAD + b));
+          if ((b ? n1 : n0) > 1) {
+            ok = __all_sync(0xffffffffu, wait(C::PVDONE + b, (b ? n1 : n0) - 2, kRowsPv, i));
+            if (!ok) break;
+          }
           mbar_arrive(bar(C::PREADY + b));
           continue;
         }
@@ -602,6 +612,8 @@ struct RowsCta {
 #pragma unroll
         for (int c = 0; c < TN; c += 32) tmem_ld32(sc + c, s + c);
         tmem_wait_ld();
+        tc_fence_before();
+        mbar_arrive(bar(C::SREAD + b));
         if (partial) {
           const RowView v = view();
 #pragma unroll
@@ -629,11 +641,17 @@ struct RowsCta {
         } else {
           mx = 1.f;
         }
+        // The products with this buffer's weights before are complete (each buffer's have
+        // a barrier, on which they are never two ahead).
+        if ((b ? n1 : n0) > 1) {
+          ok = __all_sync(0xffffffffu, wait(C::PVDONE + b, (b ? n1 : n0) - 2, kRowsPv, i));
+          if (!ok) break;
+          tc_fence_after();
+        }
+        __syncwarp();
         if (!first && __any_sync(0xffffffffu, mx != 1.f)) {
-          // O by the rows' factors, once the product before is complete.
-          // (Each buffer's products have a barrier, on which they are never two ahead.)
-          const int pb = C::NP == 2 ? b : b ^ 1;
-          ok = __all_sync(0xffffffffu, wait(C::PVDONE + pb, (pb ? n1 : n0) - (C::NP == 2 ? 2 : 1), kRowsPv, i));
+          // O by the rows' factors, once all products before are complete.
+          if (C::NP == 1) ok = __all_sync(0xffffffffu, wait(C::PVDONE + (b ^ 1), (b ? n0 : n1) - 1, kRowsPv, i));
           if (!ok) break;
           tc_fence_after();
           const uint32_t oc = tmem + lanes + C::O_COL + (C::NP == 2 ? wg : 0) * C::O_STEP;
@@ -656,21 +674,25 @@ struct RowsCta {
           sum[c & 3] += s[c];
         }
         l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        // Weights, in token order: word w holds tokens 2w, 2w + 1 of the tile.
+        // Weights, in token order: word w holds tokens 2w, 2w + 1 of the tile.  bf16: the
+        // weight cut to its first 8 bits, and what that leaves (exact in fp32) rounded.
+        const uint32_t pc = tmem + lanes + C::P_COL + b * TN;
 #pragma unroll
         for (int w0 = 0; w0 < TN / 2; w0 += 16) {
           uint32_t hi[16], lo[16];
 #pragma unroll
           for (int q = 0; q < 16; ++q) {
             const int t = 2 * (w0 + q), e = C::column(t / C::BS, t % C::BS / 8, t % 8);
-            hi[q] = F16Traits<T>::pack(s[e], s[e + 1]);
             if constexpr (C::kBf16) {
-              const float2 f = F16Traits<T>::to_float2(hi[q]);
-              lo[q] = F16Traits<T>::pack(s[e] - f.x, s[e + 1] - f.y);
+              const uint32_t x = __float_as_uint(s[e]), y = __float_as_uint(s[e + 1]);
+              hi[q] = __byte_perm(x, y, 0x7632);
+              lo[q] = F16Traits<T>::pack(s[e] - __uint_as_float(x & 0xffff0000u), s[e + 1] - __uint_as_float(y & 0xffff0000u));
+            } else {
+              hi[q] = F16Traits<T>::pack(s[e], s[e + 1]);
             }
           }
-          tmem_st16(sc + w0, hi);
-          if constexpr (C::kBf16) tmem_st16(sc + TN / 2 + w0, lo);
+          tmem_st16(pc + w0, hi);
+          if constexpr (C::kBf16) tmem_st16(pc + TN / 2 + w0, lo);
         }
         tmem_wait_st();
         tc_fence_before();
@@ -837,6 +859,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) pa_rows_kernel(const __grid_con
     mbar_init(cta.bar(C::QFREE + 1), 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(cta.bar(C::SFULL + i), 1);
+      mbar_init(cta.bar(C::SREAD + i), 128);
       mbar_init(cta.bar(C::PREADY + i), 128);
       mbar_init(cta.bar(C::PVDONE + i), 1);
     }
@@ -855,7 +878,6 @@ __global__ void __launch_bounds__(C::THREADS, 1) pa_rows_kernel(const __grid_con
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (tid == 0 && flags[1]) atomicCAS(prm.hdr + kHdrError, 0, kErrDeviceBounds);
   if (warp < WP) {
-    if constexpr (C::NP == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::SOFT_REGS));
     // Sequences with too few tokens: zeros.
     constexpr int D16 = C::D / 8;
     for (int s = blockIdx.x; s < prm.S; s += gridDim.x) {
@@ -869,7 +891,6 @@ __global__ void __launch_bounds__(C::THREADS, 1) pa_rows_kernel(const __grid_con
     __syncwarp();
     cta.softmax(tmem, warp >> 2, tid & 127);
   } else {
-    if constexpr (C::NP == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REST_REGS));
     if (warp == WP) {
       cta.producer(pref, perm, lane);
     } else if (warp == WM) {

@@ -19,11 +19,6 @@ static cudaError_t rows_go(const KParams& prm, int max_ctas, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const uint64_t bit = (dev >= 0 && dev < 64) ? (1ull << dev) : 0ull;
   if (!bit || !(opted_in.load(std::memory_order_acquire) & bit)) {
-    // (A launch with fewer registers could not deal them out as the kernel does.)
-    cudaFuncAttributes attr;
-    e = cudaFuncGetAttributes(&attr, pa_rows_kernel<C>);
-    if (e != cudaSuccess) return e;
-    if (C::NP == 2 && attr.numRegs != C::REGS) return cudaErrorInvalidConfiguration;
     e = cudaFuncSetAttribute(pa_rows_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::BYTES);
     if (e != cudaSuccess) return e;
     opted_in.fetch_or(bit, std::memory_order_acq_rel);
