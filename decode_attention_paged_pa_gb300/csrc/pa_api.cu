@@ -296,9 +296,9 @@ int decode_impl(void* out, float* lse, const void* query, const void* key_cache,
   // Over a 4-bit cache, 16 rows a unit where a kv head has more than 8: its
   // codes are unpacked once for both halves.
   const int nt = kv4 && G > kMmaGroup && D <= 128 ? 2 : 1;
-  const int gt = view && variant == PA_VARIANT_MMA && !kv_fp8 && G > kMmaGroup ? rows_per_unit(D)
+  const int gt = view && variant == PA_VARIANT_MMA && !kv_fp8 && G > kMmaGroup ? kRowsPerUnit
                  : kv4 ? nt * kMmaGroup : (variant == PA_VARIANT_MMA) ? (wide ? kMmaGroupWide : kMmaGroup) : kSimtGroup;
-  // View rows: with more than eight a kv head, 128 or 256 of them a unit on the
+  // View rows: with more than eight a kv head, 128 of them a unit on the
   // fifth-generation tensor cores (pa_rows.cuh), over 16-bit caches.
   const bool many = view && variant == PA_VARIANT_MMA && !kv_fp8 && G > kMmaGroup;
   // Four query rows per kv head (query heads, or multi-query row heads): a

@@ -92,9 +92,9 @@ cudaError_t launch_rows_f16(const KParams& prm, int D, int BS, int max_ctas, cud
 cudaError_t launch_rows_bf16(const KParams& prm, int D, int BS, int max_ctas, cudaStream_t st);
 cudaError_t launch_rows_x_f16(const KParams& prm, int D, int BS, int max_ctas, cudaStream_t st);
 cudaError_t launch_rows_x_bf16(const KParams& prm, int D, int BS, int max_ctas, cudaStream_t st);
-// Sequences of a launch, and rows of a unit at head size D.
+// Sequences of a launch, and rows of a unit.
 constexpr int kRowsSeqsPerLaunch = 256;
-constexpr int rows_per_unit(int D) { return D <= 128 ? 256 : 128; }
+constexpr int kRowsPerUnit = 128;
 
 // Over a 4-bit cache (queries and output fp16 / bf16), by head size: blocks of
 // 8, 16, 32 or 64 tokens, units of nt * 8 query rows of a kv head, or (kvu = 2, up

@@ -2,11 +2,10 @@
 // the fifth-generation tensor cores (16-bit caches).
 //
 // The rows of a kv head (query tokens x query heads of its group) are the M = 128
-// side of the products, so that a block of the cache is read once for 128 rows (256
-// in a unit of two row tiles), where the units of 8 rows of pa_mma.cuh read it
-// once for 8:
+// side of the products, so that a block of the cache is read once for 128 rows,
+// where the units of 8 rows of pa_mma.cuh read it once for 8:
 //
-//   S[rows x tokens] = Q[rows x D] . K^T       tcgen05.mma, Q and K in shared memory
+//   S[rows x tokens] = Q[rows x D] . K^T       tcgen05.mma, Q in tensor memory
 //   O[rows x D]     += P[rows x tokens] . V    tcgen05.mma, P in tensor memory
 //
 // Both operands of the cache are read as they lie in the page layouts.  A key block
@@ -14,31 +13,25 @@
 // eight dims; one instruction takes a block's tokens, or the same eight tokens of
 // every block of a tile (the stride between rows of core matrices is then that
 // between blocks).  (Blocks copied chunk by chunk, to make one column of core
-// matrices of a tile and one instruction of it, took 450 us where whole blocks take
-// 160: a bulk copy of 256 bytes takes as long as one of 4 KB.)  A value block [D][BS] is K-major with rows of 2 BS bytes: the
-// tensor copy stores it in the swizzle of that width.
+// matrices of a tile, took 450 us where whole blocks took 160: a bulk copy of 256
+// bytes takes as long as one of 4 KB.)  A value block [D][BS] is K-major with rows of
+// 2 BS bytes: the tensor copy stores it in the swizzle of that width.  Q is in tensor
+// memory because a product of N = 32 columns then takes 17 cycles, and 42 with Q in
+// shared memory, whose 4 KB it reads every time (measured; N = 128: 65 either way).
 //
-// One CTA per SM, persistent over units (sequence, partition, kv head, up to GT
+// One CTA per SM, persistent over units (sequence, partition, kv head, up to 128
 // rows), which a producer warp takes from the global counter (as in pa_kernel.cuh)
-// and streams through a ring of K and V tiles; two warps bring Q; one thread issues
-// the products.
-// Warpgroups of four warps, a row a thread, turn scores into weights: two of them
-// (NP = 2) work in turns.  With at most 128 rows in a unit both have the same rows
-// and take the tiles alternately, each with its own O, joined at the end of the
-// unit; with more, each has a row tile and takes every tile.  At head size 256 (NP
-// = 1) one warpgroup does all, with two buffers of scores.
+// and streams through a ring of K and V tiles of 64 tokens; two warps bring Q, a unit
+// ahead; one warp issues the products.  Warpgroups of four warps, a row a thread, turn
+// scores into weights: two of them (NP = 2) take the tiles in turn, each with its own
+// O, joined at the end of the unit; at head size 256 one does all.  Scores are
+// computed up to NBUF tiles ahead, into buffers that the weights then take over.
 //
 // Softmax: scores in fp32; a row keeps a reference (the maximum when it was last
 // set) and sets a new one, rescaling O, only where its maximum has grown by more
 // than 2^8 over it: weights stay below 2^8, whose sums in fp32 and, for fp16,
-// roundings are as exact as those of weights below 1.  Weights are rounded to the
-// element type; bf16 ones as the sum of two terms (two products), as in pa_mma.cuh.
-//
-// Tensor memory (512 columns of 128 lanes): two buffers of scores, two of weights, O
-// of either pipeline.  The scores of a pipeline's next tile are computed as soon as
-// those of its last are read: they and the values' products run beside the softmax.
-// (Tiles of 128 tokens whose weights took the scores' place had each step wait for
-// both products: 16 nodes 157 us where this form takes 110.)
+// roundings are as exact as those of weights below 1.  fp16 weights are rounded once;
+// bf16 ones are the sum of two terms (two products), as in pa_mma.cuh.
 //
 // A tile that some row does not see whole is masked row by row, eight tokens at a
 // time; values of it that are not finite are cleared in shared memory (their
@@ -64,10 +57,11 @@ template <typename T_, int D_, int BS_>
 struct RowsConfig {
   using T = T_;
   static constexpr int D = D_, BS = BS_;
-  static constexpr int NP = D_ <= 128 ? 2 : 1;     // pipelines (warpgroups)
-  static constexpr int TN = 64;                    // tokens per tile
-  static constexpr int GT = 128 * NP, KVU = 1;     // rows per unit; (plan_unit) kv heads per unit
-  static constexpr int NB = TN / BS, NG = BS / 8;  // blocks of a tile, groups of eight tokens of a block
+  static constexpr int NP = D_ <= 128 ? 2 : 1;      // pipelines (warpgroups)
+  static constexpr int NBUF = D_ <= 128 ? 3 : 2;    // buffers of scores and weights
+  static constexpr int TN = 64;                     // tokens per tile
+  static constexpr int GT = 128, KVU = 1;           // rows per unit; (plan_unit) kv heads per unit
+  static constexpr int NB = TN / BS, NG = BS / 8;   // blocks of a tile, groups of eight tokens of a block
   static constexpr bool kTma = BS_ >= 16;
   static constexpr bool kBf16 = std::is_same<T_, __nv_bfloat16>::value;
   static constexpr uint32_t BLK = (uint32_t)D_ * BS_ * 2, SLOT = (uint32_t)TN * D_ * 2, QTILE = 128u * D_ * 2;
@@ -77,26 +71,26 @@ struct RowsConfig {
   static constexpr bool kGroups = NG < NB;
   static constexpr int NI = kGroups ? NG : NB, N = TN / NI;
   static constexpr int LOADERS = 64;  // threads that bring Q
-  // Tensor memory columns.
-  // Two buffers of scores, two of weights (bf16: two words of 16 bits each), O.
-  static constexpr uint32_t S_COL = 0, P_COL = 2 * TN, O_COL = 4 * TN, O_STEP = 128;
-  static_assert(4 * TN + 256 <= 512, "tensor memory");
-  // Shared memory: Q tiles, the ring, then barriers, units, flags, order.
-  static constexpr uint32_t QBYTES = NP * QTILE;
+  // Tensor memory columns: the buffers (scores, then weights: bf16 two words of 16 bits
+  // a token), Q (two dims a column), O of either pipeline.
+  static constexpr uint32_t Q_COL = NBUF * TN, O_COL = 256, O_STEP = 128;
+  static_assert(Q_COL + D_ / 2 <= O_COL && O_COL + (NP == 2 ? 256 : D_) <= 512, "tensor memory");
+  // Shared memory: the next unit's Q, the ring, then barriers, units, flags, order.
+  static constexpr uint32_t QBYTES = QTILE;
+  static constexpr uint32_t bars(int ns) { return 2 * ns + 2 * UQ + 3 * NBUF + 7; }
   static constexpr uint32_t small(int ns) {
-    return al16((2 * ns + 2 * UQ + 15) * 8) + al16(UQ * sizeof(RowsUnit)) + 64 + al16((kRowsMaxUnitSeqs + 1) * 4) +
+    return al16(bars(ns) * 8) + al16(UQ * sizeof(RowsUnit)) + 64 + al16((kRowsMaxUnitSeqs + 1) * 4) +
            al16(kRowsMaxUnitSeqs * 2);
   }
-  static constexpr int NS = (int)((kRowsSmem - small(16) - QBYTES) / SLOT) < 16
-                                ? (int)((kRowsSmem - small(16) - QBYTES) / SLOT)
-                                : 16;
-  static_assert(NS >= 5, "the ring holds three tiles' keys and two tiles' values");
+  static constexpr int kFit = (int)((kRowsSmem - small(16) - QBYTES) / SLOT);
+  static constexpr int NS = kFit < 16 ? kFit : 16;
+  static_assert(NS >= 2 * NBUF, "the ring holds the keys that are ahead and two tiles' values");
   // The score column of token t of group gi of eight of block bi.
   static constexpr __device__ __forceinline__ int column(int bi, int gi, int t) {
     return kGroups ? (gi * NB + bi) * 8 + t : bi * BS_ + gi * 8 + t;
   }
   static constexpr uint32_t OFF_RING = QBYTES, OFF_BAR = OFF_RING + NS * SLOT;
-  static constexpr uint32_t OFF_INFO = OFF_BAR + al16((2 * NS + 2 * UQ + 15) * 8);
+  static constexpr uint32_t OFF_INFO = OFF_BAR + al16(bars(NS) * 8);
   static constexpr uint32_t OFF_FLAGS = OFF_INFO + al16(UQ * sizeof(RowsUnit));
   static constexpr uint32_t OFF_PREF = OFF_FLAGS + 64;
   static constexpr uint32_t OFF_PERM = OFF_PREF + al16((kRowsMaxUnitSeqs + 1) * 4);
@@ -104,16 +98,17 @@ struct RowsConfig {
   static_assert(BYTES <= kRowsSmem && QBYTES % 1024 == 0 && SLOT % 1024 == 0, "shared memory");
   static_assert(NS * SLOT >= kOrderTempBytes, "prologue temporaries fit in the ring");
   // Barriers.
-  static constexpr uint32_t FULL = 0, EMPTY = NS, UFULL = 2 * NS, UEMPTY = UFULL + UQ, QFULL = UEMPTY + UQ,
-                            QFREE = QFULL + 1, SFULL = QFREE + 2, SREAD = SFULL + 2, PREADY = SREAD + 2, PVDONE = PREADY + 2,
-                            OFREE = PVDONE + 2, XBAR = OFREE + 1, XFREE = XBAR + 1, DRAIN = XFREE + 1;
-  static_assert(DRAIN + 1 == 2 * NS + 2 * UQ + 15, "barriers");
+  static constexpr uint32_t FULL = 0, EMPTY = NS, UFULL = 2 * NS, UEMPTY = UFULL + UQ, SFULL = UEMPTY + UQ,
+                            PREADY = SFULL + NBUF, PVDONE = PREADY + NBUF, QSTAGED = PVDONE + NBUF,
+                            QTAKEN = QSTAGED + 1, QREADY = QTAKEN + 1, QFREE = QREADY + 1, OFREE = QFREE + 1,
+                            XBAR = OFREE + 1, XFREE = XBAR + 1;
+  static_assert(XFREE + 1 == bars(NS), "barriers");
 };
 
 // Wait sites of this kernel (see WaitSite).
 enum RowsSite {
   kRowsUnitSlot = 20, kRowsRing = 21, kRowsUnit = 22, kRowsQ = 23, kRowsOFree = 24, kRowsFull = 25, kRowsP = 26,
-  kRowsS = 27, kRowsPv = 28, kRowsQFree = 29, kRowsX = 30, kRowsRead = 31
+  kRowsS = 27, kRowsPv = 28, kRowsQFree = 29, kRowsX = 30
 };
 
 template <class C>
@@ -131,29 +126,30 @@ struct RowsCta {
   __device__ __forceinline__ bool wait(uint32_t b, uint32_t phase, int site, int detail) const {
     return wait_bounded(bar(b), phase & 1u, abort_flag, err, prm.timeout_ns, site, detail);
   }
-  // Ring items, in the order in which they are done with: where the pipelines take the
-  // tiles in turn, keys are two tiles ahead of the values (K0 K1 K2 V0 K3 V1 ..), else
-  // one (K0 K1 V0 K2 V1 ..).  The items of the keys and values of tile j of nt.
-  static __device__ __forceinline__ uint32_t key_item(bool both, int j) {
-    return both ? (j == 0 ? 0 : 2 * j - 1) : (j < 2 ? j : 2 * j - 2);
-  }
-  static __device__ __forceinline__ uint32_t value_item(bool both, int j, int nt) {
-    return both ? min(2 * j + 2, 2 * nt - 1) : min(2 * j + 3, nt + j);
-  }
+  // Ring items, in the order in which they are done with: keys are NBUF tiles ahead of
+  // the values (of three: K0 K1 K2 V0 K3 V1 ..).  The items of tile j of nt.
+  static __device__ __forceinline__ uint32_t key_item(int j) { return j < C::NBUF ? j : 2 * j - C::NBUF + 1; }
+  static __device__ __forceinline__ uint32_t value_item(int j, int nt) { return min(2 * j + C::NBUF, nt + j); }
+
   __device__ __forceinline__ uint32_t slot(uint32_t g) const { return g % C::NS; }
   __device__ __forceinline__ uint32_t phase(uint32_t g) const { return g / C::NS; }
 
-  // Which Q tile a unit of one row tile takes: with two of them, the one that the unit
-  // before did not (a unit of two tiles takes both, `last` = 2).
-  struct QBuffers {
-    int last = 1;
-    __device__ __forceinline__ int next(bool both) {
-      if (C::NP == 1) return last = 0;
-      if (both) {
-        last = 2;
-        return 0;
-      }
-      return last = last == 0 ? 1 : 0;
+  // How often each buffer was used before a unit; tile i of it uses buffer i % NBUF.
+  struct Uses {
+    uint32_t n[C::NBUF];
+    __device__ __forceinline__ Uses() {
+#pragma unroll
+      for (int b = 0; b < C::NBUF; ++b) n[b] = 0;
+    }
+    __device__ __forceinline__ uint32_t at(int b, int i) const {
+      uint32_t v = n[0];
+#pragma unroll
+      for (int q = 1; q < C::NBUF; ++q) v = b == q ? n[q] : v;
+      return v + (uint32_t)i / C::NBUF;
+    }
+    __device__ __forceinline__ void next(int nt) {
+#pragma unroll
+      for (int b = 0; b < C::NBUF; ++b) n[b] += (nt - b + C::NBUF - 1) / C::NBUF;
     }
   };
 
@@ -216,11 +212,10 @@ struct RowsCta {
       if (!have) break;
       int ids = fetch_ids(U, 0, lane), ids_next = U.nt > PER ? fetch_ids(U, 32, lane) : 0, claimed = 0;
       if (U.nt == 0 && lane == 0) claimed = atomicAdd(prm.hdr + kHdrWork, 1);
-      const bool both = C::NP == 2 && U.nh > 128;
       int ids_v = ids, jk = 0, jv = 0;  // the next keys' and values' tiles
       for (int i = 0; i < 2 * U.nt && ok; ++i) {
         // (Whichever of the next keys and the next values is item i.)
-        const bool value = jk == U.nt || key_item(both, jk) != (uint32_t)i;
+        const bool value = jk == U.nt || key_item(jk) != (uint32_t)i;
         const int j = value ? jv++ : jk++;
         if (!value && j > 0 && j % PER == 0) {
           ids = ids_next;
@@ -264,19 +259,19 @@ struct RowsCta {
   // The whole warp goes through the loops, so that descriptors are made in uniform
   // registers; one lane issues (descriptors made by one diverged lane cost 100 cycles
   // a product, more than the product).
-  // Scores of ring slot `sl` against Q tile q, into score buffer b.
-  __device__ __forceinline__ void issue_scores(uint32_t tmem, int q, uint32_t sl, int b, uint32_t idesc) const {
+  // Scores of ring slot `sl` into buffer b.
+  __device__ __forceinline__ void issue_scores(uint32_t tmem, uint32_t sl, int b, uint32_t idesc) const {
     constexpr uint32_t STEP = C::kGroups ? 128u : C::BLK;    // from one instruction's tokens to the next one's
     constexpr uint32_t STRIDE = C::kGroups ? C::BLK : 128u;  // from eight tokens of an instruction to the next
     constexpr uint32_t LEAD = C::BS * 16u;                   // from a chunk of dims to the next
-    const uint32_t qa = desc_lo(sbase + q * C::QTILE, 2048), ka = desc_lo(sbase + C::OFF_RING + sl * C::SLOT, LEAD);
-    const uint32_t d = tmem + C::S_COL + b * C::TN;
+    const uint32_t ka = desc_lo(sbase + C::OFF_RING + sl * C::SLOT, LEAD);
+    const uint32_t d = tmem + b * C::TN, q = tmem + C::Q_COL;
 #pragma unroll
     for (int kk = 0; kk < C::D / 16; ++kk)
 #pragma unroll
       for (int i = 0; i < C::NI; ++i)
-        mma_ss(d + i * C::N, qa + kk * (4096 / 16), desc_hi(128, kSwizzleNone), ka + (kk * 2 * LEAD + i * STEP) / 16,
-               desc_hi(STRIDE, kSwizzleNone), idesc, kk > 0);
+        mma_ts(d + i * C::N, q + kk * 8, ka + (kk * 2 * LEAD + i * STEP) / 16, desc_hi(STRIDE, kSwizzleNone), idesc,
+               kk > 0);
   }
   // O[o] (+)= weights of buffer b times the values in slot `sl`, `ks` k-steps.
   __device__ __forceinline__ void issue_values(uint32_t tmem, int o, uint32_t sl, int b, int ks, uint32_t idesc,
@@ -285,7 +280,7 @@ struct RowsCta {
     constexpr uint32_t SW = C::BS == 8 ? kSwizzleNone : C::BS == 16 ? kSwizzle32 : C::BS == 32 ? kSwizzle64 : kSwizzle128;
     constexpr uint32_t HI = desc_hi(C::BS == 8 ? 128 : C::BS * 16, SW);
     const uint32_t va = desc_lo(sbase + C::OFF_RING + sl * C::SLOT, C::BS == 8 ? C::BLK : 16);
-    const uint32_t d = tmem + C::O_COL + o * C::O_STEP, p = tmem + C::P_COL + b * C::TN;
+    const uint32_t d = tmem + C::O_COL + o * C::O_STEP, p = tmem + b * C::TN;
 #pragma unroll
     for (int h = 0; h < (C::kBf16 ? 2 : 1); ++h) {
 #pragma unroll
@@ -303,112 +298,96 @@ struct RowsCta {
     const auto all = [&](uint32_t b, uint32_t ph, int site, int detail) {
       return __all_sync(0xffffffffu, wait(b, ph, site, detail)) != 0;
     };
-    uint32_t g = 0, k = 0;          // ring items and units before this unit
-    uint32_t n0 = 0, n1 = 0;        // weights taken from each buffer
-    uint32_t r0 = 0, r1 = 0;        // scores that were read from each buffer
-    QBuffers qb;
+    uint32_t g = 0, k = 0;  // ring items and units before this unit
+    Uses uses;
     bool ok = true;
     while (ok) {
       if (!all(C::UFULL + k % C::UQ, k / C::UQ, kRowsUnit, (int)k)) break;
       const RowsUnit* up = info + k % C::UQ;
       // (Shuffles tell the compiler that these are the same in every lane.)
       const int us = __shfl_sync(0xffffffffu, up->s, 0), nt = __shfl_sync(0xffffffffu, up->nt, 0);
-      const int nh = __shfl_sync(0xffffffffu, up->nh, 0), tokens = __shfl_sync(0xffffffffu, up->t1 - up->t0, 0);
+      const int tokens = __shfl_sync(0xffffffffu, up->t1 - up->t0, 0);
       if (lane == 0) mbar_arrive(bar(C::UEMPTY + k % C::UQ));
       if (us < 0) break;
-      const bool both = C::NP == 2 && nh > 128;  // a row tile for each pipeline
-      const int steps = both ? 2 * nt : nt, q0 = qb.next(both);
-      if (!all(C::QFULL, k, kRowsQ, (int)k)) break;
-      // (The last unit's joining used the score columns; and with this wait neither side
-      // is ever more than a unit ahead, so that a parity tells the phases apart.)
+      if (!all(C::QREADY, k, kRowsQ, (int)k)) break;
+      // (The last unit's joining used the buffers; and with this wait neither side is
+      // ever more than a unit ahead, so that a parity tells the phases apart.)
       if (!all(C::XFREE, k + 1, kRowsX, (int)k)) break;
       tc_fence_after();
-      // (Scores of step i + 2 go where those of step i were, once they are read.)
-      const auto scores = [&](int i) {
-        const int j = both ? i >> 1 : i;
-        const uint32_t it = g + key_item(both, j);
-        if (!both || !(i & 1)) {
-          if (!all(C::FULL + slot(it), phase(it), kRowsFull, (int)it)) return false;
-        }
+      // Scores of tile i, into buffer b; after the last ones Q may be replaced.
+      const auto scores = [&](int i, int b) {
+        const uint32_t it = g + key_item(i);
+        if (!all(C::FULL + slot(it), phase(it), kRowsFull, (int)it)) return false;
         if (elect_one()) {
-          issue_scores(tmem, both ? i & 1 : q0, slot(it), i & 1, id_s);
-          mma_commit(bar(C::SFULL + (i & 1)));
-          if (!both || (i & 1)) mma_commit(bar(C::EMPTY + slot(it)));
+          issue_scores(tmem, slot(it), b, id_s);
+          mma_commit(bar(C::SFULL + b));
+          mma_commit(bar(C::EMPTY + slot(it)));
+          if (i + 1 == nt) mma_commit(bar(C::QFREE));
         }
         __syncwarp();
         return true;
       };
-      for (int i = 0; i < 2 && i < steps && ok; ++i) ok = scores(i);
-      for (int i = 0; i < steps && ok; ++i) {
-        const int j = both ? i >> 1 : i, b = i & 1, o = C::NP == 2 ? b : 0;
-        const uint32_t it = g + value_item(both, j, nt);
-        if (i + 2 < steps) {
-          ok = all(C::SREAD + b, (b ? r1 : r0)++, kRowsRead, i);
-          tc_fence_after();
-          ok = ok && scores(i + 2);
-        }
-        if (ok) ok = all(C::FULL + slot(it), phase(it), kRowsFull, (int)it);
-        if (ok && i < 2) ok = all(C::OFREE, k + 1, kRowsOFree, (int)k);  // the last unit's O is read
-        if (ok) ok = all(C::PREADY + b, b ? n1 : n0, kRowsP, i);
-        if (!ok) break;
-        if (b) ++n1;
-        else ++n0;
-        tc_fence_after();
-        const int left = tokens - j * C::TN, ks = left >= C::TN ? C::TN / 16 : (left + 15) / 16;
-        if (elect_one()) {
-          issue_values(tmem, o, slot(it), b, ks, id_o, C::NP == 2 ? i >= 2 : i >= 1);
-          mma_commit(bar(C::PVDONE + b));
-          if (!both || (i & 1)) mma_commit(bar(C::EMPTY + slot(it)));
-        }
+      if (nt == 0) {
+        if (elect_one()) mma_commit(bar(C::QFREE));
         __syncwarp();
       }
+      for (int i = 0; i < C::NBUF && i < nt && ok; ++i) ok = scores(i, i);
+      for (int i = 0, b = 0; i < nt && ok; ++i, b = b + 1 < C::NBUF ? b + 1 : 0) {
+        const int o = C::NP == 2 ? i & 1 : 0;
+        const uint32_t it = g + value_item(i, nt);
+        ok = all(C::FULL + slot(it), phase(it), kRowsFull, (int)it);
+        if (ok && i < C::NP) ok = all(C::OFREE, k + 1, kRowsOFree, (int)k);  // the last unit's O is read
+        if (ok) ok = all(C::PREADY + b, uses.at(b, i), kRowsP, i);
+        if (!ok) break;
+        tc_fence_after();
+        const int left = tokens - i * C::TN, ks = left >= C::TN ? C::TN / 16 : (left + 15) / 16;
+        if (elect_one()) {
+          issue_values(tmem, o, slot(it), b, ks, id_o, i >= C::NP);
+          mma_commit(bar(C::PVDONE + b));
+          mma_commit(bar(C::EMPTY + slot(it)));
+        }
+        __syncwarp();
+        // (These scores go where the weights just used were, behind their product.)
+        if (i + C::NBUF < nt) ok = scores(i + C::NBUF, b);
+      }
       if (!ok) break;
-      // (Scores that nothing followed have been read, too.)
-      for (int i = max(0, steps - 2); i < steps && ok; ++i) ok = all(C::SREAD + (i & 1), (i & 1 ? r1 : r0)++, kRowsRead, i);
-      if (!ok) break;
-      if (elect_one()) mma_commit(bar(C::QFREE + (k & 1)));
-      __syncwarp();
+      uses.next(nt);
       g += 2 * nt;
       ++k;
     }
     // What has been issued completes before tensor memory is freed.
-    if (elect_one()) mma_commit(bar(C::DRAIN));
+    const uint32_t drain = sbase + C::OFF_FLAGS + 32;
+    if (elect_one()) mma_commit(drain);
     __syncwarp();
     const uint64_t t0 = global_timer_ns();
-    while (!mbar_try_wait(bar(C::DRAIN), 0) && global_timer_ns() - t0 < 100000000ull) {
+    while (!mbar_try_wait(drain, 0) && global_timer_ns() - t0 < 100000000ull) {
     }
     __syncwarp();
   }
 
   // ---------------------------------------------------------------- Q warps
-  // The unit's row tiles, [D/8][128 rows] 16-byte pieces; rows past the unit's (up to
-  // whole warps): zeros.  Four lanes a row: 64 bytes of it an instruction.
+  // The next unit's rows, as [D/8][128 rows] 16-byte pieces in shared memory; rows past
+  // the unit's (up to whole warps): zeros.  Four lanes a row: 64 bytes of it an
+  // instruction.
   __device__ __forceinline__ void bring_rows(int tid, int lane) {
     using T = typename C::T;
     const RowsUnit* info = reinterpret_cast<const RowsUnit*>(smem + C::OFF_INFO);
-    QBuffers qb;
     for (uint32_t k = 0;; ++k) {
       const bool okw = wait(C::UFULL + k % C::UQ, k / C::UQ, kRowsUnit, (int)k);
       if (!__all_sync(0xffffffffu, okw)) break;
       const RowsUnit U = info[k % C::UQ];
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(C::UEMPTY + k % C::UQ));
-      if (U.s < 0) break;
-      const bool both = C::NP == 2 && U.nh > 128;
-      const int before = qb.last;
-      const int q0 = qb.next(both);
-      // The unit before last is done with its tiles; the last one too, where this one
-      // takes a tile of its.
-      // (Units take turns at two barriers, so that neither is waited for two phases late.)
-      bool ok = k < 2 || wait(C::QFREE + (k & 1), (k >> 1) - 1, kRowsQFree, (int)k);
-      if (ok && k >= 1 && (both || before == 2 || before == q0))
-        ok = wait(C::QFREE + ((k - 1) & 1), (k - 1) >> 1, kRowsQFree, (int)k);
-      if (!__all_sync(0xffffffffu, ok)) break;
+      if (U.s < 0) {  // (the softmax looks for the next unit's Q before it knows that there is none)
+        mbar_arrive(bar(C::QSTAGED));
+        break;
+      }
+      if (!__all_sync(0xffffffffu, wait(C::QTAKEN, k + 1, kRowsQFree, (int)k))) break;
       const int rows = (U.nh + 31) / 32 * 32;
       for (int row = tid >> 2; row < rows; row += C::LOADERS / 4) {
         const bool in = row < U.nh;
         const T* q = static_cast<const T*>(prm.q) + (in ? out_row<kView>(prm, U.s, U.h0 + row) : 0) * C::D;
-        const uint32_t dst = sbase + (both ? row >> 7 : q0) * C::QTILE + (row & 127) * 16;
+        const uint32_t dst = sbase + row * 16;
 #pragma unroll
         for (int c0 = 0; c0 < C::D / 8; c0 += 4) {
           const int c = c0 + (tid & 3);
@@ -419,16 +398,7 @@ struct RowsCta {
         }
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
-      if (prm.scale_log2 < 0.f) {
-        // The products get -Q: the softmax works with a scale that is not negativ.
-        for (int row = tid >> 2; row < rows; row += C::LOADERS / 4)
-          for (int c = tid & 3; c < C::D / 8; c += 4) {
-            uint4* x = reinterpret_cast<uint4*>(smem + (both ? row >> 7 : q0) * C::QTILE + (row & 127) * 16 + c * 2048);
-            *x = make_uint4(x->x ^ 0x80008000u, x->y ^ 0x80008000u, x->z ^ 0x80008000u, x->w ^ 0x80008000u);
-          }
-      }
-      fence_proxy_async_smem();
-      mbar_arrive(bar(C::QFULL));
+      mbar_arrive(bar(C::QSTAGED));
     }
   }
 
@@ -536,6 +506,35 @@ struct RowsCta {
     }
   }
 
+  // The staged Q of unit k into tensor memory (the first warpgroup, a row a thread),
+  // once the products with the one before are complete.  A negative scale's sign goes
+  // with it: the softmax works with one that is not negative.
+  __device__ __forceinline__ bool take_rows(uint32_t tmem, uint32_t lanes, int tid, uint32_t k) const {
+    bool ok = wait(C::QSTAGED, k, kRowsQ, (int)k);
+    if (ok) ok = wait(C::QFREE, k + 1, kRowsQFree, (int)k);
+    if (!__all_sync(0xffffffffu, ok)) return false;
+    tc_fence_after();
+    const uint32_t flip = prm.scale_log2 < 0.f ? 0x80008000u : 0u;
+    constexpr int W = C::D / 2;  // columns
+#pragma unroll
+    for (int w0 = 0; w0 < W; w0 += 16) {
+      uint32_t w[16];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        if (w0 + 4 * c >= W) break;
+        const uint4 x = *reinterpret_cast<const uint4*>(smem + (w0 / 4 + c) * 2048 + tid * 16);
+        w[4 * c] = x.x ^ flip; w[4 * c + 1] = x.y ^ flip; w[4 * c + 2] = x.z ^ flip; w[4 * c + 3] = x.w ^ flip;
+      }
+      if (w0 + 16 <= W) tmem_st16(tmem + lanes + C::Q_COL + w0, w);
+      else tmem_st8(tmem + lanes + C::Q_COL + w0, w);
+    }
+    tmem_wait_st();
+    tc_fence_before();
+    mbar_arrive(bar(C::QTAKEN));
+    mbar_arrive(bar(C::QREADY));
+    return true;
+  }
+
   __device__ __forceinline__ void softmax(uint32_t tmem, int wg, int tid) {
     using T = typename C::T;
     constexpr int TN = C::TN, NB = C::NB, NG = C::NG, D = C::D;
@@ -543,10 +542,11 @@ struct RowsCta {
     volatile int* odd_unit = reinterpret_cast<volatile int*>(smem + C::OFF_FLAGS + 16);
     const int lane = tid & 31;
     const uint32_t lanes = (uint32_t)(tid & ~31) << 16;  // this warp's lanes of tensor memory
-    // (The sign of the scale went to Q.)
     const float sl2 = fmaxf(fabsf(prm.scale_log2), 1.17549435e-38f);
     const uint64_t pol_keep = l2_policy_evict_last();
-    uint32_t g = 0, k = 0, n0 = 0, n1 = 0;  // ring items and units; scores read from each buffer
+    uint32_t g = 0, k = 0;  // ring items and units before this unit
+    Uses uses;
+    if (wg == 0 && !take_rows(tmem, lanes, tid, 0)) return;
     // (The unit's description stays in its slot while it is worked on, and what a row
     // sees is worked out where a tile is partly seen and at the end: registers hold
     // the row's scores.)
@@ -556,8 +556,7 @@ struct RowsCta {
       const volatile RowsUnit& U = info[k % C::UQ];
       if (U.s < 0) break;
       const int nh = U.nh, nt = U.nt;
-      const bool both = C::NP == 2 && nh > 128;
-      const int row = both ? wg * 128 + tid : tid;  // the thread's row of the unit
+      const int row = tid;  // the thread's row of the unit
       const bool mine = row < nh;
       const int qi = mine ? (U.h0 - U.kv * prm.G + row) / prm.Gu : -1;  // its query token
       const auto view = [&]() { return qi >= 0 ? row_view_of(prm, U.s, U.L, qi) : RowView{0, 0, 0, nullptr}; };
@@ -571,17 +570,14 @@ struct RowsCta {
         full_lo = prm.window > 0 ? (prm.masks ? U.L - prm.window : first + i1 - prm.window + 1) : 0;
       }
       float mref = -INFINITY, l = 0.f;
-      const int steps = both ? 2 * nt : nt, t0 = U.t0, t1 = U.t1, sink_blocks = U.sink_blocks, skip = U.skip;
-      int done = 0;  // this warpgroup's steps of the unit
+      const int t0 = U.t0, t1 = U.t1, sink_blocks = U.sink_blocks, skip = U.skip;
       bool ok = true;
-      for (int i = C::NP == 2 ? wg : 0; i < steps && ok; i += C::NP, ++done) {
-        const int j = both ? i >> 1 : i, b = i & 1;
-        const uint32_t sc = tmem + lanes + C::S_COL + b * TN;
-        const int tile = t0 + j * TN, left = t1 - tile, vb0 = tile / C::BS;
-        ok = __all_sync(0xffffffffu, wait(C::SFULL + b, b ? n1 : n0, kRowsS, i));
+      for (int i = C::NP == 2 ? wg : 0; i < nt && ok; i += C::NP) {
+        const int b = i % C::NBUF;
+        const uint32_t sc = tmem + lanes + b * TN;
+        const int tile = t0 + i * TN, left = t1 - tile, vb0 = tile / C::BS;
+        ok = __all_sync(0xffffffffu, wait(C::SFULL + b, uses.at(b, i), kRowsS, i));
         if (!ok) break;
-        if (b) ++n1;
-        else ++n0;
         tc_fence_after();
         // Whether every row sees the whole tile.
         const int p0 = block_pos(sink_blocks, skip, vb0);
@@ -590,21 +586,14 @@ struct RowsCta {
         const bool partial = left < TN || jump || p1 >= full_hi || (p0 < full_lo && p1 >= prm.sinks);
         if (partial) {
           // (Values: before the weights of the tile are announced.)
-          const uint32_t it = g + value_item(both, j, nt);
+          const uint32_t it = g + value_item(i, nt);
           ok = __all_sync(0xffffffffu, wait(C::FULL + slot(it), phase(it), kRowsFull, (int)it));
           if (!ok) break;
           if (clear_values(slot(it), left, tid)) *odd_unit = (int)k + 1;
           fence_proxy_async_smem();
           __syncwarp();
         }
-        if (!warp_rows) {
-          // A warp without rows only keeps the counts; it waits as the others do, or its
-          // next arrival would stand for one that theirs lack.
-          mbar_arrive(bar(C::SREAD + b));
-          if ((b ? n1 : n0) > 1) {
-            ok = __all_sync(0xffffffffu, wait(C::PVDONE + b, (b ? n1 : n0) - 2, kRowsPv, i));
-            if (!ok) break;
-          }
+        if (!warp_rows) {  // a warp without rows only keeps the count
           mbar_arrive(bar(C::PREADY + b));
           continue;
         }
@@ -612,8 +601,6 @@ struct RowsCta {
 #pragma unroll
         for (int c = 0; c < TN; c += 32) tmem_ld32(sc + c, s + c);
         tmem_wait_ld();
-        tc_fence_before();
-        mbar_arrive(bar(C::SREAD + b));
         if (partial) {
           const RowView v = view();
 #pragma unroll
@@ -631,7 +618,7 @@ struct RowsCta {
 #pragma unroll
         for (int c = 0; c < TN; ++c) m4[c & 3] = fmaxf(m4[c & 3], s[c]);
         float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * sl2;
-        const bool first = C::NP == 2 ? done == 0 : i == 0;
+        const bool first = i < C::NP;
         if (mx > mref + 8.f || (mref == -INFINITY && mx > -INFINITY)) {
           const float alpha = exp2_approx(mref - mx);
           l *= alpha;
@@ -641,17 +628,13 @@ struct RowsCta {
         } else {
           mx = 1.f;
         }
-        // The products with this buffer's weights before are complete (each buffer's have
-        // a barrier, on which they are never two ahead).
-        if ((b ? n1 : n0) > 1) {
-          ok = __all_sync(0xffffffffu, wait(C::PVDONE + b, (b ? n1 : n0) - 2, kRowsPv, i));
-          if (!ok) break;
-          tc_fence_after();
-        }
         __syncwarp();
         if (!first && __any_sync(0xffffffffu, mx != 1.f)) {
-          // O by the rows' factors, once all products before are complete.
-          if (C::NP == 1) ok = __all_sync(0xffffffffu, wait(C::PVDONE + (b ^ 1), (b ? n0 : n1) - 1, kRowsPv, i));
+          // O by the rows' factors, once the last product into it is complete.  (Each
+          // buffer's products have a barrier: this tile's scores say that all but those of
+          // the NBUF - 1 tiles before are complete, so neither is two phases off.)
+          const int ip = i - C::NP, pb = ip % C::NBUF;
+          ok = __all_sync(0xffffffffu, wait(C::PVDONE + pb, uses.at(pb, ip), kRowsPv, i));
           if (!ok) break;
           tc_fence_after();
           const uint32_t oc = tmem + lanes + C::O_COL + (C::NP == 2 ? wg : 0) * C::O_STEP;
@@ -676,7 +659,6 @@ struct RowsCta {
         l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
         // Weights, in token order: word w holds tokens 2w, 2w + 1 of the tile.  bf16: the
         // weight cut to its first 8 bits, and what that leaves (exact in fp32) rounded.
-        const uint32_t pc = tmem + lanes + C::P_COL + b * TN;
 #pragma unroll
         for (int w0 = 0; w0 < TN / 2; w0 += 16) {
           uint32_t hi[16], lo[16];
@@ -691,32 +673,37 @@ struct RowsCta {
               hi[q] = F16Traits<T>::pack(s[e], s[e + 1]);
             }
           }
-          tmem_st16(pc + w0, hi);
-          if constexpr (C::kBf16) tmem_st16(pc + TN / 2 + w0, lo);
+          tmem_st16(sc + w0, hi);
+          if constexpr (C::kBf16) tmem_st16(sc + TN / 2 + w0, lo);
         }
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(bar(C::PREADY + b));
       }
       if (!ok) break;
-      // ---- the end of the unit: join the pipelines' states (one row a thread), write.
+      if (!ok) break;
+      // ---- the end of the unit: the next one's Q, then join the pipelines' states (one row
+      // a thread) and write.
+      if (wg == 0 && !take_rows(tmem, lanes, tid, k + 1)) break;
       const uint32_t ob = tmem + lanes + C::O_COL;
       const RowView v = view();
-      if (done > 0) {
-        // (Products are complete in their order: the last one's barrier is enough.)
-        const int pb = (steps - 1) & 1, lb = C::NP == 2 ? wg : pb;
-        ok = __all_sync(0xffffffffu, wait(C::PVDONE + lb, (lb ? n1 : n0) - 1, kRowsPv, -1));
+      // The last tile of each pipeline (-1: none), whose buffers are free when their
+      // products are complete.
+      const int last = C::NP == 1 ? nt - 1 : nt - 1 - ((nt - 1 - wg) & 1);
+      const int other = C::NP == 1 ? 0 : nt - 1 - ((nt - 1 - (1 - wg)) & 1);
+      if (last >= 0) {
+        ok = __all_sync(0xffffffffu, wait(C::PVDONE + last % C::NBUF, uses.at(last % C::NBUF, last), kRowsPv, -1));
         if (!ok) break;
         tc_fence_after();
       }
-      // (mref, l) of either warpgroup's thread of a row, by the score columns.
+      // (mref, l) of either warpgroup's thread of a row, by those buffers.
       if constexpr (C::NP == 2) {
-        tmem_st2(tmem + lanes + C::S_COL + wg * TN, mref, l);
+        tmem_st2(tmem + lanes + (last >= 0 ? last % C::NBUF : wg) * TN, mref, l);
         tmem_wait_st();
         tc_fence_before();
       }
       if (nt == 0) {  // (nothing of this unit came from the product warp)
-        ok = __all_sync(0xffffffffu, wait(C::QFREE + (k & 1), k >> 1, kRowsQFree, (int)k));
+        ok = __all_sync(0xffffffffu, wait(C::QFREE, k, kRowsQFree, (int)k));
         if (!ok) break;
       }
       mbar_arrive(bar(C::XBAR));
@@ -726,11 +713,11 @@ struct RowsCta {
       const bool odd = *odd_unit == (int)k + 1;
       float f0 = 1.f, f1 = 0.f;
       bool has0 = nt > 0, has1 = false;  // pipelines with something in O
-      int o0 = 0, d_lo = 0, d_hi = D;
-      if (C::NP == 2 && !both) {
+      int d_lo = 0, d_hi = D;
+      if constexpr (C::NP == 2) {
         // Both warpgroups have every row: each writes half of its dims.
         float m2, l2;
-        tmem_ld2(tmem + lanes + C::S_COL + (1 - wg) * TN, m2, l2);
+        tmem_ld2(tmem + lanes + (other >= 0 ? other % C::NBUF : 1 - wg) * TN, m2, l2);
         tmem_wait_ld();
         tc_fence_before();
         mbar_arrive(bar(C::XFREE));
@@ -746,7 +733,6 @@ struct RowsCta {
         d_hi = wg ? D : HALF;
       } else {
         mbar_arrive(bar(C::XFREE));
-        o0 = wg;
       }
       if (warp_rows) {
         const bool some = v.hi > 0 && l != 0.f;
@@ -772,7 +758,7 @@ struct RowsCta {
 #pragma unroll
           for (int h = 0; h < NCH; ++h) {
             if (c0 + h * 16 >= d_hi) break;
-            if (has0) tmem_ld16(ob + o0 * C::O_STEP + c0 + h * 16, a[h]);
+            if (has0) tmem_ld16(ob + c0 + h * 16, a[h]);
             if (has1) tmem_ld16(ob + C::O_STEP + c0 + h * 16, b[h]);
           }
           tmem_wait_ld();
@@ -829,6 +815,7 @@ struct RowsCta {
       mbar_arrive(bar(C::OFREE));
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(C::UEMPTY + k % C::UQ));
+      uses.next(nt);
       g += 2 * nt;
       ++k;
     }
@@ -840,7 +827,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) pa_rows_kernel(const __grid_con
   extern __shared__ __align__(1024) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   RowsCta<C> cta(prm, smem);
-  int* flags = reinterpret_cast<int*>(smem + C::OFF_FLAGS);  // abort, bad length, tensor memory, -, odd unit
+  int* flags = reinterpret_cast<int*>(smem + C::OFF_FLAGS);  // abort, bad length, tensor memory, -, odd unit; a barrier
   int* pref = reinterpret_cast<int*>(smem + C::OFF_PREF);
   uint16_t* perm = reinterpret_cast<uint16_t*>(smem + C::OFF_PERM);
   constexpr int WP = C::NP * 4, WM = WP + 1, WQ = WP + 2;  // producer, product and Q warps
@@ -853,19 +840,19 @@ __global__ void __launch_bounds__(C::THREADS, 1) pa_rows_kernel(const __grid_con
       mbar_init(cta.bar(C::UFULL + i), 1);
       mbar_init(cta.bar(C::UEMPTY + i), C::NP * 4 + 3);
     }
-    mbar_init(cta.bar(C::QFULL), C::LOADERS);
-    mbar_init(cta.bar(C::XFREE), C::NP * 128);
-    mbar_init(cta.bar(C::QFREE), 1);
-    mbar_init(cta.bar(C::QFREE + 1), 1);
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < C::NBUF; ++i) {
       mbar_init(cta.bar(C::SFULL + i), 1);
-      mbar_init(cta.bar(C::SREAD + i), 128);
       mbar_init(cta.bar(C::PREADY + i), 128);
       mbar_init(cta.bar(C::PVDONE + i), 1);
     }
+    mbar_init(cta.bar(C::QSTAGED), C::LOADERS);
+    mbar_init(cta.bar(C::QTAKEN), 128);
+    mbar_init(cta.bar(C::QREADY), 128);
+    mbar_init(cta.bar(C::QFREE), 1);
     mbar_init(cta.bar(C::OFREE), C::NP * 128);
     mbar_init(cta.bar(C::XBAR), C::NP * 128);
-    mbar_init(cta.bar(C::DRAIN), 1);
+    mbar_init(cta.bar(C::XFREE), C::NP * 128);
+    mbar_init(cta.sbase + C::OFF_FLAGS + 32, 1);
     flags[0] = flags[1] = flags[4] = 0;
     fence_mbarrier_init();
   }

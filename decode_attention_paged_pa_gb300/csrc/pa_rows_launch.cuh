@@ -23,7 +23,7 @@ static cudaError_t rows_go(const KParams& prm, int max_ctas, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     opted_in.fetch_or(bit, std::memory_order_acq_rel);
   }
-  static_assert(C::GT == rows_per_unit(C::D), "rows per unit");
+  static_assert(C::GT == kRowsPerUnit, "rows per unit");
   int grid = device_sm_count();
   if (max_ctas > 0 && max_ctas < grid) grid = max_ctas;
   cudaLaunchConfig_t cfg = {};

@@ -68,6 +68,12 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* v) {
       : "memory");
 }
 
+__device__ __forceinline__ void tmem_st8(uint32_t addr, const uint32_t* v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(addr), "r"(v[0]),
+               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
 // Shared-memory matrix descriptors.  Without a swizzle an operand consists of core
 // matrices of 8 rows x 16 bytes, 128 bytes each: `lead` bytes from one to the next
 // along K, `stride` bytes along the rows.  Swizzled K-major rows of 32, 64 or 128
@@ -86,17 +92,7 @@ __device__ __forceinline__ uint32_t f16_idesc(bool bf16, int n) {
   const uint32_t t = bf16 ? 1u : 0u;
   return 1u << 4 | t << 7 | t << 10 | (uint32_t)(n >> 3) << 17 | 8u << 24;
 }
-// D[128 x N] (+)= A . B, by one thread: A in shared memory, or (ts) in tensor memory.
-__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi,
-                                       uint32_t idesc, bool add) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
-      "mov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\t"
-      "setp.ne.u32 p, %6, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d),
-      "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"((uint32_t)add)
-      : "memory");
-}
+// D[128 x N] (+)= A . B, by one thread: A in tensor memory, B in shared memory.
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t b_hi, uint32_t idesc, bool add) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
