@@ -134,24 +134,13 @@ struct RowsCta {
   __device__ __forceinline__ uint32_t slot(uint32_t g) const { return g % C::NS; }
   __device__ __forceinline__ uint32_t phase(uint32_t g) const { return g / C::NS; }
 
-  // How often each buffer was used before a unit; tile i of it uses buffer i % NBUF.
-  struct Uses {
-    uint32_t n[C::NBUF];
-    __device__ __forceinline__ Uses() {
+  // Tile i of a unit uses buffer i % NBUF; bit b: the parity of the uses of buffer b so
+  // far, which is that of the phase of its barriers' next use.
+  static __device__ __forceinline__ uint32_t parity_after(uint32_t par, int nt) {  // a unit
 #pragma unroll
-      for (int b = 0; b < C::NBUF; ++b) n[b] = 0;
-    }
-    __device__ __forceinline__ uint32_t at(int b, int i) const {
-      uint32_t v = n[0];
-#pragma unroll
-      for (int q = 1; q < C::NBUF; ++q) v = b == q ? n[q] : v;
-      return v + (uint32_t)i / C::NBUF;
-    }
-    __device__ __forceinline__ void next(int nt) {
-#pragma unroll
-      for (int b = 0; b < C::NBUF; ++b) n[b] += (nt - b + C::NBUF - 1) / C::NBUF;
-    }
-  };
+    for (int b = 0; b < C::NBUF; ++b) par ^= (uint32_t)((nt - b + C::NBUF - 1) / C::NBUF & 1) << b;
+    return par;
+  }
 
   // Position of block vb of those that the sequence's rows can see.
   static __device__ __forceinline__ int block_pos(int sink_blocks, int skip, int vb) {
@@ -178,21 +167,42 @@ struct RowsCta {
   }
 
   // ---------------------------------------------------------------- producer warp
-  __device__ __forceinline__ int fetch_ids(const RowsUnit& U, int b0, int lane) const {
-    const int nb = (U.t1 - U.t0 + C::BS - 1) / C::BS;
-    if (b0 + lane >= nb) return 0;
-    int j = U.t0 / C::BS + b0 + lane;
-    j += j < U.sink_blocks ? 0 : U.skip;
-    return __ldg(prm.bt + (size_t)U.s * prm.MB + j);
+  // Item i of a unit of nt tiles (the inverse of the two above): true for values.
+  static __device__ __forceinline__ bool item_tile(int i, int nt, int* j) {
+    const int first = min(nt, C::NBUF), rest = nt - first, p = i - first;
+    const bool value = p >= 0 && (p >= 2 * rest || !(p & 1));
+    *j = p < 0 ? i : p >= 2 * rest ? p - rest : value ? p >> 1 : first + (p >> 1);
+    return value;
+  }
+  // A lane's block of a group of GI ring items: NB lanes an item.
+  struct Lane {
+    int j;        // its tile
+    bool value, in;  // of the values; there is such an item
+    int blocks;   // blocks of the tile
+    int id;       // its block, as the table has it
+  };
+  __device__ __forceinline__ Lane lane_item(const RowsUnit& U, int i, int b) const {
+    Lane x{0, false, i < 2 * U.nt, 0, 0};
+    if (x.in) {
+      x.value = item_tile(i, U.nt, &x.j);
+      x.blocks = min(C::NB, (U.t1 - U.t0 - x.j * C::TN + C::BS - 1) / C::BS);
+      int j = U.t0 / C::BS + x.j * C::NB + b;
+      j += j < U.sink_blocks ? 0 : U.skip;
+      if (b < x.blocks) x.id = __ldg(prm.bt + (size_t)U.s * prm.MB + j);
+    }
+    return x;
   }
 
   __device__ __forceinline__ void producer(const int* pref, const uint16_t* perm, int lane) {
-    constexpr int NB = C::NB, PER = 32 / NB;  // tiles whose ids a warp holds
+    // Items issued together: as many as a warp has lanes for, up to half of the ring.
+    // (One at a time took the producer 600 cycles an item, as long as its copy.)
+    constexpr int NB = C::NB, GI = 32 / NB < C::NS / 2 ? 32 / NB : C::NS / 2;
     RowsUnit* info = reinterpret_cast<RowsUnit*>(smem + C::OFF_INFO);
     const uint64_t pol = l2_policy_evict_first();
     const int total = pref[prm.S] * prm.n_hg;
+    const int li = lane / NB, lb = lane - li * NB;  // the lane's item of a group, and block of that
     fence_proxy_async_smem();  // the prologue's temporaries lay in the ring
-    uint32_t g = 0, k = 0;
+    uint32_t g = 0, k = 0, hi = 0;  // ring items and units before this unit; items issued
     int u = blockIdx.x;
     bool ok = true;
     while (ok) {
@@ -200,6 +210,7 @@ struct RowsCta {
       RowsUnit U{};
       if (have) U = cut(plan_unit<C, kView>(prm, pref, perm, u));
       else U.s = -1;
+      Lane next = lane_item(U, li, lb);  // (no items without a unit)
       // Publish it.
       const uint32_t us = k % C::UQ;
       ok = __shfl_sync(0xffffffffu, lane == 0 ? (int)wait(C::UEMPTY + us, k / C::UQ + 1, kRowsUnitSlot, (int)k) : 0, 0);
@@ -210,48 +221,71 @@ struct RowsCta {
       }
       ++k;
       if (!have) break;
-      int ids = fetch_ids(U, 0, lane), ids_next = U.nt > PER ? fetch_ids(U, 32, lane) : 0, claimed = 0;
+      int claimed = 0;
       if (U.nt == 0 && lane == 0) claimed = atomicAdd(prm.hdr + kHdrWork, 1);
-      int ids_v = ids, jk = 0, jv = 0;  // the next keys' and values' tiles
-      for (int i = 0; i < 2 * U.nt && ok; ++i) {
-        // (Whichever of the next keys and the next values is item i.)
-        const bool value = jk == U.nt || key_item(jk) != (uint32_t)i;
-        const int j = value ? jv++ : jk++;
-        if (!value && j > 0 && j % PER == 0) {
-          ids = ids_next;
-          if (j + PER < U.nt) ids_next = fetch_ids(U, (j + PER) * NB, lane);
+      for (int i0 = 0; i0 < 2 * U.nt && ok; i0 += GI) {
+        const int cnt = min(GI, 2 * U.nt - i0);
+        Lane x = next;
+        x.in = x.in && li < GI;
+        // (The next unit is taken while this one's last items are on their way.)
+        if (i0 + cnt == 2 * U.nt && lane == 0) claimed = atomicAdd(prm.hdr + kHdrWork, 1);
+        next = lane_item(U, i0 + GI + li, lb);
+        const uint32_t gi = g + i0 + li, sl = slot(gi), ph = phase(gi), fb = bar(C::FULL + sl);
+        const size_t row = (size_t)check_block_id(prm, x.id) * prm.KH + U.kv;
+        const uint32_t dst = sbase + C::OFF_RING + sl * C::SLOT + lb * C::BLK;
+        bool done = !x.in;
+        uint64_t t_start = 0;
+        while (true) {
+          if (!done && mbar_test_wait(bar(C::EMPTY + sl), (ph & 1u) ^ 1u)) {
+            if (lb == 0) mbar_arrive_expect_tx(fb, (uint32_t)x.blocks * C::BLK);
+            if (lb < x.blocks) {
+              if (!x.value || !C::kTma)
+                bulk_copy_g2s(dst, static_cast<const uint8_t*>(x.value ? prm.vc : prm.kc) + row * C::BLK, C::BLK, fb, pol);
+              else  // (x = 0: the 16-byte alignment rule holds)
+                tma_load_3d(dst, &prm.tmv, 0, 0, (int)row, fb, pol);
+            }
+            done = true;
+          }
+          if (__all_sync(0xffffffffu, done)) break;
+          int stop = 0;
+          if (lane == 0) {
+            const uint64_t now = global_timer_ns();
+            if (t_start == 0) t_start = now;
+            if (*abort_flag) {
+              stop = 1;
+            } else if ((long long)(now - t_start) > prm.timeout_ns) {
+              record_timeout(abort_flag, err, kRowsRing, (int)g);
+              stop = 1;
+            } else {
+              __nanosleep(32);
+            }
+          }
+          if (__shfl_sync(0xffffffffu, stop, 0)) {
+            // Aborted: this group's copies land before the warp leaves.
+            ok = false;
+            if (done && x.in) {
+              const uint64_t t0 = global_timer_ns();
+              while (!mbar_try_wait(fb, ph & 1u) && global_timer_ns() - t0 < 100000000ull) {
+              }
+            }
+            __syncwarp();
+            break;
+          }
         }
-        if (value && j % PER == 0) ids_v = ids;  // (PER is 4 or more: the keys are in the same 32 blocks)
-        // (The next unit is taken while this one's last tile is on its way.)
-        if (!value && j + 1 == U.nt && lane == 0) claimed = atomicAdd(prm.hdr + kHdrWork, 1);
-        const int nb = min(NB, (U.t1 - U.t0 - j * C::TN + C::BS - 1) / C::BS);
-        const int id = check_block_id(
-            prm, __shfl_sync(0xffffffffu, value ? ids_v : ids, (j % PER) * NB + (lane < nb ? lane : 0)));
-        const uint32_t sl = slot(g), fb = bar(C::FULL + sl), dst = sbase + C::OFF_RING + sl * C::SLOT;
-        ok = __shfl_sync(0xffffffffu, lane == 0 ? (int)wait(C::EMPTY + sl, phase(g) + 1, kRowsRing, (int)g) : 0, 0);
-        if (!ok) break;
-        if (lane == 0) mbar_arrive_expect_tx(fb, (uint32_t)nb * C::BLK);
-        __syncwarp();
-        if (lane < nb) {
-          const size_t row = (size_t)id * prm.KH + U.kv;
-          if (!value || !C::kTma)
-            bulk_copy_g2s(dst + lane * C::BLK, static_cast<const uint8_t*>(value ? prm.vc : prm.kc) + row * C::BLK,
-                          C::BLK, fb, pol);
-          else  // (x = 0: the 16-byte alignment rule holds)
-            tma_load_3d(dst + lane * C::BLK, &prm.tmv, 0, 0, (int)row, fb, pol);
-        }
-        ++g;
+        if (ok) hi = gi - li + cnt;
       }
+      if (ok) g += 2 * U.nt;
       u = __shfl_sync(0xffffffffu, claimed, 0) + (int)gridDim.x;
     }
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    // Copies in flight land before the CTA ends, whatever the others did.
-    if (lane == 0)
-      for (uint32_t i = g > (uint32_t)C::NS ? g - C::NS : 0u; i < g; ++i) {
-        const uint64_t t0 = global_timer_ns();
-        while (!mbar_try_wait(bar(C::FULL + slot(i)), phase(i) & 1u) && global_timer_ns() - t0 < 100000000ull) {
-        }
+    // Copies in flight land before the CTA ends, whatever the others did: the last one
+    // of each slot.
+    if (lane < C::NS && hi > (uint32_t)lane) {
+      const uint32_t i = hi - 1 - (hi - 1 - lane) % C::NS;
+      const uint64_t t0 = global_timer_ns();
+      while (!mbar_try_wait(bar(C::FULL + lane), phase(i) & 1u) && global_timer_ns() - t0 < 100000000ull) {
       }
+    }
     __syncwarp();
   }
 
@@ -274,6 +308,7 @@ struct RowsCta {
                kk > 0);
   }
   // O[o] (+)= weights of buffer b times the values in slot `sl`, `ks` k-steps.
+  template <bool WHOLE>
   __device__ __forceinline__ void issue_values(uint32_t tmem, int o, uint32_t sl, int b, int ks, uint32_t idesc,
                                                bool add) const {
     constexpr int KB = C::BS == 8 ? 1 : C::BS / 16;  // k-steps of a block (of two blocks of eight tokens)
@@ -285,7 +320,7 @@ struct RowsCta {
     for (int h = 0; h < (C::kBf16 ? 2 : 1); ++h) {
 #pragma unroll
       for (int k = 0; k < C::TN / 16; ++k) {
-        if (k >= ks) break;
+        if (!WHOLE && k >= ks) break;
         constexpr uint32_t STEP = C::BS == 8 ? 2 * C::BLK : C::BLK;
         mma_ts(d, p + h * (C::TN / 2) + k * 8, va + ((k / KB) * STEP + (k % KB) * 32) / 16, HI, idesc,
                add || h > 0 || k > 0);
@@ -299,7 +334,7 @@ struct RowsCta {
       return __all_sync(0xffffffffu, wait(b, ph, site, detail)) != 0;
     };
     uint32_t g = 0, k = 0;  // ring items and units before this unit
-    Uses uses;
+    uint32_t par = 0;
     bool ok = true;
     while (ok) {
       if (!all(C::UFULL + k % C::UQ, k / C::UQ, kRowsUnit, (int)k)) break;
@@ -337,12 +372,14 @@ struct RowsCta {
         const uint32_t it = g + value_item(i, nt);
         ok = all(C::FULL + slot(it), phase(it), kRowsFull, (int)it);
         if (ok && i < C::NP) ok = all(C::OFREE, k + 1, kRowsOFree, (int)k);  // the last unit's O is read
-        if (ok) ok = all(C::PREADY + b, uses.at(b, i), kRowsP, i);
+        if (ok) ok = all(C::PREADY + b, par >> b, kRowsP, i);
         if (!ok) break;
+        par ^= 1u << b;
         tc_fence_after();
         const int left = tokens - i * C::TN, ks = left >= C::TN ? C::TN / 16 : (left + 15) / 16;
         if (elect_one()) {
-          issue_values(tmem, o, slot(it), b, ks, id_o, i >= C::NP);
+          if (ks == C::TN / 16) issue_values<true>(tmem, o, slot(it), b, ks, id_o, i >= C::NP);
+          else issue_values<false>(tmem, o, slot(it), b, ks, id_o, i >= C::NP);
           mma_commit(bar(C::PVDONE + b));
           mma_commit(bar(C::EMPTY + slot(it)));
         }
@@ -351,7 +388,6 @@ struct RowsCta {
         if (i + C::NBUF < nt) ok = scores(i + C::NBUF, b);
       }
       if (!ok) break;
-      uses.next(nt);
       g += 2 * nt;
       ++k;
     }
@@ -545,7 +581,7 @@ struct RowsCta {
     const float sl2 = fmaxf(fabsf(prm.scale_log2), 1.17549435e-38f);
     const uint64_t pol_keep = l2_policy_evict_last();
     uint32_t g = 0, k = 0;  // ring items and units before this unit
-    Uses uses;
+    uint32_t par = 0;       // of the buffers before the unit
     if (wg == 0 && !take_rows(tmem, lanes, tid, 0)) return;
     // (The unit's description stays in its slot while it is worked on, and what a row
     // sees is worked out where a tile is partly seen and at the end: registers hold
@@ -574,9 +610,10 @@ struct RowsCta {
       bool ok = true;
       for (int i = C::NP == 2 ? wg : 0; i < nt && ok; i += C::NP) {
         const int b = i % C::NBUF;
+        const uint32_t use = (par >> b) + i / C::NBUF;  // (its low bit counts)
         const uint32_t sc = tmem + lanes + b * TN;
         const int tile = t0 + i * TN, left = t1 - tile, vb0 = tile / C::BS;
-        ok = __all_sync(0xffffffffu, wait(C::SFULL + b, uses.at(b, i), kRowsS, i));
+        ok = __all_sync(0xffffffffu, wait(C::SFULL + b, use, kRowsS, i));
         if (!ok) break;
         tc_fence_after();
         // Whether every row sees the whole tile.
@@ -634,7 +671,7 @@ struct RowsCta {
           // buffer's products have a barrier: this tile's scores say that all but those of
           // the NBUF - 1 tiles before are complete, so neither is two phases off.)
           const int ip = i - C::NP, pb = ip % C::NBUF;
-          ok = __all_sync(0xffffffffu, wait(C::PVDONE + pb, uses.at(pb, ip), kRowsPv, i));
+          ok = __all_sync(0xffffffffu, wait(C::PVDONE + pb, (par >> pb) + ip / C::NBUF, kRowsPv, i));
           if (!ok) break;
           tc_fence_after();
           const uint32_t oc = tmem + lanes + C::O_COL + (C::NP == 2 ? wg : 0) * C::O_STEP;
@@ -692,7 +729,7 @@ struct RowsCta {
       const int last = C::NP == 1 ? nt - 1 : nt - 1 - ((nt - 1 - wg) & 1);
       const int other = C::NP == 1 ? 0 : nt - 1 - ((nt - 1 - (1 - wg)) & 1);
       if (last >= 0) {
-        ok = __all_sync(0xffffffffu, wait(C::PVDONE + last % C::NBUF, uses.at(last % C::NBUF, last), kRowsPv, -1));
+        ok = __all_sync(0xffffffffu, wait(C::PVDONE + last % C::NBUF, (par >> last % C::NBUF) + last / C::NBUF, kRowsPv, -1));
         if (!ok) break;
         tc_fence_after();
       }
@@ -815,7 +852,7 @@ struct RowsCta {
       mbar_arrive(bar(C::OFREE));
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(C::UEMPTY + k % C::UQ));
-      uses.next(nt);
+      par = parity_after(par, nt);
       g += 2 * nt;
       ++k;
     }
