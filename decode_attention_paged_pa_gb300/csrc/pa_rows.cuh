@@ -414,11 +414,11 @@ struct RowsCta {
       const RowsUnit U = info[k % C::UQ];
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(C::UEMPTY + k % C::UQ));
+      if (!__all_sync(0xffffffffu, wait(C::QTAKEN, k + 1, kRowsQFree, (int)k))) break;
       if (U.s < 0) {  // (the softmax looks for the next unit's Q before it knows that there is none)
         mbar_arrive(bar(C::QSTAGED));
         break;
       }
-      if (!__all_sync(0xffffffffu, wait(C::QTAKEN, k + 1, kRowsQFree, (int)k))) break;
       const int rows = (U.nh + 31) / 32 * 32;
       for (int row = tid >> 2; row < rows; row += C::LOADERS / 4) {
         const bool in = row < U.nh;
@@ -550,6 +550,7 @@ struct RowsCta {
     if (ok) ok = wait(C::QFREE, k + 1, kRowsQFree, (int)k);
     if (!__all_sync(0xffffffffu, ok)) return false;
     tc_fence_after();
+    __syncwarp();
     const uint32_t flip = prm.scale_log2 < 0.f ? 0x80008000u : 0u;
     constexpr int W = C::D / 2;  // columns
 #pragma unroll
@@ -635,9 +636,8 @@ struct RowsCta {
           continue;
         }
         float s[TN];
-#pragma unroll
-        for (int c = 0; c < TN; c += 32) tmem_ld32(sc + c, s + c);
-        tmem_wait_ld();
+        __syncwarp();
+        tmem_get64(sc, sc + 32, s);
         if (partial) {
           const RowView v = view();
 #pragma unroll
@@ -678,8 +678,7 @@ struct RowsCta {
 #pragma unroll 1
           for (int c = 0; c < D; c += 16) {
             float o[16];
-            tmem_ld16(oc + c, o);
-            tmem_wait_ld();
+            tmem_get16(oc + c, o);
             uint32_t w[16];
 #pragma unroll
             for (int q = 0; q < 16; ++q) w[q] = __float_as_uint(o[q] * mx);
@@ -718,7 +717,6 @@ struct RowsCta {
         mbar_arrive(bar(C::PREADY + b));
       }
       if (!ok) break;
-      if (!ok) break;
       // ---- the end of the unit: the next one's Q, then join the pipelines' states (one row
       // a thread) and write.
       if (wg == 0 && !take_rows(tmem, lanes, tid, k + 1)) break;
@@ -735,6 +733,7 @@ struct RowsCta {
       }
       // (mref, l) of either warpgroup's thread of a row, by those buffers.
       if constexpr (C::NP == 2) {
+        __syncwarp();
         tmem_st2(tmem + lanes + (last >= 0 ? last % C::NBUF : wg) * TN, mref, l);
         tmem_wait_st();
         tc_fence_before();
@@ -753,9 +752,9 @@ struct RowsCta {
       int d_lo = 0, d_hi = D;
       if constexpr (C::NP == 2) {
         // Both warpgroups have every row: each writes half of its dims.
-        float m2, l2;
-        tmem_ld2(tmem + lanes + (other >= 0 ? other % C::NBUF : 1 - wg) * TN, m2, l2);
-        tmem_wait_ld();
+        float ml[2];
+        tmem_get2(tmem + lanes + (other >= 0 ? other % C::NBUF : 1 - wg) * TN, ml);
+        const float m2 = ml[0], l2 = ml[1];
         tc_fence_before();
         mbar_arrive(bar(C::XFREE));
         const float ma = wg ? m2 : mref, la = wg ? l2 : l, mb = wg ? mref : m2, lb = wg ? l : l2;
@@ -788,44 +787,35 @@ struct RowsCta {
                   : single  ? static_cast<uint8_t*>(prm.out) + ((size_t)ri * D + (lane & 3) * 4) * sizeof(T)
                             : reinterpret_cast<uint8_t*>(prm.ws_o + ((sh0 + r) * prm.Pmax + U.p) * D + (lane & 3) * 4);
         }
-        constexpr int NCH = 2;  // pieces of 16 dims at a time
+        // (Of a pipeline without a tile, O holds anything: it is read, and not used.)
 #pragma unroll 1
-        for (int c0 = d_lo; c0 < d_hi; c0 += NCH * 16) {
-          float a[NCH][16], b[NCH][16];
+        for (int c0 = d_lo; c0 < d_hi; c0 += 16) {
+          float o[16];
+          __syncwarp();  // (rows that are not the unit's have left lanes behind)
+          if constexpr (C::NP == 2) {
+            float ab[32];
+            tmem_get32(ob + c0, ob + C::O_STEP + c0, ab);
 #pragma unroll
-          for (int h = 0; h < NCH; ++h) {
-            if (c0 + h * 16 >= d_hi) break;
-            if (has0) tmem_ld16(ob + c0 + h * 16, a[h]);
-            if (has1) tmem_ld16(ob + C::O_STEP + c0 + h * 16, b[h]);
+            for (int q = 0; q < 16; ++q) o[q] = has1 ? fmaf(ab[16 + q], f1, ab[q] * f0) : ab[q] * f0;
+          } else {
+            tmem_get16(ob + c0, o);
+#pragma unroll
+            for (int q = 0; q < 16; ++q) o[q] *= f0;
           }
-          tmem_wait_ld();
+          if (!some || !has0) {
 #pragma unroll
-          for (int h = 0; h < NCH; ++h) {
-            if (c0 + h * 16 >= d_hi) break;
-            float (&o)[16] = a[h];
-            if (has1) {
+            for (int q = 0; q < 16; ++q) o[q] = 0.f;
+          }
+          // Four lanes exchange their rows' pieces of four dims: then lane q of the four has
+          // piece q of each of their rows, and they store 16 dims of one row at a time (a
+          // lane a row touched 32 lines with every store).
+          transpose4(o, lane);
 #pragma unroll
-              for (int q = 0; q < 16; ++q) o[q] = fmaf(b[h][q], f1, o[q] * f0);
-            } else {
-#pragma unroll
-              for (int q = 0; q < 16; ++q) o[q] *= f0;
-            }
-            if (!some || !has0) {
-#pragma unroll
-              for (int q = 0; q < 16; ++q) o[q] = 0.f;
-            }
-            // Four lanes exchange their rows' pieces of four dims: then lane q of the four has
-            // piece q of each of their rows, and they store 16 dims of one row at a time (a
-            // lane a row touched 32 lines with every store).
-            __syncwarp();
-            transpose4(o, lane);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float4 x = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-              if (!to[i]) continue;
-              if (single) store4<T>(reinterpret_cast<T*>(to[i]) + c0 + 16 * h, x);
-              else st_f4_policy(reinterpret_cast<float4*>(to[i]) + (c0 + 16 * h) / 4, x, pol_keep);
-            }
+          for (int i = 0; i < 4; ++i) {
+            const float4 x = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+            if (!to[i]) continue;
+            if (single) store4<T>(reinterpret_cast<T*>(to[i]) + c0, x);
+            else st_f4_policy(reinterpret_cast<float4*>(to[i]) + c0 / 4, x, pol_keep);
           }
         }
         if (odd) {
