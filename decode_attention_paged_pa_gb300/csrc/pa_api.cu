@@ -296,11 +296,11 @@ int decode_impl(void* out, float* lse, const void* query, const void* key_cache,
   // Over a 4-bit cache, 16 rows a unit where a kv head has more than 8: its
   // codes are unpacked once for both halves.
   const int nt = kv4 && G > kMmaGroup && D <= 128 ? 2 : 1;
-  const int gt = view && variant == PA_VARIANT_MMA && !kv_fp8 && G > kMmaGroup ? kRowsPerUnit
+  const int gt = view && variant == PA_VARIANT_MMA && G > kMmaGroup ? kRowsPerUnit
                  : kv4 ? nt * kMmaGroup : (variant == PA_VARIANT_MMA) ? (wide ? kMmaGroupWide : kMmaGroup) : kSimtGroup;
   // View rows: with more than eight a kv head, 128 of them a unit on the
-  // fifth-generation tensor cores (pa_rows.cuh), over 16-bit caches.
-  const bool many = view && variant == PA_VARIANT_MMA && !kv_fp8 && G > kMmaGroup;
+  // fifth-generation tensor cores (pa_rows.cuh).
+  const bool many = view && variant == PA_VARIANT_MMA && G > kMmaGroup;
   // Four query rows per kv head (query heads, or multi-query row heads): a
   // unit's 8 columns take two kv heads (one block copy each for keys and
   // values covers both), head sizes up to 128 and blocks of 8, 16 or 32 tokens.
@@ -395,7 +395,9 @@ int decode_impl(void* out, float* lse, const void* query, const void* key_cache,
       prm.masks = view->tree ? reinterpret_cast<const uint32_t*>(view->masks) + (size_t)s0 * q_len * prm.words : nullptr;
     }
     cudaError_t e;
-    if (many)
+    if (many && kv_fp8)
+      e = dtype == PA_DTYPE_FP16 ? launch_rows8_f16(prm, D, BS, max_ctas, st) : launch_rows8_bf16(prm, D, BS, max_ctas, st);
+    else if (many)
       e = dtype == PA_DTYPE_FP16 ? launch_rows_f16(prm, D, BS, max_ctas, st) : launch_rows_bf16(prm, D, BS, max_ctas, st);
     else if (view)
       e = launch_views(prm, dtype, kv_fp8, pairs, D, BS, max_ctas, st);

@@ -87,11 +87,15 @@ cudaError_t launch_view8_g_f16(const KParams& prm, int D, int BS, int max_ctas, 
 cudaError_t launch_view8_g_bf16(const KParams& prm, int D, int BS, int max_ctas, cudaStream_t st);
 cudaError_t launch_view_f32(const KParams& prm, int D, int BS, int max_ctas, cudaStream_t st);
 cudaError_t launch_view_x_f32(const KParams& prm, int D, int BS, int max_ctas, cudaStream_t st);
-// ... and with many rows a kv head, over 16-bit caches (_x: head sizes from 112).
+// ... and with many rows a kv head (rows8: over E4M3 caches; _x: head sizes from 112).
 cudaError_t launch_rows_f16(const KParams& prm, int D, int BS, int max_ctas, cudaStream_t st);
 cudaError_t launch_rows_bf16(const KParams& prm, int D, int BS, int max_ctas, cudaStream_t st);
 cudaError_t launch_rows_x_f16(const KParams& prm, int D, int BS, int max_ctas, cudaStream_t st);
 cudaError_t launch_rows_x_bf16(const KParams& prm, int D, int BS, int max_ctas, cudaStream_t st);
+cudaError_t launch_rows8_f16(const KParams& prm, int D, int BS, int max_ctas, cudaStream_t st);
+cudaError_t launch_rows8_bf16(const KParams& prm, int D, int BS, int max_ctas, cudaStream_t st);
+cudaError_t launch_rows8_x_f16(const KParams& prm, int D, int BS, int max_ctas, cudaStream_t st);
+cudaError_t launch_rows8_x_bf16(const KParams& prm, int D, int BS, int max_ctas, cudaStream_t st);
 // Sequences of a launch, and rows of a unit.
 constexpr int kRowsSeqsPerLaunch = 256;
 constexpr int kRowsPerUnit = 128;

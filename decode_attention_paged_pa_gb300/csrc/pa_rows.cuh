@@ -41,6 +41,8 @@
 
 #include <type_traits>
 
+#include <cuda_fp8.h>
+
 #include "pa_kernel.cuh"
 #include "pa_tc.cuh"
 
@@ -53,46 +55,58 @@ struct RowsUnit {
   int s, p, kv, t0, t1, nt, np, nh, h0, L, sink_blocks, skip;
 };
 
-template <typename T_, int D_, int BS_>
+template <typename T_, int D_, int BS_, bool FP8_ = false>
 struct RowsConfig {
   using T = T_;
+  static constexpr bool kFp8 = FP8_;
+  using MT = typename std::conditional<FP8_, __half, T_>::type;  // of the products' operands
   static constexpr int D = D_, BS = BS_;
   static constexpr int NP = D_ <= 128 ? 2 : 1;      // pipelines (warpgroups)
   static constexpr int NBUF = D_ <= 128 ? 3 : 2;    // buffers of scores and weights
   static constexpr int TN = 64;                     // tokens per tile
   static constexpr int GT = 128, KVU = 1;           // rows per unit; (plan_unit) kv heads per unit
   static constexpr int NB = TN / BS, NG = BS / 8;   // blocks of a tile, groups of eight tokens of a block
-  static constexpr bool kTma = BS_ >= 16;
-  static constexpr bool kBf16 = std::is_same<T_, __nv_bfloat16>::value;
-  static constexpr uint32_t BLK = (uint32_t)D_ * BS_ * 2, SLOT = (uint32_t)TN * D_ * 2, QTILE = 128u * D_ * 2;
-  static constexpr int THREADS = NP * 128 + 128, UQ = 2;
+  static constexpr int MS = FP8_ ? TN : BS_;        // tokens of a block as the products read it
+  static constexpr bool kTma = BS_ >= 16 && !FP8_;
+  static constexpr bool kBf16 = std::is_same<MT, __nv_bfloat16>::value;
+  // An 8-bit cache's query rows of bf16 go to fp16 by a power of two of their own.
+  static constexpr bool kQScale = FP8_ && std::is_same<T_, __nv_bfloat16>::value;
+  static constexpr uint32_t BLK = (uint32_t)D_ * BS_ * (FP8_ ? 1 : 2);  // a block of the cache
+  static constexpr uint32_t SLOT = (uint32_t)TN * D_ * 2, QTILE = 128u * D_ * 2;
+  // 8-bit caches: warps that widen the codes, and the ring of tiles of codes.
+  static constexpr int CW = !FP8_ ? 0 : D_ <= 128 ? 4 : 2, NR = !FP8_ ? 0 : D_ <= 128 ? 8 : 2;
+  static constexpr uint32_t RSLOT = FP8_ ? (uint32_t)TN * D_ : 0;
+  static constexpr int LOADERS = FP8_ ? 32 : 64;  // threads that bring Q
+  static constexpr int THREADS = NP * 128 + 64 + LOADERS + CW * 32, UQ = 2;
   // A tile's scores take NI instructions a k-step of N columns each: one a block, or
   // (kGroups) one for each group of eight tokens, of every block, whichever are fewer.
-  static constexpr bool kGroups = NG < NB;
-  static constexpr int NI = kGroups ? NG : NB, N = TN / NI;
-  static constexpr int LOADERS = 64;  // threads that bring Q
+  static constexpr bool kGroups = !FP8_ && NG < NB;
+  static constexpr int NI = kGroups ? NG : TN / MS, N = TN / NI;
   // Tensor memory columns: the buffers (scores, then weights: bf16 two words of 16 bits
   // a token), Q (two dims a column), O of either pipeline.
   static constexpr uint32_t Q_COL = NBUF * TN, O_COL = 256, O_STEP = 128;
   static_assert(Q_COL + D_ / 2 <= O_COL && O_COL + (NP == 2 ? 256 : D_) <= 512, "tensor memory");
   // Shared memory: the next unit's Q, the ring, then barriers, units, flags, order.
   static constexpr uint32_t QBYTES = QTILE;
-  static constexpr uint32_t bars(int ns) { return 2 * ns + 2 * UQ + 3 * NBUF + 7; }
+  static constexpr uint32_t bars(int ns) { return 2 * ns + 2 * NR + 2 * UQ + 3 * NBUF + 7; }
+  static constexpr uint32_t QSCALE = kQScale ? 2 * 128 * 4 : 0;
   static constexpr uint32_t small(int ns) {
-    return al16(bars(ns) * 8) + al16(UQ * sizeof(RowsUnit)) + 64 + al16((kRowsMaxUnitSeqs + 1) * 4) +
+    return al16(bars(ns) * 8) + al16(UQ * sizeof(RowsUnit)) + 64 + QSCALE + al16((kRowsMaxUnitSeqs + 1) * 4) +
            al16(kRowsMaxUnitSeqs * 2);
   }
-  static constexpr int kFit = (int)((kRowsSmem - small(16) - QBYTES) / SLOT);
+  static constexpr int kFit = (int)((kRowsSmem - small(D_ > 128 ? 8 : 16) - QBYTES - NR * RSLOT) / SLOT);
   static constexpr int NS = kFit < 16 ? kFit : 16;
+  static_assert(!FP8_ || (NR % CW == 0 && NS >= CW), "a warp's waits for a slot are a phase apart at most");
   static_assert(NS >= 2 * NBUF, "the ring holds the keys that are ahead and two tiles' values");
   // The score column of token t of group gi of eight of block bi.
   static constexpr __device__ __forceinline__ int column(int bi, int gi, int t) {
     return kGroups ? (gi * NB + bi) * 8 + t : bi * BS_ + gi * 8 + t;
   }
-  static constexpr uint32_t OFF_RING = QBYTES, OFF_BAR = OFF_RING + NS * SLOT;
+  static constexpr uint32_t OFF_RING = QBYTES, OFF_CODES = OFF_RING + NS * SLOT, OFF_BAR = OFF_CODES + NR * RSLOT;
   static constexpr uint32_t OFF_INFO = OFF_BAR + al16(bars(NS) * 8);
   static constexpr uint32_t OFF_FLAGS = OFF_INFO + al16(UQ * sizeof(RowsUnit));
-  static constexpr uint32_t OFF_PREF = OFF_FLAGS + 64;
+  static constexpr uint32_t OFF_QSCALE = OFF_FLAGS + 64;
+  static constexpr uint32_t OFF_PREF = OFF_QSCALE + QSCALE;
   static constexpr uint32_t OFF_PERM = OFF_PREF + al16((kRowsMaxUnitSeqs + 1) * 4);
   static constexpr uint32_t BYTES = OFF_PERM + al16(kRowsMaxUnitSeqs * 2);
   static_assert(BYTES <= kRowsSmem && QBYTES % 1024 == 0 && SLOT % 1024 == 0, "shared memory");
@@ -101,14 +115,18 @@ struct RowsConfig {
   static constexpr uint32_t FULL = 0, EMPTY = NS, UFULL = 2 * NS, UEMPTY = UFULL + UQ, SFULL = UEMPTY + UQ,
                             PREADY = SFULL + NBUF, PVDONE = PREADY + NBUF, QSTAGED = PVDONE + NBUF,
                             QTAKEN = QSTAGED + 1, QREADY = QTAKEN + 1, QFREE = QREADY + 1, OFREE = QFREE + 1,
-                            XBAR = OFREE + 1, XFREE = XBAR + 1;
-  static_assert(XFREE + 1 == bars(NS), "barriers");
+                            XBAR = OFREE + 1, XFREE = XBAR + 1, RFULL = XFREE + 1, REMPTY = RFULL + NR;
+  static_assert(REMPTY + NR == bars(NS), "barriers");
+  // What the producer fills: the ring of tiles, or of tiles of codes.
+  static constexpr int PN = FP8_ ? NR : NS;
+  static constexpr uint32_t PFULL = FP8_ ? RFULL : FULL, PEMPTY = FP8_ ? REMPTY : EMPTY;
+  static constexpr uint32_t OFF_PRING = FP8_ ? OFF_CODES : OFF_RING, PSLOT = FP8_ ? RSLOT : SLOT;
 };
 
 // Wait sites of this kernel (see WaitSite).
 enum RowsSite {
   kRowsUnitSlot = 20, kRowsRing = 21, kRowsUnit = 22, kRowsQ = 23, kRowsOFree = 24, kRowsFull = 25, kRowsP = 26,
-  kRowsS = 27, kRowsPv = 28, kRowsQFree = 29, kRowsX = 30
+  kRowsS = 27, kRowsPv = 28, kRowsQFree = 29, kRowsX = 30, kRowsCodes = 31
 };
 
 template <class C>
@@ -196,7 +214,7 @@ struct RowsCta {
   __device__ __forceinline__ void producer(const int* pref, const uint16_t* perm, int lane) {
     // Items issued together: as many as a warp has lanes for, up to half of the ring.
     // (One at a time took the producer 600 cycles an item, as long as its copy.)
-    constexpr int NB = C::NB, GI = 32 / NB < C::NS / 2 ? 32 / NB : C::NS / 2;
+    constexpr int NB = C::NB, GI = 32 / NB < C::PN / 2 ? 32 / NB : C::PN / 2;
     RowsUnit* info = reinterpret_cast<RowsUnit*>(smem + C::OFF_INFO);
     const uint64_t pol = l2_policy_evict_first();
     const int total = pref[prm.S] * prm.n_hg;
@@ -230,13 +248,13 @@ struct RowsCta {
         // (The next unit is taken while this one's last items are on their way.)
         if (i0 + cnt == 2 * U.nt && lane == 0) claimed = atomicAdd(prm.hdr + kHdrWork, 1);
         next = lane_item(U, i0 + GI + li, lb);
-        const uint32_t gi = g + i0 + li, sl = slot(gi), ph = phase(gi), fb = bar(C::FULL + sl);
+        const uint32_t gi = g + i0 + li, sl = gi % C::PN, ph = gi / C::PN, fb = bar(C::PFULL + sl);
         const size_t row = (size_t)check_block_id(prm, x.id) * prm.KH + U.kv;
-        const uint32_t dst = sbase + C::OFF_RING + sl * C::SLOT + lb * C::BLK;
+        const uint32_t dst = sbase + C::OFF_PRING + sl * C::PSLOT + lb * C::BLK;
         bool done = !x.in;
         uint64_t t_start = 0;
         while (true) {
-          if (!done && mbar_test_wait(bar(C::EMPTY + sl), (ph & 1u) ^ 1u)) {
+          if (!done && mbar_test_wait(bar(C::PEMPTY + sl), (ph & 1u) ^ 1u)) {
             if (lb == 0) mbar_arrive_expect_tx(fb, (uint32_t)x.blocks * C::BLK);
             if (lb < x.blocks) {
               if (!x.value || !C::kTma)
@@ -280,10 +298,10 @@ struct RowsCta {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     // Copies in flight land before the CTA ends, whatever the others did: the last one
     // of each slot.
-    if (lane < C::NS && hi > (uint32_t)lane) {
-      const uint32_t i = hi - 1 - (hi - 1 - lane) % C::NS;
+    if (lane < C::PN && hi > (uint32_t)lane) {
+      const uint32_t i = hi - 1 - (hi - 1 - lane) % C::PN;
       const uint64_t t0 = global_timer_ns();
-      while (!mbar_try_wait(bar(C::FULL + lane), phase(i) & 1u) && global_timer_ns() - t0 < 100000000ull) {
+      while (!mbar_try_wait(bar(C::PFULL + lane), i / C::PN & 1u) && global_timer_ns() - t0 < 100000000ull) {
       }
     }
     __syncwarp();
@@ -297,7 +315,7 @@ struct RowsCta {
   __device__ __forceinline__ void issue_scores(uint32_t tmem, uint32_t sl, int b, uint32_t idesc) const {
     constexpr uint32_t STEP = C::kGroups ? 128u : C::BLK;    // from one instruction's tokens to the next one's
     constexpr uint32_t STRIDE = C::kGroups ? C::BLK : 128u;  // from eight tokens of an instruction to the next
-    constexpr uint32_t LEAD = C::BS * 16u;                   // from a chunk of dims to the next
+    constexpr uint32_t LEAD = C::MS * 16u;                   // from a chunk of dims to the next
     const uint32_t ka = desc_lo(sbase + C::OFF_RING + sl * C::SLOT, LEAD);
     const uint32_t d = tmem + b * C::TN, q = tmem + C::Q_COL;
 #pragma unroll
@@ -311,17 +329,17 @@ struct RowsCta {
   template <bool WHOLE>
   __device__ __forceinline__ void issue_values(uint32_t tmem, int o, uint32_t sl, int b, int ks, uint32_t idesc,
                                                bool add) const {
-    constexpr int KB = C::BS == 8 ? 1 : C::BS / 16;  // k-steps of a block (of two blocks of eight tokens)
-    constexpr uint32_t SW = C::BS == 8 ? kSwizzleNone : C::BS == 16 ? kSwizzle32 : C::BS == 32 ? kSwizzle64 : kSwizzle128;
-    constexpr uint32_t HI = desc_hi(C::BS == 8 ? 128 : C::BS * 16, SW);
-    const uint32_t va = desc_lo(sbase + C::OFF_RING + sl * C::SLOT, C::BS == 8 ? C::BLK : 16);
+    constexpr int KB = C::MS == 8 ? 1 : C::MS / 16;  // k-steps of a block (of two blocks of eight tokens)
+    constexpr uint32_t SW = C::MS == 8 ? kSwizzleNone : C::MS == 16 ? kSwizzle32 : C::MS == 32 ? kSwizzle64 : kSwizzle128;
+    constexpr uint32_t HI = desc_hi(C::MS == 8 ? 128 : C::MS * 16, SW);
+    const uint32_t va = desc_lo(sbase + C::OFF_RING + sl * C::SLOT, C::MS == 8 ? C::BLK : 16);
     const uint32_t d = tmem + C::O_COL + o * C::O_STEP, p = tmem + b * C::TN;
 #pragma unroll
     for (int h = 0; h < (C::kBf16 ? 2 : 1); ++h) {
 #pragma unroll
       for (int k = 0; k < C::TN / 16; ++k) {
         if (!WHOLE && k >= ks) break;
-        constexpr uint32_t STEP = C::BS == 8 ? 2 * C::BLK : C::BLK;
+        constexpr uint32_t STEP = C::MS == 8 ? 2 * C::BLK : C::BLK;
         mma_ts(d, p + h * (C::TN / 2) + k * 8, va + ((k / KB) * STEP + (k % KB) * 32) / 16, HI, idesc,
                add || h > 0 || k > 0);
       }
@@ -463,8 +481,8 @@ struct RowsCta {
 
   // Byte offset of tokens 8c .. 8c + 7 of dim d in a staged value block.
   static __device__ __forceinline__ uint32_t value_chunk(int d, int c) {
-    constexpr uint32_t ROW = C::BS * 2;
-    if constexpr (C::kTma) return d * ROW + ((c ^ ((d * ROW >> 7) & (ROW / 16 - 1))) << 4);
+    constexpr uint32_t ROW = C::MS * 2;
+    if constexpr (C::MS >= 16) return d * ROW + ((c ^ ((d * ROW >> 7) & (ROW / 16 - 1))) << 4);
     else return d * ROW + c * 16;
   }
 
@@ -502,22 +520,111 @@ struct RowsCta {
     return found;
   }
 
+  // Eight E4M3 codes as fp16 (exact).
+  static __device__ __forceinline__ uint4 widen8(uint32_t lo, uint32_t hi) {
+    const auto two = [](uint32_t c) {
+      const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(c & 0xffffu), __NV_E4M3);
+      return (uint32_t)h.x | (uint32_t)h.y << 16;
+    };
+    return make_uint4(two(lo), two(lo >> 16), two(hi), two(hi >> 16));
+  }
+  // Value codes of `n` tokens and anything behind them: what is past them, and NaN codes
+  // (0x7f, 0xff; `found`), become zeros.
+  static __device__ __forceinline__ uint32_t plain_codes(uint32_t w, int n, bool& found) {
+    if (n < 4) w = n <= 0 ? 0u : w & (0xffffffffu >> (32 - 8 * n));
+    const uint32_t nan = ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+    if (nan) {
+      found = true;
+      w &= ~((nan >> 7) * 0xffu);
+    }
+    return w;
+  }
+  // 8-bit caches: the ring's codes widened to fp16, into the layouts of a block of 64
+  // tokens; each of the CW warps takes every CW-th ring item, so that several are on
+  // their way and a warp's waits are another warp's work.
+  __device__ __forceinline__ void widen(int cw, int lane) {
+    const RowsUnit* info = reinterpret_cast<const RowsUnit*>(smem + C::OFF_INFO);
+    volatile int* odd_unit = reinterpret_cast<volatile int*>(smem + C::OFF_FLAGS + 16);
+    constexpr int BS = C::BS, D = C::D;
+    uint32_t g = 0;
+    for (uint32_t k = 0;; ++k) {
+      if (!__all_sync(0xffffffffu, wait(C::UFULL + k % C::UQ, k / C::UQ, kRowsUnit, (int)k))) return;
+      const RowsUnit* up = info + k % C::UQ;
+      const int us = up->s, nt = up->nt, tokens = up->t1 - up->t0;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(C::UEMPTY + k % C::UQ));
+      if (us < 0) return;
+      bool found = false;
+      for (int i = (int)((cw + C::CW - g % C::CW) % C::CW); i < 2 * nt; i += C::CW) {
+        const uint32_t it = g + i, rs = it % C::NR, sl = slot(it);
+        int j;
+        const bool value = item_tile(i, nt, &j);
+        const int left = tokens - j * C::TN;
+        bool ok = wait(C::RFULL + rs, it / C::NR, kRowsCodes, (int)it);
+        if (ok) ok = wait(C::EMPTY + sl, phase(it) + 1, kRowsRing, (int)it);
+        if (!__all_sync(0xffffffffu, ok)) return;
+        const uint4* from = reinterpret_cast<const uint4*>(smem + C::OFF_CODES + rs * C::RSLOT);
+        uint8_t* to = smem + C::OFF_RING + sl * C::SLOT;
+        constexpr int PIECES = C::TN * D / 16;
+        if (!value) {
+          // [block][D/16][BS][16]: a token's 16 dims are two pieces of the tile's [D/8][64][8].
+#pragma unroll 4
+          for (int x = lane; x < PIECES; x += 32) {
+            const int t = x % BS, c = x / BS % (D / 16), b = x / (BS * (D / 16));
+            const uint4 w = from[x];
+            uint8_t* at = to + c * 2048 + (b * BS + t) * 16;
+            *reinterpret_cast<uint4*>(at) = widen8(w.x, w.y);
+            *reinterpret_cast<uint4*>(at + 1024) = widen8(w.z, w.w);
+          }
+        } else {
+          // [block][D][BS]: 16 tokens of a dim (blocks of eight: eight tokens of two dims).
+#pragma unroll 4
+          for (int x = lane; x < PIECES; x += 32) {
+            constexpr int RP = BS >= 16 ? BS / 16 : 1;  // pieces of a dim's row
+            const int b = x / (BS * D / 16), y = x % (BS * D / 16);
+            const int d = BS >= 16 ? y / RP : 2 * y, t = b * BS + (BS >= 16 ? y % RP * 16 : 0);
+            uint4 w = from[x];
+            const int n = left - t, n2 = BS >= 16 ? n - 8 : n;
+            w.x = plain_codes(w.x, n, found);
+            w.y = plain_codes(w.y, n - 4, found);
+            w.z = plain_codes(w.z, n2, found);
+            w.w = plain_codes(w.w, n2 - 4, found);
+            *reinterpret_cast<uint4*>(to + value_chunk(d, t / 8)) = widen8(w.x, w.y);
+            *reinterpret_cast<uint4*>(to + (BS >= 16 ? value_chunk(d, t / 8 + 1) : value_chunk(d + 1, t / 8))) =
+                widen8(w.z, w.w);
+          }
+          // (Units in flight are fewer than four: a unit's word is its own.)
+          if (found) odd_unit[k & 3] = (int)k + 1;
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(bar(C::FULL + sl));
+          mbar_arrive(bar(C::REMPTY + rs));
+        }
+      }
+      g += 2 * nt;
+    }
+  }
+
   // Values that are not finite (rare; the cache itself is read): dims [d0, d1) of a
   // row that has been written get those of the tokens it sees added.  `at`: the row's
   // output or state.
   template <typename E>
   __device__ __noinline__ void add_odd(int s, int kv, int t0, int t1, int sink_blocks, int skip, int lo, int hi, int base,
                                        const uint32_t* bits, int d0, int d1, E* at) const {
-    using T = typename C::T;
-    const T* vc = static_cast<const T*>(prm.vc);
+    using CT = typename std::conditional<C::kFp8, uint8_t, typename C::T>::type;
+    const CT* vc = static_cast<const CT*>(prm.vc);
     for (int t = t0; t < t1; ++t) {
       const int pos = t + (t / C::BS < sink_blocks ? 0 : skip * C::BS);
       if (!(group_seen(RowView{lo, hi, base, bits}, pos, 1) & 1u)) continue;
       int id = prm.bt[(size_t)s * prm.MB + pos / C::BS];
       if ((unsigned)id >= (unsigned)prm.num_blocks) id = 0;
-      const T* blk = vc + ((size_t)id * prm.KH + kv) * C::D * C::BS + t % C::BS;
+      const CT* blk = vc + ((size_t)id * prm.KH + kv) * C::D * C::BS + t % C::BS;
       for (int d = d0; d < d1; ++d) {
-        const float x = (float)blk[d * C::BS];
+        float x;
+        if constexpr (C::kFp8) x = (blk[d * C::BS] & 0x7f) == 0x7f ? NAN : 0.f;
+        else x = (float)blk[d * C::BS];
         if (!(fabsf(x) < INFINITY)) at[d] = (E)((float)at[d] + x);
       }
     }
@@ -553,6 +660,22 @@ struct RowsCta {
     __syncwarp();
     const uint32_t flip = prm.scale_log2 < 0.f ? 0x80008000u : 0u;
     constexpr int W = C::D / 2;  // columns
+    // (8-bit caches) bf16 rows in fp16: times the power of two that brings the largest to
+    // 2^14 .. 2^15 (rows that are not finite: as they are), which the scores' factor undoes.
+    float up = 1.f;
+    if constexpr (C::kQScale) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int c = 0; c < C::D / 8; ++c) {
+        const uint4 x = *reinterpret_cast<const uint4*>(smem + c * 2048 + tid * 16);
+        const uint32_t e[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) m = max(m, max(e[i] & 0x7fffu, e[i] >> 16 & 0x7fffu));
+      }
+      const int ex = (int)(m >> 7);
+      up = __uint_as_float((uint32_t)(ex == 255 ? 127 : min(268 - ex, 254)) << 23);
+      reinterpret_cast<float*>(smem + C::OFF_QSCALE)[(k & 1) * 128 + tid] = 1.f / up;
+    }
 #pragma unroll
     for (int w0 = 0; w0 < W; w0 += 16) {
       uint32_t w[16];
@@ -560,7 +683,14 @@ struct RowsCta {
       for (int c = 0; c < 4; ++c) {
         if (w0 + 4 * c >= W) break;
         const uint4 x = *reinterpret_cast<const uint4*>(smem + (w0 / 4 + c) * 2048 + tid * 16);
-        w[4 * c] = x.x ^ flip; w[4 * c + 1] = x.y ^ flip; w[4 * c + 2] = x.z ^ flip; w[4 * c + 3] = x.w ^ flip;
+        const uint32_t e[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t v = e[i];
+          if constexpr (C::kQScale)
+            v = F16Traits<__half>::pack(__uint_as_float(v << 16) * up, __uint_as_float(v & 0xffff0000u) * up);
+          w[4 * c + i] = v ^ flip;
+        }
       }
       if (w0 + 16 <= W) tmem_st16(tmem + lanes + C::Q_COL + w0, w);
       else tmem_st8(tmem + lanes + C::Q_COL + w0, w);
@@ -574,16 +704,21 @@ struct RowsCta {
 
   __device__ __forceinline__ void softmax(uint32_t tmem, int wg, int tid) {
     using T = typename C::T;
+    using MT = typename C::MT;
     constexpr int TN = C::TN, NB = C::NB, NG = C::NG, D = C::D;
     const RowsUnit* info = reinterpret_cast<const RowsUnit*>(smem + C::OFF_INFO);
     volatile int* odd_unit = reinterpret_cast<volatile int*>(smem + C::OFF_FLAGS + 16);
     const int lane = tid & 31;
     const uint32_t lanes = (uint32_t)(tid & ~31) << 16;  // this warp's lanes of tensor memory
-    const float sl2 = fmaxf(fabsf(prm.scale_log2), 1.17549435e-38f);
+    // (Not zero: a masked score, -inf, times it is -inf.)
+    const float sl2_all = fmaxf(fabsf(prm.scale_log2), 1.17549435e-38f);
     const uint64_t pol_keep = l2_policy_evict_last();
     uint32_t g = 0, k = 0;  // ring items and units before this unit
     uint32_t par = 0;       // of the buffers before the unit
-    if (wg == 0 && !take_rows(tmem, lanes, tid, 0)) return;
+    const bool q_ok = wg != 0 || take_rows(tmem, lanes, tid, 0);
+    if constexpr (C::kQScale && C::NP == 2)  // (the factors; later units': with XBAR)
+      asm volatile("bar.sync 1, %0;" ::"n"(C::NP * 128) : "memory");
+    if (!q_ok) return;
     // (The unit's description stays in its slot while it is worked on, and what a row
     // sees is worked out where a tile is partly seen and at the end: registers hold
     // the row's scores.)
@@ -606,7 +741,9 @@ struct RowsCta {
         full_hi = prm.masks ? first : first + i0 + 1;
         full_lo = prm.window > 0 ? (prm.masks ? U.L - prm.window : first + i1 - prm.window + 1) : 0;
       }
-      float mref = -INFINITY, l = 0.f;
+      float mref = -INFINITY, l = 0.f, sl2 = sl2_all;
+      if constexpr (C::kQScale)
+        sl2 = fmaxf(sl2 * reinterpret_cast<const volatile float*>(smem + C::OFF_QSCALE)[(k & 1) * 128 + row], 1.17549435e-38f);
       const int t0 = U.t0, t1 = U.t1, sink_blocks = U.sink_blocks, skip = U.skip;
       bool ok = true;
       for (int i = C::NP == 2 ? wg : 0; i < nt && ok; i += C::NP) {
@@ -622,7 +759,7 @@ struct RowsCta {
         const int p1 = block_pos(sink_blocks, skip, vb0 + (min(left, TN) - 1) / C::BS) + C::BS - 1;
         const bool jump = vb0 < sink_blocks && skip > 0;
         const bool partial = left < TN || jump || p1 >= full_hi || (p0 < full_lo && p1 >= prm.sinks);
-        if (partial) {
+        if (!C::kFp8 && partial) {
           // (Values: before the weights of the tile are announced.)
           const uint32_t it = g + value_item(i, nt);
           ok = __all_sync(0xffffffffu, wait(C::FULL + slot(it), phase(it), kRowsFull, (int)it));
@@ -704,9 +841,9 @@ struct RowsCta {
             if constexpr (C::kBf16) {
               const uint32_t x = __float_as_uint(s[e]), y = __float_as_uint(s[e + 1]);
               hi[q] = __byte_perm(x, y, 0x7632);
-              lo[q] = F16Traits<T>::pack(s[e] - __uint_as_float(x & 0xffff0000u), s[e + 1] - __uint_as_float(y & 0xffff0000u));
+              lo[q] = F16Traits<MT>::pack(s[e] - __uint_as_float(x & 0xffff0000u), s[e + 1] - __uint_as_float(y & 0xffff0000u));
             } else {
-              hi[q] = F16Traits<T>::pack(s[e], s[e + 1]);
+              hi[q] = F16Traits<MT>::pack(s[e], s[e + 1]);
             }
           }
           tmem_st16(sc + w0, hi);
@@ -746,7 +883,7 @@ struct RowsCta {
       ok = __all_sync(0xffffffffu, wait(C::XBAR, k, kRowsX, (int)k));
       if (!ok) break;
       tc_fence_after();
-      const bool odd = *odd_unit == (int)k + 1;
+      const bool odd = odd_unit[C::kFp8 ? k & 3 : 0] == (int)k + 1;
       float f0 = 1.f, f1 = 0.f;
       bool has0 = nt > 0, has1 = false;  // pipelines with something in O
       int d_lo = 0, d_hi = D;
@@ -772,7 +909,7 @@ struct RowsCta {
       }
       if (warp_rows) {
         const bool some = v.hi > 0 && l != 0.f;
-        const float inv = some ? 1.f / l : 0.f;
+        const float inv = some ? (C::kFp8 ? prm.v_scale / l : 1.f / l) : 0.f;
         f0 *= inv;
         f1 *= inv;
         const bool single = U.np == 1;
@@ -854,7 +991,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) pa_rows_kernel(const __grid_con
   extern __shared__ __align__(1024) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   RowsCta<C> cta(prm, smem);
-  int* flags = reinterpret_cast<int*>(smem + C::OFF_FLAGS);  // abort, bad length, tensor memory, -, odd unit; a barrier
+  int* flags = reinterpret_cast<int*>(smem + C::OFF_FLAGS);  // abort, bad length, tensor memory, -, odd units [4]; a barrier
   int* pref = reinterpret_cast<int*>(smem + C::OFF_PREF);
   uint16_t* perm = reinterpret_cast<uint16_t*>(smem + C::OFF_PERM);
   constexpr int WP = C::NP * 4, WM = WP + 1, WQ = WP + 2;  // producer, product and Q warps
@@ -863,9 +1000,13 @@ __global__ void __launch_bounds__(C::THREADS, 1) pa_rows_kernel(const __grid_con
       mbar_init(cta.bar(C::FULL + i), 1);
       mbar_init(cta.bar(C::EMPTY + i), 1);
     }
+    for (int i = 0; i < C::NR; ++i) {
+      mbar_init(cta.bar(C::RFULL + i), 1);
+      mbar_init(cta.bar(C::REMPTY + i), 1);
+    }
     for (int i = 0; i < C::UQ; ++i) {
       mbar_init(cta.bar(C::UFULL + i), 1);
-      mbar_init(cta.bar(C::UEMPTY + i), C::NP * 4 + 3);
+      mbar_init(cta.bar(C::UEMPTY + i), C::NP * 4 + 1 + C::LOADERS / 32 + C::CW);
     }
     for (int i = 0; i < C::NBUF; ++i) {
       mbar_init(cta.bar(C::SFULL + i), 1);
@@ -880,7 +1021,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) pa_rows_kernel(const __grid_con
     mbar_init(cta.bar(C::XBAR), C::NP * 128);
     mbar_init(cta.bar(C::XFREE), C::NP * 128);
     mbar_init(cta.sbase + C::OFF_FLAGS + 32, 1);
-    flags[0] = flags[1] = flags[4] = 0;
+    flags[0] = flags[1] = flags[4] = flags[5] = flags[6] = flags[7] = 0;
     fence_mbarrier_init();
   }
   if (warp == WM) tmem_alloc(smem_addr(flags + 2), 512);
@@ -909,8 +1050,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) pa_rows_kernel(const __grid_con
       cta.producer(pref, perm, lane);
     } else if (warp == WM) {
       cta.products(tmem, lane);
-    } else {
+    } else if (warp < WQ + C::LOADERS / 32) {
       cta.bring_rows(tid - WQ * 32, lane);
+    } else if constexpr (C::kFp8) {
+      cta.widen(warp - WQ - C::LOADERS / 32, lane);
     }
   }
   tc_fence_before();

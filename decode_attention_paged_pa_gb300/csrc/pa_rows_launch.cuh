@@ -40,13 +40,13 @@ static cudaError_t rows_go(const KParams& prm, int max_ctas, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, pa_rows_kernel<C>, prm);
 }
 
-template <typename T, int D>
+template <typename T, int D, bool FP8 = false>
 static cudaError_t rows_by_block(const KParams& prm, int BS, int max_ctas, cudaStream_t st) {
   switch (BS) {
-    case 8: return rows_go<RowsConfig<T, D, 8>>(prm, max_ctas, st);
-    case 16: return rows_go<RowsConfig<T, D, 16>>(prm, max_ctas, st);
-    case 32: return rows_go<RowsConfig<T, D, 32>>(prm, max_ctas, st);
-    default: return rows_go<RowsConfig<T, D, 64>>(prm, max_ctas, st);
+    case 8: return rows_go<RowsConfig<T, D, 8, FP8>>(prm, max_ctas, st);
+    case 16: return rows_go<RowsConfig<T, D, 16, FP8>>(prm, max_ctas, st);
+    case 32: return rows_go<RowsConfig<T, D, 32, FP8>>(prm, max_ctas, st);
+    default: return rows_go<RowsConfig<T, D, 64, FP8>>(prm, max_ctas, st);
   }
 }
 

@@ -355,3 +355,56 @@ def test_many_rows_of_large_scores():
             kc[bt[0, t // BS], :, :, t % BS] = (t / 256.0) * (1.0 if t % 7 else -1.0)
         got, lse = run(q, kc, vc, bt, lens, 0.15, 5000, 0, P=1024)
         check(got, lse, q, kc, vc, bt, lens, 0.15, 5000, 0)
+
+
+MANY8 = [("fp16", 16, 4, 128, 16), ("bf16", 12, 1, 128, 32), ("bf16", 8, 2, 64, 8), ("fp16", 6, 2, 80, 64),
+         ("bf16", 5, 1, 256, 16), ("fp16", 4, 2, 256, 64), ("fp16", 10, 1, 96, 32), ("bf16", 4, 4, 112, 16),
+         ("fp16", 4, 1, 256, 8), ("bf16", 3, 1, 256, 32), ("fp16", 4, 1, 128, 8), ("bf16", 4, 1, 128, 64)]
+
+
+@pytest.mark.parametrize("n,window,sinks,P", [(40, 0, 0, 128), (130, 200, 10, 256), (70, 70, 300, 192)])
+@pytest.mark.parametrize("shape", MANY8, ids=["-".join(map(str, s)) for s in MANY8])
+def test_many_rows_over_e4m3(shape, n, window, sinks, P):
+    """As above over an E4M3 cache; slots that no row sees hold NaN codes."""
+    dtype, H, KH, D, BS = shape
+    lens = [n, n + 1, n + 333, n + 700]
+    see = torch.stack([ancestors(tree_parents(n + s, n, n - 9 * s)) for s in range(len(lens))])
+    for tree in (True, False):
+        w = window if tree or window else 150
+        case = make(D + n, T[dtype], "e4m3", n, H, KH, D, BS, lens, w, sinks, see if tree else None)
+        got, lse = run(*case, 0.07 if tree else -0.07, w, sinks, see if tree else None, P=P)
+        check(got, lse, *case, 0.07 if tree else -0.07, w, sinks, see if tree else None)
+
+
+def test_many_rows_over_e4m3_of_any_size():
+    """bf16 queries far outside fp16's range, each row by a power of two of its own,
+    and one row of zeros: exact in the kernel, so the usual bound holds."""
+    n, H, KH, D, BS, L = 40, 4, 1, 128, 16, 300
+    for up, scale in ((2.0 ** 90, 0.1 * 2.0 ** -90), (2.0 ** -60, 0.1 * 2.0 ** 60)):
+        q, kc, vc, bt, lens = make(6, torch.bfloat16, "e4m3", n, H, KH, D, BS, [L], 120, 3)
+        q = (q.float() * up).to(torch.bfloat16)
+        q[0, 5] = 0
+        got, lse = run(q, kc, vc, bt, lens, scale, 120, 3)
+        check(got, lse, q, kc, vc, bt, lens, scale, 120, 3)
+
+
+def test_many_rows_that_see_nan_codes():
+    """A NaN code in a value reaches the rows that see it, in tiles that every row sees
+    (dim 9) and at the edges of windows (dims 3 and 7)."""
+    n, H, KH, D, BS, L = 36, 4, 1, 128, 16, 400
+    for dtype in (torch.float16, torch.bfloat16):
+        q, kc, vc, bt, lens = make(3, dtype, "e4m3", n, H, KH, D, BS, [L], 200, 0, poison=False)
+        lo = L - n + 1 - 200
+        clean = vc.clone()
+        vc[bt[0, (L - 5) // BS], 0, 3, (L - 5) % BS] = 0xFF
+        vc[bt[0, (lo + 2) // BS], 0, 7, (lo + 2) % BS] = NAN_E4M3
+        vc[bt[0, 290 // BS], 0, 9, 290 % BS] = NAN_E4M3
+        got, _ = run(q, kc, vc, bt, lens, 0.1, 200, 0)
+        odd = torch.zeros(n, D, dtype=torch.bool)
+        odd[n - 5:, 3] = True
+        odd[:3, 7] = True
+        odd[:, 9] = True
+        assert torch.equal(got[0].isnan(), odd[:, None].expand(n, H, D))
+        ref, _, bound = attend64(q, kc, clean, bt, lens, 0.1, 200, 0, None, K_SCALE, V_SCALE)
+        fine = ~odd[None, :, None].expand(1, n, H, D)
+        assert bool(((got.double() - ref).abs() <= bound)[fine].all())
