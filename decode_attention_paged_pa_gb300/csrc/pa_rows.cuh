@@ -22,7 +22,7 @@
 // One CTA per SM, persistent over units (sequence, partition, kv head, up to 128
 // rows), which a producer warp takes from the global counter (as in pa_kernel.cuh)
 // and streams through a ring of K and V tiles of 64 tokens; two warps bring Q, a unit
-// ahead; one warp issues the products.  Warpgroups of four warps, a row a thread, turn
+// ahead; one warp issues the scores' products, one those with the values.  Warpgroups of four warps, a row a thread, turn
 // scores into weights: two of them (NP = 2) take the tiles in turn, each with its own
 // O, joined at the end of the unit; at head size 256 one does all.  Scores are
 // computed up to NBUF tiles ahead, into buffers that the weights then take over.
@@ -77,7 +77,7 @@ struct RowsConfig {
   static constexpr int CW = !FP8_ ? 0 : D_ <= 128 ? 4 : 2, NR = !FP8_ ? 0 : D_ <= 128 ? 8 : 2;
   static constexpr uint32_t RSLOT = FP8_ ? (uint32_t)TN * D_ : 0;
   static constexpr int LOADERS = FP8_ ? 32 : 64;  // threads that bring Q
-  static constexpr int THREADS = NP * 128 + 64 + LOADERS + CW * 32, UQ = 2;
+  static constexpr int THREADS = NP * 128 + 96 + LOADERS + CW * 32, UQ = 2;
   // A tile's scores take NI instructions a k-step of N columns each: one a block, or
   // (kGroups) one for each group of eight tokens, of every block, whichever are fewer.
   static constexpr bool kGroups = !FP8_ && NG < NB;
@@ -95,8 +95,10 @@ struct RowsConfig {
            al16(kRowsMaxUnitSeqs * 2);
   }
   static constexpr int kFit = (int)((kRowsSmem - small(D_ > 128 ? 8 : 16) - QBYTES - NR * RSLOT) / SLOT);
-  static constexpr int NS = kFit < 16 ? kFit : 16;
-  static_assert(!FP8_ || (NR % CW == 0 && NS >= CW), "a warp's waits for a slot are a phase apart at most");
+  // (8-bit caches: an even number, and NR a multiple of CW, so that a warp that widens
+  // codes is never two phases off at a slot.)
+  static constexpr int NS = (kFit < 16 ? kFit : 16) & (FP8_ ? ~1 : ~0);
+  static_assert(!FP8_ || (NR % (FP8_ ? CW : 1) == 0 && NS >= CW), "a warp's waits for a slot are a phase apart at most");
   static_assert(NS >= 2 * NBUF, "the ring holds the keys that are ahead and two tiles' values");
   // The score column of token t of group gi of eight of block bi.
   static constexpr __device__ __forceinline__ int column(int bi, int gi, int t) {
@@ -307,8 +309,8 @@ struct RowsCta {
     __syncwarp();
   }
 
-  // ---------------------------------------------------------------- product warp
-  // The whole warp goes through the loops, so that descriptors are made in uniform
+  // ---------------------------------------------------------------- product warps
+  // A whole warp goes through the loops, so that descriptors are made in uniform
   // registers; one lane issues (descriptors made by one diverged lane cost 100 cycles
   // a product, more than the product).
   // Scores of ring slot `sl` into buffer b.
@@ -345,55 +347,87 @@ struct RowsCta {
       }
     }
   }
-  __device__ __forceinline__ void products(uint32_t tmem, int lane) {
+  __device__ __forceinline__ bool all(uint32_t b, uint32_t ph, int site, int detail) const {
+    return __all_sync(0xffffffffu, wait(b, ph, site, detail)) != 0;
+  }
+  // What the warp has issued completes before tensor memory is freed.
+  __device__ __forceinline__ void drain(uint32_t at) const {
+    if (elect_one()) mma_commit(at);
+    __syncwarp();
+    const uint64_t t0 = global_timer_ns();
+    while (!mbar_try_wait(at, 0) && global_timer_ns() - t0 < 100000000ull) {
+    }
+    __syncwarp();
+  }
+  // One warp issues the scores' products ...
+  __device__ __forceinline__ void score_products(uint32_t tmem, int lane) {
     const RowsUnit* info = reinterpret_cast<const RowsUnit*>(smem + C::OFF_INFO);
-    const uint32_t id_s = f16_idesc(C::kBf16, C::N), id_o = f16_idesc(C::kBf16, C::D);
-    const auto all = [&](uint32_t b, uint32_t ph, int site, int detail) {
-      return __all_sync(0xffffffffu, wait(b, ph, site, detail)) != 0;
-    };
-    uint32_t g = 0, k = 0;  // ring items and units before this unit
-    uint32_t par = 0;
+    const uint32_t id_s = f16_idesc(C::kBf16, C::N);
+    uint32_t g = 0, par = 0;  // ring items before this unit; as in the softmax
     bool ok = true;
-    while (ok) {
+    for (uint32_t k = 0; ok; ++k) {
       if (!all(C::UFULL + k % C::UQ, k / C::UQ, kRowsUnit, (int)k)) break;
       const RowsUnit* up = info + k % C::UQ;
       // (Shuffles tell the compiler that these are the same in every lane.)
       const int us = __shfl_sync(0xffffffffu, up->s, 0), nt = __shfl_sync(0xffffffffu, up->nt, 0);
-      const int tokens = __shfl_sync(0xffffffffu, up->t1 - up->t0, 0);
       if (lane == 0) mbar_arrive(bar(C::UEMPTY + k % C::UQ));
       if (us < 0) break;
       if (!all(C::QREADY, k, kRowsQ, (int)k)) break;
-      // (The last unit's joining used the buffers; and with this wait neither side is
-      // ever more than a unit ahead, so that a parity tells the phases apart.)
+      // (The last unit's joining used the buffers, and its products are complete; and
+      // with this wait neither side is ever more than a unit ahead, so that a parity
+      // tells the phases apart.)
       if (!all(C::XFREE, k + 1, kRowsX, (int)k)) break;
       tc_fence_after();
-      // Scores of tile i, into buffer b; after the last ones Q may be replaced.
-      const auto scores = [&](int i, int b) {
-        const uint32_t it = g + key_item(i);
-        if (!all(C::FULL + slot(it), phase(it), kRowsFull, (int)it)) return false;
-        if (elect_one()) {
-          issue_scores(tmem, slot(it), b, id_s);
-          mma_commit(bar(C::SFULL + b));
-          mma_commit(bar(C::EMPTY + slot(it)));
-          if (i + 1 == nt) mma_commit(bar(C::QFREE));
-        }
-        __syncwarp();
-        return true;
-      };
       if (nt == 0) {
         if (elect_one()) mma_commit(bar(C::QFREE));
         __syncwarp();
       }
-      for (int i = 0; i < C::NBUF && i < nt && ok; ++i) ok = scores(i, i);
-      for (int i = 0, b = 0; i < nt && ok; ++i, b = b + 1 < C::NBUF ? b + 1 : 0) {
-        const int o = C::NP == 2 ? i & 1 : 0;
+      for (int i = 0, b = 0; i < nt; ++i, b = b + 1 < C::NBUF ? b + 1 : 0) {
+        const uint32_t it = g + key_item(i);
+        // (The buffer's weights have been used; this wait comes first, so that the one for
+        // the slot is a phase off at most.)
+        if (i >= C::NBUF) {
+          ok = all(C::PVDONE + b, (par >> b) + (i / C::NBUF - 1), kRowsPv, i);
+          tc_fence_after();
+        }
+        if (ok) ok = all(C::FULL + slot(it), phase(it), kRowsFull, (int)it);
+        if (!ok) break;
+        if (elect_one()) {
+          issue_scores(tmem, slot(it), b, id_s);
+          mma_commit(bar(C::SFULL + b));
+          mma_commit(bar(C::EMPTY + slot(it)));
+          if (i + 1 == nt) mma_commit(bar(C::QFREE));  // Q may be replaced
+        }
+        __syncwarp();
+      }
+      par = parity_after(par, nt);
+      g += 2 * nt;
+    }
+    drain(sbase + C::OFF_FLAGS + 32);
+  }
+  // ... and one those with the values.  (One warp that did both, wait for wait, took
+  // 1800 cycles a tile, of which the products are 530.)
+  __device__ __forceinline__ void value_products(uint32_t tmem, int lane) {
+    const RowsUnit* info = reinterpret_cast<const RowsUnit*>(smem + C::OFF_INFO);
+    const uint32_t id_o = f16_idesc(C::kBf16, C::D);
+    uint32_t g = 0, par = 0;
+    bool ok = true;
+    for (uint32_t k = 0; ok; ++k) {
+      if (!all(C::UFULL + k % C::UQ, k / C::UQ, kRowsUnit, (int)k)) break;
+      const RowsUnit* up = info + k % C::UQ;
+      const int us = __shfl_sync(0xffffffffu, up->s, 0), nt = __shfl_sync(0xffffffffu, up->nt, 0);
+      const int tokens = __shfl_sync(0xffffffffu, up->t1 - up->t0, 0);
+      if (lane == 0) mbar_arrive(bar(C::UEMPTY + k % C::UQ));
+      if (us < 0) break;
+      if (!all(C::OFREE, k + 1, kRowsOFree, (int)k)) break;  // the last unit's O is read
+      for (int i = 0, b = 0; i < nt; ++i, b = b + 1 < C::NBUF ? b + 1 : 0) {
         const uint32_t it = g + value_item(i, nt);
-        ok = all(C::FULL + slot(it), phase(it), kRowsFull, (int)it);
-        if (ok && i < C::NP) ok = all(C::OFREE, k + 1, kRowsOFree, (int)k);  // the last unit's O is read
-        if (ok) ok = all(C::PREADY + b, par >> b, kRowsP, i);
+        ok = all(C::PREADY + b, par >> b, kRowsP, i);
+        if (ok) ok = all(C::FULL + slot(it), phase(it), kRowsFull, (int)it);
         if (!ok) break;
         par ^= 1u << b;
         tc_fence_after();
+        const int o = C::NP == 2 ? i & 1 : 0;
         const int left = tokens - i * C::TN, ks = left >= C::TN ? C::TN / 16 : (left + 15) / 16;
         if (elect_one()) {
           if (ks == C::TN / 16) issue_values<true>(tmem, o, slot(it), b, ks, id_o, i >= C::NP);
@@ -402,21 +436,10 @@ struct RowsCta {
           mma_commit(bar(C::EMPTY + slot(it)));
         }
         __syncwarp();
-        // (These scores go where the weights just used were, behind their product.)
-        if (i + C::NBUF < nt) ok = scores(i + C::NBUF, b);
       }
-      if (!ok) break;
       g += 2 * nt;
-      ++k;
     }
-    // What has been issued completes before tensor memory is freed.
-    const uint32_t drain = sbase + C::OFF_FLAGS + 32;
-    if (elect_one()) mma_commit(drain);
-    __syncwarp();
-    const uint64_t t0 = global_timer_ns();
-    while (!mbar_try_wait(drain, 0) && global_timer_ns() - t0 < 100000000ull) {
-    }
-    __syncwarp();
+    drain(sbase + C::OFF_FLAGS + 40);
   }
 
   // ---------------------------------------------------------------- Q warps
@@ -457,24 +480,19 @@ struct RowsCta {
   }
 
   // ---------------------------------------------------------------- softmax warpgroups
-  // The tokens of a group of eight that a row sees: positions p .. p + 7, `n` of them
-  // in the unit.
-  static __device__ __forceinline__ uint32_t first_bits(int n) { return n >= 8 ? 0xffu : n <= 0 ? 0u : (1u << n) - 1u; }
-  __device__ __forceinline__ uint32_t group_seen(const RowView& v, int p, int n) const {
-    uint32_t m = first_bits(min(v.hi - p, n));
+  // The tokens that a row sees of 64 at positions p .. p + 63, `n` of them there.
+  static __device__ __forceinline__ uint64_t first_bits(int n) { return n >= 64 ? ~0ull : n <= 0 ? 0ull : (1ull << n) - 1ull; }
+  __device__ __forceinline__ uint64_t seen64(const RowView& v, int p, int n) const {
+    uint64_t m = first_bits(min(v.hi - p, n));
     m &= ~first_bits(v.lo - p) | first_bits(prm.sinks - p);
-    if (v.bits && p + 7 >= v.base) {
-      const int off = p - v.base;
-      uint64_t w;
-      if (off < 0) {
-        w = (uint64_t)__ldg(v.bits) << -off | ((1ull << -off) - 1);
-      } else {
-        const int i = off >> 5;
-        w = i < prm.words ? __ldg(v.bits + i) : 0u;
-        if (i + 1 < prm.words) w |= (uint64_t)__ldg(v.bits + i + 1) << 32;
-        w >>= off & 31;
-      }
-      m &= (uint32_t)w;
+    if (v.bits && p + 63 >= v.base) {
+      // Node j of the row's mask is the token at base + j.
+      const int off = p - v.base, i = max(off, 0) >> 5, sh = max(off, 0) & 31;
+      uint32_t w[3];
+#pragma unroll
+      for (int q = 0; q < 3; ++q) w[q] = i + q < prm.words ? __ldg(v.bits + i + q) : 0u;
+      const uint64_t b = (uint64_t)__funnelshift_r(w[1], w[2], sh) << 32 | __funnelshift_r(w[0], w[1], sh);
+      m &= off >= 0 ? b : b << -off | first_bits(-off);
     }
     return m;
   }
@@ -492,30 +510,29 @@ struct RowsCta {
     constexpr uint32_t kExp = C::kBf16 ? 0x7f80u : 0x7c00u;
     uint8_t* v = smem + C::OFF_RING + sl * C::SLOT;
     const int groups = min(C::TN / 8, (left + 15) / 16 * 2);
+    // (Not finite: the number without its sign is kExp at least, so that adding `up` sets
+    // the sign's bit.)
+    constexpr uint32_t up = C::kBf16 ? 0x00800080u : 0x04000400u;
     bool found = false;
+#pragma unroll 4
     for (int i = tid; i < C::D * groups; i += 128) {
       const int gr = i / C::D, d = i - gr * C::D, b = gr / C::NG, c = gr % C::NG, n = left - gr * 8;
       uint4* at = reinterpret_cast<uint4*>(v + b * C::BLK + value_chunk(d, c));
-      if (n <= 0) {
-        *at = make_uint4(0, 0, 0, 0);
-        continue;
-      }
-      uint4 x = *at;
+      const uint4 x = *at;
       uint32_t w[4] = {x.x, x.y, x.z, x.w};
-      bool change = false;
+      uint32_t any = 0;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) any |= (w[q] & 0x7fff7fffu) + up;
+      if (!(any & 0x80008000u) && n >= 8) continue;
 #pragma unroll
       for (int q = 0; q < 4; ++q)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const bool past = 2 * q + h >= n;
-          const bool odd = ((w[q] >> (16 * h)) & kExp) == kExp;
-          if (past || odd) {
-            w[q] &= h ? 0xffffu : 0xffff0000u;
-            change = true;
-          }
+          const bool past = 2 * q + h >= n, odd = ((w[q] >> (16 * h)) & kExp) == kExp;
+          if (past || odd) w[q] &= h ? 0xffffu : 0xffff0000u;
           found |= odd && !past;
         }
-      if (change) *at = make_uint4(w[0], w[1], w[2], w[3]);
+      *at = make_uint4(w[0], w[1], w[2], w[3]);
     }
     return found;
   }
@@ -617,7 +634,7 @@ struct RowsCta {
     const CT* vc = static_cast<const CT*>(prm.vc);
     for (int t = t0; t < t1; ++t) {
       const int pos = t + (t / C::BS < sink_blocks ? 0 : skip * C::BS);
-      if (!(group_seen(RowView{lo, hi, base, bits}, pos, 1) & 1u)) continue;
+      if (!(seen64(RowView{lo, hi, base, bits}, pos, 1) & 1ull)) continue;
       int id = prm.bt[(size_t)s * prm.MB + pos / C::BS];
       if ((unsigned)id >= (unsigned)prm.num_blocks) id = 0;
       const CT* blk = vc + ((size_t)id * prm.KH + kv) * C::D * C::BS + t % C::BS;
@@ -777,15 +794,16 @@ struct RowsCta {
         tmem_get64(sc, sc + 32, s);
         if (partial) {
           const RowView v = view();
+          // (A tile can have the end of the first tokens' blocks in it, and then others.)
+          uint64_t m = seen64(v, p0, left);
+          if (jump) {
+            const int n = sink_blocks * C::BS - tile;  // of its tokens are before it
+            if (n < TN) m = (m & first_bits(n)) | (seen64(v, p0 + skip * C::BS, left) & ~first_bits(n));
+          }
+          const uint32_t mm[2] = {(uint32_t)m, (uint32_t)(m >> 32)};
 #pragma unroll
-          for (int gi = 0; gi < NG; ++gi)
-#pragma unroll
-            for (int bi = 0; bi < NB; ++bi) {
-              const uint32_t m = group_seen(v, block_pos(sink_blocks, skip, vb0 + bi) + gi * 8, left - bi * C::BS - gi * 8);
-#pragma unroll
-              for (int t = 0; t < 8; ++t)
-                if (!((m >> t) & 1u)) s[C::column(bi, gi, t)] = -INFINITY;
-            }
+          for (int t = 0; t < TN; ++t)
+            if (!(mm[t / 32] >> (t % 32) & 1u)) s[C::column(t / C::BS, t % C::BS / 8, t % 8)] = -INFINITY;
           __syncwarp();
         }
         float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -925,34 +943,41 @@ struct RowsCta {
                             : reinterpret_cast<uint8_t*>(prm.ws_o + ((sh0 + r) * prm.Pmax + U.p) * D + (lane & 3) * 4);
         }
         // (Of a pipeline without a tile, O holds anything: it is read, and not used.)
+        constexpr int NCH = (D / 2 % 32 == 0 && C::NP == 2) || C::NP == 1 ? 2 : 1;  // pieces of 16 dims at a time
 #pragma unroll 1
-        for (int c0 = d_lo; c0 < d_hi; c0 += 16) {
-          float o[16];
+        for (int c0 = d_lo; c0 < d_hi; c0 += NCH * 16) {
+          float o[NCH][16];
           __syncwarp();  // (rows that are not the unit's have left lanes behind)
-          if constexpr (C::NP == 2) {
-            float ab[32];
-            tmem_get32(ob + c0, ob + C::O_STEP + c0, ab);
+          if constexpr (C::NP == 2 && NCH == 2) {
+            float ab[64];
+            tmem_get64(ob + c0, ob + C::O_STEP + c0, ab);
 #pragma unroll
-            for (int q = 0; q < 16; ++q) o[q] = has1 ? fmaf(ab[16 + q], f1, ab[q] * f0) : ab[q] * f0;
+            for (int q = 0; q < 32; ++q) o[q / 16][q % 16] = has1 ? fmaf(ab[32 + q], f1, ab[q] * f0) : ab[q] * f0;
           } else {
-            tmem_get16(ob + c0, o);
+            float ab[32];
+            tmem_get32(ob + c0, ob + (C::NP == 2 ? C::O_STEP : 16) + c0, ab);
 #pragma unroll
-            for (int q = 0; q < 16; ++q) o[q] *= f0;
+            for (int q = 0; q < NCH * 16; ++q)
+              o[q / 16][q % 16] = C::NP == 2 && has1 ? fmaf(ab[(16 + q) % 32], f1, ab[q] * f0) : ab[q] * f0;
           }
           if (!some || !has0) {
 #pragma unroll
-            for (int q = 0; q < 16; ++q) o[q] = 0.f;
+            for (int q = 0; q < NCH * 16; ++q) o[q / 16][q % 16] = 0.f;
           }
           // Four lanes exchange their rows' pieces of four dims: then lane q of the four has
           // piece q of each of their rows, and they store 16 dims of one row at a time (a
           // lane a row touched 32 lines with every store).
-          transpose4(o, lane);
+#pragma unroll
+          for (int h = 0; h < NCH; ++h) transpose4(o[h], lane);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const float4 x = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
             if (!to[i]) continue;
-            if (single) store4<T>(reinterpret_cast<T*>(to[i]) + c0, x);
-            else st_f4_policy(reinterpret_cast<float4*>(to[i]) + c0 / 4, x, pol_keep);
+#pragma unroll
+            for (int h = 0; h < NCH; ++h) {
+              const float4 x = make_float4(o[h][4 * i], o[h][4 * i + 1], o[h][4 * i + 2], o[h][4 * i + 3]);
+              if (single) store4<T>(reinterpret_cast<T*>(to[i]) + c0 + 16 * h, x);
+              else st_f4_policy(reinterpret_cast<float4*>(to[i]) + (c0 + 16 * h) / 4, x, pol_keep);
+            }
           }
         }
         if (odd) {
@@ -991,10 +1016,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) pa_rows_kernel(const __grid_con
   extern __shared__ __align__(1024) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   RowsCta<C> cta(prm, smem);
-  int* flags = reinterpret_cast<int*>(smem + C::OFF_FLAGS);  // abort, bad length, tensor memory, -, odd units [4]; a barrier
+  int* flags = reinterpret_cast<int*>(smem + C::OFF_FLAGS);  // abort, bad length, tensor memory, -, odd units [4]; two barriers
   int* pref = reinterpret_cast<int*>(smem + C::OFF_PREF);
   uint16_t* perm = reinterpret_cast<uint16_t*>(smem + C::OFF_PERM);
-  constexpr int WP = C::NP * 4, WM = WP + 1, WQ = WP + 2;  // producer, product and Q warps
+  constexpr int WP = C::NP * 4, WM = WP + 1, WV = WP + 2, WQ = WP + 3;  // producer, product and Q warps
   if (tid == 0) {
     for (int i = 0; i < C::NS; ++i) {
       mbar_init(cta.bar(C::FULL + i), 1);
@@ -1006,7 +1031,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) pa_rows_kernel(const __grid_con
     }
     for (int i = 0; i < C::UQ; ++i) {
       mbar_init(cta.bar(C::UFULL + i), 1);
-      mbar_init(cta.bar(C::UEMPTY + i), C::NP * 4 + 1 + C::LOADERS / 32 + C::CW);
+      mbar_init(cta.bar(C::UEMPTY + i), C::NP * 4 + 2 + C::LOADERS / 32 + C::CW);
     }
     for (int i = 0; i < C::NBUF; ++i) {
       mbar_init(cta.bar(C::SFULL + i), 1);
@@ -1021,6 +1046,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) pa_rows_kernel(const __grid_con
     mbar_init(cta.bar(C::XBAR), C::NP * 128);
     mbar_init(cta.bar(C::XFREE), C::NP * 128);
     mbar_init(cta.sbase + C::OFF_FLAGS + 32, 1);
+    mbar_init(cta.sbase + C::OFF_FLAGS + 40, 1);
     flags[0] = flags[1] = flags[4] = flags[5] = flags[6] = flags[7] = 0;
     fence_mbarrier_init();
   }
@@ -1049,7 +1075,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) pa_rows_kernel(const __grid_con
     if (warp == WP) {
       cta.producer(pref, perm, lane);
     } else if (warp == WM) {
-      cta.products(tmem, lane);
+      cta.score_products(tmem, lane);
+    } else if (warp == WV) {
+      cta.value_products(tmem, lane);
     } else if (warp < WQ + C::LOADERS / 32) {
       cta.bring_rows(tid - WQ * 32, lane);
     } else if constexpr (C::kFp8) {
