@@ -89,9 +89,8 @@ struct RowsConfig {
   // Shared memory: the next unit's Q, the ring, then barriers, units, flags, order.
   static constexpr uint32_t QBYTES = QTILE;
   static constexpr uint32_t bars(int ns) { return 2 * ns + 2 * NR + 2 * UQ + 3 * NBUF + 7; }
-  static constexpr uint32_t QSCALE = kQScale ? 2 * 128 * 4 : 0;
   static constexpr uint32_t small(int ns) {
-    return al16(bars(ns) * 8) + al16(UQ * sizeof(RowsUnit)) + 64 + QSCALE + al16((kRowsMaxUnitSeqs + 1) * 4) +
+    return al16(bars(ns) * 8) + al16(UQ * sizeof(RowsUnit)) + 64 + al16((kRowsMaxUnitSeqs + 1) * 4) +
            al16(kRowsMaxUnitSeqs * 2);
   }
   static constexpr int kFit = (int)((kRowsSmem - small(D_ > 128 ? 8 : 16) - QBYTES - NR * RSLOT) / SLOT);
@@ -107,8 +106,7 @@ struct RowsConfig {
   static constexpr uint32_t OFF_RING = QBYTES, OFF_CODES = OFF_RING + NS * SLOT, OFF_BAR = OFF_CODES + NR * RSLOT;
   static constexpr uint32_t OFF_INFO = OFF_BAR + al16(bars(NS) * 8);
   static constexpr uint32_t OFF_FLAGS = OFF_INFO + al16(UQ * sizeof(RowsUnit));
-  static constexpr uint32_t OFF_QSCALE = OFF_FLAGS + 64;
-  static constexpr uint32_t OFF_PREF = OFF_QSCALE + QSCALE;
+  static constexpr uint32_t OFF_PREF = OFF_FLAGS + 64;
   static constexpr uint32_t OFF_PERM = OFF_PREF + al16((kRowsMaxUnitSeqs + 1) * 4);
   static constexpr uint32_t BYTES = OFF_PERM + al16(kRowsMaxUnitSeqs * 2);
   static_assert(BYTES <= kRowsSmem && QBYTES % 1024 == 0 && SLOT % 1024 == 0, "shared memory");
@@ -647,29 +645,22 @@ struct RowsCta {
     }
   }
 
-  // o[4 i + e] of lane q of four becomes what lane i had in o[4 q + e].
-  static __device__ __forceinline__ void transpose4(float (&o)[16], int lane) {
-#pragma unroll
-    for (int st = 1; st < 4; st <<= 1) {
-      const bool up = lane & st;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (i & st) continue;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float &a = o[4 * i + e], &b = o[4 * (i + st) + e];
-          const float got = __shfl_xor_sync(0xffffffffu, up ? a : b, st);
-          if (up) a = got;
-          else b = got;
-        }
-      }
+  // 32 bytes, by one store where `wide` says that they are aligned to it.
+  static __device__ __forceinline__ void st_32b(uint8_t* at, const uint32_t (&w)[8], bool wide) {
+    if (wide) {
+      asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                   "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                   : "memory");
+    } else {
+      reinterpret_cast<uint4*>(at)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+      reinterpret_cast<uint4*>(at)[1] = make_uint4(w[4], w[5], w[6], w[7]);
     }
   }
 
-  // The staged Q of unit k into tensor memory (the first warpgroup, a row a thread),
-  // once the products with the one before are complete.  A negative scale's sign goes
+  // The staged Q of unit k into tensor memory (a row a thread, the pipelines' warpgroups
+  // in turn), once the products with the one before are complete.  A negative scale's sign goes
   // with it: the softmax works with one that is not negative.
-  __device__ __forceinline__ bool take_rows(uint32_t tmem, uint32_t lanes, int tid, uint32_t k) const {
+  __device__ __forceinline__ bool take_rows(uint32_t tmem, uint32_t lanes, int wg, int tid, uint32_t k, float& factor) const {
     bool ok = wait(C::QSTAGED, k, kRowsQ, (int)k);
     if (ok) ok = wait(C::QFREE, k + 1, kRowsQFree, (int)k);
     if (!__all_sync(0xffffffffu, ok)) return false;
@@ -691,10 +682,11 @@ struct RowsCta {
       }
       const int ex = (int)(m >> 7);
       up = __uint_as_float((uint32_t)(ex == 255 ? 127 : min(268 - ex, 254)) << 23);
-      reinterpret_cast<float*>(smem + C::OFF_QSCALE)[(k & 1) * 128 + tid] = 1.f / up;
+      factor = 1.f / up;
     }
 #pragma unroll
     for (int w0 = 0; w0 < W; w0 += 16) {
+      if (C::NP == 2 && (w0 / 16 & 1) != wg) continue;
       uint32_t w[16];
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
@@ -732,10 +724,8 @@ struct RowsCta {
     const uint64_t pol_keep = l2_policy_evict_last();
     uint32_t g = 0, k = 0;  // ring items and units before this unit
     uint32_t par = 0;       // of the buffers before the unit
-    const bool q_ok = wg != 0 || take_rows(tmem, lanes, tid, 0);
-    if constexpr (C::kQScale && C::NP == 2)  // (the factors; later units': with XBAR)
-      asm volatile("bar.sync 1, %0;" ::"n"(C::NP * 128) : "memory");
-    if (!q_ok) return;
+    float factor = 1.f;  // (kQScale) of the row's scores
+    if (!take_rows(tmem, lanes, wg, tid, 0, factor)) return;
     // (The unit's description stays in its slot while it is worked on, and what a row
     // sees is worked out where a tile is partly seen and at the end: registers hold
     // the row's scores.)
@@ -759,8 +749,7 @@ struct RowsCta {
         full_lo = prm.window > 0 ? (prm.masks ? U.L - prm.window : first + i1 - prm.window + 1) : 0;
       }
       float mref = -INFINITY, l = 0.f, sl2 = sl2_all;
-      if constexpr (C::kQScale)
-        sl2 = fmaxf(sl2 * reinterpret_cast<const volatile float*>(smem + C::OFF_QSCALE)[(k & 1) * 128 + row], 1.17549435e-38f);
+      if constexpr (C::kQScale) sl2 = fmaxf(sl2 * factor, 1.17549435e-38f);
       const int t0 = U.t0, t1 = U.t1, sink_blocks = U.sink_blocks, skip = U.skip;
       bool ok = true;
       for (int i = C::NP == 2 ? wg : 0; i < nt && ok; i += C::NP) {
@@ -874,7 +863,7 @@ struct RowsCta {
       if (!ok) break;
       // ---- the end of the unit: the next one's Q, then join the pipelines' states (one row
       // a thread) and write.
-      if (wg == 0 && !take_rows(tmem, lanes, tid, k + 1)) break;
+      if (!take_rows(tmem, lanes, wg, tid, k + 1, factor)) break;
       const uint32_t ob = tmem + lanes + C::O_COL;
       const RowView v = view();
       // The last tile of each pipeline (-1: none), whose buffers are free when their
@@ -933,15 +922,9 @@ struct RowsCta {
         const bool single = U.np == 1;
         const size_t sh0 = (size_t)U.s * prm.H + U.h0, sh = sh0 + row;
         const int orow = mine ? (int)out_row<kView>(prm, U.s, U.h0 + row) : 0;  // (below 2^25: 256 sequences)
-        // Where the lane stores: its piece of four dims of each of its four lanes' rows.
-        uint8_t* to[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = (row & ~3) + i, ri = __shfl_sync(0xffffffffu, orow, (lane & ~3) + i);
-          to[i] = r >= nh ? nullptr
-                  : single  ? static_cast<uint8_t*>(prm.out) + ((size_t)ri * D + (lane & 3) * 4) * sizeof(T)
-                            : reinterpret_cast<uint8_t*>(prm.ws_o + ((sh0 + r) * prm.Pmax + U.p) * D + (lane & 3) * 4);
-        }
+        uint8_t* to = single ? static_cast<uint8_t*>(prm.out) + (size_t)orow * D * sizeof(T)
+                             : reinterpret_cast<uint8_t*>(prm.ws_o + ((sh0 + row) * prm.Pmax + U.p) * D);
+        const bool wide = (reinterpret_cast<uintptr_t>(single ? prm.out : static_cast<void*>(prm.ws_o)) & 31) == 0;
         // (Of a pipeline without a tile, O holds anything: it is read, and not used.)
         constexpr int NCH = (D / 2 % 32 == 0 && C::NP == 2) || C::NP == 1 ? 2 : 1;  // pieces of 16 dims at a time
 #pragma unroll 1
@@ -952,31 +935,43 @@ struct RowsCta {
             float ab[64];
             tmem_get64(ob + c0, ob + C::O_STEP + c0, ab);
 #pragma unroll
-            for (int q = 0; q < 32; ++q) o[q / 16][q % 16] = has1 ? fmaf(ab[32 + q], f1, ab[q] * f0) : ab[q] * f0;
+            for (int q = 0; q < 32; ++q) o[q / 16][q % 16] = ab[q] * f0;
+            if (has1) {
+#pragma unroll
+              for (int q = 0; q < 32; ++q) o[q / 16][q % 16] = fmaf(ab[32 + q], f1, o[q / 16][q % 16]);
+            }
           } else {
             float ab[32];
             tmem_get32(ob + c0, ob + (C::NP == 2 ? C::O_STEP : 16) + c0, ab);
 #pragma unroll
-            for (int q = 0; q < NCH * 16; ++q)
-              o[q / 16][q % 16] = C::NP == 2 && has1 ? fmaf(ab[(16 + q) % 32], f1, ab[q] * f0) : ab[q] * f0;
+            for (int q = 0; q < NCH * 16; ++q) o[q / 16][q % 16] = ab[q] * f0;
+            if (C::NP == 2 && has1) {
+#pragma unroll
+              for (int q = 0; q < 16; ++q) o[0][q] = fmaf(ab[(16 + q) % 32], f1, o[0][q]);
+            }
           }
           if (!some || !has0) {
 #pragma unroll
             for (int q = 0; q < NCH * 16; ++q) o[q / 16][q % 16] = 0.f;
           }
-          // Four lanes exchange their rows' pieces of four dims: then lane q of the four has
-          // piece q of each of their rows, and they store 16 dims of one row at a time (a
-          // lane a row touched 32 lines with every store).
-#pragma unroll
-          for (int h = 0; h < NCH; ++h) transpose4(o[h], lane);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            if (!to[i]) continue;
+          if (mine) {
+            // (32 bytes of its row a lane: whole sectors.)
 #pragma unroll
             for (int h = 0; h < NCH; ++h) {
-              const float4 x = make_float4(o[h][4 * i], o[h][4 * i + 1], o[h][4 * i + 2], o[h][4 * i + 3]);
-              if (single) store4<T>(reinterpret_cast<T*>(to[i]) + c0 + 16 * h, x);
-              else st_f4_policy(reinterpret_cast<float4*>(to[i]) + (c0 + 16 * h) / 4, x, pol_keep);
+              if (single) {
+                uint32_t w[8];
+#pragma unroll
+                for (int q = 0; q < 8; ++q) w[q] = F16Traits<T>::pack(o[h][2 * q], o[h][2 * q + 1]);
+                st_32b(to + (c0 + 16 * h) * sizeof(T), w, wide);
+              } else {
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                  uint32_t w[8];
+#pragma unroll
+                  for (int q = 0; q < 8; ++q) w[q] = __float_as_uint(o[h][8 * x + q]);
+                  st_32b(to + (c0 + 16 * h + 8 * x) * 4, w, wide);
+                }
+              }
             }
           }
         }
@@ -994,9 +989,12 @@ struct RowsCta {
         }
         if (mine && d_lo == 0) {
           const float mn = some ? mref * kLn2 : -INFINITY;
-          st_f32_policy(prm.ws_m + sh * prm.Pmax + U.p, mn, pol_keep);
-          st_f32_policy(prm.ws_l + sh * prm.Pmax + U.p, some ? l : 0.f, pol_keep);
-          if (single && prm.lse) prm.lse[orow] = some ? mn + logf(l) : -INFINITY;
+          if (!single) {
+            st_f32_policy(prm.ws_m + sh * prm.Pmax + U.p, mn, pol_keep);
+            st_f32_policy(prm.ws_l + sh * prm.Pmax + U.p, some ? l : 0.f, pol_keep);
+          } else if (prm.lse) {
+            prm.lse[orow] = some ? mn + logf(l) : -INFINITY;
+          }
         }
         __syncwarp();
       }
@@ -1039,8 +1037,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) pa_rows_kernel(const __grid_con
       mbar_init(cta.bar(C::PVDONE + i), 1);
     }
     mbar_init(cta.bar(C::QSTAGED), C::LOADERS);
-    mbar_init(cta.bar(C::QTAKEN), 128);
-    mbar_init(cta.bar(C::QREADY), 128);
+    mbar_init(cta.bar(C::QTAKEN), C::NP * 128);
+    mbar_init(cta.bar(C::QREADY), C::NP * 128);
     mbar_init(cta.bar(C::QFREE), 1);
     mbar_init(cta.bar(C::OFREE), C::NP * 128);
     mbar_init(cta.bar(C::XBAR), C::NP * 128);

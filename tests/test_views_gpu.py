@@ -408,3 +408,24 @@ def test_many_rows_that_see_nan_codes():
         ref, _, bound = attend64(q, kc, clean, bt, lens, 0.1, 200, 0, None, K_SCALE, V_SCALE)
         fine = ~odd[None, :, None].expand(1, n, H, D)
         assert bool(((got.double() - ref).abs() <= bound)[fine].all())
+
+
+@pytest.mark.parametrize("P", [128, 4096])
+def test_many_rows_into_tensors_aligned_to_16_bytes(P):
+    """An output and a workspace that start 16 bytes past a 32-byte boundary."""
+    n, H, KH, D, BS = 40, 4, 1, 80, 16
+    for cache in ("same", "e4m3"):
+        case = make(2, torch.bfloat16, cache, n, H, KH, D, BS, [n, 300], 150, 2)
+        d = [t.to("cuda") for t in case]
+        out = torch.full((d[0].numel() + 8,), float("nan"), dtype=d[0].dtype, device="cuda")[8:].view(d[0].shape)
+        size = binding.view_workspace_bytes(2, n, H, KH, D, d[3].shape[1], BS, P, 150, 2)
+        ws = torch.full((size + 16,), 0x7F, dtype=torch.uint8, device="cuda")[16:]
+        assert out.data_ptr() % 32 == 16 and ws.data_ptr() % 32 == 16
+        if cache == "e4m3":
+            binding.pa_decode_v2_window_fp8(out, *d, 0.1, 150, 2, k_scale=K_SCALE, v_scale=V_SCALE, partition_size=P,
+                                            workspace=ws)
+        else:
+            binding.pa_decode_v2_window(out, *d, 0.1, 150, 2, partition_size=P, workspace=ws)
+        assert binding.device_status(ws) == binding.PA_OK
+        ref, _, bound = attend64(*case, 0.1, 150, 2, None, K_SCALE, V_SCALE)
+        assert bool(((out.cpu().double() - ref).abs() <= bound).all())
