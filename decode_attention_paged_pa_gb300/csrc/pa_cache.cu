@@ -42,6 +42,7 @@ struct WriteParams {
   long long total;           // slots in the pool
   float scale[2];
   int N, KH, D, BS, T;       // T: rows per CTA
+  int shift;                 // BS = 1 << shift
 };
 
 constexpr int kWriteThreads = 256;
@@ -49,40 +50,122 @@ constexpr int kWriteThreads = 256;
 // Source elements of the rows.
 enum Source { kCopy, kHalf, kBfloat, kFloat };
 
-// 16 bytes of a row as they are held in the cache: copied, or 8 (4) elements
-// rounded to E4M3 (the quotient by the scale in fp32, to nearest even, kept within
-// +-448; NaN stays NaN).
+// E4M3 codes of x / scale: the quotient in fp32, to nearest even, rounded again to
+// nearest even and kept within +-448; NaN stays NaN.  The quotient comes from x times the
+// reciprocal in two steps: the first is within an ulp, and from one that is, with the
+// reciprocal rounded to nearest, the remainder times it gives the rounded quotient
+// (P. Markstein, "Computation of elementary functions on the IBM RISC System/6000
+// processor", 1990).  Two elements an instruction; with x and the reciprocal negated, a
+// zero keeps its sign.  Where a quotient is 1024 or more, or the remainders could leave
+// fp32's exact range, the division itself.  (One division for each element, and one for
+// each index, took 60 us where this takes 45: 24 prompts of 1100 tokens, 8 kv heads of
+// 128 dims, fp16.)
+struct Divisor {
+  uint64_t s2, i2;  // the scale (which is positive) and -1 / scale, twice each
+  float scale, most;
+  __device__ __forceinline__ static uint64_t both(float a, float b) {
+    uint64_t x;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a), "f"(b));
+    return x;
+  }
+  __device__ __forceinline__ explicit Divisor(float s) {
+    const float inv = -1.f / s;
+    s2 = both(s, s);
+    i2 = both(inv, inv);
+    scale = s;
+    most = s >= 0x1p-64f && s <= 0x1p64f ? 1024.f * s : -1.f;
+  }
+};
+__device__ __forceinline__ uint32_t e4m3x2_of(float a, float b) {
+  return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+}
+// `a` and `b`: -x of two elements.
+__device__ __forceinline__ uint32_t e4m3x2_of(float a, float b, const Divisor& s) {
+  const auto fma2 = [](uint64_t x, uint64_t y, uint64_t z) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(x), "l"(y), "l"(z));
+    return d;
+  };
+  const uint64_t x = Divisor::both(a, b);
+  uint64_t q;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(q) : "l"(x), "l"(s.i2));
+#pragma unroll
+  for (int i = 0; i < 2; ++i) q = fma2(fma2(q, s.s2, x), s.i2, q);
+  float qa, qb;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(qa), "=f"(qb) : "l"(q));
+  return e4m3x2_of(qa, qb);
+}
+template <typename T>
+__device__ __noinline__ uint2 e4m3x8_divided(uint4 x, float scale) {
+  float f[8];
+  unpack_chunk<T>(x, f);
+  uint32_t w[2] = {0, 0};
+  for (int i = 0; i < 4; ++i)
+    w[i / 2] |= e4m3x2_of(__fdiv_rn(f[2 * i], scale), __fdiv_rn(f[2 * i + 1], scale)) << (16 * (i & 1));
+  return make_uint2(w[0], w[1]);
+}
+__device__ __noinline__ uint32_t e4m3x4_divided(uint4 x, float s) {
+  return e4m3x2_of(__fdiv_rn(__uint_as_float(x.x), s), __fdiv_rn(__uint_as_float(x.y), s)) |
+         e4m3x2_of(__fdiv_rn(__uint_as_float(x.z), s), __fdiv_rn(__uint_as_float(x.w), s)) << 16;
+}
+// (The largest magnitude of eight elements, NaN if there is one: two of them.)
+__device__ __forceinline__ float2 most_of(const uint4& x, __half) {
+  const __half2* h = reinterpret_cast<const __half2*>(&x);
+  return __half22float2(__hmax2_nan(__hmax2_nan(__habs2(h[0]), __habs2(h[1])), __hmax2_nan(__habs2(h[2]), __habs2(h[3]))));
+}
+__device__ __forceinline__ float2 most_of(const uint4& x, __nv_bfloat16) {
+  const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&x);
+  return __bfloat1622float2(
+      __hmax2_nan(__hmax2_nan(__habs2(h[0]), __habs2(h[1])), __hmax2_nan(__habs2(h[2]), __habs2(h[3]))));
+}
+template <typename T>
+__device__ __forceinline__ uint2 e4m3x8_of(const uint4& x, const Divisor& s) {
+  const float2 m = most_of(x, T());
+  if (!(m.x < s.most && m.y < s.most)) return e4m3x8_divided<T>(x, s.scale);
+  float f[8];
+  constexpr uint32_t flip = 0x80008000u;
+  unpack_chunk<T>(make_uint4(x.x ^ flip, x.y ^ flip, x.z ^ flip, x.w ^ flip), f);
+  return make_uint2(e4m3x2_of(f[0], f[1], s) | e4m3x2_of(f[2], f[3], s) << 16,
+                    e4m3x2_of(f[4], f[5], s) | e4m3x2_of(f[6], f[7], s) << 16);
+}
+// 16 bytes of a row as they are held in the cache: copied, or 8 (4) elements rounded.
 template <int SRC>
 struct Piece {
   using V = uint4;
-  static __device__ __forceinline__ V make(const uint4& x, float) { return x; }
+  static __device__ __forceinline__ V make(const uint4& x, const Divisor&) { return x; }
 };
-__device__ __forceinline__ uint32_t e4m3x2_of(float a, float b, float scale) {
-  return __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(a, scale), __fdiv_rn(b, scale)), __NV_SATFINITE, __NV_E4M3);
-}
-template <typename T>
-__device__ __forceinline__ uint2 e4m3x8_of(const uint4& x, float scale) {
-  float f[8];
-  unpack_chunk<T>(x, f);
-  return make_uint2(e4m3x2_of(f[0], f[1], scale) | e4m3x2_of(f[2], f[3], scale) << 16,
-                    e4m3x2_of(f[4], f[5], scale) | e4m3x2_of(f[6], f[7], scale) << 16);
-}
 template <>
 struct Piece<kHalf> {
   using V = uint2;
-  static __device__ __forceinline__ V make(const uint4& x, float s) { return e4m3x8_of<__half>(x, s); }
+  static __device__ __forceinline__ V make(const uint4& x, const Divisor& s) { return e4m3x8_of<__half>(x, s); }
 };
 template <>
 struct Piece<kBfloat> {
   using V = uint2;
-  static __device__ __forceinline__ V make(const uint4& x, float s) { return e4m3x8_of<__nv_bfloat16>(x, s); }
+  static __device__ __forceinline__ V make(const uint4& x, const Divisor& s) { return e4m3x8_of<__nv_bfloat16>(x, s); }
 };
 template <>
 struct Piece<kFloat> {
   using V = uint32_t;
-  static __device__ __forceinline__ V make(const uint4& x, float s) {
-    return e4m3x2_of(__uint_as_float(x.x), __uint_as_float(x.y), s) |
-           e4m3x2_of(__uint_as_float(x.z), __uint_as_float(x.w), s) << 16;
+  static __device__ __forceinline__ V make(const uint4& x, const Divisor& s) {
+    const float a = __uint_as_float(x.x), b = __uint_as_float(x.y), c = __uint_as_float(x.z), d = __uint_as_float(x.w);
+    if (!(fabsf(a) < s.most && fabsf(b) < s.most && fabsf(c) < s.most && fabsf(d) < s.most))
+      return e4m3x4_divided(x, s.scale);
+    return e4m3x2_of(-a, -b, s) | e4m3x2_of(-c, -d, s) << 16;
+  }
+};
+
+// i, i + kWriteThreads, .. as a * n + b: one division for all.
+struct Walk {
+  int a, b, da, db, n;
+  __device__ __forceinline__ Walk(int i, int n_) : a(i / n_), b(i - a * n_), da(kWriteThreads / n_), db(kWriteThreads - da * n_), n(n_) {}
+  __device__ __forceinline__ void next() {
+    a += da;
+    b += db;
+    if (b >= n) {
+      b -= n;
+      ++a;
+    }
   }
 };
 
@@ -111,13 +194,14 @@ __device__ __forceinline__ void gather_dim(const uint32_t (&w)[CT], int i, uint3
 }
 
 template <int SRC, int E, int CT>
-__global__ void __launch_bounds__(kWriteThreads) cache_write_kernel(const __grid_constant__ WriteParams p) {
+__global__ void __launch_bounds__(kWriteThreads, 4) cache_write_kernel(const __grid_constant__ WriteParams p) {
   using PV = typename Piece<SRC>::V;
   using EL = typename Elem<E>::T;
   constexpr int SE = SRC == kCopy ? E : SRC == kFloat ? 4 : 2;  // bytes of a row's element
   constexpr int X = 16 / E, DPW = 4 / E;                        // dims of a key chunk, of a 4-byte word
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ int s_n, s_end;  // chunks, and the end of the rows that they need
+  __shared__ int s_n, s_end;     // chunks, and the end of the rows that they need
+  __shared__ uint32_t s_next[4];  // bit i: row i follows the one before in its chunk
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x;
@@ -133,47 +217,81 @@ __global__ void __launch_bounds__(kWriteThreads) cache_write_kernel(const __grid
   }
   const int D = p.D, BS = p.BS, T = p.T, kv = blockIdx.y;
   const int r0 = blockIdx.x * T, rows = min(T + CT - 1, p.N - r0);  // (r0 < N < 2^31 - T - CT)
-  const int pitch = D * E + 16;
+  const int pitch = D * E + 16, ppr = D * SE / 16;                  // 16-byte pieces per row
   uint8_t* tile[2] = {smem, smem + (size_t)(T + CT - 1) * pitch};
-  long long* slot = reinterpret_cast<long long*>(smem + 2 * (size_t)(T + CT - 1) * pitch);  // of rows r0 - 1 ..
-  int4* chunk = reinterpret_cast<int4*>(slot + T + CT);  // [T] first row, rows, block, offset in the block
-  for (int i = tid; i < rows + 1; i += kWriteThreads) {
-    const int r = r0 - 1 + i;
-    const long long s = r >= 0 ? p.slots[r] : -1;
-    slot[i] = s >= 0 && s < p.total ? s : -2;  // (-2 and its successor are no slots)
+  int4* chunk = reinterpret_cast<int4*>(smem + 2 * (size_t)(T + CT - 1) * pitch);  // [T] first row, rows, block, offset in the block
+  // The slots of the tile's rows, and on their way with them the rows' first pieces.
+  long long s = -2, before = -2;  // (-2 and its successor are no slots)
+  if (tid < rows) {
+    s = p.slots[r0 + tid];
+    if (r0 + tid > 0) before = p.slots[r0 + tid - 1];
+  }
+  constexpr int LB = 4;  // loads in flight, of keys and of values
+  const uint8_t* src[2];
+#pragma unroll
+  for (int w = 0; w < 2; ++w) src[w] = p.row[w] + (size_t)r0 * p.stride[w] + (size_t)kv * D * SE;
+  Walk at(tid, ppr);
+  uint4 x[2][LB];
+  int where[LB];
+  const int own = min(rows, T);
+#pragma unroll
+  for (int u = 0; u < LB; ++u) {
+    where[u] = at.a < own ? at.a * pitch + at.b * (int)sizeof(PV) : -1;
+    if (where[u] >= 0)
+#pragma unroll
+      for (int w = 0; w < 2; ++w) x[w][u] = *reinterpret_cast<const uint4*>(src[w] + (size_t)at.a * p.stride[w] + at.b * 16);
+    at.next();
   }
   if (tid == 0) s_n = s_end = 0;
-  __syncthreads();
-  if (tid < T && tid < rows) {
-    const long long s = slot[tid + 1];
-    if (s >= 0 && !(slot[tid] + 1 == s && s % CT != 0)) {
-      int n = 1;
-      while (tid + n < rows && (s + n) % CT != 0 && slot[tid + 1 + n] == s + n) ++n;
-      const int k = atomicAdd(&s_n, 1);
-      const long long blk = s / BS;
-      chunk[k] = make_int4(tid, n, (int)blk, (int)(s - blk * BS));
-      atomicMax(&s_end, tid + n);
-    }
+  if (s < 0 || s >= p.total) s = -2;
+  if (before < 0 || before >= p.total) before = -2;
+  const bool follows = s >= 0 && before + 1 == s && s % CT != 0;
+  if (tid < 128) {
+    const uint32_t m = __ballot_sync(0xffffffffu, follows);
+    if ((tid & 31) == 0) s_next[tid >> 5] = m;
   }
   __syncthreads();
-  const int nch = s_n, need = s_end, ppr = D * SE / 16;  // 16-byte pieces per row
+  if (tid < T && s >= 0 && !follows) {
+    const int i = tid + 1;  // (T is 64 at most)
+    const int n = 1 + __ffs(~__funnelshift_r(s_next[i >> 5], s_next[(i >> 5) + 1], i & 31)) - 1;
+    const int k = atomicAdd(&s_n, 1);
+    const int blk = (int)((unsigned long long)s >> p.shift);
+    chunk[k] = make_int4(tid, n, blk, (int)(s - ((long long)blk << p.shift)));
+    atomicMax(&s_end, tid + n);
+  }
+  __syncthreads();
+  const int nch = s_n, need = s_end;
   if (nch == 0) return;
   // (At least one row in front may belong to the CTA before: it is loaded for nothing.)
+  const Divisor div[2] = {Divisor(p.scale[0]), Divisor(p.scale[1])};
 #pragma unroll
-  for (int w = 0; w < 2; ++w) {
-    const uint8_t* src = p.row[w] + (size_t)r0 * p.stride[w] + (size_t)kv * D * SE;
-#pragma unroll 4
-    for (int i = tid; i < need * ppr; i += kWriteThreads) {
-      const int r = i / ppr, q = i - r * ppr;
-      const uint4 x = *reinterpret_cast<const uint4*>(src + (size_t)r * p.stride[w] + q * 16);
-      reinterpret_cast<PV*>(tile[w] + r * pitch)[q] = Piece<SRC>::make(x, p.scale[w]);
+  for (int u = 0; u < LB; ++u)
+    if (where[u] >= 0)
+#pragma unroll
+      for (int w = 0; w < 2; ++w) *reinterpret_cast<PV*>(tile[w] + where[u]) = Piece<SRC>::make(x[w][u], div[w]);
+  const int rest = tid + min(own * ppr, LB * kWriteThreads);  // pieces before it are there
+  at = Walk(rest, ppr);
+  for (int i = rest; i < need * ppr; i += LB * kWriteThreads) {
+#pragma unroll
+    for (int u = 0; u < LB; ++u) {
+      where[u] = at.a < need ? at.a * pitch + at.b * (int)sizeof(PV) : -1;
+      if (where[u] >= 0)
+#pragma unroll
+        for (int w = 0; w < 2; ++w) x[w][u] = *reinterpret_cast<const uint4*>(src[w] + (size_t)at.a * p.stride[w] + at.b * 16);
+      at.next();
     }
+#pragma unroll
+    for (int u = 0; u < LB; ++u)
+      if (where[u] >= 0)
+#pragma unroll
+        for (int w = 0; w < 2; ++w) *reinterpret_cast<PV*>(tile[w] + where[u]) = Piece<SRC>::make(x[w][u], div[w]);
   }
   __syncthreads();
   // Keys: 16 bytes a token and chunk of dims, tokens next to each other.
   const int DC = D / X;
-  for (int i = tid; i < nch * DC * CT; i += kWriteThreads) {
-    const int j = i % CT, kc = i / CT, k = kc / DC, c = kc - k * DC;
+  Walk kat(tid, DC * CT);
+  for (; kat.a < nch; kat.next()) {
+    const int k = kat.a, j = kat.b % CT, c = kat.b / CT;
     const int4 ch = chunk[k];
     if (j >= ch.y) continue;
     *reinterpret_cast<uint4*>(p.cache[0] + ((((size_t)ch.z * p.KH + kv) * DC + c) * BS + ch.w + j) * 16) =
@@ -181,8 +299,10 @@ __global__ void __launch_bounds__(kWriteThreads) cache_write_kernel(const __grid
   }
   // Values: 4 / E dims a thread.
   const int DW = D / DPW;
-  for (int i = tid; i < nch * DW; i += kWriteThreads) {
-    const int k = i / DW, g = i - k * DW;
+  const bool wide = (reinterpret_cast<uintptr_t>(p.cache[1]) & 31) == 0;
+  Walk vat(tid, DW);
+  for (; vat.a < nch; vat.next()) {
+    const int k = vat.a, g = vat.b;
     const int4 ch = chunk[k];
     const int n = ch.y;
     uint8_t* dst = p.cache[1] + ((((size_t)ch.z * p.KH + kv) * D + g * DPW) * BS + ch.w) * E;
@@ -191,17 +311,27 @@ __global__ void __launch_bounds__(kWriteThreads) cache_write_kernel(const __grid
       uint32_t w[CT];
 #pragma unroll
       for (int j = 0; j < CT; ++j) w[j] = *reinterpret_cast<const uint32_t*>(src + j * pitch);
+      constexpr int CW = CT * E / 4;  // words of a dim
+      if (CW == 4 && BS == CT) {
+        // Blocks of one chunk: two dims are 32 bytes.
 #pragma unroll
-      for (int d = 0; d < DPW; ++d) {
-        uint32_t o[CT * E / 4];
-        gather_dim<E, CT>(w, d, o);
-        uint8_t* to = dst + (size_t)d * BS * E;
-        if constexpr (CT * E == 8) {
-          *reinterpret_cast<uint2*>(to) = make_uint2(o[0], o[1]);
-        } else {
+        for (int d = 0; d < DPW; d += 2) {
+          uint32_t o[2][CW], both[8];
+          gather_dim<E, CT>(w, d, o[0]);
+          gather_dim<E, CT>(w, d + (DPW > 1), o[1]);
 #pragma unroll
-          for (int q = 0; q < CT * E / 16; ++q)
-            reinterpret_cast<uint4*>(to)[q] = make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+          for (int q = 0; q < 8; ++q) both[q] = o[q / CW % 2][q % CW];
+          st_32b(dst + (size_t)d * BS * E, both, wide);
+        }
+      } else {
+#pragma unroll
+        for (int d = 0; d < DPW; ++d) {
+          uint32_t o[CW];
+          gather_dim<E, CT>(w, d, o);
+          uint8_t* to = dst + (size_t)d * BS * E;
+          if constexpr (CW == 8) st_32b(to, o, wide);
+          else if constexpr (CW == 4) *reinterpret_cast<uint4*>(to) = make_uint4(o[0], o[1], o[2], o[3]);
+          else *reinterpret_cast<uint2*>(to) = make_uint2(o[0], o[1]);
         }
       }
     } else {
@@ -216,13 +346,12 @@ __global__ void __launch_bounds__(kWriteThreads) cache_write_kernel(const __grid
 template <int SRC, int E, int CT>
 cudaError_t launch_write(const WriteParams& prm, cudaStream_t st) {
   WriteParams p = prm;
-  // Rows per CTA: as many as still give every SM four CTAs, 2 to 64 (even: the
-  // chunks in shared memory start on 16 bytes).
+  // Rows per CTA: as many as still give every SM four CTAs, 2 to 64.
   const long long want = 4ll * device_sm_count();
   p.T = 64;
   while (p.T > 2 && ((long long)p.N + p.T - 1) / p.T * p.KH < want) p.T /= 2;
   const size_t rows = (size_t)p.T + CT - 1;
-  const size_t smem = 2 * rows * (p.D * E + 16) + (p.T + CT) * sizeof(long long) + p.T * sizeof(int4);
+  const size_t smem = 2 * rows * (p.D * E + 16) + p.T * sizeof(int4);
   const long long tiles = ((long long)p.N + p.T - 1) / p.T;
   static std::atomic<uint64_t> opted_in{0};
   int dev = 0;
@@ -419,6 +548,7 @@ extern "C" int pa_cache_write(void* key_cache, void* value_cache, const void* ke
   p.KH = num_kv_heads;
   p.D = D;
   p.BS = BS;
+  p.shift = BS == 8 ? 3 : BS == 16 ? 4 : BS == 32 ? 5 : 6;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (!fp8) e = E == 2 ? by_block<kCopy, 2>(p, st) : by_block<kCopy, 4>(p, st);

@@ -140,6 +140,17 @@ __device__ __forceinline__ void st_f4_policy(float4* dst, const float4& v, uint6
                "f"(v.z), "f"(v.w), "l"(policy)
                : "memory");
 }
+// 32 bytes, by one store where `wide` says that they are aligned to it.
+__device__ __forceinline__ void st_32b(uint8_t* at, const uint32_t (&w)[8], bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(at)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    reinterpret_cast<uint4*>(at)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
 __device__ __forceinline__ void st_f32_policy(float* dst, float v, uint64_t policy) {
   asm volatile("st.global.L2::cache_hint.f32 [%0], %1, %2;" ::"l"(dst), "f"(v), "l"(policy) : "memory");
 }

@@ -645,18 +645,6 @@ struct RowsCta {
     }
   }
 
-  // 32 bytes, by one store where `wide` says that they are aligned to it.
-  static __device__ __forceinline__ void st_32b(uint8_t* at, const uint32_t (&w)[8], bool wide) {
-    if (wide) {
-      asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at), "r"(w[0]), "r"(w[1]), "r"(w[2]),
-                   "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-                   : "memory");
-    } else {
-      reinterpret_cast<uint4*>(at)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-      reinterpret_cast<uint4*>(at)[1] = make_uint4(w[4], w[5], w[6], w[7]);
-    }
-  }
-
   // The staged Q of unit k into tensor memory (a row a thread, the pipelines' warpgroups
   // in turn), once the products with the one before are complete.  A negative scale's sign goes
   // with it: the softmax works with one that is not negative.

@@ -1,6 +1,8 @@
 """Slot maps, tree masks, cache writes and accepted paths against plain Python
 restatements: whole numbers and copied values equal, E4M3 codes equal to torch's
 rounding of the quotient."""
+import math
+
 import pytest
 import torch
 
@@ -226,6 +228,38 @@ def test_write_rounds_every_pattern():
         kc, vc = caches(3, 32, 2, 64, 16, torch.uint8)
         for ks, vs in ((1.0, 0.5), (0.37, 3.0), (448.0, 1e-3)):
             check_write(kc, vc, x, x.flip(0), torch.arange(512, dtype=torch.int64), ks, vs)
+
+
+def test_write_divides_exactly():
+    """Scales that are powers of two and not, tiny and huge ones; zeros of either
+    sign, infinities and NaN; rows of every type."""
+    kc, vc = caches(4, 8, 2, 64, 16, torch.uint8)
+    g = torch.Generator().manual_seed(2)
+    for dtype in T.values():
+        for ks, vs in ((0.3, 0.7), (1e-30, 1e-25), (3e25, 0.0625), (448.0, 1e-3)):
+            x = [(torch.randn((100, 2, 64), generator=g) * min(abs(s) * 40, 1e4)).to(dtype) for s in (ks, vs)]
+            for t in x:
+                t[::7, 0, 5], t[::9, 1, 6], t[3, 0, 7], t[4, 1, 8], t[5, 0, 9] = 0.0, -0.0, math.inf, -math.inf, math.nan
+            check_write(kc, vc, *x, torch.arange(3, 103, dtype=torch.int64), ks, vs)
+
+
+@pytest.mark.parametrize("dtype,cache,BS", [("fp16", None, 16), ("fp32", None, 8), ("bf16", torch.uint8, 16),
+                                            ("fp16", torch.uint8, 32), ("fp32", torch.uint8, 64)])
+def test_write_into_caches_aligned_to_16_bytes(dtype, cache, BS):
+    kc, vc = caches(4, 6, 2, 80, BS, cache or T[dtype])
+    key, value = (torch.randn((3 * BS, 2, 80), generator=torch.Generator().manual_seed(i)).to(T[dtype]) for i in (1, 2))
+    slots = torch.arange(5, 5 + 3 * BS, dtype=torch.int64)
+    want = plain_write(kc, vc, key, value, slots, 1.0, 1.0)
+    got = []
+    for t in (kc, vc):
+        size = t.numel() * t.element_size()
+        room = torch.zeros(size + 16, dtype=torch.uint8, device=DEV)[16:]
+        assert room.data_ptr() % 32 == 16
+        got.append(room.view(t.dtype).view(t.shape))
+        got[-1].copy_(t)
+    assert status(binding.pa_cache_write(*got, key.to(DEV), value.to(DEV), slots.to(DEV))) == binding.PA_OK
+    for a, b in zip(got, want):
+        assert torch.equal(a.cpu().view(torch.uint8), b.view(torch.uint8))
 
 
 def test_write_edges():
