@@ -537,11 +537,14 @@ struct RowsCta {
 
   // Eight E4M3 codes as fp16 (exact).
   static __device__ __forceinline__ uint4 widen8(uint32_t lo, uint32_t hi) {
-    const auto two = [](uint32_t c) {
-      const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(c & 0xffffu), __NV_E4M3);
-      return (uint32_t)h.x | (uint32_t)h.y << 16;
-    };
-    return make_uint4(two(lo), two(lo >> 16), two(hi), two(hi >> 16));
+    uint4 x;
+    asm("{\n\t.reg .b16 a, b, c, d;\n\t"
+        "mov.b32 {a, b}, %4;\n\tmov.b32 {c, d}, %5;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %2, c;\n\tcvt.rn.f16x2.e4m3x2 %3, d;\n\t}"
+        : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+        : "r"(lo), "r"(hi));
+    return x;
   }
   // Value codes of `n` tokens and anything behind them: what is past them, and NaN codes
   // (0x7f, 0xff; `found`), become zeros.
@@ -583,7 +586,7 @@ struct RowsCta {
         constexpr int PIECES = C::TN * D / 16;
         if (!value) {
           // [block][D/16][BS][16]: a token's 16 dims are two pieces of the tile's [D/8][64][8].
-#pragma unroll 4
+#pragma unroll 2
           for (int x = lane; x < PIECES; x += 32) {
             const int t = x % BS, c = x / BS % (D / 16), b = x / (BS * (D / 16));
             const uint4 w = from[x];
@@ -593,17 +596,21 @@ struct RowsCta {
           }
         } else {
           // [block][D][BS]: 16 tokens of a dim (blocks of eight: eight tokens of two dims).
-#pragma unroll 4
+#pragma unroll 2
           for (int x = lane; x < PIECES; x += 32) {
             constexpr int RP = BS >= 16 ? BS / 16 : 1;  // pieces of a dim's row
             const int b = x / (BS * D / 16), y = x % (BS * D / 16);
             const int d = BS >= 16 ? y / RP : 2 * y, t = b * BS + (BS >= 16 ? y % RP * 16 : 0);
             uint4 w = from[x];
-            const int n = left - t, n2 = BS >= 16 ? n - 8 : n;
-            w.x = plain_codes(w.x, n, found);
-            w.y = plain_codes(w.y, n - 4, found);
-            w.z = plain_codes(w.z, n2, found);
-            w.w = plain_codes(w.w, n2 - 4, found);
+            constexpr uint32_t m7 = 0x7f7f7f7fu, one = 0x01010101u;
+            const uint32_t nan = ((w.x & m7) + one) | ((w.y & m7) + one) | ((w.z & m7) + one) | ((w.w & m7) + one);
+            if (left < C::TN || (nan & 0x80808080u)) {
+              const int n = left - t, n2 = BS >= 16 ? n - 8 : n;
+              w.x = plain_codes(w.x, n, found);
+              w.y = plain_codes(w.y, n - 4, found);
+              w.z = plain_codes(w.z, n2, found);
+              w.w = plain_codes(w.w, n2 - 4, found);
+            }
             *reinterpret_cast<uint4*>(to + value_chunk(d, t / 8)) = widen8(w.x, w.y);
             *reinterpret_cast<uint4*>(to + (BS >= 16 ? value_chunk(d, t / 8 + 1) : value_chunk(d + 1, t / 8))) =
                 widen8(w.z, w.w);
