@@ -922,11 +922,15 @@ def pa_tree_accept(new_lens, key_caches, value_caches, block_tables, seq_lens, a
         raise ValueError("as many value caches as key caches, and one at least")
     shape = _cache_shape("pa_tree_accept", key_caches[0], value_caches[0], dev)
     cdt = key_caches[0].dtype
-    for k, v in zip(key_caches[1:], value_caches[1:]):
-        if k.dtype is not cdt or k.shape != key_caches[0].shape or v.shape != value_caches[0].shape:
-            raise ValueError("caches must have one shape and type")
-        _need("key_cache", k, cdt, 5, dev)
-        _need("value_cache", v, cdt, 4, dev)
+    kshape, vshape = key_caches[0].shape, value_caches[0].shape
+    for name, caches, want in (("key_cache", key_caches, kshape), ("value_cache", value_caches, vshape)):
+        for t in caches[1:]:
+            # (One expression where all holds, as in _need.)
+            if not (t.__class__ is torch.Tensor and t.dtype is cdt and t.shape == want and t.get_device() == dev
+                    and t.is_contiguous()):
+                _need(name, t, cdt, len(want), dev)
+                if t.shape != want:
+                    raise ValueError("caches must have one shape and type")
     NB, KH, D, BS = shape
     _need("new_lens", new_lens, torch.int32, 1, dev)
     _need("block_tables", block_tables, torch.int32, 2, dev)

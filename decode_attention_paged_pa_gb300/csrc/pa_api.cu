@@ -311,17 +311,19 @@ int decode_impl(void* out, float* lse, const void* query, const void* key_cache,
   // fit a warp's ring).
   const bool kv4_pairs = kv4 && G * 2 <= kMmaGroup && KH % 2 == 0 && D <= 128 && BS <= 32;
   const int kvu = pairs || kv4_pairs ? 2 : 1;
-  // With many rows a unit the states of a partition are many too, and each unit has
-  // its start and end: partitions are taken together, in powers of two, as long as
-  // every SM can still have four units (16 nodes a sequence, 48 sequences of 3000
-  // tokens, partitions of 512: 218 us as they are, 168 with four together).
+  // View rows on the tensor cores: partitions are taken together, in powers of two, as long as every SM can
+  // still have three units (four with many rows a unit, whose lengths differ more): each
+  // has its start and end, and states that are joined.  (16 nodes a sequence, 48
+  // sequences of 3000 tokens, partitions of 512: 218 us as they were, 168 with eight
+  // together; one row, 128 sequences, a window of 1024: 108 us, 102 with two and 95 with
+  // four together, which is a unit for every two kv heads of a sequence.)
   int part = view && P > MB * BS ? MB * BS : P;
-  if (many) {
-    const long long cap = (long long)view_blocks(q_len, MB, BS, view->window, view->sinks) * BS;
-    const long long tiles = (long long)S * KH * ((G + gt - 1) / gt), want = 4ll * device_sm_count();
+  if (view && variant == PA_VARIANT_MMA) {
+    const int blocks = view_blocks(q_len, MB, BS, view->window, view->sinks);
+    const long long cap = (long long)blocks * BS, want = (many ? 4ll : 3ll) * device_sm_count();
+    const long long tiles = (long long)S * (KH / kvu) * ((G + gt - 1) / gt);
     while (part < cap && tiles * ((cap + 2ll * part - 1) / (2ll * part)) >= want) part *= 2;
-    if (!ws_layout(S, H, KH, D, view_blocks(q_len, MB, BS, view->window, view->sinks), BS, part, &w))
-      return PA_ERR_INVALID_ARG;
+    if (!ws_layout(S, H, KH, D, blocks, BS, part, &w)) return PA_ERR_INVALID_ARG;
   }
   const int hg_per_kv = (G + gt - 1) / gt;
   const int n_hg = KH * hg_per_kv / kvu;
