@@ -322,7 +322,9 @@ int decode_impl(void* out, float* lse, const void* query, const void* key_cache,
     const int blocks = view_blocks(q_len, MB, BS, view->window, view->sinks);
     const long long cap = (long long)blocks * BS, want = (many ? 4ll : 3ll) * device_sm_count();
     const long long tiles = (long long)S * (KH / kvu) * ((G + gt - 1) / gt);
-    while (part < cap && tiles * ((cap + 2ll * part - 1) / (2ll * part)) >= want) part *= 2;
+    long long joined = part;
+    while (joined < cap && tiles * ((cap + 2 * joined - 1) / (2 * joined)) >= want) joined *= 2;
+    part = (int)(joined < (long long)MB * BS ? joined : (long long)MB * BS);
     if (!ws_layout(S, H, KH, D, blocks, BS, part, &w)) return PA_ERR_INVALID_ARG;
   }
   const int hg_per_kv = (G + gt - 1) / gt;

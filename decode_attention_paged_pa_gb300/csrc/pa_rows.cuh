@@ -37,6 +37,17 @@
 // time; values of it that are not finite are cleared in shared memory (their
 // products with other rows' zero weights would be NaN), and the rows that do see
 // them get them added at the end of the unit.
+//
+// 8-bit caches: the ring of tiles is filled by warps that widen E4M3 codes to fp16 from a
+// ring of codes, into the layouts of a block of 64 tokens whatever the cache's block.
+//
+// Measured (32 heads over 8 of 128 dims; whole calls): 16 nodes of 48 sequences of 1001 to
+// 4999 tokens, bf16 131 us (of the cache's bytes: 82), fp16 116; 64 nodes of 16 sequences of
+// 2048 to 8192, bf16 159 (bytes 49, products 85 with two terms a weight), fp16 133; chunks of
+// 128 tokens over a window of 1024, fp16 99, E4M3 121 (products 27).  A tile takes about 1100
+// cycles (fp16) where its products are 530: what is left is the way from a tile's scores
+// through its weights to the buffer's next scores, three buffers for two warpgroups; and
+// 5700 cycles from a unit to the next one.
 #pragma once
 
 #include <type_traits>
