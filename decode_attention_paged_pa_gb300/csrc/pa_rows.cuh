@@ -42,9 +42,9 @@
 // ring of codes, into the layouts of a block of 64 tokens whatever the cache's block.
 //
 // Measured (32 heads over 8 of 128 dims; whole calls): 16 nodes of 48 sequences of 1001 to
-// 4999 tokens, bf16 131 us (of the cache's bytes: 82), fp16 116; 64 nodes of 16 sequences of
-// 2048 to 8192, bf16 159 (bytes 49, products 85 with two terms a weight), fp16 133; chunks of
-// 128 tokens over a window of 1024, fp16 99, E4M3 121 (products 27).  A tile takes about 1100
+// 4999 tokens, bf16 129 us (of the cache's bytes: 82), fp16 115; 64 nodes of 16 sequences of
+// 2048 to 8192, bf16 154 (bytes 49, products 85 with two terms a weight), fp16 132; chunks of
+// 128 tokens over a window of 1024, fp16 97, E4M3 121 (products 27).  A tile takes about 1100
 // cycles (fp16) where its products are 530: what is left is the way from a tile's scores
 // through its weights to the buffer's next scores, three buffers for two warpgroups; and
 // 5700 cycles from a unit to the next one.
@@ -105,9 +105,10 @@ struct RowsConfig {
            al16(kRowsMaxUnitSeqs * 2);
   }
   static constexpr int kFit = (int)((kRowsSmem - small(D_ > 128 ? 8 : 16) - QBYTES - NR * RSLOT) / SLOT);
-  // (8-bit caches: an even number, and NR a multiple of CW, so that a warp that widens
-  // codes is never two phases off at a slot.)
-  static constexpr int NS = (kFit < 16 ? kFit : 16) & (FP8_ ? ~1 : ~0);
+  // (An even number: keys have the slots of one parity within a unit, values those of the
+  // other, in the middle of it, so that who waits for one kind is a phase off at most.  And
+  // NR a multiple of CW, for the warps that widen codes.)
+  static constexpr int NS = (kFit < 16 ? kFit : 16) & ~1;
   static_assert(!FP8_ || (NR % (FP8_ ? CW : 1) == 0 && NS >= CW), "a warp's waits for a slot are a phase apart at most");
   static_assert(NS >= 2 * NBUF, "the ring holds the keys that are ahead and two tiles' values");
   // The score column of token t of group gi of eight of block bi.
@@ -393,13 +394,11 @@ struct RowsCta {
       }
       for (int i = 0, b = 0; i < nt; ++i, b = b + 1 < C::NBUF ? b + 1 : 0) {
         const uint32_t it = g + key_item(i);
-        // (The buffer's weights have been used; this wait comes first, so that the one for
-        // the slot is a phase off at most.)
-        if (i >= C::NBUF) {
+        ok = all(C::FULL + slot(it), phase(it), kRowsFull, (int)it);
+        if (ok && i >= C::NBUF) {  // the buffer's weights have been used
           ok = all(C::PVDONE + b, (par >> b) + (i / C::NBUF - 1), kRowsPv, i);
           tc_fence_after();
         }
-        if (ok) ok = all(C::FULL + slot(it), phase(it), kRowsFull, (int)it);
         if (!ok) break;
         if (elect_one()) {
           issue_scores(tmem, slot(it), b, id_s);
@@ -431,8 +430,8 @@ struct RowsCta {
       if (!all(C::OFREE, k + 1, kRowsOFree, (int)k)) break;  // the last unit's O is read
       for (int i = 0, b = 0; i < nt; ++i, b = b + 1 < C::NBUF ? b + 1 : 0) {
         const uint32_t it = g + value_item(i, nt);
-        ok = all(C::PREADY + b, par >> b, kRowsP, i);
-        if (ok) ok = all(C::FULL + slot(it), phase(it), kRowsFull, (int)it);
+        ok = all(C::FULL + slot(it), phase(it), kRowsFull, (int)it);
+        if (ok) ok = all(C::PREADY + b, par >> b, kRowsP, i);
         if (!ok) break;
         par ^= 1u << b;
         tc_fence_after();

@@ -429,3 +429,67 @@ def test_many_rows_into_tensors_aligned_to_16_bytes(P):
         assert binding.device_status(ws) == binding.PA_OK
         ref, _, bound = attend64(*case, 0.1, 150, 2, None, K_SCALE, V_SCALE)
         assert bool(((out.cpu().double() - ref).abs() <= bound).all())
+
+
+@pytest.mark.parametrize("cache", ["same", "e4m3"])
+def test_pools_past_32_bits(cache):
+    """Blocks whose first element lies past 2^31 elements (2^32 bytes for fp16): written by
+    their slots, read by one row, many rows and a tree, and moved by an accepted path."""
+    dev, BS, D, S, MB, n = torch.device("cuda"), 16, 64, 2, 40, 12
+    NB = (1 << 21) + 128
+    ct, x = (torch.uint8, 16) if cache == "e4m3" else (torch.float16, 8)
+    kc = torch.empty((NB, 1, D // x, BS, x), dtype=ct, device=dev)
+    vc = torch.empty((NB, 1, D, BS), dtype=ct, device=dev)
+    g = torch.Generator().manual_seed(12)
+    ids = torch.randperm(128, generator=g)[:S * MB] + (1 << 21)
+    ids[3], ids[45] = 5, (1 << 20) + 1
+    bt = ids.view(S, MB).to(torch.int32)
+    lens = [600, 333]
+    t = [torch.arange(L) for L in lens]
+    slots = torch.cat([bt[s, t[s] // BS].long() * BS + t[s] % BS for s in range(S)])
+    key, value = (torch.randn((sum(lens), 1, D), generator=g).half() for _ in range(2))
+    more = dict(k_scale=K_SCALE, v_scale=V_SCALE) if cache == "e4m3" else {}
+    ws = binding.pa_cache_write(kc, vc, key.to(dev), value.to(dev), slots.to(dev), **more)
+    assert binding.device_status(ws) == binding.PA_OK
+    small = torch.arange(S * MB).view(S, MB).to(torch.int32)
+    see = torch.stack([ancestors(tree_parents(s, n)) for s in range(S)])
+
+    def check_rows(q, lens, window, see):
+        pages = [c[ids.to(dev)].cpu() for c in (kc, vc)]
+        L = torch.tensor(lens, dtype=torch.int32)
+        out = torch.full_like(q, float("nan"), device=dev)
+        d = (out, q.to(dev), kc, vc, bt.to(dev), L.to(dev))
+        if see is None:
+            call = binding.pa_decode_v2_window_fp8 if cache == "e4m3" else binding.pa_decode_v2_window
+            ws = call(*d, 0.1, window, 3, partition_size=128, **more)
+        else:
+            call = binding.pa_decode_v2_tree_fp8 if cache == "e4m3" else binding.pa_decode_v2_tree
+            ws = call(*d, pack(see).to(dev), 0.1, partition_size=128, **more)
+        assert binding.device_status(ws) == binding.PA_OK
+        ref, _, bound = attend64(q, *pages, small, L, 0.1, window, 3, see, K_SCALE, V_SCALE)
+        assert bool(((out.cpu().double() - ref).abs() <= bound).all())
+        return pages
+
+    check_rows(torch.randn((S, 1, 4, D), generator=g).half(), lens, 200, None)
+    check_rows(torch.randn((S, n, 4, D), generator=g).half(), lens, 200, None)
+    pages = check_rows(torch.randn((S, n, 4, D), generator=g).half(), lens, 0, see)
+    for s, L in enumerate(lens):  # what was written is what is there
+        want = value[sum(lens[:s]):][:L]
+        if cache == "e4m3":
+            want = (want.float() / torch.tensor(V_SCALE)).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+        assert torch.equal(pages[1][s * MB + t[s] // BS, :, :, t[s] % BS], want)
+    path = [1, 4, 5, 9]
+    new = torch.empty((S,), dtype=torch.int32, device=dev)
+    ws = binding.pa_tree_accept(new, kc, vc, bt.to(dev), torch.tensor(lens, dtype=torch.int32, device=dev),
+                                torch.tensor([path] * S, dtype=torch.int32, device=dev),
+                                torch.tensor([4] * S, dtype=torch.int32, device=dev), n)
+    assert binding.device_status(ws) == binding.PA_OK and new.tolist() == [L - n + 4 for L in lens]
+    for c, before in zip((kc, vc), pages):
+        after = c[ids.to(dev)].cpu()
+        for s, L in enumerate(lens):
+            for i, node in enumerate(path):
+                to, at = L - n + i, L - n + node
+                a, b = after[s * MB + to // BS], before[s * MB + at // BS]
+                assert torch.equal(a[:, :, to % BS], b[:, :, at % BS])
+    lens = new.tolist()
+    check_rows(torch.randn((S, n, 4, D), generator=g).half(), lens, 200, None)
