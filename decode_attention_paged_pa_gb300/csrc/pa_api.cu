@@ -311,16 +311,18 @@ int decode_impl(void* out, float* lse, const void* query, const void* key_cache,
   // fit a warp's ring).
   const bool kv4_pairs = kv4 && G * 2 <= kMmaGroup && KH % 2 == 0 && D <= 128 && BS <= 32;
   const int kvu = pairs || kv4_pairs ? 2 : 1;
-  // View rows on the tensor cores: partitions are taken together, in powers of two, as long as every SM can
-  // still have three units (four with many rows a unit, whose lengths differ more): each
-  // has its start and end, and states that are joined.  (16 nodes a sequence, 48
-  // sequences of 3000 tokens, partitions of 512: 218 us as they were, 168 with eight
-  // together; one row, 128 sequences, a window of 1024: 108 us, 102 with two and 95 with
-  // four together, which is a unit for every two kv heads of a sequence.)
+  // View rows on the tensor cores: partitions are taken together, in powers of two, as long
+  // as full tables still give every SM three units, or with many rows a unit one: each has
+  // its start and end, and states that are joined.  (Partitions of 512 as they are, units
+  // for four, two and one an SM: 16 nodes, 48 sequences of 3000 tokens: 218, 129, 118, 118
+  // us; 64 nodes, 16 sequences of 5000: 155 with four, 136, 122; 32 nodes, 4 sequences of 3000:
+  // 33 with two, 27.  One row, 128 sequences, a window of 1024: 108 as they are, 95 for three
+  // or two; 40 such sequences: 45 for three, 49 for two.)  The lengths are not known here:
+  // sequences far shorter than their tables get fewer units than that.
   int part = view && P > MB * BS ? MB * BS : P;
   if (view && variant == PA_VARIANT_MMA) {
     const int blocks = view_blocks(q_len, MB, BS, view->window, view->sinks);
-    const long long cap = (long long)blocks * BS, want = (many ? 4ll : 3ll) * device_sm_count();
+    const long long cap = (long long)blocks * BS, want = (many ? 1ll : 3ll) * device_sm_count();
     const long long tiles = (long long)S * (KH / kvu) * ((G + gt - 1) / gt);
     long long joined = part;
     while (joined < cap && tiles * ((cap + 2 * joined - 1) / (2 * joined)) >= want) joined *= 2;

@@ -42,8 +42,8 @@
 // ring of codes, into the layouts of a block of 64 tokens whatever the cache's block.
 //
 // Measured (32 heads over 8 of 128 dims; whole calls): 16 nodes of 48 sequences of 1001 to
-// 4999 tokens, bf16 129 us (of the cache's bytes: 82), fp16 115; 64 nodes of 16 sequences of
-// 2048 to 8192, bf16 154 (bytes 49, products 85 with two terms a weight), fp16 132; chunks of
+// 4999 tokens, bf16 118 us (of the cache's bytes: 82), fp16 104; 64 nodes of 16 sequences of
+// 2048 to 8192, bf16 122 (bytes 49, products 85 with two terms a weight), fp16 96; chunks of
 // 128 tokens over a window of 1024, fp16 97, E4M3 121 (products 27).  A tile takes about 1100
 // cycles (fp16) where its products are 530: what is left is the way from a tile's scores
 // through its weights to the buffer's next scores, three buffers for two warpgroups; and
