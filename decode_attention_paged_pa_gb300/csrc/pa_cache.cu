@@ -425,7 +425,9 @@ __device__ __forceinline__ bool path_bad(const AcceptParams& p, int s, int i0, i
   for (int i = i0; i < a; i += step) {
     const int node = p.accepted[(size_t)s * p.A + i];
     const int before = i > 0 ? p.accepted[(size_t)s * p.A + i - 1] : -1;
-    if (node <= before || node >= p.n) {
+    // (Each entry by itself: the one before may be anything, and no table entry outside
+    // the row is read for what is not a node or a place among the nodes.)
+    if (i >= p.n || node < 0 || node <= before || node >= p.n) {
       bad = true;
       continue;
     }
