@@ -33,10 +33,10 @@
 // roundings are as exact as those of weights below 1.  fp16 weights are rounded once;
 // bf16 ones are the sum of two terms (two products), as in pa_mma.cuh.
 //
-// A tile that some row does not see whole is masked row by row, eight tokens at a
-// time; values of it that are not finite are cleared in shared memory (their
-// products with other rows' zero weights would be NaN), and the rows that do see
-// them get them added at the end of the unit.
+// A tile that some row does not see whole is masked row by row, 64 tokens at a time;
+// values of it that are not finite are cleared in shared memory (their products with
+// other rows' zero weights would be NaN).  Such tiles are noted (RowsOdd), and at the
+// end of the unit the rows that see them get their values from the cache added.
 //
 // 8-bit caches: the ring of tiles is filled by warps that widen E4M3 codes to fp16 from a
 // ring of codes, into the layouts of a block of 64 tokens whatever the cache's block.
@@ -64,6 +64,35 @@ constexpr uint32_t kRowsSmem = 227u * 1024u;
 
 struct RowsUnit {
   int s, p, kv, t0, t1, nt, np, nh, h0, L, sink_blocks, skip;
+};
+
+// What a unit's values that are not finite leave to its end: the partly seen tiles
+// where one was cleared, as a set (tile + 1 by linear probing, 0: free), and for
+// 8-bit caches, whose NaN codes are cleared in every tile, the dims (bits) with one in
+// a tile that every row sees.  Partly seen tiles lie around the end of the first tokens,
+// the start of the window and the end of the rows, each over at most the rows' 512
+// tokens: fewer than 28.  (`all` is set if there should be more: every tile is gone through.)
+struct RowsOdd {
+  static constexpr int kTiles = 32;
+  int any, all;
+  int tile[kTiles];
+  uint32_t dims[8];
+  __device__ __forceinline__ void clear(int lane) {  // a warp
+    for (int i = lane; i < (int)(sizeof(RowsOdd) / 4); i += 32) reinterpret_cast<int*>(this)[i] = 0;
+  }
+  __device__ __forceinline__ void add_tile(int i) {
+    int at = i % kTiles;
+    for (int n = 0; n < kTiles; ++n, at = (at + 1) % kTiles) {
+      const int was = atomicCAS(&tile[at], 0, i + 1);
+      if (was == 0 || was == i + 1) break;
+      if (n + 1 == kTiles) *const_cast<volatile int*>(&all) = 1;
+    }
+    *const_cast<volatile int*>(&any) = 1;
+  }
+  __device__ __forceinline__ void add_dim(int d) {
+    atomicOr(&dims[d >> 5], 1u << (d & 31));
+    *const_cast<volatile int*>(&any) = 1;
+  }
 };
 
 template <typename T_, int D_, int BS_, bool FP8_ = false>
@@ -101,8 +130,8 @@ struct RowsConfig {
   static constexpr uint32_t QBYTES = QTILE;
   static constexpr uint32_t bars(int ns) { return 2 * ns + 2 * NR + 2 * UQ + 3 * NBUF + 7; }
   static constexpr uint32_t small(int ns) {
-    return al16(bars(ns) * 8) + al16(UQ * sizeof(RowsUnit)) + 64 + al16((kRowsMaxUnitSeqs + 1) * 4) +
-           al16(kRowsMaxUnitSeqs * 2);
+    return al16(bars(ns) * 8) + al16(UQ * sizeof(RowsUnit)) + al16(UQ * sizeof(RowsOdd)) + 64 +
+           al16((kRowsMaxUnitSeqs + 1) * 4) + al16(kRowsMaxUnitSeqs * 2);
   }
   static constexpr int kFit = (int)((kRowsSmem - small(D_ > 128 ? 8 : 16) - QBYTES - NR * RSLOT) / SLOT);
   // (An even number: keys have the slots of one parity within a unit, values those of the
@@ -117,7 +146,8 @@ struct RowsConfig {
   }
   static constexpr uint32_t OFF_RING = QBYTES, OFF_CODES = OFF_RING + NS * SLOT, OFF_BAR = OFF_CODES + NR * RSLOT;
   static constexpr uint32_t OFF_INFO = OFF_BAR + al16(bars(NS) * 8);
-  static constexpr uint32_t OFF_FLAGS = OFF_INFO + al16(UQ * sizeof(RowsUnit));
+  static constexpr uint32_t OFF_ODD = OFF_INFO + al16(UQ * sizeof(RowsUnit));
+  static constexpr uint32_t OFF_FLAGS = OFF_ODD + al16(UQ * sizeof(RowsOdd));
   static constexpr uint32_t OFF_PREF = OFF_FLAGS + 64;
   static constexpr uint32_t OFF_PERM = OFF_PREF + al16((kRowsMaxUnitSeqs + 1) * 4);
   static constexpr uint32_t BYTES = OFF_PERM + al16(kRowsMaxUnitSeqs * 2);
@@ -170,6 +200,10 @@ struct RowsCta {
 #pragma unroll
     for (int b = 0; b < C::NBUF; ++b) par ^= (uint32_t)((nt - b + C::NBUF - 1) / C::NBUF & 1) << b;
     return par;
+  }
+
+  __device__ __forceinline__ RowsOdd* odd_of(uint32_t k) const {
+    return reinterpret_cast<RowsOdd*>(smem + C::OFF_ODD) + k % C::UQ;
   }
 
   // Position of block vb of those that the sequence's rows can see.
@@ -245,6 +279,8 @@ struct RowsCta {
       const uint32_t us = k % C::UQ;
       ok = __shfl_sync(0xffffffffu, lane == 0 ? (int)wait(C::UEMPTY + us, k / C::UQ + 1, kRowsUnitSlot, (int)k) : 0, 0);
       if (!ok) break;
+      odd_of(k)->clear(lane);  // (nothing looks at the unit before in this slot any more)
+      __syncwarp();
       if (lane == 0) {
         info[us] = U;
         mbar_arrive(bar(C::UFULL + us));
@@ -505,6 +541,37 @@ struct RowsCta {
     return m;
   }
 
+  // Positions [lo, hi) that every row of a unit sees (padding apart).
+  struct Full {
+    int lo, hi;
+  };
+  __device__ __forceinline__ Full full_of(int L, int kv, int h0, int nh) const {
+    const int first = L - prm.q_len, l0 = h0 - kv * prm.G;
+    const int i0 = l0 / prm.Gu, i1 = (l0 + nh - 1) / prm.Gu;
+    return Full{prm.window > 0 ? (prm.masks ? L - prm.window : first + i1 - prm.window + 1) : 0,
+                prm.masks ? first : first + i0 + 1};
+  }
+  // A tile of the unit's work, `left` tokens from its start to the unit's end: where it
+  // lies, and whether some row of the unit does not see the whole of it.
+  struct Tile {
+    int p0;        // the position of its first token
+    int n;         // its tokens in front of skipped blocks; the others are skip blocks further on
+    bool partial;
+  };
+  __device__ __forceinline__ Tile tile_at(int tile, int left, int sink_blocks, int skip, const Full& full) const {
+    const int vb0 = tile / C::BS, p0 = block_pos(sink_blocks, skip, vb0);
+    const int p1 = block_pos(sink_blocks, skip, vb0 + (min(left, C::TN) - 1) / C::BS) + C::BS - 1;
+    const bool jump = skip > 0 && vb0 < sink_blocks && vb0 + C::NB > sink_blocks;
+    return Tile{p0, jump ? (sink_blocks - vb0) * C::BS : C::TN,
+                left < C::TN || jump || p1 >= full.hi || (p0 < full.lo && p1 >= prm.sinks)};
+  }
+  // The tokens of it that a row sees.
+  __device__ __forceinline__ uint64_t tile_seen(const RowView& v, const Tile& t, int left, int skip) const {
+    uint64_t m = seen64(v, t.p0, left);
+    if (t.n < C::TN) m = (m & first_bits(t.n)) | (seen64(v, t.p0 + skip * C::BS, left) & ~first_bits(t.n));
+    return m;
+  }
+
   // Byte offset of tokens 8c .. 8c + 7 of dim d in a staged value block.
   static __device__ __forceinline__ uint32_t value_chunk(int d, int c) {
     constexpr uint32_t ROW = C::MS * 2;
@@ -567,12 +634,27 @@ struct RowsCta {
     }
     return w;
   }
+  // Tile j, whose codes are in ring slot rs, has NaN codes: it is noted, or if every row
+  // sees it, the dims that have one.
+  __device__ __noinline__ void note_codes(uint32_t k, uint32_t rs, int j, int lane) const {
+    const RowsUnit U = reinterpret_cast<const RowsUnit*>(smem + C::OFF_INFO)[k % C::UQ];
+    RowsOdd* odd = odd_of(k);
+    const int tile = U.t0 + j * C::TN;
+    if (tile_at(tile, U.t1 - tile, U.sink_blocks, U.skip, full_of(U.L, U.kv, U.h0, U.nh)).partial) {
+      if (lane == 0) odd->add_tile(j);
+      return;
+    }
+    const uint32_t* codes = reinterpret_cast<const uint32_t*>(smem + C::OFF_CODES + rs * C::RSLOT);
+    for (int x = lane; x < C::TN * C::D / 4; x += 32) {  // [block][D][BS]
+      const uint32_t w = codes[x];
+      if (((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) odd->add_dim(x * 4 / C::BS % C::D);
+    }
+  }
   // 8-bit caches: the ring's codes widened to fp16, into the layouts of a block of 64
   // tokens; each of the CW warps takes every CW-th ring item, so that several are on
   // their way and a warp's waits are another warp's work.
   __device__ __forceinline__ void widen(int cw, int lane) {
     const RowsUnit* info = reinterpret_cast<const RowsUnit*>(smem + C::OFF_INFO);
-    volatile int* odd_unit = reinterpret_cast<volatile int*>(smem + C::OFF_FLAGS + 16);
     constexpr int BS = C::BS, D = C::D;
     uint32_t g = 0;
     for (uint32_t k = 0;; ++k) {
@@ -582,12 +664,12 @@ struct RowsCta {
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(C::UEMPTY + k % C::UQ));
       if (us < 0) return;
-      bool found = false;
       for (int i = (int)((cw + C::CW - g % C::CW) % C::CW); i < 2 * nt; i += C::CW) {
         const uint32_t it = g + i, rs = it % C::NR, sl = slot(it);
         int j;
         const bool value = item_tile(i, nt, &j);
         const int left = tokens - j * C::TN;
+        bool found = false;
         bool ok = wait(C::RFULL + rs, it / C::NR, kRowsCodes, (int)it);
         if (ok) ok = wait(C::EMPTY + sl, phase(it) + 1, kRowsRing, (int)it);
         if (!__all_sync(0xffffffffu, ok)) return;
@@ -625,8 +707,7 @@ struct RowsCta {
             *reinterpret_cast<uint4*>(to + (BS >= 16 ? value_chunk(d, t / 8 + 1) : value_chunk(d + 1, t / 8))) =
                 widen8(w.z, w.w);
           }
-          // (Units in flight are fewer than four: a unit's word is its own.)
-          if (found) odd_unit[k & 3] = (int)k + 1;
+          if (__any_sync(0xffffffffu, found)) note_codes(k, rs, j, lane);
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -641,24 +722,65 @@ struct RowsCta {
 
   // Values that are not finite (rare; the cache itself is read): dims [d0, d1) of a
   // row that has been written get those of the tokens it sees added.  `at`: the row's
-  // output or state.
+  // output or state.  (Only the noted tiles: by the latency of its loads one takes as long
+  // as a hundred tiles of the unit, which may have thousands.)
   template <typename E>
-  __device__ __noinline__ void add_odd(int s, int kv, int t0, int t1, int sink_blocks, int skip, int lo, int hi, int base,
-                                       const uint32_t* bits, int d0, int d1, E* at) const {
+  __device__ __noinline__ void add_odd(uint32_t k, int qi, int d0, int d1, E* at) const {
     using CT = typename std::conditional<C::kFp8, uint8_t, typename C::T>::type;
-    const CT* vc = static_cast<const CT*>(prm.vc);
-    for (int t = t0; t < t1; ++t) {
-      const int pos = t + (t / C::BS < sink_blocks ? 0 : skip * C::BS);
-      if (!(seen64(RowView{lo, hi, base, bits}, pos, 1) & 1ull)) continue;
-      int id = prm.bt[(size_t)s * prm.MB + pos / C::BS];
-      if ((unsigned)id >= (unsigned)prm.num_blocks) id = 0;
-      const CT* blk = vc + ((size_t)id * prm.KH + kv) * C::D * C::BS + t % C::BS;
-      for (int d = d0; d < d1; ++d) {
-        float x;
-        if constexpr (C::kFp8) x = (blk[d * C::BS] & 0x7f) == 0x7f ? NAN : 0.f;
-        else x = (float)blk[d * C::BS];
-        if (!(fabsf(x) < INFINITY)) at[d] = (E)((float)at[d] + x);
+    constexpr int PER = 8 / (int)sizeof(CT), BS = C::BS;  // elements of 8 bytes
+    constexpr uint32_t kExp = C::kBf16 ? 0x7f80u : 0x7c00u;
+    const RowsUnit U = reinterpret_cast<const RowsUnit*>(smem + C::OFF_INFO)[k % C::UQ];
+    const RowView v = row_view_of(prm, U.s, U.L, qi);
+    const Full full = full_of(U.L, U.kv, U.h0, U.nh);
+    const int t0 = U.t0, t1 = U.t1;
+    const volatile RowsOdd& o = *odd_of(k);
+    const bool all = o.all != 0;
+    const int tiles = all ? (t1 - t0 + C::TN - 1) / C::TN : RowsOdd::kTiles;
+    for (int q = 0; q < tiles; ++q) {
+      const int i = all ? q : o.tile[q] - 1;
+      if (i < 0) continue;
+      const int tile = t0 + i * C::TN, left = t1 - tile;
+      const uint64_t m = tile_seen(v, tile_at(tile, left, U.sink_blocks, U.skip, full), left, U.skip);
+      for (int b = 0; b < C::NB; ++b) {
+        const uint64_t mb = m >> (b * BS) & first_bits(BS);
+        if (mb == 0) continue;
+        int id = prm.bt[(size_t)U.s * prm.MB + block_pos(U.sink_blocks, U.skip, tile / BS + b) / BS];
+        if ((unsigned)id >= (unsigned)prm.num_blocks) id = 0;
+        const CT* rows = static_cast<const CT*>(prm.vc) + ((size_t)id * prm.KH + U.kv) * C::D * BS;
+        // (A call whose registers are few: with more of it unrolled the kernel spilled.)
+#pragma unroll 1
+        for (int d = d0; d < d1; ++d) {
+          float sum = 0.f;
+          bool any = false;
+#pragma unroll 4
+          for (int w = 0; w < BS / PER; ++w) {
+            const uint2 x = __ldg(reinterpret_cast<const uint2*>(rows + (size_t)d * BS) + w);
+#pragma unroll
+            for (int e = 0; e < PER; ++e) {
+              const uint32_t word = e * (int)sizeof(CT) < 4 ? x.x : x.y;
+              bool is;
+              float x1 = NAN;
+              if constexpr (C::kFp8) {
+                is = (word >> (8 * (e & 3)) & 0x7fu) == 0x7fu;
+              } else {
+                const uint32_t h = word >> (16 * (e & 1)) & 0xffffu;
+                is = (h & kExp) == kExp;
+                if (h == kExp) x1 = INFINITY;
+                if (h == (kExp | 0x8000u)) x1 = -INFINITY;
+              }
+              if (is && (mb >> (w * PER + e) & 1u)) {
+                sum += x1;
+                any = true;
+              }
+            }
+          }
+          if (any) at[d] = (E)((float)at[d] + sum);
+        }
       }
+    }
+    if constexpr (C::kFp8) {
+      for (int d = d0; d < d1; ++d)
+        if (o.dims[d >> 5] >> (d & 31) & 1u) at[d] = (E)NAN;
     }
   }
 
@@ -721,7 +843,6 @@ struct RowsCta {
     using MT = typename C::MT;
     constexpr int TN = C::TN, NB = C::NB, NG = C::NG, D = C::D;
     const RowsUnit* info = reinterpret_cast<const RowsUnit*>(smem + C::OFF_INFO);
-    volatile int* odd_unit = reinterpret_cast<volatile int*>(smem + C::OFF_FLAGS + 16);
     const int lane = tid & 31;
     const uint32_t lanes = (uint32_t)(tid & ~31) << 16;  // this warp's lanes of tensor memory
     // (Not zero: a masked score, -inf, times it is -inf.)
@@ -745,14 +866,7 @@ struct RowsCta {
       const int qi = mine ? (U.h0 - U.kv * prm.G + row) / prm.Gu : -1;  // its query token
       const auto view = [&]() { return qi >= 0 ? row_view_of(prm, U.s, U.L, qi) : RowView{0, 0, 0, nullptr}; };
       const bool warp_rows = (row & ~31) < nh;
-      // Positions that every row of the unit sees (padding apart).
-      int full_lo, full_hi;
-      {
-        const int first = U.L - prm.q_len, l0 = U.h0 - U.kv * prm.G;
-        const int i0 = l0 / prm.Gu, i1 = (l0 + nh - 1) / prm.Gu;
-        full_hi = prm.masks ? first : first + i0 + 1;
-        full_lo = prm.window > 0 ? (prm.masks ? U.L - prm.window : first + i1 - prm.window + 1) : 0;
-      }
+      const Full full = full_of(U.L, U.kv, U.h0, nh);
       float mref = -INFINITY, l = 0.f, sl2 = sl2_all;
       if constexpr (C::kQScale) sl2 = fmaxf(sl2 * factor, 1.17549435e-38f);
       const int t0 = U.t0, t1 = U.t1, sink_blocks = U.sink_blocks, skip = U.skip;
@@ -761,21 +875,18 @@ struct RowsCta {
         const int b = i % C::NBUF;
         const uint32_t use = (par >> b) + i / C::NBUF;  // (its low bit counts)
         const uint32_t sc = tmem + lanes + b * TN;
-        const int tile = t0 + i * TN, left = t1 - tile, vb0 = tile / C::BS;
+        const int tile = t0 + i * TN, left = t1 - tile;
         ok = __all_sync(0xffffffffu, wait(C::SFULL + b, use, kRowsS, i));
         if (!ok) break;
         tc_fence_after();
-        // Whether every row sees the whole tile.
-        const int p0 = block_pos(sink_blocks, skip, vb0);
-        const int p1 = block_pos(sink_blocks, skip, vb0 + (min(left, TN) - 1) / C::BS) + C::BS - 1;
-        const bool jump = vb0 < sink_blocks && skip > 0;
-        const bool partial = left < TN || jump || p1 >= full_hi || (p0 < full_lo && p1 >= prm.sinks);
+        const Tile place = tile_at(tile, left, sink_blocks, skip, full);
+        const bool partial = place.partial;
         if (!C::kFp8 && partial) {
           // (Values: before the weights of the tile are announced.)
           const uint32_t it = g + value_item(i, nt);
           ok = __all_sync(0xffffffffu, wait(C::FULL + slot(it), phase(it), kRowsFull, (int)it));
           if (!ok) break;
-          if (clear_values(slot(it), left, tid)) *odd_unit = (int)k + 1;
+          if (clear_values(slot(it), left, tid)) odd_of(k)->add_tile(i);
           fence_proxy_async_smem();
           __syncwarp();
         }
@@ -787,13 +898,7 @@ struct RowsCta {
         __syncwarp();
         tmem_get64(sc, sc + 32, s);
         if (partial) {
-          const RowView v = view();
-          // (A tile can have the end of the first tokens' blocks in it, and then others.)
-          uint64_t m = seen64(v, p0, left);
-          if (jump) {
-            const int n = sink_blocks * C::BS - tile;  // of its tokens are before it
-            if (n < TN) m = (m & first_bits(n)) | (seen64(v, p0 + skip * C::BS, left) & ~first_bits(n));
-          }
+          const uint64_t m = tile_seen(view(), place, left, skip);
           const uint32_t mm[2] = {(uint32_t)m, (uint32_t)(m >> 32)};
 #pragma unroll
           for (int t = 0; t < TN; ++t)
@@ -870,7 +975,7 @@ struct RowsCta {
       // a thread) and write.
       if (!take_rows(tmem, lanes, wg, tid, k + 1, factor)) break;
       const uint32_t ob = tmem + lanes + C::O_COL;
-      const RowView v = view();
+      const bool live = view().hi > 0;
       // The last tile of each pipeline (-1: none), whose buffers are free when their
       // products are complete.
       const int last = C::NP == 1 ? nt - 1 : nt - 1 - ((nt - 1 - wg) & 1);
@@ -895,7 +1000,7 @@ struct RowsCta {
       ok = __all_sync(0xffffffffu, wait(C::XBAR, k, kRowsX, (int)k));
       if (!ok) break;
       tc_fence_after();
-      const bool odd = odd_unit[C::kFp8 ? k & 3 : 0] == (int)k + 1;
+      const bool odd = *const_cast<const volatile int*>(&odd_of(k)->any) != 0;
       float f0 = 1.f, f1 = 0.f;
       bool has0 = nt > 0, has1 = false;  // pipelines with something in O
       int d_lo = 0, d_hi = D;
@@ -920,7 +1025,7 @@ struct RowsCta {
         mbar_arrive(bar(C::XFREE));
       }
       if (warp_rows) {
-        const bool some = v.hi > 0 && l != 0.f;
+        const bool some = live && l != 0.f;
         const float inv = some ? (C::kFp8 ? prm.v_scale / l : 1.f / l) : 0.f;
         f0 *= inv;
         f1 *= inv;
@@ -984,11 +1089,9 @@ struct RowsCta {
           __syncwarp();
           if (mine && some) {
             if (single)
-              add_odd(U.s, U.kv, t0, t1, sink_blocks, skip, v.lo, v.hi, v.base, v.bits, d_lo, d_hi,
-                      static_cast<T*>(prm.out) + (size_t)orow * D);
+              add_odd(k, qi, d_lo, d_hi, static_cast<T*>(prm.out) + (size_t)orow * D);
             else
-              add_odd(U.s, U.kv, t0, t1, sink_blocks, skip, v.lo, v.hi, v.base, v.bits, d_lo, d_hi,
-                      prm.ws_o + (sh * prm.Pmax + U.p) * D);
+              add_odd(k, qi, d_lo, d_hi, prm.ws_o + (sh * prm.Pmax + U.p) * D);
           }
           __syncwarp();
         }
@@ -1019,7 +1122,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) pa_rows_kernel(const __grid_con
   extern __shared__ __align__(1024) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   RowsCta<C> cta(prm, smem);
-  int* flags = reinterpret_cast<int*>(smem + C::OFF_FLAGS);  // abort, bad length, tensor memory, -, odd units [4]; two barriers
+  int* flags = reinterpret_cast<int*>(smem + C::OFF_FLAGS);  // abort, bad length, tensor memory; at 32 two barriers
   int* pref = reinterpret_cast<int*>(smem + C::OFF_PREF);
   uint16_t* perm = reinterpret_cast<uint16_t*>(smem + C::OFF_PERM);
   constexpr int WP = C::NP * 4, WM = WP + 1, WV = WP + 2, WQ = WP + 3;  // producer, product and Q warps
@@ -1050,7 +1153,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) pa_rows_kernel(const __grid_con
     mbar_init(cta.bar(C::XFREE), C::NP * 128);
     mbar_init(cta.sbase + C::OFF_FLAGS + 32, 1);
     mbar_init(cta.sbase + C::OFF_FLAGS + 40, 1);
-    flags[0] = flags[1] = flags[4] = flags[5] = flags[6] = flags[7] = 0;
+    flags[0] = flags[1] = 0;
     fence_mbarrier_init();
   }
   if (warp == WM) tmem_alloc(smem_addr(flags + 2), 512);
