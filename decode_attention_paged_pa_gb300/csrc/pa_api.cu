@@ -311,29 +311,21 @@ int decode_impl(void* out, float* lse, const void* query, const void* key_cache,
   // fit a warp's ring).
   const bool kv4_pairs = kv4 && G * 2 <= kMmaGroup && KH % 2 == 0 && D <= 128 && BS <= 32;
   const int kvu = pairs || kv4_pairs ? 2 : 1;
-  // View rows on the tensor cores: partitions are taken together, in powers of two, as long
-  // as full tables still give every SM three units, or with many rows a unit one: each has
-  // its start and end, and states that are joined.  (Partitions of 512 as they are, units
+  // View rows on the tensor cores: partitions are taken together where the lengths leave
+  // every SM its share without them (joined_partition): units of which three make an SM's
+  // work, or with many rows a quarter more than it.  (Partitions of 512 as they are, units
   // for four, two and one an SM: 16 nodes, 48 sequences of 3000 tokens: 218, 129, 118, 118
   // us; 64 nodes, 16 sequences of 5000: 155 with four, 136, 122; 32 nodes, 4 sequences of 3000:
   // 33 with two, 27.  One row, 128 sequences, a window of 1024: 108 as they are, 95 for three
-  // or two; 40 such sequences: 45 for three, 49 for two.)  The lengths are not known here:
-  // sequences far shorter than their tables get fewer units than that.
-  int part = view && P > MB * BS ? MB * BS : P;
-  if (view && variant == PA_VARIANT_MMA) {
-    const int blocks = view_blocks(q_len, MB, BS, view->window, view->sinks);
-    const long long cap = (long long)blocks * BS, want = (many ? 1ll : 3ll) * device_sm_count();
-    const long long tiles = (long long)S * (KH / kvu) * ((G + gt - 1) / gt);
-    long long joined = part;
-    while (joined < cap && tiles * ((cap + 2 * joined - 1) / (2 * joined)) >= want) joined *= 2;
-    part = (int)(joined < (long long)MB * BS ? joined : (long long)MB * BS);
-    if (!ws_layout(S, H, KH, D, blocks, BS, part, &w)) return PA_ERR_INVALID_ARG;
-  }
+  // or two; 40 such sequences: 45 for three, 49 for two.)
+  const bool joined = view && variant == PA_VARIANT_MMA;
+  const int units = !joined ? 0 : many ? (device_sm_count() * 4 + 4) / 5 : 3 * device_sm_count();
   const int hg_per_kv = (G + gt - 1) / gt;
   const int n_hg = KH * hg_per_kv / kvu;
   const int rows_per_launch = many ? kRowsSeqsPerLaunch : kMaxSeqsPerLaunch;  // sequences per launch
   const int chunk = S < rows_per_launch ? S : rows_per_launch;
-  if ((long long)chunk * w.pmax * n_hg > INT_MAX / 2) return PA_ERR_UNSUPPORTED;
+  // (Joined partitions are longer than half of the share of one of `units`, or one a sequence.)
+  if ((long long)chunk * (joined ? 1 : w.pmax) * n_hg > INT_MAX / 2) return PA_ERR_UNSUPPORTED;
   // The tensor-core kernels over 16-bit caches in blocks of 16 tokens or more
   // stage value blocks by swizzled tensor copies (z coordinates are int32).
   const bool tma_values = variant == PA_VARIANT_MMA && !kv_fp8 && !kv4 && BS >= 16;
@@ -353,6 +345,40 @@ int decode_impl(void* out, float* lse, const void* query, const void* key_cache,
   }
   int status = PA_OK;
   const size_t esz = elem_bytes(dtype);
+  // Phase 2 over sequences s0 .. s0 + n - 1 (no sequence has more than one
+  // partition if the table holds at most P tokens).  Warps per row: enough that a
+  // warp takes at most 16 partitions (one batch of loads), up to 8.
+  const auto combine = [&](int s0, int n) {
+    if (w.pmax <= 1) return cudaSuccess;
+    const size_t rows = (size_t)s0 * H;
+    CParams cp;
+    std::memset(&cp, 0, sizeof cp);
+    cp.out = static_cast<uint8_t*>(out) + rows * D * esz;
+    cp.lse = lse ? lse + rows : nullptr;
+    cp.ws_m = reinterpret_cast<const float*>(ws + w.m) + rows * w.pmax;
+    cp.ws_l = reinterpret_cast<const float*>(ws + w.l) + rows * w.pmax;
+    cp.ws_o = reinterpret_cast<const float*>(ws + w.o) + rows * w.pmax * D;
+    cp.lens = seq_lens + s0;
+    cp.S = n;
+    cp.H = H;
+    cp.Pmax = w.pmax;
+    cp.P = view && P > MB * BS ? MB * BS : P;
+    cp.max_len = MB * BS;
+    cp.BS = BS;
+    if (view) {
+      cp.view = 1;
+      cp.window = view->window;
+      cp.sinks = view->sinks;
+      cp.units = units;
+      cp.n_hg = n_hg;
+    }
+    cp.wpr = w.pmax > 64 ? 8 : w.pmax > 32 ? 4 : w.pmax > 16 ? 2 : 1;
+    cp.q_len = q_len;
+    cp.Hu = num_heads;
+    cp.Gu = num_heads / KH;
+    cp.G = G;
+    return launch_combine(cp, (int)esz, dtype == PA_DTYPE_BF16, D, st);
+  };
   for (int s0 = 0; s0 < S && status == PA_OK; s0 += rows_per_launch) {
     const int n = (S - s0) < rows_per_launch ? (S - s0) : rows_per_launch;
     // The header (error word, work counter, timeout record) starts at zero;
@@ -389,7 +415,8 @@ int decode_impl(void* out, float* lse, const void* query, const void* key_cache,
     prm.num_blocks = num_blocks;
     // (A partition past the table's capacity is the capacity: sums of lengths
     // and partition sizes stay in 32 bits.)
-    prm.P = view ? part : kv4 && P > MB * BS ? MB * BS : P;
+    prm.P = (view || kv4) && P > MB * BS ? MB * BS : P;
+    prm.units = units;
     prm.Pmax = w.pmax;
     prm.hg_per_kv = hg_per_kv;
     prm.n_hg = n_hg;
@@ -466,38 +493,11 @@ int decode_impl(void* out, float* lse, const void* query, const void* key_cache,
     else
       e = dtype == PA_DTYPE_FP16 ? launch_simt_f16(prm, D, BS, max_ctas, st)
                                  : launch_simt_bf16(prm, D, BS, max_ctas, st);
+    // (View rows: the next launch has partitions of its own.)
+    if (e == cudaSuccess && view) e = combine(s0, n);
     if (e != cudaSuccess) status = PA_ERR_CUDA;
   }
-  // Phase 2 over the whole batch (no sequence has more than one partition if
-  // the table holds at most P tokens).  Warps per row: enough that a warp
-  // takes at most 16 partitions (one batch of loads), up to 8.
-  if (status == PA_OK && w.pmax > 1) {
-    CParams cp;
-    std::memset(&cp, 0, sizeof cp);
-    cp.out = out;
-    cp.lse = lse;
-    cp.ws_m = reinterpret_cast<const float*>(ws + w.m);
-    cp.ws_l = reinterpret_cast<const float*>(ws + w.l);
-    cp.ws_o = reinterpret_cast<const float*>(ws + w.o);
-    cp.lens = seq_lens;
-    cp.S = S;
-    cp.H = H;
-    cp.Pmax = w.pmax;
-    cp.P = view ? part : P;
-    cp.max_len = MB * BS;
-    cp.BS = BS;
-    if (view) {
-      cp.view = 1;
-      cp.window = view->window;
-      cp.sinks = view->sinks;
-    }
-    cp.wpr = w.pmax > 64 ? 8 : w.pmax > 32 ? 4 : w.pmax > 16 ? 2 : 1;
-    cp.q_len = q_len;
-    cp.Hu = num_heads;
-    cp.Gu = num_heads / KH;
-    cp.G = G;
-    if (launch_combine(cp, (int)esz, dtype == PA_DTYPE_BF16, D, st) != cudaSuccess) status = PA_ERR_CUDA;
-  }
+  if (status == PA_OK && !view && combine(0, S) != cudaSuccess) status = PA_ERR_CUDA;
   if (own && cudaFreeAsync(ws, st) != cudaSuccess && status == PA_OK) status = PA_ERR_CUDA;
   return status;
 }

@@ -7,7 +7,7 @@ namespace pa {
 
 namespace {
 
-template <typename T, int D>
+template <typename T, int D, bool VIEW>
 cudaError_t go(const CParams& prm, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.dynamicSmemBytes = 0;
@@ -29,27 +29,38 @@ cudaError_t go(const CParams& prm, cudaStream_t st) {
     const int sms = device_sm_count();
     cfg.gridDim = dim3((unsigned)(rows < sms ? rows : sms), 1, 1);
     cfg.blockDim = dim3(kRowsWarps * 32, 1, 1);
-    return cudaLaunchKernelEx(&cfg, pa_combine_rows_kernel<T, D>, prm);
+    return cudaLaunchKernelEx(&cfg, pa_combine_rows_kernel<T, D, VIEW>, prm);
   }
   // CTAs of 4 warps where a row takes at most 4 (five CTAs of a 98-register
   // kernel fit an SM where two of 8 warps did: 20 warps in flight, not 16).
   const int nw = prm.wpr <= 4 ? 4 : kCombineWarps;
   const int rpc = nw / prm.wpr;
-  cfg.gridDim = dim3((unsigned)prm.S, (unsigned)((prm.H + rpc - 1) / rpc), 1);
+  unsigned groups = (unsigned)((prm.H + rpc - 1) / rpc);
+  if constexpr (VIEW) {
+    // Often no sequence has two partitions, which is known on the device only: no more
+    // CTAs than run at once (five an SM) find that out.
+    const unsigned most = (unsigned)(5 * device_sm_count() / prm.S);
+    groups = groups < most ? groups : most > 1 ? most : 1;
+  }
+  cfg.gridDim = dim3((unsigned)prm.S, groups, 1);
   cfg.blockDim = dim3(nw * 32, 1, 1);
-  if (nw == 4) return cudaLaunchKernelEx(&cfg, pa_combine_kernel<T, D, 4>, prm);
-  return cudaLaunchKernelEx(&cfg, pa_combine_kernel<T, D, kCombineWarps>, prm);
+  if constexpr (VIEW) {
+    return cudaLaunchKernelEx(&cfg, pa_combine_kernel<T, D, 4, true>, prm);  // (Pmax is 16 at most: one warp a row)
+  } else {
+    if (nw == 4) return cudaLaunchKernelEx(&cfg, pa_combine_kernel<T, D, 4, false>, prm);
+    return cudaLaunchKernelEx(&cfg, pa_combine_kernel<T, D, kCombineWarps, false>, prm);
+  }
 }
 
-template <typename T>
+template <typename T, bool VIEW>
 cudaError_t by_head_size(const CParams& prm, int D, cudaStream_t st) {
   switch (D) {
-    case 64: return go<T, 64>(prm, st);
-    case 80: return go<T, 80>(prm, st);
-    case 96: return go<T, 96>(prm, st);
-    case 112: return go<T, 112>(prm, st);
-    case 128: return go<T, 128>(prm, st);
-    case 256: return go<T, 256>(prm, st);
+    case 64: return go<T, 64, VIEW>(prm, st);
+    case 80: return go<T, 80, VIEW>(prm, st);
+    case 96: return go<T, 96, VIEW>(prm, st);
+    case 112: return go<T, 112, VIEW>(prm, st);
+    case 128: return go<T, 128, VIEW>(prm, st);
+    case 256: return go<T, 256, VIEW>(prm, st);
     default: return cudaErrorInvalidValue;
   }
 }
@@ -57,8 +68,12 @@ cudaError_t by_head_size(const CParams& prm, int D, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_combine(const CParams& prm, int elem_bytes, bool bf16, int D, cudaStream_t st) {
-  if (elem_bytes == 4) return by_head_size<float>(prm, D, st);
-  return bf16 ? by_head_size<__nv_bfloat16>(prm, D, st) : by_head_size<__half>(prm, D, st);
+  if (prm.view) {
+    if (elem_bytes == 4) return by_head_size<float, true>(prm, D, st);
+    return bf16 ? by_head_size<__nv_bfloat16, true>(prm, D, st) : by_head_size<__half, true>(prm, D, st);
+  }
+  if (elem_bytes == 4) return by_head_size<float, false>(prm, D, st);
+  return bf16 ? by_head_size<__nv_bfloat16, false>(prm, D, st) : by_head_size<__half, false>(prm, D, st);
 }
 
 }  // namespace pa

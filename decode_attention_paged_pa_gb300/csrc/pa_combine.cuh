@@ -52,6 +52,7 @@ struct CParams {
   int wpr;             // pa_combine_kernel: warps per row, 1, 2, 4 or 8
   int q_len, Hu, Gu, G;  // multi-query rows (q_len > 1): row head -> output row
   int view, window, sinks, BS;  // view rows (1): see ViewSpan
+  int units, n_hg;     // ... and joined_partition
 };
 
 // pa_combine_kernel: 8 warps where a row takes 8 of them, 4 otherwise (with
@@ -70,10 +71,43 @@ __device__ __forceinline__ size_t combine_out_row(const CParams& prm, int s, int
   return ((size_t)s * prm.q_len + i) * prm.Hu + kv * prm.Gu + (l - i * prm.Gu);
 }
 
-__device__ __forceinline__ int seq_partitions(const CParams& prm, int s) {
-  int L = min(max(prm.lens[s], 0), prm.max_len);
-  if (prm.view) L = view_tokens(L, prm.q_len, prm.window, prm.sinks, prm.BS);
-  return (L + prm.P - 1) / prm.P;
+// Tokens of sequence s that phase 1 worked on.
+template <bool VIEW>
+__device__ __forceinline__ int seq_work(const CParams& prm, int s) {
+  const int L = min(max(prm.lens[s], 0), prm.max_len);
+  return VIEW ? view_tokens(L, prm.q_len, prm.window, prm.sinks, prm.BS) : L;
+}
+template <bool VIEW>
+__device__ __forceinline__ int seq_partitions(const CParams& prm, int s, int P) {
+  return (seq_work<VIEW>(prm, s) + P - 1) / P;
+}
+// The launch's tokens per partition; every thread of the CTA calls it.
+template <int NW, bool VIEW>
+__device__ __forceinline__ int partition_tokens(const CParams& prm) {
+  if (!VIEW || prm.units == 0) return prm.P;
+  __shared__ unsigned long long s_sum[NW];
+  __shared__ int s_most[NW];
+  unsigned long long sum = 0;
+  int most = 0;
+#pragma unroll 4
+  for (int s = threadIdx.x; s < prm.S; s += NW * 32) {
+    const int L = seq_work<VIEW>(prm, s);
+    sum += (unsigned)L;
+    most = max(most, L);
+  }
+  reduce_lengths(sum, most);
+  if ((threadIdx.x & 31) == 0) {
+    s_sum[threadIdx.x >> 5] = sum;
+    s_most[threadIdx.x >> 5] = most;
+  }
+  __syncthreads();
+  sum = 0;
+#pragma unroll
+  for (int w = 0; w < NW; ++w) {
+    sum += s_sum[w];
+    most = max(most, s_most[w]);
+  }
+  return joined_partition(sum, most, prm.P, prm.units, prm.n_hg, prm.max_len);
 }
 
 // Combine the row group of rows h0 .. h0 + NW / wpr - 1 (those below H) of
@@ -192,19 +226,29 @@ __device__ __forceinline__ void combine_rows(const CParams& prm, int s, int np, 
   if (lane == 0 && prm.lse) prm.lse[orow] = Mr + logf(total);
 }
 
-template <typename T, int D, int NW>
-__global__ void __launch_bounds__(NW * 32) pa_combine_kernel(const __grid_constant__ CParams prm) {
+template <typename T, int D, int NW, bool VIEW>
+__global__ void __launch_bounds__(NW * 32, VIEW ? 5 : 1) pa_combine_kernel(const __grid_constant__ CParams prm) {
   __shared__ float4 s_acc[NW][D / 4];
   __shared__ float s_m[NW], s_t[NW];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int s = blockIdx.x;
-  const int np = seq_partitions(prm, s);
+  const int np = seq_partitions<VIEW>(prm, s, partition_tokens<NW, VIEW>(prm));
   // Partition states are phase 1's output; and no CTA ends before phase 1 has
   // (see the top).
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  // (What follows waits for this launch to complete; its own launch need not.)
+  if constexpr (VIEW) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (np <= 1) return;  // finished by phase 1 (or empty: zeros written there)
   const int rpc = NW / prm.wpr;
-  combine_rows<T, D, NW>(prm, s, np, prm.wpr, blockIdx.y * rpc, warp, lane, s_acc, s_m, s_t);
+  if constexpr (VIEW) {
+    // A CTA may have several groups: see the launch.
+    for (int h0 = blockIdx.y * rpc; h0 < prm.H; h0 += gridDim.y * rpc) {
+      combine_rows<T, D, NW>(prm, s, np, prm.wpr, h0, warp, lane, s_acc, s_m, s_t);
+      __syncthreads();  // the next one reuses s_acc, s_m, s_t
+    }
+  } else {
+    combine_rows<T, D, NW>(prm, s, np, prm.wpr, blockIdx.y * rpc, warp, lane, s_acc, s_m, s_t);
+  }
 }
 
 // Warps per row of a sequence with np partitions (pa_combine_rows_kernel).
@@ -214,13 +258,14 @@ __device__ __forceinline__ int rows_wpr(int np) {
   return w;
 }
 
-template <typename T, int D>
+template <typename T, int D, bool VIEW>
 __global__ void __launch_bounds__(kRowsWarps * 32, 1) pa_combine_rows_kernel(const __grid_constant__ CParams prm) {
   __shared__ float4 s_acc[kRowsWarps][D / 4];
   __shared__ float s_m[kRowsWarps], s_t[kRowsWarps];
   __shared__ int s_pref[kRowsMaxSeqs + 1];  // row groups before each sequence
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int S = prm.S;
+  const int P = partition_tokens<kRowsWarps, VIEW>(prm);
   // Row groups per sequence (none below two partitions) and their prefix:
   // one warp, 32 sequences a step, an inclusive shuffle scan.
   if (warp == 0) {
@@ -229,7 +274,7 @@ __global__ void __launch_bounds__(kRowsWarps * 32, 1) pa_combine_rows_kernel(con
       const int s = b + lane;
       int ng = 0;
       if (s < S) {
-        const int np = seq_partitions(prm, s);
+        const int np = seq_partitions<VIEW>(prm, s, P);
         if (np > 1) {
           const int rpc = kRowsWarps / rows_wpr(np);
           ng = (prm.H + rpc - 1) / rpc;
@@ -251,13 +296,14 @@ __global__ void __launch_bounds__(kRowsWarps * 32, 1) pa_combine_rows_kernel(con
   // Partition states are phase 1's output; and no CTA ends before phase 1 has
   // (see the top).
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  if constexpr (VIEW) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   for (int v = blockIdx.x; v < total; v += gridDim.x) {
     int lo = 0, hi = S;  // s_pref[lo] <= v < s_pref[lo + 1]
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
       if (s_pref[mid] <= v) lo = mid; else hi = mid;
     }
-    const int s = lo, np = seq_partitions(prm, s), wpr = rows_wpr(np), rpc = kRowsWarps / wpr;
+    const int s = lo, np = seq_partitions<VIEW>(prm, s, P), wpr = rows_wpr(np), rpc = kRowsWarps / wpr;
     combine_rows<T, D, kRowsWarps>(prm, s, np, wpr, (v - s_pref[s]) * rpc, warp, lane, s_acc, s_m, s_t);
     __syncthreads();  // the next row group reuses s_acc, s_m, s_t
   }

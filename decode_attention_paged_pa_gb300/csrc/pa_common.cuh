@@ -20,6 +20,7 @@ constexpr int kErrTimeout = 6;
 constexpr int kHdrError = 0;    // first device-side error code (0 = none)
 constexpr int kHdrWork = 1;     // dynamic work counter (units handed out)
 constexpr int kHdrWhere = 2;    // first timed-out wait: site, CTA, warp, detail (4 ints)
+constexpr int kHdrPart = 6;     // view rows: tokens of a partition in the last launch (for inspection)
 constexpr int kHdrInts = 64;    // header size in ints (256 bytes)
 
 constexpr float kLog2e = 1.4426950408889634f;

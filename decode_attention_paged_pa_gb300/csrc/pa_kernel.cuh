@@ -94,6 +94,7 @@ struct KParams {
   // `sinks` ones; masks: the trees' masks [S, q_len, words], or null.
   int window, sinks, words;
   const uint32_t* masks;
+  int units;  // the launch's work is cut into this many units, or more (0: partitions of P; see joined_partition)
 };
 
 // Cached tokens of sequence s, clamped to [0, max_len].  A length outside
@@ -268,7 +269,7 @@ struct UnitPlan {
 // partitions, whose combines are the longest chains, start first, and the
 // last units handed out belong to the shortest sequences.
 template <class C, int MODE>
-__device__ __forceinline__ UnitPlan plan_unit(const KParams& prm, const int* pref, const uint16_t* perm, int u) {
+__device__ __forceinline__ UnitPlan plan_unit(const KParams& prm, int P, const int* pref, const uint16_t* perm, int u) {
   constexpr int BS = C::BS, GT = C::GT;
   UnitPlan U;
   const int pair = u / prm.n_hg;
@@ -284,8 +285,8 @@ __device__ __forceinline__ UnitPlan plan_unit(const KParams& prm, const int* pre
   U.np = pref[lo + 1] - pref[lo];
   const int L = seq_tokens<MODE>(prm, U.s, prm.MB * C::BS, &bad);
   U.L = L;
-  U.t0 = U.p * prm.P;
-  U.t1 = min(U.t0 + prm.P, work_tokens<MODE>(prm, L, BS));
+  U.t0 = U.p * P;
+  U.t1 = min(U.t0 + P, work_tokens<MODE>(prm, L, BS));
   U.span = ViewSpan{0, 0};
   if constexpr (MODE == kView) U.span = view_span(L, prm.q_len, prm.window, prm.sinks, BS);
   U.nb = (U.t1 - U.t0 + BS - 1) / BS;
@@ -328,7 +329,7 @@ __device__ __forceinline__ int load_block_id(const KParams& prm, const UnitPlan&
 }
 
 template <class C, class LY, int MODE>
-__device__ __forceinline__ void producer_loop(const KParams& prm, uint8_t* smem, const int* pref,
+__device__ __forceinline__ void producer_loop(const KParams& prm, int P, uint8_t* smem, const int* pref,
                                               const uint16_t* perm, UnitInfo* info, volatile int* abort_flag,
                                               volatile uint32_t* issued, int lane) {
   using T = typename C::T;
@@ -345,7 +346,7 @@ __device__ __forceinline__ void producer_loop(const KParams& prm, uint8_t* smem,
   const int total = pref[prm.S] * prm.n_hg;
   auto plan_next = [&](int u, UnitPlan& Up) -> bool {
     if (u >= total) return false;
-    Up = plan_unit<C, MODE>(prm, pref, perm, u);
+    Up = plan_unit<C, MODE>(prm, P, pref, perm, u);
     return true;
   };
 
@@ -834,10 +835,11 @@ __device__ __forceinline__ void epilogue_loop(const KParams& prm, uint8_t* smem,
 // stable counting sort); pref[r] = partitions of ranks before r.  Lengths
 // are clamped to [0, MB*BS]; an out-of-range length is recorded as a device
 // error.  Temporaries live in `tmp`: the ring,
-// unused until the producer starts.
+// unused until the producer starts.  View rows: the partition's tokens follow from the
+// lengths, and are left in *part (joined_partition).
 template <int MODE, int BS, int THREADS>
 __device__ __forceinline__ void plan_order(const KParams& prm, uint8_t* tmp, int* pref, uint16_t* perm,
-                                           int* bad_len) {
+                                           int* bad_len, int* part) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   constexpr int NW = THREADS / 32;
   constexpr int NBK = 128;  // sort buckets
@@ -847,14 +849,46 @@ __device__ __forceinline__ void plan_order(const KParams& prm, uint8_t* tmp, int
   int* parts = bucket + NBK;                          // [S] partitions per sequence
   int* scan = parts + kMaxSeqsPerLaunch;              // [2 * NW] warp totals, then warp starts
   for (int i = tid; i < NBK; i += nthr) bucket[i] = 0;
-  __syncthreads();
-  for (int s = tid; s < S; s += nthr) {
-    bool bad = false;
-    const int L = work_tokens<MODE>(prm, seq_tokens<MODE>(prm, s, max_len, &bad), BS);
-    if (bad) *bad_len = 1;
-    const int np = (L + prm.P - 1) / prm.P;
-    parts[s] = np;
-    atomicAdd(&bucket[NBK - 1 - min(np, NBK - 1)], 1);
+  if constexpr (MODE == kView) {
+    unsigned* sums = reinterpret_cast<unsigned*>(scan + 64);  // [32][2] of the warps, and their longest
+    int* most = scan + 128;
+    unsigned long long sum = 0;
+    int longest = 0;
+    for (int s = tid; s < S; s += nthr) {
+      bool bad = false;
+      const int L = work_tokens<MODE>(prm, seq_tokens<MODE>(prm, s, max_len, &bad), BS);
+      if (bad) *bad_len = 1;
+      parts[s] = L;
+      sum += (unsigned)L;
+      longest = max(longest, L);
+    }
+    reduce_lengths(sum, longest);
+    if (lane == 0) {
+      sums[2 * warp] = (unsigned)sum & 0xffffu;
+      sums[2 * warp + 1] = (unsigned)(sum >> 16);  // (2^9 sequences of less than 2^30 tokens at most)
+      most[warp] = longest;
+    }
+    __syncthreads();
+    sum = __reduce_add_sync(0xffffffffu, lane < NW ? sums[2 * lane] : 0u) +
+          ((unsigned long long)__reduce_add_sync(0xffffffffu, lane < NW ? sums[2 * lane + 1] : 0u) << 16);
+    longest = __reduce_max_sync(0xffffffffu, lane < NW ? most[lane] : 0);
+    const int P = joined_partition(sum, longest, prm.P, prm.units, prm.n_hg, max_len);
+    if (tid == 0) *part = P;
+    for (int s = tid; s < S; s += nthr) {
+      const int np = (parts[s] + P - 1) / P;
+      parts[s] = np;
+      atomicAdd(&bucket[NBK - 1 - min(np, NBK - 1)], 1);
+    }
+  } else {
+    __syncthreads();
+    for (int s = tid; s < S; s += nthr) {
+      bool bad = false;
+      const int L = seq_tokens<MODE>(prm, s, max_len, &bad);
+      if (bad) *bad_len = 1;
+      const int np = (L + prm.P - 1) / prm.P;
+      parts[s] = np;
+      atomicAdd(&bucket[NBK - 1 - min(np, NBK - 1)], 1);
+    }
   }
   __syncthreads();
   if (warp == 0) {
@@ -927,7 +961,7 @@ __device__ __forceinline__ void plan_order(const KParams& prm, uint8_t* tmp, int
     run += parts[perm[r]];
   }
 }
-constexpr int kOrderTempBytes = (128 + kMaxSeqsPerLaunch + 64) * 4;  // plan_order's temporaries
+constexpr int kOrderTempBytes = (128 + kMaxSeqsPerLaunch + 160) * 4;  // plan_order's temporaries
 
 template <class C, int NC, int NSTAGE, int CTAS_PER_SM, int MODE>
 __global__ void __launch_bounds__(Layout<C, NC, NSTAGE>::THREADS, CTAS_PER_SM)
@@ -941,6 +975,7 @@ __global__ void __launch_bounds__(Layout<C, NC, NSTAGE>::THREADS, CTAS_PER_SM)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + LY::OFF_FLAGS);
   volatile uint32_t* issued = reinterpret_cast<volatile uint32_t*>(smem + LY::OFF_FLAGS + 8);
   int* bad_len = reinterpret_cast<int*>(smem + LY::OFF_FLAGS + 16);  // a length out of range
+  int* part = reinterpret_cast<int*>(smem + LY::OFF_FLAGS + 20);     // (kView) tokens of a partition
   int* pref = reinterpret_cast<int*>(smem + LY::OFF_PREF);
   uint16_t* perm = reinterpret_cast<uint16_t*>(smem + LY::perm_off(prm.S));
   UnitInfo* info = reinterpret_cast<UnitInfo*>(smem + LY::OFF_INFO);
@@ -962,15 +997,16 @@ __global__ void __launch_bounds__(Layout<C, NC, NSTAGE>::THREADS, CTAS_PER_SM)
     *bad_len = 0;
     fence_mbarrier_init();
   }
-  plan_order<MODE, C::BS, LY::THREADS>(prm, smem, pref, perm, bad_len);
+  plan_order<MODE, C::BS, LY::THREADS>(prm, smem, pref, perm, bad_len, part);
   __syncthreads();
   // This launch is a programmatic dependent of the kernel that clears the
   // workspace header: everything above overlaps it, nothing below may touch
   // the header before it has completed.
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (tid == 0 && *bad_len) atomicCAS(prm.hdr + kHdrError, 0, kErrDeviceBounds);
+  if (MODE == kView && tid == 0 && blockIdx.x == 0) prm.hdr[kHdrPart] = *part;
   if (warp == NC) {
-    producer_loop<C, LY, MODE>(prm, smem, pref, perm, info, abort_flag, issued, lane);
+    producer_loop<C, LY, MODE>(prm, MODE == kView ? *part : prm.P, smem, pref, perm, info, abort_flag, issued, lane);
   } else if (warp == NC + 1) {
     epilogue_loop<C, LY, MODE>(prm, smem, abort_flag, lane);
   } else {

@@ -257,7 +257,7 @@ struct RowsCta {
     return x;
   }
 
-  __device__ __forceinline__ void producer(const int* pref, const uint16_t* perm, int lane) {
+  __device__ __forceinline__ void producer(int P, const int* pref, const uint16_t* perm, int lane) {
     // Items issued together: as many as a warp has lanes for, up to half of the ring.
     // (One at a time took the producer 600 cycles an item, as long as its copy.)
     constexpr int NB = C::NB, GI = 32 / NB < C::PN / 2 ? 32 / NB : C::PN / 2;
@@ -272,7 +272,7 @@ struct RowsCta {
     while (ok) {
       const bool have = u < total;
       RowsUnit U{};
-      if (have) U = cut(plan_unit<C, kView>(prm, pref, perm, u));
+      if (have) U = cut(plan_unit<C, kView>(prm, P, pref, perm, u));
       else U.s = -1;
       Lane next = lane_item(U, li, lb);  // (no items without a unit)
       // Publish it.
@@ -1122,7 +1122,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) pa_rows_kernel(const __grid_con
   extern __shared__ __align__(1024) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   RowsCta<C> cta(prm, smem);
-  int* flags = reinterpret_cast<int*>(smem + C::OFF_FLAGS);  // abort, bad length, tensor memory; at 32 two barriers
+  int* flags = reinterpret_cast<int*>(smem + C::OFF_FLAGS);  // abort, bad length, tensor memory, partition; at 32 two barriers
   int* pref = reinterpret_cast<int*>(smem + C::OFF_PREF);
   uint16_t* perm = reinterpret_cast<uint16_t*>(smem + C::OFF_PERM);
   constexpr int WP = C::NP * 4, WM = WP + 1, WV = WP + 2, WQ = WP + 3;  // producer, product and Q warps
@@ -1157,13 +1157,14 @@ __global__ void __launch_bounds__(C::THREADS, 1) pa_rows_kernel(const __grid_con
     fence_mbarrier_init();
   }
   if (warp == WM) tmem_alloc(smem_addr(flags + 2), 512);
-  plan_order<kView, C::BS, C::THREADS>(prm, smem + C::OFF_RING, pref, perm, flags + 1);
+  plan_order<kView, C::BS, C::THREADS>(prm, smem + C::OFF_RING, pref, perm, flags + 1, flags + 3);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = (uint32_t)flags[2];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (tid == 0 && flags[1]) atomicCAS(prm.hdr + kHdrError, 0, kErrDeviceBounds);
+  if (tid == 0 && blockIdx.x == 0) prm.hdr[kHdrPart] = flags[3];
   if (warp < WP) {
     // Sequences with too few tokens: zeros.
     constexpr int D16 = C::D / 8;
@@ -1179,7 +1180,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) pa_rows_kernel(const __grid_con
     cta.softmax(tmem, warp >> 2, tid & 127);
   } else {
     if (warp == WP) {
-      cta.producer(pref, perm, lane);
+      cta.producer(flags[3], pref, perm, lane);
     } else if (warp == WM) {
       cta.score_products(tmem, lane);
     } else if (warp == WV) {

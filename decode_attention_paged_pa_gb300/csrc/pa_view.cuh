@@ -31,6 +31,29 @@ __device__ __forceinline__ int view_tokens(int L, int q_len, int window, int sin
   return L < q_len ? 0 : L - view_span(L, q_len, window, sinks, BS).skip * BS;
 }
 
+// Tokens of a partition of a launch of view rows, which has `sum` tokens to work on, `most`
+// of one sequence: partitions of P are taken together, in powers of two, as long as no unit
+// (of n_hg a partition) gets longer than one of `units` equal ones would be (0: never).  Each
+// unit has its start and its end, and states that are joined; but the longest one is what
+// the call may wait for, whatever the room in the tables.  Both phases work it out from
+// the lengths.
+__device__ __forceinline__ int joined_partition(unsigned long long sum, int most, int P, int units, int n_hg,
+                                                int max_len) {
+  if (units > 0) {
+    const unsigned long long work = sum * n_hg;  // (below 2^9 * 2^30 * 2^16)
+    while (P < most && (unsigned long long)min(2ll * P, (long long)most) * units <= work)
+      P = (int)min(2ll * P, (long long)max_len);
+  }
+  return P;
+}
+// `sum` and `most` over a warp; a thread's sum is of a few sequences, below 2^32.
+__device__ __forceinline__ void reduce_lengths(unsigned long long& sum, int& most) {
+  const unsigned lo = __reduce_add_sync(0xffffffffu, (unsigned)sum & 0xffffu);
+  const unsigned hi = __reduce_add_sync(0xffffffffu, (unsigned)sum >> 16);
+  sum = ((unsigned long long)hi << 16) + lo;
+  most = __reduce_max_sync(0xffffffffu, most);
+}
+
 // What row head h of sequence s (of L tokens) sees: position t where
 //   t < hi  and  (t >= lo or t < sinks)  and  (t < base or bit t - base of `bits`).
 // A window row at position p has lo = p - window + 1 and hi = base = p + 1.  A

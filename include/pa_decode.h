@@ -298,8 +298,11 @@ int pa_decode_v2_mq_fp8(void* out, float* lse, const void* query, const void* ke
  *               the window may have been given back
  *   q_len       1 .. 512
  *   workspace   >= pa_decode_v2_view_workspace_bytes(num_seqs, q_len, ...) bytes,
- *               or NULL.  Partitions count the visible blocks only, and where there
- *               is work enough without them several are taken together.
+ *               or NULL.  Partitions count the visible blocks only.  Over 16-bit
+ *               and E4M3 caches several are taken together where the lengths leave
+ *               every SM its share of the work without them: on the device, from the
+ *               lengths of the call (of each 256 or 512 sequences of it), whatever
+ *               room the tables have.
  * Elements, shapes, lse, ownership and errors are those of pa_decode_v2_mq (fp32:
  * not blocks of 64 tokens at head size 256, PA_ERR_UNSUPPORTED).  A key or value
  * that is not finite reaches the rows that see it, no others.
