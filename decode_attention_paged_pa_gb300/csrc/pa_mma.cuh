@@ -63,10 +63,11 @@ constexpr uint32_t al1024(uint32_t x) { return (x + 1023u) & ~1023u; }
 // the 8 columns of a tile hold the query heads of KVU = 8 / G consecutive kv
 // heads: a stage then holds one block of each of them (the cache keeps the kv
 // heads of a block contiguous, so still one copy for the keys and one for the
-// values), and each product runs once per kv head with the query (scores) or
-// weight (values) columns of the other kv heads zeroed, into the same
-// accumulators.  The softmax, the weights and the stage's waits then serve
-// KVU kv heads at once, and the copies are KVU times larger.
+// values), and each product runs once per kv head, into accumulators of its own,
+// of which each column's kv head's are used (with zeros in the other columns and
+// one set of accumulators, an infinity or NaN in one kv head's key or value made
+// the rows of the others NaN).  The softmax, the weights and the stage's waits
+// then serve KVU kv heads at once, and the copies are KVU times larger.
 // VIEW_: rows that see a window and the first tokens, or the nodes of a tree
 // (RowView): most work items are seen whole by every row of the unit and go
 // the same way as a causal unit's; in the others each score is masked by its
@@ -135,12 +136,11 @@ struct MmaConsumer {
     }
   }
 
-  // Q^T fragments (B operand) per column tile and kv head of the unit, packed
-  // element pairs (with KVU > 1, the columns of the other kv heads zero).
-  uint32_t qb[NK][NT * KVU_][2];
-  int ub;  // KVU > 1: the kv head (0 .. KVU - 1) of this lane's weight column
+  // Q^T fragments (B operand) per column tile, packed element pairs.
+  uint32_t qb[NK][NT][2];
   float m[NT][2], l[NT][2];  // heads 8t + 2*(lane%4) and 8t + 2*(lane%4) + 1 of tile t
-  float acc[NMT][NT][4];
+  static_assert(KVU_ == 1 || (KVU_ == 2 && NT == 1), "one kv head, or two in one column tile");
+  float acc[NMT][NT * KVU_][4];  // (per kv head of the unit)
   float scale_log2;
   int lim[NT][2];  // positions [0, lim) the lane's heads see (causal rows of multi-query decode)
 
@@ -225,8 +225,7 @@ struct MmaConsumer {
   // that see their tokens (weights w of the score fragment not 0) become what the
   // sums would: +-infinity, or NaN.  Infinities are counted by products with
   // 0 / 1 operands; a NaN counts as one of each sign.
-  __device__ __forceinline__ static void value_guard(uint32_t (&a)[4], float (&acc4)[4], const float (&w)[4],
-                                                     bool mine) {
+  __device__ __forceinline__ static void value_guard(uint32_t (&a)[4], float (&acc4)[4], const float (&w)[4]) {
     constexpr uint32_t kExp = std::is_same<MT, __half>::value ? 0x7c00u : 0x7f80u;
     constexpr uint32_t kOne = std::is_same<MT, __half>::value ? 0x3c00u : 0x3f80u;
     bool bad = false;
@@ -251,8 +250,8 @@ struct MmaConsumer {
     const uint32_t f0 = movmatrix_trans((w[0] != 0.f ? kOne : 0u) | (w[1] != 0.f ? kOne << 16 : 0u));
     const uint32_t f1 = movmatrix_trans((w[2] != 0.f ? kOne : 0u) | (w[3] != 0.f ? kOne << 16 : 0u));
     float nu[4] = {0.f, 0.f, 0.f, 0.f}, nd[4] = {0.f, 0.f, 0.f, 0.f};
-    Mma<MT>::run(nu, up, mine ? f0 : 0u, mine ? f1 : 0u);
-    Mma<MT>::run(nd, down, mine ? f0 : 0u, mine ? f1 : 0u);
+    Mma<MT>::run(nu, up, f0, f1);
+    Mma<MT>::run(nd, down, f0, f1);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if (nu[i] > 0.f) acc4[i] += INFINITY;
@@ -281,6 +280,9 @@ struct MmaConsumer {
     return (uint32_t)h.x | ((uint32_t)h.y << 16);
   }
 
+  // KVU = 2: whether this lane's columns 2 (lane % 4) and 2 (lane % 4) + 1 are the second kv head's.
+  __device__ __forceinline__ static bool second_head(int lane) { return (lane & 2) != 0; }
+
   // Positions each of this lane's heads may see: limit_of(h) for head h of
   // the unit (a single-query unit sees every position of the sequence).
   template <class F>
@@ -291,11 +293,9 @@ struct MmaConsumer {
       for (int j = 0; j < 2; ++j) lim[t][j] = limit_of(8 * t + (lane & 3) * 2 + j);
   }
 
-  // G: query heads per kv head (columns n of a KVU > 1 unit belong to kv
-  // head n / G of the unit).
-  __device__ __forceinline__ void begin_unit(const T* qs, int nh, float sl2, int lane, int G) {
+  // (A unit of two kv heads has four query rows of each: columns 4u .. 4u + 3.)
+  __device__ __forceinline__ void begin_unit(const T* qs, int nh, float sl2, int lane, int) {
     const int n = lane >> 2, kq = (lane & 3) * 2;
-    ub = KVU_ > 1 ? n / G : 0;
     const uint16_t* q16 = reinterpret_cast<const uint16_t*>(qs);
     if constexpr (kFp8) {
       // Dims 16ks + 4c .. +3 of head n, scaled by 2^s so that the unit's
@@ -325,12 +325,8 @@ struct MmaConsumer {
           lo = F16Traits<__half>::pack(a.x * up, a.y * up);
           hi = F16Traits<__half>::pack(b.x * up, b.y * up);
         }
-#pragma unroll
-        for (int u = 0; u < KVU_; ++u) {
-          const bool mine = KVU_ == 1 || ub == u;
-          qb[ks][u][0] = mine ? lo : 0u;
-          qb[ks][u][1] = mine ? hi : 0u;
-        }
+        qb[ks][0][0] = lo;
+        qb[ks][0][1] = hi;
       }
       sl2 *= down;
     } else {
@@ -344,12 +340,8 @@ struct MmaConsumer {
             lo = *reinterpret_cast<const uint32_t*>(q16 + h * QROW + ks * 16 + kq);
             hi = *reinterpret_cast<const uint32_t*>(q16 + h * QROW + ks * 16 + kq + 8);
           }
-#pragma unroll
-          for (int u = 0; u < KVU_; ++u) {
-            const bool mine = KVU_ == 1 || ub == u;
-            qb[ks][t * KVU_ + u][0] = mine ? lo : 0u;
-            qb[ks][t * KVU_ + u][1] = mine ? hi : 0u;
-          }
+          qb[ks][t][0] = lo;
+          qb[ks][t][1] = hi;
         }
     }
 #pragma unroll
@@ -360,7 +352,7 @@ struct MmaConsumer {
 #pragma unroll
     for (int mt = 0; mt < NMT; ++mt)
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
+      for (int t = 0; t < NT * KVU_; ++t)
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[mt][t][i] = 0.f;
     scale_log2 = sl2;
@@ -450,8 +442,8 @@ struct MmaConsumer {
     float sc[NTI][NT][4];
 #pragma unroll
     for (int tt = 0; tt < NTI; ++tt) {
-      // Two accumulators (even / odd k-steps) per column tile halve the
-      // dependent mma chain.
+      // Two accumulators per column tile halve the dependent mma chain: of the even
+      // and the odd k-steps, or of two kv heads.
       float c[NT][4], c2[NT][4];
 #pragma unroll
       for (int t = 0; t < NT; ++t)
@@ -467,8 +459,8 @@ struct MmaConsumer {
           ldmatrix_x4(kt[tt] + u * KTILE + (chunk * BS + tok) * 16, a);
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
-            if ((kk * KVU + u) & 1) Mma<T>::run(c2[t], a, qb[kk][t * KVU + u][0], qb[kk][t * KVU + u][1]);
-            else Mma<T>::run(c[t], a, qb[kk][t * KVU + u][0], qb[kk][t * KVU + u][1]);
+            if ((kk * KVU + u) & 1) Mma<T>::run(c2[t], a, qb[kk][t][0], qb[kk][t][1]);
+            else Mma<T>::run(c[t], a, qb[kk][t][0], qb[kk][t][1]);
           }
         }
       }
@@ -476,7 +468,7 @@ struct MmaConsumer {
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) c[t][i] += c2[t][i];
+        for (int i = 0; i < 4; ++i) c[t][i] = KVU == 1 ? c[t][i] + c2[t][i] : second_head(lane) ? c2[t][i] : c[t][i];
         if constexpr (VIEW_) {
           const int p_lo = pos_of(tok0, t_lo), p_hi = pos_of(tok0, t_hi);
           sc[tt][t][0] = t_lo < ntok && sees(p_lo, 0, partial) ? c[t][0] * scale_log2 : -INFINITY;
@@ -520,11 +512,11 @@ struct MmaConsumer {
 #pragma unroll
     for (int mt = 0; mt < NMT; ++mt)
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        acc[mt][t][0] *= alpha[t][0];
-        acc[mt][t][1] *= alpha[t][1];
-        acc[mt][t][2] *= alpha[t][0];
-        acc[mt][t][3] *= alpha[t][1];
+      for (int t = 0; t < NT * KVU; ++t) {
+        acc[mt][t][0] *= alpha[t / KVU][0];
+        acc[mt][t][1] *= alpha[t / KVU][1];
+        acc[mt][t][2] *= alpha[t / KVU][0];
+        acc[mt][t][3] *= alpha[t / KVU][1];
       }
     // Slots past the sequence end hold arbitrary cache contents: the value
     // fragments' elements of those tokens are zeroed in registers, so that
@@ -557,8 +549,6 @@ struct MmaConsumer {
       }
 #pragma unroll
       for (int u = 0; u < KVU; ++u) {
-        // kv head u's value product takes the weight columns of its own query heads.
-        const bool mine = KVU == 1 || ub == u;
 #pragma unroll
         for (int mt = 0; mt < NMT; ++mt) {
           uint32_t a[4];
@@ -572,12 +562,12 @@ struct MmaConsumer {
             a[0] &= k0; a[1] &= k0; a[2] &= k1; a[3] &= k1;
           }
           if constexpr (VIEW_) {
-            if (partial) value_guard(a, acc[mt][0], sc[tt][0], mine);
+            if (partial) value_guard(a, acc[mt][u], sc[tt][0]);
           }
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
-            Mma<T>::run(acc[mt][t], a, mine ? b0[t] : 0u, mine ? b1[t] : 0u);
-            if constexpr (kSplitWeights) Mma<T>::run(acc[mt][t], a, mine ? r0[t] : 0u, mine ? r1[t] : 0u);
+            Mma<T>::run(acc[mt][t * KVU + u], a, b0[t], b1[t]);
+            if constexpr (kSplitWeights) Mma<T>::run(acc[mt][t * KVU + u], a, r0[t], r1[t]);
           }
         }
       }
@@ -634,12 +624,12 @@ struct MmaConsumer {
         for (int kk = 0; kk < NK; ++kk) {
           const uint32_t a[4] = {e4m3x2(wk[kk][0]), e4m3x2(wk[kk][1]), e4m3x2(wk[kk][0] >> 16),
                                  e4m3x2(wk[kk][1] >> 16)};
-          if ((kk * KVU + u) & 1) Mma<__half>::run(c1, a, qb[kk][u][0], qb[kk][u][1]);
-          else Mma<__half>::run(c0, a, qb[kk][u][0], qb[kk][u][1]);
+          if ((kk * KVU + u) & 1) Mma<__half>::run(c1, a, qb[kk][0][0], qb[kk][0][1]);
+          else Mma<__half>::run(c0, a, qb[kk][0][0], qb[kk][0][1]);
         }
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) c0[i] += c1[i];
+      for (int i = 0; i < 4; ++i) c0[i] = KVU == 1 ? c0[i] + c1[i] : second_head(lane) ? c1[i] : c0[i];
       const int t_lo = tt * 16 + trow_lo, t_hi = tt * 16 + trow_hi;
       const int p_lo = pos_of(tok0, t_lo), p_hi = pos_of(tok0, t_hi);
       sc[tt][0] = t_lo < ntok && sees(p_lo, 0, partial) ? c0[0] * scale_log2 : -INFINITY;
@@ -682,10 +672,13 @@ struct MmaConsumer {
     }
 #pragma unroll
     for (int mt = 0; mt < NMT; ++mt) {
-      acc[mt][0][0] *= alpha[0];
-      acc[mt][0][1] *= alpha[1];
-      acc[mt][0][2] *= alpha[0];
-      acc[mt][0][3] *= alpha[1];
+#pragma unroll
+      for (int u = 0; u < KVU; ++u) {
+        acc[mt][u][0] *= alpha[0];
+        acc[mt][u][1] *= alpha[1];
+        acc[mt][u][2] *= alpha[0];
+        acc[mt][u][3] *= alpha[1];
+      }
     }
     // The weights' B fragments per tile (quads c >= 2 find their tokens 4c,
     // 4c+1 in score rows 2c+8, 2c+9), and the value bytes each tile keeps:
@@ -713,11 +706,8 @@ struct MmaConsumer {
             wv[tt][mt][1] = lds32(vv[tt] + u * KTILE + (mt * 16 + r + 8) * BS);
           }
       }
-      // kv head u's value product takes the weight columns of its own query heads.
-      const bool mine = KVU == 1 || ub == u;
 #pragma unroll
       for (int tt = 0; tt < NT2; ++tt) {
-        const uint32_t b0 = mine ? bw[tt][0] : 0u, b1 = mine ? bw[tt][1] : 0u;
 #pragma unroll
         for (int mt = 0; mt < NMT; ++mt) {
           const uint32_t v0 = wv[tt][mt][0] & vmask[tt], v1 = wv[tt][mt][1] & vmask[tt];
@@ -725,17 +715,16 @@ struct MmaConsumer {
           if constexpr (VIEW_) {
             // (The guard's products take the weights' rows in the tile's order: quads
             // c >= 2 find their tokens 4c, 4c + 1 in score rows 2c + 8, 2c + 9.)
-            if (partial) fp8_value_guard(a, acc[mt][0], sc[tt], mine, c);
+            if (partial) fp8_value_guard(a, acc[mt][u], sc[tt], c);
           }
-          Mma<__half>::run(acc[mt][0], a, b0, b1);
+          Mma<__half>::run(acc[mt][u], a, bw[tt][0], bw[tt][1]);
         }
       }
     }
   }
 
   // value_guard for a tile of E4M3 values (of which only NaN is not finite).
-  __device__ __forceinline__ static void fp8_value_guard(uint32_t (&a)[4], float (&acc4)[4], const float (&w)[4],
-                                                         bool mine, int c) {
+  __device__ __forceinline__ static void fp8_value_guard(uint32_t (&a)[4], float (&acc4)[4], const float (&w)[4], int c) {
     constexpr uint32_t kExp = 0x7c00u, kOne = 0x3c00u;
     bool bad = false;
 #pragma unroll
@@ -756,7 +745,7 @@ struct MmaConsumer {
     const uint32_t f1 = movmatrix_trans((w[2] != 0.f ? kOne : 0u) | (w[3] != 0.f ? kOne << 16 : 0u));
     const uint32_t b0 = c >= 2 ? f1 : f0, b1 = c >= 2 ? f0 : f1;
     float n[4] = {0.f, 0.f, 0.f, 0.f};
-    Mma<__half>::run(n, is, mine ? b0 : 0u, mine ? b1 : 0u);
+    Mma<__half>::run(n, is, b0, b1);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       if (n[i] > 0.f) acc4[i] = __int_as_float(0x7fffffff);
@@ -784,10 +773,13 @@ struct MmaConsumer {
         // Accumulator rows r and r + 8 of value tile mt hold dims mt * 16 + r and + 8.
         float* o = acc_out + (8 * t + hq) * AROW;
         const int d_lo = mt * 16 + r, d_hi = d_lo + 8;
-        o[d_lo] = acc[mt][t][0];
-        o[AROW + d_lo] = acc[mt][t][1];
-        o[d_hi] = acc[mt][t][2];
-        o[AROW + d_hi] = acc[mt][t][3];
+        float a[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) a[i] = KVU > 1 && second_head(lane) ? acc[mt][t * KVU + KVU - 1][i] : acc[mt][t * KVU][i];
+        o[d_lo] = a[0];
+        o[AROW + d_lo] = a[1];
+        o[d_hi] = a[2];
+        o[AROW + d_hi] = a[3];
       }
   }
 };
