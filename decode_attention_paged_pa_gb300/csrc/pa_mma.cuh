@@ -71,8 +71,8 @@ constexpr uint32_t al1024(uint32_t x) { return (x + 1023u) & ~1023u; }
 // VIEW_: rows that see a window and the first tokens, or the nodes of a tree
 // (RowView): most work items are seen whole by every row of the unit and go
 // the same way as a causal unit's; in the others each score is masked by its
-// row's view, and a value that is not finite reaches only the rows that see it
-// (its product with another row's zero weight would be NaN).
+// row's view, and a value that is not finite reaches the rows that see it, whatever
+// their weight, and no others (its product with their zero weight would be NaN).
 template <typename T_, int D_, int BS_, bool FP8_ = false, int KVU_ = 1, bool VIEW_ = false>
 struct MmaConsumer {
   using T = T_;
@@ -222,10 +222,10 @@ struct MmaConsumer {
 
   // The 16-bit value fragment `a` (dims x tokens, one k-step) of a partial item:
   // elements that are not finite are taken out, and the accumulators of the rows
-  // that see their tokens (weights w of the score fragment not 0) become what the
-  // sums would: +-infinity, or NaN.  Infinities are counted by products with
-  // 0 / 1 operands; a NaN counts as one of each sign.
-  __device__ __forceinline__ static void value_guard(uint32_t (&a)[4], float (&acc4)[4], const float (&w)[4]) {
+  // that see their tokens (seen, bit i: element i of the score fragment; its weight may
+  // be 0) become what the sums would: +-infinity, or NaN.  Infinities are counted by
+  // products with 0 / 1 operands; a NaN counts as one of each sign.
+  __device__ __forceinline__ static void value_guard(uint32_t (&a)[4], float (&acc4)[4], uint32_t seen) {
     constexpr uint32_t kExp = std::is_same<MT, __half>::value ? 0x7c00u : 0x7f80u;
     constexpr uint32_t kOne = std::is_same<MT, __half>::value ? 0x3c00u : 0x3f80u;
     bool bad = false;
@@ -247,8 +247,8 @@ struct MmaConsumer {
         a[i] &= ~(0xffffu << s);
       }
     }
-    const uint32_t f0 = movmatrix_trans((w[0] != 0.f ? kOne : 0u) | (w[1] != 0.f ? kOne << 16 : 0u));
-    const uint32_t f1 = movmatrix_trans((w[2] != 0.f ? kOne : 0u) | (w[3] != 0.f ? kOne << 16 : 0u));
+    const uint32_t f0 = movmatrix_trans((seen & 1u ? kOne : 0u) | (seen & 2u ? kOne << 16 : 0u));
+    const uint32_t f1 = movmatrix_trans((seen & 4u ? kOne : 0u) | (seen & 8u ? kOne << 16 : 0u));
     float nu[4] = {0.f, 0.f, 0.f, 0.f}, nd[4] = {0.f, 0.f, 0.f, 0.f};
     Mma<MT>::run(nu, up, f0, f1);
     Mma<MT>::run(nd, down, f0, f1);
@@ -439,6 +439,7 @@ struct MmaConsumer {
                                         bool has_b, int ntok, int lane, int tok0) {
     const int r = lane >> 2;
     const bool partial = is_partial(tok0, ntok);
+    uint32_t seen = 0;  // (view rows) bit 4 tt + i: element i of tile tt's score fragment
     float sc[NTI][NT][4];
 #pragma unroll
     for (int tt = 0; tt < NTI; ++tt) {
@@ -471,10 +472,13 @@ struct MmaConsumer {
         for (int i = 0; i < 4; ++i) c[t][i] = KVU == 1 ? c[t][i] + c2[t][i] : second_head(lane) ? c2[t][i] : c[t][i];
         if constexpr (VIEW_) {
           const int p_lo = pos_of(tok0, t_lo), p_hi = pos_of(tok0, t_hi);
-          sc[tt][t][0] = t_lo < ntok && sees(p_lo, 0, partial) ? c[t][0] * scale_log2 : -INFINITY;
-          sc[tt][t][1] = t_lo < ntok && sees(p_lo, 1, partial) ? c[t][1] * scale_log2 : -INFINITY;
-          sc[tt][t][2] = t_hi < ntok && sees(p_hi, 0, partial) ? c[t][2] * scale_log2 : -INFINITY;
-          sc[tt][t][3] = t_hi < ntok && sees(p_hi, 1, partial) ? c[t][3] * scale_log2 : -INFINITY;
+          const bool v[4] = {t_lo < ntok && sees(p_lo, 0, partial), t_lo < ntok && sees(p_lo, 1, partial),
+                             t_hi < ntok && sees(p_hi, 0, partial), t_hi < ntok && sees(p_hi, 1, partial)};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            sc[tt][t][i] = v[i] ? c[t][i] * scale_log2 : -INFINITY;
+            seen |= v[i] ? 1u << (4 * tt + i) : 0u;
+          }
           continue;
         }
         sc[tt][t][0] = (t_lo < ntok && tok0 + t_lo < lim[t][0]) ? c[t][0] * scale_log2 : -INFINITY;
@@ -562,7 +566,7 @@ struct MmaConsumer {
             a[0] &= k0; a[1] &= k0; a[2] &= k1; a[3] &= k1;
           }
           if constexpr (VIEW_) {
-            if (partial) value_guard(a, acc[mt][u], sc[tt][0]);
+            if (partial) value_guard(a, acc[mt][u], seen >> (4 * tt));
           }
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
@@ -607,6 +611,7 @@ struct MmaConsumer {
     const int r = lane >> 2, c = lane & 3;
     const int trow_lo = kTok(r), trow_hi = kTok(r + 8);
     const bool partial = is_partial(tok0, ntok);
+    uint32_t seen = 0;  // (view rows: as above)
     float sc[NT2][4];
 #pragma unroll
     for (int tt = 0; tt < NT2; ++tt) {
@@ -632,10 +637,13 @@ struct MmaConsumer {
       for (int i = 0; i < 4; ++i) c0[i] = KVU == 1 ? c0[i] + c1[i] : second_head(lane) ? c1[i] : c0[i];
       const int t_lo = tt * 16 + trow_lo, t_hi = tt * 16 + trow_hi;
       const int p_lo = pos_of(tok0, t_lo), p_hi = pos_of(tok0, t_hi);
-      sc[tt][0] = t_lo < ntok && sees(p_lo, 0, partial) ? c0[0] * scale_log2 : -INFINITY;
-      sc[tt][1] = t_lo < ntok && sees(p_lo, 1, partial) ? c0[1] * scale_log2 : -INFINITY;
-      sc[tt][2] = t_hi < ntok && sees(p_hi, 0, partial) ? c0[2] * scale_log2 : -INFINITY;
-      sc[tt][3] = t_hi < ntok && sees(p_hi, 1, partial) ? c0[3] * scale_log2 : -INFINITY;
+      const bool v[4] = {t_lo < ntok && sees(p_lo, 0, partial), t_lo < ntok && sees(p_lo, 1, partial),
+                         t_hi < ntok && sees(p_hi, 0, partial), t_hi < ntok && sees(p_hi, 1, partial)};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        sc[tt][i] = v[i] ? c0[i] * scale_log2 : -INFINITY;
+        if constexpr (VIEW_) seen |= v[i] ? 1u << (4 * tt + i) : 0u;
+      }
     }
     // Value words (dims mt*16 + r and + 8, tokens tt*16 + 4c .. +3) do not
     // depend on the weights: read them before the softmax.
@@ -715,7 +723,7 @@ struct MmaConsumer {
           if constexpr (VIEW_) {
             // (The guard's products take the weights' rows in the tile's order: quads
             // c >= 2 find their tokens 4c, 4c + 1 in score rows 2c + 8, 2c + 9.)
-            if (partial) fp8_value_guard(a, acc[mt][u], sc[tt], c);
+            if (partial) fp8_value_guard(a, acc[mt][u], seen >> (4 * tt), c);
           }
           Mma<__half>::run(acc[mt][u], a, bw[tt][0], bw[tt][1]);
         }
@@ -724,7 +732,7 @@ struct MmaConsumer {
   }
 
   // value_guard for a tile of E4M3 values (of which only NaN is not finite).
-  __device__ __forceinline__ static void fp8_value_guard(uint32_t (&a)[4], float (&acc4)[4], const float (&w)[4], int c) {
+  __device__ __forceinline__ static void fp8_value_guard(uint32_t (&a)[4], float (&acc4)[4], uint32_t seen, int c) {
     constexpr uint32_t kExp = 0x7c00u, kOne = 0x3c00u;
     bool bad = false;
 #pragma unroll
@@ -741,8 +749,8 @@ struct MmaConsumer {
         a[i] &= ~(0xffffu << s);
       }
     }
-    const uint32_t f0 = movmatrix_trans((w[0] != 0.f ? kOne : 0u) | (w[1] != 0.f ? kOne << 16 : 0u));
-    const uint32_t f1 = movmatrix_trans((w[2] != 0.f ? kOne : 0u) | (w[3] != 0.f ? kOne << 16 : 0u));
+    const uint32_t f0 = movmatrix_trans((seen & 1u ? kOne : 0u) | (seen & 2u ? kOne << 16 : 0u));
+    const uint32_t f1 = movmatrix_trans((seen & 4u ? kOne : 0u) | (seen & 8u ? kOne << 16 : 0u));
     const uint32_t b0 = c >= 2 ? f1 : f0, b1 = c >= 2 ? f0 : f1;
     float n[4] = {0.f, 0.f, 0.f, 0.f};
     Mma<__half>::run(n, is, b0, b1);

@@ -18,7 +18,7 @@ def place(vc, bt, s, t, kv, d, BS, value):
     vc[bt[s, t // BS], kv, d, t % BS] = value
 
 
-def check(case, spots, cache, n, window, sinks, see, P):
+def check(case, spots, cache, n, window, sinks, see, P, scale=0.09):
     """spots: (sequence, position, kv head, dim, +1, -1 or 0 for NaN)."""
     q, kc, vc, bt, lens = case
     BS, H, KH = vc.shape[3], q.shape[2], vc.shape[1]
@@ -27,8 +27,8 @@ def check(case, spots, cache, n, window, sinks, see, P):
         place(clean, bt, s, t, kv, d, BS, 0)
     for s, t, kv, d, sign in spots:
         place(vc, bt, s, t, kv, d, BS, NAN_E4M3 if cache == "e4m3" else sign * math.inf)
-    got, lse = run(q, kc, vc, bt, lens, 0.09, window, sinks, see, P=P)
-    ref, ref_lse = run(q, kc, clean, bt, lens, 0.09, window, sinks, see, P=P)
+    got, lse = run(q, kc, vc, bt, lens, scale, window, sinks, see, P=P)
+    ref, ref_lse = run(q, kc, clean, bt, lens, scale, window, sinks, see, P=P)
     assert bool(ref.isfinite().all())
     odd = torch.zeros_like(got, dtype=torch.bool)
     seen = [visible(int(L), n, window, sinks, None if see is None else see[s]) for s, L in enumerate(lens)]
@@ -79,6 +79,28 @@ def test_signs():
         got = check(case, spots, "same", n, 0, 0, see, 4096)[0, :, 0]
         assert got[0, 1] == math.inf and got[1, 1] == math.inf and got[1, 2] == -math.inf and got[3, 2] == -math.inf
         assert bool(got[2, 1].isnan())
+
+
+@pytest.mark.parametrize("shape", [("fp16", "same", 4, 4, 64, 16, 3), ("bf16", "same", 8, 2, 128, 32, 1), ("bf16", "same", 4, 1, 80, 8, 2),
+                                   ("fp16", "same", 2, 1, 256, 64, 4), ("fp16", "e4m3", 8, 2, 128, 16, 1), ("bf16", "e4m3", 4, 2, 64, 8, 4),
+                                   ("bf16", "e4m3", 2, 1, 256, 64, 3), ("fp32", "same", 2, 1, 64, 16, 4), ("fp16", "same", 8, 2, 128, 16, 9),
+                                   ("bf16", "e4m3", 8, 2, 64, 32, 9)], ids=lambda s: "-".join(map(str, s)))
+def test_also_where_the_weight_is_zero(shape):
+    """Scores hundreds apart: almost every weight is 0 in fp32.  A value that is not finite
+    reaches the rows that see it all the same, in nodes and at windows' edges."""
+    dtype, cache, H, KH, D, BS, n = shape
+    lens = [n + 60, n + 7, n]
+    see = torch.stack([ancestors(tree_parents(s, n)) for s in range(len(lens))])
+    g = torch.Generator().manual_seed(D)
+    for window, v in ((0, see), (20, None)):
+        case = make(D + n, T[dtype], cache, n, H, KH, D, BS, lens, window, 3 if v is None else 0, v, poison=False)
+        spots = []
+        for s, L in enumerate(lens):
+            for t in [0, L - 1, L - n, min(L - 1, max(0, L - n + 1 - window))] + torch.randint(0, L, (8,), generator=g).tolist():
+                spots.append((s, t, int(torch.randint(0, KH, (1,), generator=g)), int(torch.randint(0, D, (1,), generator=g)),
+                              int(torch.randint(0, 3, (1,), generator=g)) - 1))
+        # (One value a place: a later one replaces an earlier one in either form.)
+        check(case, list({x[:4]: x for x in spots}.values()), cache, n, window, 3 if v is None else 0, v, 4096, scale=30.0)
 
 
 def call_time(f):
