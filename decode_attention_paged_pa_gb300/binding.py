@@ -221,24 +221,33 @@ def _stream_handle(stream, like: torch.Tensor | None = None) -> int | None:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _new_workspace(nbytes: int, device: int, stream) -> torch.Tensor:
-    """A workspace for a call on ``stream`` (None: the current one), allocated
-    there: PyTorch's allocator gives memory that was dropped to later work of the
-    stream that it was allocated on, which has to be the call's."""
-    def empty():
-        return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=torch.device("cuda", device))
-
+def _on_stream(f, device: int, stream):
+    """``f()`` with ``stream`` (None: the current one) as PyTorch's current stream."""
     if stream is None:
-        return empty()
+        return f()
     handle = _stream_handle(stream)
     current = _raw_stream(device) if _raw_stream is not None else torch.cuda.current_stream(device).cuda_stream
     if handle == current:
-        return empty()
+        return f()
     if not isinstance(stream, torch.cuda.Stream):
         # (1 names the legacy default stream, as 0 does.)
         stream = torch.cuda.ExternalStream(0 if handle == 1 else handle, device=torch.device("cuda", device))
     with torch.cuda.stream(stream):
-        return empty()
+        return f()
+
+
+def _new_workspace(nbytes: int, device: int, stream) -> torch.Tensor:
+    """A workspace for a call on ``stream`` (None: the current one), allocated
+    there: PyTorch's allocator gives memory that was dropped to later work of the
+    stream that it was allocated on, which has to be the call's."""
+    return _on_stream(lambda: torch.empty(max(nbytes, 256), dtype=torch.uint8, device=torch.device("cuda", device)),
+                      device, stream)
+
+
+def _clear_status(workspace, device: int, stream) -> None:
+    """For a call without sequences, which the library returns from before it uses the
+    workspace: the status that :func:`device_status` reads is that of this call."""
+    _on_stream(lambda: workspace[:4].zero_(), device, stream)
 
 
 def _check_tensor(name, t, dtype=None, ndim=None):
@@ -807,6 +816,8 @@ def _decode_view(name, out, query, key_cache, value_cache, block_tables, seq_len
                 _stream_handle(stream, query), MB, NB, workspace.data_ptr(), workspace.numel())
     if st != PA_OK:
         raise PaError(st, name)
+    if S == 0:
+        _clear_status(workspace, dev, stream)
     return workspace
 
 
@@ -950,6 +961,8 @@ def pa_tree_accept(new_lens, key_caches, value_caches, block_tables, seq_lens, a
             workspace.numel())
     if st != PA_OK:
         raise PaError(st, "pa_tree_accept")
+    if S == 0:
+        _clear_status(workspace, dev, stream)
     return workspace
 
 

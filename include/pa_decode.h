@@ -758,6 +758,8 @@ int pa_decode_v2_static_scratch(void* out, const void* query, const void* key_ca
 /*
  * Device-side status of the last call that used `workspace`: synchronises
  * `stream`, copies the error word and stores it in *status (PA_OK if none).
+ * (A decode call or pa_tree_accept with num_seqs 0 enqueues nothing and does not use
+ * its workspace.)
  * Returns PA_OK, or PA_ERR_CUDA if the copy or the synchronisation failed.
  */
 int pa_decode_v2_device_status(const void* workspace, void* stream, int* status);

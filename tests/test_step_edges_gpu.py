@@ -41,3 +41,28 @@ def test_accept_reads_no_entry_outside_its_row_for_a_bad_path(dtype):
         for t, row in zip((16, 17), rows):
             ref[bt[5, t // BS], :, :, t % BS] = row
         assert torch.equal(got.view(torch.uint8), ref.view(torch.uint8))
+
+
+@pytest.mark.parametrize("given", [True, False])
+@pytest.mark.parametrize("op", ["accept", "window", "tree"])
+def test_a_call_without_sequences_has_a_status(op, given):
+    """On a workspace full of 0x7f bytes, on a side stream too; nothing else is touched."""
+    kc, vc = (t.to(DEV) for t in caches(1, 4, 2, 64, 16, torch.float16))
+    before = kc.clone(), vc.clone()
+    bt, none = torch.empty((0, 2), dtype=torch.int32, device=DEV), torch.empty((0,), dtype=torch.int32, device=DEV)
+    for stream in (None, torch.cuda.Stream()):
+        ws = torch.full((1024,), 0x7F, dtype=torch.uint8, device=DEV) if given else None
+        torch.cuda.synchronize()
+        if op == "accept":
+            ws = binding.pa_tree_accept(none, kc, vc, bt, none, torch.empty((0, 3), dtype=torch.int32, device=DEV), none, 4,
+                                        workspace=ws, stream=stream)
+        else:
+            q = torch.empty((0, 3, 4, 64), dtype=torch.float16, device=DEV)
+            args = (torch.empty_like(q), q, kc, vc, bt, none)
+            if op == "window":
+                ws = binding.pa_decode_v2_window(*args, 0.1, 16, workspace=ws, stream=stream)
+            else:
+                ws = binding.pa_decode_v2_tree(*args, torch.empty((0, 3, 1), dtype=torch.int32, device=DEV), 0.1, workspace=ws,
+                                               stream=stream)
+        assert binding.device_status(ws, stream) == binding.PA_OK
+        assert torch.equal(kc, before[0]) and torch.equal(vc, before[1])
