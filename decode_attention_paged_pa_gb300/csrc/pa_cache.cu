@@ -540,6 +540,14 @@ extern "C" int pa_cache_write(void* key_cache, void* value_cache, const void* ke
   if (!key_cache || !value_cache || !aligned(key_cache, 16) || !aligned(value_cache, 16)) return PA_ERR_INVALID_ARG;
   if (num_tokens > 0 && (!key || !value || !slots || !aligned(key, 16) || !aligned(value, 16) || !aligned(slots, 8)))
     return PA_ERR_INVALID_ARG;
+  const size_t N = (size_t)num_tokens, cache = (size_t)num_blocks * BS * (size_t)width * E, hdr = kHdrInts * sizeof(int);
+  const auto rows = [&](long long stride) { return N > 0 ? ((N - 1) * (size_t)stride + (size_t)width) * esz : 0; };
+  // (The first three are written.)
+  const struct { const void* p; size_t n; } a[] = {{key_cache, cache},        {value_cache, cache},        {workspace, hdr},
+                                                   {key, rows(key_stride)}, {value, rows(value_stride)}, {slots, 8 * N}};
+  for (int i = 0; i < 3; ++i)
+    for (int j = i + 1; j < 6; ++j)
+      if (overlap(a[i].p, a[i].n, a[j].p, a[j].n)) return PA_ERR_INVALID_ARG;
   WriteParams p = {};
   p.cache[0] = static_cast<uint8_t*>(key_cache);
   p.cache[1] = static_cast<uint8_t*>(value_cache);

@@ -462,8 +462,9 @@ int pa_pages_slots(int64_t* slots, int32_t* positions, int32_t* seq_ids, int32_t
  *                +-448 (infinities too; NaN becomes NaN), so that a code c stands for
  *                scale * c as pa_decode_v2_fp8 reads it; scales positive and finite
  *   workspace    >= 256 bytes, 16-byte aligned, required; holds the status
- * Only the rows' slots are written.  One launch on `stream`; it can be captured
- * into a CUDA graph.
+ * Only the rows' slots are written.  The caches and the workspace may not overlap
+ * one another nor what is read (PA_ERR_INVALID_ARG).  One launch on `stream`; it can be
+ * captured into a CUDA graph.
  */
 int pa_cache_write(void* key_cache, void* value_cache, const void* key, const void* value,
                    const int64_t* slots, float k_scale, float v_scale, int num_tokens, int num_kv_heads,
