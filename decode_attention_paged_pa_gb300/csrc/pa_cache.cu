@@ -26,9 +26,11 @@
 // for 156 MB (3.8 TB/s; 23 at the copy's rate), bound by the instructions of rounding and
 // transposing.  The paths of a batch's trees in eight layers 14 us (dependent loads: length,
 // path, table, row).
+#include <algorithm>
 #include <atomic>
 #include <climits>
 #include <cstring>
+#include <new>
 
 #include <cuda_fp8.h>
 
@@ -507,6 +509,22 @@ bool overlap(const void* a, size_t na, const void* b, size_t nb) {
   return a && b && na > 0 && nb > 0 && x < y + nb && y < x + na;
 }
 
+// Whether any two of the caches, `bytes` each, overlap.
+bool caches_overlap(void* const* keys, void* const* values, int n, size_t bytes) {
+  uintptr_t few[256], *at = few;
+  if (2 * (size_t)n > sizeof few / sizeof *few) at = new (std::nothrow) uintptr_t[2 * (size_t)n];
+  if (!at) return true;
+  for (int i = 0; i < n; ++i) {
+    at[2 * i] = reinterpret_cast<uintptr_t>(keys[i]);
+    at[2 * i + 1] = reinterpret_cast<uintptr_t>(values[i]);
+  }
+  std::sort(at, at + 2 * (size_t)n);
+  bool found = false;
+  for (int i = 1; i < 2 * n; ++i) found |= at[i] - at[i - 1] < bytes;
+  if (at != few) delete[] at;
+  return found;
+}
+
 bool head_size_ok(int D) { return D == 64 || D == 80 || D == 96 || D == 112 || D == 128 || D == 256; }
 bool block_size_ok(int BS) { return BS == 8 || BS == 16 || BS == 32 || BS == 64; }
 
@@ -607,6 +625,15 @@ extern "C" int pa_tree_accept(int32_t* new_lens, void* const* key_caches, void* 
   for (const auto& x : a)
     if (overlap(new_lens, s4, x.p, x.n) || (x.p != workspace && overlap(workspace, kHdrInts * sizeof(int), x.p, x.n)))
       return PA_ERR_INVALID_ARG;
+  const int E = cache_dtype == PA_DTYPE_E4M3 ? 1 : cache_dtype == PA_DTYPE_FP32 ? 4 : 2;
+  const size_t bytes = (size_t)num_blocks * num_kv_heads * D * BS * E;
+  if (caches_overlap(key_caches, value_caches, num_caches, bytes)) return PA_ERR_INVALID_ARG;
+  for (int i = 0; i < num_caches; ++i)
+    for (const void* c : {key_caches[i], value_caches[i]}) {
+      if (overlap(new_lens, s4, c, bytes)) return PA_ERR_INVALID_ARG;
+      for (const auto& x : a)
+        if (overlap(c, bytes, x.p, x.n)) return PA_ERR_INVALID_ARG;
+    }
   AcceptParams p = {};
   p.bt = block_tables;
   p.lens = seq_lens;
@@ -622,7 +649,6 @@ extern "C" int pa_tree_accept(int32_t* new_lens, void* const* key_caches, void* 
   p.NB = num_blocks;
   p.KH = num_kv_heads;
   p.D = D;
-  const int E = cache_dtype == PA_DTYPE_E4M3 ? 1 : cache_dtype == PA_DTYPE_FP32 ? 4 : 2;
   const long long cols = (long long)num_kv_heads * (D * E / 16 + D);
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(kAcceptThreads, 1, 1);

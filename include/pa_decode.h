@@ -400,7 +400,9 @@ int pa_tree_masks(int32_t* masks, int32_t* positions, const int32_t* parents, co
  * what they held or a moved token.
  *   key_caches, value_caches   HOST arrays of num_caches DEVICE pointers, 16-byte
  *               aligned: caches of one shape and element type (layouts of
- *               pa_decode_v2 and pa_decode_v2_fp8); read before the call returns
+ *               pa_decode_v2 and pa_decode_v2_fp8), each named once: none may overlap
+ *               another one or any other array (PA_ERR_INVALID_ARG); the two arrays
+ *               are read before the call returns
  *   accepted    [num_seqs, max_accepted] int32 (entries past num_accepted are not
  *               read); max_accepted 0 .. 512
  *   num_accepted  [num_seqs] int32, each in [0, max_accepted]

@@ -30,3 +30,27 @@ def write(**kw):
 ])
 def test_write_refuses_overlaps(kw):
     assert write(**kw) == BAD
+
+
+def accept(**kw):
+    a = dict(new=M, k=[8 * M, 10 * M], v=[9 * M, 11 * M], bt=2 * M, lens=3 * M, acc=4 * M, num=5 * M, S=2, n=5, A=4, KH=2, D=64,
+             BS=16, cdt=0, stream=None, MB=4, NB=8, ws=6 * M, bytes=256)
+    a.update(kw)
+    k, v = ((ctypes.c_void_p * len(a[x]))(*a[x]) for x in "kv")
+    return binding.lib().pa_tree_accept(a["new"], k, v, len(a["k"]), *[a[x] for x in (
+        "bt", "lens", "acc", "num", "S", "n", "A", "KH", "D", "BS", "cdt", "stream", "MB", "NB", "ws", "bytes")])
+
+
+LAYERS = [(100 + 2 * i) * M for i in range(200)]
+
+
+@pytest.mark.parametrize("kw", [
+    dict(k=[8 * M, 8 * M]), dict(v=[8 * M, 11 * M]), dict(v=[9 * M, 10 * M]), dict(k=[8 * M, 9 * M + CACHE - 16]),
+    dict(k=[11 * M + CACHE - 16, 10 * M]), dict(k=[8 * M], v=[8 * M]), dict(cdt=3, k=[8 * M, 9 * M - CACHE // 2 + 16]),
+    dict(cdt=2, k=[8 * M, 9 * M + 2 * CACHE - 16]),
+    dict(k=LAYERS, v=[x + M for x in LAYERS[:-1]] + [LAYERS[3] + M]),  # more than one launch takes
+    dict(new=8 * M + 64), dict(new=11 * M + CACHE - 4), dict(ws=9 * M - 240), dict(bt=10 * M), dict(lens=10 * M + 4),
+    dict(acc=9 * M + CACHE - 4), dict(num=8 * M - 4),
+])
+def test_accept_refuses_overlaps(kw):
+    assert accept(**kw) == BAD
