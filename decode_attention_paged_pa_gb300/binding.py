@@ -63,6 +63,7 @@ EXPORTED_SYMBOLS = (
     "pa_decode_v2_window_fp8",
     "pa_decode_v2_tree",
     "pa_decode_v2_tree_fp8",
+    "pa_decode_v2_view_ex",
     "pa_decode_v2_view_workspace_bytes",
     "pa_tree_masks",
     "pa_tree_accept",
@@ -140,7 +141,11 @@ def _declare(lib):
     # ... with the masks after the lengths
     lib.pa_decode_v2_tree.argtypes = [vp, vp] + base[1:6] + [vp, cf] + [ci] * 4 + base[8:]
     lib.pa_decode_v2_tree_fp8.argtypes = [vp, vp] + base[1:6] + [vp, cf, cf, cf] + [ci] * 4 + base[8:]
-    for fn in (lib.pa_decode_v2_window, lib.pa_decode_v2_window_fp8, lib.pa_decode_v2_tree, lib.pa_decode_v2_tree_fp8):
+    # ... with masks, scales and, after the dtype, tree and fp8 always, and the controls
+    lib.pa_decode_v2_view_ex.argtypes = ([vp, vp] + base[1:6] + [vp, cf, cf, cf] + [ci] * 4 + base[8:14] + [ci, ci] + base[14:] +
+                                         [ci, cll])
+    for fn in (lib.pa_decode_v2_window, lib.pa_decode_v2_window_fp8, lib.pa_decode_v2_tree, lib.pa_decode_v2_tree_fp8,
+               lib.pa_decode_v2_view_ex):
         fn.restype = ci
     lib.pa_decode_v2_view_workspace_bytes.argtypes = [ci] * 10
     lib.pa_decode_v2_view_workspace_bytes.restype = cs
@@ -768,7 +773,7 @@ def view_workspace_bytes(num_seqs, q_len, num_heads, num_kv_heads, head_size, ma
 
 
 def _decode_view(name, out, query, key_cache, value_cache, block_tables, seq_lens, masks, scale, scales, window, sinks,
-                 partition_size, workspace, stream, lse):
+                 partition_size, workspace, stream, lse, max_ctas=0, timeout_ns=0):
     fp8 = scales is not None
     dt, ndim = query.dtype, query.dim()
     if dt not in (_DTYPE_CODE if fp8 else _DTYPE_CODE_F32):
@@ -805,15 +810,22 @@ def _decode_view(name, out, query, key_cache, value_cache, block_tables, seq_len
         raise PaError(PA_ERR_INVALID_ARG, name)
     workspace = _need_workspace(
         workspace, dev, lambda: view_workspace_bytes(S, QL, H, KH, D, MB, BS, partition_size, window, sinks), stream)
-    fn = getattr(lib(), name + ("_fp8" if fp8 else ""))
     args = (out.data_ptr(), _ptr(lse), query.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(),
             block_tables.data_ptr(), seq_lens.data_ptr())
-    if masks is not None:
-        args += (masks.data_ptr(),)
-    args += (float(scale),) + (scales if fp8 else ())
+    sizes = (window, sinks, S, QL, H, KH, D, BS, int(partition_size), _DTYPE_CODE_F32[dt])
+    if max_ctas or timeout_ns:
+        fn = lib().pa_decode_v2_view_ex
+        args += (_ptr(masks), float(scale), *(scales if fp8 else (1.0, 1.0)))
+        sizes += (int(masks is not None), int(fp8))
+        more = (int(max_ctas), int(timeout_ns))
+    else:
+        fn = getattr(lib(), name + ("_fp8" if fp8 else ""))
+        if masks is not None:
+            args += (masks.data_ptr(),)
+        args += (float(scale),) + (scales if fp8 else ())
+        more = ()
     with _current(dev):
-        st = fn(*args, window, sinks, S, QL, H, KH, D, BS, int(partition_size), _DTYPE_CODE_F32[dt],
-                _stream_handle(stream, query), MB, NB, workspace.data_ptr(), workspace.numel())
+        st = fn(*args, *sizes, _stream_handle(stream, query), MB, NB, workspace.data_ptr(), workspace.numel(), *more)
     if st != PA_OK:
         raise PaError(st, name)
     if S == 0:
@@ -829,52 +841,57 @@ def _need_query(query, *ndims):
 
 def pa_decode_v2_window(out, query, key_cache, value_cache, block_tables, seq_lens, scale: float, window: int,
                         sinks: int = 0, partition_size: int = 512, workspace: torch.Tensor | None = None,
-                        stream=None, lse: torch.Tensor | None = None):
+                        stream=None, lse: torch.Tensor | None = None, max_ctas: int = 0, timeout_ns: int = 0):
     """Attention to a sliding window and the first ``sinks`` tokens (see
     include/pa_decode.h): query/out [S, H, D] or [S, q_len, H, D]; a row at
     position p sees t <= p with t > p - window or t < sinks.  Caches, tables and
     ``lse`` as for :func:`pa_decode_v2` and :func:`pa_decode_v2_mq`.  Table entries
-    of blocks that no row sees are not read.  Returns the workspace used."""
+    of blocks that no row sees are not read.  ``max_ctas`` and ``timeout_ns`` are the
+    controls of ``pa_decode_v2_view_ex``.  Returns the workspace used."""
     _need_query(query, 3, 4)
     return _decode_view("pa_decode_v2_window", out, query, key_cache, value_cache, block_tables, seq_lens, None, scale,
-                        None, window, sinks, partition_size, workspace, stream, lse)
+                        None, window, sinks, partition_size, workspace, stream, lse, max_ctas, timeout_ns)
 
 
 def pa_decode_v2_window_fp8(out, query, key_cache, value_cache, block_tables, seq_lens, scale: float, window: int,
                             sinks: int = 0, k_scale: float = 1.0, v_scale: float = 1.0, partition_size: int = 512,
-                            workspace: torch.Tensor | None = None, stream=None, lse: torch.Tensor | None = None):
+                            workspace: torch.Tensor | None = None, stream=None, lse: torch.Tensor | None = None,
+                            max_ctas: int = 0, timeout_ns: int = 0):
     """:func:`pa_decode_v2_window` over an E4M3 cache (caches and scales of
     :func:`pa_decode_v2_fp8`).  Returns the workspace used."""
     _need_query(query, 3, 4)
     return _decode_view("pa_decode_v2_window", out, query, key_cache, value_cache, block_tables, seq_lens, None, scale,
-                        (float(k_scale), float(v_scale)), window, sinks, partition_size, workspace, stream, lse)
+                        (float(k_scale), float(v_scale)), window, sinks, partition_size, workspace, stream, lse, max_ctas,
+                        timeout_ns)
 
 
 def pa_decode_v2_tree(out, query, key_cache, value_cache, block_tables, seq_lens, masks, scale: float, window: int = 0,
                       sinks: int = 0, partition_size: int = 512, workspace: torch.Tensor | None = None, stream=None,
-                      lse: torch.Tensor | None = None):
+                      lse: torch.Tensor | None = None, max_ctas: int = 0, timeout_ns: int = 0):
     """Attention for a tree of drafted tokens, each sequence's last ``n`` cached
     ones (see include/pa_decode.h): query/out [S, n, H, D]; masks int32
     [S, n, ceil(n / 32)] as :func:`pa_tree_masks` makes them; every node sees the
     tokens before the tree (within ``window``, if it is not 0, and the first
     ``sinks``) and the nodes of its mask; a node without a bit is padding.
+    ``max_ctas`` and ``timeout_ns`` are the controls of ``pa_decode_v2_view_ex``.
     Returns the workspace used."""
     _need_query(query, 4)
     _check_tensor("masks", masks)
     return _decode_view("pa_decode_v2_tree", out, query, key_cache, value_cache, block_tables, seq_lens, masks, scale,
-                        None, window, sinks, partition_size, workspace, stream, lse)
+                        None, window, sinks, partition_size, workspace, stream, lse, max_ctas, timeout_ns)
 
 
 def pa_decode_v2_tree_fp8(out, query, key_cache, value_cache, block_tables, seq_lens, masks, scale: float,
                           window: int = 0, sinks: int = 0, k_scale: float = 1.0, v_scale: float = 1.0,
                           partition_size: int = 512, workspace: torch.Tensor | None = None, stream=None,
-                          lse: torch.Tensor | None = None):
+                          lse: torch.Tensor | None = None, max_ctas: int = 0, timeout_ns: int = 0):
     """:func:`pa_decode_v2_tree` over an E4M3 cache (caches and scales of
     :func:`pa_decode_v2_fp8`).  Returns the workspace used."""
     _need_query(query, 4)
     _check_tensor("masks", masks)
     return _decode_view("pa_decode_v2_tree", out, query, key_cache, value_cache, block_tables, seq_lens, masks, scale,
-                        (float(k_scale), float(v_scale)), window, sinks, partition_size, workspace, stream, lse)
+                        (float(k_scale), float(v_scale)), window, sinks, partition_size, workspace, stream, lse, max_ctas,
+                        timeout_ns)
 
 
 def pa_tree_masks(masks, positions, parents, seq_lens, workspace: torch.Tensor | None = None, stream=None):

@@ -558,17 +558,31 @@ extern "C" size_t pa_decode_v2_view_workspace_bytes(int num_seqs, int q_len, int
   return w.total;
 }
 
+extern "C" int pa_decode_v2_view_ex(void* out, float* lse, const void* query, const void* key_cache,
+                                    const void* value_cache, const int32_t* block_tables, const int32_t* seq_lens,
+                                    const int32_t* masks, float scale, float k_scale, float v_scale, int window,
+                                    int sinks, int num_seqs, int q_len, int num_heads, int num_kv_heads, int head_size,
+                                    int block_size, int partition_size, int dtype, int tree, int fp8, void* stream,
+                                    int max_blocks_per_seq, int num_blocks, void* workspace, size_t workspace_bytes,
+                                    int max_ctas, long long timeout_ns) {
+  if (!fp8 && (k_scale != 1.f || v_scale != 1.f)) return PA_ERR_INVALID_ARG;
+  const ViewArgs view = {view_tokens_arg(window), view_tokens_arg(sinks), masks, tree != 0};
+  return decode_impl(out, lse, query, key_cache, value_cache, block_tables, seq_lens, scale, num_seqs, q_len,
+                     num_heads, num_kv_heads, head_size, block_size, partition_size, dtype, stream,
+                     max_blocks_per_seq, num_blocks, workspace, workspace_bytes, PA_VARIANT_AUTO, max_ctas, timeout_ns,
+                     fp8 != 0, k_scale, v_scale, false, &view);
+}
+
 extern "C" int pa_decode_v2_window(void* out, float* lse, const void* query, const void* key_cache,
                                    const void* value_cache, const int32_t* block_tables, const int32_t* seq_lens,
                                    float scale, int window, int sinks, int num_seqs, int q_len, int num_heads,
                                    int num_kv_heads, int head_size, int block_size, int partition_size, int dtype,
                                    void* stream, int max_blocks_per_seq, int num_blocks, void* workspace,
                                    size_t workspace_bytes) {
-  const ViewArgs view = {view_tokens_arg(window), view_tokens_arg(sinks), nullptr, false};
-  return decode_impl(out, lse, query, key_cache, value_cache, block_tables, seq_lens, scale, num_seqs, q_len,
-                     num_heads, num_kv_heads, head_size, block_size, partition_size, dtype, stream,
-                     max_blocks_per_seq, num_blocks, workspace, workspace_bytes, PA_VARIANT_AUTO, 0, 0, false, 1.f,
-                     1.f, false, &view);
+  return pa_decode_v2_view_ex(out, lse, query, key_cache, value_cache, block_tables, seq_lens, nullptr, scale, 1.f, 1.f,
+                              window, sinks, num_seqs, q_len, num_heads, num_kv_heads, head_size, block_size,
+                              partition_size, dtype, 0, 0, stream, max_blocks_per_seq, num_blocks, workspace,
+                              workspace_bytes, 0, 0);
 }
 
 extern "C" int pa_decode_v2_window_fp8(void* out, float* lse, const void* query, const void* key_cache,
@@ -578,11 +592,10 @@ extern "C" int pa_decode_v2_window_fp8(void* out, float* lse, const void* query,
                                        int num_kv_heads, int head_size, int block_size, int partition_size,
                                        int dtype, void* stream, int max_blocks_per_seq, int num_blocks,
                                        void* workspace, size_t workspace_bytes) {
-  const ViewArgs view = {view_tokens_arg(window), view_tokens_arg(sinks), nullptr, false};
-  return decode_impl(out, lse, query, key_cache, value_cache, block_tables, seq_lens, scale, num_seqs, q_len,
-                     num_heads, num_kv_heads, head_size, block_size, partition_size, dtype, stream,
-                     max_blocks_per_seq, num_blocks, workspace, workspace_bytes, PA_VARIANT_AUTO, 0, 0, true,
-                     k_scale, v_scale, false, &view);
+  return pa_decode_v2_view_ex(out, lse, query, key_cache, value_cache, block_tables, seq_lens, nullptr, scale, k_scale,
+                              v_scale, window, sinks, num_seqs, q_len, num_heads, num_kv_heads, head_size, block_size,
+                              partition_size, dtype, 0, 1, stream, max_blocks_per_seq, num_blocks, workspace,
+                              workspace_bytes, 0, 0);
 }
 
 extern "C" int pa_decode_v2_tree(void* out, float* lse, const void* query, const void* key_cache,
@@ -591,11 +604,10 @@ extern "C" int pa_decode_v2_tree(void* out, float* lse, const void* query, const
                                  int num_nodes, int num_heads, int num_kv_heads, int head_size, int block_size,
                                  int partition_size, int dtype, void* stream, int max_blocks_per_seq,
                                  int num_blocks, void* workspace, size_t workspace_bytes) {
-  const ViewArgs view = {view_tokens_arg(window), view_tokens_arg(sinks), masks, true};
-  return decode_impl(out, lse, query, key_cache, value_cache, block_tables, seq_lens, scale, num_seqs, num_nodes,
-                     num_heads, num_kv_heads, head_size, block_size, partition_size, dtype, stream,
-                     max_blocks_per_seq, num_blocks, workspace, workspace_bytes, PA_VARIANT_AUTO, 0, 0, false, 1.f,
-                     1.f, false, &view);
+  return pa_decode_v2_view_ex(out, lse, query, key_cache, value_cache, block_tables, seq_lens, masks, scale, 1.f, 1.f,
+                              window, sinks, num_seqs, num_nodes, num_heads, num_kv_heads, head_size, block_size,
+                              partition_size, dtype, 1, 0, stream, max_blocks_per_seq, num_blocks, workspace,
+                              workspace_bytes, 0, 0);
 }
 
 extern "C" int pa_decode_v2_tree_fp8(void* out, float* lse, const void* query, const void* key_cache,
@@ -605,11 +617,10 @@ extern "C" int pa_decode_v2_tree_fp8(void* out, float* lse, const void* query, c
                                      int num_heads, int num_kv_heads, int head_size, int block_size,
                                      int partition_size, int dtype, void* stream, int max_blocks_per_seq,
                                      int num_blocks, void* workspace, size_t workspace_bytes) {
-  const ViewArgs view = {view_tokens_arg(window), view_tokens_arg(sinks), masks, true};
-  return decode_impl(out, lse, query, key_cache, value_cache, block_tables, seq_lens, scale, num_seqs, num_nodes,
-                     num_heads, num_kv_heads, head_size, block_size, partition_size, dtype, stream,
-                     max_blocks_per_seq, num_blocks, workspace, workspace_bytes, PA_VARIANT_AUTO, 0, 0, true,
-                     k_scale, v_scale, false, &view);
+  return pa_decode_v2_view_ex(out, lse, query, key_cache, value_cache, block_tables, seq_lens, masks, scale, k_scale,
+                              v_scale, window, sinks, num_seqs, num_nodes, num_heads, num_kv_heads, head_size,
+                              block_size, partition_size, dtype, 1, 1, stream, max_blocks_per_seq, num_blocks,
+                              workspace, workspace_bytes, 0, 0);
 }
 
 extern "C" int pa_decode_v2_ex(void* out, const void* query, const void* key_cache,

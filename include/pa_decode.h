@@ -362,6 +362,21 @@ int pa_decode_v2_tree_fp8(void* out, float* lse, const void* query, const void* 
                           int max_blocks_per_seq, int num_blocks, void* workspace, size_t workspace_bytes);
 
 /*
+ * pa_decode_v2_window (tree 0; masks are not used) and pa_decode_v2_tree (tree 1), over
+ * E4M3 caches where fp8 is 1 (else k_scale and v_scale are 1), with the controls of
+ * pa_decode_v2_ex, for tests and measurement: max_ctas bounds the persistent grid (0 =
+ * one CTA per SM), timeout_ns every device-side wait (0 = 2^31 ns); a wait that runs out
+ * is recorded as PA_ERR_TIMEOUT, and the output is then not complete.
+ */
+int pa_decode_v2_view_ex(void* out, float* lse, const void* query, const void* key_cache,
+                         const void* value_cache, const int32_t* block_tables, const int32_t* seq_lens,
+                         const int32_t* masks, float scale, float k_scale, float v_scale, int window, int sinks,
+                         int num_seqs, int q_len, int num_heads, int num_kv_heads, int head_size,
+                         int block_size, int partition_size, int dtype, int tree, int fp8, void* stream,
+                         int max_blocks_per_seq, int num_blocks, void* workspace, size_t workspace_bytes,
+                         int max_ctas, long long timeout_ns);
+
+/*
  * Bytes of workspace for pa_decode_v2_window and pa_decode_v2_tree (q_len:
  * num_nodes; window 0: a tree without one).  0 for invalid sizes.
  */
