@@ -150,3 +150,28 @@ def test_one_value_of_a_long_sequence_costs_little(cache, H, D):
     assert torch.equal(~out.isfinite().cpu(), odd)
     assert torch.equal(out.cpu()[~odd], ref.cpu()[~odd])
     assert with_one < 3 * clean + 1, f"{with_one:.3f} ms, {clean:.3f} without"
+
+
+@pytest.mark.parametrize("shape", SHAPES, ids=["-".join(map(str, s)) for s in SHAPES])
+def test_keys_with_many_rows(shape):
+    """A key with a NaN (or infinities, whose products with a row are an infinity or NaN):
+    the rows of its kv head that see it are NaN with a NaN log-sum-exp; in nodes, at
+    windows' edges and in tiles that every row sees.  Others: as with the key replaced."""
+    dtype, cache, H, KH, D, BS = shape
+    n, lens = 40, [40 + 700, 40 + 3]
+    see = torch.stack([ancestors(tree_parents(s, n, n - s)) for s in range(len(lens))])
+    for window, v in ((0, see), (300, None)):
+        q, kc, vc, bt, L = make(D, T[dtype], cache, n, H, KH, D, BS, lens, window, 2, v, poison=False)
+        seen = [visible(length, n, window, 2, None if v is None else v[s]) for s, length in enumerate(lens)]
+        ref, ref_lse = run(q, kc, vc, bt, L, 0.09, window, 2, v, P=256)
+        bad = [NAN_E4M3] if cache == "e4m3" else [math.nan, math.inf, -math.inf]
+        for s, length in enumerate(lens):
+            for i, t in enumerate([length - 2, length - n + 5, max(0, length - n + 3 - window), max(0, length - 130)]):
+                k2 = kc.clone()
+                k2[bt[s, t // BS], KH - 1, :, t % BS] = bad[i % len(bad)]
+                got, lse = run(q, k2, vc, bt, L, 0.09, window, 2, v, P=256)
+                hit = torch.zeros(lse.shape, dtype=torch.bool)
+                hit[s, :, (KH - 1) * (H // KH):] = seen[s][:, t, None]
+                # (An infinity times a row of both signs is NaN; the rows are not of one sign.)
+                assert bool(got[hit].isnan().all()) and bool(lse[hit].isnan().all())
+                assert torch.equal(lse[~hit], ref_lse[~hit]) and torch.equal(got[~hit], ref[~hit])
