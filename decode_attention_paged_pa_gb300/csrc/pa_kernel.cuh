@@ -831,7 +831,8 @@ __device__ __forceinline__ void epilogue_loop(const KParams& prm, uint8_t* smem,
 
 // Longest-first order.  Every CTA computes the same order from the lengths:
 // perm[r] = the sequence of rank r, sequences sorted by partition count,
-// most first (counts of 127 or more as equals), ties in batch order (a
+// most first (counts of 127 or more as equals; view rows, whose partitions may
+// be whole sequences: by tokens, in 16ths of the longest), ties in batch order (a
 // stable counting sort); pref[r] = partitions of ranks before r.  Lengths
 // are clamped to [0, MB*BS]; an out-of-range length is recorded as a device
 // error.  Temporaries live in `tmp`: the ring,
@@ -848,6 +849,7 @@ __device__ __forceinline__ void plan_order(const KParams& prm, uint8_t* tmp, int
   int* bucket = reinterpret_cast<int*>(tmp);       // [NBK] counts, then next free rank
   int* parts = bucket + NBK;                          // [S] partitions per sequence
   int* scan = parts + kMaxSeqsPerLaunch;              // [2 * NW] warp totals, then warp starts
+  int* keys = scan + 160;                             // [S] sort buckets (kView)
   for (int i = tid; i < NBK; i += nthr) bucket[i] = 0;
   if constexpr (MODE == kView) {
     unsigned* sums = reinterpret_cast<unsigned*>(scan + 64);  // [32][2] of the warps, and their longest
@@ -874,10 +876,12 @@ __device__ __forceinline__ void plan_order(const KParams& prm, uint8_t* tmp, int
     longest = __reduce_max_sync(0xffffffffu, lane < NW ? most[lane] : 0);
     const int P = joined_partition(sum, longest, prm.P, prm.units, prm.n_hg, max_len);
     if (tid == 0) *part = P;
+    const float step = 16.f / (float)(longest + 1);
     for (int s = tid; s < S; s += nthr) {
-      const int np = (parts[s] + P - 1) / P;
-      parts[s] = np;
-      atomicAdd(&bucket[NBK - 1 - min(np, NBK - 1)], 1);
+      const int L = parts[s], key = NBK - 1 - min((int)((float)L * step), 15);
+      parts[s] = (L + P - 1) / P;
+      keys[s] = key;
+      atomicAdd(&bucket[key], 1);
     }
   } else {
     __syncthreads();
@@ -916,7 +920,7 @@ __device__ __forceinline__ void plan_order(const KParams& prm, uint8_t* tmp, int
     // take consecutive ranks in lane order.
     for (int c0 = 0; c0 < S; c0 += 32) {
       const int s = c0 + lane;
-      const int key = s < S ? NBK - 1 - min(parts[s], NBK - 1) : -1 - lane;
+      const int key = s >= S ? -1 - lane : MODE == kView ? keys[s] : NBK - 1 - min(parts[s], NBK - 1);
       const unsigned peers = __match_any_sync(0xffffffffu, key);
       const int before = __popc(peers & ((1u << lane) - 1u));
       const int base = s < S ? bucket[key] : 0;
@@ -961,7 +965,7 @@ __device__ __forceinline__ void plan_order(const KParams& prm, uint8_t* tmp, int
     run += parts[perm[r]];
   }
 }
-constexpr int kOrderTempBytes = (128 + kMaxSeqsPerLaunch + 160) * 4;  // plan_order's temporaries
+constexpr int kOrderTempBytes = (128 + 2 * kMaxSeqsPerLaunch + 160) * 4;  // plan_order's temporaries
 
 template <class C, int NC, int NSTAGE, int CTAS_PER_SM, int MODE>
 __global__ void __launch_bounds__(Layout<C, NC, NSTAGE>::THREADS, CTAS_PER_SM)

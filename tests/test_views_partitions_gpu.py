@@ -133,3 +133,33 @@ def test_replayed_with_other_lengths(n):
         ref, _, bound = attend64(q, kc, vc, bt, lens, 0.1, 0, 0, see)
         assert bool(((out.cpu().double() - ref).abs() <= bound).all())
     assert parts[0] == parts[3] and all(p >= P for p in parts)
+
+
+def test_the_order_of_a_batch_does_not_matter():
+    """16 sequences of 3000 to 8000 tokens whose partitions are whole: shortest first or longest
+    first, the long ones start first and the call takes the same time (without that it
+    took a fifth longer with the longest last)."""
+    dev, S, n, H, KH, D, BS, P = torch.device("cuda"), 16, 64, 32, 8, 128, 16, 512
+    lens = [3000 + 5000 * i // (S - 1) for i in range(S)]
+    MB = -(-lens[-1] // BS)
+    NB = S * MB
+    kc, vc = (torch.randn(s, dtype=torch.bfloat16, device=dev) for s in ((NB, KH, D // 8, BS, 8), (NB, KH, D, BS)))
+    bt = torch.randperm(NB, device=dev).view(S, MB).to(torch.int32)
+    q = torch.randn((S, n, H, D), dtype=torch.bfloat16, device=dev)
+    masks = pack(torch.stack([ancestors(tree_parents(s, n)) for s in range(S)])).to(dev)
+    ws = torch.empty(binding.view_workspace_bytes(S, n, H, KH, D, MB, BS, P, 0, 0), dtype=torch.uint8, device=dev)
+    times = []
+    for order in (lens, lens[::-1]):
+        L, out = torch.tensor(order, dtype=torch.int32, device=dev), torch.empty_like(q)
+        best = float("inf")
+        for _ in range(5):
+            a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            a.record()
+            for _ in range(10):
+                binding.pa_decode_v2_tree(out, q, kc, vc, bt, L, masks, 0.1, partition_size=P, workspace=ws)
+            b.record()
+            b.synchronize()
+            best = min(best, a.elapsed_time(b))
+        assert header(ws)[0] == S * KH * 2
+        times.append(best)
+    assert max(times) <= 1.1 * min(times), times
