@@ -21,11 +21,11 @@
 // before their stores.  Accepted nodes ascend, so node i of the path lies at or
 // behind place i: a store never lands on what a later batch reads.
 //
-// Measured: one token of 128 sequences (8 kv heads of 128 dims, bf16) 3.8 us a call in a
+// Measured: one token of 128 sequences (8 kv heads of 128 dims, bf16) 3.9 us a call in a
 // graph, a launch's latency; 24 prompts of 257 to 2049 tokens, fp16 rows into E4M3 codes, 41 us
 // for 156 MB (3.8 TB/s; 23 at the copy's rate), bound by the instructions of rounding and
 // transposing.  The paths of a batch's trees in eight layers 14 us (dependent loads: length,
-// path, table, row).
+// path, table, row; nodes that are in their places already are moved like the others).
 #include <algorithm>
 #include <atomic>
 #include <climits>
@@ -452,7 +452,7 @@ __global__ void __launch_bounds__(kAcceptThreads)
   const bool bad = __syncthreads_or(path_bad(p, s, tid, kAcceptThreads)) != 0;
   const int a = bad ? 0 : p.count[s], base = L - p.n;
   if (p.first && layer == 0 && blockIdx.z == 0 && tid == 0) p.new_lens[s] = bad ? L : base + a;
-  // Nodes that are in their places already: the path's first ones.
+  // Where each node of the path is, and where it goes.
   for (int i = tid; i < a; i += kAcceptThreads) {
     const int pos[2] = {base + p.accepted[(size_t)s * p.A + i], base + i};
 #pragma unroll

@@ -34,6 +34,9 @@
 //    and the grid is one wave however skewed the lengths.
 //  - pa_combine_kernel (otherwise): grid (S, ceil(H / RPC)), 8 warps a CTA,
 //    one WPR for the launch from the table's largest partition count.
+// View rows (VIEW): one launch for each launch of phase 1, whose tokens per partition
+// every CTA works out from the lengths as phase 1 did; often they leave nothing to
+// combine, so the grid has no more CTAs than run at once.
 #pragma once
 
 #include "pa_common.cuh"

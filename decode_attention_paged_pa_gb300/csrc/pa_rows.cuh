@@ -41,13 +41,14 @@
 // 8-bit caches: the ring of tiles is filled by warps that widen E4M3 codes to fp16 from a
 // ring of codes, into the layouts of a block of 64 tokens whatever the cache's block.
 //
-// Measured (32 heads over 8 of 128 dims; whole calls): 16 nodes of 48 sequences of 1001 to
-// 4999 tokens, bf16 118 us (of the cache's bytes: 82), fp16 104; 64 nodes of 16 sequences of
-// 2048 to 8192, bf16 122 (bytes 49, products 85 with two terms a weight), fp16 96; chunks of
-// 128 tokens over a window of 1024, fp16 97, E4M3 121 (products 27).  A tile takes about 1100
-// cycles (fp16) where its products are 530: what is left is the way from a tile's scores
-// through its weights to the buffer's next scores, three buffers for two warpgroups; and
-// 5700 cycles from a unit to the next one.
+// Measured (32 heads over 8 of 128 dims, blocks of 16; whole calls, one after the other): 16
+// nodes of 48 sequences of 1001 to 4999 tokens, bf16 108 us (of the cache's bytes: 82), fp16
+// 101; 64 nodes of 16 sequences of 2048 to 8192, bf16 119 (blocks of 32: 111; bytes 49, products
+// 85 with two terms a weight), fp16 99, E4M3 155; chunks of 128 tokens over a window of 1024,
+// fp16 99, E4M3 123 (products 27).  A tile takes about 1100 cycles (fp16) where its products
+// are 530: what is left is the way from a tile's scores through its weights to the buffer's
+// next scores, three buffers for two warpgroups; and 5700 cycles from a unit to the next one.
+// With one infinite value in a node of 16, over one sequence of 8192 tokens: 155 us instead of 30.
 #pragma once
 
 #include <type_traits>

@@ -17,7 +17,7 @@
 // (counts, scan, lengths, table: about four) and their launches: a step of up to
 // kRows rows is one launch, whose only CTA also leaves the status; larger ones
 // have the workspace's header cleared by a launch before.  Measured (calls in
-// a graph): 128 sequences of one new token 2.9 us, 512 of up to 256 (1.1 MB written and read) 3.9.
+// a graph): 128 sequences of one new token 3.1 us, 512 of up to 256 (1.1 MB written and read) 4.0.
 #include <climits>
 #include <cstring>
 

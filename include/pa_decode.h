@@ -305,7 +305,9 @@ int pa_decode_v2_mq_fp8(void* out, float* lse, const void* query, const void* ke
  *               room the tables have.
  * Elements, shapes, lse, ownership and errors are those of pa_decode_v2_mq (fp32:
  * not blocks of 64 tokens at head size 256, PA_ERR_UNSUPPORTED).  A key or value
- * that is not finite reaches the rows that see it, no others.
+ * that is not finite reaches the rows that see it, no others: they are not finite
+ * where they would be by the formula (an infinite value may give NaN, where its
+ * weight is 0 or is held in two terms).
  */
 int pa_decode_v2_window(void* out, float* lse, const void* query, const void* key_cache,
                         const void* value_cache, const int32_t* block_tables, const int32_t* seq_lens,
@@ -453,9 +455,9 @@ int pa_tree_accept(int32_t* new_lens, void* const* key_caches, void* const* valu
  *   block_size  any positive number
  *   workspace   >= 256 bytes, 16-byte aligned, required; holds the status
  * A negative count (taken as 0), more rows than num_tokens (those behind are left
- * out), a length below the count or above the table's capacity (slots and
- * positions of -1) and a negative block id (slots of -1) are recorded as
- * PA_ERR_DEVICE_BOUNDS.  What is written may not overlap another array
+ * out), of a sequence with rows a length below its count or above the table's
+ * capacity (slots and positions of -1), and a row's negative block id (a slot of -1)
+ * are recorded as PA_ERR_DEVICE_BOUNDS.  What is written may not overlap another array
  * (PA_ERR_INVALID_ARG).
  */
 int pa_pages_slots(int64_t* slots, int32_t* positions, int32_t* seq_ids, int32_t* cu_tokens,
