@@ -345,6 +345,8 @@ int pa_decode_v2_window_fp8(void* out, float* lse, const void* query, const void
  *   seq_lens    each in [num_nodes, max_blocks_per_seq*block_size] (others:
  *               PA_ERR_DEVICE_BOUNDS; below num_nodes: zeros)
  *   num_nodes   1 .. 512
+ *   block_tables  the entries of the nodes' blocks and of those that a child of the
+ *               tokens before the tree sees are read, whatever the masks
  *   workspace   >= pa_decode_v2_view_workspace_bytes(num_seqs, num_nodes, ...)
  * All else is as for pa_decode_v2_window.
  */
